@@ -46,7 +46,8 @@ enum na3d_status {
     NA3D_ERR_ARCH = 8,           /* the current device is not compute capability 10.3 */
     NA3D_ERR_CUDA = 9,           /* a CUDA runtime or driver call failed */
     NA3D_ERR_DEVICE_TIMEOUT = 10, /* a pipeline wait inside the kernel gave up */
-    NA3D_ERR_UNSUPPORTED = 11    /* valid but not implemented (no current argument returns it) */
+    NA3D_ERR_UNSUPPORTED = 11    /* valid but not implemented: HD > 128 or a softcap outside its range in
+                                     the na3d_scored_ calls, R > 128 in the na3d_lora_ calls */
 };
 
 /*
@@ -170,6 +171,142 @@ int na3d_fwd_region(const void* q, const void* k, const void* v, void* out,
  */
 int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv,
                   int64_t M, int64_t C, int64_t NH, int64_t HD, void* stream);
+
+/*
+ * na3d_scored_fwd - neighborhood attention whose scores are shaped before the
+ * softmax, on a batch that may pack several clips into one grid. Query i sees
+ * the keys j of its window (the window of na3d_fwd, on the whole grid); with
+ * a = q_i . k_j,
+ *   s = a, or softcap * tanh(a / softcap) where softcap > 0,
+ *   s -= slopes[head][0] |t_i - t_j| + slopes[head][1] |h_i - h_j|
+ *        + slopes[head][2] |w_i - w_j|                 (slopes not NULL),
+ * and key j is masked
+ *   - where doc_i != doc_j or doc_i < 0                (doc not NULL): clips
+ *     do not see one another, and a position with a negative document is
+ *     padding, which sees nothing and is seen by nothing;
+ *   - where t_j > t_i and t_j >= prefix[b]             (prefix not NULL):
+ *     causal along T, with the first prefix[b] frames seen by every frame.
+ * out_i = sum_j p_ij v_j with p the softmax of the s that are not masked, and
+ * lse_i = log sum_j e^s. A row that sees nothing has out 0 and lse -infinity.
+ * What masked keys and padding hold (infinities and NaN included) reaches no
+ * row that does not see them. Sums, statistics and probabilities are fp32; the
+ * probabilities are rounded to bf16 for their product with v, out is rounded
+ * once.
+ *
+ * q (scaled by HD^-0.5), k, v: bf16 with a token stride, as
+ *   na3d_fwd_strided; out: contiguous (B,T,H,W,NH,HD).
+ * lse: fp32 (B,T,H,W,NH), or NULL; the backward pass needs it.
+ * softcap: 0 (none) or 2^-10 .. 2^20, else NA3D_ERR_UNSUPPORTED.
+ * slopes: fp32 (NH, 3) or NULL; doc: int32 (B,T,H,W) or NULL; prefix: int32
+ *   (B) or NULL. All DEVICE pointers, 4-byte aligned, read when the kernels
+ *   run (a replayed graph sees their current contents).
+ * HD: 16, 32, 64 or 128; other powers of two return NA3D_ERR_UNSUPPORTED.
+ * out and lse must not overlap an input or one another. All other arguments,
+ * the errors, the asynchrony and the capture into graphs are those of
+ * na3d_fwd_strided.
+ */
+int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                    int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t HD,
+                    int64_t KT, int64_t KH, int64_t KW, int64_t q_token_stride,
+                    int64_t k_token_stride, int64_t v_token_stride, float softcap,
+                    const float* slopes, const int32_t* doc, const int32_t* prefix,
+                    void* stream);
+
+/*
+ * na3d_scored_bwd - the gradients of na3d_scored_fwd. With p = e^(s - lse),
+ * dp = dout_i . v_j, delta_i = dout_i . out_i and
+ * da = p (dp - delta_i) (1 - tanh(a / softcap)^2)   (the last factor 1 without a cap),
+ *   dq_i = sum_j da k_j,   dk_j = sum_i da q_i,   dv_j = sum_i p dout_i.
+ * dq is the gradient of the scaled q that was passed. slopes, doc and prefix
+ * are constants. The sums have a fixed order: equal inputs give equal bits.
+ * p and da are rounded to bf16 for their products (fp32 sums), the gradients
+ * once at the end.
+ *
+ * out, lse: what na3d_scored_fwd wrote for the same arguments; dout: bf16,
+ *   contiguous (B,T,H,W,NH,HD).
+ * dq, dk, dv: bf16 with token strides (the three blocks of a fused
+ *   (B,T,H,W,3,NH,HD) gradient, for instance); written whole, padding's
+ *   gradients as 0. They must not share elements with one another or overlap
+ *   an input or the workspace.
+ * work: DEVICE workspace of na3d_scored_bwd_workspace() bytes, 16-byte
+ *   aligned, its contents arbitrary; in use until the call's kernels end, so
+ *   calls that may run at the same time need their own.
+ * All other arguments and errors are those of na3d_scored_fwd.
+ */
+int na3d_scored_bwd(const void* q, const void* k, const void* v, const void* out,
+                    const float* lse, const void* dout, void* dq, void* dk, void* dv, void* work,
+                    int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t HD,
+                    int64_t KT, int64_t KH, int64_t KW, int64_t q_token_stride,
+                    int64_t k_token_stride, int64_t v_token_stride, int64_t dq_token_stride,
+                    int64_t dk_token_stride, int64_t dv_token_stride, float softcap,
+                    const float* slopes, const int32_t* doc, const int32_t* prefix,
+                    void* stream);
+
+/* Bytes of workspace of na3d_scored_bwd; -1 where a size is invalid. */
+int64_t na3d_scored_bwd_workspace(int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH);
+
+/*
+ * na3d_lora_qkv_proj - na3d_qkv_proj with a low-rank adapter for each request
+ * of the batch. Rows offsets[r] <= m < offsets[r+1] belong to request r, whose
+ * adapter is a = adapter[r]:
+ *   t[m] = scaling[a] * ( x[m] A_a^T )                      (R values)
+ *   qkv[m][n] = bf16( s_n * ( sum_c x[m][c] w[n][c] + bias[n] + sum_r t[m][r] B_a[n][r] ) )
+ * with s_n as in na3d_qkv_proj. Rows outside every request, and requests whose
+ * id is not in 0 .. n_adapters - 1 (-1, say), get the base projection alone;
+ * several requests may name one adapter. All sums are fp32; t is rounded to
+ * bf16 for its product with B_a.
+ *
+ * x, w, bias, qkv, M, C, NH, HD: as na3d_qkv_proj.
+ * lora_a: DEVICE, bf16 (n_adapters, R, C); lora_b: DEVICE, bf16
+ *   (n_adapters, 3*NH*HD, R), 16-byte aligned. An adapter of lower rank is
+ *   padded with zeros. R: a multiple of 8 (else NA3D_ERR_ALIGN) up to 128 (else
+ *   NA3D_ERR_UNSUPPORTED).
+ * scaling: DEVICE, fp32 (n_adapters).
+ * offsets: DEVICE, int32 (n_requests + 1), not decreasing, within 0 .. M;
+ *   adapter: DEVICE, int32 (n_requests). Both are read when the kernels run,
+ *   so a replayed graph may be given other requests. Offsets that decrease or
+ *   leave 0 .. M touch no memory outside the tensors, but which adapter such
+ *   rows get is unspecified.
+ * n_requests, n_adapters >= 1.
+ * work: DEVICE workspace of na3d_lora_workspace(..., 0) bytes, 16-byte aligned,
+ *   contents arbitrary; as in na3d_scored_bwd, one call at a time.
+ * qkv and work must not overlap an input or one another. Errors, asynchrony
+ * and capture as na3d_qkv_proj.
+ */
+int na3d_lora_qkv_proj(const void* x, const void* w, const void* bias, const void* lora_a,
+                       const void* lora_b, const float* scaling, const int32_t* offsets,
+                       const int32_t* adapter, void* qkv, void* work, int64_t M, int64_t C,
+                       int64_t NH, int64_t HD, int64_t R, int64_t n_requests,
+                       int64_t n_adapters, void* stream);
+
+/*
+ * na3d_lora_qkv_proj_bwd - the gradients of na3d_lora_qkv_proj with a frozen
+ * base weight, bias and scaling. With g = s_n dqkv and, for each row's
+ * adapter, u = scaling[a] * ( g B_a ):
+ *   dx = g W + u A_a,
+ *   dlora_a[a] = sum over the adapter's rows of u^T x,
+ *   dlora_b[a] = sum over the adapter's rows of g^T t.
+ * Sums are fp32 in a fixed order; t and u are rounded to bf16 for their
+ * products, the results once at the end. An adapter that no row has gets
+ * zeros.
+ *
+ * dqkv: DEVICE, bf16 (M, 3*NH*HD), 16-byte aligned.
+ * dx: bf16 (M, C), or NULL where it is not wanted; dlora_a, dlora_b: as lora_a,
+ *   lora_b; all written whole, 16-byte aligned.
+ * work: na3d_lora_workspace(..., 1) bytes. No output may overlap an input, the
+ * workspace or another output. All other arguments and errors are those of
+ * na3d_lora_qkv_proj.
+ */
+int na3d_lora_qkv_proj_bwd(const void* dqkv, const void* x, const void* w, const void* lora_a,
+                           const void* lora_b, const float* scaling, const int32_t* offsets,
+                           const int32_t* adapter, void* dx, void* dlora_a, void* dlora_b,
+                           void* work, int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R,
+                           int64_t n_requests, int64_t n_adapters, void* stream);
+
+/* Bytes of workspace of na3d_lora_qkv_proj (backward 0) or its backward pass
+ * (backward 1); -1 where a size is invalid or not supported. */
+int64_t na3d_lora_workspace(int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R,
+                            int64_t n_requests, int64_t n_adapters, int backward);
 
 /*
  * na3d_selftest_withhold - a self-test of the kernel's failure detection:

@@ -14,19 +14,24 @@ import os
 
 __all__ = [
     "NA3DError", "NA3DUnavailable", "na3d_attention", "na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region",
-    "na3d_qkv_proj", "qkv_views", "na3d_status_string", "na3d_plan",
+    "na3d_qkv_proj", "qkv_views", "na3d_scored_fwd", "na3d_scored_attention", "na3d_scored_bwd",
+    "na3d_lora_qkv_proj", "na3d_lora_qkv_proj_bwd", "na3d_lora_workspace",
+    "na3d_scored_bwd_workspace", "na3d_status_string", "na3d_plan",
     "na3d_device_status", "library_path", "load_library", "EXPORTED_SYMBOLS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libna3d.so")
 EXPORTED_SYMBOLS = ("na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region", "na3d_qkv_proj",
+                    "na3d_scored_fwd", "na3d_scored_bwd", "na3d_scored_bwd_workspace",
+                    "na3d_lora_qkv_proj", "na3d_lora_qkv_proj_bwd", "na3d_lora_workspace",
                     "na3d_selftest_withhold", "na3d_status_string", "na3d_plan",
                     "na3d_device_status")
 
 NA3D_OK = 0
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
+_F32 = ctypes.c_float
 _lib = None
 
 
@@ -72,6 +77,18 @@ def load_library():
     lib.na3d_fwd_region.restype = ctypes.c_int
     lib.na3d_qkv_proj.argtypes = [_P, _P, _P, _P] + [_I64] * 4 + [_P]
     lib.na3d_qkv_proj.restype = ctypes.c_int
+    lib.na3d_scored_fwd.argtypes = [_P] * 5 + [_I64] * 12 + [_F32] + [_P] * 4
+    lib.na3d_scored_fwd.restype = ctypes.c_int
+    lib.na3d_scored_bwd.argtypes = [_P] * 10 + [_I64] * 15 + [_F32] + [_P] * 4
+    lib.na3d_scored_bwd.restype = ctypes.c_int
+    lib.na3d_scored_bwd_workspace.argtypes = [_I64] * 5
+    lib.na3d_scored_bwd_workspace.restype = _I64
+    lib.na3d_lora_qkv_proj.argtypes = [_P] * 10 + [_I64] * 7 + [_P]
+    lib.na3d_lora_qkv_proj.restype = ctypes.c_int
+    lib.na3d_lora_qkv_proj_bwd.argtypes = [_P] * 12 + [_I64] * 7 + [_P]
+    lib.na3d_lora_qkv_proj_bwd.restype = ctypes.c_int
+    lib.na3d_lora_workspace.argtypes = [_I64] * 7 + [ctypes.c_int]
+    lib.na3d_lora_workspace.restype = _I64
     lib.na3d_selftest_withhold.argtypes = [_P, _P, _P, _P] + [_I64] * 10 + [_P]
     lib.na3d_selftest_withhold.restype = ctypes.c_int
     lib.na3d_status_string.argtypes = [ctypes.c_int]
@@ -248,6 +265,222 @@ def qkv_views(qkv):
     """q, k, v views (B, T, H, W, NH, HD) of a (B, T, H, W, 3, NH, HD)
     projection output, for ``na3d_fwd_strided``."""
     return qkv[..., 0, :, :], qkv[..., 1, :, :], qkv[..., 2, :, :]
+
+
+def _check_on_device(tensors):
+    """Each (name, tensor, dtype, shape) is a contiguous tensor of that dtype
+    and shape on the current CUDA device."""
+    torch = _torch_module()
+    dev = torch.cuda.current_device() if _cuda_ok else -2
+    for name, t, dtype, shape in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not dtype or t.get_device() != dev:
+            raise TypeError(f"{name} must be a {dtype} tensor on the current CUDA device")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _empty(stream, shape, dtype):
+    """A new tensor on the current device, allocated on the stream that the
+    call uses, so that the allocator may reuse its memory only behind the call."""
+    torch = _torch_module()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def _workspace(work, need, stream):
+    """`work` where it is given and large enough, else a new workspace."""
+    torch = _torch_module()
+    if work is None:
+        return _empty(stream, (need,), torch.uint8)
+    dev = torch.cuda.current_device() if _cuda_ok else -2
+    if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
+        raise TypeError("work must be a contiguous tensor on the current CUDA device")
+    if work.numel() * work.element_size() < need:
+        raise ValueError(f"work must hold {need} bytes")
+    return work
+
+
+def _scored_options(q, softcap, slopes, doc, prefix):
+    """The score arguments of the na3d_scored_ calls, checked: (softcap, the
+    three pointers or None)."""
+    torch = _torch_module()
+    B, T, H, W, NH, _ = q.shape
+    given = []
+    if slopes is not None:
+        given.append(("slopes", slopes, torch.float32, (NH, 3)))
+    if doc is not None:
+        given.append(("doc", doc, torch.int32, (B, T, H, W)))
+    if prefix is not None:
+        given.append(("prefix", prefix, torch.int32, (B,)))
+    _check_on_device(given)
+    return (float(softcap),) + tuple(None if t is None else t.data_ptr() for t in (slopes, doc, prefix))
+
+
+def na3d_scored_fwd(q, k, v, out, kernel_size, lse=None, softcap=0.0, slopes=None, doc=None, prefix=None,
+                    stream=None) -> None:
+    """``na3d_fwd_strided`` with shaped scores (see ``na3d_scored_fwd`` in
+    include/na3d.h): a tanh cap (``softcap`` > 0), a bias that falls with the
+    distance (``slopes``: fp32 (NH, 3), per head along T, H and W), a document
+    mask (``doc``: int32 (B, T, H, W), negative for padding) and a causal mask
+    along T with a free prefix (``prefix``: int32 (B,) frames). ``lse``, where
+    given, receives the fp32 (B, T, H, W, NH) log-sum-exp of the scores. q, k,
+    v may be views with a token stride; ``out`` is contiguous. HD up to 128."""
+    lib = _lib if _lib is not None else load_library()
+    _check_bf16_on_device((("q", q), ("k", k), ("v", v), ("out", out)))
+    shape = q.shape
+    if len(shape) != 6 or k.shape != shape or v.shape != shape or out.shape != shape:
+        raise ValueError("q, k, v and out must have the same 6-D (B,T,H,W,NH,HD) shape")
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    if lse is not None:
+        _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
+    options = _scored_options(q, softcap, slopes, doc, prefix)
+    KT, KH, KW = (int(x) for x in kernel_size)
+    rc = lib.na3d_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                             None if lse is None else lse.data_ptr(), *shape, KT, KH, KW,
+                             _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
+                             *options, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_scored_fwd")
+
+
+def na3d_scored_attention(q, k, v, kernel_size, softcap=0.0, slopes=None, doc=None, prefix=None,
+                          return_lse=False, stream=None):
+    """``na3d_scored_fwd`` into a new tensor: returns out, or (out, lse) where
+    ``return_lse`` is true (what ``na3d_scored_bwd`` needs)."""
+    torch = _torch_module()
+    _check_bf16_on_device((("q", q),))
+    out = _empty(stream, q.shape, torch.bfloat16)
+    lse = _empty(stream, q.shape[:-1], torch.float32) if return_lse else None
+    na3d_scored_fwd(q, k, v, out, kernel_size, lse, softcap, slopes, doc, prefix, stream)
+    return (out, lse) if return_lse else out
+
+
+def na3d_scored_bwd_workspace(B, T, H, W, NH) -> int:
+    """Bytes of workspace that ``na3d_scored_bwd`` uses."""
+    need = int(load_library().na3d_scored_bwd_workspace(B, T, H, W, NH))
+    if need < 0:
+        raise ValueError("every size must be at least 1")
+    return need
+
+
+def na3d_scored_bwd(q, k, v, out, lse, dout, dq, dk, dv, kernel_size, softcap=0.0, slopes=None, doc=None,
+                    prefix=None, work=None, stream=None) -> None:
+    """dq, dk, dv = the gradients of ``na3d_scored_fwd`` for the gradient
+    ``dout`` of its output. ``out`` and ``lse`` are what the forward pass wrote;
+    the other arguments are the forward pass's. dq, dk and dv may be views with
+    a token stride, e.g. ``qkv_views`` of a fused gradient. ``work``: a tensor of
+    ``na3d_scored_bwd_workspace`` bytes, kept by the caller (one call at a time);
+    None allocates one."""
+    lib = _lib if _lib is not None else load_library()
+    names = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
+    tensors = (q, k, v, out, dout, dq, dk, dv)
+    _check_bf16_on_device(zip(names, tensors))
+    shape = q.shape
+    if len(shape) != 6 or any(t.shape != shape for t in tensors):
+        raise ValueError("q, k, v, out, dout, dq, dk and dv must have the same 6-D (B,T,H,W,NH,HD) shape")
+    if not (out.is_contiguous() and dout.is_contiguous()):
+        raise ValueError("out and dout must be contiguous")
+    _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
+    options = _scored_options(q, softcap, slopes, doc, prefix)
+    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))]
+    KT, KH, KW = (int(x) for x in kernel_size)
+    work = _workspace(work, na3d_scored_bwd_workspace(*shape[:5]), stream)
+    rc = lib.na3d_scored_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                             dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(),
+                             *shape, KT, KH, KW, *strides, *options, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_scored_bwd")
+
+
+def na3d_lora_workspace(M, C, num_heads, head_dim, rank, n_requests, n_adapters, backward=False) -> int:
+    """Bytes of workspace of ``na3d_lora_qkv_proj``, or of its backward pass."""
+    need = int(load_library().na3d_lora_workspace(M, C, num_heads, head_dim, rank, n_requests, n_adapters,
+                                                  1 if backward else 0))
+    if need < 0:
+        raise ValueError("sizes that na3d_lora_qkv_proj does not take")
+    return need
+
+
+def _check_lora(x, w, lora_a, lora_b, scaling, offsets, adapter, num_heads, head_dim):
+    """The arguments both directions share, checked: (M, C, NH, HD, R, n_req, n_ad)."""
+    torch = _torch_module()
+    bf16, i32 = torch.bfloat16, torch.int32
+    NH, HD = int(num_heads), int(head_dim)
+    for name, t, dims in (("x", x, None), ("lora_a", lora_a, 3), ("adapter", adapter, 1)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() == 0 or (dims and t.dim() != dims):
+            raise ValueError(f"{name} has the wrong number of dimensions")
+    C, N = int(x.shape[-1]), 3 * NH * HD
+    n_ad, R, n_req = int(lora_a.shape[0]), int(lora_a.shape[1]), int(adapter.shape[0])
+    _check_on_device((("x", x, bf16, x.shape), ("w", w, bf16, (N, C)), ("lora_a", lora_a, bf16, (n_ad, R, C)),
+                      ("lora_b", lora_b, bf16, (n_ad, N, R)), ("scaling", scaling, torch.float32, (n_ad,)),
+                      ("offsets", offsets, i32, (n_req + 1,)), ("adapter", adapter, i32, (n_req,))))
+    return (x.numel() // C if C else 0), C, NH, HD, R, n_req, n_ad
+
+
+def na3d_lora_qkv_proj(x, w, bias, lora_a, lora_b, scaling, offsets, adapter, qkv, num_heads, head_dim, work=None,
+                       stream=None) -> None:
+    """``na3d_qkv_proj`` with a low-rank adapter for each request of the batch
+    (see ``na3d_lora_qkv_proj`` in include/na3d.h). Tokens
+    offsets[r] .. offsets[r+1] - 1 of x are request r's, with the adapter
+    adapter[r] (none where the id is not 0 .. n_adapters - 1): lora_a
+    (n_adapters, R, C) and lora_b (n_adapters, 3*NH*HD, R) in bf16, scaling fp32
+    (n_adapters,); offsets int32 (n_requests + 1,) and adapter int32
+    (n_requests,) on the device. R is a multiple of 8 up to 128. ``work``: a
+    tensor of ``na3d_lora_workspace`` bytes, kept by the caller (one call at a
+    time); None allocates one."""
+    lib = _lib if _lib is not None else load_library()
+    sizes = _check_lora(x, w, lora_a, lora_b, scaling, offsets, adapter, num_heads, head_dim)
+    _check_bf16_on_device((("qkv", qkv),))
+    if bias is not None:
+        _check_on_device((("bias", bias, _torch.bfloat16, w.shape[:1]),))
+    if not qkv.is_contiguous():
+        raise ValueError("qkv must be contiguous")
+    if qkv.numel() != sizes[0] * w.shape[0]:
+        raise ValueError("qkv must hold 3*NH*HD values per token of x")
+    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 0)), stream)
+    rc = lib.na3d_lora_qkv_proj(x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                                lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), offsets.data_ptr(),
+                                adapter.data_ptr(), qkv.data_ptr(), work.data_ptr(), *sizes, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_lora_qkv_proj")
+
+
+def na3d_lora_qkv_proj_bwd(dqkv, x, w, lora_a, lora_b, scaling, offsets, adapter, dx, dlora_a, dlora_b, num_heads,
+                           head_dim, work=None, stream=None) -> None:
+    """The gradients of ``na3d_lora_qkv_proj`` with respect to x (``dx``, or
+    None where it is not wanted) and the adapters, for the gradient ``dqkv`` of
+    its output; the base weight, the bias and the scalings are frozen. ``work``:
+    as there, with ``backward=True``."""
+    lib = _lib if _lib is not None else load_library()
+    sizes = _check_lora(x, w, lora_a, lora_b, scaling, offsets, adapter, num_heads, head_dim)
+    bf16 = _torch.bfloat16
+    _check_bf16_on_device((("dqkv", dqkv),))
+    if not dqkv.is_contiguous():
+        raise ValueError("dqkv must be contiguous")
+    if dqkv.numel() != sizes[0] * w.shape[0]:
+        raise ValueError("dqkv must hold 3*NH*HD values per token of x")
+    outputs = [("dlora_a", dlora_a, bf16, lora_a.shape), ("dlora_b", dlora_b, bf16, lora_b.shape)]
+    if dx is not None:
+        outputs.append(("dx", dx, bf16, x.shape))
+    _check_on_device(outputs)
+    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 1)), stream)
+    rc = lib.na3d_lora_qkv_proj_bwd(dqkv.data_ptr(), x.data_ptr(), w.data_ptr(), lora_a.data_ptr(),
+                                    lora_b.data_ptr(), scaling.data_ptr(), offsets.data_ptr(), adapter.data_ptr(),
+                                    None if dx is None else dx.data_ptr(), dlora_a.data_ptr(), dlora_b.data_ptr(),
+                                    work.data_ptr(), *sizes, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_lora_qkv_proj_bwd")
 
 
 def na3d_plan(T, H, W, NH, HD, KT, KH, KW) -> dict:

@@ -10,41 +10,21 @@
 #include <tuple>
 
 #include "na3d.h"
+#include "na3d_host.cuh"
 #include "na3d_kernel.cuh"
 #include "na3d_proj.cuh"
 
 namespace {
 
+using na3d::EncodeTiledFn;
 using na3d::KernelParams;
 using na3d::VariantInfo;
-
-// ------------------------------------------------------------------ validation
-
-bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
-
-int validate_shape(int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t HD, int64_t KT,
-                   int64_t KH, int64_t KW) {
-    if (B < 1 || NH < 1 || T < 1 || H < 1 || W < 1 || HD < 1) return NA3D_ERR_SHAPE;
-    const int64_t ks[3] = {KT, KH, KW}, ns[3] = {T, H, W};
-    for (int a = 0; a < 3; ++a)
-        if (ks[a] < 1 || (ks[a] & 1) == 0 || ks[a] > ns[a]) return NA3D_ERR_KERNEL;
-    if (!is_pow2(HD) || HD < 16) return NA3D_ERR_HEAD_DIM;
-    // element count and byte size of one tensor must fit int64; TMA limits:
-    // every global dimension < 2^32, every stride < 2^40 bytes.
-    int64_t n = 1;
-    const int64_t dims[6] = {B, T, H, W, NH, HD};
-    for (int i = 0; i < 6; ++i)
-        if (!mul_ok(n, dims[i], &n)) return NA3D_ERR_OVERFLOW;
-    if (!mul_ok(n, 2, &n)) return NA3D_ERR_OVERFLOW;
-    // a head's column offset is a signed 32-bit TMA coordinate
-    if (NH * HD >= (int64_t(1) << 31) || W >= (int64_t(1) << 31) || H >= (int64_t(1) << 31) ||
-        T >= (int64_t(1) << 31) || B >= (int64_t(1) << 31))
-        return NA3D_ERR_OVERFLOW;
-    if (n / dims[0] >= (int64_t(1) << 40)) return NA3D_ERR_OVERFLOW;  // batch stride in bytes
-    return NA3D_OK;
-}
+using na3d::encode_fn;
+using na3d::encode_map_2d;
+using na3d::is_pow2;
+using na3d::mul_ok;
+using na3d::overlaps;
+using na3d::validate_shape;
 
 // ------------------------------------------------------------------ planner
 
@@ -217,24 +197,6 @@ Plan choose_plan(const Axis& at, const Axis& ah, const Axis& aw, int hd) {
 
 // ------------------------------------------------------------------ TMA descriptors
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
-}
-
 // The (B,T,H,W,NH,HD) tensor viewed as 5-D (NH*HD, W, H, T, B), with
 // `token_stride` elements between consecutive grid positions: a box of
 // {hd_box, bx, by, bz, 1} at x = head*HD + column picks one head's rows.
@@ -254,27 +216,6 @@ bool encode_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t T, int64_t H
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// A row-major (outer, inner) bf16 matrix as a 2-D tensor map with a
-// (box_inner, box_outer) box and the 128-byte swizzle (box_inner = 64).
-bool encode_map_2d(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int box_inner,
-                   int box_outer) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
-    const cuuint64_t strides[1] = {cuuint64_t(inner * 2)};
-    const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_outer)};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Do the byte ranges [a, a + a_bytes) and [b, b + b_bytes) intersect?
-bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + uintptr_t(b_bytes) && y < x + uintptr_t(a_bytes);
 }
 
 }  // namespace
@@ -355,13 +296,8 @@ int fwd_region(const void* q, const void* k, const void* v, void* out, int64_t B
         overlaps(out, out_bytes, v, spans[2]))
         return NA3D_ERR_ALIAS;
 
-    int dev = 0, major = 0, minor = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return NA3D_ERR_CUDA;
-    if (major != 10 || minor != 3) return NA3D_ERR_ARCH;
+    int sms = 0;
+    if ((rc = na3d::current_device(&sms)) != NA3D_OK) return rc;
 
     VariantInfo vi;
     const Plan pl = choose_plan(Axis{Tq, t0, T, KT}, Axis{Hq, h0, H, KH}, Axis{Wq, w0, W, KW}, int(HD));
@@ -485,13 +421,8 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv, int
     if (overlaps(qkv, ob, x, xb) || overlaps(qkv, ob, w, wb) || (bias && overlaps(qkv, ob, bias, N * 2)))
         return NA3D_ERR_ALIAS;
 
-    int dev = 0, major = 0, minor = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return NA3D_ERR_CUDA;
-    if (major != 10 || minor != 3) return NA3D_ERR_ARCH;
+    int sms = 0;
+    if (const int rc = na3d::current_device(&sms)) return rc;
 
     na3d::ProjParams pp;
     pp.M = int32_t(M);

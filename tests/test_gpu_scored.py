@@ -1,0 +1,247 @@
+"""The score-shaped attention on the GPU against the 64-bit reference, forward
+and backward, every value within the bound that the reference derives."""
+import pytest
+import torch
+
+import neighborhood_attention_video_gb300 as na
+import packed_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def make(shape, seed, scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    q, k, v, g = (torch.randn(shape, generator=gen) for _ in range(4))
+    return [(x * s).to(BF16) for x, s in ((q, scale * shape[-1] ** -0.5), (k, 1), (v, 1), (g, 1))]
+
+
+def make_options(shape, seed, softcap=0.0, slopes=False, docs=0, pad=0, prefix=None):
+    B, T, H, W, NH, _ = shape
+    gen = torch.Generator().manual_seed(seed + 1000)
+    o = dict(softcap=softcap, slopes=None, doc=None, prefix=None)
+    if slopes:
+        o["slopes"] = torch.rand((NH, 3), generator=gen)
+    if docs:
+        cuts = torch.randint(0, T + 1, (B, docs - 1), generator=gen)
+        doc = (torch.arange(T)[None, :, None] >= cuts[:, None]).sum(-1)[:, :, None, None]
+        doc = doc + 7 * torch.randint(0, 2, (B, 1, H, 1), generator=gen)      # and along H
+        o["doc"] = doc.expand(B, T, H, W).to(torch.int32).contiguous()
+        if pad:
+            o["doc"][..., W - pad:] = -1 - torch.arange(pad, dtype=torch.int32)
+    if prefix is not None:
+        o["prefix"] = torch.tensor([(prefix + b) for b in range(B)], dtype=torch.int32)
+    return o
+
+
+def cuda(o):
+    return {n: x.cuda() if isinstance(x, torch.Tensor) else x for n, x in o.items()}
+
+
+def run(q, k, v, g, kernel, opts):
+    """Forward and backward on the GPU through a fused projection's views."""
+    o = cuda(opts)
+    qkv = torch.stack([q, k, v], 4).cuda()
+    views = na.qkv_views(qkv)
+    out, lse = na.na3d_scored_attention(*views, kernel, return_lse=True, **o)
+    dqkv = torch.full_like(qkv, float("nan"))
+    na.na3d_scored_bwd(*views, out, lse, g.cuda(), *na.qkv_views(dqkv), kernel, **o)
+    torch.cuda.synchronize()
+    return dict(out=out, lse=lse, **dict(zip(("dq", "dk", "dv"), na.qkv_views(dqkv))))
+
+
+CASES = [
+    # shape (B,T,H,W,NH,HD), window, options
+    ((1, 4, 8, 16, 2, 32), (3, 5, 5), {}),
+    ((1, 1, 1, 1, 1, 16), (1, 1, 1), dict(softcap=5.0, slopes=True)),
+    ((1, 3, 9, 13, 2, 64), (1, 1, 1), dict(slopes=True)),
+    ((2, 5, 7, 11, 3, 16), (3, 5, 7), dict(softcap=2.0, slopes=True, docs=2, pad=3, prefix=0)),
+    ((1, 8, 16, 16, 2, 64), (3, 7, 7), dict(softcap=30.0, slopes=True)),
+    ((1, 6, 10, 18, 2, 64), (3, 7, 7), dict(docs=3)),
+    ((2, 6, 9, 14, 1, 128), (3, 5, 5), dict(prefix=2)),
+    ((1, 5, 12, 10, 2, 128), (5, 3, 7), dict(softcap=1.0, slopes=True, docs=2, pad=1, prefix=1)),
+    ((1, 4, 11, 33, 2, 64), (3, 7, 33), dict(slopes=True, docs=2, pad=4)),
+    ((1, 1, 1, 70, 2, 32), (1, 1, 45), dict(softcap=10.0, prefix=0)),
+    ((1, 40, 1, 1, 2, 32), (21, 1, 1), dict(prefix=3, slopes=True)),
+    ((1, 1, 37, 3, 2, 16), (1, 37, 3), dict(docs=1)),
+    ((1, 12, 13, 13, 1, 64), (11, 11, 11), dict(softcap=50.0)),
+    ((3, 2, 5, 6, 5, 32), (1, 5, 3), dict(docs=2, pad=5)),
+    ((1, 2, 3, 200, 1, 64), (1, 3, 151), dict(slopes=True)),
+]
+
+
+@pytest.mark.parametrize("shape,kernel,opts", CASES, ids=lambda v: str(v).replace(" ", ""))
+def test_matches_the_reference(shape, kernel, opts):
+    q, k, v, g = make(shape, sum(shape) + sum(kernel))
+    o = make_options(shape, sum(shape), **opts)
+    want = ref.scored(q, k, v, kernel, dout=g, **o)
+    got = run(q, k, v, g, kernel, o)
+    for name in want:
+        ref.check(name, got[name], want[name])
+
+
+@pytest.mark.parametrize("scale,softcap", [(30.0, 0.0), (30.0, 8.0), (200.0, 20.0), (1e-3, 2.0 ** -10), (3.0, 2.0 ** 20)])
+def test_large_and_small_scores(scale, softcap):
+    """Scores far from 0 keep their softmax; caps at both ends of their range."""
+    shape, kernel = (1, 4, 9, 11, 2, 64), (3, 5, 5)
+    q, k, v, g = make(shape, 17, scale)
+    o = dict(softcap=softcap, slopes=None, doc=None, prefix=None)
+    want = ref.scored(q, k, v, kernel, dout=g, **o)
+    got = run(q, k, v, g, kernel, o)
+    for name in want:
+        ref.check(name, got[name], want[name])
+
+
+def test_random_problems():
+    """Forty seeded problems over every option."""
+    gen = torch.Generator().manual_seed(5)
+    pick = lambda *c: c[int(torch.randint(0, len(c), (1,), generator=gen))]  # noqa: E731
+    upto = lambda n: 1 + int(torch.randint(0, n, (1,), generator=gen))  # noqa: E731
+    for i in range(40):
+        shape = (upto(2), upto(7), upto(14), upto(22), upto(3), pick(16, 32, 64, 128))
+        kernel = tuple(1 + 2 * ((upto(min(n, m)) - 1) // 2) for n, m in zip(shape[1:4], (5, 9, 17)))
+        o = make_options(shape, i, pick(0.0, 4.0, 30.0), pick(True, False), pick(0, 1, 2, 3), upto(shape[3]) - 1,
+                         pick(None, 0, 2))
+        q, k, v, g = make(shape, i)
+        want = ref.scored(q, k, v, kernel, dout=g, **o)
+        got = run(q, k, v, g, kernel, o)
+        for name in want:
+            ref.check(f"problem {i} {shape} {kernel} {name}", got[name], want[name])
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf"), 3.0e38])
+@pytest.mark.parametrize("HD", [32, 128])
+def test_masked_values_reach_nothing(what, HD):
+    """Padding, and another clip's keys and queries, may hold anything: rows that
+    do not see them keep the bits they have without it."""
+    shape, kernel = (1, 6, 8, 12, 2, HD), (3, 5, 5)
+    q, k, v, g = make(shape, 3)
+    o = make_options(shape, 3)
+    o["doc"] = torch.zeros(shape[:4], dtype=torch.int32)
+    o["doc"][:, 3:] = 1
+    o["doc"][:, :, :, 10:] = -1
+    o["softcap"] = 20.0
+    clean = {n: x.clone() for n, x in run(q, k, v, g, kernel, o).items()}
+    bad = o["doc"] == 1
+    bad[:, :, :, 10:] = True
+    for x in (q, k, v, g):
+        x[bad] = what
+    got = run(q, k, v, g, kernel, o)
+    keep = o["doc"] == 0
+    want = ref.scored(*[torch.where(bad[..., None, None], 0.0, x.float()) for x in (q, k, v)], kernel, dout=torch.where(
+        bad[..., None, None], 0.0, g.float()), **o)
+    for name in got:
+        value, bound = want[name]
+        ref.check(name, got[name].cpu()[keep], (value[keep], bound[keep]))
+        assert torch.isfinite(clean[name].cpu()[keep]).all()
+    pad = (o["doc"] < 0)
+    for name in ("out", "dq", "dk", "dv"):
+        assert bool((got[name].cpu()[pad] == 0).all()), name
+    assert bool(torch.isneginf(got["lse"].cpu()[pad]).all())
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_a_bad_value_stays_in_its_windows(what):
+    """A non-finite key or value reaches exactly the queries whose windows hold it."""
+    shape, kernel = (1, 5, 9, 20, 1, 64), (3, 3, 5)
+    q, k, v, g = make(shape, 4)
+    v[0, 2, 4, 9, 0, 5] = what
+    got = run(q, k, v, g, kernel, make_options(shape, 4))
+    idx = ref.window_index(5, 9, 20, kernel)
+    hit = (idx == (2 * 9 + 4) * 20 + 9).any(-1).reshape(5, 9, 20)
+    bad = ~torch.isfinite(got["out"].cpu()[0]).all(-1).all(-1)
+    assert torch.equal(bad, hit)
+    assert torch.isfinite(got["lse"]).all()
+
+
+def test_same_inputs_same_bits():
+    shape, kernel = (1, 6, 16, 17, 4, 64), (3, 5, 7)
+    q, k, v, g = make(shape, 8)
+    o = make_options(shape, 8, 20.0, True, 2, 2, 1)
+    first = {n: x.clone() for n, x in run(q, k, v, g, kernel, o).items()}
+    for _ in range(10):
+        got = run(q, k, v, g, kernel, o)
+        for n in first:
+            assert torch.equal(got[n].view(torch.int16 if n != "lse" else torch.int32),
+                               first[n].view(torch.int16 if n != "lse" else torch.int32)), n
+
+
+def test_outputs_stay_inside_their_tensors():
+    shape, kernel = (1, 3, 7, 9, 2, 32), (3, 5, 5)
+    q, k, v, g = (x.cuda() for x in make(shape, 9))
+    n, rows = q.numel(), q.numel() // 32
+
+    def guarded(count, dtype):
+        buf = torch.full((count + 256,), 3.0, dtype=dtype, device="cuda")
+        return buf, buf[128:128 + count]
+
+    bufs = [guarded(n, BF16) for _ in range(4)] + [guarded(rows, torch.float32)]
+    out, dq, dk, dv = (b[1].view(shape) for b in bufs[:4])
+    lse = bufs[4][1].view(shape[:5])
+    na.na3d_scored_fwd(q, k, v, out, kernel, lse)
+    na.na3d_scored_bwd(q, k, v, out, lse, g, dq, dk, dv, kernel)
+    torch.cuda.synchronize()
+    for buf, view in bufs:
+        assert bool((buf[:128] == 3.0).all()) and bool((buf[128 + view.numel():] == 3.0).all())
+
+
+def test_streams_and_graph():
+    """A call on a side stream, and forward and backward captured into a graph and
+    replayed on other inputs, documents included."""
+    shape, kernel = (1, 4, 10, 12, 2, 64), (3, 5, 5)
+    o = make_options(shape, 1, 20.0, True, 2, 2, 1)
+    q, k, v, g = make(shape, 1)
+    dev = [x.cuda() for x in (q, k, v, g)]
+    co = cuda(o)
+    out = torch.empty_like(dev[0])
+    lse = torch.empty(shape[:5], device="cuda")
+    grads = [torch.empty_like(dev[0]) for _ in range(3)]
+    work = torch.empty(na.na3d_scored_bwd_workspace(*shape[:5]), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    side_out = na.na3d_scored_attention(*dev[:3], kernel, stream=side, **co)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        na.na3d_scored_fwd(*dev[:3], out, kernel, lse, **co)
+        na.na3d_scored_bwd(*dev[:3], out, lse, dev[3], *grads, kernel, work=work, **co)
+    for seed in (1, 2):
+        new = make(shape, seed)
+        no = make_options(shape, seed, 20.0, True, 2, 2, 1)
+        for d, s in zip(dev, new):
+            d.copy_(s)
+        for name in ("slopes", "doc", "prefix"):
+            co[name].copy_(no[name])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.scored(*new[:3], kernel, dout=new[3], **no)
+        for name, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            ref.check(name, x, want[name])
+        if seed == 1:
+            assert torch.equal(out, side_out)
+
+
+def test_offsets_past_32_bits():
+    """A fused tensor of more than 2^31 elements: its last rows against the
+    reference on their own frames."""
+    B, T, H, W, NH, HD = 1, 96, 96, 96, 16, 64
+    kernel = (1, 3, 3)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.empty((B, T, H, W, 3, NH, HD), dtype=BF16, device="cuda")
+    assert qkv.numel() > 2 ** 31
+    for t in range(T):
+        qkv[:, t] = torch.randn(qkv[:, t].shape, generator=gen, device="cuda").to(BF16)
+    out, lse = na.na3d_scored_attention(*na.qkv_views(qkv), kernel, return_lse=True)
+    dqkv = torch.empty_like(qkv)
+    na.na3d_scored_bwd(*na.qkv_views(qkv), out, lse, out, *na.qkv_views(dqkv), kernel)
+    # frames are independent (KT = 1): the last frame's last rows, whose windows end in row H - 1
+    rows = slice(H - 6, H)
+    cut = qkv[:, -1:, rows].cpu()
+    want = ref.scored(*na.qkv_views(cut), (1, 3, 3), dout=out[:, -1:, rows].cpu())
+    for name, x in (("out", out), ("lse", lse), ("dq", na.qkv_views(dqkv)[0])):
+        # the first row of the cut has its window elsewhere; the second row's stays
+        value, bound = want[name]
+        ref.check(name, x[:, -1:, rows].cpu()[:, :, 1:], (value[:, :, 1:], bound[:, :, 1:]))
+    for name, x in zip(("dk", "dv"), na.qkv_views(dqkv)[1:]):
+        value, bound = want[name]
+        ref.check(name, x[:, -1:, rows].cpu()[:, :, 3:], (value[:, :, 3:], bound[:, :, 3:]))
