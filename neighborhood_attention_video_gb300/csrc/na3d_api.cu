@@ -13,13 +13,13 @@
 #include "na3d_host.cuh"
 #include "na3d_kernel.cuh"
 #include "na3d_proj.cuh"
+#include "na3d_scored.cuh"
 
 namespace {
 
-using na3d::EncodeTiledFn;
 using na3d::KernelParams;
 using na3d::VariantInfo;
-using na3d::encode_fn;
+using na3d::encode_map;
 using na3d::encode_map_2d;
 using na3d::is_pow2;
 using na3d::mul_ok;
@@ -193,29 +193,6 @@ Plan choose_plan(const Axis& at, const Axis& ah, const Axis& aw, int hd) {
         if (best.bt == 0 || pl.cost <= best.cost) best = pl;
     }
     return best;
-}
-
-// ------------------------------------------------------------------ TMA descriptors
-
-// The (B,T,H,W,NH,HD) tensor viewed as 5-D (NH*HD, W, H, T, B), with
-// `token_stride` elements between consecutive grid positions: a box of
-// {hd_box, bx, by, bz, 1} at x = head*HD + column picks one head's rows.
-bool encode_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t T, int64_t H, int64_t W,
-                int64_t NH, int64_t HD, int64_t token_stride, int hd_box, int bx, int by, int bz) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[5] = {cuuint64_t(NH * HD), cuuint64_t(W), cuuint64_t(H), cuuint64_t(T),
-                                cuuint64_t(B)};
-    const cuuint64_t row = cuuint64_t(token_stride * 2);
-    const cuuint64_t strides[4] = {row, row * W, row * W * H, row * W * H * T};
-    const cuuint32_t box[5] = {cuuint32_t(hd_box), cuuint32_t(bx), cuuint32_t(by), cuuint32_t(bz), 1};
-    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    const CUtensorMapSwizzle swz = hd_box == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                   : hd_box == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -448,11 +425,12 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv, int
 }
 
 int na3d_device_status(void* stream) {
-    unsigned int flag = 0, pflag = 0;
+    unsigned int flag = 0, pflag = 0, sflag = 0;
     if (na3d::take_device_error(static_cast<cudaStream_t>(stream), &flag) != cudaSuccess ||
-        na3d::take_proj_error(static_cast<cudaStream_t>(stream), &pflag) != cudaSuccess)
+        na3d::take_proj_error(static_cast<cudaStream_t>(stream), &pflag) != cudaSuccess ||
+        na3d::take_scored_error(static_cast<cudaStream_t>(stream), &sflag) != cudaSuccess)
         return NA3D_ERR_CUDA;
-    return (flag || pflag) ? NA3D_ERR_DEVICE_TIMEOUT : NA3D_OK;
+    return (flag || pflag || sflag) ? NA3D_ERR_DEVICE_TIMEOUT : NA3D_OK;
 }
 
 }  // extern "C"

@@ -76,6 +76,27 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// The (B,T,H,W,NH,HD) tensor viewed as 5-D (NH*HD, W, H, T, B), with
+// `token_stride` elements between consecutive grid positions: a box of
+// {hd_box, bx, by, bz, 1} at x = head*HD + column picks one head's rows.
+inline bool encode_map(CUtensorMap* m, const void* ptr, int64_t B, int64_t T, int64_t H, int64_t W,
+                int64_t NH, int64_t HD, int64_t token_stride, int hd_box, int bx, int by, int bz) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[5] = {cuuint64_t(NH * HD), cuuint64_t(W), cuuint64_t(H), cuuint64_t(T),
+                                cuuint64_t(B)};
+    const cuuint64_t row = cuuint64_t(token_stride * 2);
+    const cuuint64_t strides[4] = {row, row * W, row * W * H, row * W * H * T};
+    const cuuint32_t box[5] = {cuuint32_t(hd_box), cuuint32_t(bx), cuuint32_t(by), cuuint32_t(bz), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapSwizzle swz = hd_box == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                   : hd_box == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                  : CU_TENSOR_MAP_SWIZZLE_32B;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A row-major (outer, inner) bf16 matrix as a 2-D tensor map with a
 // (box_inner, box_outer) box and the 128-byte swizzle (box_inner = 64).
 inline bool encode_map_2d(CUtensorMap* m, const void* ptr, int64_t inner, int64_t outer, int box_inner,

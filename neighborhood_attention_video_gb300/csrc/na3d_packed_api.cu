@@ -18,12 +18,14 @@ using na3d::overlaps;
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Heads of HD values every `stride` elements: bytes spanned, or an error.
-int strided_span(int64_t tokens, int64_t stride, int64_t row, int64_t* bytes) {
+// `row` values every `stride` elements: bytes spanned, or an error. The strides
+// of a TMA descriptor stay below 2^40 bytes: `grid` tokens of a batch entry.
+int strided_span(int64_t tokens, int64_t grid, int64_t stride, int64_t row, int64_t* bytes) {
     if (stride < row) return NA3D_ERR_SHAPE;
     if (stride % 8 != 0) return NA3D_ERR_ALIGN;
     int64_t span;
-    if (!mul_ok(tokens - 1, stride, &span) || !mul_ok(span + row, 2, bytes)) return NA3D_ERR_OVERFLOW;
+    if (stride >= (int64_t(1) << 39) / grid || !mul_ok(tokens - 1, stride, &span) || !mul_ok(span + row, 2, bytes))
+        return NA3D_ERR_OVERFLOW;
     return NA3D_OK;
 }
 
@@ -51,6 +53,7 @@ int check_scored(int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t
     // tanh(a / c) keeps its relative precision over this range of caps
     if (HD > 128 || !(softcap == 0.f || (softcap >= 0x1p-10f && softcap <= 0x1p20f))) return NA3D_ERR_UNSUPPORTED;
     *n = B * T * H * W;
+    if (*n >= (int64_t(1) << 34) / NH) return NA3D_ERR_OVERFLOW;   // rows, 16 to a unit of work
     if (!aligned(slopes, 4) || !aligned(doc, 4) || !aligned(prefix, 4)) return NA3D_ERR_ALIGN;
     return NA3D_OK;
 }
@@ -70,7 +73,7 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
     const void* in[3] = {q, k, v};
     int64_t bytes[3];
     for (int i = 0; i < 3; ++i)
-        if (const int rc = strided_span(n, ts[i], row, &bytes[i])) return rc;
+        if (const int rc = strided_span(n, T * H * W, ts[i], row, &bytes[i])) return rc;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4))
         return NA3D_ERR_ALIGN;
     const Span written[2] = {{out, n * row * 2}, {lse, n * NH * 4}};
@@ -101,7 +104,7 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
 }
 
 int64_t na3d_scored_bwd_workspace(int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH) {
-    int64_t n = 4;
+    int64_t n = 8;
     const int64_t dims[5] = {B, T, H, W, NH};
     for (const int64_t d : dims)
         if (d < 1 || !mul_ok(n, d, &n)) return -1;
@@ -124,18 +127,18 @@ int na3d_scored_bwd(const void* q, const void* k, const void* v, const void* out
                            dq_token_stride, dk_token_stride, dv_token_stride};
     int64_t bytes[6];
     for (int i = 0; i < 6; ++i)
-        if (const int rc = strided_span(n, ts[i], row, &bytes[i])) return rc;
+        if (const int rc = strided_span(n, T * H * W, ts[i], row, &bytes[i])) return rc;
     for (const void* p : all)
         if (!aligned(p, p == lse ? 4 : 16)) return NA3D_ERR_ALIGN;
     const void* const grads[3] = {dq, dk, dv};
-    const Span written[4] = {{dq, bytes[3]}, {dk, bytes[4]}, {dv, bytes[5]}, {work, n * NH * 4}};
+    const Span written[4] = {{dq, bytes[3]}, {dk, bytes[4]}, {dv, bytes[5]}, {work, n * NH * 8}};
     const Span read[9] = {{q, bytes[0]}, {k, bytes[1]}, {v, bytes[2]}, {out, n * row * 2}, {dout, n * row * 2},
                           {lse, n * NH * 4}, {slopes, NH * 12}, {doc, n * 4}, {prefix, B * 4}};
     for (const Span& a : written)
         for (const Span& b : read)
             if (b.ptr && overlaps(a.ptr, a.bytes, b.ptr, b.bytes)) return NA3D_ERR_ALIAS;
     for (int i = 0; i < 3; ++i) {
-        if (overlaps(work, n * NH * 4, grads[i], bytes[3 + i])) return NA3D_ERR_ALIAS;
+        if (overlaps(work, n * NH * 8, grads[i], bytes[3 + i])) return NA3D_ERR_ALIAS;
         for (int j = 0; j < i; ++j)
             if (written_overlap(grads[i], bytes[3 + i], ts[3 + i], grads[j], bytes[3 + j], ts[3 + j], row))
                 return NA3D_ERR_ALIAS;
@@ -157,7 +160,7 @@ int na3d_scored_bwd(const void* q, const void* k, const void* v, const void* out
     p.dq = static_cast<uint16_t*>(dq);
     p.dk = static_cast<uint16_t*>(dk);
     p.dv = static_cast<uint16_t*>(dv);
-    p.delta = static_cast<float*>(work);
+    p.stat = static_cast<float2*>(work);
     p.softcap = softcap;
     p.slopes = slopes;
     p.doc = doc;

@@ -12,25 +12,40 @@
 //   ds = p (dp - delta_i),  da = ds (1 - tanh(a / c)^2)
 //   dq_i = sum_j da k_j,  dk_j = sum_i da q_i,  dv_j = sum_i p dout_i.
 //
-// One warp computes one row of one head, its lanes splitting the head dim;
-// a masked key is skipped, so what it holds never reaches the row.
+// The tile kernel (scored_tiles) computes all three passes. One warp holds 16
+// rows, a small box of the grid, and streams the union of their windows in
+// steps of 16 keys through mma.sync. Why warps of 16 rows and not 128-row
+// tiles for tcgen05: what bounds this operator is the work on each score (cap,
+// bias, mask, exponential), and the union of a small box's windows holds half
+// as many scores that no row wants: 320 keys a row against 784 for a (3,7,7)
+// window of 147 keys and a 2 x 8 x 8 tile.
+//
+// The row functions compute one row of one head by one warp, its lanes
+// splitting the head dim, and skip masked keys, so what those hold never
+// reaches the row. They serve the rows of the tile kernel that met a value
+// that is not finite: 0 times infinity is not 0 in a tile's products.
+#include <atomic>
+#include <cstring>
 #include <cuda_bf16.h>
 
+#include "na3d_host.cuh"
 #include "na3d_scored.cuh"
+#include "sm103_ptx.cuh"
 
 namespace na3d {
 
+__device__ unsigned int g_scored_timeout_flag = 0;
+
 namespace {
 
-constexpr int kRowWarps = 8;
-
-__device__ __forceinline__ int win_start(int i, int K, int N) {
-    return max(0, min(i - K / 2, N - K));
+__host__ __device__ __forceinline__ int win_start(int i, int K, int N) {
+    const int s = i - K / 2 < N - K ? i - K / 2 : N - K;
+    return s > 0 ? s : 0;
 }
 
 // The queries whose windows hold position j of an axis: [first, last].
-__device__ __forceinline__ int inv_first(int j, int K) { return j < K ? 0 : j - K / 2; }
-__device__ __forceinline__ int inv_last(int j, int K, int N) { return j >= N - K ? N - 1 : j + K / 2; }
+__host__ __device__ __forceinline__ int inv_first(int j, int K) { return j < K ? 0 : j - K / 2; }
+__host__ __device__ __forceinline__ int inv_last(int j, int K, int N) { return j >= N - K ? N - 1 : j + K / 2; }
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -80,18 +95,6 @@ struct Pos {
 
 __device__ __forceinline__ int64_t token_of(const ScoredParams& p, int b, int t, int h, int w) {
     return ((int64_t(b) * p.T + t) * p.H + h) * p.W + w;
-}
-
-__device__ __forceinline__ Pos pos_of(const ScoredParams& p, int64_t row) {
-    Pos o;
-    o.head = int(row % p.NH);
-    o.token = row / p.NH;
-    int64_t r = o.token;
-    o.w = int(r % p.W); r /= p.W;
-    o.h = int(r % p.H); r /= p.H;
-    o.t = int(r % p.T);
-    o.b = int(r / p.T);
-    return o;
 }
 
 // May the query in document `qdoc` at frame qt see the key at frame kt?
@@ -153,7 +156,7 @@ __device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane) {
     if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-// Gradient of one query, and its delta.
+// Gradient of one query.
 template <int HD>
 __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
     Row<HD> q, g, acc, x, y;
@@ -164,7 +167,6 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
     const float lse = p.lse[row];
     // a row that sees nothing has no part in any gradient, whatever dout holds
     const float delta = lse == -INFINITY ? 0.f : g.dot(y);
-    if (lane == 0) p.delta[row] = delta;
     acc.zero();
     float slope[3], ds;
     load_slopes(p, o.head, slope);
@@ -208,54 +210,846 @@ __device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane) {
                 g.load(p.dout + row * HD, lane);
                 const float e = expf(s - lse);
                 dv.axpy(e, g);
-                dk.axpy(e * (g.dot(v) - p.delta[row]) * ds, x);
+                dk.axpy(e * (g.dot(v) - p.stat[row].y) * ds, x);
             }
     dk.store(p.dk + o.token * p.dk_ts + int64_t(o.head) * HD, lane);
     dv.store(p.dv + o.token * p.dv_ts + int64_t(o.head) * HD, lane);
 }
 
+// ------------------------------------------------------------------ tiles
+
 enum { kFwd, kDq, kDkv };
 
-template <int HD, int MODE>
-__global__ void __launch_bounds__(kRowWarps * 32) scored_rows(const ScoredParams p) {
-    const int64_t rows = int64_t(p.B) * p.T * p.H * p.W * p.NH;
-    const int lane = threadIdx.x & 31;
-    for (int64_t r = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); r < rows;
-         r += int64_t(gridDim.x) * kRowWarps) {
-        const Pos o = pos_of(p, r);
-        if (MODE == kFwd) row_fwd<HD>(p, o, lane);
-        else if (MODE == kDq) row_dq<HD>(p, o, lane);
-        else row_dkv<HD>(p, o, lane);
+// Blocks an SM holds, and the most warps of a block: as many rows in flight as
+// the registers of an instance allow (accumulators, fixed fragments and about
+// 60 more a thread).
+__host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= (mode == kDkv ? 32 : 64) ? 2 : 1; }
+__host__ __device__ constexpr int max_warps(int hd, int mode) {
+    return blocks_per_sm(hd, mode) == 2 || hd > 64 ? 8 : 12;
+}
+// Buffers of the fixed tensors: two where a step reads them again (their
+// fragments and the accumulators together exceed the registers).
+__host__ __device__ constexpr int fixed_buffers(int hd, int mode) { return hd > 64 && mode == kDkv ? 2 : 1; }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;      // log2 growth of the scores past the kept maximum before a rescale
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 500000000ull;
+constexpr int kMaxStages = 4, kMaxRing = kMaxStages + 2;   // ring places: stages and fixed buffers
+
+// The positions that row i of an axis of length N meets: keys of its window
+// (FWD, DQ), or the queries whose windows hold it (DKV). Both ends grow with i.
+__host__ __device__ __forceinline__ int range_lo(bool dkv, int i, int K, int N) {
+    return dkv ? inv_first(i, K) : win_start(i, K, N);
+}
+__host__ __device__ __forceinline__ int range_hi(bool dkv, int i, int K, int N) {   // exclusive
+    return dkv ? inv_last(i, K, N) + 1 : win_start(i, K, N) + K;
+}
+
+// Geometry of one launch. A block's brick is st x (nw * sh) x sw rows, warp w
+// the sh grid rows from w * sh; its columns stream in chunks of one frame,
+// cr grid rows and cc columns. sw <= 8, so that rows r and r + 8 of a warp, a
+// thread's two, lie in one column of the grid.
+struct TileGeom {
+    int32_t st, sh, sw, nw, bh;
+    int32_t nbt, nbh, nbw;
+    int32_t cr, cc;
+    int32_t nt, nhc, nwc;      // chunks of a unit: frames, and parts along H and W
+    int32_t stages;
+    int32_t mask_steps;        // steps whose mask words fit a warp's buffer
+    int32_t mask_kept;         // 1: they hold a whole unit, and serve all heads of a brick
+    int32_t units;             // (brick, head) pairs, head fastest
+    // shared memory, bytes from a 1024-byte boundary
+    int32_t x_bytes;           // one streamed tensor of a stage (regions of 64 columns)
+    int32_t off_x, off_stat, off_mask, off_hw, off_bar, smem;
+};
+
+struct Sync {
+    uint32_t bar0;
+    volatile uint32_t* abort_flag;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
+    // Wait for a barrier phase; false once this block has given up.
+    __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
+        if (mbar_try_wait(b, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(b, parity)) return true;
+            if ((it & 255u) == 0u) {
+                if (*abort_flag) return false;
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    *abort_flag = 1u;
+                    atomicOr(&g_scored_timeout_flag, 1u);
+                    return false;
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of the 16-byte chunk c of row r in a box of HD-column rows as
+// TMA writes it: rows of up to 128 bytes, their chunks permuted over the
+// banks; HD 128 takes two such regions.
+template <int HD>
+__device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t region) {
+    if (HD == 16) return uint32_t(r) * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+    if (HD == 32) return uint32_t(r) * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return (c >> 3) * region + uint32_t(r) * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// tanh to about 2^-22 of its value. Up to 1/2 (a score of half the cap) an odd
+// polynomial, fitted for the least largest relative error (1.5e-8), keeps the
+// special-function unit free; larger values take 1 - 2 / (1 + e^2|z|), once
+// any of the warp's needs it.
+__device__ __forceinline__ float tanh_poly(float z) {
+    const float y = z * z;
+    float p = fmaf(y, 0.0172414667904377f, -0.05304548144340515f);
+    p = fmaf(y, p, 0.13325878977775574f);
+    p = fmaf(y, p, -0.333331435918808f);
+    return fmaf(z * y, p, z);
+}
+__device__ __forceinline__ float tanh_exp(float z) {
+    const float e = ex2_approx(fabsf(z) * (2.f * kLog2e));
+    return copysignf(fmaf(-2.f, rcp_approx(e + 1.f), 1.f), z);
+}
+
+template <int N>
+__device__ __forceinline__ void tanh_all(float* z) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
+    if (__any_sync(0xffffffffu, !(big <= 0.5f))) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = fabsf(z[i]) <= 0.5f ? tanh_poly(z[i]) : tanh_exp(z[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = tanh_poly(z[i]);
     }
 }
 
-int row_grid(const ScoredParams& p, int sms) {
-    const int64_t rows = int64_t(p.B) * p.T * p.H * p.W * p.NH;
-    const int64_t need = (rows + kRowWarps - 1) / kRowWarps;
-    return int(need < int64_t(sms) * 8 ? need : int64_t(sms) * 8);
+struct Brick {
+    int b, t0, h0, w0;   // first row
+};
+
+__device__ __forceinline__ Brick brick_of(const TileGeom& g, int n) {
+    Brick o;
+    o.w0 = n % g.nbw * g.sw; n /= g.nbw;
+    o.h0 = n % g.nbh * g.bh; n /= g.nbh;
+    o.t0 = n % g.nbt * g.st;
+    o.b = n / g.nbt;
+    return o;
 }
 
+// Union of the ranges of n rows from i (rows past the axis end count as the last).
+__device__ __forceinline__ int2 box_of(bool dkv, int i, int n, int K, int N) {
+    const int first = min(i, N - 1), last = min(i + n - 1, N - 1);
+    return make_int2(range_lo(dkv, first, K, N), range_hi(dkv, last, K, N));
+}
+
+// Mask bits of one step (16 columns from index i0 of a warp's box in a chunk)
+// for the warp's 16 rows: word g holds row g in its low and row g + 8 in its
+// high half. A lane computes half the columns of one row.
+template <bool DKV>
+__device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom& g, uint32_t* words, int b, int rt,
+                                          int rh, int rw, bool rvalid, int rdoc, int prefix, int t, int h0, int w0,
+                                          int rows, int i0) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bits = 0;
+    if (rvalid) {
+        const int lt = range_lo(DKV, rt, p.KT, p.T), ht = range_hi(DKV, rt, p.KT, p.T);
+        const int lh = range_lo(DKV, rh, p.KH, p.H), hh = range_hi(DKV, rh, p.KH, p.H);
+        const int lw = range_lo(DKV, rw, p.KW, p.W), hw = range_hi(DKV, rw, p.KW, p.W);
+        bool frame = t >= lt && t < ht;
+        if (p.prefix) {
+            const int qt = DKV ? t : rt, kt = DKV ? rt : t;
+            frame = frame && (kt <= qt || kt < prefix);
+        }
+        if (frame && !(p.doc && rdoc < 0)) {
+            const int first = i0 + 8 * (lane >> 4);
+            int y = first / g.cc, x = first - y * g.cc;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int h = h0 + y, w = w0 + x;
+                bool ok = y < rows && h >= lh && h < hh && w >= lw && w < hw;
+                if (ok && p.doc) ok = p.doc[token_of(p, b, t, h, w)] == rdoc;
+                bits |= uint32_t(ok) << i;
+                if (++x == g.cc) { x = 0; ++y; }
+            }
+        }
+    }
+    // columns 8..15 join 0..7 (lanes 16 + r and r), then rows r and r + 8
+    bits |= __shfl_down_sync(0xffffffffu, bits, 16) << 8;
+    bits |= __shfl_down_sync(0xffffffffu, bits, 8) << 16;
+    if (lane < 8) words[lane] = bits;
+}
+
+// One persistent block; nw warps, 16 rows each.
+//   FWD: fixed rows Q; streamed K, V. DQ: fixed Q, dO; streamed K, V.
+//   DKV: fixed K, V; streamed Q, dO and each query's (lse, delta).
+// A block takes a contiguous run of units, so consecutive units mostly share
+// their brick, and with it the mask words. The warps run freely over a ring of
+// stages; the warp that is last to be done with a stage starts the load of the
+// chunk that is next to use it, so no warp waits for an empty stage and none
+// is kept for loading (a ninth would cost the other eight a fifth of their
+// registers).
+template <int HD, int MODE>
+__global__ void __launch_bounds__(max_warps(HD, MODE) * 32, blocks_per_sm(HD, MODE))
+scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ CUtensorMap tm_f1,
+             const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
+             const ScoredParams p, const TileGeom g) {
+    constexpr bool DKV = MODE == kDkv;
+    constexpr int NF = MODE == kFwd ? 1 : 2;           // fixed tensors
+    constexpr int FB = fixed_buffers(HD, MODE);
+    constexpr int NFR = FB == 2 ? 1 : NF;              // fixed tensors whose fragments stay in registers
+    constexpr int KB = HD / 16;                        // 16-column blocks of the head dim
+    constexpr int REG = HD > 64 ? HD / 64 : 1;         // 64-column regions
+    constexpr int HDB = HD > 64 ? 64 : HD;             // columns of a box
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nw = g.nw, S = g.stages;
+    const int f_rows = g.st * g.bh * g.sw;
+    const uint32_t f_region = (uint32_t(f_rows) * HDB * 2 + 1023u) & ~1023u, f_bytes = f_region * REG;
+    const uint32_t x_region = g.x_bytes / REG;
+
+    // control words: abort flag, then done and issued counts of each ring
+    // (the stages, then the fixed buffers); barriers: one a ring place
+    uint32_t* misc = reinterpret_cast<uint32_t*>(base_ptr + g.off_bar);
+    const Sync sy{base + g.off_bar + 64, misc};
+    uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S + FB; ++i) {
+            mbar_init(sy.bar(i), DKV && i < S ? 33 : 1);
+            done[i] = 0;
+            issued[i] = 0;
+        }
+        misc[0] = 0u;
+        fence_mbar_init();
+    }
+    // The stages start as zeros: a step reads up to 15 rows past a chunk's box,
+    // whose probabilities are 0, and those rows must hold numbers.
+    for (int i = threadIdx.x * 16; i < 2 * S * g.x_bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4*>(base_ptr + g.off_x + i) = make_uint4(0, 0, 0, 0);
+    if (DKV)
+        for (int i = threadIdx.x * 8; i < g.off_mask - g.off_stat; i += blockDim.x * 8)
+            *reinterpret_cast<uint2*>(base_ptr + g.off_stat + i) = make_uint2(0, 0);
+    // (row, column) of the chunk's index, as floats
+    float2* const hw = reinterpret_cast<float2*>(base_ptr + g.off_hw);
+    for (int i = threadIdx.x; i < g.cr * g.cc + 16; i += blockDim.x)
+        hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
+    fence_proxy_async_smem();
+    __syncthreads();
+
+    const int u0 = int(int64_t(g.units) * blockIdx.x / gridDim.x);
+    const int u1 = int(int64_t(g.units) * (blockIdx.x + 1) / gridDim.x);
+    const int per_unit = g.nt * g.nhc * g.nwc;
+    const int stat_rows = g.cr * g.cc + 16;
+
+    // Start the load of chunk c of unit u into stage s (a whole warp). A chunk
+    // past the brick's own box (the boxes at the borders are smaller) brings nothing.
+    auto load_chunk = [&](int u, int c, int s) {
+        const Brick o = brick_of(g, u / p.NH);
+        const int head = u % p.NH;
+        const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
+        const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
+        const int t = bt.x + c / (g.nhc * g.nwc), h = bh.x + c / g.nwc % g.nhc * g.cr, w = bw.x + c % g.nwc * g.cc;
+        const bool inside = t < bt.y && h < bh.y && w < bw.y;
+        const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * g.x_bytes;
+        if (lane == 0) {
+            ++issued[s];
+            if (inside) {
+                mbar_arrive_expect_tx(full, 2 * REG * g.cr * g.cc * HDB * 2);
+                for (int r = 0; r < REG; ++r) {
+                    tma_load_5d(x0 + r * x_region, &tm_x0, full, head * HD + r * 64, w, h, t, o.b);
+                    tma_load_5d(x0 + g.x_bytes + r * x_region, &tm_x1, full, head * HD + r * 64, w, h, t, o.b);
+                }
+            } else {
+                mbar_arrive(full);
+            }
+        }
+        if (DKV) {
+            const uint32_t st = base + g.off_stat + s * stat_rows * 8;
+            if (inside)
+                for (int i = lane; i < g.cr * g.cc; i += 32) {
+                    const int y = h + i / g.cc, x = w + i % g.cc;
+                    if (y < p.H && x < p.W) {
+                        const float2* src = p.stat + token_of(p, o.b, t, y, x) * p.NH + head;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + i * 8), "l"(src) : "memory");
+                    }
+                }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        }
+    };
+    auto load_fixed = [&](int u, int f) {   // one thread
+        const Brick o = brick_of(g, u / p.NH);
+        const int head = u % p.NH;
+        const uint32_t full = sy.bar(S + f), x = base + f * NF * f_bytes;
+        ++issued[S + f];
+        mbar_arrive_expect_tx(full, NF * REG * f_rows * HDB * 2);
+        for (int r = 0; r < REG; ++r) {
+            tma_load_5d(x + r * f_region, &tm_f0, full, head * HD + r * 64, o.w0, o.h0, o.t0, o.b);
+            if (NF == 2) tma_load_5d(x + f_bytes + r * f_region, &tm_f1, full, head * HD + r * 64, o.w0, o.h0, o.t0, o.b);
+        }
+    };
+    // This warp is done with a ring place; true where it is the last to be.
+    auto last_done = [&](int i) {
+        uint32_t n = 0;
+        __syncwarp();
+        if (lane == 0)
+            asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;"
+                         : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
+        return __shfl_sync(0xffffffffu, n, 0) == uint32_t(nw - 1);
+    };
+    if (warp == 0 && u0 < u1) {
+        for (int f = 0; f < FB; ++f)
+            if (lane == 0 && u0 + f < u1) load_fixed(u0 + f, f);
+        for (int s = 0; s < S; ++s)
+            if (u0 + s / per_unit < u1) load_chunk(u0 + s / per_unit, s % per_unit, s);
+    }
+
+    const int r0 = lane >> 2, c2 = lane & 3;    // this thread's rows r0, r0 + 8 and column pair of a fragment
+    const int hi = lane >> 4;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(base_ptr + g.off_mask) + warp * g.mask_steps * 8;
+    const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
+    const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
+    const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
+    uint32_t it = 0, ft = 0;
+    int mask_brick = -1;
+    bool ok = true;
+
+    for (int u = u0; u < u1; ++u, ++ft) {
+        const int nb = u / p.NH;
+        const Brick o = brick_of(g, nb);
+        const int head = u % p.NH;
+        const int wh0 = o.h0 + warp * g.sh;
+        const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
+        const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
+        // this warp's part of the streamed rows; none where its rows lie past the grid
+        int2 mine = box_of(DKV, wh0, g.sh, p.KH, p.H);
+        if (wh0 >= p.H) mine = make_int2(0, 0);
+
+        // the row of mask_step: lane & 15
+        const int mr = lane & 15;
+        const int mw = o.w0 + mr % g.sw, mh = wh0 + mr / g.sw % g.sh, mt = o.t0 + mr / (g.sw * g.sh);
+        const bool mvalid = mw < p.W && mh < p.H && mt < p.T;
+        const int mdoc = p.doc && mvalid ? p.doc[token_of(p, o.b, mt, mh, mw)] : 0;
+        const int prefix = p.prefix ? p.prefix[o.b] : 0;
+        auto box_rows = [&](int h, int* first) {   // rows of this warp in the chunk at h
+            *first = max(mine.x, h);
+            return min(mine.y, h + g.cr) - *first;
+        };
+        if (g.mask_kept && nb != mask_brick) {
+            int ms = 0;
+            __syncwarp();
+            for (int t = bt.x; t < bt.y; ++t)
+                for (int h = bh.x; h < bh.y; h += g.cr)
+                    for (int w = bw.x; w < bw.y; w += g.cc) {
+                        int hf;
+                        const int rows = box_rows(h, &hf);
+                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16, ++ms)
+                            mask_step<DKV>(p, g, mask + ms * 8, o.b, mt, mh, mw, mvalid, mdoc, prefix, t, hf, w, rows, i0);
+                    }
+            __syncwarp();
+            mask_brick = nb;
+        }
+
+        // rows r0 and r0 + 8, in one column of the grid
+        const int rw = o.w0 + r0 % g.sw;
+        int rt[2], rh[2];
+        int64_t row[2];   // token * NH + head, -1 past the grid
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = r0 + 8 * i;
+            rh[i] = wh0 + r / g.sw % g.sh;
+            rt[i] = o.t0 + r / (g.sw * g.sh);
+            row[i] = rw < p.W && rh[i] < p.H && rt[i] < p.T ? token_of(p, o.b, rt[i], rh[i], rw) * p.NH + head : -1;
+        }
+        float sl[3] = {0.f, 0.f, 0.f};
+        if (biased) {
+            load_slopes(p, head, sl);
+#pragma unroll
+            for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
+        }
+        float ref[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};   // log2 reference that scores are taken from
+        if (MODE == kDq) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (row[i] >= 0) {
+                    const float2 s = p.stat[row[i]];
+                    ref[i] = s.x * kLog2e;
+                    delta[i] = s.y;
+                }
+        }
+
+        // fixed fragments
+        uint32_t fa[NFR][KB][4];
+        const int fb = ft % FB;
+        if (!(ok = ok && sy.wait(sy.bar(S + fb), (ft / FB) & 1u))) break;
+        const int fr = (((lane & 15) / (g.sw * g.sh)) * g.bh + warp * g.sh + (lane & 15) / g.sw % g.sh) * g.sw + (lane & 15) % g.sw;
+        const uint32_t f_at = base + fb * NF * f_bytes;
+#pragma unroll
+        for (int n = 0; n < NFR; ++n)
+#pragma unroll
+            for (int kk = 0; kk < KB; ++kk) ldsm4(f_at + n * f_bytes + swizzled<HD>(fr, 2 * kk + hi, f_region), fa[n][kk]);
+        if (NFR == NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(u + FB, fb);
+
+        float acc0[2 * KB][4], acc1[MODE == kDkv ? 2 * KB : 1][4];   // O, dQ or dK; dV
+#pragma unroll
+        for (int j = 0; j < 2 * KB; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc0[j][i] = 0.f;
+                if (MODE == kDkv) acc1[j][i] = 0.f;
+            }
+        // FWD: the sum of e^(s - ref), and the growth that moves the reference:
+        // any for a row that has met no key, so that ref starts at a score
+        float l[2] = {0.f, 0.f}, grow[2] = {-INFINITY, -INFINITY};
+
+        int ms = 0;
+        for (int c = 0; c < per_unit; ++c, ++it) {
+            const int s = it % S;
+            if (!(ok = sy.wait(sy.bar(s), (it / S) & 1u))) break;
+            const int t = bt.x + c / (g.nhc * g.nwc), h = bh.x + c / g.nwc % g.nhc * g.cr, w = bw.x + c % g.nwc * g.cc;
+            int hf;
+            const int rows = box_rows(h, &hf);
+            const int n = t < bt.y && h < bh.y && w < bw.y ? rows * g.cc : 0;
+            const uint32_t x0 = base + g.off_x + 2 * s * g.x_bytes, x1 = x0 + g.x_bytes;
+            const int first = (hf - h) * g.cc;
+            const float2* stat = reinterpret_cast<const float2*>(base_ptr + g.off_stat + s * stat_rows * 8) + first;
+            if (!g.mask_kept) {
+                ms = 0;
+                __syncwarp();
+                for (int i0 = 0, k = 0; i0 < n; i0 += 16, ++k)
+                    mask_step<DKV>(p, g, mask + k * 8, o.b, mt, mh, mw, mvalid, mdoc, prefix, t, hf, w, rows, i0);
+                __syncwarp();
+            }
+            const float far_t[2] = {sl[0] * float(abs(t - rt[0])), sl[0] * float(abs(t - rt[1]))};
+            const float at_h[2] = {float(hf - rh[0]), float(hf - rh[1])}, at_w = float(w - rw);
+            for (int i0 = 0; i0 < n; i0 += 16, ++ms) {
+                const int xr = first + i0 + (lane & 15);
+                // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of
+                // row (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1)
+                float sc[8] = {}, dp[8] = {};
+                uint32_t f[4];
+#pragma unroll
+                for (int kk = 0; kk < KB; ++kk) {
+                    ldsm4(x0 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                    mma16816(sc, fa[0][kk], f[0], f[2]);
+                    mma16816(sc + 4, fa[0][kk], f[1], f[3]);
+                }
+                if (MODE != kFwd) {
+#pragma unroll
+                    for (int kk = 0; kk < KB; ++kk) {
+                        uint32_t a[4];
+                        if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(fr, 2 * kk + hi, f_region), a);
+                        ldsm4(x1 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        mma16816(dp, NFR < NF ? a : fa[NFR - 1][kk], f[0], f[2]);
+                        mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], f[1], f[3]);
+                    }
+                }
+                const uint32_t bits = mask[ms * 8 + r0] >> (2 * c2);   // 0, 1, 8, 9 of row r0; 16, 17, 24, 25 of r0 + 8
+                auto seen = [&](int i) { return (bits >> (8 * (i >> 2) + 16 * ((i >> 1) & 1) + (i & 1)) & 1u) != 0u; };
+                float2 cs[4];   // DKV: (log2 reference, delta) of the four columns
+                if (DKV) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        cs[j] = stat[i0 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
+                        cs[j].x *= kLog2e;
+                    }
+                }
+                float sv[8];   // score minus reference, log2
+                if (biased) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // column 8 * (j >> 1) + 2 * c2 + (j & 1)
+                        const float2 x = hw[i0 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
+                        const float dw = fabsf(x.y + at_w);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sv[4 * (j >> 1) + 2 * i + (j & 1)] =
+                                fmaf(sl[1], fabsf(x.x + at_h[i]), fmaf(sl[2], dw, far_t[i] - (DKV ? cs[j].x : ref[i])));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sv[i] = -(DKV ? cs[2 * (i >> 2) + (i & 1)].x : ref[(i >> 1) & 1]);
+                }
+                if (capped) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sc[i] *= inv_cap;
+                    tanh_all<8>(sc);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sv[i] = fmaf(sc[i], to_log2, sv[i]);
+                if (MODE == kFwd) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sv[i] = seen(i) ? sv[i] : -INFINITY;
+                    float top[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        top[i] = fmaxf(max3f(sv[2 * i], sv[2 * i + 1], sv[4 + 2 * i]), sv[5 + 2 * i]);
+                    if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = top[i];
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                            // a row that has met a key moves up only; the first keys set the reference
+                            if (grow[i] == kGrow || x == -INFINITY) x = fmaxf(x, 0.f);
+                            else grow[i] = -kGrow;
+                            const float r = grow[i] == kGrow ? ex2_approx(-x) : 0.f;
+                            if (grow[i] == -kGrow) grow[i] = kGrow;
+                            ref[i] += x;
+                            l[i] *= r;
+#pragma unroll
+                            for (int j = 0; j < 2 * KB; ++j) {
+                                acc0[j][2 * i] *= r;
+                                acc0[j][2 * i + 1] *= r;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) sv[4 * (j >> 1) + 2 * i + (j & 1)] -= x;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        sv[i] = ex2_approx(sv[i]);
+                        l[(i >> 1) & 1] += sv[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = ex2_approx(sv[i]);
+                        float d = e * (dp[i] - (DKV ? cs[2 * (i >> 2) + (i & 1)].y : delta[(i >> 1) & 1]));
+                        if (capped) d *= fmaf(-sc[i], sc[i], 1.f);
+                        sv[i] = seen(i) ? e : 0.f;
+                        dp[i] = seen(i) ? d : 0.f;
+                    }
+                }
+                // products: probabilities (FWD: with V; DKV: with dO) and da (with K or Q)
+                if (MODE != kDq) {
+                    const uint32_t a[4] = {pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]),
+                                           pack_bf16x2(sv[4], sv[5]), pack_bf16x2(sv[6], sv[7])};
+#pragma unroll
+                    for (int kk = 0; kk < KB; ++kk) {
+                        ldsm4t(x1 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        mma16816(MODE == kFwd ? acc0[2 * kk] : acc1[MODE == kDkv ? 2 * kk : 0], a, f[0], f[1]);
+                        mma16816(MODE == kFwd ? acc0[2 * kk + 1] : acc1[MODE == kDkv ? 2 * kk + 1 : 0], a, f[2], f[3]);
+                    }
+                }
+                if (MODE != kFwd) {
+                    const uint32_t a[4] = {pack_bf16x2(dp[0], dp[1]), pack_bf16x2(dp[2], dp[3]),
+                                           pack_bf16x2(dp[4], dp[5]), pack_bf16x2(dp[6], dp[7])};
+#pragma unroll
+                    for (int kk = 0; kk < KB; ++kk) {
+                        ldsm4t(x0 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        mma16816(acc0[2 * kk], a, f[0], f[1]);
+                        mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
+                    }
+                }
+            }
+            // the stage's next chunk is S further on
+            if (last_done(s)) {
+                const int n_next = c + S;
+                const int u_next = u + n_next / per_unit;
+                if (u_next < u1) load_chunk(u_next, n_next % per_unit, s);
+            }
+        }
+        if (!ok) break;
+        if (NFR < NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(u + FB, fb);
+
+        // rows out; a row that is not finite throughout is computed again by itself
+        uint32_t bad = 0;
+        float inv[2] = {1.f, 1.f};
+        if (MODE == kFwd) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                inv[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
+                if (row[i] >= 0 && c2 == 0 && p.lse)
+                    p.lse[row[i]] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
+                if (!(l[i] < INFINITY)) bad |= 1u << i;
+            }
+        }
+        uint16_t* const out0 = MODE == kFwd ? p.out : MODE == kDq ? p.dq : p.dk;
+        const int64_t ts0 = MODE == kFwd ? int64_t(p.NH) * HD : MODE == kDq ? p.dq_ts : p.dk_ts;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool valid = row[i] >= 0;
+            const int64_t token = valid ? token_of(p, o.b, rt[i], rh[i], rw) : 0;
+            uint16_t* const at0 = out0 + token * ts0 + int64_t(head) * HD + 2 * c2;
+            uint16_t* const at1 = p.dv + token * p.dv_ts + int64_t(head) * HD + 2 * c2;
+            float probe = 0.f;   // 0 times every value: NaN where one is not finite
+#pragma unroll
+            for (int j = 0; j < 2 * KB; ++j) {
+                const float x = acc0[j][2 * i] * inv[i], y = acc0[j][2 * i + 1] * inv[i];
+                probe = fmaf(x, 0.f, fmaf(y, 0.f, probe));
+                if (valid) *reinterpret_cast<uint32_t*>(at0 + 8 * j) = pack_bf16x2(x, y);
+                if (MODE == kDkv) {
+                    const float x1 = acc1[j][2 * i], y1 = acc1[j][2 * i + 1];
+                    probe = fmaf(x1, 0.f, fmaf(y1, 0.f, probe));
+                    if (valid) *reinterpret_cast<uint32_t*>(at1 + 8 * j) = pack_bf16x2(x1, y1);
+                }
+            }
+            if (probe != 0.f) bad |= 1u << i;
+            if (!valid) bad &= ~(1u << i);
+        }
+        if (__any_sync(0xffffffffu, bad != 0u)) {
+            for (int r = 0; r < 16; ++r) {
+                if (!__ballot_sync(0xffffffffu, (bad >> (r >> 3) & 1u) && r0 == (r & 7))) continue;
+                Pos q;
+                q.b = o.b;
+                q.w = o.w0 + r % g.sw;
+                q.h = wh0 + r / g.sw % g.sh;
+                q.t = o.t0 + r / (g.sw * g.sh);
+                q.head = head;
+                q.token = token_of(p, q.b, q.t, q.h, q.w);
+                __syncwarp();
+                if (MODE == kFwd) row_fwd<HD>(p, q, lane);
+                else if (MODE == kDq) row_dq<HD>(p, q, lane);
+                else row_dkv<HD>(p, q, lane);
+            }
+        }
+    }
+
+    // every issued load lands before the block may exit: where all went well
+    // each has been waited for
+    if (DKV) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (misc[0] && threadIdx.x == 0)
+        for (int i = 0; i < S + FB; ++i)
+            if (issued[i] && !mbar_wait_bounded(sy.bar(i), (issued[i] - 1u) & 1u, kDrainLimitNs))
+                atomicOr(&g_scored_timeout_flag, 1u);
+}
+
+// (lse, delta) of every row for the backward passes: delta_i = dout_i . out_i;
+// a row that sees nothing gets (0, 0). A row takes HD / 8 lanes, 16 bytes each.
 template <int HD>
-cudaError_t fwd(const ScoredParams& p, int sms, cudaStream_t stream) {
-    scored_rows<HD, kFwd><<<row_grid(p, sms), kRowWarps * 32, 0, stream>>>(p);
+__global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t rows) {
+    constexpr int L = HD / 8;
+    const int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
+    const int c = threadIdx.x % L;
+    const bool live = r < rows;
+    float d = 0.f;
+    if (live) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p.out + r * HD + c * 8);
+        const uint4 b = *reinterpret_cast<const uint4*>(p.dout + r * HD + c * 8);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), d);
+            d = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), d);
+        }
+    }
+#pragma unroll
+    for (int k = L / 2; k; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
+    if (live && c == 0) {
+        const float lse = p.lse[r];
+        p.stat[r] = lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse, d);
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+// Largest union of the ranges of `step` consecutive rows that start at a
+// multiple of step: inside an axis K + step - 1; a key near a border is held
+// by up to K + K/2 queries' windows, most in the rows around K and N - K.
+int widest(bool dkv, int step, int K, int N) {
+    const int inner = K + step - 1 < N ? K + step - 1 : N;
+    if (!dkv) return inner;
+    int best = inner;
+    const int at[2] = {(K - 1) / step * step, (N - K) / step * step};
+    for (const int i : at) {
+        const int last = i + step - 1 < N ? i + step - 1 : N - 1;
+        const int e = range_hi(true, last, K, N) - range_lo(true, i, K, N);
+        if (e > best) best = e;
+    }
+    return best;
+}
+
+int align_up(int x, int a) { return (x + a - 1) / a * a; }
+
+constexpr int kSmemMax = 227 * 1024;
+
+// Shared memory of a geometry with `stages` stages and chunks of cr x cc.
+void lay_out(TileGeom* g, int hd, int mode) {
+    const bool dkv = mode == kDkv;
+    const int nf = (mode == kFwd ? 1 : 2) * fixed_buffers(hd, mode);
+    const int hdb = hd > 64 ? 64 : hd, reg = hd > 64 ? hd / 64 : 1;
+    const int f_region = align_up(g->st * g->bh * g->sw * hdb * 2, 1024);
+    g->x_bytes = align_up((g->cr * g->cc + 16) * hdb * 2, 1024) * reg;
+    g->off_x = f_region * reg * nf;
+    g->off_stat = g->off_x + 2 * g->stages * g->x_bytes;
+    g->off_mask = g->off_stat + (dkv ? g->stages * (g->cr * g->cc + 16) * 8 : 0);
+    g->off_hw = g->off_mask + g->nw * g->mask_steps * 32;
+    g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
+    g->smem = g->off_bar + 64 + 8 * kMaxRing + 1024;
+}
+
+// Chooses rows, brick and chunks for the least modelled time.
+bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms) {
+    const bool dkv = mode == kDkv;
+    const int blocks = blocks_per_sm(hd, mode);
+    double best_cost = 0;
+    bool found = false;
+    for (int st = 1; st <= 16; st *= 2)
+        for (int sh = 1; st * sh <= 16; sh *= 2) {
+            const int sw = 16 / (st * sh);
+            if (sw > 8) continue;
+            const int et = widest(dkv, st, p.KT, p.T), ew = widest(dkv, sw, p.KW, p.W);
+            const int eh_w = widest(dkv, sh, p.KH, p.H);
+            for (int nw = 1; nw <= max_warps(hd, mode); nw += nw < 4 ? nw : 4) {
+                if (nw > 1 && (nw / 2) * sh >= p.H) break;
+                TileGeom g{};
+                g.st = st; g.sh = sh; g.sw = sw; g.nw = nw; g.bh = nw * sh;
+                if (g.bh > 256) continue;
+                g.nbt = (p.T + st - 1) / st;
+                g.nbh = (p.H + g.bh - 1) / g.bh;
+                g.nbw = (p.W + sw - 1) / sw;
+                const int64_t units = int64_t(p.B) * g.nbt * g.nbh * g.nbw * p.NH;
+                if (units >= (int64_t(1) << 31)) continue;
+                g.units = int32_t(units);
+                const int eh = widest(dkv, g.bh, p.KH, p.H);
+                // chunks: whole rows of the box, as many as leave room for two
+                // stages; narrower ones where a single row does not
+                const int room = kSmemMax / blocks - 1024;
+                g.nwc = (ew + 255) / 256;
+                for (int parts = (eh + 255) / 256;; ++parts) {
+                    g.cc = (ew + g.nwc - 1) / g.nwc;
+                    g.cr = (eh + parts - 1) / parts;
+                    const int nhc = (eh + g.cr - 1) / g.cr;
+                    g.nt = et;
+                    g.nhc = nhc;
+                    // steps of a warp: its box in each chunk that it meets, rounded up to 16
+                    const int met = (eh_w + g.cr - 2) / g.cr + 1 < nhc ? (eh_w + g.cr - 2) / g.cr + 1 : nhc;
+                    const int all = et * g.nwc * ((eh_w * g.cc + 15) / 16 + met - 1);
+                    g.mask_steps = all;
+                    g.mask_kept = 1;
+                    g.stages = 2;
+                    lay_out(&g, hd, mode);
+                    if (g.smem > room) {   // masks chunk by chunk where a unit's do not fit
+                        g.mask_kept = 0;
+                        g.mask_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
+                        lay_out(&g, hd, mode);
+                    }
+                    if (g.smem > room) {
+                        if (g.cr > 1) continue;
+                        if (g.cc == 1) break;   // never: a column a chunk fits
+                        g.nwc *= 2;
+                        parts = (eh + 255) / 256 - 1;
+                        continue;
+                    }
+                    while (g.stages < kMaxStages) {
+                        TileGeom more = g;
+                        ++more.stages;
+                        lay_out(&more, hd, mode);
+                        if (more.smem > room) break;
+                        g = more;
+                    }
+                    const double steps = double(all) * (g.mask_kept ? 1.0 : 1.6);
+                    const double slots = double(sms) * blocks;
+                    const double waves = g.units <= slots ? 1.0 : double(g.units) / slots;
+                    // cycles of a unit: steps of its warps sharing the SM's schedulers, or their own
+                    // latency, or the bytes that its chunks bring in
+                    const double work = steps * nw * blocks * 28.0, lat = steps * 300.0;
+                    const double load = double(et) * g.nwc * nhc * g.cr * g.cc * hd * 4 * blocks / 45.0;
+                    const double unit = (work > lat ? work : lat) + 0.5 * load + 3000.0;
+                    const double cost = waves * unit;
+                    if (!found || cost < best_cost) {
+                        found = true;
+                        best_cost = cost;
+                        *best = g;
+                    }
+                    if (g.mask_kept || g.cr == 1) break;
+                }
+            }
+        }
+    return found;
+}
+
+// The plan of a call; a thread keeps the last few, since the search takes
+// some microseconds.
+bool cached_plan(TileGeom* out, const ScoredParams& p, int hd, int mode, int sms) {
+    struct Entry {
+        int32_t key[11];
+        TileGeom g;
+    };
+    static thread_local Entry cache[16] = {};
+    static thread_local unsigned next = 0;
+    const int32_t key[11] = {p.B, p.T, p.H, p.W, p.NH, p.KT, p.KH, p.KW, hd, mode, sms};
+    for (const Entry& e : cache)
+        if (memcmp(e.key, key, sizeof key) == 0) {
+            *out = e.g;
+            return true;
+        }
+    if (!plan_tiles(out, p, hd, mode, sms)) return false;
+    Entry& e = cache[next++ % 16];
+    memcpy(e.key, key, sizeof key);
+    e.g = *out;
+    return true;
+}
+
+template <int HD, int MODE>
+cudaError_t launch_tiles(const ScoredParams& p, int sms, cudaStream_t stream) {
+    TileGeom g;
+    if (!cached_plan(&g, p, HD, MODE, sms)) return cudaErrorInvalidValue;
+    constexpr int HDB = HD > 64 ? 64 : HD;
+    const int64_t row = int64_t(p.NH) * HD;
+    struct Src { const void* ptr; int64_t ts; };
+    const Src q{p.q, p.q_ts}, k{p.k, p.k_ts}, v{p.v, p.v_ts}, d{p.dout, row};
+    const Src f0 = MODE == kDkv ? k : q, f1 = MODE == kFwd ? q : MODE == kDq ? d : v;
+    const Src x0 = MODE == kDkv ? q : k, x1 = MODE == kDkv ? d : v;
+    CUtensorMap mf0, mf1, mx0, mx1;
+    auto fixed = [&](CUtensorMap* m, const Src& s) {
+        return encode_map(m, s.ptr, p.B, p.T, p.H, p.W, p.NH, HD, s.ts, HDB, g.sw, g.bh, g.st);
+    };
+    auto streamed = [&](CUtensorMap* m, const Src& s) {
+        return encode_map(m, s.ptr, p.B, p.T, p.H, p.W, p.NH, HD, s.ts, HDB, g.cc, g.cr, 1);
+    };
+    if (!fixed(&mf0, f0) || !fixed(&mf1, f1) || !streamed(&mx0, x0) || !streamed(&mx1, x1))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(scored_tiles<HD, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    const int64_t slots = int64_t(sms) * blocks_per_sm(HD, MODE);
+    const int grid = int(g.units < slots ? g.units : slots);
+    scored_tiles<HD, MODE><<<grid, g.nw * 32, g.smem, stream>>>(mf0, mf1, mx0, mx1, p, g);
     return cudaGetLastError();
 }
 
 template <int HD>
 cudaError_t bwd(const ScoredParams& p, int sms, cudaStream_t stream) {
-    scored_rows<HD, kDq><<<row_grid(p, sms), kRowWarps * 32, 0, stream>>>(p);
-    scored_rows<HD, kDkv><<<row_grid(p, sms), kRowWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int64_t rows = int64_t(p.B) * p.T * p.H * p.W * p.NH;
+    const int64_t blocks = (rows * (HD / 8) + 255) / 256;
+    if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    scored_stat<HD><<<unsigned(blocks), 256, 0, stream>>>(p, rows);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = launch_tiles<HD, kDq>(p, sms, stream);
+    if (e != cudaSuccess) return e;
+    return launch_tiles<HD, kDkv>(p, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream) {
     switch (hd) {
-        case 16: return fwd<16>(p, sms, stream);
-        case 32: return fwd<32>(p, sms, stream);
-        case 64: return fwd<64>(p, sms, stream);
-        case 128: return fwd<128>(p, sms, stream);
+        case 16: return launch_tiles<16, kFwd>(p, sms, stream);
+        case 32: return launch_tiles<32, kFwd>(p, sms, stream);
+        case 64: return launch_tiles<64, kFwd>(p, sms, stream);
+        case 128: return launch_tiles<128, kFwd>(p, sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -268,6 +1062,27 @@ cudaError_t launch_scored_bwd(int hd, const ScoredParams& p, int sms, cudaStream
         case 128: return bwd<128>(p, sms, stream);
         default: return cudaErrorInvalidValue;
     }
+}
+
+// The flag is taken as for the attention kernel: one atomic exchange per
+// status request, its old value left in a slot of that request's own.
+constexpr unsigned int kStatusSlots = 256;
+__device__ unsigned int g_scored_status_slots[kStatusSlots];
+
+__global__ void take_scored_flag(unsigned int slot) {
+    g_scored_status_slots[slot] = atomicExch(&g_scored_timeout_flag, 0u);
+}
+
+cudaError_t take_scored_error(cudaStream_t stream, unsigned int* flag) {
+    static std::atomic<unsigned int> next{0};
+    const unsigned int slot = next.fetch_add(1u) % kStatusSlots;
+    take_scored_flag<<<1, 1, 0, stream>>>(slot);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyFromSymbolAsync(flag, g_scored_status_slots, sizeof(unsigned int), slot * sizeof(unsigned int),
+                                  cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(stream);
 }
 
 }  // namespace na3d

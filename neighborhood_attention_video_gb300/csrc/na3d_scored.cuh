@@ -17,7 +17,7 @@ struct ScoredParams {
     float* lse;                    // (B,T,H,W,NH) or null: written forward, read backward
     const uint16_t* dout;          // backward: bf16, as out
     uint16_t *dq, *dk, *dv;
-    float* delta;                  // backward workspace (B,T,H,W,NH): rowsum(dout * out)
+    float2* stat;                  // backward workspace (B,T,H,W,NH): (lse, dout . out)
     float softcap;                 // 0: none
     const float* slopes;           // (NH, 3) or null
     const int32_t* doc;            // (B,T,H,W) or null
@@ -26,5 +26,9 @@ struct ScoredParams {
 
 cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_scored_bwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream);
+
+// After the work already on `stream`, take (read and clear in one atomic
+// step) these kernels' timeout flag, then synchronize `stream`.
+cudaError_t take_scored_error(cudaStream_t stream, unsigned int* flag);
 
 }  // namespace na3d
