@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "na3d_host.cuh"
+#include "na3d_kernel.cuh"
 #include "na3d_scored.cuh"
 #include "sm103_ptx.cuh"
 
@@ -256,12 +257,15 @@ struct TileGeom {
     int32_t cr, cc;
     int32_t nt, nhc, nwc;      // chunks of a unit: frames, and parts along H and W
     int32_t stages;
-    int32_t mask_steps;        // steps whose mask words fit a warp's buffer
+    int32_t lut;               // 1: a frame's biases and (h, w) windows come from a table of each warp
+    int32_t lut_pitch;         // floats of a table row (one for each (h, w) of the warp's rows)
+    int32_t mask_steps;        // steps whose mask words fit a warp's buffer (0: none are needed)
     int32_t mask_kept;         // 1: they hold a whole unit, and serve all heads of a brick
     int32_t units;             // (brick, head) pairs, head fastest
     // shared memory, bytes from a 1024-byte boundary
     int32_t x_bytes;           // one streamed tensor of a stage (regions of 64 columns)
-    int32_t off_x, off_stat, off_mask, off_hw, off_bar, smem;
+    int32_t off_x, off_stat, off_lut, off_mask, off_hw, off_bar, smem;
+    FastDiv div_nh, div_nbw, div_nbh, div_nbt, div_chunks, div_nwc;
 };
 
 struct Sync {
@@ -311,34 +315,51 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t region) {
     return (c >> 3) * region + uint32_t(r) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_dup(float x) { return f2_pack(x, x); }
+
 // tanh to about 2^-22 of its value. Up to 1/2 (a score of half the cap) an odd
 // polynomial, fitted for the least largest relative error (1.5e-8), keeps the
 // special-function unit free; larger values take 1 - 2 / (1 + e^2|z|), once
 // any of the warp's needs it.
-__device__ __forceinline__ float tanh_poly(float z) {
-    const float y = z * z;
-    float p = fmaf(y, 0.0172414667904377f, -0.05304548144340515f);
-    p = fmaf(y, p, 0.13325878977775574f);
-    p = fmaf(y, p, -0.333331435918808f);
-    return fmaf(z * y, p, z);
+__device__ __forceinline__ uint64_t tanh_poly(uint64_t z) {
+    const uint64_t y = f2_mul(z, z);
+    uint64_t p = f2_fma(y, f2_dup(0.0172414667904377f), f2_dup(-0.05304548144340515f));
+    p = f2_fma(y, p, f2_dup(0.13325878977775574f));
+    p = f2_fma(y, p, f2_dup(-0.333331435918808f));
+    return f2_fma(f2_mul(z, y), p, z);
 }
 __device__ __forceinline__ float tanh_exp(float z) {
     const float e = ex2_approx(fabsf(z) * (2.f * kLog2e));
     return copysignf(fmaf(-2.f, rcp_approx(e + 1.f), 1.f), z);
 }
 
-template <int N>
-__device__ __forceinline__ void tanh_all(float* z) {
-    float big = 0.f;
+// z[0..3], pairs, to their tanh.
+__device__ __forceinline__ void tanh_all(uint64_t* z) {
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
-    if (__any_sync(0xffffffffu, !(big <= 0.5f))) {
+    for (int i = 0; i < 4; ++i) f2_unpack(z[i], x[2 * i], x[2 * i + 1]);
+    const float big = fmaxf(max3f(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])),
+                            fmaxf(max3f(fabsf(x[3]), fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = fabsf(z[i]) <= 0.5f ? tanh_poly(z[i]) : tanh_exp(z[i]);
-    } else {
+    for (int i = 0; i < 4; ++i) z[i] = tanh_poly(z[i]);
+    if (__any_sync(0xffffffffu, big > 0.5f)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = tanh_poly(z[i]);
+        for (int i = 0; i < 4; ++i) {
+            float lo, up;
+            f2_unpack(z[i], lo, up);
+            z[i] = f2_pack(fabsf(x[2 * i]) > 0.5f ? tanh_exp(x[2 * i]) : lo,
+                           fabsf(x[2 * i + 1]) > 0.5f ? tanh_exp(x[2 * i + 1]) : up);
+        }
     }
+}
+
+__device__ __forceinline__ int fast_div(const FastDiv& d, int n) {
+    return int((uint64_t(uint32_t(n)) * d.mul) >> d.shift);
 }
 
 struct Brick {
@@ -347,11 +368,22 @@ struct Brick {
 
 __device__ __forceinline__ Brick brick_of(const TileGeom& g, int n) {
     Brick o;
-    o.w0 = n % g.nbw * g.sw; n /= g.nbw;
-    o.h0 = n % g.nbh * g.bh; n /= g.nbh;
-    o.t0 = n % g.nbt * g.st;
-    o.b = n / g.nbt;
+    int q = fast_div(g.div_nbw, n);
+    o.w0 = (n - q * g.nbw) * g.sw; n = q;
+    q = fast_div(g.div_nbh, n);
+    o.h0 = (n - q * g.nbh) * g.bh; n = q;
+    o.b = fast_div(g.div_nbt, n);
+    o.t0 = (n - o.b * g.nbt) * g.st;
     return o;
+}
+
+// First position of chunk c of a unit whose box starts at (t0, h0, w0).
+__device__ __forceinline__ void chunk_at(const TileGeom& g, int c, int t0, int h0, int w0, int* t, int* h, int* w) {
+    const int f = fast_div(g.div_chunks, c);
+    const int r = c - f * (g.nhc * g.nwc), y = fast_div(g.div_nwc, r);
+    *t = t0 + f;
+    *h = h0 + y * g.cr;
+    *w = w0 + (r - y * g.nwc) * g.cc;
 }
 
 // Union of the ranges of n rows from i (rows past the axis end count as the last).
@@ -362,34 +394,32 @@ __device__ __forceinline__ int2 box_of(bool dkv, int i, int n, int K, int N) {
 
 // Mask bits of one step (16 columns from index i0 of a warp's box in a chunk)
 // for the warp's 16 rows: word g holds row g in its low and row g + 8 in its
-// high half. A lane computes half the columns of one row.
+// high half. A lane computes half the columns of one row. Where the table
+// applies the windows, the bits are those of the documents alone: all set
+// but where clips meet.
 template <bool DKV>
-__device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom& g, uint32_t* words, int b, int rt,
-                                          int rh, int rw, bool rvalid, int rdoc, int prefix, int t, int h0, int w0,
-                                          int rows, int i0) {
+__device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom& g, uint32_t* words, int b, int rh,
+                                          int rw, bool rvalid, int rdoc, int t, int h0, int w0, int rows, int i0) {
     const int lane = threadIdx.x & 31;
-    uint32_t bits = 0;
-    if (rvalid) {
-        const int lt = range_lo(DKV, rt, p.KT, p.T), ht = range_hi(DKV, rt, p.KT, p.T);
+    uint32_t bits = g.lut ? 0xffu : 0u;
+    if (rvalid && !(p.doc && rdoc < 0)) {
         const int lh = range_lo(DKV, rh, p.KH, p.H), hh = range_hi(DKV, rh, p.KH, p.H);
         const int lw = range_lo(DKV, rw, p.KW, p.W), hw = range_hi(DKV, rw, p.KW, p.W);
-        bool frame = t >= lt && t < ht;
-        if (p.prefix) {
-            const int qt = DKV ? t : rt, kt = DKV ? rt : t;
-            frame = frame && (kt <= qt || kt < prefix);
-        }
-        if (frame && !(p.doc && rdoc < 0)) {
-            const int first = i0 + 8 * (lane >> 4);
-            int y = first / g.cc, x = first - y * g.cc;
+        const int first = i0 + 8 * (lane >> 4);
+        int y = first / g.cc, x = first - y * g.cc;
+        bits = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int h = h0 + y, w = w0 + x;
-                bool ok = y < rows && h >= lh && h < hh && w >= lw && w < hw;
-                if (ok && p.doc) ok = p.doc[token_of(p, b, t, h, w)] == rdoc;
-                bits |= uint32_t(ok) << i;
-                if (++x == g.cc) { x = 0; ++y; }
-            }
+        for (int i = 0; i < 8; ++i) {
+            const int h = h0 + y, w = w0 + x;
+            const bool in = y < rows && h >= lh && h < hh && w >= lw && w < hw;
+            // the positions of rows' windows are inside the grid
+            bool ok = in || g.lut;
+            if (in && p.doc) ok = p.doc[token_of(p, b, t, h, w)] == rdoc;
+            bits |= uint32_t(ok) << i;
+            if (++x == g.cc) { x = 0; ++y; }
         }
+    } else if (rvalid) {
+        bits = 0;
     }
     // columns 8..15 join 0..7 (lanes 16 + r and r), then rows r and r + 8
     bits |= __shfl_down_sync(0xffffffffu, bits, 16) << 8;
@@ -446,7 +476,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     for (int i = threadIdx.x * 16; i < 2 * S * g.x_bytes; i += blockDim.x * 16)
         *reinterpret_cast<uint4*>(base_ptr + g.off_x + i) = make_uint4(0, 0, 0, 0);
     if (DKV)
-        for (int i = threadIdx.x * 8; i < g.off_mask - g.off_stat; i += blockDim.x * 8)
+        for (int i = threadIdx.x * 8; i < S * (g.cr * g.cc + 16) * 8; i += blockDim.x * 8)
             *reinterpret_cast<uint2*>(base_ptr + g.off_stat + i) = make_uint2(0, 0);
     // (row, column) of the chunk's index, as floats
     float2* const hw = reinterpret_cast<float2*>(base_ptr + g.off_hw);
@@ -463,11 +493,12 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     // Start the load of chunk c of unit u into stage s (a whole warp). A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
     auto load_chunk = [&](int u, int c, int s) {
-        const Brick o = brick_of(g, u / p.NH);
-        const int head = u % p.NH;
+        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
+        const Brick o = brick_of(g, nb);
         const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
         const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
-        const int t = bt.x + c / (g.nhc * g.nwc), h = bh.x + c / g.nwc % g.nhc * g.cr, w = bw.x + c % g.nwc * g.cc;
+        int t, h, w;
+        chunk_at(g, c, bt.x, bh.x, bw.x, &t, &h, &w);
         const bool inside = t < bt.y && h < bh.y && w < bw.y;
         const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * g.x_bytes;
         if (lane == 0) {
@@ -496,8 +527,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         }
     };
     auto load_fixed = [&](int u, int f) {   // one thread
-        const Brick o = brick_of(g, u / p.NH);
-        const int head = u % p.NH;
+        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
+        const Brick o = brick_of(g, nb);
         const uint32_t full = sy.bar(S + f), x = base + f * NF * f_bytes;
         ++issued[S + f];
         mbar_arrive_expect_tx(full, NF * REG * f_rows * HDB * 2);
@@ -529,13 +560,14 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
     const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
     uint32_t it = 0, ft = 0;
-    int mask_brick = -1;
+    int mask_brick = -1, lut_brick = -1;
+    float* const lut = reinterpret_cast<float*>(base_ptr + g.off_lut) + warp * g.sh * g.sw * g.lut_pitch;
+    const bool masked = g.mask_steps > 0, same_hw = g.sh * g.sw <= 8;
     bool ok = true;
 
     for (int u = u0; u < u1; ++u, ++ft) {
-        const int nb = u / p.NH;
+        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
         const Brick o = brick_of(g, nb);
-        const int head = u % p.NH;
         const int wh0 = o.h0 + warp * g.sh;
         const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
         const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
@@ -553,6 +585,38 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             *first = max(mine.x, h);
             return min(mine.y, h + g.cr) - *first;
         };
+        float sl[3] = {0.f, 0.f, 0.f};
+        if (biased) {
+            load_slopes(p, head, sl);
+#pragma unroll
+            for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
+        }
+        // the table: for each (h, w) of the rows, the bias of a frame's columns, -inf
+        // outside the window; it serves every frame, and without slopes every head
+        if (g.lut && (biased || nb != lut_brick)) {
+            __syncwarp();
+            for (int rp = hi; rp < g.sh * g.sw; rp += 2) {
+                const int lh = wh0 + rp / g.sw, lw = o.w0 + rp % g.sw;
+                const bool inside = lh < p.H && lw < p.W;
+                const int h_lo = range_lo(DKV, lh, p.KH, p.H), h_n = inside ? range_hi(DKV, lh, p.KH, p.H) - h_lo : 0;
+                const int w_lo = range_lo(DKV, lw, p.KW, p.W), w_n = range_hi(DKV, lw, p.KW, p.W) - w_lo;
+                float* to = lut + rp * g.lut_pitch + (lane & 15);
+                for (int h = bh.x; h < bh.y; h += g.cr)
+                    for (int w = bw.x; w < bw.y; w += g.cc) {
+                        int hf;
+                        const int rows = box_rows(h, &hf);
+                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16, to += 16) {
+                            const float2 at = hw[i0 + (lane & 15)];
+                            const int y = int(at.x), x = int(at.y);
+                            const bool in = y < rows && uint32_t(hf + y - h_lo) < uint32_t(h_n) &&
+                                            uint32_t(w + x - w_lo) < uint32_t(w_n);
+                            *to = in ? fmaf(sl[1], float(abs(hf + y - lh)), sl[2] * float(abs(w + x - lw))) : -INFINITY;
+                        }
+                    }
+            }
+            __syncwarp();
+            lut_brick = nb;
+        }
         if (g.mask_kept && nb != mask_brick) {
             int ms = 0;
             __syncwarp();
@@ -562,7 +626,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         int hf;
                         const int rows = box_rows(h, &hf);
                         for (int i0 = 0; i0 < rows * g.cc; i0 += 16, ++ms)
-                            mask_step<DKV>(p, g, mask + ms * 8, o.b, mt, mh, mw, mvalid, mdoc, prefix, t, hf, w, rows, i0);
+                            mask_step<DKV>(p, g, mask + ms * 8, o.b, mh, mw, mvalid, mdoc, t, hf, w, rows, i0);
                     }
             __syncwarp();
             mask_brick = nb;
@@ -579,19 +643,13 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             rt[i] = o.t0 + r / (g.sw * g.sh);
             row[i] = rw < p.W && rh[i] < p.H && rt[i] < p.T ? token_of(p, o.b, rt[i], rh[i], rw) * p.NH + head : -1;
         }
-        float sl[3] = {0.f, 0.f, 0.f};
-        if (biased) {
-            load_slopes(p, head, sl);
-#pragma unroll
-            for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
-        }
         float ref[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};   // log2 reference that scores are taken from
         if (MODE == kDq) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (row[i] >= 0) {
                     const float2 s = p.stat[row[i]];
-                    ref[i] = s.x * kLog2e;
+                    ref[i] = s.x;
                     delta[i] = s.y;
                 }
         }
@@ -620,35 +678,65 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // any for a row that has met no key, so that ref starts at a score
         float l[2] = {0.f, 0.f}, grow[2] = {-INFINITY, -INFINITY};
 
-        int ms = 0;
+        int ms = 0, ls = 0, lut_t = bt.x;   // next steps of the masks and of the table, and its frame
         for (int c = 0; c < per_unit; ++c, ++it) {
             const int s = it % S;
             if (!(ok = sy.wait(sy.bar(s), (it / S) & 1u))) break;
-            const int t = bt.x + c / (g.nhc * g.nwc), h = bh.x + c / g.nwc % g.nhc * g.cr, w = bw.x + c % g.nwc * g.cc;
+            int t, h, w;
+            chunk_at(g, c, bt.x, bh.x, bw.x, &t, &h, &w);
             int hf;
             const int rows = box_rows(h, &hf);
             const int n = t < bt.y && h < bh.y && w < bw.y ? rows * g.cc : 0;
-            const uint32_t x0 = base + g.off_x + 2 * s * g.x_bytes, x1 = x0 + g.x_bytes;
+            const uint32_t x0 = base + g.off_x + 2 * s * g.x_bytes;
             const int first = (hf - h) * g.cc;
             const float2* stat = reinterpret_cast<const float2*>(base_ptr + g.off_stat + s * stat_rows * 8) + first;
-            if (!g.mask_kept) {
+            if (t != lut_t) {
+                lut_t = t;
+                ls = 0;
+            }
+            if (masked && !g.mask_kept) {
                 ms = 0;
                 __syncwarp();
                 for (int i0 = 0, k = 0; i0 < n; i0 += 16, ++k)
-                    mask_step<DKV>(p, g, mask + k * 8, o.b, mt, mh, mw, mvalid, mdoc, prefix, t, hf, w, rows, i0);
+                    mask_step<DKV>(p, g, mask + k * 8, o.b, mh, mw, mvalid, mdoc, t, hf, w, rows, i0);
                 __syncwarp();
             }
-            const float far_t[2] = {sl[0] * float(abs(t - rt[0])), sl[0] * float(abs(t - rt[1]))};
+            // the frame's part of the score: -inf for a row that does not see it
+            float far_t[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int qt = DKV ? t : rt[i], kt = DKV ? rt[i] : t;
+                const bool sees = t >= range_lo(DKV, rt[i], p.KT, p.T) && t < range_hi(DKV, rt[i], p.KT, p.T) &&
+                                  (!p.prefix || kt <= qt || kt < prefix);
+                far_t[i] = sees ? sl[0] * float(abs(t - rt[i])) : -INFINITY;
+            }
+            const bool frame_seen = __any_sync(0xffffffffu, fmaxf(far_t[0], far_t[1]) > -INFINITY);
+            const int n_steps = n > 0 ? (n + 15) >> 4 : 0;
             const float at_h[2] = {float(hf - rh[0]), float(hf - rh[1])}, at_w = float(w - rw);
-            for (int i0 = 0; i0 < n; i0 += 16, ++ms) {
-                const int xr = first + i0 + (lane & 15);
+            // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
+            // step moves them by 16 rows and a column block by an exclusive or
+            uint32_t a0 = x0 + swizzled<HD>(first + (lane & 15), hi, x_region);
+            const float* lut_at = lut + (r0 % (g.sh * g.sw)) * g.lut_pitch + ls * 16 + 2 * c2;
+            ls += n_steps;
+            const uint32_t* mask_at = mask + ms * 8 + r0;
+            ms += n_steps;
+            for (int k = 0; frame_seen && k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8) {
+                bool mixed = false;
+                uint32_t bits = 0;   // 0, 1, 8, 9: the columns of row r0; 16, 17, 24, 25: of r0 + 8
+                if (masked) {
+                    bits = *mask_at;
+                    if (!__any_sync(0xffffffffu, bits)) continue;
+                    mixed = !__all_sync(0xffffffffu, bits == 0xffffffffu);
+                    bits >>= 2 * c2;
+                }
+                auto seen = [&](int i) { return (bits >> (8 * (i >> 2) + 16 * ((i >> 1) & 1) + (i & 1)) & 1u) != 0u; };
                 // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of
                 // row (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1)
                 float sc[8] = {}, dp[8] = {};
                 uint32_t f[4];
 #pragma unroll
                 for (int kk = 0; kk < KB; ++kk) {
-                    ldsm4(x0 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                    ldsm4((a0 + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
                     mma16816(sc, fa[0][kk], f[0], f[2]);
                     mma16816(sc + 4, fa[0][kk], f[1], f[3]);
                 }
@@ -657,46 +745,62 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     for (int kk = 0; kk < KB; ++kk) {
                         uint32_t a[4];
                         if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(fr, 2 * kk + hi, f_region), a);
-                        ldsm4(x1 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        ldsm4((a0 + g.x_bytes + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
                         mma16816(dp, NFR < NF ? a : fa[NFR - 1][kk], f[0], f[2]);
                         mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], f[1], f[3]);
                     }
                 }
-                const uint32_t bits = mask[ms * 8 + r0] >> (2 * c2);   // 0, 1, 8, 9 of row r0; 16, 17, 24, 25 of r0 + 8
-                auto seen = [&](int i) { return (bits >> (8 * (i >> 2) + 16 * ((i >> 1) & 1) + (i & 1)) & 1u) != 0u; };
                 float2 cs[4];   // DKV: (log2 reference, delta) of the four columns
                 if (DKV) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        cs[j] = stat[i0 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
-                        cs[j].x *= kLog2e;
-                    }
+                    for (int j = 0; j < 4; ++j) cs[j] = stat[k * 16 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
                 }
-                float sv[8];   // score minus reference, log2
-                if (biased) {
+                // bias minus reference, log2: pair 2 * (tile) + row
+                uint64_t s2[4];
+                const float from[2] = {far_t[0] - ref[0], far_t[1] - ref[1]};
+                if (g.lut) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // column 8 * (j >> 1) + 2 * c2 + (j & 1)
-                        const float2 x = hw[i0 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
-                        const float dw = fabsf(x.y + at_w);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 8 * j);
+                        const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 8 * j);
+                        s2[2 * j] = f2_add(x, f2_dup(from[0]));
+                        s2[2 * j + 1] = f2_add(y, f2_dup(from[1]));
+                    }
+                } else if (biased) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 x = *reinterpret_cast<const float4*>(hw + k * 16 + 8 * j + 2 * c2);
+                        const float d0 = fabsf(x.y + at_w), d1 = fabsf(x.w + at_w);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            sv[4 * (j >> 1) + 2 * i + (j & 1)] =
-                                fmaf(sl[1], fabsf(x.x + at_h[i]), fmaf(sl[2], dw, far_t[i] - (DKV ? cs[j].x : ref[i])));
+                            s2[2 * j + i] = f2_pack(fmaf(sl[1], fabsf(x.x + at_h[i]), fmaf(sl[2], d0, from[i])),
+                                                    fmaf(sl[1], fabsf(x.z + at_h[i]), fmaf(sl[2], d1, from[i])));
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sv[i] = -(DKV ? cs[2 * (i >> 2) + (i & 1)].x : ref[(i >> 1) & 1]);
+                    for (int j = 0; j < 4; ++j) s2[j] = f2_dup(from[j & 1]);
                 }
+                if (DKV) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s2[j] = f2_add(s2[j], f2_pack(-cs[2 * (j >> 1)].x, -cs[2 * (j >> 1) + 1].x));
+                }
+                uint64_t th[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) th[j] = f2_pack(sc[2 * j], sc[2 * j + 1]);
                 if (capped) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sc[i] *= inv_cap;
-                    tanh_all<8>(sc);
+                    for (int j = 0; j < 4; ++j) th[j] = f2_mul(th[j], f2_dup(inv_cap));
+                    tanh_all(th);
                 }
+                float sv[8];   // scores minus reference, log2; then probabilities
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sv[i] = fmaf(sc[i], to_log2, sv[i]);
-                if (MODE == kFwd) {
+                for (int j = 0; j < 4; ++j) f2_unpack(f2_fma(th[j], f2_dup(to_log2), s2[j]), sv[2 * j], sv[2 * j + 1]);
+                if (mixed) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sv[i] = seen(i) ? sv[i] : -INFINITY;
+                }
+                if (MODE == kFwd) {
                     float top[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -708,10 +812,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                             // a row that has met a key moves up only; the first keys set the reference
-                            if (grow[i] == kGrow || x == -INFINITY) x = fmaxf(x, 0.f);
-                            else grow[i] = -kGrow;
-                            const float r = grow[i] == kGrow ? ex2_approx(-x) : 0.f;
-                            if (grow[i] == -kGrow) grow[i] = kGrow;
+                            const bool begun = grow[i] == kGrow;
+                            if (begun || x == -INFINITY) x = fmaxf(x, 0.f);
+                            else grow[i] = kGrow;
+                            const float r = begun ? ex2_approx(-x) : 0.f;
                             ref[i] += x;
                             l[i] *= r;
 #pragma unroll
@@ -724,18 +828,23 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sv[i] = ex2_approx(sv[i]);
-                        l[(i >> 1) & 1] += sv[i];
-                    }
+                    for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+                    l[0] += (sv[0] + sv[1]) + (sv[4] + sv[5]);
+                    l[1] += (sv[2] + sv[3]) + (sv[6] + sv[7]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float e = ex2_approx(sv[i]);
-                        float d = e * (dp[i] - (DKV ? cs[2 * (i >> 2) + (i & 1)].y : delta[(i >> 1) & 1]));
-                        if (capped) d *= fmaf(-sc[i], sc[i], 1.f);
-                        sv[i] = seen(i) ? e : 0.f;
-                        dp[i] = seen(i) ? d : 0.f;
+                    for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint64_t d = f2_add(f2_pack(dp[2 * j], dp[2 * j + 1]),
+                                            DKV ? f2_pack(-cs[2 * (j >> 1)].y, -cs[2 * (j >> 1) + 1].y) : f2_dup(-delta[j & 1]));
+                        d = f2_mul(d, f2_pack(sv[2 * j], sv[2 * j + 1]));
+                        if (capped) d = f2_mul(d, f2_fma(f2_mul(th[j], f2_dup(-1.f)), th[j], f2_dup(1.f)));
+                        f2_unpack(d, dp[2 * j], dp[2 * j + 1]);
+                    }
+                    if (mixed) {   // 0 times what a masked row holds need not be 0
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dp[i] = seen(i) ? dp[i] : 0.f;
                     }
                 }
                 // products: probabilities (FWD: with V; DKV: with dO) and da (with K or Q)
@@ -744,7 +853,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                            pack_bf16x2(sv[4], sv[5]), pack_bf16x2(sv[6], sv[7])};
 #pragma unroll
                     for (int kk = 0; kk < KB; ++kk) {
-                        ldsm4t(x1 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        ldsm4t((a0 + g.x_bytes + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
                         mma16816(MODE == kFwd ? acc0[2 * kk] : acc1[MODE == kDkv ? 2 * kk : 0], a, f[0], f[1]);
                         mma16816(MODE == kFwd ? acc0[2 * kk + 1] : acc1[MODE == kDkv ? 2 * kk + 1 : 0], a, f[2], f[3]);
                     }
@@ -754,7 +863,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                            pack_bf16x2(dp[4], dp[5]), pack_bf16x2(dp[6], dp[7])};
 #pragma unroll
                     for (int kk = 0; kk < KB; ++kk) {
-                        ldsm4t(x0 + swizzled<HD>(xr, 2 * kk + hi, x_region), f);
+                        ldsm4t((a0 + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
                         mma16816(acc0[2 * kk], a, f[0], f[1]);
                         mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
                     }
@@ -835,8 +944,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 atomicOr(&g_scored_timeout_flag, 1u);
 }
 
-// (lse, delta) of every row for the backward passes: delta_i = dout_i . out_i;
-// a row that sees nothing gets (0, 0). A row takes HD / 8 lanes, 16 bytes each.
+// (lse in log2 units, delta) of every row for the backward passes:
+// delta_i = dout_i . out_i; a row that sees nothing gets (0, 0). A row takes HD / 8 lanes, 16 bytes each.
 template <int HD>
 __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t rows) {
     constexpr int L = HD / 8;
@@ -858,7 +967,7 @@ __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t
     for (int k = L / 2; k; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
     if (live && c == 0) {
         const float lse = p.lse[r];
-        p.stat[r] = lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse, d);
+        p.stat[r] = lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse * kLog2e, d);
     }
 }
 
@@ -893,8 +1002,9 @@ void lay_out(TileGeom* g, int hd, int mode) {
     g->x_bytes = align_up((g->cr * g->cc + 16) * hdb * 2, 1024) * reg;
     g->off_x = f_region * reg * nf;
     g->off_stat = g->off_x + 2 * g->stages * g->x_bytes;
-    g->off_mask = g->off_stat + (dkv ? g->stages * (g->cr * g->cc + 16) * 8 : 0);
-    g->off_hw = g->off_mask + g->nw * g->mask_steps * 32;
+    g->off_lut = align_up(g->off_stat + (dkv ? g->stages * (g->cr * g->cc + 16) * 8 : 0), 16);
+    g->off_mask = g->off_lut + (g->lut ? g->nw * g->sh * g->sw * g->lut_pitch * 4 : 0);
+    g->off_hw = align_up(g->off_mask + g->nw * g->mask_steps * 32, 16);
     g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
     g->smem = g->off_bar + 64 + 8 * kMaxRing + 1024;
 }
@@ -936,11 +1046,23 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     // steps of a warp: its box in each chunk that it meets, rounded up to 16
                     const int met = (eh_w + g.cr - 2) / g.cr + 1 < nhc ? (eh_w + g.cr - 2) / g.cr + 1 : nhc;
                     const int all = et * g.nwc * ((eh_w * g.cc + 15) / 16 + met - 1);
-                    g.mask_steps = all;
-                    g.mask_kept = 1;
+                    // the table of a frame (pitch: the rows of eight lanes in different banks),
+                    // and masks of a whole unit where there are documents; where the table does
+                    // not fit, masks hold the windows too; where they do not fit, a chunk's
+                    const int frame = all / et * 16;
                     g.stages = 2;
+                    g.lut = 1;
+                    g.lut_pitch = (frame + 23) / 32 * 32 + 8;
+                    g.mask_steps = p.doc ? all : 0;
+                    g.mask_kept = p.doc ? 1 : 0;
                     lay_out(&g, hd, mode);
-                    if (g.smem > room) {   // masks chunk by chunk where a unit's do not fit
+                    if (g.smem > room) {
+                        g.lut = 0;
+                        g.mask_steps = all;
+                        g.mask_kept = 1;
+                        lay_out(&g, hd, mode);
+                    }
+                    if (g.smem > room) {
                         g.mask_kept = 0;
                         g.mask_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
                         lay_out(&g, hd, mode);
@@ -959,7 +1081,7 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                         if (more.smem > room) break;
                         g = more;
                     }
-                    const double steps = double(all) * (g.mask_kept ? 1.0 : 1.6);
+                    const double steps = double(all) * (g.lut ? 1.0 : 1.3) * (g.mask_steps && !g.mask_kept ? 1.6 : 1.0);
                     const double slots = double(sms) * blocks;
                     const double waves = g.units <= slots ? 1.0 : double(g.units) / slots;
                     // cycles of a unit: steps of its warps sharing the SM's schedulers, or their own
@@ -973,10 +1095,18 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                         best_cost = cost;
                         *best = g;
                     }
-                    if (g.mask_kept || g.cr == 1) break;
+                    if (g.lut || g.cr == 1) break;
                 }
             }
         }
+    if (found) {
+        best->div_nh = make_fastdiv(p.NH);
+        best->div_nbw = make_fastdiv(best->nbw);
+        best->div_nbh = make_fastdiv(best->nbh);
+        best->div_nbt = make_fastdiv(best->nbt);
+        best->div_chunks = make_fastdiv(best->nhc * best->nwc);
+        best->div_nwc = make_fastdiv(best->nwc);
+    }
     return found;
 }
 
@@ -984,12 +1114,12 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
 // some microseconds.
 bool cached_plan(TileGeom* out, const ScoredParams& p, int hd, int mode, int sms) {
     struct Entry {
-        int32_t key[11];
+        int32_t key[12];
         TileGeom g;
     };
     static thread_local Entry cache[16] = {};
     static thread_local unsigned next = 0;
-    const int32_t key[11] = {p.B, p.T, p.H, p.W, p.NH, p.KT, p.KH, p.KW, hd, mode, sms};
+    const int32_t key[12] = {p.B, p.T, p.H, p.W, p.NH, p.KT, p.KH, p.KW, hd, mode, sms, p.doc != nullptr};
     for (const Entry& e : cache)
         if (memcmp(e.key, key, sizeof key) == 0) {
             *out = e.g;
