@@ -224,7 +224,7 @@ enum { kFwd, kDq, kDkv };
 // Blocks an SM holds, and the most warps of a block: as many rows in flight as
 // the registers of an instance allow (accumulators, fixed fragments and about
 // 60 more a thread).
-__host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= (mode == kDkv ? 32 : 64) ? 2 : 1; }
+__host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= 32 ? 2 : 1; }
 __host__ __device__ constexpr int max_warps(int hd, int mode) {
     return blocks_per_sm(hd, mode) == 2 || hd > 64 ? 8 : 12;
 }
@@ -236,7 +236,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;      // log2 growth of the scores past the kept maximum before a rescale
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 500000000ull;
-constexpr int kMaxStages = 4, kMaxRing = kMaxStages + 2;   // ring places: stages and fixed buffers
+constexpr int kMaxStages = 6, kMaxRing = kMaxStages + 2;   // ring places: stages and fixed buffers
+constexpr int kControl = 8 + 8 * kMaxRing;                     // bytes of the control words
 
 // The positions that row i of an axis of length N meets: keys of its window
 // (FWD, DQ), or the queries whose windows hold it (DKV). Both ends grow with i.
@@ -261,11 +262,11 @@ struct TileGeom {
     int32_t lut_pitch;         // floats of a table row (one for each (h, w) of the warp's rows)
     int32_t mask_steps;        // steps whose mask words fit a warp's buffer (0: none are needed)
     int32_t mask_kept;         // 1: they hold a whole unit, and serve all heads of a brick
-    int32_t units;             // (brick, head) pairs, head fastest
+    int32_t units, bricks;     // (head, brick) pairs, brick fastest
     // shared memory, bytes from a 1024-byte boundary
     int32_t x_bytes;           // one streamed tensor of a stage (regions of 64 columns)
     int32_t off_x, off_stat, off_lut, off_mask, off_hw, off_bar, smem;
-    FastDiv div_nh, div_nbw, div_nbh, div_nbt, div_chunks, div_nwc;
+    FastDiv div_bricks, div_nbw, div_nbh, div_nbt, div_chunks, div_nwc;
 };
 
 struct Sync {
@@ -392,46 +393,42 @@ __device__ __forceinline__ int2 box_of(bool dkv, int i, int n, int K, int N) {
     return make_int2(range_lo(dkv, first, K, N), range_hi(dkv, last, K, N));
 }
 
-// Mask bits of one step (16 columns from index i0 of a warp's box in a chunk)
-// for the warp's 16 rows: word g holds row g in its low and row g + 8 in its
-// high half. A lane computes half the columns of one row. Where the table
-// applies the windows, the bits are those of the documents alone: all set
-// but where clips meet.
+// Mask words of one step (16 columns from index i0 of a warp's box in a chunk)
+// for the warp's 16 rows: word r holds row r in its low and row r + 8 in its
+// high half. Where the table applies the windows, the bits are those of the
+// documents alone: all set but where clips meet. Lane j takes column j & 15;
+// rdoc and the windows are those of row lane & 15.
 template <bool DKV>
 __device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom& g, uint32_t* words, int b, int rh,
                                           int rw, bool rvalid, int rdoc, int t, int h0, int w0, int rows, int i0) {
     const int lane = threadIdx.x & 31;
-    uint32_t bits = g.lut ? 0xffu : 0u;
-    if (rvalid && !(p.doc && rdoc < 0)) {
-        const int lh = range_lo(DKV, rh, p.KH, p.H), hh = range_hi(DKV, rh, p.KH, p.H);
-        const int lw = range_lo(DKV, rw, p.KW, p.W), hw = range_hi(DKV, rw, p.KW, p.W);
-        const int first = i0 + 8 * (lane >> 4);
-        int y = first / g.cc, x = first - y * g.cc;
-        bits = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int h = h0 + y, w = w0 + x;
-            const bool in = y < rows && h >= lh && h < hh && w >= lw && w < hw;
-            // the positions of rows' windows are inside the grid
-            bool ok = in || g.lut;
-            if (in && p.doc) ok = p.doc[token_of(p, b, t, h, w)] == rdoc;
-            bits |= uint32_t(ok) << i;
-            if (++x == g.cc) { x = 0; ++y; }
+    const int i = i0 + (lane & 15), y = i / g.cc, h = h0 + y, w = w0 + i - y * g.cc;
+    const bool in = y < rows && h < p.H && w < p.W;
+    // positions outside the box count as of another document: no row sees them
+    const int kdoc = !in ? -2 : p.doc ? p.doc[token_of(p, b, t, h, w)] : 0;
+    uint32_t bits = 0;
+#pragma unroll 4
+    for (int r = 0; r < 16; ++r) {
+        const int d = __shfl_sync(0xffffffffu, rvalid ? rdoc : -1, r);
+        bool ok = d >= 0 && d == kdoc;
+        if (!g.lut) {
+            const int qh = __shfl_sync(0xffffffffu, rh, r), qw = __shfl_sync(0xffffffffu, rw, r);
+            ok = ok && h >= range_lo(DKV, qh, p.KH, p.H) && h < range_hi(DKV, qh, p.KH, p.H) &&
+                 w >= range_lo(DKV, qw, p.KW, p.W) && w < range_hi(DKV, qw, p.KW, p.W);
         }
-    } else if (rvalid) {
-        bits = 0;
+        const uint32_t row = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+        if ((lane & 7) == (r & 7)) bits |= row << (2 * (r & 8));
     }
-    // columns 8..15 join 0..7 (lanes 16 + r and r), then rows r and r + 8
-    bits |= __shfl_down_sync(0xffffffffu, bits, 16) << 8;
-    bits |= __shfl_down_sync(0xffffffffu, bits, 8) << 16;
     if (lane < 8) words[lane] = bits;
 }
 
 // One persistent block; nw warps, 16 rows each.
 //   FWD: fixed rows Q; streamed K, V. DQ: fixed Q, dO; streamed K, V.
 //   DKV: fixed K, V; streamed Q, dO and each query's (lse, delta).
-// A block takes a contiguous run of units, so consecutive units mostly share
-// their brick, and with it the mask words. The warps run freely over a ring of
+// A block takes a contiguous run of units, consecutive bricks of one head, so
+// that most find the table of their predecessor: it depends on the head and on
+// where the rows' windows lie about them, the same for all rows away from the
+// borders. The warps run freely over a ring of
 // stages; the warp that is last to be done with a stage starts the load of the
 // chunk that is next to use it, so no warp waits for an empty stage and none
 // is kept for loading (a ninth would cost the other eight a fifth of their
@@ -460,7 +457,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     // control words: abort flag, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
     uint32_t* misc = reinterpret_cast<uint32_t*>(base_ptr + g.off_bar);
-    const Sync sy{base + g.off_bar + 64, misc};
+    const Sync sy{base + g.off_bar + kControl, misc};
     uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S + FB; ++i) {
@@ -493,8 +490,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     // Start the load of chunk c of unit u into stage s (a whole warp). A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
     auto load_chunk = [&](int u, int c, int s) {
-        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
-        const Brick o = brick_of(g, nb);
+        const int head = fast_div(g.div_bricks, u);
+        const Brick o = brick_of(g, u - head * g.bricks);
         const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
         const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
         int t, h, w;
@@ -527,8 +524,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         }
     };
     auto load_fixed = [&](int u, int f) {   // one thread
-        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
-        const Brick o = brick_of(g, nb);
+        const int head = fast_div(g.div_bricks, u);
+        const Brick o = brick_of(g, u - head * g.bricks);
         const uint32_t full = sy.bar(S + f), x = base + f * NF * f_bytes;
         ++issued[S + f];
         mbar_arrive_expect_tx(full, NF * REG * f_rows * HDB * 2);
@@ -560,14 +557,14 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
     const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
     uint32_t it = 0, ft = 0;
-    int mask_brick = -1, lut_brick = -1;
+    int lut_head = -1, lut_h = -2, lut_w = -2, lut_chunk = -1;
     float* const lut = reinterpret_cast<float*>(base_ptr + g.off_lut) + warp * g.sh * g.sw * g.lut_pitch;
-    const bool masked = g.mask_steps > 0, same_hw = g.sh * g.sw <= 8;
+    const bool same_hw = g.sh * g.sw <= 8;
     bool ok = true;
 
     for (int u = u0; u < u1; ++u, ++ft) {
-        const int nb = fast_div(g.div_nh, u), head = u - nb * p.NH;
-        const Brick o = brick_of(g, nb);
+        const int head = fast_div(g.div_bricks, u);
+        const Brick o = brick_of(g, u - head * g.bricks);
         const int wh0 = o.h0 + warp * g.sh;
         const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
         const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
@@ -592,32 +589,53 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
         }
         // the table: for each (h, w) of the rows, the bias of a frame's columns, -inf
-        // outside the window; it serves every frame, and without slopes every head
-        if (g.lut && (biased || nb != lut_brick)) {
+        // outside the window. It is kept while the head (where it matters) and the rows'
+        // place stay; rows away from the borders all have the same.
+        const int place_h = wh0 >= p.KH && wh0 + g.sh - 1 < p.H - p.KH ? -1 : wh0;
+        const int place_w = o.w0 >= p.KW && o.w0 + g.sw - 1 < p.W - p.KW ? -1 : o.w0;
+        const int in_chunk = g.nhc > 1 ? mine.x - bh.x : 0;
+        if (g.lut && ((biased && head != lut_head) || place_h != lut_h || place_w != lut_w || in_chunk != lut_chunk)) {
             __syncwarp();
             for (int rp = hi; rp < g.sh * g.sw; rp += 2) {
                 const int lh = wh0 + rp / g.sw, lw = o.w0 + rp % g.sw;
-                const bool inside = lh < p.H && lw < p.W;
-                const int h_lo = range_lo(DKV, lh, p.KH, p.H), h_n = inside ? range_hi(DKV, lh, p.KH, p.H) - h_lo : 0;
-                const int w_lo = range_lo(DKV, lw, p.KW, p.W), w_n = range_hi(DKV, lw, p.KW, p.W) - w_lo;
+                const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
+                const float h_n = lh < p.H && lw < p.W ? float(range_hi(DKV, lh, p.KH, p.H) - h_lo) : 0.f;
+                const float w_n = float(range_hi(DKV, lw, p.KW, p.W) - w_lo);
                 float* to = lut + rp * g.lut_pitch + (lane & 15);
                 for (int h = bh.x; h < bh.y; h += g.cr)
                     for (int w = bw.x; w < bw.y; w += g.cc) {
                         int hf;
                         const int rows = box_rows(h, &hf);
+                        const float h_in = float(hf - h_lo), w_in = float(w - w_lo), h_far = float(hf - lh), w_far = float(w - lw);
+                        const float n_rows = float(rows);
                         for (int i0 = 0; i0 < rows * g.cc; i0 += 16, to += 16) {
                             const float2 at = hw[i0 + (lane & 15)];
-                            const int y = int(at.x), x = int(at.y);
-                            const bool in = y < rows && uint32_t(hf + y - h_lo) < uint32_t(h_n) &&
-                                            uint32_t(w + x - w_lo) < uint32_t(w_n);
-                            *to = in ? fmaf(sl[1], float(abs(hf + y - lh)), sl[2] * float(abs(w + x - lw))) : -INFINITY;
+                            const bool in = at.x < n_rows && at.x + h_in >= 0.f && at.x + h_in < h_n &&
+                                            at.y + w_in >= 0.f && at.y + w_in < w_n;
+                            *to = in ? fmaf(sl[1], fabsf(at.x + h_far), sl[2] * fabsf(at.y + w_far)) : -INFINITY;
                         }
                     }
             }
             __syncwarp();
-            lut_brick = nb;
+            lut_head = head;
+            lut_h = place_h;
+            lut_w = place_w;
+            lut_chunk = in_chunk;
         }
-        if (g.mask_kept && nb != mask_brick) {
+        // documents: no masks where the whole box is of one document, the rows' own
+        bool masked = g.mask_steps > 0;
+        if (masked && g.lut) {
+            const int d0 = __shfl_sync(0xffffffffu, mdoc, 0);
+            bool other = mvalid && (mdoc != d0 || mdoc < 0);
+            const int width = bw.y - bw.x;
+            for (int t = bt.x; t < bt.y; ++t)
+                for (int i = lane; i < (mine.y - mine.x) * width; i += 32) {
+                    const int y = i / width;
+                    other = other || p.doc[token_of(p, o.b, t, mine.x + y, bw.x + i - y * width)] != d0;
+                }
+            masked = __any_sync(0xffffffffu, other);
+        }
+        if (masked && g.mask_kept) {
             int ms = 0;
             __syncwarp();
             for (int t = bt.x; t < bt.y; ++t)
@@ -629,7 +647,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             mask_step<DKV>(p, g, mask + ms * 8, o.b, mh, mw, mvalid, mdoc, t, hf, w, rows, i0);
                     }
             __syncwarp();
-            mask_brick = nb;
         }
 
         // rows r0 and r0 + 8, in one column of the grid
@@ -1006,7 +1023,7 @@ void lay_out(TileGeom* g, int hd, int mode) {
     g->off_mask = g->off_lut + (g->lut ? g->nw * g->sh * g->sw * g->lut_pitch * 4 : 0);
     g->off_hw = align_up(g->off_mask + g->nw * g->mask_steps * 32, 16);
     g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
-    g->smem = g->off_bar + 64 + 8 * kMaxRing + 1024;
+    g->smem = g->off_bar + kControl + 8 * kMaxRing + 1024;
 }
 
 // Chooses rows, brick and chunks for the least modelled time.
@@ -1021,8 +1038,8 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
             if (sw > 8) continue;
             const int et = widest(dkv, st, p.KT, p.T), ew = widest(dkv, sw, p.KW, p.W);
             const int eh_w = widest(dkv, sh, p.KH, p.H);
-            for (int nw = 1; nw <= max_warps(hd, mode); nw += nw < 4 ? nw : 4) {
-                if (nw > 1 && (nw / 2) * sh >= p.H) break;
+            for (int nw = 1; nw <= max_warps(hd, mode); nw += nw < 4 ? 1 : nw < 8 ? 2 : 4) {
+                if ((nw - 1) * sh >= p.H) break;
                 TileGeom g{};
                 g.st = st; g.sh = sh; g.sw = sw; g.nw = nw; g.bh = nw * sh;
                 if (g.bh > 256) continue;
@@ -1032,12 +1049,14 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                 const int64_t units = int64_t(p.B) * g.nbt * g.nbh * g.nbw * p.NH;
                 if (units >= (int64_t(1) << 31)) continue;
                 g.units = int32_t(units);
+                g.bricks = g.units / p.NH;
                 const int eh = widest(dkv, g.bh, p.KH, p.H);
                 // chunks: whole rows of the box, as many as leave room for two
                 // stages; narrower ones where a single row does not
                 const int room = kSmemMax / blocks - 1024;
                 g.nwc = (ew + 255) / 256;
                 for (int parts = (eh + 255) / 256;; ++parts) {
+                    if (parts > eh) break;
                     g.cc = (ew + g.nwc - 1) / g.nwc;
                     g.cr = (eh + parts - 1) / parts;
                     const int nhc = (eh + g.cr - 1) / g.cr;
@@ -1052,7 +1071,7 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     const int frame = all / et * 16;
                     g.stages = 2;
                     g.lut = 1;
-                    g.lut_pitch = (frame + 23) / 32 * 32 + 8;
+                    g.lut_pitch = frame / 16 * 16 + 8;
                     g.mask_steps = p.doc ? all : 0;
                     g.mask_kept = p.doc ? 1 : 0;
                     lay_out(&g, hd, mode);
@@ -1069,7 +1088,7 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     }
                     if (g.smem > room) {
                         if (g.cr > 1) continue;
-                        if (g.cc == 1) break;   // never: a column a chunk fits
+                        if (found || g.cc == 1) break;   // a column a chunk always fits
                         g.nwc *= 2;
                         parts = (eh + 255) / 256 - 1;
                         continue;
@@ -1081,26 +1100,33 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                         if (more.smem > room) break;
                         g = more;
                     }
-                    const double steps = double(all) * (g.lut ? 1.0 : 1.3) * (g.mask_steps && !g.mask_kept ? 1.6 : 1.0);
+                    // cycles: a step issues about 140 instructions (more without the table, and
+                    // for masks made again for each chunk) on four schedulers that find one
+                    // ready in two cycles of three; a frame's load takes its latency and 45
+                    // bytes a cycle, and hides behind the computation where two frames fit
+                    const double instr = (mode == kFwd ? 140.0 : 190.0) * (hd + 64) / 128 * (g.lut ? 1.0 : 1.4) *
+                                         (g.mask_steps && !g.mask_kept ? 1.8 : 1.0);
+                    const double work = double(all) / et * nw * blocks * instr / 2.6;
+                    const double lat = double(all) / et * instr * 2.5;
+                    const double comp = work > lat ? work : lat;
+                    const double load = 1500.0 + double(g.nwc) * nhc * g.cr * g.cc * hd * 4 * blocks / 45.0;
+                    const bool deep = g.stages >= 2 * g.nwc * nhc;
+                    const double frame_t = deep ? (comp > load ? comp : load) : comp + load;
+                    const double unit = et * (frame_t + 0.1 * (comp + load)) + 3000.0;
                     const double slots = double(sms) * blocks;
                     const double waves = g.units <= slots ? 1.0 : double(g.units) / slots;
-                    // cycles of a unit: steps of its warps sharing the SM's schedulers, or their own
-                    // latency, or the bytes that its chunks bring in
-                    const double work = steps * nw * blocks * 28.0, lat = steps * 300.0;
-                    const double load = double(et) * g.nwc * nhc * g.cr * g.cc * hd * 4 * blocks / 45.0;
-                    const double unit = (work > lat ? work : lat) + 0.5 * load + 3000.0;
                     const double cost = waves * unit;
                     if (!found || cost < best_cost) {
                         found = true;
                         best_cost = cost;
                         *best = g;
                     }
-                    if (g.lut || g.cr == 1) break;
+                    if (g.cr == 1 || parts >= 12) break;
                 }
             }
         }
     if (found) {
-        best->div_nh = make_fastdiv(p.NH);
+        best->div_bricks = make_fastdiv(best->bricks);
         best->div_nbw = make_fastdiv(best->nbw);
         best->div_nbh = make_fastdiv(best->nbh);
         best->div_nbt = make_fastdiv(best->nbt);
