@@ -258,15 +258,15 @@ struct TileGeom {
     int32_t cr, cc;
     int32_t nt, nhc, nwc;      // chunks of a unit: frames, and parts along H and W
     int32_t stages;
-    int32_t lut;               // 1: a frame's biases and (h, w) windows come from a table of each warp
+    int32_t lut;               // 1: a frame's biases and (h, w) windows come from a table of each warp,
+                               // 0: its windows from mask words
     int32_t lut_pitch;         // floats of a table row (one for each (h, w) of the warp's rows)
-    int32_t mask_steps;        // steps whose mask words fit a warp's buffer (0: none are needed)
-    int32_t mask_kept;         // 1: they hold a whole unit, and serve all heads of a brick
+    int32_t frame_steps;       // steps of 16 columns that a warp's box takes in a frame, at most
     int32_t units, bricks;     // (head, brick) pairs, brick fastest
     // shared memory, bytes from a 1024-byte boundary
     int32_t x_bytes;           // one streamed tensor of a stage (regions of 64 columns)
-    int32_t off_x, off_stat, off_lut, off_mask, off_hw, off_bar, smem;
-    FastDiv div_bricks, div_nbw, div_nbh, div_nbt, div_chunks, div_nwc;
+    int32_t off_x, off_stat, off_doc, off_lut, off_hw, off_bar, smem;
+    FastDiv div_bricks, div_nbw, div_nbh, div_nbt;
 };
 
 struct Sync {
@@ -378,48 +378,28 @@ __device__ __forceinline__ Brick brick_of(const TileGeom& g, int n) {
     return o;
 }
 
-// First position of chunk c of a unit whose box starts at (t0, h0, w0).
-__device__ __forceinline__ void chunk_at(const TileGeom& g, int c, int t0, int h0, int w0, int* t, int* h, int* w) {
-    const int f = fast_div(g.div_chunks, c);
-    const int r = c - f * (g.nhc * g.nwc), y = fast_div(g.div_nwc, r);
-    *t = t0 + f;
-    *h = h0 + y * g.cr;
-    *w = w0 + (r - y * g.nwc) * g.cc;
-}
-
 // Union of the ranges of n rows from i (rows past the axis end count as the last).
 __device__ __forceinline__ int2 box_of(bool dkv, int i, int n, int K, int N) {
     const int first = min(i, N - 1), last = min(i + n - 1, N - 1);
     return make_int2(range_lo(dkv, first, K, N), range_hi(dkv, last, K, N));
 }
 
-// Mask words of one step (16 columns from index i0 of a warp's box in a chunk)
-// for the warp's 16 rows: word r holds row r in its low and row r + 8 in its
-// high half. Where the table applies the windows, the bits are those of the
-// documents alone: all set but where clips meet. Lane j takes column j & 15;
-// rdoc and the windows are those of row lane & 15.
+// The (head, brick) of a unit and the box that its chunks cover.
+struct Unit {
+    Brick o;
+    int head;
+    int2 bt, bh, bw;
+};
+
 template <bool DKV>
-__device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom& g, uint32_t* words, int b, int rh,
-                                          int rw, bool rvalid, int rdoc, int t, int h0, int w0, int rows, int i0) {
-    const int lane = threadIdx.x & 31;
-    const int i = i0 + (lane & 15), y = i / g.cc, h = h0 + y, w = w0 + i - y * g.cc;
-    const bool in = y < rows && h < p.H && w < p.W;
-    // positions outside the box count as of another document: no row sees them
-    const int kdoc = !in ? -2 : p.doc ? p.doc[token_of(p, b, t, h, w)] : 0;
-    uint32_t bits = 0;
-#pragma unroll 4
-    for (int r = 0; r < 16; ++r) {
-        const int d = __shfl_sync(0xffffffffu, rvalid ? rdoc : -1, r);
-        bool ok = d >= 0 && d == kdoc;
-        if (!g.lut) {
-            const int qh = __shfl_sync(0xffffffffu, rh, r), qw = __shfl_sync(0xffffffffu, rw, r);
-            ok = ok && h >= range_lo(DKV, qh, p.KH, p.H) && h < range_hi(DKV, qh, p.KH, p.H) &&
-                 w >= range_lo(DKV, qw, p.KW, p.W) && w < range_hi(DKV, qw, p.KW, p.W);
-        }
-        const uint32_t row = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        if ((lane & 7) == (r & 7)) bits |= row << (2 * (r & 8));
-    }
-    if (lane < 8) words[lane] = bits;
+__device__ __forceinline__ Unit unit_of(const ScoredParams& p, const TileGeom& g, int u) {
+    Unit x;
+    x.head = fast_div(g.div_bricks, u);
+    x.o = brick_of(g, u - x.head * g.bricks);
+    x.bt = box_of(DKV, x.o.t0, g.st, p.KT, p.T);
+    x.bh = box_of(DKV, x.o.h0, g.bh, p.KH, p.H);
+    x.bw = box_of(DKV, x.o.w0, g.sw, p.KW, p.W);
+    return x;
 }
 
 // One persistent block; nw warps, 16 rows each.
@@ -428,16 +408,15 @@ __device__ __forceinline__ void mask_step(const ScoredParams& p, const TileGeom&
 // A block takes a contiguous run of units, consecutive bricks of one head, so
 // that most find the table of their predecessor: it depends on the head and on
 // where the rows' windows lie about them, the same for all rows away from the
-// borders. The warps run freely over a ring of
-// stages; the warp that is last to be done with a stage starts the load of the
-// chunk that is next to use it, so no warp waits for an empty stage and none
-// is kept for loading (a ninth would cost the other eight a fifth of their
-// registers).
+// borders. The warps run freely over a ring of stages; the warp that is last
+// to be done with a stage starts the load of the chunk that is next to use it,
+// so no warp waits for an empty stage and none is kept for loading (a
+// thirteenth would cost the other twelve a fifth of their registers).
 template <int HD, int MODE>
 __global__ void __launch_bounds__(max_warps(HD, MODE) * 32, blocks_per_sm(HD, MODE))
 scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ CUtensorMap tm_f1,
              const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_x1,
-             const ScoredParams p, const TileGeom g) {
+             const __grid_constant__ ScoredParams p, const __grid_constant__ TileGeom g) {
     constexpr bool DKV = MODE == kDkv;
     constexpr int NF = MODE == kFwd ? 1 : 2;           // fixed tensors
     constexpr int FB = fixed_buffers(HD, MODE);
@@ -452,7 +431,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const int nw = g.nw, S = g.stages;
     const int f_rows = g.st * g.bh * g.sw;
     const uint32_t f_region = (uint32_t(f_rows) * HDB * 2 + 1023u) & ~1023u, f_bytes = f_region * REG;
-    const uint32_t x_region = g.x_bytes / REG;
+    const uint32_t x_bytes = g.x_bytes, x_region = REG > 1 ? x_bytes / REG : 0;
+    const bool docs = p.doc != nullptr;
+    const int side_rows = g.cr * g.cc + 16;            // of a stage's (lse, delta) and documents
+    const int side_lanes = DKV || docs ? 32 : 0;       // lanes that bring those in
 
     // control words: abort flag, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
@@ -461,7 +443,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S + FB; ++i) {
-            mbar_init(sy.bar(i), DKV && i < S ? 33 : 1);
+            mbar_init(sy.bar(i), i < S ? 1 + side_lanes : 1);
             done[i] = 0;
             issued[i] = 0;
         }
@@ -470,68 +452,65 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     }
     // The stages start as zeros: a step reads up to 15 rows past a chunk's box,
     // whose probabilities are 0, and those rows must hold numbers.
-    for (int i = threadIdx.x * 16; i < 2 * S * g.x_bytes; i += blockDim.x * 16)
+    for (int i = threadIdx.x * 16; i < g.off_lut - g.off_x; i += blockDim.x * 16)
         *reinterpret_cast<uint4*>(base_ptr + g.off_x + i) = make_uint4(0, 0, 0, 0);
-    if (DKV)
-        for (int i = threadIdx.x * 8; i < S * (g.cr * g.cc + 16) * 8; i += blockDim.x * 8)
-            *reinterpret_cast<uint2*>(base_ptr + g.off_stat + i) = make_uint2(0, 0);
     // (row, column) of the chunk's index, as floats
     float2* const hw = reinterpret_cast<float2*>(base_ptr + g.off_hw);
-    for (int i = threadIdx.x; i < g.cr * g.cc + 16; i += blockDim.x)
-        hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
+    for (int i = threadIdx.x; i < side_rows; i += blockDim.x) hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
     fence_proxy_async_smem();
     __syncthreads();
 
     const int u0 = int(int64_t(g.units) * blockIdx.x / gridDim.x);
     const int u1 = int(int64_t(g.units) * (blockIdx.x + 1) / gridDim.x);
-    const int per_unit = g.nt * g.nhc * g.nwc;
-    const int stat_rows = g.cr * g.cc + 16;
 
-    // Start the load of chunk c of unit u into stage s (a whole warp). A chunk
+    // Start the load of chunk (it, ih, iw) of a unit into stage s (a whole warp). A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
-    auto load_chunk = [&](int u, int c, int s) {
-        const int head = fast_div(g.div_bricks, u);
-        const Brick o = brick_of(g, u - head * g.bricks);
-        const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
-        const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
-        int t, h, w;
-        chunk_at(g, c, bt.x, bh.x, bw.x, &t, &h, &w);
-        const bool inside = t < bt.y && h < bh.y && w < bw.y;
-        const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * g.x_bytes;
+    auto load_chunk = [&](const Unit& x, int it, int ih, int iw, int s) {
+        const int t = x.bt.x + it, h = x.bh.x + ih * g.cr, w = x.bw.x + iw * g.cc;
+        const bool inside = t < x.bt.y && h < x.bh.y && w < x.bw.y;
+        const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * x_bytes;
         if (lane == 0) {
             ++issued[s];
             if (inside) {
                 mbar_arrive_expect_tx(full, 2 * REG * g.cr * g.cc * HDB * 2);
                 for (int r = 0; r < REG; ++r) {
-                    tma_load_5d(x0 + r * x_region, &tm_x0, full, head * HD + r * 64, w, h, t, o.b);
-                    tma_load_5d(x0 + g.x_bytes + r * x_region, &tm_x1, full, head * HD + r * 64, w, h, t, o.b);
+                    tma_load_5d(x0 + r * x_region, &tm_x0, full, x.head * HD + r * 64, w, h, t, x.o.b);
+                    tma_load_5d(x0 + x_bytes + r * x_region, &tm_x1, full, x.head * HD + r * 64, w, h, t, x.o.b);
                 }
             } else {
                 mbar_arrive(full);
             }
         }
-        if (DKV) {
-            const uint32_t st = base + g.off_stat + s * stat_rows * 8;
-            if (inside)
-                for (int i = lane; i < g.cr * g.cc; i += 32) {
-                    const int y = h + i / g.cc, x = w + i % g.cc;
-                    if (y < p.H && x < p.W) {
-                        const float2* src = p.stat + token_of(p, o.b, t, y, x) * p.NH + head;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + i * 8), "l"(src) : "memory");
+        if (side_lanes) {
+            if (inside) {
+                const uint32_t st = base + g.off_stat + s * side_rows * 8, dc = base + g.off_doc + s * side_rows * 4;
+                const int64_t frame = token_of(p, x.o.b, t, h, w);
+                const int rows = min(g.cr, p.H - h), cols = min(g.cc, p.W - w);
+                for (int i = lane; i < rows * g.cc; i += 32) {
+                    const float2 at = hw[i];
+                    const int y = int(at.x), c = int(at.y);
+                    if (c < cols) {
+                        const int64_t tok = frame + int64_t(y) * p.W + c;
+                        if (DKV)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + i * 8),
+                                         "l"(p.stat + tok * p.NH + x.head) : "memory");
+                        if (docs)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dc + i * 4), "l"(p.doc + tok)
+                                         : "memory");
                     }
                 }
+            }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
         }
     };
-    auto load_fixed = [&](int u, int f) {   // one thread
-        const int head = fast_div(g.div_bricks, u);
-        const Brick o = brick_of(g, u - head * g.bricks);
-        const uint32_t full = sy.bar(S + f), x = base + f * NF * f_bytes;
+    auto load_fixed = [&](const Unit& x, int f) {   // one thread
+        const uint32_t full = sy.bar(S + f), to = base + f * NF * f_bytes;
         ++issued[S + f];
         mbar_arrive_expect_tx(full, NF * REG * f_rows * HDB * 2);
         for (int r = 0; r < REG; ++r) {
-            tma_load_5d(x + r * f_region, &tm_f0, full, head * HD + r * 64, o.w0, o.h0, o.t0, o.b);
-            if (NF == 2) tma_load_5d(x + f_bytes + r * f_region, &tm_f1, full, head * HD + r * 64, o.w0, o.h0, o.t0, o.b);
+            tma_load_5d(to + r * f_region, &tm_f0, full, x.head * HD + r * 64, x.o.w0, x.o.h0, x.o.t0, x.o.b);
+            if (NF == 2)
+                tma_load_5d(to + f_bytes + r * f_region, &tm_f1, full, x.head * HD + r * 64, x.o.w0, x.o.h0, x.o.t0, x.o.b);
         }
     };
     // This warp is done with a ring place; true where it is the last to be.
@@ -543,76 +522,115 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                          : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
         return __shfl_sync(0xffffffffu, n, 0) == uint32_t(nw - 1);
     };
-    if (warp == 0 && u0 < u1) {
-        for (int f = 0; f < FB; ++f)
-            if (lane == 0 && u0 + f < u1) load_fixed(u0 + f, f);
-        for (int s = 0; s < S; ++s)
-            if (u0 + s / per_unit < u1) load_chunk(u0 + s / per_unit, s % per_unit, s);
+    Unit cur = unit_of<DKV>(p, g, min(u0, g.units - 1));
+    // the chunk that is S after the current one: its place in its unit, and whether
+    // that is the next (there are at most per_unit stages)
+    int nt_i = 0, nh_i = 0, nw_i = 0;
+    bool in_next = false;
+    auto advance = [&] {
+        if (++nw_i < g.nwc) return;
+        nw_i = 0;
+        if (++nh_i < g.nhc) return;
+        nh_i = 0;
+        if (++nt_i < g.nt) return;
+        nt_i = 0;
+        in_next = true;
+    };
+    for (int s = 0; s < S; ++s) {
+        if (warp == 0 && u0 < u1) load_chunk(cur, nt_i, nh_i, nw_i, s);
+        advance();
+    }
+    if (warp == 0 && lane == 0 && u0 < u1) {
+        load_fixed(cur, 0);
+        if (FB == 2 && u0 + 1 < u1) load_fixed(unit_of<DKV>(p, g, u0 + 1), 1);
     }
 
     const int r0 = lane >> 2, c2 = lane & 3;    // this thread's rows r0, r0 + 8 and column pair of a fragment
     const int hi = lane >> 4;
-    uint32_t* mask = reinterpret_cast<uint32_t*>(base_ptr + g.off_mask) + warp * g.mask_steps * 8;
+    const int n_hw = g.sh * g.sw;               // (h, w) places of a warp's rows
+    const bool same_hw = n_hw <= 8, use_lut = g.lut != 0;
+    float* const lut = reinterpret_cast<float*>(base_ptr + g.off_lut) + warp * n_hw * g.lut_pitch;
+    uint32_t* const mask = reinterpret_cast<uint32_t*>(base_ptr + g.off_lut) + warp * g.frame_steps * 8;
+    const float* const lut_row = lut + (r0 % n_hw) * g.lut_pitch + 2 * c2;
+    const int row_t0 = r0 / n_hw, row_t1 = (r0 + 8) / n_hw;
+    const int row_h0 = r0 / g.sw % g.sh, row_h1 = (r0 + 8) / g.sw % g.sh, row_w = r0 % g.sw;
+    const int frag_row = (((lane & 15) / n_hw) * g.bh + warp * g.sh + (lane & 15) / g.sw % g.sh) * g.sw + (lane & 15) % g.sw;
+    const uint32_t lane_x = swizzled<HD>(lane & 15, hi, 0);   // of the first rows of a stage
     const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
     const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
     const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
-    uint32_t it = 0, ft = 0;
-    int lut_head = -1, lut_h = -2, lut_w = -2, lut_chunk = -1;
-    float* const lut = reinterpret_cast<float*>(base_ptr + g.off_lut) + warp * g.sh * g.sw * g.lut_pitch;
-    const bool same_hw = g.sh * g.sw <= 8;
+    int lut_head = -1, lut_h = -2, lut_w = -2, lut_chunk = -1;   // what the table holds
+    float sl[3] = {0.f, 0.f, 0.f};
+    int s = 0;             // stage of the current chunk, and the parity of its turn
+    uint32_t turn = 0, ft = 0;
     bool ok = true;
 
     for (int u = u0; u < u1; ++u, ++ft) {
-        const int head = fast_div(g.div_bricks, u);
-        const Brick o = brick_of(g, u - head * g.bricks);
-        const int wh0 = o.h0 + warp * g.sh;
-        const int2 bt = box_of(DKV, o.t0, g.st, p.KT, p.T), bh = box_of(DKV, o.h0, g.bh, p.KH, p.H);
-        const int2 bw = box_of(DKV, o.w0, g.sw, p.KW, p.W);
+        const Unit next = unit_of<DKV>(p, g, min(u + 1, g.units - 1));
+        in_next = S == g.nt * g.nhc * g.nwc;
+        const Brick o = cur.o;
+        const int head = cur.head, wh0 = o.h0 + warp * g.sh;
         // this warp's part of the streamed rows; none where its rows lie past the grid
         int2 mine = box_of(DKV, wh0, g.sh, p.KH, p.H);
         if (wh0 >= p.H) mine = make_int2(0, 0);
 
-        // the row of mask_step: lane & 15
-        const int mr = lane & 15;
-        const int mw = o.w0 + mr % g.sw, mh = wh0 + mr / g.sw % g.sh, mt = o.t0 + mr / (g.sw * g.sh);
-        const bool mvalid = mw < p.W && mh < p.H && mt < p.T;
-        const int mdoc = p.doc && mvalid ? p.doc[token_of(p, o.b, mt, mh, mw)] : 0;
+        // rows r0 and r0 + 8, in one column of the grid
+        const int rw = o.w0 + row_w;
+        const int rt[2] = {o.t0 + row_t0, o.t0 + row_t1}, rh[2] = {wh0 + row_h0, wh0 + row_h1};
+        int64_t token[2];   // -1 past the grid
+        float ref[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};   // log2 reference that scores are taken from
+        int row_doc[2] = {-1, -1};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            token[i] = rw < p.W && rh[i] < p.H && rt[i] < p.T ? token_of(p, o.b, rt[i], rh[i], rw) : -1;
+            if (token[i] < 0) continue;
+            if (MODE == kDq) {
+                const float2 x = p.stat[token[i] * p.NH + head];
+                ref[i] = x.x;
+                delta[i] = x.y;
+            }
+            if (docs) row_doc[i] = p.doc[token[i]];
+        }
         const int prefix = p.prefix ? p.prefix[o.b] : 0;
-        auto box_rows = [&](int h, int* first) {   // rows of this warp in the chunk at h
-            *first = max(mine.x, h);
-            return min(mine.y, h + g.cr) - *first;
-        };
-        float sl[3] = {0.f, 0.f, 0.f};
-        if (biased) {
+        if (biased && head != lut_head) {
             load_slopes(p, head, sl);
 #pragma unroll
             for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
         }
-        // the table: for each (h, w) of the rows, the bias of a frame's columns, -inf
-        // outside the window. It is kept while the head (where it matters) and the rows'
-        // place stay; rows away from the borders all have the same.
+
+        // The table: for each (h, w) of the rows, the bias of a frame's columns, -inf
+        // outside the window (or the mask words: word r of a step holds row r in its low
+        // and row r + 8 in its high half). It is kept while the head (where it matters) and
+        // the rows' place stay; rows away from the borders all have the same.
         const int place_h = wh0 >= p.KH && wh0 + g.sh - 1 < p.H - p.KH ? -1 : wh0;
         const int place_w = o.w0 >= p.KW && o.w0 + g.sw - 1 < p.W - p.KW ? -1 : o.w0;
-        const int in_chunk = g.nhc > 1 ? mine.x - bh.x : 0;
-        if (g.lut && ((biased && head != lut_head) || place_h != lut_h || place_w != lut_w || in_chunk != lut_chunk)) {
+        const int in_chunk = g.nhc > 1 ? mine.x - cur.bh.x : 0;
+        if ((biased && head != lut_head) || place_h != lut_h || place_w != lut_w || in_chunk != lut_chunk) {
             __syncwarp();
-            for (int rp = hi; rp < g.sh * g.sw; rp += 2) {
-                const int lh = wh0 + rp / g.sw, lw = o.w0 + rp % g.sw;
+            for (int r = use_lut ? hi : 0; r < (use_lut ? n_hw : 16); r += use_lut ? 2 : 1) {
+                const int lh = wh0 + r / g.sw % g.sh, lw = o.w0 + r % g.sw;
                 const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
                 const float h_n = lh < p.H && lw < p.W ? float(range_hi(DKV, lh, p.KH, p.H) - h_lo) : 0.f;
                 const float w_n = float(range_hi(DKV, lw, p.KW, p.W) - w_lo);
-                float* to = lut + rp * g.lut_pitch + (lane & 15);
-                for (int h = bh.x; h < bh.y; h += g.cr)
-                    for (int w = bw.x; w < bw.y; w += g.cc) {
-                        int hf;
-                        const int rows = box_rows(h, &hf);
+                float* to = lut + r * g.lut_pitch + (lane & 15);
+                uint16_t* words = reinterpret_cast<uint16_t*>(mask) + 2 * (r & 7) + (r >> 3);
+                for (int h = cur.bh.x; h < cur.bh.y; h += g.cr)
+                    for (int w = cur.bw.x; w < cur.bw.y; w += g.cc) {
+                        const int hf = max(mine.x, h), rows = min(mine.y, h + g.cr) - hf;
                         const float h_in = float(hf - h_lo), w_in = float(w - w_lo), h_far = float(hf - lh), w_far = float(w - lw);
                         const float n_rows = float(rows);
-                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16, to += 16) {
+                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16) {
                             const float2 at = hw[i0 + (lane & 15)];
                             const bool in = at.x < n_rows && at.x + h_in >= 0.f && at.x + h_in < h_n &&
                                             at.y + w_in >= 0.f && at.y + w_in < w_n;
-                            *to = in ? fmaf(sl[1], fabsf(at.x + h_far), sl[2] * fabsf(at.y + w_far)) : -INFINITY;
+                            if (use_lut) {
+                                *to = in ? fmaf(sl[1], fabsf(at.x + h_far), sl[2] * fabsf(at.y + w_far)) : -INFINITY;
+                                to += 16;
+                            } else {
+                                const uint32_t bits = __ballot_sync(0xffffffffu, in) & 0xffffu;
+                                if (lane == 0) *words = uint16_t(bits);
+                                words += 16;
+                            }
                         }
                     }
             }
@@ -622,66 +640,18 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             lut_w = place_w;
             lut_chunk = in_chunk;
         }
-        // documents: no masks where the whole box is of one document, the rows' own
-        bool masked = g.mask_steps > 0;
-        if (masked && g.lut) {
-            const int d0 = __shfl_sync(0xffffffffu, mdoc, 0);
-            bool other = mvalid && (mdoc != d0 || mdoc < 0);
-            const int width = bw.y - bw.x;
-            for (int t = bt.x; t < bt.y; ++t)
-                for (int i = lane; i < (mine.y - mine.x) * width; i += 32) {
-                    const int y = i / width;
-                    other = other || p.doc[token_of(p, o.b, t, mine.x + y, bw.x + i - y * width)] != d0;
-                }
-            masked = __any_sync(0xffffffffu, other);
-        }
-        if (masked && g.mask_kept) {
-            int ms = 0;
-            __syncwarp();
-            for (int t = bt.x; t < bt.y; ++t)
-                for (int h = bh.x; h < bh.y; h += g.cr)
-                    for (int w = bw.x; w < bw.y; w += g.cc) {
-                        int hf;
-                        const int rows = box_rows(h, &hf);
-                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16, ++ms)
-                            mask_step<DKV>(p, g, mask + ms * 8, o.b, mh, mw, mvalid, mdoc, t, hf, w, rows, i0);
-                    }
-            __syncwarp();
-        }
-
-        // rows r0 and r0 + 8, in one column of the grid
-        const int rw = o.w0 + r0 % g.sw;
-        int rt[2], rh[2];
-        int64_t row[2];   // token * NH + head, -1 past the grid
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = r0 + 8 * i;
-            rh[i] = wh0 + r / g.sw % g.sh;
-            rt[i] = o.t0 + r / (g.sw * g.sh);
-            row[i] = rw < p.W && rh[i] < p.H && rt[i] < p.T ? token_of(p, o.b, rt[i], rh[i], rw) * p.NH + head : -1;
-        }
-        float ref[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};   // log2 reference that scores are taken from
-        if (MODE == kDq) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (row[i] >= 0) {
-                    const float2 s = p.stat[row[i]];
-                    ref[i] = s.x;
-                    delta[i] = s.y;
-                }
-        }
 
         // fixed fragments
         uint32_t fa[NFR][KB][4];
         const int fb = ft % FB;
-        if (!(ok = ok && sy.wait(sy.bar(S + fb), (ft / FB) & 1u))) break;
-        const int fr = (((lane & 15) / (g.sw * g.sh)) * g.bh + warp * g.sh + (lane & 15) / g.sw % g.sh) * g.sw + (lane & 15) % g.sw;
+        if (!(ok = sy.wait(sy.bar(S + fb), (ft / FB) & 1u))) break;
         const uint32_t f_at = base + fb * NF * f_bytes;
 #pragma unroll
         for (int n = 0; n < NFR; ++n)
 #pragma unroll
-            for (int kk = 0; kk < KB; ++kk) ldsm4(f_at + n * f_bytes + swizzled<HD>(fr, 2 * kk + hi, f_region), fa[n][kk]);
-        if (NFR == NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(u + FB, fb);
+            for (int kk = 0; kk < KB; ++kk)
+                ldsm4(f_at + n * f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), fa[n][kk]);
+        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) load_fixed(next, fb);
 
         float acc0[2 * KB][4], acc1[MODE == kDkv ? 2 * KB : 1][4];   // O, dQ or dK; dV
 #pragma unroll
@@ -695,206 +665,244 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // any for a row that has met no key, so that ref starts at a score
         float l[2] = {0.f, 0.f}, grow[2] = {-INFINITY, -INFINITY};
 
-        int ms = 0, ls = 0, lut_t = bt.x;   // next steps of the masks and of the table, and its frame
-        for (int c = 0; c < per_unit; ++c, ++it) {
-            const int s = it % S;
-            if (!(ok = sy.wait(sy.bar(s), (it / S) & 1u))) break;
-            int t, h, w;
-            chunk_at(g, c, bt.x, bh.x, bw.x, &t, &h, &w);
-            int hf;
-            const int rows = box_rows(h, &hf);
-            const int n = t < bt.y && h < bh.y && w < bw.y ? rows * g.cc : 0;
-            const uint32_t x0 = base + g.off_x + 2 * s * g.x_bytes;
-            const int first = (hf - h) * g.cc;
-            const float2* stat = reinterpret_cast<const float2*>(base_ptr + g.off_stat + s * stat_rows * 8) + first;
-            if (t != lut_t) {
-                lut_t = t;
-                ls = 0;
-            }
-            if (masked && !g.mask_kept) {
-                ms = 0;
-                __syncwarp();
-                for (int i0 = 0, k = 0; i0 < n; i0 += 16, ++k)
-                    mask_step<DKV>(p, g, mask + k * 8, o.b, mh, mw, mvalid, mdoc, t, hf, w, rows, i0);
-                __syncwarp();
-            }
+        for (int it = 0; it < g.nt && ok; ++it) {
+            const int t = cur.bt.x + it;
             // the frame's part of the score: -inf for a row that does not see it
             float far_t[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int qt = DKV ? t : rt[i], kt = DKV ? rt[i] : t;
                 const bool sees = t >= range_lo(DKV, rt[i], p.KT, p.T) && t < range_hi(DKV, rt[i], p.KT, p.T) &&
-                                  (!p.prefix || kt <= qt || kt < prefix);
+                                  (!p.prefix || kt <= qt || kt < prefix) && !(docs && row_doc[i] < 0);
                 far_t[i] = sees ? sl[0] * float(abs(t - rt[i])) : -INFINITY;
             }
-            const bool frame_seen = __any_sync(0xffffffffu, fmaxf(far_t[0], far_t[1]) > -INFINITY);
-            const int n_steps = n > 0 ? (n + 15) >> 4 : 0;
-            const float at_h[2] = {float(hf - rh[0]), float(hf - rh[1])}, at_w = float(w - rw);
-            // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
-            // step moves them by 16 rows and a column block by an exclusive or
-            uint32_t a0 = x0 + swizzled<HD>(first + (lane & 15), hi, x_region);
-            const float* lut_at = lut + (r0 % (g.sh * g.sw)) * g.lut_pitch + ls * 16 + 2 * c2;
-            ls += n_steps;
-            const uint32_t* mask_at = mask + ms * 8 + r0;
-            ms += n_steps;
-            for (int k = 0; frame_seen && k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8) {
-                bool mixed = false;
-                uint32_t bits = 0;   // 0, 1, 8, 9: the columns of row r0; 16, 17, 24, 25: of r0 + 8
-                if (masked) {
-                    bits = *mask_at;
-                    if (!__any_sync(0xffffffffu, bits)) continue;
-                    mixed = !__all_sync(0xffffffffu, bits == 0xffffffffu);
-                    bits >>= 2 * c2;
-                }
-                auto seen = [&](int i) { return (bits >> (8 * (i >> 2) + 16 * ((i >> 1) & 1) + (i & 1)) & 1u) != 0u; };
-                // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of
-                // row (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1)
-                float sc[8] = {}, dp[8] = {};
-                uint32_t f[4];
-#pragma unroll
-                for (int kk = 0; kk < KB; ++kk) {
-                    ldsm4((a0 + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
-                    mma16816(sc, fa[0][kk], f[0], f[2]);
-                    mma16816(sc + 4, fa[0][kk], f[1], f[3]);
-                }
-                if (MODE != kFwd) {
-#pragma unroll
-                    for (int kk = 0; kk < KB; ++kk) {
-                        uint32_t a[4];
-                        if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(fr, 2 * kk + hi, f_region), a);
-                        ldsm4((a0 + g.x_bytes + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
-                        mma16816(dp, NFR < NF ? a : fa[NFR - 1][kk], f[0], f[2]);
-                        mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], f[1], f[3]);
+            // no row of this warp sees the frame: its chunks are passed over
+            const bool frame_seen = t < cur.bt.y && __any_sync(0xffffffffu, fmaxf(far_t[0], far_t[1]) > -INFINITY);
+            int step = 0;   // of the frame's table
+            for (int ih = 0; ih < g.nhc && ok; ++ih)
+                for (int iw = 0; iw < g.nwc; ++iw) {
+                    if (!(ok = sy.wait(sy.bar(s), turn))) break;
+                    const int h = cur.bh.x + ih * g.cr, w = cur.bw.x + iw * g.cc;
+                    const int hf = max(mine.x, h), n = (min(mine.y, h + g.cr) - hf) * g.cc;
+                    int n_steps = n > 0 && w < cur.bw.y ? (n + 15) >> 4 : 0;
+                    const int first = (hf - h) * g.cc;
+                    const int* key_doc = reinterpret_cast<const int*>(base_ptr + g.off_doc) + s * side_rows + first;
+                    const float* lut_at = lut_row + step * 16;
+                    const uint32_t* mask_at = mask + step * 8 + r0;
+                    step += n_steps;
+                    // documents: a comparison for each score where the chunk holds others than
+                    // the rows', none where it does not, no work where no row's is there
+                    bool mixed = false;
+                    if (docs && frame_seen) {
+                        const int d0 = __shfl_sync(0xffffffffu, row_doc[0], 0);
+                        bool other = row_doc[0] != d0 || row_doc[1] != d0;
+                        bool met = __any_sync(0xffffffffu, other);
+                        for (int i = lane; i < n; i += 32) {
+                            other = other || key_doc[i] != d0;
+                            met = met || key_doc[i] == d0;
+                        }
+                        mixed = __any_sync(0xffffffffu, other);
+                        if (!__any_sync(0xffffffffu, met)) n_steps = 0;
                     }
-                }
-                float2 cs[4];   // DKV: (log2 reference, delta) of the four columns
-                if (DKV) {
+                    if (!frame_seen) n_steps = 0;
+
+                    // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
+                    // step moves them by 16 rows and a column block by an exclusive or
+                    uint32_t a0 = base + g.off_x + 2 * s * x_bytes;
+                    a0 += first % 8 ? swizzled<HD>(first + (lane & 15), hi, 0) : first * (HDB * 2) + lane_x;
+                    const float2* stat = reinterpret_cast<const float2*>(base_ptr + g.off_stat) + s * side_rows + first;
+                    auto columns = [&](uint32_t at, int kk) { return (at + (kk >> 2) * x_region) ^ ((kk & 3) << 5); };
+                    auto scores = [&](uint32_t at, float* sc) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) cs[j] = stat[k * 16 + 8 * (j >> 1) + 2 * c2 + (j & 1)];
-                }
-                // bias minus reference, log2: pair 2 * (tile) + row
-                uint64_t s2[4];
-                const float from[2] = {far_t[0] - ref[0], far_t[1] - ref[1]};
-                if (g.lut) {
+                        for (int i = 0; i < 8; ++i) sc[i] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 8 * j);
-                        const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 8 * j);
-                        s2[2 * j] = f2_add(x, f2_dup(from[0]));
-                        s2[2 * j + 1] = f2_add(y, f2_dup(from[1]));
-                    }
-                } else if (biased) {
+                        for (int kk = 0; kk < KB; ++kk) {
+                            uint32_t f[4];
+                            ldsm4(columns(at, kk), f);
+                            mma16816(sc, fa[0][kk], f[0], f[2]);
+                            mma16816(sc + 4, fa[0][kk], f[1], f[3]);
+                        }
+                    };
+                    // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
+                    // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1). FWD takes the next
+                    // step's before this one's softmax, so that the two overlap.
+                    constexpr bool AHEAD = MODE == kFwd && HD <= 64;
+                    float ahead[8];
+                    if (AHEAD && n_steps > 0) scores(a0, ahead);
+                    for (int k = 0; k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8, stat += 16, key_doc += 16) {
+                        const uint32_t a1 = a0 + x_bytes;
+                        float sc[8], dp[8] = {};
+                        uint32_t f[4];
+                        if (AHEAD) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float4 x = *reinterpret_cast<const float4*>(hw + k * 16 + 8 * j + 2 * c2);
-                        const float d0 = fabsf(x.y + at_w), d1 = fabsf(x.w + at_w);
+                            for (int i = 0; i < 8; ++i) sc[i] = ahead[i];
+                            if (k + 1 < n_steps) scores(a0 + 16 * HDB * 2, ahead);
+                        } else {
+                            scores(a0, sc);
+                        }
+                        if (MODE != kFwd) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            s2[2 * j + i] = f2_pack(fmaf(sl[1], fabsf(x.x + at_h[i]), fmaf(sl[2], d0, from[i])),
-                                                    fmaf(sl[1], fabsf(x.z + at_h[i]), fmaf(sl[2], d1, from[i])));
-                    }
-                } else {
+                            for (int kk = 0; kk < KB; ++kk) {
+                                uint32_t a[4];
+                                if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), a);
+                                ldsm4(columns(a1, kk), f);
+                                mma16816(dp, NFR < NF ? a : fa[NFR - 1][kk], f[0], f[2]);
+                                mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], f[1], f[3]);
+                            }
+                        }
+                        float2 cs[4];   // DKV: (log2 reference, delta) of the four columns
+                        if (DKV) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s2[j] = f2_dup(from[j & 1]);
-                }
-                if (DKV) {
+                            for (int j = 0; j < 4; ++j) cs[j] = stat[8 * (j >> 1) + 2 * c2 + (j & 1)];
+                        }
+                        // bias minus reference, log2: pair 2 * tile + row
+                        uint64_t s2[4];
+                        const float from[2] = {far_t[0] - ref[0], far_t[1] - ref[1]};
+                        uint32_t bits = 0;   // 0, 1, 8, 9: the columns of row r0; 16, 17, 24, 25: of r0 + 8
+                        if (use_lut) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s2[j] = f2_add(s2[j], f2_pack(-cs[2 * (j >> 1)].x, -cs[2 * (j >> 1) + 1].x));
-                }
-                uint64_t th[4];
+                            for (int j = 0; j < 2; ++j) {
+                                const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 8 * j);
+                                const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 8 * j);
+                                s2[2 * j] = f2_add(x, f2_dup(from[0]));
+                                s2[2 * j + 1] = f2_add(y, f2_dup(from[1]));
+                            }
+                        } else {
+                            bits = *mask_at >> (2 * c2);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) th[j] = f2_pack(sc[2 * j], sc[2 * j + 1]);
-                if (capped) {
+                            for (int j = 0; j < 4; ++j) s2[j] = f2_dup(from[j & 1]);
+                            if (biased) {
+                                const float at_h[2] = {float(hf - rh[0]), float(hf - rh[1])}, at_w = float(w - rw);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) th[j] = f2_mul(th[j], f2_dup(inv_cap));
-                    tanh_all(th);
-                }
-                float sv[8];   // scores minus reference, log2; then probabilities
+                                for (int j = 0; j < 2; ++j) {
+                                    const float4 x = *reinterpret_cast<const float4*>(hw + k * 16 + 8 * j + 2 * c2);
+                                    const float d0 = fabsf(x.y + at_w), d1 = fabsf(x.w + at_w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f2_unpack(f2_fma(th[j], f2_dup(to_log2), s2[j]), sv[2 * j], sv[2 * j + 1]);
-                if (mixed) {
+                                    for (int i = 0; i < 2; ++i)
+                                        s2[2 * j + i] = f2_pack(fmaf(sl[1], fabsf(x.x + at_h[i]), fmaf(sl[2], d0, from[i])),
+                                                                fmaf(sl[1], fabsf(x.z + at_h[i]), fmaf(sl[2], d1, from[i])));
+                                }
+                            }
+                        }
+                        if (DKV) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sv[i] = seen(i) ? sv[i] : -INFINITY;
-                }
-                if (MODE == kFwd) {
-                    float top[2];
+                            for (int j = 0; j < 4; ++j)
+                                s2[j] = f2_add(s2[j], f2_pack(-cs[2 * (j >> 1)].x, -cs[2 * (j >> 1) + 1].x));
+                        }
+                        uint64_t th[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        top[i] = fmaxf(max3f(sv[2 * i], sv[2 * i + 1], sv[4 + 2 * i]), sv[5 + 2 * i]);
-                    if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
+                        for (int j = 0; j < 4; ++j) th[j] = f2_pack(sc[2 * j], sc[2 * j + 1]);
+                        if (capped) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x = top[i];
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                            // a row that has met a key moves up only; the first keys set the reference
-                            const bool begun = grow[i] == kGrow;
-                            if (begun || x == -INFINITY) x = fmaxf(x, 0.f);
-                            else grow[i] = kGrow;
-                            const float r = begun ? ex2_approx(-x) : 0.f;
-                            ref[i] += x;
-                            l[i] *= r;
+                            for (int j = 0; j < 4; ++j) th[j] = f2_mul(th[j], f2_dup(inv_cap));
+                            tanh_all(th);
+                        }
+                        float sv[8];   // scores minus reference, log2; then probabilities
 #pragma unroll
-                            for (int j = 0; j < 2 * KB; ++j) {
-                                acc0[j][2 * i] *= r;
-                                acc0[j][2 * i + 1] *= r;
+                        for (int j = 0; j < 4; ++j)
+                            f2_unpack(f2_fma(th[j], f2_dup(to_log2), s2[j]), sv[2 * j], sv[2 * j + 1]);
+                        if (mixed || !use_lut) {
+                            uint32_t gone = 0;   // bit i: value i is masked
+                            if (!use_lut) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    gone |= (~bits >> (8 * (i >> 2) + 16 * ((i >> 1) & 1) + (i & 1)) & 1u) << i;
+                            }
+                            if (mixed) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int2 d = make_int2(key_doc[8 * j + 2 * c2], key_doc[8 * j + 2 * c2 + 1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        gone |= uint32_t(row_doc[i >> 1] != ((i & 1) ? d.y : d.x)) << (4 * j + i);
+                                }
                             }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) sv[4 * (j >> 1) + 2 * i + (j & 1)] -= x;
+                            for (int i = 0; i < 8; ++i) {
+                                if (gone >> i & 1u) {   // 0 times what a masked row holds need not be 0
+                                    sv[i] = -INFINITY;
+                                    if (MODE != kFwd) dp[i] = 0.f;
+                                }
+                            }
+                        }
+                        if (MODE == kFwd) {
+                            float top[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                top[i] = fmaxf(max3f(sv[2 * i], sv[2 * i + 1], sv[4 + 2 * i]), sv[5 + 2 * i]);
+                            if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    float x = top[i];
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                                    // a row that has met a key moves up only; the first keys set the reference
+                                    const bool begun = grow[i] == kGrow;
+                                    if (begun || x == -INFINITY) x = fmaxf(x, 0.f);
+                                    else grow[i] = kGrow;
+                                    const float r = begun ? ex2_approx(-x) : 0.f;
+                                    ref[i] += x;
+                                    l[i] *= r;
+#pragma unroll
+                                    for (int j = 0; j < 2 * KB; ++j) {
+                                        acc0[j][2 * i] *= r;
+                                        acc0[j][2 * i + 1] *= r;
+                                    }
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) sv[4 * (j >> 1) + 2 * i + (j & 1)] -= x;
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+                            l[0] += (sv[0] + sv[1]) + (sv[4] + sv[5]);
+                            l[1] += (sv[2] + sv[3]) + (sv[6] + sv[7]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint64_t d = f2_add(f2_pack(dp[2 * j], dp[2 * j + 1]),
+                                                    DKV ? f2_pack(-cs[2 * (j >> 1)].y, -cs[2 * (j >> 1) + 1].y)
+                                                        : f2_dup(-delta[j & 1]));
+                                d = f2_mul(d, f2_pack(sv[2 * j], sv[2 * j + 1]));
+                                if (capped) d = f2_mul(d, f2_fma(f2_mul(th[j], f2_dup(-1.f)), th[j], f2_dup(1.f)));
+                                f2_unpack(d, dp[2 * j], dp[2 * j + 1]);
+                            }
+                        }
+                        // products: probabilities (FWD: with V; DKV: with dO) and da (with K or Q)
+                        if (MODE != kDq) {
+                            const uint32_t a[4] = {pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]),
+                                                   pack_bf16x2(sv[4], sv[5]), pack_bf16x2(sv[6], sv[7])};
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) {
+                                ldsm4t(columns(a1, kk), f);
+                                mma16816(MODE == kFwd ? acc0[2 * kk] : acc1[MODE == kDkv ? 2 * kk : 0], a, f[0], f[1]);
+                                mma16816(MODE == kFwd ? acc0[2 * kk + 1] : acc1[MODE == kDkv ? 2 * kk + 1 : 0], a, f[2], f[3]);
+                            }
+                        }
+                        if (MODE != kFwd) {
+                            const uint32_t a[4] = {pack_bf16x2(dp[0], dp[1]), pack_bf16x2(dp[2], dp[3]),
+                                                   pack_bf16x2(dp[4], dp[5]), pack_bf16x2(dp[6], dp[7])};
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) {
+                                ldsm4t(columns(a0, kk), f);
+                                mma16816(acc0[2 * kk], a, f[0], f[1]);
+                                mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
-                    l[0] += (sv[0] + sv[1]) + (sv[4] + sv[5]);
-                    l[1] += (sv[2] + sv[3]) + (sv[6] + sv[7]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint64_t d = f2_add(f2_pack(dp[2 * j], dp[2 * j + 1]),
-                                            DKV ? f2_pack(-cs[2 * (j >> 1)].y, -cs[2 * (j >> 1) + 1].y) : f2_dup(-delta[j & 1]));
-                        d = f2_mul(d, f2_pack(sv[2 * j], sv[2 * j + 1]));
-                        if (capped) d = f2_mul(d, f2_fma(f2_mul(th[j], f2_dup(-1.f)), th[j], f2_dup(1.f)));
-                        f2_unpack(d, dp[2 * j], dp[2 * j + 1]);
-                    }
-                    if (mixed) {   // 0 times what a masked row holds need not be 0
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dp[i] = seen(i) ? dp[i] : 0.f;
+                    // the stage's next chunk is S further on
+                    if (last_done(s) && (!in_next || u + 1 < u1))
+                        load_chunk(in_next ? next : cur, nt_i, nh_i, nw_i, s);
+                    advance();
+                    if (++s == S) {
+                        s = 0;
+                        turn ^= 1u;
                     }
                 }
-                // products: probabilities (FWD: with V; DKV: with dO) and da (with K or Q)
-                if (MODE != kDq) {
-                    const uint32_t a[4] = {pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]),
-                                           pack_bf16x2(sv[4], sv[5]), pack_bf16x2(sv[6], sv[7])};
-#pragma unroll
-                    for (int kk = 0; kk < KB; ++kk) {
-                        ldsm4t((a0 + g.x_bytes + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
-                        mma16816(MODE == kFwd ? acc0[2 * kk] : acc1[MODE == kDkv ? 2 * kk : 0], a, f[0], f[1]);
-                        mma16816(MODE == kFwd ? acc0[2 * kk + 1] : acc1[MODE == kDkv ? 2 * kk + 1 : 0], a, f[2], f[3]);
-                    }
-                }
-                if (MODE != kFwd) {
-                    const uint32_t a[4] = {pack_bf16x2(dp[0], dp[1]), pack_bf16x2(dp[2], dp[3]),
-                                           pack_bf16x2(dp[4], dp[5]), pack_bf16x2(dp[6], dp[7])};
-#pragma unroll
-                    for (int kk = 0; kk < KB; ++kk) {
-                        ldsm4t((a0 + (kk >> 2) * x_region) ^ ((kk & 3) << 5), f);
-                        mma16816(acc0[2 * kk], a, f[0], f[1]);
-                        mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
-                    }
-                }
-            }
-            // the stage's next chunk is S further on
-            if (last_done(s)) {
-                const int n_next = c + S;
-                const int u_next = u + n_next / per_unit;
-                if (u_next < u1) load_chunk(u_next, n_next % per_unit, s);
-            }
         }
         if (!ok) break;
-        if (NFR < NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(u + FB, fb);
+        if (NFR < NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(unit_of<DKV>(p, g, u + FB), fb);
 
         // rows out; a row that is not finite throughout is computed again by itself
         uint32_t bad = 0;
@@ -905,8 +913,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
                 inv[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
-                if (row[i] >= 0 && c2 == 0 && p.lse)
-                    p.lse[row[i]] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
+                if (token[i] >= 0 && c2 == 0 && p.lse)
+                    p.lse[token[i] * p.NH + head] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
                 if (!(l[i] < INFINITY)) bad |= 1u << i;
             }
         }
@@ -914,10 +922,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         const int64_t ts0 = MODE == kFwd ? int64_t(p.NH) * HD : MODE == kDq ? p.dq_ts : p.dk_ts;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool valid = row[i] >= 0;
-            const int64_t token = valid ? token_of(p, o.b, rt[i], rh[i], rw) : 0;
-            uint16_t* const at0 = out0 + token * ts0 + int64_t(head) * HD + 2 * c2;
-            uint16_t* const at1 = p.dv + token * p.dv_ts + int64_t(head) * HD + 2 * c2;
+            const bool valid = token[i] >= 0;
+            uint16_t* const at0 = out0 + token[i] * ts0 + int64_t(head) * HD + 2 * c2;
+            uint16_t* const at1 = p.dv + token[i] * p.dv_ts + int64_t(head) * HD + 2 * c2;
             float probe = 0.f;   // 0 times every value: NaN where one is not finite
 #pragma unroll
             for (int j = 0; j < 2 * KB; ++j) {
@@ -940,7 +947,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 q.b = o.b;
                 q.w = o.w0 + r % g.sw;
                 q.h = wh0 + r / g.sw % g.sh;
-                q.t = o.t0 + r / (g.sw * g.sh);
+                q.t = o.t0 + r / n_hw;
                 q.head = head;
                 q.token = token_of(p, q.b, q.t, q.h, q.w);
                 __syncwarp();
@@ -949,11 +956,12 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 else row_dkv<HD>(p, q, lane);
             }
         }
+        cur = next;
     }
 
     // every issued load lands before the block may exit: where all went well
     // each has been waited for
-    if (DKV) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (side_lanes) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (misc[0] && threadIdx.x == 0)
         for (int i = 0; i < S + FB; ++i)
@@ -1011,7 +1019,7 @@ int align_up(int x, int a) { return (x + a - 1) / a * a; }
 constexpr int kSmemMax = 227 * 1024;
 
 // Shared memory of a geometry with `stages` stages and chunks of cr x cc.
-void lay_out(TileGeom* g, int hd, int mode) {
+void lay_out(TileGeom* g, int hd, int mode, bool docs) {
     const bool dkv = mode == kDkv;
     const int nf = (mode == kFwd ? 1 : 2) * fixed_buffers(hd, mode);
     const int hdb = hd > 64 ? 64 : hd, reg = hd > 64 ? hd / 64 : 1;
@@ -1019,16 +1027,17 @@ void lay_out(TileGeom* g, int hd, int mode) {
     g->x_bytes = align_up((g->cr * g->cc + 16) * hdb * 2, 1024) * reg;
     g->off_x = f_region * reg * nf;
     g->off_stat = g->off_x + 2 * g->stages * g->x_bytes;
-    g->off_lut = align_up(g->off_stat + (dkv ? g->stages * (g->cr * g->cc + 16) * 8 : 0), 16);
-    g->off_mask = g->off_lut + (g->lut ? g->nw * g->sh * g->sw * g->lut_pitch * 4 : 0);
-    g->off_hw = align_up(g->off_mask + g->nw * g->mask_steps * 32, 16);
+    const int side_rows = g->cr * g->cc + 16;
+    g->off_doc = align_up(g->off_stat + (dkv ? g->stages * side_rows * 8 : 0), 16);
+    g->off_lut = align_up(g->off_doc + (docs ? g->stages * side_rows * 4 : 0), 16);
+    g->off_hw = align_up(g->off_lut + g->nw * (g->lut ? g->sh * g->sw * g->lut_pitch * 4 : g->frame_steps * 32), 16);
     g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
     g->smem = g->off_bar + kControl + 8 * kMaxRing + 1024;
 }
 
 // Chooses rows, brick and chunks for the least modelled time.
 bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms) {
-    const bool dkv = mode == kDkv;
+    const bool dkv = mode == kDkv, docs = p.doc != nullptr;
     const int blocks = blocks_per_sm(hd, mode);
     double best_cost = 0;
     bool found = false;
@@ -1065,26 +1074,16 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     // steps of a warp: its box in each chunk that it meets, rounded up to 16
                     const int met = (eh_w + g.cr - 2) / g.cr + 1 < nhc ? (eh_w + g.cr - 2) / g.cr + 1 : nhc;
                     const int all = et * g.nwc * ((eh_w * g.cc + 15) / 16 + met - 1);
-                    // the table of a frame (pitch: the rows of eight lanes in different banks),
-                    // and masks of a whole unit where there are documents; where the table does
-                    // not fit, masks hold the windows too; where they do not fit, a chunk's
-                    const int frame = all / et * 16;
-                    g.stages = 2;
+                    // the table of a frame (its pitch puts the rows of four lanes in different
+                    // banks), or mask words where it does not fit
+                    g.frame_steps = all / et;
+                    g.stages = et * nhc * g.nwc < 2 ? 1 : 2;
                     g.lut = 1;
-                    g.lut_pitch = frame / 16 * 16 + 8;
-                    g.mask_steps = p.doc ? all : 0;
-                    g.mask_kept = p.doc ? 1 : 0;
-                    lay_out(&g, hd, mode);
+                    g.lut_pitch = g.frame_steps * 16 + 8;
+                    lay_out(&g, hd, mode, docs);
                     if (g.smem > room) {
                         g.lut = 0;
-                        g.mask_steps = all;
-                        g.mask_kept = 1;
-                        lay_out(&g, hd, mode);
-                    }
-                    if (g.smem > room) {
-                        g.mask_kept = 0;
-                        g.mask_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
-                        lay_out(&g, hd, mode);
+                        lay_out(&g, hd, mode, docs);
                     }
                     if (g.smem > room) {
                         if (g.cr > 1) continue;
@@ -1093,19 +1092,18 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                         parts = (eh + 255) / 256 - 1;
                         continue;
                     }
-                    while (g.stages < kMaxStages) {
+                    while (g.stages < kMaxStages && g.stages < et * nhc * g.nwc) {
                         TileGeom more = g;
                         ++more.stages;
-                        lay_out(&more, hd, mode);
+                        lay_out(&more, hd, mode, docs);
                         if (more.smem > room) break;
                         g = more;
                     }
-                    // cycles: a step issues about 140 instructions (more without the table, and
-                    // for masks made again for each chunk) on four schedulers that find one
-                    // ready in two cycles of three; a frame's load takes its latency and 45
-                    // bytes a cycle, and hides behind the computation where two frames fit
-                    const double instr = (mode == kFwd ? 140.0 : 190.0) * (hd + 64) / 128 * (g.lut ? 1.0 : 1.4) *
-                                         (g.mask_steps && !g.mask_kept ? 1.8 : 1.0);
+                    // cycles: a step issues about 140 instructions (more without the table) on
+                    // four schedulers that find one ready in two cycles of three; a frame's
+                    // load takes its latency and 45 bytes a cycle, and hides behind the
+                    // computation where two frames fit
+                    const double instr = (mode == kFwd ? 140.0 : 190.0) * (hd + 64) / 128 * (g.lut ? 1.0 : 1.4);
                     const double work = double(all) / et * nw * blocks * instr / 2.6;
                     const double lat = double(all) / et * instr * 2.5;
                     const double comp = work > lat ? work : lat;
@@ -1130,8 +1128,6 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
         best->div_nbw = make_fastdiv(best->nbw);
         best->div_nbh = make_fastdiv(best->nbh);
         best->div_nbt = make_fastdiv(best->nbt);
-        best->div_chunks = make_fastdiv(best->nhc * best->nwc);
-        best->div_nwc = make_fastdiv(best->nwc);
     }
     return found;
 }
