@@ -26,6 +26,7 @@
 // that is not finite: 0 times infinity is not 0 in a tile's products.
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 #include "na3d_host.cuh"
@@ -323,15 +324,19 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f2_dup(float x) { return f2_pack(x, x); }
 
+// tanh z = z + z^3 P(z^2) for |z| <= 1/2.
+__device__ constexpr float kTanh[4] = {-0.333331435918808f, 0.13325878977775574f, -0.05304548144340515f,
+                                       0.0172414667904377f};
+
 // tanh to about 2^-22 of its value. Up to 1/2 (a score of half the cap) an odd
 // polynomial, fitted for the least largest relative error (1.5e-8), keeps the
 // special-function unit free; larger values take 1 - 2 / (1 + e^2|z|), once
 // any of the warp's needs it.
 __device__ __forceinline__ uint64_t tanh_poly(uint64_t z) {
     const uint64_t y = f2_mul(z, z);
-    uint64_t p = f2_fma(y, f2_dup(0.0172414667904377f), f2_dup(-0.05304548144340515f));
-    p = f2_fma(y, p, f2_dup(0.13325878977775574f));
-    p = f2_fma(y, p, f2_dup(-0.333331435918808f));
+    uint64_t p = f2_fma(y, f2_dup(kTanh[3]), f2_dup(kTanh[2]));
+    p = f2_fma(y, p, f2_dup(kTanh[1]));
+    p = f2_fma(y, p, f2_dup(kTanh[0]));
     return f2_fma(f2_mul(z, y), p, z);
 }
 __device__ __forceinline__ float tanh_exp(float z) {
@@ -382,6 +387,27 @@ __device__ __forceinline__ Brick brick_of(const TileGeom& g, int n) {
 __device__ __forceinline__ int2 box_of(bool dkv, int i, int n, int K, int N) {
     const int first = min(i, N - 1), last = min(i + n - 1, N - 1);
     return make_int2(range_lo(dkv, first, K, N), range_hi(dkv, last, K, N));
+}
+
+// The reference of row i of a thread's two moves up by the returned amount, for
+// scores (minus the old one) up to `top`: what the row has summed is scaled. A
+// row that has met a key moves up only; the first keys set the reference.
+template <int N>
+__device__ __forceinline__ float move_reference(float top, float& grow, float& ref, float& l, float (&acc)[N][4], int i) {
+    float x = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    const bool begun = grow == kGrow;
+    if (begun || x == -INFINITY) x = fmaxf(x, 0.f);
+    else grow = kGrow;
+    const float r = begun ? ex2_approx(-x) : 0.f;
+    ref += x;
+    l *= r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        acc[j][2 * i] *= r;
+        acc[j][2 * i + 1] *= r;
+    }
+    return x;
 }
 
 // The (head, brick) of a unit and the box that its chunks cover.
@@ -465,7 +491,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
     // Start the load of chunk (it, ih, iw) of a unit into stage s (a whole warp). A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
-    auto load_chunk = [&](const Unit& x, int it, int ih, int iw, int s) {
+    auto load_chunk = [&](int u, int it, int ih, int iw, int s) {
+        const Unit x = unit_of<DKV>(p, g, u);
         const int t = x.bt.x + it, h = x.bh.x + ih * g.cr, w = x.bw.x + iw * g.cc;
         const bool inside = t < x.bt.y && h < x.bh.y && w < x.bw.y;
         const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * x_bytes;
@@ -522,7 +549,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                          : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
         return __shfl_sync(0xffffffffu, n, 0) == uint32_t(nw - 1);
     };
-    Unit cur = unit_of<DKV>(p, g, min(u0, g.units - 1));
     // the chunk that is S after the current one: its place in its unit, and whether
     // that is the next (there are at most per_unit stages)
     int nt_i = 0, nh_i = 0, nw_i = 0;
@@ -537,11 +563,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         in_next = true;
     };
     for (int s = 0; s < S; ++s) {
-        if (warp == 0 && u0 < u1) load_chunk(cur, nt_i, nh_i, nw_i, s);
+        if (warp == 0 && u0 < u1) load_chunk(u0, nt_i, nh_i, nw_i, s);
         advance();
     }
     if (warp == 0 && lane == 0 && u0 < u1) {
-        load_fixed(cur, 0);
+        load_fixed(unit_of<DKV>(p, g, u0), 0);
         if (FB == 2 && u0 + 1 < u1) load_fixed(unit_of<DKV>(p, g, u0 + 1), 1);
     }
 
@@ -559,6 +585,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
     const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
     const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
+    const float half_cap = 0.5f * p.softcap, inv2 = inv_cap * inv_cap;
+    const float poly[4] = {kTanh[0] * inv2 * kLog2e, kTanh[1] * inv2 * inv2 * kLog2e, kTanh[2] * inv2 * inv2 * inv2 * kLog2e,
+                           kTanh[3] * inv2 * inv2 * inv2 * inv2 * kLog2e};
     int lut_head = -1, lut_h = -2, lut_w = -2, lut_chunk = -1;   // what the table holds
     float sl[3] = {0.f, 0.f, 0.f};
     int s = 0;             // stage of the current chunk, and the parity of its turn
@@ -566,8 +595,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     bool ok = true;
 
     for (int u = u0; u < u1; ++u, ++ft) {
-        const Unit next = unit_of<DKV>(p, g, min(u + 1, g.units - 1));
         in_next = S == g.nt * g.nhc * g.nwc;
+        const Unit cur = unit_of<DKV>(p, g, u);
         const Brick o = cur.o;
         const int head = cur.head, wh0 = o.h0 + warp * g.sh;
         // this warp's part of the streamed rows; none where its rows lie past the grid
@@ -598,6 +627,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
         }
 
+        // Scores under a cap whose bias falls with the distance need no running maximum: a
+        // row's largest lies within the cap of 0 (its own position has no bias), so that
+        // the powers stay in the range of fp32 and bf16 with 0 as the reference.
+        const bool bounded = MODE == kFwd && capped && to_log2 <= 96.f && fmaxf(fmaxf(sl[0], sl[1]), sl[2]) <= 0.f;
         // The table: for each (h, w) of the rows, the bias of a frame's columns, -inf
         // outside the window (or the mask words: word r of a step holds row r in its low
         // and row r + 8 in its high half). It is kept while the head (where it matters) and
@@ -651,7 +684,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < KB; ++kk)
                 ldsm4(f_at + n * f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), fa[n][kk]);
-        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) load_fixed(next, fb);
+        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) load_fixed(unit_of<DKV>(p, g, u + 1), fb);
 
         float acc0[2 * KB][4], acc1[MODE == kDkv ? 2 * KB : 1][4];   // O, dQ or dK; dV
 #pragma unroll
@@ -724,22 +757,141 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         }
                     };
                     // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
-                    // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1). FWD takes the next
-                    // step's before this one's softmax, so that the two overlap.
-                    constexpr bool AHEAD = MODE == kFwd && HD <= 64;
-                    float ahead[8];
-                    if (AHEAD && n_steps > 0) scores(a0, ahead);
+                    // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
+                    // The plain chunks of the forward pass, with the table and without documents to
+                    // compare, take N steps at a time, so that the steps' chains of matrix products
+                    // and powers overlap.
+                    if (MODE == kFwd && use_lut && !mixed && (!capped || bounded)) {
+                        uint32_t ak[KB];   // a column block's address; the next step's is 16 rows on
+#pragma unroll
+                        for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
+                        auto plain = [&](auto n_const, auto cap_const) {
+                            constexpr int N = decltype(n_const)::value;
+                            constexpr bool CAP = decltype(cap_const)::value;
+                            float sc[N][8];
+#pragma unroll
+                            for (int m = 0; m < N; ++m) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) sc[m][i] = 0.f;
+#pragma unroll
+                                for (int kk = 0; kk < KB; ++kk) {
+                                    uint32_t f[4];
+                                    ldsm4(ak[kk] + m * 16 * HDB * 2, f);
+                                    mma16816(sc[m], fa[0][kk], f[0], f[2]);
+                                    mma16816(sc[m] + 4, fa[0][kk], f[1], f[3]);
+                                }
+                            }
+                            uint64_t s2[N][4], x2[N][4];   // bias minus reference, then the score; a
+                            const uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
+#pragma unroll
+                            for (int m = 0; m < N; ++m)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 16 * m + 8 * j);
+                                    const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 16 * m + 8 * j);
+                                    s2[m][2 * j] = f2_add(x, from[0]);
+                                    s2[m][2 * j + 1] = f2_add(y, from[1]);
+                                }
+                            float big = 0.f;
+#pragma unroll
+                            for (int m = 0; m < N; ++m)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    x2[m][j] = f2_pack(sc[m][2 * j], sc[m][2 * j + 1]);
+                                    if (CAP) big = max3f(big, fabsf(sc[m][2 * j]), fabsf(sc[m][2 * j + 1]));
+                                }
+                            if (CAP && __any_sync(0xffffffffu, big > half_cap)) {
+#pragma unroll
+                                for (int m = 0; m < N; ++m)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        float z[2];
+                                        f2_unpack(f2_mul(x2[m][j], f2_dup(inv_cap)), z[0], z[1]);
+                                        float q[2];
+                                        f2_unpack(tanh_poly(f2_pack(z[0], z[1])), q[0], q[1]);
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i) q[i] = fabsf(z[i]) > 0.5f ? tanh_exp(z[i]) : q[i];
+                                        s2[m][j] = f2_fma(f2_pack(q[0], q[1]), f2_dup(to_log2), s2[m][j]);
+                                    }
+                            } else if (CAP) {
+                                // c tanh(a / c) = a + a^3 P(a^2): the polynomial of tanh_poly in a itself
+#pragma unroll
+                                for (int m = 0; m < N; ++m)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) {
+                                        const uint64_t a = x2[m][j], y = f2_mul(a, a);
+                                        uint64_t q = f2_fma(y, f2_dup(poly[3]), f2_dup(poly[2]));
+                                        q = f2_fma(y, q, f2_dup(poly[1]));
+                                        q = f2_fma(y, q, f2_dup(poly[0]));
+                                        s2[m][j] = f2_fma(f2_mul(a, y), q, f2_fma(a, f2_dup(kLog2e), s2[m][j]));
+                                    }
+                            } else {
+#pragma unroll
+                                for (int m = 0; m < N; ++m)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) s2[m][j] = f2_fma(x2[m][j], f2_dup(kLog2e), s2[m][j]);
+                            }
+                            float sv[N][8];
+#pragma unroll
+                            for (int m = 0; m < N; ++m)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) f2_unpack(s2[m][j], sv[m][2 * j], sv[m][2 * j + 1]);
+                            if (!CAP) {
+                                float top[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    top[i] = -INFINITY;
+#pragma unroll
+                                    for (int m = 0; m < N; ++m)
+                                        top[i] = max3f(max3f(top[i], sv[m][2 * i], sv[m][2 * i + 1]), sv[m][4 + 2 * i], sv[m][5 + 2 * i]);
+                                }
+                                if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const float x = move_reference(top[i], grow[i], ref[i], l[i], acc0, i);
+#pragma unroll
+                                        for (int m = 0; m < N; ++m)
+#pragma unroll
+                                            for (int j = 0; j < 4; ++j) sv[m][4 * (j >> 1) + 2 * i + (j & 1)] -= x;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int m = 0; m < N; ++m) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) sv[m][i] = ex2_approx(sv[m][i]);
+                                l[0] += (sv[m][0] + sv[m][1]) + (sv[m][4] + sv[m][5]);
+                                l[1] += (sv[m][2] + sv[m][3]) + (sv[m][6] + sv[m][7]);
+                                const uint32_t a[4] = {pack_bf16x2(sv[m][0], sv[m][1]), pack_bf16x2(sv[m][2], sv[m][3]),
+                                                       pack_bf16x2(sv[m][4], sv[m][5]), pack_bf16x2(sv[m][6], sv[m][7])};
+#pragma unroll
+                                for (int kk = 0; kk < KB; ++kk) {
+                                    uint32_t f[4];
+                                    ldsm4t(ak[kk] + x_bytes + m * 16 * HDB * 2, f);
+                                    mma16816(acc0[2 * kk], a, f[0], f[1]);
+                                    mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
+                                }
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) ak[kk] += N * 16 * HDB * 2;
+                            lut_at += 16 * N;
+                        };
+                        using std::integral_constant;
+                        int k = 0;
+                        if (capped) {
+                            for (; k + 2 <= n_steps; k += 2) plain(integral_constant<int, 2>{}, integral_constant<bool, true>{});
+                            if (k < n_steps) plain(integral_constant<int, 1>{}, integral_constant<bool, true>{});
+                        } else {
+                            for (; k + 2 <= n_steps; k += 2) plain(integral_constant<int, 2>{}, integral_constant<bool, false>{});
+                            if (k < n_steps) plain(integral_constant<int, 1>{}, integral_constant<bool, false>{});
+                        }
+                        n_steps = 0;
+                    }
                     for (int k = 0; k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8, stat += 16, key_doc += 16) {
                         const uint32_t a1 = a0 + x_bytes;
                         float sc[8], dp[8] = {};
                         uint32_t f[4];
-                        if (AHEAD) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) sc[i] = ahead[i];
-                            if (k + 1 < n_steps) scores(a0 + 16 * HDB * 2, ahead);
-                        } else {
-                            scores(a0, sc);
-                        }
+                        scores(a0, sc);
                         if (MODE != kFwd) {
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk) {
@@ -833,21 +985,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    float x = top[i];
-                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                                    // a row that has met a key moves up only; the first keys set the reference
-                                    const bool begun = grow[i] == kGrow;
-                                    if (begun || x == -INFINITY) x = fmaxf(x, 0.f);
-                                    else grow[i] = kGrow;
-                                    const float r = begun ? ex2_approx(-x) : 0.f;
-                                    ref[i] += x;
-                                    l[i] *= r;
-#pragma unroll
-                                    for (int j = 0; j < 2 * KB; ++j) {
-                                        acc0[j][2 * i] *= r;
-                                        acc0[j][2 * i + 1] *= r;
-                                    }
+                                    const float x = move_reference(top[i], grow[i], ref[i], l[i], acc0, i);
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) sv[4 * (j >> 1) + 2 * i + (j & 1)] -= x;
                                 }
@@ -893,7 +1031,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     }
                     // the stage's next chunk is S further on
                     if (last_done(s) && (!in_next || u + 1 < u1))
-                        load_chunk(in_next ? next : cur, nt_i, nh_i, nw_i, s);
+                        load_chunk(u + (in_next ? 1 : 0), nt_i, nh_i, nw_i, s);
                     advance();
                     if (++s == S) {
                         s = 0;
@@ -956,7 +1094,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 else row_dkv<HD>(p, q, lane);
             }
         }
-        cur = next;
     }
 
     // every issued load lands before the block may exit: where all went well
@@ -1047,7 +1184,7 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
             if (sw > 8) continue;
             const int et = widest(dkv, st, p.KT, p.T), ew = widest(dkv, sw, p.KW, p.W);
             const int eh_w = widest(dkv, sh, p.KH, p.H);
-            for (int nw = 1; nw <= max_warps(hd, mode); nw += nw < 4 ? 1 : nw < 8 ? 2 : 4) {
+            for (int nw = 1; nw <= max_warps(hd, mode); ++nw) {
                 if ((nw - 1) * sh >= p.H) break;
                 TileGeom g{};
                 g.st = st; g.sh = sh; g.sw = sw; g.nw = nw; g.bh = nw * sh;
