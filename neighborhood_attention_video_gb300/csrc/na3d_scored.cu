@@ -344,6 +344,13 @@ __device__ __forceinline__ float tanh_exp(float z) {
     return copysignf(fmaf(-2.f, rcp_approx(e + 1.f), 1.f), z);
 }
 
+// Largest of a, |b| and |c|, NaN where one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return d;
+}
+
 // z[0..3], pairs, to their tanh.
 __device__ __forceinline__ void tanh_all(uint64_t* z) {
     float x[8];
@@ -372,14 +379,16 @@ struct Brick {
     int b, t0, h0, w0;   // first row
 };
 
+// Bricks run along T first: neighbours there share their rows' places in the
+// grid's (h, w) plane, and most of their frames.
 __device__ __forceinline__ Brick brick_of(const TileGeom& g, int n) {
     Brick o;
-    int q = fast_div(g.div_nbw, n);
+    int q = fast_div(g.div_nbt, n);
+    o.t0 = (n - q * g.nbt) * g.st; n = q;
+    q = fast_div(g.div_nbw, n);
     o.w0 = (n - q * g.nbw) * g.sw; n = q;
-    q = fast_div(g.div_nbh, n);
-    o.h0 = (n - q * g.nbh) * g.bh; n = q;
-    o.b = fast_div(g.div_nbt, n);
-    o.t0 = (n - o.b * g.nbt) * g.st;
+    o.b = fast_div(g.div_nbh, n);
+    o.h0 = (n - o.b * g.nbh) * g.bh;
     return o;
 }
 
@@ -426,6 +435,30 @@ __device__ __forceinline__ Unit unit_of(const ScoredParams& p, const TileGeom& g
     x.bh = box_of(DKV, x.o.h0, g.bh, p.KH, p.H);
     x.bw = box_of(DKV, x.o.w0, g.sw, p.KW, p.W);
     return x;
+}
+
+// The unit after x.
+template <bool DKV>
+__device__ __forceinline__ void next_unit(const ScoredParams& p, const TileGeom& g, Unit& x) {
+    x.o.t0 += g.st;
+    if (x.o.t0 >= p.T) {
+        x.o.t0 = 0;
+        x.o.w0 += g.sw;
+        if (x.o.w0 >= p.W) {
+            x.o.w0 = 0;
+            x.o.h0 += g.bh;
+            if (x.o.h0 >= p.H) {
+                x.o.h0 = 0;
+                if (++x.o.b == p.B) {
+                    x.o.b = 0;
+                    ++x.head;
+                }
+            }
+            x.bh = box_of(DKV, x.o.h0, g.bh, p.KH, p.H);
+        }
+        x.bw = box_of(DKV, x.o.w0, g.sw, p.KW, p.W);
+    }
+    x.bt = box_of(DKV, x.o.t0, g.st, p.KT, p.T);
 }
 
 // One persistent block; nw warps, 16 rows each.
@@ -491,8 +524,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
     // Start the load of chunk (it, ih, iw) of a unit into stage s (a whole warp). A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
-    auto load_chunk = [&](int u, int it, int ih, int iw, int s) {
-        const Unit x = unit_of<DKV>(p, g, u);
+    auto load_chunk = [&](const Unit& x, int it, int ih, int iw, int s) {
         const int t = x.bt.x + it, h = x.bh.x + ih * g.cr, w = x.bw.x + iw * g.cc;
         const bool inside = t < x.bt.y && h < x.bh.y && w < x.bw.y;
         const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * x_bytes;
@@ -549,6 +581,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                          : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
         return __shfl_sync(0xffffffffu, n, 0) == uint32_t(nw - 1);
     };
+    Unit cur = unit_of<DKV>(p, g, min(u0, g.units - 1));
     // the chunk that is S after the current one: its place in its unit, and whether
     // that is the next (there are at most per_unit stages)
     int nt_i = 0, nh_i = 0, nw_i = 0;
@@ -563,11 +596,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         in_next = true;
     };
     for (int s = 0; s < S; ++s) {
-        if (warp == 0 && u0 < u1) load_chunk(u0, nt_i, nh_i, nw_i, s);
+        if (warp == 0 && u0 < u1) load_chunk(cur, nt_i, nh_i, nw_i, s);
         advance();
     }
     if (warp == 0 && lane == 0 && u0 < u1) {
-        load_fixed(unit_of<DKV>(p, g, u0), 0);
+        load_fixed(cur, 0);
         if (FB == 2 && u0 + 1 < u1) load_fixed(unit_of<DKV>(p, g, u0 + 1), 1);
     }
 
@@ -596,7 +629,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
     for (int u = u0; u < u1; ++u, ++ft) {
         in_next = S == g.nt * g.nhc * g.nwc;
-        const Unit cur = unit_of<DKV>(p, g, u);
         const Brick o = cur.o;
         const int head = cur.head, wh0 = o.h0 + warp * g.sh;
         // this warp's part of the streamed rows; none where its rows lie past the grid
@@ -606,21 +638,32 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // rows r0 and r0 + 8, in one column of the grid
         const int rw = o.w0 + row_w;
         const int rt[2] = {o.t0 + row_t0, o.t0 + row_t1}, rh[2] = {wh0 + row_h0, wh0 + row_h1};
-        int64_t token[2];   // -1 past the grid
+        const bool row_in[2] = {rw < p.W && rh[0] < p.H && rt[0] < p.T, rw < p.W && rh[1] < p.H && rt[1] < p.T};
         float ref[2] = {0.f, 0.f}, delta[2] = {0.f, 0.f};   // log2 reference that scores are taken from
         int row_doc[2] = {-1, -1};
+        // the frames that a row sees (FWD, DQ) or that see it: its window's, less those that
+        // come too late; none for a row past the grid or in no document
+        const int prefix = p.prefix ? p.prefix[o.b] : 0;
+        int t_lo[2], t_n[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            token[i] = rw < p.W && rh[i] < p.H && rt[i] < p.T ? token_of(p, o.b, rt[i], rh[i], rw) : -1;
-            if (token[i] < 0) continue;
-            if (MODE == kDq) {
-                const float2 x = p.stat[token[i] * p.NH + head];
-                ref[i] = x.x;
-                delta[i] = x.y;
+            int lo = range_lo(DKV, rt[i], p.KT, p.T), end = range_hi(DKV, rt[i], p.KT, p.T);
+            if (p.prefix) {
+                if (!DKV) end = min(end, max(rt[i] + 1, prefix));
+                else if (rt[i] >= prefix) lo = max(lo, rt[i]);
             }
-            if (docs) row_doc[i] = p.doc[token[i]];
+            if (MODE == kDq || docs) {
+                const int64_t token = row_in[i] ? token_of(p, o.b, rt[i], rh[i], rw) : 0;
+                if (MODE == kDq) {
+                    const float2 x = p.stat[token * p.NH + head];
+                    ref[i] = x.x;
+                    delta[i] = x.y;
+                }
+                if (docs) row_doc[i] = p.doc[token];
+            }
+            t_lo[i] = lo;
+            t_n[i] = row_in[i] && !(docs && row_doc[i] < 0) ? end - lo : 0;
         }
-        const int prefix = p.prefix ? p.prefix[o.b] : 0;
         if (biased && head != lut_head) {
             load_slopes(p, head, sl);
 #pragma unroll
@@ -684,7 +727,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < KB; ++kk)
                 ldsm4(f_at + n * f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), fa[n][kk]);
-        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) load_fixed(unit_of<DKV>(p, g, u + 1), fb);
+        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) {
+            Unit next = cur;
+            next_unit<DKV>(p, g, next);
+            load_fixed(next, fb);
+        }
 
         float acc0[2 * KB][4], acc1[MODE == kDkv ? 2 * KB : 1][4];   // O, dQ or dK; dV
 #pragma unroll
@@ -703,12 +750,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             // the frame's part of the score: -inf for a row that does not see it
             float far_t[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int qt = DKV ? t : rt[i], kt = DKV ? rt[i] : t;
-                const bool sees = t >= range_lo(DKV, rt[i], p.KT, p.T) && t < range_hi(DKV, rt[i], p.KT, p.T) &&
-                                  (!p.prefix || kt <= qt || kt < prefix) && !(docs && row_doc[i] < 0);
-                far_t[i] = sees ? sl[0] * float(abs(t - rt[i])) : -INFINITY;
-            }
+            for (int i = 0; i < 2; ++i)
+                far_t[i] = t - t_lo[i] >= 0 && t - t_lo[i] < t_n[i] ? sl[0] * fabsf(float(t - rt[i])) : -INFINITY;
             // no row of this warp sees the frame: its chunks are passed over
             const bool frame_seen = t < cur.bt.y && __any_sync(0xffffffffu, fmaxf(far_t[0], far_t[1]) > -INFINITY);
             int step = 0;   // of the frame's table
@@ -1030,8 +1073,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         }
                     }
                     // the stage's next chunk is S further on
-                    if (last_done(s) && (!in_next || u + 1 < u1))
-                        load_chunk(u + (in_next ? 1 : 0), nt_i, nh_i, nw_i, s);
+                    if (last_done(s) && (!in_next || u + 1 < u1)) {
+                        Unit of = cur;
+                        if (in_next) next_unit<DKV>(p, g, of);
+                        load_chunk(of, nt_i, nh_i, nw_i, s);
+                    }
                     advance();
                     if (++s == S) {
                         s = 0;
@@ -1044,39 +1090,35 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
         // rows out; a row that is not finite throughout is computed again by itself
         uint32_t bad = 0;
-        float inv[2] = {1.f, 1.f};
-        if (MODE == kFwd) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                inv[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
-                if (token[i] >= 0 && c2 == 0 && p.lse)
-                    p.lse[token[i] * p.NH + head] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
-                if (!(l[i] < INFINITY)) bad |= 1u << i;
-            }
-        }
         uint16_t* const out0 = MODE == kFwd ? p.out : MODE == kDq ? p.dq : p.dk;
         const int64_t ts0 = MODE == kFwd ? int64_t(p.NH) * HD : MODE == kDq ? p.dq_ts : p.dk_ts;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool valid = token[i] >= 0;
-            uint16_t* const at0 = out0 + token[i] * ts0 + int64_t(head) * HD + 2 * c2;
-            uint16_t* const at1 = p.dv + token[i] * p.dv_ts + int64_t(head) * HD + 2 * c2;
-            float probe = 0.f;   // 0 times every value: NaN where one is not finite
+            const int64_t token = token_of(p, o.b, rt[i], rh[i], rw);
+            float inv = 1.f;
+            float top = 0.f;   // the largest magnitude, NaN where there is one
+            if (MODE == kFwd) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                top = l[i];
+                if (row_in[i] && c2 == 0 && p.lse)
+                    p.lse[token * p.NH + head] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
+            }
+            uint16_t* const at0 = out0 + token * ts0 + int64_t(head) * HD + 2 * c2;
+            uint16_t* const at1 = p.dv + token * p.dv_ts + int64_t(head) * HD + 2 * c2;
 #pragma unroll
             for (int j = 0; j < 2 * KB; ++j) {
-                const float x = acc0[j][2 * i] * inv[i], y = acc0[j][2 * i + 1] * inv[i];
-                probe = fmaf(x, 0.f, fmaf(y, 0.f, probe));
-                if (valid) *reinterpret_cast<uint32_t*>(at0 + 8 * j) = pack_bf16x2(x, y);
+                float x = acc0[j][2 * i], y = acc0[j][2 * i + 1];
+                if (MODE == kFwd) f2_unpack(f2_mul(f2_pack(x, y), f2_dup(inv)), x, y);
+                top = max3_nan(top, x, y);
+                if (row_in[i]) *reinterpret_cast<uint32_t*>(at0 + 8 * j) = pack_bf16x2(x, y);
                 if (MODE == kDkv) {
-                    const float x1 = acc1[j][2 * i], y1 = acc1[j][2 * i + 1];
-                    probe = fmaf(x1, 0.f, fmaf(y1, 0.f, probe));
-                    if (valid) *reinterpret_cast<uint32_t*>(at1 + 8 * j) = pack_bf16x2(x1, y1);
+                    top = max3_nan(top, acc1[j][2 * i], acc1[j][2 * i + 1]);
+                    if (row_in[i]) *reinterpret_cast<uint32_t*>(at1 + 8 * j) = pack_bf16x2(acc1[j][2 * i], acc1[j][2 * i + 1]);
                 }
             }
-            if (probe != 0.f) bad |= 1u << i;
-            if (!valid) bad &= ~(1u << i);
+            if (row_in[i] && !(top < INFINITY)) bad |= 1u << i;
         }
         if (__any_sync(0xffffffffu, bad != 0u)) {
             for (int r = 0; r < 16; ++r) {
@@ -1094,6 +1136,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 else row_dkv<HD>(p, q, lane);
             }
         }
+        next_unit<DKV>(p, g, cur);
     }
 
     // every issued load lands before the block may exit: where all went well
