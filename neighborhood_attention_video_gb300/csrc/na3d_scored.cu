@@ -99,6 +99,11 @@ __device__ __forceinline__ int64_t token_of(const ScoredParams& p, int b, int t,
     return ((int64_t(b) * p.T + t) * p.H + h) * p.W + w;
 }
 
+// Place of a token's statistics: one head's are together, along the grid.
+__device__ __forceinline__ int64_t stat_at(const ScoredParams& p, int b, int64_t token, int head) {
+    return token + (int64_t(b) * (p.NH - 1) + head) * (int64_t(p.T) * p.H * p.W);
+}
+
 // May the query in document `qdoc` at frame qt see the key at frame kt?
 __device__ __forceinline__ bool visible(const ScoredParams& p, int qdoc, int kdoc, int qt, int kt, int prefix) {
     if (p.doc && (qdoc != kdoc || qdoc < 0)) return false;
@@ -212,7 +217,7 @@ __device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane) {
                 g.load(p.dout + row * HD, lane);
                 const float e = expf(s - lse);
                 dv.axpy(e, g);
-                dk.axpy(e * (g.dot(v) - p.stat[row].y) * ds, x);
+                dk.axpy(e * (g.dot(v) - p.stat[stat_at(p, o.b, tok, o.head)].y) * ds, x);
             }
     dk.store(p.dk + o.token * p.dk_ts + int64_t(o.head) * HD, lane);
     dv.store(p.dv + o.token * p.dv_ts + int64_t(o.head) * HD, lane);
@@ -225,9 +230,9 @@ enum { kFwd, kDq, kDkv };
 // Blocks an SM holds, and the most warps of a block: as many rows in flight as
 // the registers of an instance allow (accumulators, fixed fragments and about
 // 60 more a thread).
-__host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= 32 ? 2 : 1; }
+__host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= 32 && mode == kFwd ? 2 : 1; }
 __host__ __device__ constexpr int max_warps(int hd, int mode) {
-    return blocks_per_sm(hd, mode) == 2 || hd > 64 ? 8 : 12;
+    return blocks_per_sm(hd, mode) == 2 || hd > 64 || (hd > 32 && mode == kDkv) ? 8 : 12;
 }
 // Buffers of the fixed tensors: two where a step reads them again (their
 // fragments and the accumulators together exceed the registers).
@@ -262,7 +267,8 @@ struct TileGeom {
     int32_t lut;               // 1: a frame's biases and (h, w) windows come from a table of each warp,
                                // 0: its windows from mask words
     int32_t lut_pitch;         // floats of a table row (one for each (h, w) of the warp's rows)
-    int32_t frame_steps;       // steps of 16 columns that a warp's box takes in a frame, at most
+    int32_t frame_steps;       // steps of 16 columns that a warp's box takes in a frame, at most,
+    int32_t chunk_steps;       // and in a chunk
     int32_t units, bricks;     // (head, brick) pairs, brick fastest
     // shared memory, bytes from a 1024-byte boundary
     int32_t x_bytes;           // one streamed tensor of a stage (regions of 64 columns)
@@ -301,7 +307,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void mma16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -492,8 +498,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const uint32_t f_region = (uint32_t(f_rows) * HDB * 2 + 1023u) & ~1023u, f_bytes = f_region * REG;
     const uint32_t x_bytes = g.x_bytes, x_region = REG > 1 ? x_bytes / REG : 0;
     const bool docs = p.doc != nullptr;
-    const int side_rows = g.cr * g.cc + 16;            // of a stage's (lse, delta) and documents
-    const int side_lanes = DKV || docs ? 32 : 0;       // lanes that bring those in
 
     // control words: abort flag, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
@@ -502,7 +506,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S + FB; ++i) {
-            mbar_init(sy.bar(i), i < S ? 1 + side_lanes : 1);
+            mbar_init(sy.bar(i), 1);
             done[i] = 0;
             issued[i] = 0;
         }
@@ -515,51 +519,28 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         *reinterpret_cast<uint4*>(base_ptr + g.off_x + i) = make_uint4(0, 0, 0, 0);
     // (row, column) of the chunk's index, as floats
     float2* const hw = reinterpret_cast<float2*>(base_ptr + g.off_hw);
-    for (int i = threadIdx.x; i < side_rows; i += blockDim.x) hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
+    for (int i = threadIdx.x; i < g.cr * g.cc + 16; i += blockDim.x) hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
     fence_proxy_async_smem();
     __syncthreads();
 
     const int u0 = int(int64_t(g.units) * blockIdx.x / gridDim.x);
     const int u1 = int(int64_t(g.units) * (blockIdx.x + 1) / gridDim.x);
 
-    // Start the load of chunk (it, ih, iw) of a unit into stage s (a whole warp). A chunk
+    // Start the load of chunk (it, ih, iw) of a unit into stage s. A chunk
     // past the brick's own box (the boxes at the borders are smaller) brings nothing.
-    auto load_chunk = [&](const Unit& x, int it, int ih, int iw, int s) {
+    auto load_chunk = [&](const Unit& x, int it, int ih, int iw, int s) {   // one thread
         const int t = x.bt.x + it, h = x.bh.x + ih * g.cr, w = x.bw.x + iw * g.cc;
         const bool inside = t < x.bt.y && h < x.bh.y && w < x.bw.y;
         const uint32_t full = sy.bar(s), x0 = base + g.off_x + 2 * s * x_bytes;
-        if (lane == 0) {
-            ++issued[s];
-            if (inside) {
-                mbar_arrive_expect_tx(full, 2 * REG * g.cr * g.cc * HDB * 2);
-                for (int r = 0; r < REG; ++r) {
-                    tma_load_5d(x0 + r * x_region, &tm_x0, full, x.head * HD + r * 64, w, h, t, x.o.b);
-                    tma_load_5d(x0 + x_bytes + r * x_region, &tm_x1, full, x.head * HD + r * 64, w, h, t, x.o.b);
-                }
-            } else {
-                mbar_arrive(full);
-            }
+        ++issued[s];
+        if (!inside) {
+            mbar_arrive(full);
+            return;
         }
-        if (side_lanes) {
-            if (inside) {
-                const uint32_t st = base + g.off_stat + s * side_rows * 8, dc = base + g.off_doc + s * side_rows * 4;
-                const int64_t frame = token_of(p, x.o.b, t, h, w);
-                const int rows = min(g.cr, p.H - h), cols = min(g.cc, p.W - w);
-                for (int i = lane; i < rows * g.cc; i += 32) {
-                    const float2 at = hw[i];
-                    const int y = int(at.x), c = int(at.y);
-                    if (c < cols) {
-                        const int64_t tok = frame + int64_t(y) * p.W + c;
-                        if (DKV)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + i * 8),
-                                         "l"(p.stat + tok * p.NH + x.head) : "memory");
-                        if (docs)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dc + i * 4), "l"(p.doc + tok)
-                                         : "memory");
-                    }
-                }
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        mbar_arrive_expect_tx(full, 2 * REG * g.cr * g.cc * HDB * 2);
+        for (int r = 0; r < REG; ++r) {
+            tma_load_5d(x0 + r * x_region, &tm_x0, full, x.head * HD + r * 64, w, h, t, x.o.b);
+            tma_load_5d(x0 + x_bytes + r * x_region, &tm_x1, full, x.head * HD + r * 64, w, h, t, x.o.b);
         }
     };
     auto load_fixed = [&](const Unit& x, int f) {   // one thread
@@ -596,7 +577,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         in_next = true;
     };
     for (int s = 0; s < S; ++s) {
-        if (warp == 0 && u0 < u1) load_chunk(cur, nt_i, nh_i, nw_i, s);
+        if (threadIdx.x == 0 && u0 < u1) load_chunk(cur, nt_i, nh_i, nw_i, s);
         advance();
     }
     if (warp == 0 && lane == 0 && u0 < u1) {
@@ -621,6 +602,13 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const float half_cap = 0.5f * p.softcap, inv2 = inv_cap * inv_cap;
     const float poly[4] = {kTanh[0] * inv2 * kLog2e, kTanh[1] * inv2 * inv2 * kLog2e, kTanh[2] * inv2 * inv2 * inv2 * kLog2e,
                            kTanh[3] * inv2 * inv2 * inv2 * inv2 * kLog2e};
+    // Columns' documents and (lse, delta): a warp keeps those of its current chunk in a
+    // buffer of its own and the next chunk's first ones in registers meanwhile.
+    constexpr int PF = 3;
+    int* const col_doc = reinterpret_cast<int*>(base_ptr + g.off_doc) + warp * g.chunk_steps * 16;
+    float2* const col_stat = reinterpret_cast<float2*>(base_ptr + g.off_stat) + warp * g.chunk_steps * 16;
+    int pre_doc[PF] = {};
+    float2 pre_stat[DKV ? PF : 1];
     int lut_head = -1, lut_h = -2, lut_w = -2, lut_chunk = -1;   // what the table holds
     float sl[3] = {0.f, 0.f, 0.f};
     int s = 0;             // stage of the current chunk, and the parity of its turn
@@ -655,7 +643,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             if (MODE == kDq || docs) {
                 const int64_t token = row_in[i] ? token_of(p, o.b, rt[i], rh[i], rw) : 0;
                 if (MODE == kDq) {
-                    const float2 x = p.stat[token * p.NH + head];
+                    const float2 x = p.stat[stat_at(p, o.b, token, head)];
                     ref[i] = x.x;
                     delta[i] = x.y;
                 }
@@ -669,6 +657,36 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 #pragma unroll
             for (int a = 0; a < 3; ++a) sl[a] *= -kLog2e;
         }
+
+        const int d0 = docs ? __shfl_sync(0xffffffffu, row_doc[0], 0) : 0;
+        const int64_t stat0 = DKV ? stat_at(p, o.b, 0, head) : 0;
+        // one column's, of the chunk whose part for this warp starts at (t, hf, w); past the
+        // grid there is nothing, and no row sees it
+        auto fetch = [&](int i, int n, int t, int hf, int w, int& doc, float2& stat) {
+            if (i >= n) return;
+            const float2 at = hw[i];
+            const int x = w + int(at.y);
+            doc = d0;
+            stat = make_float2(0.f, 0.f);
+            if (x >= p.W) return;
+            const int64_t token = token_of(p, o.b, t, hf + int(at.x), x);
+            if (docs) doc = p.doc[token];
+            if (DKV) stat = p.stat[stat0 + token];
+        };
+        auto part_of = [&](int ih, int iw, int& hf, int& w) {   // columns of this warp in a chunk
+            const int h = cur.bh.x + ih * g.cr;
+            w = cur.bw.x + iw * g.cc;
+            hf = max(mine.x, h);
+            return w < cur.bw.y ? (min(mine.y, h + g.cr) - hf) * g.cc : 0;
+        };
+        auto prefetch = [&](int it, int ih, int iw) {
+            int hf, w;
+            const int n = part_of(ih, iw, hf, w), t = cur.bt.x + it;
+            if (t < cur.bt.y)
+#pragma unroll
+                for (int j = 0; j < PF; ++j) fetch(lane + 32 * j, n, t, hf, w, pre_doc[j], pre_stat[DKV ? j : 0]);
+        };
+        if (DKV || docs) prefetch(0, 0, 0);
 
         // Scores under a cap whose bias falls with the distance need no running maximum: a
         // row's largest lies within the cap of 0 (its own position has no bias), so that
@@ -758,47 +776,59 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             for (int ih = 0; ih < g.nhc && ok; ++ih)
                 for (int iw = 0; iw < g.nwc; ++iw) {
                     if (!(ok = sy.wait(sy.bar(s), turn))) break;
-                    const int h = cur.bh.x + ih * g.cr, w = cur.bw.x + iw * g.cc;
-                    const int hf = max(mine.x, h), n = (min(mine.y, h + g.cr) - hf) * g.cc;
-                    int n_steps = n > 0 && w < cur.bw.y ? (n + 15) >> 4 : 0;
-                    const int first = (hf - h) * g.cc;
-                    const int* key_doc = reinterpret_cast<const int*>(base_ptr + g.off_doc) + s * side_rows + first;
+                    int hf, w;
+                    const int n = part_of(ih, iw, hf, w);
+                    int n_steps = n > 0 ? (n + 15) >> 4 : 0;
+                    const int first = (hf - cur.bh.x - ih * g.cr) * g.cc;
                     const float* lut_at = lut_row + step * 16;
                     const uint32_t* mask_at = mask + step * 8 + r0;
                     step += n_steps;
                     // documents: a comparison for each score where the chunk holds others than
                     // the rows', none where it does not, no work where no row's is there
                     bool mixed = false;
-                    if (docs && frame_seen) {
-                        const int d0 = __shfl_sync(0xffffffffu, row_doc[0], 0);
-                        bool other = row_doc[0] != d0 || row_doc[1] != d0;
-                        bool met = __any_sync(0xffffffffu, other);
-                        for (int i = lane; i < n; i += 32) {
-                            other = other || key_doc[i] != d0;
-                            met = met || key_doc[i] == d0;
+                    if (DKV || docs) {
+                        bool other = docs && (row_doc[0] != d0 || row_doc[1] != d0);
+                        bool met = other;
+#pragma unroll
+                        for (int j = 0; j < PF; ++j) {
+                            const int i = lane + 32 * j;
+                            if (i < n) {
+                                if (docs) {
+                                    col_doc[i] = pre_doc[j];
+                                    other = other || pre_doc[j] != d0;
+                                    met = met || pre_doc[j] == d0;
+                                }
+                                if (DKV) col_stat[i] = pre_stat[DKV ? j : 0];
+                            }
                         }
-                        mixed = __any_sync(0xffffffffu, other);
-                        if (!__any_sync(0xffffffffu, met)) n_steps = 0;
+                        for (int i = lane + 32 * PF; i < n; i += 32) {
+                            int d = 0;
+                            float2 x = make_float2(0.f, 0.f);
+                            fetch(i, n, t, hf, w, d, x);
+                            if (docs) {
+                                col_doc[i] = d;
+                                other = other || d != d0;
+                                met = met || d == d0;
+                            }
+                            if (DKV) col_stat[i] = x;
+                        }
+                        if (docs) {
+                            mixed = __any_sync(0xffffffffu, other);
+                            if (!__any_sync(0xffffffffu, met)) n_steps = 0;
+                        }
+                        __syncwarp();
+                        const bool row_end = iw + 1 == g.nwc, part_end = row_end && ih + 1 == g.nhc;
+                        if (!part_end || it + 1 < g.nt) prefetch(it + part_end, part_end ? 0 : ih + row_end, row_end ? 0 : iw + 1);
                     }
+                    const int* key_doc = col_doc;
+                    const float2* stat = col_stat;
                     if (!frame_seen) n_steps = 0;
 
                     // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
                     // step moves them by 16 rows and a column block by an exclusive or
                     uint32_t a0 = base + g.off_x + 2 * s * x_bytes;
                     a0 += first % 8 ? swizzled<HD>(first + (lane & 15), hi, 0) : first * (HDB * 2) + lane_x;
-                    const float2* stat = reinterpret_cast<const float2*>(base_ptr + g.off_stat) + s * side_rows + first;
                     auto columns = [&](uint32_t at, int kk) { return (at + (kk >> 2) * x_region) ^ ((kk & 3) << 5); };
-                    auto scores = [&](uint32_t at, float* sc) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sc[i] = 0.f;
-#pragma unroll
-                        for (int kk = 0; kk < KB; ++kk) {
-                            uint32_t f[4];
-                            ldsm4(columns(at, kk), f);
-                            mma16816(sc, fa[0][kk], f[0], f[2]);
-                            mma16816(sc + 4, fa[0][kk], f[1], f[3]);
-                        }
-                    };
                     // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
                     // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
                     // The plain chunks of the forward pass, with the table and without documents to
@@ -813,17 +843,19 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             constexpr bool CAP = decltype(cap_const)::value;
                             float sc[N][8];
 #pragma unroll
-                            for (int m = 0; m < N; ++m) {
+                            for (int m = 0; m < N; ++m)
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) sc[m][i] = 0.f;
+                            // 2 N accumulators in turn: a product finds its sum ready
 #pragma unroll
-                                for (int kk = 0; kk < KB; ++kk) {
+                            for (int kk = 0; kk < KB; ++kk)
+#pragma unroll
+                                for (int m = 0; m < N; ++m) {
                                     uint32_t f[4];
                                     ldsm4(ak[kk] + m * 16 * HDB * 2, f);
                                     mma16816(sc[m], fa[0][kk], f[0], f[2]);
                                     mma16816(sc[m] + 4, fa[0][kk], f[1], f[3]);
                                 }
-                            }
                             uint64_t s2[N][4], x2[N][4];   // bias minus reference, then the score; a
                             const uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
 #pragma unroll
@@ -934,10 +966,14 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         const uint32_t a1 = a0 + x_bytes;
                         float sc[8], dp[8] = {};
                         uint32_t f[4];
-                        scores(a0, sc);
-                        if (MODE != kFwd) {
 #pragma unroll
-                            for (int kk = 0; kk < KB; ++kk) {
+                        for (int i = 0; i < 8; ++i) sc[i] = 0.f;
+#pragma unroll
+                        for (int kk = 0; kk < KB; ++kk) {
+                            ldsm4(columns(a0, kk), f);
+                            mma16816(sc, fa[0][kk], f[0], f[2]);
+                            mma16816(sc + 4, fa[0][kk], f[1], f[3]);
+                            if (MODE != kFwd) {
                                 uint32_t a[4];
                                 if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), a);
                                 ldsm4(columns(a1, kk), f);
@@ -1073,7 +1109,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         }
                     }
                     // the stage's next chunk is S further on
-                    if (last_done(s) && (!in_next || u + 1 < u1)) {
+                    if (last_done(s) && lane == 0 && (!in_next || u + 1 < u1)) {
                         Unit of = cur;
                         if (in_next) next_unit<DKV>(p, g, of);
                         load_chunk(of, nt_i, nh_i, nw_i, s);
@@ -1141,7 +1177,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
     // every issued load lands before the block may exit: where all went well
     // each has been waited for
-    if (side_lanes) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (misc[0] && threadIdx.x == 0)
         for (int i = 0; i < S + FB; ++i)
@@ -1172,7 +1207,10 @@ __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t
     for (int k = L / 2; k; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
     if (live && c == 0) {
         const float lse = p.lse[r];
-        p.stat[r] = lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse * kLog2e, d);
+        const int64_t token = r / p.NH;
+        const int b = int(token / (int64_t(p.T) * p.H * p.W));
+        p.stat[stat_at(p, b, token, int(r - token * p.NH))] =
+            lse == -INFINITY ? make_float2(0.f, 0.f) : make_float2(lse * kLog2e, d);
     }
 }
 
@@ -1207,9 +1245,8 @@ void lay_out(TileGeom* g, int hd, int mode, bool docs) {
     g->x_bytes = align_up((g->cr * g->cc + 16) * hdb * 2, 1024) * reg;
     g->off_x = f_region * reg * nf;
     g->off_stat = g->off_x + 2 * g->stages * g->x_bytes;
-    const int side_rows = g->cr * g->cc + 16;
-    g->off_doc = align_up(g->off_stat + (dkv ? g->stages * side_rows * 8 : 0), 16);
-    g->off_lut = align_up(g->off_doc + (docs ? g->stages * side_rows * 4 : 0), 16);
+    g->off_doc = g->off_stat + (dkv ? g->nw * g->chunk_steps * 16 * 8 : 0);
+    g->off_lut = g->off_doc + (docs ? g->nw * g->chunk_steps * 16 * 4 : 0);
     g->off_hw = align_up(g->off_lut + g->nw * (g->lut ? g->sh * g->sw * g->lut_pitch * 4 : g->frame_steps * 32), 16);
     g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
     g->smem = g->off_bar + kControl + 8 * kMaxRing + 1024;
@@ -1257,6 +1294,7 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     // the table of a frame (its pitch puts the rows of four lanes in different
                     // banks), or mask words where it does not fit
                     g.frame_steps = all / et;
+                    g.chunk_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
                     g.stages = et * nhc * g.nwc < 2 ? 1 : 2;
                     g.lut = 1;
                     g.lut_pitch = g.frame_steps * 16 + 8;
