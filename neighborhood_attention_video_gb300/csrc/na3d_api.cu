@@ -12,6 +12,7 @@
 #include "na3d.h"
 #include "na3d_host.cuh"
 #include "na3d_kernel.cuh"
+#include "na3d_lora.cuh"
 #include "na3d_proj.cuh"
 #include "na3d_scored.cuh"
 
@@ -425,12 +426,13 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv, int
 }
 
 int na3d_device_status(void* stream) {
-    unsigned int flag = 0, pflag = 0, sflag = 0;
+    unsigned int flag = 0, pflag = 0, sflag = 0, lflag = 0;
     if (na3d::take_device_error(static_cast<cudaStream_t>(stream), &flag) != cudaSuccess ||
         na3d::take_proj_error(static_cast<cudaStream_t>(stream), &pflag) != cudaSuccess ||
-        na3d::take_scored_error(static_cast<cudaStream_t>(stream), &sflag) != cudaSuccess)
+        na3d::take_scored_error(static_cast<cudaStream_t>(stream), &sflag) != cudaSuccess ||
+        na3d::take_lora_error(static_cast<cudaStream_t>(stream), &lflag) != cudaSuccess)
         return NA3D_ERR_CUDA;
-    return (flag || pflag || sflag) ? NA3D_ERR_DEVICE_TIMEOUT : NA3D_OK;
+    return (flag || pflag || sflag || lflag) ? NA3D_ERR_DEVICE_TIMEOUT : NA3D_OK;
 }
 
 }  // extern "C"

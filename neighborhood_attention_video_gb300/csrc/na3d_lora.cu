@@ -3,163 +3,922 @@
 //
 // Rows offsets[r] .. offsets[r+1] - 1 are request r's, with adapter
 // a = adapter[r] (none where the id is not in 0 .. n_ad - 1):
-//   t = scaling_a x A_a^T                     (rank R, fp32 sums)
+//   t = scaling_a x A_a^T                     (rank R, fp32 sums, rounded to bf16)
 //   qkv = s_n (x W^T + bias + t B_a^T)        (s_n = HD^-0.5 in the q block, else 1)
 // Backward, with g = s_n dqkv:
 //   u = scaling_a g B_a,  dx = g W + u A_a,
 //   dA_a = sum over the adapter's rows of u^T x,  dB_a = sum of g^T t.
 // The base weight and the scalings are frozen: they get no gradient.
+//
+// lora_down computes t and u. It writes them once for each pair of a 128-row
+// tile and a request that meets it, zeros in the rows of others, so that the
+// large product takes an adapter as R more columns of its contraction: the
+// accumulator tile of lora_gemm gets t B_a^T from the tensor cores and leaves
+// the SM once. Pair (tile i, request r) is block i + r of the workspace: along
+// the rows one of the two grows from pair to pair, so no two share a block.
+#include <atomic>
 #include <cuda_bf16.h>
 
+#include "na3d_host.cuh"
 #include "na3d_lora.cuh"
+#include "sm103_ptx.cuh"
 
 namespace na3d {
+
+__device__ unsigned int g_lora_timeout_flag = 0;
 
 namespace {
 
 __device__ __forceinline__ float f32(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }
 __device__ __forceinline__ uint16_t b16(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// The adapter of a row, -1 for none: the last request that starts at or
-// before the row, where it reaches that far.
-__device__ __forceinline__ int adapter_of(const LoraParams& p, int m) {
-    int lo = 0, hi = p.n_req;   // requests [0, lo) start at or before m
+// ------------------------------------------------------------------ requests
+
+// The first request that ends behind row m (n_req where none does).
+__device__ __forceinline__ int first_request(const LoraParams& p, int m) {
+    int lo = 0, hi = p.n_req;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (p.offsets[mid] <= m) lo = mid + 1;
-        else hi = mid;
+        if (p.offsets[mid + 1] > m) hi = mid;
+        else lo = mid + 1;
     }
-    if (lo == 0 || m >= p.offsets[lo]) return -1;
-    const int a = p.adapter[lo - 1];
-    return a >= 0 && a < p.n_ad ? a : -1;
+    return lo;
 }
 
-// t (from x and A) or u (from g and B) of every row: a warp per row.
-template <bool BWD>
-__global__ void __launch_bounds__(256) lora_down(const LoraParams p, float* t) {
-    const int lane = threadIdx.x & 31;
-    for (int m = blockIdx.x * 8 + (threadIdx.x >> 5); m < p.M; m += gridDim.x * 8) {
-        const int a = adapter_of(p, m);
-        for (int r = 0; r < p.R; ++r) {
-            float s = 0.f;
-            if (a >= 0 && !BWD) {
-                const uint16_t *x = p.x + int64_t(m) * p.C, *ar = p.a + (int64_t(a) * p.R + r) * p.C;
-                for (int c = lane; c < p.C; c += 32) s = fmaf(f32(x[c]), f32(ar[c]), s);
-            } else if (a >= 0) {
-                const uint16_t *g = p.dqkv + int64_t(m) * p.N, *br = p.b + int64_t(a) * p.N * p.R + r;
-                for (int n = lane; n < p.N; n += 32)
-                    s = fmaf(f32(g[n]) * (n < p.Nq ? p.q_scale : 1.f), f32(br[int64_t(n) * p.R]), s);
+// The requests with an adapter that meet rows [m0, m0 + 128), in order. Every
+// role of every kernel walks them alike.
+struct Walk {
+    int r, a, lo, hi;   // request, its adapter, its rows
+    __device__ __forceinline__ void start(const LoraParams& p, int m0) {
+        r = first_request(p, m0) - 1;
+        next(p, m0);
+    }
+    __device__ __forceinline__ void next(const LoraParams& p, int m0) {
+        for (++r; r < p.n_req; ++r) {
+            lo = p.offsets[r];
+            if (lo >= m0 + 128) break;
+            hi = p.offsets[r + 1];
+            a = p.adapter[r];
+            if (hi > lo && hi > m0 && a >= 0 && a < p.n_ad) return;
+        }
+        r = p.n_req;
+    }
+    __device__ __forceinline__ bool more(const LoraParams& p) const { return r < p.n_req; }
+};
+
+__host__ __device__ __forceinline__ int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+
+// ------------------------------------------------------------------ mma.sync pieces
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes, zeros where not `in`.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Chunk c (16 bytes) of row r of a tile with rows of `row` bytes, permuted so
+// that eight consecutive rows lie in different banks.
+template <int ROW>
+__device__ __forceinline__ uint32_t at(int r, int c) {
+    if (ROW == 32) return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
+    if (ROW == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    return r * ROW + ((c ^ (r & 7)) << 4);
+}
+
+// ------------------------------------------------------------------ t and u
+
+constexpr int kDownStages = 4;
+
+// t (from x and A) or u (from g = s dqkv and B) of the pairs of one 128-row
+// tile, RT rows a block: rows by 16 over the warps (RT 64), or, where there
+// are few tiles, 16 rows whose contraction the four warps share (RT 16).
+// Bound by the read of x (dqkv), which the large product then finds in L2
+// where it fits. RP: the rank, padded.
+template <int RP, bool BWD, int RT>
+__global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* out) {
+    constexpr int X_TILE = RT * 128, B_TILE = RP * 128, STAGE = X_TILE + B_TILE, NT = RP / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m_first = blockIdx.x * RT, m0 = m_first & ~127;
+    const int K = BWD ? p.N : p.C, blocks = (K + 63) / 64;
+    const uint16_t* const src = BWD ? p.dqkv : p.x;
+    const int g = lane >> 2, c2 = lane & 3;
+
+    Walk w;
+    for (w.start(p, m0); w.more(p); w.next(p, m0)) {
+        uint16_t* const to = out + ((int64_t(m0 >> 7) + w.r) * 128 + (m_first & 127)) * RP;
+        const int lo = max(w.lo, m_first), hi = min(min(w.hi, p.M), m_first + RT);   // rows of this block
+        if (lo >= hi) {
+            for (int i = threadIdx.x; i < RT * RP / 8; i += 128) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        auto load = [&](int kb) {
+            const uint32_t st = base + (kb % kDownStages) * STAGE;
+            const int k0 = kb * 64;
+            for (int i = threadIdx.x; i < RT * 8; i += 128) {
+                const int r = i >> 3, c = i & 7, m = m_first + r, k = k0 + c * 8;
+                const bool in = m >= lo && m < hi && k < K;
+                cp16(st + at<128>(r, c), src + (in ? int64_t(m) * K + k : 0), in);
             }
+            if (!BWD) {
+                for (int i = threadIdx.x; i < RP * 8; i += 128) {
+                    const int r = i >> 3, c = i & 7, k = k0 + c * 8;
+                    const bool in = r < p.R && k < K;
+                    cp16(st + X_TILE + at<128>(r, c), p.a + (in ? (int64_t(w.a) * p.R + r) * K + k : 0), in);
+                }
+            } else {
+                for (int i = threadIdx.x; i < 64 * (RP / 8); i += 128) {
+                    const int n = i / (RP / 8), c = i % (RP / 8);
+                    const bool in = k0 + n < K && c * 8 < p.R;
+                    cp16(st + X_TILE + at<RP * 2>(n, c), p.b + (in ? (int64_t(w.a) * K + k0 + n) * p.R + c * 8 : 0), in);
+                }
+            }
+        };
+        float acc[NT][4] = {};
+        auto step = [&](int kb, int kk, int row16) {   // 16 of the contraction
+            const uint32_t st = base + (kb % kDownStages) * STAGE, bt = st + X_TILE;
+            uint32_t a[4], f[4];
+            ldsm4(st + at<128>(row16 + (lane & 15), 2 * kk + (lane >> 4)), a);
 #pragma unroll
-            for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-            if (lane == 0) t[int64_t(m) * p.R + r] = a >= 0 ? s * p.scaling[a] : 0.f;
+            for (int j = 0; j < NT / 2; ++j) {
+                if (!BWD) {
+                    ldsm4(bt + at<128>(16 * j + (lane & 15), 2 * kk + (lane >> 4)), f);
+                    mma16816(acc[2 * j], a, f[0], f[2]);
+                    mma16816(acc[2 * j + 1], a, f[1], f[3]);
+                } else {
+                    ldsm4t(bt + at<RP * 2>(16 * kk + (lane & 15), 2 * j + (lane >> 4)), f);
+                    mma16816(acc[2 * j], a, f[0], f[1]);
+                    mma16816(acc[2 * j + 1], a, f[2], f[3]);
+                }
+            }
+        };
+        __syncthreads();   // the stages of the request before are read
+        for (int s = 0; s < kDownStages - 1; ++s) {
+            if (s < blocks) load(s);
+            cp_commit();
+        }
+        bool scaled = !BWD;   // the q block's sums have got their scale
+        for (int kb = 0; kb < blocks; ++kb) {
+            cp_wait<kDownStages - 2>();
+            __syncthreads();
+            if (kb + kDownStages - 1 < blocks) load(kb + kDownStages - 1);
+            cp_commit();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                if (RT == 16 && kk != warp) continue;
+                // the q block comes first: its sums are scaled once it is through (Nq is a
+                // multiple of 16)
+                if (!scaled && kb * 64 + kk * 16 >= p.Nq) {
+                    scaled = true;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[j][i] *= p.q_scale;
+                }
+                step(kb, kk, RT == 16 ? 0 : 16 * warp);
+            }
+        }
+        cp_wait<0>();
+        if (!scaled)   // a warp of RT 16 that met no column behind the q block
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] *= p.q_scale;
+        const float by = p.scaling[w.a];
+        if (RT == 16) {   // the warps' parts of the sum, in their order
+            float* part = reinterpret_cast<float*>(smem);
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[warp * 16 * RP + (g + 8 * (i >> 1)) * RP + 8 * j + 2 * c2 + (i & 1)] = acc[j][i];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 16 * RP; i += 128) {
+                const int m = m_first + i / RP;
+                const float s = (part[i] + part[16 * RP + i]) + (part[32 * RP + i] + part[48 * RP + i]);
+                to[i] = m >= lo && m < hi ? b16(s * by) : uint16_t(0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * warp + g + 8 * i, m = m_first + r;
+                const bool in = m >= lo && m < hi;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    *reinterpret_cast<uint32_t*>(to + r * RP + 8 * j + 2 * c2) =
+                        in ? pack_bf16x2(acc[j][2 * i] * by, acc[j][2 * i + 1] * by) : 0u;
+            }
         }
     }
 }
 
-// A 64 x 64 tile of sum_k a(i, k) b(j, k), 4 x 4 values a thread.
-template <class FA, class FB>
-__device__ __forceinline__ void tile_product(FA fa, FB fb, int i0, int j0, int I, int J, int K, float (&acc)[4][4]) {
-    __shared__ float sa[16][65], sb[16][65];
-    const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int e = threadIdx.x; e < 64 * 16; e += 256) {
-            const int i = e >> 4, k = e & 15;
-            sa[k][i] = i0 + i < I && k0 + k < K ? fa(i0 + i, k0 + k) : 0.f;
-            sb[k][i] = j0 + i < J && k0 + k < K ? fb(j0 + i, k0 + k) : 0.f;
+// ------------------------------------------------------------------ the large product
+
+constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
+constexpr int kThreads = 320;   // eight epilogue warps, a loading and an issuing one
+constexpr int A_TILE = kBM * kBK * 2, B_TILE = kBN * kBK * 2, STAGE = A_TILE + B_TILE;
+constexpr int OFF_BAR = kStages * STAGE;
+constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + 2, B_DRAIN = B_AEMPTY + 2,
+              NBAR = B_DRAIN + 1;
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int OFF_BIAS = (OFF_MISC + 16 + 15) & ~15;   // a tile's bias, fp32, for each epilogue warp its columns
+constexpr int SMEM_ALLOC = OFF_BIAS + 8 * 128 * 4 + 1024;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 500000000ull;
+
+struct Sync {
+    uint32_t bar0;
+    volatile uint32_t* abort_flag;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
+    // Wait for a barrier phase; false once this block has given up.
+    __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
+        if (mbar_try_wait(b, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(b, parity)) return true;
+            if ((it & 1023u) == 0u) {
+                if (*abort_flag) return false;
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    *abort_flag = 1u;
+                    atomicOr(&g_lora_timeout_flag, 1u);
+                    return false;
+                }
+            }
         }
+    }
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(bar) : "memory");
+}
+
+struct GemmParams {
+    int32_t K, cols;            // contraction and output columns
+    int32_t n_tiles, n_tiles_n, k_blocks;
+    int32_t out_v8;             // 1: output rows allow 32-byte stores
+    const uint16_t* t;          // pairs of t (u), [block][128][padded rank]
+    uint16_t* out;
+};
+
+// One output value from the inputs, for a row whose tile holds another
+// request's values that are not finite.
+template <bool BWD>
+__device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& q, int m, int col) {
+    float s = 0.f, sq = 0.f;
+    const int rp = padded_rank(p.R);
+    if (!BWD) {
+        for (int c = 0; c < p.C; ++c) s = fmaf(f32(p.x[int64_t(m) * p.C + c]), f32(p.w[int64_t(col) * p.C + c]), s);
+    } else {
+        for (int n = 0; n < p.N; ++n) {
+            if (n == p.Nq) { sq = s * p.q_scale; s = 0.f; }
+            s = fmaf(f32(p.dqkv[int64_t(m) * p.N + n]), f32(p.w[int64_t(n) * p.C + col]), s);
+        }
+        s += sq;
+    }
+    Walk w;
+    for (w.start(p, m & ~127); w.more(p); w.next(p, m & ~127)) {
+        if (m < w.lo || m >= w.hi) continue;
+        const uint16_t* t = q.t + ((int64_t(m >> 7) + w.r) * 128 + (m & 127)) * rp;
+        for (int r = 0; r < p.R; ++r)
+            s = fmaf(f32(t[r]), f32(BWD ? p.a[(int64_t(w.a) * p.R + r) * p.C + col] : p.b[(int64_t(w.a) * p.N + col) * p.R + r]), s);
+    }
+    return s;
+}
+
+// FWD: qkv = s_n (x W^T + bias + t B^T); BWD: dx = g W + u A with W and A read
+// along their columns. A persistent, warp-specialised tcgen05 product, one
+// block per SM, tiles of 128 x 256:
+//   warps 0..7  epilogue, two for each quarter of the rows (TMEM lanes), 128
+//               columns each;
+//   warp 8      TMA producer: 64-column blocks of the contraction into a ring
+//               of four stages, then each adapter's block;
+//   warp 9      MMA issuer, owns the tensor memory.
+// FWD alternates two 256-column accumulators between tiles. BWD gives the q
+// block's contraction one accumulator and the rest the other, since only the
+// first is scaled (HD^-0.5 is no power of two for every HD): the epilogue
+// takes the scaled q sums into registers while the rest accumulates, which
+// frees that accumulator for the next tile.
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads, 1)
+lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+          const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_l,
+          const __grid_constant__ LoraParams p, const __grid_constant__ GemmParams q) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rp = padded_rank(p.R), rb = rp < 64 ? rp : 64;   // an adapter's columns, and a block's
+
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(base_ptr + OFF_MISC);
+    Sync sy{base + OFF_BAR, misc + 1};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NBAR; ++i) mbar_init(sy.bar(i), (i >= B_AEMPTY && i < B_AEMPTY + 2) ? 256u : 1u);
+        misc[1] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+        tma_prefetch_desc(&tm_t);
+        tma_prefetch_desc(&tm_l);
+    }
+    if (warp == 9) {
+        tmem_alloc(base + OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+
+    if (warp == 8 && lane == 0) {
+        // ---------------------------------------------------------- producer
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < q.n_tiles; t += gridDim.x) {
+            const int i = t / q.n_tiles_n, m0 = i * kBM, n0 = (t % q.n_tiles_n) * kBN;
+            for (int kb = 0; kb < q.k_blocks; ++kb, ++it) {
+                const uint32_t st = it % kStages, to = base + st * STAGE;
+                if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
+                const uint32_t full = sy.bar(B_FULL + st);
+                mbar_arrive_expect_tx(full, STAGE);
+                tma_load_2d(to, &tm_a, full, kb * kBK, m0);
+                if (!BWD) {
+                    tma_load_2d(to + A_TILE, &tm_b, full, kb * kBK, n0);
+                } else {
+                    for (int c = 0; c < 4; ++c)
+                        tma_load_2d(to + A_TILE + c * (kBK * 128), &tm_b, full, n0 + c * 64, kb * kBK);
+                }
+            }
+            Walk w;
+            for (w.start(p, m0); ok && w.more(p); w.next(p, m0))
+                for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
+                    const uint32_t st = it % kStages, to = base + st * STAGE;
+                    if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
+                    const uint32_t full = sy.bar(B_FULL + st);
+                    mbar_arrive_expect_tx(full, (kBM + kBN) * rb * 2);
+                    tma_load_2d(to, &tm_t, full, r0, (i + w.r) * kBM);
+                    if (!BWD) {
+                        tma_load_2d(to + A_TILE, &tm_l, full, r0, w.a * p.N + n0);
+                    } else {
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_3d(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
+                    }
+                }
+        }
+        // every issued load lands before the CTA may exit
+        for (uint32_t s = 0; s < kStages; ++s) {
+            const uint32_t f = it / kStages + (s < it % kStages ? 1u : 0u);
+            if (f && !mbar_wait_bounded(sy.bar(B_FULL + s), (f - 1u) & 1u, kDrainLimitNs))
+                atomicOr(&g_lora_timeout_flag, 1u);
+        }
+    } else if (warp == 9 && lane == 0) {
+        // ---------------------------------------------------------- MMA issuer
+        const uint32_t idesc = make_idesc_bf16(kBM, kBN, 0, BWD ? 1 : 0);
+        const uint64_t ad0 = make_smem_desc(base, 16, 1024, kSwizzle128B);
+        // BWD: columns outermost in memory (MN-major), 64 to a region of kBK rows
+        const uint64_t bd0 = make_smem_desc(base + A_TILE, BWD ? kBK * 128 : 16, 1024, kSwizzle128B);
+        const uint32_t swz = rb == 64 ? kSwizzle128B : rb == 32 ? kSwizzle64B : kSwizzle32B;
+        const uint64_t td0 = make_smem_desc(base, 16, rb * 16, swz);
+        const uint64_t ld0 = BWD ? make_smem_desc(base + A_TILE, rb * 128, 1024, kSwizzle128B)
+                                 : make_smem_desc(base + A_TILE, 16, rb * 16, swz);
+        const uint32_t a_hi = uint32_t(ad0 >> 32), b_hi = uint32_t(bd0 >> 32);
+        const uint32_t t_hi = uint32_t(td0 >> 32), l_hi = uint32_t(ld0 >> 32);
+        constexpr uint32_t b_step = BWD ? (16 * 128) >> 4 : 2;   // 16 of the contraction further
+        uint32_t it = 0, lt = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < q.n_tiles; t += gridDim.x, ++lt) {
+            const int m0 = (t / q.n_tiles_n) * kBM;
+            // FWD: this tile's accumulator; BWD: 0, then 1 behind the q block
+            uint32_t buf = BWD ? 0u : lt & 1u;
+            if (!sy.wait(sy.bar(B_AEMPTY + buf), ((BWD ? lt : lt >> 1) & 1u) ^ 1u)) break;
+            tc_fence_after();
+            uint32_t d = tmem + buf * kBN;
+            bool fresh = true;
+            for (int kb = 0; kb < q.k_blocks; ++kb, ++it) {
+                const uint32_t st = it % kStages;
+                if (!sy.wait(sy.bar(B_FULL + st), (it / kStages) & 1u)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t a_lo = uint32_t(ad0) + ((st * STAGE) >> 4), b_lo = uint32_t(bd0) + ((st * STAGE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (BWD && buf == 0 && kb * kBK + kk * 16 >= p.Nq) {
+                        umma_commit(sy.bar(B_AFULL));
+                        buf = 1;
+                        if (!sy.wait(sy.bar(B_AEMPTY + 1), (lt & 1u) ^ 1u)) { ok = false; break; }
+                        tc_fence_after();
+                        d = tmem + kBN;
+                        fresh = true;
+                    }
+                    if (fresh) umma_ss_halves<0>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
+                    else umma_ss_halves<1>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
+                    fresh = false;
+                }
+                if (!ok) break;
+                umma_commit(sy.bar(B_EMPTY + st));
+            }
+            Walk w;
+            for (w.start(p, m0); ok && w.more(p); w.next(p, m0))
+                for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
+                    const uint32_t st = it % kStages;
+                    if (!sy.wait(sy.bar(B_FULL + st), (it / kStages) & 1u)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a_lo = uint32_t(td0) + ((st * STAGE) >> 4), b_lo = uint32_t(ld0) + ((st * STAGE) >> 4);
+                    for (int kk = 0; kk < rb / 16; ++kk)
+                        umma_ss_halves<1>(d, a_lo + kk * 2, t_hi, b_lo + kk * b_step, l_hi, idesc);
+                    umma_commit(sy.bar(B_EMPTY + st));
+                }
+            if (!ok) break;
+            umma_commit(sy.bar(B_AFULL + buf));
+        }
+        umma_commit(sy.bar(B_DRAIN));
+        if (!mbar_wait_bounded(sy.bar(B_DRAIN), 0, kDrainLimitNs)) atomicOr(&g_lora_timeout_flag, 1u);
+    } else if (warp < 8) {
+        // ---------------------------------------------------------- epilogue
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + half * 128;
+        float* bias_s = reinterpret_cast<float*>(base_ptr + OFF_BIAS) + warp * 128;   // this warp's copy
+        uint32_t lt = 0;
+        for (int t = blockIdx.x; t < q.n_tiles; t += gridDim.x, ++lt) {
+            const int m0 = (t / q.n_tiles_n) * kBM, n0 = (t % q.n_tiles_n) * kBN + half * 128;
+            const int row = m0 + quad * 32 + lane;
+            uint16_t* orow = q.out + int64_t(row) * q.cols;
+            if (!BWD) {
+                // the columns' bias (0 past N or without bias), one coalesced pass
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = n0 + 32 * i + lane;
+                    bias_s[32 * i + lane] = (p.bias && c < p.N) ? f32(p.bias[c]) : 0.f;
+                }
+                __syncwarp();
+            }
+            // does the tile hold rows of more than one request?
+            Walk w;
+            w.start(p, m0);
+            const bool shared = w.more(p) && (w.lo > m0 || w.hi < min(m0 + kBM, p.M));
+            float held[BWD ? 128 : 1];   // BWD: the scaled sums of the q block
+            if (BWD) {
+                if (!sy.wait(sy.bar(B_AFULL), lt & 1u)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_row + 32 * c, held + (BWD ? 32 * c : 0));
+                tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive(sy.bar(B_AEMPTY));
+            }
+            const uint32_t buf = BWD ? 1u : lt & 1u;
+            if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int c0 = n0 + 32 * c;
+                if (c0 >= q.cols) break;   // ragged last tile (uniform over the warp)
+                float acc[32];
+                tmem_ld32(t_row + buf * kBN + 32 * c, acc);
+                tmem_wait_ld();
+                if (BWD) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
+                }
+                if (shared) {
+                    float probe = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) probe = fmaf(acc[j], 0.f, probe);
+                    if (probe != 0.f && row < p.M)
+#pragma unroll 1
+                        for (int j = 0; j < 32 && c0 + j < q.cols; ++j) {
+                            const float x = lone_value<BWD>(p, q, row, c0 + j);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (k == j) acc[k] = x;
+                        }
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float v0 = acc[2 * j], v1 = acc[2 * j + 1];
+                    if (!BWD) {
+                        const float2 b = *reinterpret_cast<const float2*>(bias_s + 32 * c + 2 * j);
+                        // the q block (columns below NH * HD) carries the HD^-0.5 scale
+                        v0 = (v0 + b.x) * (c0 + 2 * j < p.Nq ? p.q_scale : 1.f);
+                        v1 = (v1 + b.y) * (c0 + 2 * j + 1 < p.Nq ? p.q_scale : 1.f);
+                    }
+                    pk[j] = pack_bf16x2(v0, v1);
+                }
+                if (row < p.M) {
+                    const int nval = min(32, q.cols - c0);   // a multiple of 8
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (q.out_v8 && 16 * i + 16 <= nval) {
+                            st_global_v8(orow + c0 + 16 * i, pk + 8 * i);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (16 * i + 8 * h < nval)
+                                    *reinterpret_cast<uint4*>(orow + c0 + 16 * i + 8 * h) =
+                                        make_uint4(pk[8 * i + 4 * h], pk[8 * i + 4 * h + 1], pk[8 * i + 4 * h + 2], pk[8 * i + 4 * h + 3]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();   // the bias copy is rewritten for the next tile
+            tc_fence_before();
+            mbar_arrive(sy.bar(B_AEMPTY + buf));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ adapters' gradients
+
+constexpr int kChunk = 64;   // rows of a request that lora_grad takes at a time
+
+// Where the rows of each adapter are: offsets made non-decreasing and kept in
+// 0 .. M (which good ones are already), the requests with an adapter in the
+// order of the adapters, and the chunks of each request and adapter.
+struct Plan {
+    int32_t *offsets;      // n_req + 1
+    int32_t *request;      // n_req, by adapter
+    int32_t *first;        // n_req + 1: first chunk of request[i]
+    int32_t *ad_first;     // n_ad + 1: first chunk of an adapter
+    int32_t *ad_req;       // n_ad + 1: first place of an adapter in request[]
+};
+
+__host__ __device__ __forceinline__ Plan plan_at(void* work, int n_req, int n_ad) {
+    Plan q;
+    q.offsets = static_cast<int32_t*>(work);
+    q.request = q.offsets + n_req + 1;
+    q.first = q.request + n_req;
+    q.ad_first = q.first + n_req + 1;
+    q.ad_req = q.ad_first + n_ad + 1;
+    return q;
+}
+
+// One block.
+__global__ void __launch_bounds__(256) lora_plan(const LoraParams p, const Plan q) {
+    __shared__ int top[256];
+    const int per = (p.n_req + 256) / 256, lo = min(int(threadIdx.x) * per, p.n_req + 1), hi = min(lo + per, p.n_req + 1);
+    int m = 0;
+    for (int i = lo; i < hi; ++i) m = max(m, min(p.offsets[i], p.M));
+    top[threadIdx.x] = m;
+    __syncthreads();
+    m = 0;
+    for (int i = 0; i < int(threadIdx.x); ++i) m = max(m, top[i]);
+    for (int i = lo; i < hi; ++i) {
+        m = max(m, min(p.offsets[i], p.M));
+        q.offsets[i] = m;
+    }
+    __syncthreads();
+    for (int a = threadIdx.x; a < p.n_ad; a += 256) {
+        int n = 0, c = 0;
+        for (int r = 0; r < p.n_req; ++r)
+            if (p.adapter[r] == a) {
+                ++n;
+                c += (q.offsets[r + 1] - q.offsets[r] + kChunk - 1) / kChunk;
+            }
+        q.ad_req[a + 1] = n;
+        q.ad_first[a + 1] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        q.ad_req[0] = q.ad_first[0] = 0;
+        for (int a = 0; a < p.n_ad; ++a) {
+            q.ad_req[a + 1] += q.ad_req[a];
+            q.ad_first[a + 1] += q.ad_first[a];
+        }
+        q.first[q.ad_req[p.n_ad]] = q.ad_first[p.n_ad];
+    }
+    __syncthreads();
+    for (int a = threadIdx.x; a < p.n_ad; a += 256) {
+        int n = q.ad_req[a], c = q.ad_first[a];
+        for (int r = 0; r < p.n_req; ++r)
+            if (p.adapter[r] == a) {
+                q.request[n] = r;
+                q.first[n++] = c;
+                c += (q.offsets[r + 1] - q.offsets[r] + kChunk - 1) / kChunk;
+            }
+    }
+}
+
+constexpr int kGradStages = 3;
+
+// Part of dA_a = u^T x (blocks of columns below C) and dB_a^T = t^T dqkv (the
+// others): one block takes 128 columns and an equal run of the chunks, which
+// are in the order of the adapters, and writes a sum for each adapter that it
+// meets. Part s + a: along the runs one of the two grows, so the parts are as
+// few as splits and adapters together. Bound by the read of x and dqkv.
+template <int RP>
+__global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan q, const uint16_t* tt, const uint16_t* uu,
+                                                 float* part, int splits) {
+    constexpr int X_TILE = kChunk * 256, U_TILE = kChunk * RP * 2, STAGE_G = X_TILE + U_TILE, MT = RP / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c2 = lane & 3;
+    const int c_blocks = (p.C + 127) / 128;
+    const bool is_b = int(blockIdx.x) >= c_blocks;
+    const int cols = is_b ? p.N : p.C, col0 = (is_b ? blockIdx.x - c_blocks : blockIdx.x) * 128;
+    const uint16_t* const x = is_b ? p.dqkv : p.x;
+    const uint16_t* const u = is_b ? tt : uu;
+    const int total = q.ad_first[p.n_ad], per = (total + splits - 1) / splits;
+    const int first = blockIdx.y * per, last = min(first + per, total);
+    if (first >= last) return;
+
+    // the place of the first chunk: the last request that starts at or before it
+    int j = 0;
+    {
+        int hi = q.ad_req[p.n_ad];
+        while (j + 1 < hi) {
+            const int mid = (j + hi) >> 1;
+            if (q.first[mid] <= first) j = mid;
+            else hi = mid;
+        }
+    }
+    const int n_sorted = q.ad_req[p.n_ad];
+    int jl = j;   // of the loads
+    auto load = [&](int c) {
+        const uint32_t st = base + (c - first) % kGradStages * STAGE_G;
+        while (jl + 1 < n_sorted && q.first[jl + 1] <= c) ++jl;
+        const int r = q.request[jl], m0 = q.offsets[r] + (c - q.first[jl]) * kChunk, end = q.offsets[r + 1];
+        for (int i = threadIdx.x; i < kChunk * 16; i += 256) {
+            const int k = i >> 4, cc = i & 15, m = m0 + k, col = col0 + cc * 8;
+            const bool in = m < end && col < cols;
+            cp16(st + (cc >> 3) * (kChunk * 128) + at<128>(k, cc & 7), x + (in ? int64_t(m) * cols + col : 0), in);
+        }
+        for (int i = threadIdx.x; i < kChunk * (RP / 8); i += 256) {
+            const int k = i / (RP / 8), cc = i % (RP / 8), m = m0 + k;
+            const bool in = m < end;
+            cp16(st + X_TILE + at<RP * 2>(k, cc), u + (in ? ((int64_t(m >> 7) + r) * 128 + (m & 127)) * RP + cc * 8 : 0), in);
+        }
+    };
+    float acc[MT][2][4] = {};
+    int a = p.adapter[q.request[j]];
+    auto flush = [&] {
+        float* to = part + (int64_t(blockIdx.y) + a) * RP * (p.C + p.N) + (is_b ? p.C : 0);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * t + g + 8 * (i >> 1), col = col0 + 16 * warp + 8 * n + 2 * c2 + (i & 1);
+                    if (col < cols) to[int64_t(row) * (p.C + p.N) + col] = acc[t][n][i];
+                    acc[t][n][i] = 0.f;
+                }
+    };
+    for (int s = 0; s < kGradStages - 1; ++s) {
+        if (first + s < last) load(first + s);
+        cp_commit();
+    }
+    for (int c = first; c < last; ++c) {
+        cp_wait<kGradStages - 2>();
         __syncthreads();
-        for (int k = 0; k < 16; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ti * 4 + i], sb[k][tj * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-}
-
-__global__ void __launch_bounds__(256) lora_fwd_tile(const LoraParams p, const float* t) {
-    float acc[4][4] = {};
-    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    tile_product([&](int m, int c) { return f32(p.x[int64_t(m) * p.C + c]); },
-                 [&](int n, int c) { return f32(p.w[int64_t(n) * p.C + c]); }, i0, j0, p.M, p.N, p.C, acc);
-    for (int i = 0; i < 4; ++i) {
-        const int m = i0 + (threadIdx.x >> 4) * 4 + i;
-        if (m >= p.M) break;
-        const int a = adapter_of(p, m);
-        for (int j = 0; j < 4; ++j) {
-            const int n = j0 + (threadIdx.x & 15) * 4 + j;
-            if (n >= p.N) break;
-            float s = acc[i][j] + (p.bias ? f32(p.bias[n]) : 0.f);
-            for (int r = 0; a >= 0 && r < p.R; ++r)
-                s = fmaf(t[int64_t(m) * p.R + r], f32(p.b[(int64_t(a) * p.N + n) * p.R + r]), s);
-            p.qkv[int64_t(m) * p.N + n] = b16(s * (n < p.Nq ? p.q_scale : 1.f));
+        if (c + kGradStages - 1 < last) load(c + kGradStages - 1);
+        cp_commit();
+        bool moved = false;
+        while (j + 1 < n_sorted && q.first[j + 1] <= c) { ++j; moved = true; }
+        if (moved && p.adapter[q.request[j]] != a) {
+            flush();
+            a = p.adapter[q.request[j]];
+        }
+        const uint32_t st = base + (c - first) % kGradStages * STAGE_G;
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk) {
+            uint32_t f[4], e[4];
+            const int k = 16 * kk + (lane & 15), cc = 2 * warp + (lane >> 4);
+            ldsm4t(st + (cc >> 3) * (kChunk * 128) + at<128>(k, cc & 7), f);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                // rows of u are the contraction: transposed, 16 of its columns are the rows of A
+                ldsm4t(st + X_TILE + at<RP * 2>(16 * kk + (lane & 7) + 8 * (lane >> 4), 2 * t + ((lane >> 3) & 1)), e);
+                mma16816(acc[t][0], e, f[0], f[1]);
+                mma16816(acc[t][1], e, f[2], f[3]);
+            }
         }
     }
+    cp_wait<0>();
+    flush();
 }
 
-__global__ void __launch_bounds__(256) lora_dx_tile(const LoraParams p, const float* u) {
-    float acc[4][4] = {};
-    const int i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    tile_product([&](int m, int n) { return f32(p.dqkv[int64_t(m) * p.N + n]) * (n < p.Nq ? p.q_scale : 1.f); },
-                 [&](int c, int n) { return f32(p.w[int64_t(n) * p.C + c]); }, i0, j0, p.M, p.C, p.N, acc);
-    for (int i = 0; i < 4; ++i) {
-        const int m = i0 + (threadIdx.x >> 4) * 4 + i;
-        if (m >= p.M) break;
-        const int a = adapter_of(p, m);
-        for (int j = 0; j < 4; ++j) {
-            const int c = j0 + (threadIdx.x & 15) * 4 + j;
-            if (c >= p.C) break;
-            float s = acc[i][j];
-            for (int r = 0; a >= 0 && r < p.R; ++r)
-                s = fmaf(u[int64_t(m) * p.R + r], f32(p.a[(int64_t(a) * p.R + r) * p.C + c]), s);
-            p.dx[int64_t(m) * p.C + c] = b16(s);
-        }
-    }
-}
-
-// dA[a][r][c] and dB[a][n][r]: a thread per value, over the rows of every
-// request with the adapter, in their order.
-template <bool B>
-__global__ void __launch_bounds__(256) lora_dab(const LoraParams p, const float* tu) {
-    const int64_t per = int64_t(p.R) * (B ? p.N : p.C);
+// The parts of each adapter, in their order, to dA (n_ad, R, C) and dB
+// (n_ad, N, R), the q block's rows of dB scaled. A thread sums eight ranks of
+// one column.
+__global__ void __launch_bounds__(256) lora_grad_sum(const LoraParams p, const Plan q, const float* part, int splits, int rp) {
+    const int cols = p.C + p.N, n8 = p.R / 8;
     const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= per * p.n_ad) return;
-    const int a = int(e / per);
-    const int64_t f = e % per;
-    const int r = B ? int(f % p.R) : int(f / p.C), c = B ? int(f / p.R) : int(f % p.C);
-    float s = 0.f;
-    for (int q = 0; q < p.n_req; ++q) {
-        if (p.adapter[q] != a) continue;
-        const int m1 = min(p.M, p.offsets[q + 1]);
-        for (int m = max(0, p.offsets[q]); m < m1; ++m)
-            s = fmaf(tu[int64_t(m) * p.R + r], f32(B ? p.dqkv[int64_t(m) * p.N + c] : p.x[int64_t(m) * p.C + c]), s);
+    if (e >= int64_t(p.n_ad) * n8 * cols) return;
+    const int col = int(e % cols), r0 = int(e / cols % n8) * 8, a = int(e / cols / n8);
+    const int total = q.ad_first[p.n_ad], per = (total + splits - 1) / splits;
+    const int c0 = q.ad_first[a], c1 = q.ad_first[a + 1];
+    float s[8] = {};
+    if (c0 < c1)
+        for (int k = c0 / per; k <= (c1 - 1) / per; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += part[((int64_t(k) + a) * rp + r0 + i) * cols + col];
+    if (col < p.C) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.da[(int64_t(a) * p.R + r0 + i) * p.C + col] = b16(s[i]);
+    } else {
+        const float by = col - p.C < p.Nq ? p.q_scale : 1.f;
+        uint4 v;
+        v.x = pack_bf16x2(s[0] * by, s[1] * by);
+        v.y = pack_bf16x2(s[2] * by, s[3] * by);
+        v.z = pack_bf16x2(s[4] * by, s[5] * by);
+        v.w = pack_bf16x2(s[6] * by, s[7] * by);
+        *reinterpret_cast<uint4*>(p.db + (int64_t(a) * p.N + col - p.C) * p.R + r0) = v;
     }
-    if (B && c < p.Nq) s *= p.q_scale;
-    (B ? p.db : p.da)[e] = b16(s);
 }
 
-unsigned ceil_div(int64_t a, int64_t b) { return unsigned((a + b - 1) / b); }
+// ------------------------------------------------------------------ launch
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Runs of chunks that lora_grad's blocks share a column block's rows by: about
+// three blocks an SM.
+int grad_splits(int64_t M, int64_t C, int64_t N) {
+    const int64_t s = ceil_div(3 * 152, ceil_div(C, 128) + ceil_div(N, 128)), most = ceil_div(M, kChunk);
+    return int(s < 1 ? 1 : s > most ? most : s);
+}
+
+struct Work {
+    int64_t t, u, plan, part, bytes;
+};
+
+Work lay_out(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req, int64_t n_ad, bool backward) {
+    Work w;
+    const int64_t rp = padded_rank(int(R)), pairs = (ceil_div(M, 128) + n_req) * 128 * rp * 2;
+    w.t = 0;
+    w.u = w.t + align256(pairs);
+    w.plan = w.u + (backward ? align256(pairs) : 0);
+    w.part = w.plan + (backward ? align256((3 * n_req + 2 * n_ad + 4) * 4) : 0);
+    w.bytes = w.part + (backward ? (grad_splits(M, C, N) + n_ad) * rp * (C + N) * 4 : 0);
+    return w;
+}
+
+// A tensor map of up to three dimensions of bf16, strides in elements.
+bool map_of(CUtensorMap* m, const void* ptr, int dims, const int64_t* size, const int64_t* stride, int box0, int box1) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[3], s[2];
+    const cuuint32_t box[3] = {cuuint32_t(box0), cuuint32_t(box1), 1}, one[3] = {1, 1, 1};
+    for (int i = 0; i < dims; ++i) d[i] = cuuint64_t(size[i]);
+    for (int i = 0; i + 1 < dims; ++i) s[i] = cuuint64_t(stride[i] * 2);
+    const CUtensorMapSwizzle swz = box0 == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                   : box0 == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_32B;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(ptr), d, s, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int RP, bool BWD, int RT>
+cudaError_t down_t(const LoraParams& p, uint16_t* out, cudaStream_t stream) {
+    constexpr int smem = kDownStages * (RT * 128 + RP * 128);
+    static_assert(RT != 16 || 4 * 16 * RP * 4 <= smem, "the warps' parts fit the stages");
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(lora_down<RP, BWD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    lora_down<RP, BWD, RT><<<unsigned(ceil_div(p.M, 128) * 128 / RT), 128, smem, stream>>>(p, out);
+    return cudaGetLastError();
+}
+
+template <bool BWD>
+cudaError_t down(const LoraParams& p, uint16_t* out, int sms, cudaStream_t stream) {
+    // 64 rows a block leave SMs idle below 64 * sms rows
+    const bool small = p.M < 64 * sms;
+    switch (padded_rank(p.R)) {
+        case 16: return small ? down_t<16, BWD, 16>(p, out, stream) : down_t<16, BWD, 64>(p, out, stream);
+        case 32: return small ? down_t<32, BWD, 16>(p, out, stream) : down_t<32, BWD, 64>(p, out, stream);
+        case 64: return small ? down_t<64, BWD, 16>(p, out, stream) : down_t<64, BWD, 64>(p, out, stream);
+        default: return small ? down_t<128, BWD, 16>(p, out, stream) : down_t<128, BWD, 64>(p, out, stream);
+    }
+}
+
+template <bool BWD>
+cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
+    GemmParams q{};
+    q.K = BWD ? p.N : p.C;
+    q.cols = BWD ? p.C : p.N;
+    q.n_tiles_n = int32_t(ceil_div(q.cols, kBN));
+    const int64_t tiles = ceil_div(p.M, kBM) * q.n_tiles_n;
+    if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    q.n_tiles = int32_t(tiles);
+    q.k_blocks = int32_t(ceil_div(q.K, kBK));
+    q.t = t;
+    q.out = BWD ? p.dx : p.qkv;
+    q.out_v8 = reinterpret_cast<uintptr_t>(q.out) % 32 == 0 && q.cols % 16 == 0;
+    const int rp = padded_rank(p.R), rb = rp < 64 ? rp : 64;
+    CUtensorMap ta, tb, tt, tl;
+    const int64_t blocks = (ceil_div(p.M, 128) + p.n_req) * 128;
+    const int64_t sa[2] = {q.K, p.M}, ka[1] = {q.K}, st[2] = {rp, blocks}, kt[1] = {rp};
+    const int64_t sw[2] = {p.C, p.N}, kw[1] = {p.C};
+    const int64_t sb[2] = {p.R, int64_t(p.n_ad) * p.N}, kb[1] = {p.R};
+    const int64_t sl[3] = {p.C, p.R, p.n_ad}, kl[2] = {p.C, int64_t(p.R) * p.C};
+    bool ok = map_of(&ta, BWD ? p.dqkv : p.x, 2, sa, ka, 64, kBM) && map_of(&tt, t, 2, st, kt, rb, kBM);
+    if (BWD) ok = ok && map_of(&tb, p.w, 2, sw, kw, 64, kBK) && map_of(&tl, p.a, 3, sl, kl, 64, rb);
+    else ok = ok && map_of(&tb, p.w, 2, sw, kw, 64, kBN) && map_of(&tl, p.b, 2, sb, kb, rb, kBN);
+    if (!ok) return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(lora_gemm<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
+    if (e != cudaSuccess) return e;
+    lora_gemm<BWD><<<int(tiles < sms ? tiles : sms), kThreads, SMEM_ALLOC, stream>>>(ta, tb, tt, tl, p, q);
+    return cudaGetLastError();
+}
+
+template <int RP>
+cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const uint16_t* u, float* part, cudaStream_t stream) {
+    constexpr int smem = kGradStages * (kChunk * 256 + kChunk * RP * 2);
+    cudaError_t e = cudaFuncSetAttribute(lora_grad<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int splits = grad_splits(p.M, p.C, p.N);
+    lora_grad<RP><<<dim3(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits)), 256, smem, stream>>>(
+        p, q, t, u, part, splits);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t n = int64_t(p.n_ad) * (p.R / 8) * (int64_t(p.C) + p.N);
+    lora_grad_sum<<<unsigned(ceil_div(n, 256)), 256, 0, stream>>>(p, q, part, splits, RP);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
-int64_t lora_workspace(int64_t M, int64_t, int64_t, int64_t R, int64_t, int64_t, bool backward) {
-    return M * R * 4 * (backward ? 2 : 1);
+int64_t lora_workspace(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req, int64_t n_ad, bool backward) {
+    return lay_out(M, C, N, R, n_req, n_ad, backward).bytes;
 }
 
 cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
-    float* t = static_cast<float*>(p.work);
-    lora_down<false><<<sms * 8, 256, 0, stream>>>(p, t);
-    lora_fwd_tile<<<dim3(ceil_div(p.N, 64), ceil_div(p.M, 64)), 256, 0, stream>>>(p, t);
-    return cudaGetLastError();
+    uint16_t* t = static_cast<uint16_t*>(p.work);
+    const cudaError_t e = down<false>(p, t, sms, stream);
+    return e != cudaSuccess ? e : gemm<false>(p, t, sms, stream);
 }
 
-cudaError_t launch_lora_bwd(const LoraParams& p, int sms, cudaStream_t stream) {
-    float *t = static_cast<float*>(p.work), *u = t + int64_t(p.M) * p.R;
-    lora_down<false><<<sms * 8, 256, 0, stream>>>(p, t);
-    lora_down<true><<<sms * 8, 256, 0, stream>>>(p, u);
-    if (p.dx) lora_dx_tile<<<dim3(ceil_div(p.C, 64), ceil_div(p.M, 64)), 256, 0, stream>>>(p, u);
-    lora_dab<false><<<ceil_div(int64_t(p.n_ad) * p.R * p.C, 256), 256, 0, stream>>>(p, u);
-    lora_dab<true><<<ceil_div(int64_t(p.n_ad) * p.R * p.N, 256), 256, 0, stream>>>(p, t);
-    return cudaGetLastError();
+cudaError_t launch_lora_bwd(const LoraParams& p0, int sms, cudaStream_t stream) {
+    const Work w = lay_out(p0.M, p0.C, p0.N, p0.R, p0.n_req, p0.n_ad, true);
+    uint8_t* work = static_cast<uint8_t*>(p0.work);
+    uint16_t *t = reinterpret_cast<uint16_t*>(work + w.t), *u = reinterpret_cast<uint16_t*>(work + w.u);
+    const Plan q = plan_at(work + w.plan, p0.n_req, p0.n_ad);
+    lora_plan<<<1, 256, 0, stream>>>(p0, q);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    LoraParams p = p0;   // every pass walks the plan's offsets
+    p.offsets = q.offsets;
+    if ((e = down<false>(p, t, sms, stream)) != cudaSuccess) return e;
+    if ((e = down<true>(p, u, sms, stream)) != cudaSuccess) return e;
+    if (p.dx && (e = gemm<true>(p, u, sms, stream)) != cudaSuccess) return e;
+    float* part = reinterpret_cast<float*>(work + w.part);
+    switch (padded_rank(p.R)) {
+        case 16: return grad<16>(p, q, t, u, part, stream);
+        case 32: return grad<32>(p, q, t, u, part, stream);
+        case 64: return grad<64>(p, q, t, u, part, stream);
+        default: return grad<128>(p, q, t, u, part, stream);
+    }
+}
+
+// The flag is taken as for the attention kernel: one atomic exchange per
+// status request, its old value left in a slot of that request's own.
+constexpr unsigned int kStatusSlots = 256;
+__device__ unsigned int g_lora_status_slots[kStatusSlots];
+
+__global__ void take_lora_flag(unsigned int slot) { g_lora_status_slots[slot] = atomicExch(&g_lora_timeout_flag, 0u); }
+
+cudaError_t take_lora_error(cudaStream_t stream, unsigned int* flag) {
+    static std::atomic<unsigned int> next{0};
+    const unsigned int slot = next.fetch_add(1u) % kStatusSlots;
+    take_lora_flag<<<1, 1, 0, stream>>>(slot);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyFromSymbolAsync(flag, g_lora_status_slots, sizeof(unsigned int), slot * sizeof(unsigned int),
+                                  cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(stream);
 }
 
 }  // namespace na3d

@@ -27,4 +27,8 @@ int64_t lora_workspace(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req
 cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_lora_bwd(const LoraParams& p, int sms, cudaStream_t stream);
 
+// After the work already on `stream`, take (read and clear in one atomic
+// step) these kernels' timeout flag, then synchronize `stream`.
+cudaError_t take_lora_error(cudaStream_t stream, unsigned int* flag);
+
 }  // namespace na3d

@@ -182,7 +182,8 @@ int check_lora_sizes(int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R, in
     if (R > 128) return NA3D_ERR_UNSUPPORTED;
     const int64_t lim = int64_t(1) << 31;
     int64_t b;
-    if (!mul_ok(3 * NH, HD, N) || *N >= lim || M >= lim - 128 || C >= lim || n_req >= lim - 1 || n_ad >= lim / 128 ||
+    if (!mul_ok(3 * NH, HD, N) || *N >= lim || M >= lim - 256 || C >= lim ||
+        n_req >= lim / 128 - (M + 127) / 128 || n_ad >= lim / *N || n_ad >= lim / 128 ||
         !mul_ok(M, *N, &b) || !mul_ok(b, 2, &b) || !mul_ok(M, C, &b) || !mul_ok(b, 2, &b) ||
         !mul_ok(n_ad * R, *N, &b) || !mul_ok(b, 2, &b) || !mul_ok(n_ad * R, C, &b) || !mul_ok(b, 2, &b))
         return NA3D_ERR_OVERFLOW;
