@@ -101,6 +101,11 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
     return r * ROW + ((c ^ (r & 7)) << 4);
 }
 
+// A kernel lets the next one of its stream start, and waits for the one before
+// it to be through (nothing to wait for where it was launched plainly).
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ t and u
 
 constexpr int kDownStages = 4;
@@ -120,6 +125,7 @@ __global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* o
     const int K = BWD ? p.N : p.C, blocks = (K + 63) / 64;
     const uint16_t* const src = BWD ? p.dqkv : p.x;
     const int g = lane >> 2, c2 = lane & 3;
+    dependents_may_start();
 
     Walk w;
     for (w.start(p, m0); w.more(p); w.next(p, m0)) {
@@ -374,7 +380,9 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 }
             }
             Walk w;
-            for (w.start(p, m0); ok && w.more(p); w.next(p, m0))
+            w.start(p, m0);
+            if (w.more(p)) wait_for_primary();   // t
+            for (; ok && w.more(p); w.next(p, m0))
                 for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
                     const uint32_t st = it % kStages, to = base + st * STAGE;
                     if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
@@ -389,6 +397,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                     }
                 }
         }
+        wait_for_primary();
         // every issued load lands before the CTA may exit
         for (uint32_t s = 0; s < kStages; ++s) {
             const uint32_t f = it / kStages + (s < it % kStages ? 1u : 0u);
@@ -458,6 +467,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         if (!mbar_wait_bounded(sy.bar(B_DRAIN), 0, kDrainLimitNs)) atomicOr(&g_lora_timeout_flag, 1u);
     } else if (warp < 8) {
         // ---------------------------------------------------------- epilogue
+        wait_for_primary();
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + half * 128;
         float* bias_s = reinterpret_cast<float*>(base_ptr + OFF_BIAS) + warp * 128;   // this warp's copy
@@ -555,6 +565,104 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+
+constexpr int kSmallRows = 32;   // up to here the product streams W past the rows
+
+// t of up to kSmallRows rows, [row][R]: a warp for each value.
+__global__ void __launch_bounds__(256) lora_down_few(const LoraParams p, uint16_t* t) {
+    dependents_may_start();
+    const int m = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    Walk w;
+    for (w.start(p, 0); w.more(p) && w.hi <= m; w.next(p, 0)) {}
+    if (!w.more(p) || w.lo > m) return;   // nothing reads this row's
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + int64_t(m) * p.C);
+    const uint4* a = reinterpret_cast<const uint4*>(p.a + (int64_t(w.a) * p.R + r) * p.C);
+    float s = 0.f;
+#pragma unroll 4
+    for (int i = lane; i < p.C / 8; i += 32) {
+        const uint4 u = x[i], v = a[i];
+        const uint32_t e[4] = {u.x, u.y, u.z, u.w}, f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s = fmaf(__uint_as_float(e[k] << 16), __uint_as_float(f[k] << 16), s);
+            s = fmaf(__uint_as_float(e[k] & 0xffff0000u), __uint_as_float(f[k] & 0xffff0000u), s);
+        }
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0) t[m * p.R + r] = b16(s * p.scaling[w.a]);
+}
+
+// qkv of up to 8 * MT rows: a block takes 16 rows of W, read once from memory
+// straight into fragments (a thread's 16 bytes are 8 consecutive channels, the
+// same for W and x, so the contraction is permuted alike on both sides), its
+// warps an eighth of the channels each. Bound by the read of W; t is waited for
+// behind it only.
+template <int MT>
+__global__ void __launch_bounds__(256) lora_fwd_few(const LoraParams p, const uint16_t* t) {
+    constexpr int U = MT <= 2 ? 4 : 2;   // blocks of 32 channels in flight
+    __shared__ float part[8][16][8 * MT + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c2 = lane & 3;
+    const int n0 = blockIdx.x * 16;   // N is a multiple of 16
+    const uint16_t* const w0 = p.w + int64_t(n0 + g) * p.C;
+    const uint16_t* const w1 = w0 + int64_t(8) * p.C;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float acc[MT][4] = {};
+    const int blocks = (p.C + 31) / 32;
+    for (int b = warp; b < blocks; b += 8 * U) {
+        uint4 a0[U], a1[U], x[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = (b + 8 * u) * 32 + 8 * c2;
+            const bool in = c < p.C;
+            a0[u] = in ? *reinterpret_cast<const uint4*>(w0 + c) : zero;
+            a1[u] = in ? *reinterpret_cast<const uint4*>(w1 + c) : zero;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                x[u][i] = in && 8 * i + g < p.M ? *reinterpret_cast<const uint4*>(p.x + int64_t(8 * i + g) * p.C + c) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t lo[4] = {a0[u].x, a1[u].x, a0[u].y, a1[u].y}, hi[4] = {a0[u].z, a1[u].z, a0[u].w, a1[u].w};
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                mma16816(acc[i], lo, x[u][i].x, x[u][i].y);
+                mma16816(acc[i], hi, x[u][i].z, x[u][i].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) part[warp][g + 8 * (k >> 1)][8 * i + 2 * c2 + (k & 1)] = acc[i][k];
+    wait_for_primary();
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * p.M; e += 256) {
+        const int n = e & 15, m = e >> 4, col = n0 + n;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += part[i][n][m];
+        if (p.bias) s += f32(p.bias[col]);
+        Walk w;
+        for (w.start(p, 0); w.more(p) && w.hi <= m; w.next(p, 0)) {}
+        if (w.more(p) && w.lo <= m) {
+            const uint4* b = reinterpret_cast<const uint4*>(p.b + (int64_t(w.a) * p.N + col) * p.R);
+            const uint4* tm = reinterpret_cast<const uint4*>(t + m * p.R);
+            for (int i = 0; i < p.R / 8; ++i) {
+                const uint4 u = b[i], v = tm[i];
+                const uint32_t f[4] = {u.x, u.y, u.z, u.w}, h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s = fmaf(__uint_as_float(h[k] << 16), __uint_as_float(f[k] << 16), s);
+                    s = fmaf(__uint_as_float(h[k] & 0xffff0000u), __uint_as_float(f[k] & 0xffff0000u), s);
+                }
+            }
+        }
+        p.qkv[int64_t(m) * p.N + col] = b16(s * (col < p.Nq ? p.q_scale : 1.f));
     }
 }
 
@@ -800,6 +908,23 @@ bool map_of(CUtensorMap* m, const void* ptr, int dims, const int64_t* size, cons
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may start while the kernel before it, which lets it, still
+// runs; it waits for that kernel itself where it reads its results.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, int smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 template <int RP, bool BWD, int RT>
 cudaError_t down_t(const LoraParams& p, uint16_t* out, cudaStream_t stream) {
     constexpr int smem = kDownStages * (RT * 128 + RP * 128);
@@ -850,8 +975,8 @@ cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t s
     if (!ok) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(lora_gemm<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    lora_gemm<BWD><<<int(tiles < sms ? tiles : sms), kThreads, SMEM_ALLOC, stream>>>(ta, tb, tt, tl, p, q);
-    return cudaGetLastError();
+    return launch_dependent(lora_gemm<BWD>, unsigned(tiles < sms ? tiles : sms), kThreads, SMEM_ALLOC, stream, ta, tb, tt, tl,
+                            p, q);
 }
 
 template <int RP>
@@ -876,6 +1001,15 @@ int64_t lora_workspace(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req
 
 cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
     uint16_t* t = static_cast<uint16_t*>(p.work);
+    if (p.M <= kSmallRows) {
+        lora_down_few<<<dim3(unsigned(p.M), unsigned(p.R / 8)), 256, 0, stream>>>(p, t);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const unsigned grid = unsigned(p.N / 16);
+        if (p.M <= 8) return launch_dependent(lora_fwd_few<1>, grid, 256, 0, stream, p, t);
+        if (p.M <= 16) return launch_dependent(lora_fwd_few<2>, grid, 256, 0, stream, p, t);
+        return launch_dependent(lora_fwd_few<4>, grid, 256, 0, stream, p, t);
+    }
     const cudaError_t e = down<false>(p, t, sms, stream);
     return e != cudaSuccess ? e : gemm<false>(p, t, sms, stream);
 }
