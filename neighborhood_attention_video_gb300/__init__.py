@@ -177,6 +177,9 @@ def _token_stride(name, t) -> int:
     """Elements between consecutive (b,t,h,w) positions of a (B,T,H,W,NH,HD)
     view whose heads are packed (head stride HD, unit element stride)."""
     st, sh = t.stride(), t.shape
+    if (st[5] == 1 and st[4] == sh[5] and st[2] == sh[3] * st[3] and st[1] == sh[2] * st[2]
+            and st[0] == sh[1] * st[1]):
+        return st[3]
     if st[5] != 1 or (sh[4] > 1 and st[4] != sh[5]):
         raise ValueError(f"{name}: heads must be packed (strides [..., HD, 1])")
     for i in (2, 1, 0):
@@ -264,7 +267,7 @@ def na3d_qkv_proj(x, w, bias, qkv, num_heads, head_dim, stream=None) -> None:
 def qkv_views(qkv):
     """q, k, v views (B, T, H, W, NH, HD) of a (B, T, H, W, 3, NH, HD)
     projection output, for ``na3d_fwd_strided``."""
-    return qkv[..., 0, :, :], qkv[..., 1, :, :], qkv[..., 2, :, :]
+    return qkv.select(-3, 0), qkv.select(-3, 1), qkv.select(-3, 2)
 
 
 def _check_on_device(tensors):
@@ -283,23 +286,23 @@ def _check_on_device(tensors):
             raise ValueError(f"{name} must be contiguous")
 
 
-def _empty(stream, shape, dtype):
-    """A new tensor on the current device, allocated on the stream that the
+def _empty(stream, like, shape, dtype):
+    """A new tensor on the device of `like`, allocated on the stream that the
     call uses, so that the allocator may reuse its memory only behind the call."""
     torch = _torch_module()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device="cuda")
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _workspace(work, need, stream):
+def _workspace(work, need, like, stream):
     """`work` where it is given and large enough, else a new workspace."""
     torch = _torch_module()
     if work is None:
-        return _empty(stream, (need,), torch.uint8)
+        return _empty(stream, like, (need,), torch.uint8)
     dev = torch.cuda.current_device() if _cuda_ok else -2
     if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
         raise TypeError("work must be a contiguous tensor on the current CUDA device")
@@ -358,8 +361,8 @@ def na3d_scored_attention(q, k, v, kernel_size, softcap=0.0, slopes=None, doc=No
     ``return_lse`` is true (what ``na3d_scored_bwd`` needs)."""
     torch = _torch_module()
     _check_bf16_on_device((("q", q),))
-    out = _empty(stream, q.shape, torch.bfloat16)
-    lse = _empty(stream, q.shape[:-1], torch.float32) if return_lse else None
+    out = _empty(stream, q, q.shape, torch.bfloat16)
+    lse = _empty(stream, q, q.shape[:-1], torch.float32) if return_lse else None
     na3d_scored_fwd(q, k, v, out, kernel_size, lse, softcap, slopes, doc, prefix, stream)
     return (out, lse) if return_lse else out
 
@@ -393,7 +396,7 @@ def na3d_scored_bwd(q, k, v, out, lse, dout, dq, dk, dv, kernel_size, softcap=0.
     options = _scored_options(q, softcap, slopes, doc, prefix)
     strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))]
     KT, KH, KW = (int(x) for x in kernel_size)
-    work = _workspace(work, na3d_scored_bwd_workspace(*shape[:5]), stream)
+    work = _workspace(work, lib.na3d_scored_bwd_workspace(*shape[:5]), q, stream)
     rc = lib.na3d_scored_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(),
                              *shape, KT, KH, KW, *strides, *options, _stream_handle(stream))
@@ -448,7 +451,7 @@ def na3d_lora_qkv_proj(x, w, bias, lora_a, lora_b, scaling, offsets, adapter, qk
         raise ValueError("qkv must be contiguous")
     if qkv.numel() != sizes[0] * w.shape[0]:
         raise ValueError("qkv must hold 3*NH*HD values per token of x")
-    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 0)), stream)
+    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 0)), x, stream)
     rc = lib.na3d_lora_qkv_proj(x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
                                 lora_a.data_ptr(), lora_b.data_ptr(), scaling.data_ptr(), offsets.data_ptr(),
                                 adapter.data_ptr(), qkv.data_ptr(), work.data_ptr(), *sizes, _stream_handle(stream))
@@ -474,7 +477,7 @@ def na3d_lora_qkv_proj_bwd(dqkv, x, w, lora_a, lora_b, scaling, offsets, adapter
     if dx is not None:
         outputs.append(("dx", dx, bf16, x.shape))
     _check_on_device(outputs)
-    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 1)), stream)
+    work = _workspace(work, max(0, lib.na3d_lora_workspace(*sizes, 1)), x, stream)
     rc = lib.na3d_lora_qkv_proj_bwd(dqkv.data_ptr(), x.data_ptr(), w.data_ptr(), lora_a.data_ptr(),
                                     lora_b.data_ptr(), scaling.data_ptr(), offsets.data_ptr(), adapter.data_ptr(),
                                     None if dx is None else dx.data_ptr(), dlora_a.data_ptr(), dlora_b.data_ptr(),

@@ -116,7 +116,7 @@ constexpr int kDownStages = 4;
 // Bound by the read of x (dqkv), which the large product then finds in L2
 // where it fits. RP: the rank, padded.
 template <int RP, bool BWD, int RT>
-__global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* out) {
+__device__ __forceinline__ void down_rows(const LoraParams& p, uint16_t* out) {
     constexpr int X_TILE = RT * 128, B_TILE = RP * 128, STAGE = X_TILE + B_TILE, NT = RP / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* o
     const int K = BWD ? p.N : p.C, blocks = (K + 63) / 64;
     const uint16_t* const src = BWD ? p.dqkv : p.x;
     const int g = lane >> 2, c2 = lane & 3;
-    dependents_may_start();
 
     Walk w;
     for (w.start(p, m0); w.more(p); w.next(p, m0)) {
@@ -234,6 +233,21 @@ __global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* o
             }
         }
     }
+}
+
+template <int RP, int RT>
+__global__ void __launch_bounds__(128) lora_down(const LoraParams p, uint16_t* t) {
+    dependents_may_start();
+    down_rows<RP, false, RT>(p, t);
+}
+
+// Both of the backward pass: u, then (blockIdx.y 1) t.
+template <int RP, int RT>
+__global__ void __launch_bounds__(128) lora_down_both(const LoraParams p, uint16_t* t, uint16_t* u) {
+    wait_for_primary();   // the plan's offsets
+    dependents_may_start();
+    if (blockIdx.y == 0) down_rows<RP, true, RT>(p, u);
+    else down_rows<RP, false, RT>(p, t);
 }
 
 // ------------------------------------------------------------------ the large product
@@ -468,6 +482,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
     } else if (warp < 8) {
         // ---------------------------------------------------------- epilogue
         wait_for_primary();
+        dependents_may_start();   // who reads t and u too
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + half * 128;
         float* bias_s = reinterpret_cast<float*>(base_ptr + OFF_BIAS) + warp * 128;   // this warp's copy
@@ -693,6 +708,7 @@ __host__ __device__ __forceinline__ Plan plan_at(void* work, int n_req, int n_ad
 
 // One block.
 __global__ void __launch_bounds__(256) lora_plan(const LoraParams p, const Plan q) {
+    dependents_may_start();
     __shared__ int top[256];
     const int per = (p.n_req + 256) / 256, lo = min(int(threadIdx.x) * per, p.n_req + 1), hi = min(lo + per, p.n_req + 1);
     int m = 0;
@@ -746,7 +762,10 @@ constexpr int kGradStages = 3;
 // few as splits and adapters together. Bound by the read of x and dqkv.
 template <int RP>
 __global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan q, const uint16_t* tt, const uint16_t* uu,
-                                                 float* part, int splits) {
+                                                 float* part, int splits, bool beside) {
+    // beside the large product, which started behind t and u; else behind those
+    if (!beside) wait_for_primary();
+    dependents_may_start();
     constexpr int X_TILE = kChunk * 256, U_TILE = kChunk * RP * 2, STAGE_G = X_TILE + U_TILE, MT = RP / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -758,7 +777,10 @@ __global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan 
     const uint16_t* const u = is_b ? tt : uu;
     const int total = q.ad_first[p.n_ad], per = (total + splits - 1) / splits;
     const int first = blockIdx.y * per, last = min(first + per, total);
-    if (first >= last) return;
+    if (first >= last) {
+        if (beside) wait_for_primary();
+        return;
+    }
 
     // the place of the first chunk: the last request that starts at or before it
     int j = 0;
@@ -834,12 +856,14 @@ __global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan 
     }
     cp_wait<0>();
     flush();
+    if (beside) wait_for_primary();   // ends behind the product beside it
 }
 
 // The parts of each adapter, in their order, to dA (n_ad, R, C) and dB
 // (n_ad, N, R), the q block's rows of dB scaled. A thread sums eight ranks of
 // one column.
 __global__ void __launch_bounds__(256) lora_grad_sum(const LoraParams p, const Plan q, const float* part, int splits, int rp) {
+    wait_for_primary();
     const int cols = p.C + p.N, n8 = p.R / 8;
     const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
     if (e >= int64_t(p.n_ad) * n8 * cols) return;
@@ -911,12 +935,12 @@ bool map_of(CUtensorMap* m, const void* ptr, int dims, const int64_t* size, cons
 // A launch that may start while the kernel before it, which lets it, still
 // runs; it waits for that kernel itself where it reads its results.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, int smem, cudaStream_t stream, const A&... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, int smem, cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute a = {};
     a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a.val.programmaticStreamSerializationAllowed = 1;
-    c.gridDim = dim3(grid);
+    c.gridDim = grid;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = stream;
@@ -925,27 +949,31 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threa
     return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
-template <int RP, bool BWD, int RT>
-cudaError_t down_t(const LoraParams& p, uint16_t* out, cudaStream_t stream) {
+// t, or with `u` both.
+template <int RP, int RT>
+cudaError_t down_t(const LoraParams& p, uint16_t* t, uint16_t* u, cudaStream_t stream) {
     constexpr int smem = kDownStages * (RT * 128 + RP * 128);
     static_assert(RT != 16 || 4 * 16 * RP * 4 <= smem, "the warps' parts fit the stages");
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(lora_down<RP, BWD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e =
+            u ? cudaFuncSetAttribute(lora_down_both<RP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+              : cudaFuncSetAttribute(lora_down<RP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    lora_down<RP, BWD, RT><<<unsigned(ceil_div(p.M, 128) * 128 / RT), 128, smem, stream>>>(p, out);
+    const unsigned grid = unsigned(ceil_div(p.M, 128) * 128 / RT);
+    if (u) return launch_dependent(lora_down_both<RP, RT>, dim3(grid, 2), 128, smem, stream, p, t, u);
+    lora_down<RP, RT><<<grid, 128, smem, stream>>>(p, t);
     return cudaGetLastError();
 }
 
-template <bool BWD>
-cudaError_t down(const LoraParams& p, uint16_t* out, int sms, cudaStream_t stream) {
+cudaError_t down(const LoraParams& p, uint16_t* t, uint16_t* u, int sms, cudaStream_t stream) {
     // 64 rows a block leave SMs idle below 64 * sms rows
     const bool small = p.M < 64 * sms;
     switch (padded_rank(p.R)) {
-        case 16: return small ? down_t<16, BWD, 16>(p, out, stream) : down_t<16, BWD, 64>(p, out, stream);
-        case 32: return small ? down_t<32, BWD, 16>(p, out, stream) : down_t<32, BWD, 64>(p, out, stream);
-        case 64: return small ? down_t<64, BWD, 16>(p, out, stream) : down_t<64, BWD, 64>(p, out, stream);
-        default: return small ? down_t<128, BWD, 16>(p, out, stream) : down_t<128, BWD, 64>(p, out, stream);
+        case 16: return small ? down_t<16, 16>(p, t, u, stream) : down_t<16, 64>(p, t, u, stream);
+        case 32: return small ? down_t<32, 16>(p, t, u, stream) : down_t<32, 64>(p, t, u, stream);
+        case 64: return small ? down_t<64, 16>(p, t, u, stream) : down_t<64, 64>(p, t, u, stream);
+        default: return small ? down_t<128, 16>(p, t, u, stream) : down_t<128, 64>(p, t, u, stream);
     }
 }
 
@@ -975,7 +1003,7 @@ cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t s
     if (!ok) return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(lora_gemm<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    return launch_dependent(lora_gemm<BWD>, unsigned(tiles < sms ? tiles : sms), kThreads, SMEM_ALLOC, stream, ta, tb, tt, tl,
+    return launch_dependent(lora_gemm<BWD>, dim3(unsigned(tiles < sms ? tiles : sms)), kThreads, SMEM_ALLOC, stream, ta, tb, tt, tl,
                             p, q);
 }
 
@@ -985,12 +1013,11 @@ cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const ui
     cudaError_t e = cudaFuncSetAttribute(lora_grad<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int splits = grad_splits(p.M, p.C, p.N);
-    lora_grad<RP><<<dim3(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits)), 256, smem, stream>>>(
-        p, q, t, u, part, splits);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const dim3 grid(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits));
+    e = launch_dependent(lora_grad<RP>, grid, 256, smem, stream, p, q, t, u, part, splits, p.dx != nullptr);
+    if (e != cudaSuccess) return e;
     const int64_t n = int64_t(p.n_ad) * (p.R / 8) * (int64_t(p.C) + p.N);
-    lora_grad_sum<<<unsigned(ceil_div(n, 256)), 256, 0, stream>>>(p, q, part, splits, RP);
-    return cudaGetLastError();
+    return launch_dependent(lora_grad_sum, dim3(unsigned(ceil_div(n, 256))), 256, 0, stream, p, q, part, splits, RP);
 }
 
 }  // namespace
@@ -1005,12 +1032,12 @@ cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
         lora_down_few<<<dim3(unsigned(p.M), unsigned(p.R / 8)), 256, 0, stream>>>(p, t);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const unsigned grid = unsigned(p.N / 16);
+        const dim3 grid(unsigned(p.N / 16));
         if (p.M <= 8) return launch_dependent(lora_fwd_few<1>, grid, 256, 0, stream, p, t);
         if (p.M <= 16) return launch_dependent(lora_fwd_few<2>, grid, 256, 0, stream, p, t);
         return launch_dependent(lora_fwd_few<4>, grid, 256, 0, stream, p, t);
     }
-    const cudaError_t e = down<false>(p, t, sms, stream);
+    const cudaError_t e = down(p, t, nullptr, sms, stream);
     return e != cudaSuccess ? e : gemm<false>(p, t, sms, stream);
 }
 
@@ -1024,8 +1051,7 @@ cudaError_t launch_lora_bwd(const LoraParams& p0, int sms, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     LoraParams p = p0;   // every pass walks the plan's offsets
     p.offsets = q.offsets;
-    if ((e = down<false>(p, t, sms, stream)) != cudaSuccess) return e;
-    if ((e = down<true>(p, u, sms, stream)) != cudaSuccess) return e;
+    if ((e = down(p, t, u, sms, stream)) != cudaSuccess) return e;
     if (p.dx && (e = gemm<true>(p, u, sms, stream)) != cudaSuccess) return e;
     float* part = reinterpret_cast<float*>(work + w.part);
     switch (padded_rank(p.R)) {

@@ -259,7 +259,8 @@ __host__ __device__ __forceinline__ int range_hi(bool dkv, int i, int K, int N) 
 // cr grid rows and cc columns. sw <= 8, so that rows r and r + 8 of a warp, a
 // thread's two, lie in one column of the grid.
 struct TileGeom {
-    int32_t st, sh, sw, nw, bh;
+    int32_t st, sh, sw, nw, bh;   // st, sh and sw: powers of two
+    int32_t sw_log2;
     int32_t nbt, nbh, nbw;
     int32_t cr, cc;
     int32_t nt, nhc, nwc;      // chunks of a unit: frames, and parts along H and W
@@ -297,6 +298,11 @@ struct Sync {
         }
     }
 };
+
+// A kernel lets the next one of its stream start, and waits for the one before
+// it to be through.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -498,6 +504,13 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const uint32_t f_region = (uint32_t(f_rows) * HDB * 2 + 1023u) & ~1023u, f_bytes = f_region * REG;
     const uint32_t x_bytes = g.x_bytes, x_region = REG > 1 ? x_bytes / REG : 0;
     const bool docs = p.doc != nullptr;
+
+    // the kernel before (the forward pass has none that lets it start early) brings the
+    // statistics; the one behind needs nothing of this one
+    if (MODE == kDq) {
+        wait_for_primary();
+        dependents_may_start();
+    }
 
     // control words: abort flag, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
@@ -701,33 +714,35 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         const int in_chunk = g.nhc > 1 ? mine.x - cur.bh.x : 0;
         if ((biased && head != lut_head) || place_h != lut_h || place_w != lut_w || in_chunk != lut_chunk) {
             __syncwarp();
-            for (int r = use_lut ? hi : 0; r < (use_lut ? n_hw : 16); r += use_lut ? 2 : 1) {
-                const int lh = wh0 + r / g.sw % g.sh, lw = o.w0 + r % g.sw;
-                const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
-                const float h_n = lh < p.H && lw < p.W ? float(range_hi(DKV, lh, p.KH, p.H) - h_lo) : 0.f;
-                const float w_n = float(range_hi(DKV, lw, p.KW, p.W) - w_lo);
-                float* to = lut + r * g.lut_pitch + (lane & 15);
-                uint16_t* words = reinterpret_cast<uint16_t*>(mask) + 2 * (r & 7) + (r >> 3);
-                for (int h = cur.bh.x; h < cur.bh.y; h += g.cr)
-                    for (int w = cur.bw.x; w < cur.bw.y; w += g.cc) {
-                        const int hf = max(mine.x, h), rows = min(mine.y, h + g.cr) - hf;
-                        const float h_in = float(hf - h_lo), w_in = float(w - w_lo), h_far = float(hf - lh), w_far = float(w - lw);
-                        const float n_rows = float(rows);
-                        for (int i0 = 0; i0 < rows * g.cc; i0 += 16) {
-                            const float2 at = hw[i0 + (lane & 15)];
-                            const bool in = at.x < n_rows && at.x + h_in >= 0.f && at.x + h_in < h_n &&
-                                            at.y + w_in >= 0.f && at.y + w_in < w_n;
+            int at_step = 0;
+            for (int ih = 0; ih < g.nhc; ++ih)
+                for (int iw = 0; iw < g.nwc; ++iw) {
+                    int hf, w;
+                    const int n = part_of(ih, iw, hf, w);
+                    for (int i0 = 0; i0 < n; i0 += 16, ++at_step) {
+                        const float2 at = hw[i0 + (lane & 15)];
+                        // this lane's column; one past the box is in no window
+                        const int h = i0 + (lane & 15) < n ? hf + int(at.x) : 1 << 30, x = w + int(at.y);
+                        // two rows' places at a time, one in each half of the warp (mask words: all
+                        // sixteen rows)
+#pragma unroll 4
+                        for (int r = hi; r < (use_lut ? n_hw : 16); r += 2) {
+                            const int lh = wh0 + ((r >> g.sw_log2) & (g.sh - 1)), lw = o.w0 + (r & (g.sw - 1));
+                            const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
+                            const bool in = lh < p.H && lw < p.W && h >= h_lo && x >= w_lo &&
+                                            h < range_hi(DKV, lh, p.KH, p.H) && x < range_hi(DKV, lw, p.KW, p.W);
                             if (use_lut) {
-                                *to = in ? fmaf(sl[1], fabsf(at.x + h_far), sl[2] * fabsf(at.y + w_far)) : -INFINITY;
-                                to += 16;
+                                lut[r * g.lut_pitch + at_step * 16 + (lane & 15)] =
+                                    in ? fmaf(sl[1], float(abs(h - lh)), sl[2] * float(abs(x - lw))) : -INFINITY;
                             } else {
-                                const uint32_t bits = __ballot_sync(0xffffffffu, in) & 0xffffu;
-                                if (lane == 0) *words = uint16_t(bits);
-                                words += 16;
+                                const uint32_t bits = __ballot_sync(0xffffffffu, in);
+                                if ((lane & 15) == 0)
+                                    reinterpret_cast<uint16_t*>(mask)[at_step * 16 + 2 * (r & 7) + (r >> 3)] =
+                                        uint16_t(hi ? bits >> 16 : bits & 0xffffu);
                             }
                         }
                     }
-            }
+                }
             __syncwarp();
             lut_head = head;
             lut_h = place_h;
@@ -1175,6 +1190,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         next_unit<DKV>(p, g, cur);
     }
 
+    if (DKV) wait_for_primary();   // ends behind the kernel beside it
     // every issued load lands before the block may exit: where all went well
     // each has been waited for
     __syncthreads();
@@ -1189,6 +1205,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 template <int HD>
 __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t rows) {
     constexpr int L = HD / 8;
+    dependents_may_start();
     const int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / L;
     const int c = threadIdx.x % L;
     const bool live = r < rows;
@@ -1267,7 +1284,8 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
             for (int nw = 1; nw <= max_warps(hd, mode); ++nw) {
                 if ((nw - 1) * sh >= p.H) break;
                 TileGeom g{};
-                g.st = st; g.sh = sh; g.sw = sw; g.nw = nw; g.bh = nw * sh;
+                g.st = st; g.sh = sh; g.sw = sw; g.nw = nw;
+                g.sw_log2 = sw == 8 ? 3 : sw == 4 ? 2 : sw == 2 ? 1 : 0; g.bh = nw * sh;
                 if (g.bh > 256) continue;
                 g.nbt = (p.T + st - 1) / st;
                 g.nbh = (p.H + g.bh - 1) / g.bh;
@@ -1395,8 +1413,22 @@ cudaError_t launch_tiles(const ScoredParams& p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int64_t slots = int64_t(sms) * blocks_per_sm(HD, MODE);
     const int grid = int(g.units < slots ? g.units : slots);
-    scored_tiles<HD, MODE><<<grid, g.nw * 32, g.smem, stream>>>(mf0, mf1, mx0, mx1, p, g);
-    return cudaGetLastError();
+    if (MODE == kFwd) {
+        scored_tiles<HD, MODE><<<grid, g.nw * 32, g.smem, stream>>>(mf0, mf1, mx0, mx1, p, g);
+        return cudaGetLastError();
+    }
+    // starts while the kernel before it, which lets it, still runs
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(g.nw * 32);
+    c.dynamicSmemBytes = g.smem;
+    c.stream = stream;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, scored_tiles<HD, MODE>, mf0, mf1, mx0, mx1, p, g);
 }
 
 template <int HD>
