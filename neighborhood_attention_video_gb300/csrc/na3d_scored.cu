@@ -232,7 +232,7 @@ enum { kFwd, kDq, kDkv };
 // 60 more a thread).
 __host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= 32 && mode == kFwd ? 2 : 1; }
 __host__ __device__ constexpr int max_warps(int hd, int mode) {
-    return blocks_per_sm(hd, mode) == 2 || hd > 64 || (hd > 32 && mode == kDkv) ? 8 : 12;
+    return blocks_per_sm(hd, mode) == 2 || hd > 64 || (hd > 32 && mode != kDq) ? 8 : 12;
 }
 // Buffers of the fixed tensors: two where a step reads them again (their
 // fragments and the accumulators together exceed the registers).
@@ -566,14 +566,14 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 tma_load_5d(to + f_bytes + r * f_region, &tm_f1, full, x.head * HD + r * 64, x.o.w0, x.o.h0, x.o.t0, x.o.b);
         }
     };
-    // This warp is done with a ring place; true where it is the last to be.
+    // This warp is done with a ring place; true, in lane 0, where it is the last to be.
     auto last_done = [&](int i) {
-        uint32_t n = 0;
         __syncwarp();
-        if (lane == 0)
-            asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;"
-                         : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
-        return __shfl_sync(0xffffffffu, n, 0) == uint32_t(nw - 1);
+        if (lane != 0) return false;
+        uint32_t n;
+        asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;"
+                     : "=r"(n) : "r"(smem_u32(done + i)), "r"(uint32_t(nw - 1)) : "memory");
+        return n == uint32_t(nw - 1);
     };
     Unit cur = unit_of<DKV>(p, g, min(u0, g.units - 1));
     // the chunk that is S after the current one: its place in its unit, and whether
@@ -608,13 +608,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const int row_t0 = r0 / n_hw, row_t1 = (r0 + 8) / n_hw;
     const int row_h0 = r0 / g.sw % g.sh, row_h1 = (r0 + 8) / g.sw % g.sh, row_w = r0 % g.sw;
     const int frag_row = (((lane & 15) / n_hw) * g.bh + warp * g.sh + (lane & 15) / g.sw % g.sh) * g.sw + (lane & 15) % g.sw;
-    const uint32_t lane_x = swizzled<HD>(lane & 15, hi, 0);   // of the first rows of a stage
+    const bool one_chunk = g.nhc * g.nwc == 1;
     const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
     const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
     const float to_log2 = capped ? p.softcap * kLog2e : kLog2e;
-    const float half_cap = 0.5f * p.softcap, inv2 = inv_cap * inv_cap;
-    const float poly[4] = {kTanh[0] * inv2 * kLog2e, kTanh[1] * inv2 * inv2 * kLog2e, kTanh[2] * inv2 * inv2 * inv2 * kLog2e,
-                           kTanh[3] * inv2 * inv2 * inv2 * inv2 * kLog2e};
+    const float exp_scale = 2.f * kLog2e * inv_cap;
     // Columns' documents and (lse, delta): a warp keeps those of its current chunk in a
     // buffer of its own and the next chunk's first ones in registers meanwhile.
     constexpr int PF = 3;
@@ -760,7 +758,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < KB; ++kk)
                 ldsm4(f_at + n * f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), fa[n][kk]);
-        if (NFR == NF && last_done(S + fb) && lane == 0 && u + 1 < u1) {
+        if (NFR == NF && last_done(S + fb) && u + 1 < u1) {
             Unit next = cur;
             next_unit<DKV>(p, g, next);
             load_fixed(next, fb);
@@ -778,26 +776,38 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // any for a row that has met no key, so that ref starts at a score
         float l[2] = {0.f, 0.f}, grow[2] = {-INFINITY, -INFINITY};
 
+        // this warp's part of a chunk: its columns from (hf, w), their steps, and the addresses of
+        // the first ones in a stage (and its tables, where a frame has one chunk, once a unit)
+        int hf = 0, w = 0, n = 0, part_steps = 0, step = 0;
+        uint32_t part_at = 0;
+        float row_t[2] = {float(rt[0] - cur.bt.x), float(rt[1] - cur.bt.x)};   // frames ahead
         for (int it = 0; it < g.nt && ok; ++it) {
             const int t = cur.bt.x + it;
             // the frame's part of the score: -inf for a row that does not see it
             float far_t[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                far_t[i] = t - t_lo[i] >= 0 && t - t_lo[i] < t_n[i] ? sl[0] * fabsf(float(t - rt[i])) : -INFINITY;
+            for (int i = 0; i < 2; ++i) {
+                far_t[i] = uint32_t(t - t_lo[i]) < uint32_t(t_n[i]) ? sl[0] * fabsf(row_t[i]) : -INFINITY;
+                row_t[i] -= 1.f;
+            }
             // no row of this warp sees the frame: its chunks are passed over
             const bool frame_seen = t < cur.bt.y && __any_sync(0xffffffffu, fmaxf(far_t[0], far_t[1]) > -INFINITY);
-            int step = 0;   // of the frame's table
+            if (!one_chunk) step = 0;   // of the frame's table
             for (int ih = 0; ih < g.nhc && ok; ++ih)
                 for (int iw = 0; iw < g.nwc; ++iw) {
                     if (!(ok = sy.wait(sy.bar(s), turn))) break;
-                    int hf, w;
-                    const int n = part_of(ih, iw, hf, w);
-                    int n_steps = n > 0 ? (n + 15) >> 4 : 0;
-                    const int first = (hf - cur.bh.x - ih * g.cr) * g.cc;
+                    if (!one_chunk || it == 0) {
+                        n = part_of(ih, iw, hf, w);
+                        step += part_steps;
+                        if (iw == 0 && ih == 0) step = 0;
+                        part_steps = n > 0 ? (n + 15) >> 4 : 0;
+                        // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
+                        // step moves them by 16 rows and a column block by an exclusive or
+                        part_at = swizzled<HD>((hf - cur.bh.x - ih * g.cr) * g.cc + (lane & 15), hi, 0);
+                    }
+                    int n_steps = frame_seen ? part_steps : 0;
                     const float* lut_at = lut_row + step * 16;
                     const uint32_t* mask_at = mask + step * 8 + r0;
-                    step += n_steps;
                     // documents: a comparison for each score where the chunk holds others than
                     // the rows', none where it does not, no work where no row's is there
                     bool mixed = false;
@@ -837,41 +847,49 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     }
                     const int* key_doc = col_doc;
                     const float2* stat = col_stat;
-                    if (!frame_seen) n_steps = 0;
-
-                    // ldmatrix addresses: the permutation of a row's chunks repeats every 8 rows, so a
-                    // step moves them by 16 rows and a column block by an exclusive or
-                    uint32_t a0 = base + g.off_x + 2 * s * x_bytes;
-                    a0 += first % 8 ? swizzled<HD>(first + (lane & 15), hi, 0) : first * (HDB * 2) + lane_x;
+                    uint32_t a0 = base + g.off_x + 2 * s * x_bytes + part_at;
                     auto columns = [&](uint32_t at, int kk) { return (at + (kk >> 2) * x_region) ^ ((kk & 3) << 5); };
                     // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
                     // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
                     // The plain chunks of the forward pass, with the table and without documents to
-                    // compare, take N steps at a time, so that the steps' chains of matrix products
+                    // compare, take NS steps at a time, so that the steps' chains of matrix products
                     // and powers overlap.
+                    constexpr int NS = 1;
                     if (MODE == kFwd && use_lut && !mixed && (!capped || bounded)) {
                         uint32_t ak[KB];   // a column block's address; the next step's is 16 rows on
 #pragma unroll
                         for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
-                        auto plain = [&](auto n_const, auto cap_const) {
+                        // the scores of N steps, m steps on from ak; N steps ahead of the softmax, whose
+                        // instructions fill the issue slots between these matrix products (the last
+                        // ones read rows past the chunk, for nothing)
+                        float next[NS][8];
+                        auto scores = [&](auto n_const, int m0) {
                             constexpr int N = decltype(n_const)::value;
-                            constexpr bool CAP = decltype(cap_const)::value;
-                            float sc[N][8];
 #pragma unroll
                             for (int m = 0; m < N; ++m)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) sc[m][i] = 0.f;
+                                for (int i = 0; i < 8; ++i) next[m][i] = 0.f;
                             // 2 N accumulators in turn: a product finds its sum ready
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk)
 #pragma unroll
                                 for (int m = 0; m < N; ++m) {
                                     uint32_t f[4];
-                                    ldsm4(ak[kk] + m * 16 * HDB * 2, f);
-                                    mma16816(sc[m], fa[0][kk], f[0], f[2]);
-                                    mma16816(sc[m] + 4, fa[0][kk], f[1], f[3]);
+                                    ldsm4(ak[kk] + (m0 + m) * 16 * HDB * 2, f);
+                                    mma16816(next[m], fa[0][kk], f[0], f[2]);
+                                    mma16816(next[m] + 4, fa[0][kk], f[1], f[3]);
                                 }
-                            uint64_t s2[N][4], x2[N][4];   // bias minus reference, then the score; a
+                        };
+                        auto plain = [&](auto n_const, auto cap_const, auto ahead_const) {
+                            constexpr int N = decltype(n_const)::value;
+                            constexpr bool CAP = decltype(cap_const)::value;
+                            float sc[N][8];
+#pragma unroll
+                            for (int m = 0; m < N; ++m)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) sc[m][i] = next[m][i];
+                            scores(ahead_const, N);
+                            float sv[N][8];
                             const uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
 #pragma unroll
                             for (int m = 0; m < N; ++m)
@@ -879,53 +897,25 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                 for (int j = 0; j < 2; ++j) {
                                     const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 16 * m + 8 * j);
                                     const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 16 * m + 8 * j);
-                                    s2[m][2 * j] = f2_add(x, from[0]);
-                                    s2[m][2 * j + 1] = f2_add(y, from[1]);
-                                }
-                            float big = 0.f;
 #pragma unroll
-                            for (int m = 0; m < N; ++m)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    x2[m][j] = f2_pack(sc[m][2 * j], sc[m][2 * j + 1]);
-                                    if (CAP) big = max3f(big, fabsf(sc[m][2 * j]), fabsf(sc[m][2 * j + 1]));
-                                }
-                            if (CAP && __any_sync(0xffffffffu, big > half_cap)) {
-#pragma unroll
-                                for (int m = 0; m < N; ++m)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        float z[2];
-                                        f2_unpack(f2_mul(x2[m][j], f2_dup(inv_cap)), z[0], z[1]);
-                                        float q[2];
-                                        f2_unpack(tanh_poly(f2_pack(z[0], z[1])), q[0], q[1]);
-#pragma unroll
-                                        for (int i = 0; i < 2; ++i) q[i] = fabsf(z[i]) > 0.5f ? tanh_exp(z[i]) : q[i];
-                                        s2[m][j] = f2_fma(f2_pack(q[0], q[1]), f2_dup(to_log2), s2[m][j]);
+                                    for (int i = 0; i < 2; ++i) {
+                                        float* const s4 = &sc[m][4 * j + 2 * i];
+                                        const uint64_t bias = f2_add(i ? y : x, from[i]);   // minus the reference
+                                        uint64_t s;
+                                        if (CAP) {
+                                            // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)); within a few 2^-24 of c, and
+                                            // c <= 64 here
+                                            const uint64_t z = f2_mul(f2_pack(s4[0], s4[1]), f2_dup(exp_scale));
+                                            float e0, e1;
+                                            f2_unpack(z, e0, e1);
+                                            f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);
+                                            s = f2_fma(f2_pack(rcp_approx(e0), rcp_approx(e1)), f2_dup(-2.f * to_log2), f2_add(bias, f2_dup(to_log2)));
+                                        } else {
+                                            s = f2_fma(f2_pack(s4[0], s4[1]), f2_dup(kLog2e), bias);
+                                        }
+                                        f2_unpack(s, sv[m][4 * j + 2 * i], sv[m][4 * j + 2 * i + 1]);
                                     }
-                            } else if (CAP) {
-                                // c tanh(a / c) = a + a^3 P(a^2): the polynomial of tanh_poly in a itself
-#pragma unroll
-                                for (int m = 0; m < N; ++m)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        const uint64_t a = x2[m][j], y = f2_mul(a, a);
-                                        uint64_t q = f2_fma(y, f2_dup(poly[3]), f2_dup(poly[2]));
-                                        q = f2_fma(y, q, f2_dup(poly[1]));
-                                        q = f2_fma(y, q, f2_dup(poly[0]));
-                                        s2[m][j] = f2_fma(f2_mul(a, y), q, f2_fma(a, f2_dup(kLog2e), s2[m][j]));
-                                    }
-                            } else {
-#pragma unroll
-                                for (int m = 0; m < N; ++m)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) s2[m][j] = f2_fma(x2[m][j], f2_dup(kLog2e), s2[m][j]);
-                            }
-                            float sv[N][8];
-#pragma unroll
-                            for (int m = 0; m < N; ++m)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) f2_unpack(s2[m][j], sv[m][2 * j], sv[m][2 * j + 1]);
+                                }
                             if (!CAP) {
                                 float top[2];
 #pragma unroll
@@ -967,13 +957,23 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             lut_at += 16 * N;
                         };
                         using std::integral_constant;
-                        int k = 0;
-                        if (capped) {
-                            for (; k + 2 <= n_steps; k += 2) plain(integral_constant<int, 2>{}, integral_constant<bool, true>{});
-                            if (k < n_steps) plain(integral_constant<int, 1>{}, integral_constant<bool, true>{});
-                        } else {
-                            for (; k + 2 <= n_steps; k += 2) plain(integral_constant<int, 2>{}, integral_constant<bool, false>{});
-                            if (k < n_steps) plain(integral_constant<int, 1>{}, integral_constant<bool, false>{});
+                        const integral_constant<int, NS> full{};
+                        const integral_constant<int, 1> one{};
+                        auto run = [&](auto cap_const) {
+                            int k = 0;
+                            if (n_steps >= NS) {
+                                scores(full, 0);
+                                for (; k + 2 * NS <= n_steps; k += NS) plain(full, cap_const, full);
+                                plain(full, cap_const, one);
+                                k += NS;
+                            } else {
+                                scores(one, 0);
+                            }
+                            for (; k < n_steps; ++k) plain(one, cap_const, one);
+                        };
+                        if (n_steps > 0) {
+                            if (capped) run(integral_constant<bool, true>{});
+                            else run(integral_constant<bool, false>{});
                         }
                         n_steps = 0;
                     }
@@ -1124,7 +1124,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         }
                     }
                     // the stage's next chunk is S further on
-                    if (last_done(s) && lane == 0 && (!in_next || u + 1 < u1)) {
+                    if (last_done(s) && (!in_next || u + 1 < u1)) {
                         Unit of = cur;
                         if (in_next) next_unit<DKV>(p, g, of);
                         load_chunk(of, nt_i, nh_i, nw_i, s);
@@ -1137,7 +1137,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 }
         }
         if (!ok) break;
-        if (NFR < NF && last_done(S + fb) && lane == 0 && u + FB < u1) load_fixed(unit_of<DKV>(p, g, u + FB), fb);
+        if (NFR < NF && last_done(S + fb) && u + FB < u1) load_fixed(unit_of<DKV>(p, g, u + FB), fb);
 
         // rows out; a row that is not finite throughout is computed again by itself
         uint32_t bad = 0;
