@@ -860,33 +860,33 @@ __global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan 
 }
 
 // The parts of each adapter, in their order, to dA (n_ad, R, C) and dB
-// (n_ad, N, R), the q block's rows of dB scaled. A thread sums eight ranks of
-// one column.
+// (n_ad, N, R), the q block's rows of dB scaled. A thread sums one value: the
+// parts lie far apart, so what counts is how many reads are under way.
 __global__ void __launch_bounds__(256) lora_grad_sum(const LoraParams p, const Plan q, const float* part, int splits, int rp) {
     wait_for_primary();
-    const int cols = p.C + p.N, n8 = p.R / 8;
+    const int cols = p.C + p.N;
     const int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= int64_t(p.n_ad) * n8 * cols) return;
-    const int col = int(e % cols), r0 = int(e / cols % n8) * 8, a = int(e / cols / n8);
+    if (e >= int64_t(p.n_ad) * p.R * cols) return;
+    const int col = int(e % cols), r = int(e / cols % p.R), a = int(e / cols / p.R);
     const int total = q.ad_first[p.n_ad], per = (total + splits - 1) / splits;
     const int c0 = q.ad_first[a], c1 = q.ad_first[a + 1];
-    float s[8] = {};
-    if (c0 < c1)
-        for (int k = c0 / per; k <= (c1 - 1) / per; ++k)
+    float s = 0.f;
+    if (c0 < c1) {
+        const int k1 = (c1 - 1) / per;
+        const float* from = part + ((int64_t(c0 / per) + a) * rp + r) * cols + col;
+        const int64_t next = int64_t(rp) * cols;
+        int k = c0 / per;
+        for (; k + 7 <= k1; k += 8, from += 8 * next) {
+            float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += part[((int64_t(k) + a) * rp + r0 + i) * cols + col];
-    if (col < p.C) {
+            for (int i = 0; i < 8; ++i) x[i] = from[i * next];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p.da[(int64_t(a) * p.R + r0 + i) * p.C + col] = b16(s[i]);
-    } else {
-        const float by = col - p.C < p.Nq ? p.q_scale : 1.f;
-        uint4 v;
-        v.x = pack_bf16x2(s[0] * by, s[1] * by);
-        v.y = pack_bf16x2(s[2] * by, s[3] * by);
-        v.z = pack_bf16x2(s[4] * by, s[5] * by);
-        v.w = pack_bf16x2(s[6] * by, s[7] * by);
-        *reinterpret_cast<uint4*>(p.db + (int64_t(a) * p.N + col - p.C) * p.R + r0) = v;
+            for (int i = 0; i < 8; ++i) s += x[i];
+        }
+        for (; k <= k1; ++k, from += next) s += *from;
     }
+    if (col < p.C) p.da[(int64_t(a) * p.R + r) * p.C + col] = b16(s);
+    else p.db[(int64_t(a) * p.N + col - p.C) * p.R + r] = b16(s * (col - p.C < p.Nq ? p.q_scale : 1.f));
 }
 
 // ------------------------------------------------------------------ launch
@@ -1016,7 +1016,7 @@ cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const ui
     const dim3 grid(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits));
     e = launch_dependent(lora_grad<RP>, grid, 256, smem, stream, p, q, t, u, part, splits, p.dx != nullptr);
     if (e != cudaSuccess) return e;
-    const int64_t n = int64_t(p.n_ad) * (p.R / 8) * (int64_t(p.C) + p.N);
+    const int64_t n = int64_t(p.n_ad) * p.R * (int64_t(p.C) + p.N);
     return launch_dependent(lora_grad_sum, dim3(unsigned(ceil_div(n, 256))), 256, 0, stream, p, q, part, splits, RP);
 }
 
