@@ -45,9 +45,10 @@ __device__ __forceinline__ int first_request(const LoraParams& p, int m) {
     return lo;
 }
 
-// The requests with an adapter that meet rows [m0, m0 + 128), in order. Every
+// The requests with an adapter that meet rows [m0, m0 + SPAN), in order. Every
 // role of every kernel walks them alike.
-struct Walk {
+template <int SPAN>
+struct WalkOf {
     int r, a, lo, hi;   // request, its adapter, its rows
     __device__ __forceinline__ void start(const LoraParams& p, int m0) {
         r = first_request(p, m0) - 1;
@@ -56,7 +57,7 @@ struct Walk {
     __device__ __forceinline__ void next(const LoraParams& p, int m0) {
         for (++r; r < p.n_req; ++r) {
             lo = p.offsets[r];
-            if (lo >= m0 + 128) break;
+            if (lo >= m0 + SPAN) break;
             hi = p.offsets[r + 1];
             a = p.adapter[r];
             if (hi > lo && hi > m0 && a >= 0 && a < p.n_ad) return;
@@ -65,6 +66,7 @@ struct Walk {
     }
     __device__ __forceinline__ bool more(const LoraParams& p) const { return r < p.n_req; }
 };
+using Walk = WalkOf<128>;
 
 __host__ __device__ __forceinline__ int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
@@ -252,15 +254,23 @@ __global__ void __launch_bounds__(128) lora_down_both(const LoraParams p, uint16
 
 // ------------------------------------------------------------------ the large product
 
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
+constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kThreads = 320;   // eight epilogue warps, a loading and an issuing one
-constexpr int A_TILE = kBM * kBK * 2, B_TILE = kBN * kBK * 2, STAGE = A_TILE + B_TILE;
-constexpr int OFF_BAR = kStages * STAGE;
-constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + 2, B_DRAIN = B_AEMPTY + 2,
-              NBAR = B_DRAIN + 1;
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-constexpr int OFF_BIAS = (OFF_MISC + 16 + 15) & ~15;   // a tile's bias, fp32, for each epilogue warp its columns
-constexpr int SMEM_ALLOC = OFF_BIAS + 8 * 128 * 4 + 1024;
+
+// Shared memory of a block, alone (CG 1) or one of a pair (CG 2): each block of
+// a pair holds its own 128 rows of A and half of the columns of B.
+template <int CG>
+struct Shape {
+    static constexpr int kStages = CG == 2 ? 6 : 4;
+    static constexpr int BN = kBN / CG;
+    static constexpr int A_TILE = kBM * kBK * 2, B_TILE = BN * kBK * 2, STAGE = A_TILE + B_TILE;
+    static constexpr int OFF_BAR = kStages * STAGE;
+    static constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + 2,
+                         B_DRAIN = B_AEMPTY + 2, NBAR = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_BIAS = (OFF_MISC + 16 + 15) & ~15;   // a tile's bias, fp32, for each epilogue warp its columns
+    static constexpr int SMEM = OFF_BIAS + 8 * 128 * 4 + 1024;
+};
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 500000000ull;
 
@@ -268,12 +278,21 @@ struct Sync {
     uint32_t bar0;
     volatile uint32_t* abort_flag;
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
+    // (the other block of a pair arrives on some of the barriers)
+    static __device__ __forceinline__ bool try_wait(uint32_t b, uint32_t parity) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(b), "r"(parity) : "memory");
+        return ok != 0;
+    }
     // Wait for a barrier phase; false once this block has given up.
     __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
-        if (mbar_try_wait(b, parity)) return true;
+        if (try_wait(b, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(b, parity)) return true;
+            if (try_wait(b, parity)) return true;
             if ((it & 1023u) == 0u) {
                 if (*abort_flag) return false;
                 if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -294,10 +313,77 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "r"(bar) : "memory");
 }
 
+// Pairs of blocks (cta_group::2): a cluster of two whose tensor cores work on one
+// tile of 256 rows. The leader (rank 0) issues; barriers that both sides of a
+// pair signal are the leader's.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t leaders(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1) {
+    if (CG == 1) {
+        tma_load_2d(dst, map, bar, c0, c1);
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+    if (CG == 1) {
+        tma_load_3d(dst, map, bar, c0, c1, c2);
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
+            "r"(bar) : "memory");
+    }
+}
+template <int CG, uint32_t ACC>
+__device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+    if (CG == 1) {
+        umma_ss_halves<ACC>(d, a_lo, a_hi, b_lo, b_hi, idesc);
+    } else {
+        asm volatile(
+            "{\n\t.reg .b64 da, db;\n\t.reg .pred p;\n\t"
+            "mov.b64 da, {%1, %2};\n\t"
+            "mov.b64 db, {%3, %4};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo),
+            "r"(b_hi), "r"(idesc), "n"(ACC) : "memory");
+    }
+}
+// Arrive on `bar` (of both blocks of a pair) once the products issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (CG == 1) {
+        umma_commit(bar);
+    } else {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                     "h"(uint16_t(3)) : "memory");
+    }
+}
+
 struct GemmParams {
     int32_t K, cols;            // contraction and output columns
     int32_t n_tiles, n_tiles_n, k_blocks;
     int32_t out_v8;             // 1: output rows allow 32-byte stores
+    int32_t t_rows;             // rows of t
     const uint16_t* t;          // pairs of t (u), [block][128][padded rank]
     uint16_t* out;
 };
@@ -340,11 +426,18 @@ __device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& 
 // first is scaled (HD^-0.5 is no power of two for every HD): the epilogue
 // takes the scaled q sums into registers while the rest accumulates, which
 // frees that accumulator for the next tile.
-template <bool BWD>
+// CG 2: pairs of blocks on tiles of 256 x 256, each bringing in half of B. At
+// C = 512 what bounds the product is the 49 bytes a cycle that an SM takes in
+// from L2: 96 bytes of operands for each of its 128 x 256 x 1 products alone,
+// 64 in a pair.
+template <bool BWD, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
           const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_l,
           const __grid_constant__ LoraParams p, const __grid_constant__ GemmParams q) {
+    using S = Shape<CG>;
+    constexpr int kStages = S::kStages, A_TILE = S::A_TILE, STAGE = S::STAGE, BN = S::BN;
+    constexpr int B_FULL = S::B_FULL, B_EMPTY = S::B_EMPTY, B_AFULL = S::B_AFULL, B_AEMPTY = S::B_AEMPTY, B_DRAIN = S::B_DRAIN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -352,10 +445,11 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rp = padded_rank(p.R), rb = rp < 64 ? rp : 64;   // an adapter's columns, and a block's
 
-    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(base_ptr + OFF_MISC);
-    Sync sy{base + OFF_BAR, misc + 1};
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(base_ptr + S::OFF_MISC);
+    Sync sy{base + S::OFF_BAR, misc + 1};
+    const int rank = CG == 2 ? int(cluster_rank()) : 0, unit = blockIdx.x / CG, units = gridDim.x / CG;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NBAR; ++i) mbar_init(sy.bar(i), (i >= B_AEMPTY && i < B_AEMPTY + 2) ? 256u : 1u);
+        for (int i = 0; i < S::NBAR; ++i) mbar_init(sy.bar(i), (i >= B_AEMPTY && i < B_AEMPTY + 2) ? 256u * CG : 1u);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -366,11 +460,18 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         tma_prefetch_desc(&tm_l);
     }
     if (warp == 9) {
-        tmem_alloc(base + OFF_MISC, 512);
-        tmem_relinquish();
+        if (CG == 1) {
+            tmem_alloc(base + S::OFF_MISC, 512);
+            tmem_relinquish();
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + S::OFF_MISC), "r"(512)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();   // both blocks' barriers are there
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
@@ -378,49 +479,52 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         // ---------------------------------------------------------- producer
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < q.n_tiles; t += gridDim.x) {
-            const int i = t / q.n_tiles_n, m0 = i * kBM, n0 = (t % q.n_tiles_n) * kBN;
+        for (int t = unit; ok && t < q.n_tiles; t += units) {
+            const int i = t / q.n_tiles_n * CG + rank, m0 = i * kBM, span0 = m0 - rank * kBM;
+            const int n0 = (t % q.n_tiles_n) * kBN + rank * BN;   // of this block's part of B
             for (int kb = 0; kb < q.k_blocks; ++kb, ++it) {
                 const uint32_t st = it % kStages, to = base + st * STAGE;
                 if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
-                const uint32_t full = sy.bar(B_FULL + st);
-                mbar_arrive_expect_tx(full, STAGE);
-                tma_load_2d(to, &tm_a, full, kb * kBK, m0);
+                const uint32_t full = CG == 2 ? leaders(sy.bar(B_FULL + st)) : sy.bar(B_FULL + st);
+                if (rank == 0) mbar_arrive_expect_tx(sy.bar(B_FULL + st), STAGE * CG);
+                load_2d<CG>(to, &tm_a, full, kb * kBK, m0);
                 if (!BWD) {
-                    tma_load_2d(to + A_TILE, &tm_b, full, kb * kBK, n0);
+                    load_2d<CG>(to + A_TILE, &tm_b, full, kb * kBK, n0);
                 } else {
-                    for (int c = 0; c < 4; ++c)
-                        tma_load_2d(to + A_TILE + c * (kBK * 128), &tm_b, full, n0 + c * 64, kb * kBK);
+                    for (int c = 0; c < BN / 64; ++c)
+                        load_2d<CG>(to + A_TILE + c * (kBK * 128), &tm_b, full, n0 + c * 64, kb * kBK);
                 }
             }
-            Walk w;
-            w.start(p, m0);
+            WalkOf<kBM * CG> w;
+            w.start(p, span0);
             if (w.more(p)) wait_for_primary();   // t
-            for (; ok && w.more(p); w.next(p, m0))
+            for (; ok && w.more(p); w.next(p, span0))
                 for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
                     const uint32_t st = it % kStages, to = base + st * STAGE;
                     if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
-                    const uint32_t full = sy.bar(B_FULL + st);
-                    mbar_arrive_expect_tx(full, (kBM + kBN) * rb * 2);
-                    tma_load_2d(to, &tm_t, full, r0, (i + w.r) * kBM);
+                    const uint32_t full = CG == 2 ? leaders(sy.bar(B_FULL + st)) : sy.bar(B_FULL + st);
+                    if (rank == 0) mbar_arrive_expect_tx(sy.bar(B_FULL + st), (kBM + BN) * rb * 2 * CG);
+                    // the other block's request: zeros (rows past the tensor) for this one
+                    const bool mine = w.lo < m0 + kBM && w.hi > m0;
+                    load_2d<CG>(to, &tm_t, full, r0, mine ? (i + w.r) * kBM : q.t_rows);
                     if (!BWD) {
-                        tma_load_2d(to + A_TILE, &tm_l, full, r0, w.a * p.N + n0);
+                        load_2d<CG>(to + A_TILE, &tm_l, full, r0, w.a * p.N + n0);
                     } else {
-                        for (int c = 0; c < 4; ++c)
-                            tma_load_3d(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
+                        for (int c = 0; c < BN / 64; ++c)
+                            load_3d<CG>(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
                     }
                 }
         }
         wait_for_primary();
-        // every issued load lands before the CTA may exit
-        for (uint32_t s = 0; s < kStages; ++s) {
+        // every issued load lands before the CTA may exit (the pair's end waits for the leader)
+        for (uint32_t s = 0; rank == 0 && s < kStages; ++s) {
             const uint32_t f = it / kStages + (s < it % kStages ? 1u : 0u);
             if (f && !mbar_wait_bounded(sy.bar(B_FULL + s), (f - 1u) & 1u, kDrainLimitNs))
                 atomicOr(&g_lora_timeout_flag, 1u);
         }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9 && lane == 0 && rank == 0) {
         // ---------------------------------------------------------- MMA issuer
-        const uint32_t idesc = make_idesc_bf16(kBM, kBN, 0, BWD ? 1 : 0);
+        const uint32_t idesc = make_idesc_bf16(kBM * CG, kBN, 0, BWD ? 1 : 0);
         const uint64_t ad0 = make_smem_desc(base, 16, 1024, kSwizzle128B);
         // BWD: columns outermost in memory (MN-major), 64 to a region of kBK rows
         const uint64_t bd0 = make_smem_desc(base + A_TILE, BWD ? kBK * 128 : 16, 1024, kSwizzle128B);
@@ -433,8 +537,8 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         constexpr uint32_t b_step = BWD ? (16 * 128) >> 4 : 2;   // 16 of the contraction further
         uint32_t it = 0, lt = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < q.n_tiles; t += gridDim.x, ++lt) {
-            const int m0 = (t / q.n_tiles_n) * kBM;
+        for (int t = unit; ok && t < q.n_tiles; t += units, ++lt) {
+            const int m0 = (t / q.n_tiles_n) * kBM * CG;
             // FWD: this tile's accumulator; BWD: 0, then 1 behind the q block
             uint32_t buf = BWD ? 0u : lt & 1u;
             if (!sy.wait(sy.bar(B_AEMPTY + buf), ((BWD ? lt : lt >> 1) & 1u) ^ 1u)) break;
@@ -449,21 +553,21 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     if (BWD && buf == 0 && kb * kBK + kk * 16 >= p.Nq) {
-                        umma_commit(sy.bar(B_AFULL));
+                        commit<CG>(sy.bar(B_AFULL));
                         buf = 1;
                         if (!sy.wait(sy.bar(B_AEMPTY + 1), (lt & 1u) ^ 1u)) { ok = false; break; }
                         tc_fence_after();
                         d = tmem + kBN;
                         fresh = true;
                     }
-                    if (fresh) umma_ss_halves<0>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
-                    else umma_ss_halves<1>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
+                    if (fresh) umma<CG, 0>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
+                    else umma<CG, 1>(d, a_lo + kk * 2, a_hi, b_lo + kk * b_step, b_hi, idesc);
                     fresh = false;
                 }
                 if (!ok) break;
-                umma_commit(sy.bar(B_EMPTY + st));
+                commit<CG>(sy.bar(B_EMPTY + st));
             }
-            Walk w;
+            WalkOf<kBM * CG> w;
             for (w.start(p, m0); ok && w.more(p); w.next(p, m0))
                 for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
                     const uint32_t st = it % kStages;
@@ -471,13 +575,13 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                     tc_fence_after();
                     const uint32_t a_lo = uint32_t(td0) + ((st * STAGE) >> 4), b_lo = uint32_t(ld0) + ((st * STAGE) >> 4);
                     for (int kk = 0; kk < rb / 16; ++kk)
-                        umma_ss_halves<1>(d, a_lo + kk * 2, t_hi, b_lo + kk * b_step, l_hi, idesc);
-                    umma_commit(sy.bar(B_EMPTY + st));
+                        umma<CG, 1>(d, a_lo + kk * 2, t_hi, b_lo + kk * b_step, l_hi, idesc);
+                    commit<CG>(sy.bar(B_EMPTY + st));
                 }
             if (!ok) break;
-            umma_commit(sy.bar(B_AFULL + buf));
+            commit<CG>(sy.bar(B_AFULL + buf));
         }
-        umma_commit(sy.bar(B_DRAIN));
+        commit<CG>(sy.bar(B_DRAIN));
         if (!mbar_wait_bounded(sy.bar(B_DRAIN), 0, kDrainLimitNs)) atomicOr(&g_lora_timeout_flag, 1u);
     } else if (warp < 8) {
         // ---------------------------------------------------------- epilogue
@@ -485,10 +589,10 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         dependents_may_start();   // who reads t and u too
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + half * 128;
-        float* bias_s = reinterpret_cast<float*>(base_ptr + OFF_BIAS) + warp * 128;   // this warp's copy
+        float* bias_s = reinterpret_cast<float*>(base_ptr + S::OFF_BIAS) + warp * 128;   // this warp's copy
         uint32_t lt = 0;
-        for (int t = blockIdx.x; t < q.n_tiles; t += gridDim.x, ++lt) {
-            const int m0 = (t / q.n_tiles_n) * kBM, n0 = (t % q.n_tiles_n) * kBN + half * 128;
+        for (int t = unit; t < q.n_tiles; t += units, ++lt) {
+            const int m0 = ((t / q.n_tiles_n) * CG + rank) * kBM, n0 = (t % q.n_tiles_n) * kBN + half * 128;
             const int row = m0 + quad * 32 + lane;
             uint16_t* orow = q.out + int64_t(row) * q.cols;
             if (!BWD) {
@@ -501,9 +605,10 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 __syncwarp();
             }
             // does the tile hold rows of more than one request?
-            Walk w;
-            w.start(p, m0);
-            const bool shared = w.more(p) && (w.lo > m0 || w.hi < min(m0 + kBM, p.M));
+            const int span0 = m0 - rank * kBM;
+            WalkOf<kBM * CG> w;
+            w.start(p, span0);
+            const bool shared = w.more(p) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M));
             float held[BWD ? 128 : 1];   // BWD: the scaled sums of the q block
             if (BWD) {
                 if (!sy.wait(sy.bar(B_AFULL), lt & 1u)) break;
@@ -512,7 +617,8 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 for (int c = 0; c < 4; ++c) tmem_ld32(t_row + 32 * c, held + (BWD ? 32 * c : 0));
                 tmem_wait_ld();
                 tc_fence_before();
-                mbar_arrive(sy.bar(B_AEMPTY));
+                if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY)));
+                else mbar_arrive(sy.bar(B_AEMPTY));
             }
             const uint32_t buf = BWD ? 1u : lt & 1u;
             if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
@@ -571,15 +677,18 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
             }
             __syncwarp();   // the bias copy is rewritten for the next tile
             tc_fence_before();
-            mbar_arrive(sy.bar(B_AEMPTY + buf));
+            if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + buf)));
+            else mbar_arrive(sy.bar(B_AEMPTY + buf));
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();   // no block ends while the other may still reach its memory
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if (CG == 1) tmem_dealloc(tmem, 512);
+        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -935,17 +1044,21 @@ bool map_of(CUtensorMap* m, const void* ptr, int dims, const int64_t* size, cons
 // A launch that may start while the kernel before it, which lets it, still
 // runs; it waits for that kernel itself where it reads its results.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, int smem, cudaStream_t stream, const A&... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, int smem, cudaStream_t stream, int cluster,
+                             const A&... args) {
     cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute a = {};
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute a[2] = {};
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    a[1].id = cudaLaunchAttributeClusterDimension;
+    a[1].val.clusterDim.x = unsigned(cluster);
+    a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
     c.gridDim = grid;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = stream;
-    c.attrs = &a;
-    c.numAttrs = 1;
+    c.attrs = a;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
@@ -961,7 +1074,7 @@ cudaError_t down_t(const LoraParams& p, uint16_t* t, uint16_t* u, cudaStream_t s
         if (e != cudaSuccess) return e;
     }
     const unsigned grid = unsigned(ceil_div(p.M, 128) * 128 / RT);
-    if (u) return launch_dependent(lora_down_both<RP, RT>, dim3(grid, 2), 128, smem, stream, p, t, u);
+    if (u) return launch_dependent(lora_down_both<RP, RT>, dim3(grid, 2), 128, smem, stream, 1, p, t, u);
     lora_down<RP, RT><<<grid, 128, smem, stream>>>(p, t);
     return cudaGetLastError();
 }
@@ -977,13 +1090,13 @@ cudaError_t down(const LoraParams& p, uint16_t* t, uint16_t* u, int sms, cudaStr
     }
 }
 
-template <bool BWD>
-cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
+template <bool BWD, int CG>
+cudaError_t gemm_t(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
     GemmParams q{};
     q.K = BWD ? p.N : p.C;
     q.cols = BWD ? p.C : p.N;
     q.n_tiles_n = int32_t(ceil_div(q.cols, kBN));
-    const int64_t tiles = ceil_div(p.M, kBM) * q.n_tiles_n;
+    const int64_t tiles = ceil_div(p.M, kBM * CG) * q.n_tiles_n;
     if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     q.n_tiles = int32_t(tiles);
     q.k_blocks = int32_t(ceil_div(q.K, kBK));
@@ -993,18 +1106,28 @@ cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t s
     const int rp = padded_rank(p.R), rb = rp < 64 ? rp : 64;
     CUtensorMap ta, tb, tt, tl;
     const int64_t blocks = (ceil_div(p.M, 128) + p.n_req) * 128;
+    q.t_rows = int32_t(blocks);
     const int64_t sa[2] = {q.K, p.M}, ka[1] = {q.K}, st[2] = {rp, blocks}, kt[1] = {rp};
     const int64_t sw[2] = {p.C, p.N}, kw[1] = {p.C};
     const int64_t sb[2] = {p.R, int64_t(p.n_ad) * p.N}, kb[1] = {p.R};
     const int64_t sl[3] = {p.C, p.R, p.n_ad}, kl[2] = {p.C, int64_t(p.R) * p.C};
     bool ok = map_of(&ta, BWD ? p.dqkv : p.x, 2, sa, ka, 64, kBM) && map_of(&tt, t, 2, st, kt, rb, kBM);
     if (BWD) ok = ok && map_of(&tb, p.w, 2, sw, kw, 64, kBK) && map_of(&tl, p.a, 3, sl, kl, 64, rb);
-    else ok = ok && map_of(&tb, p.w, 2, sw, kw, 64, kBN) && map_of(&tl, p.b, 2, sb, kb, rb, kBN);
+    else ok = ok && map_of(&tb, p.w, 2, sw, kw, 64, Shape<CG>::BN) && map_of(&tl, p.b, 2, sb, kb, rb, Shape<CG>::BN);
     if (!ok) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(lora_gemm<BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC);
+    const cudaError_t e =
+        cudaFuncSetAttribute(lora_gemm<BWD, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<CG>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_dependent(lora_gemm<BWD>, dim3(unsigned(tiles < sms ? tiles : sms)), kThreads, SMEM_ALLOC, stream, ta, tb, tt, tl,
-                            p, q);
+    const int64_t units = sms / CG;
+    return launch_dependent(lora_gemm<BWD, CG>, dim3(unsigned((tiles < units ? tiles : units) * CG)), kThreads, Shape<CG>::SMEM,
+                            stream, CG, ta, tb, tt, tl, p, q);
+}
+
+template <bool BWD>
+cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
+    // pairs where there is a tile of 256 rows for each
+    const int64_t tiles = (p.M / (2 * kBM)) * ceil_div(BWD ? p.C : p.N, kBN);
+    return tiles >= sms / 2 ? gemm_t<BWD, 2>(p, t, sms, stream) : gemm_t<BWD, 1>(p, t, sms, stream);
 }
 
 template <int RP>
@@ -1014,10 +1137,10 @@ cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const ui
     if (e != cudaSuccess) return e;
     const int splits = grad_splits(p.M, p.C, p.N);
     const dim3 grid(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits));
-    e = launch_dependent(lora_grad<RP>, grid, 256, smem, stream, p, q, t, u, part, splits, p.dx != nullptr);
+    e = launch_dependent(lora_grad<RP>, grid, 256, smem, stream, 1, p, q, t, u, part, splits, p.dx != nullptr);
     if (e != cudaSuccess) return e;
     const int64_t n = int64_t(p.n_ad) * p.R * (int64_t(p.C) + p.N);
-    return launch_dependent(lora_grad_sum, dim3(unsigned(ceil_div(n, 256))), 256, 0, stream, p, q, part, splits, RP);
+    return launch_dependent(lora_grad_sum, dim3(unsigned(ceil_div(n, 256))), 256, 0, stream, 1, p, q, part, splits, RP);
 }
 
 }  // namespace
@@ -1033,9 +1156,9 @@ cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         const dim3 grid(unsigned(p.N / 16));
-        if (p.M <= 8) return launch_dependent(lora_fwd_few<1>, grid, 256, 0, stream, p, t);
-        if (p.M <= 16) return launch_dependent(lora_fwd_few<2>, grid, 256, 0, stream, p, t);
-        return launch_dependent(lora_fwd_few<4>, grid, 256, 0, stream, p, t);
+        if (p.M <= 8) return launch_dependent(lora_fwd_few<1>, grid, 256, 0, stream, 1, p, t);
+        if (p.M <= 16) return launch_dependent(lora_fwd_few<2>, grid, 256, 0, stream, 1, p, t);
+        return launch_dependent(lora_fwd_few<4>, grid, 256, 0, stream, 1, p, t);
     }
     const cudaError_t e = down(p, t, nullptr, sms, stream);
     return e != cudaSuccess ? e : gemm<false>(p, t, sms, stream);

@@ -55,6 +55,10 @@ CASES = [
     (777, 256, 4, 128, 16, 2, (0, 300, 777), (1, 1)),                  # one adapter throughout
     (1000, 1032, 1, 64, 72, 3, (10, 20, 500, 990), (0, -1, 2)),
     (2500, 520, 3, 32, 32, 4, (0, 1000, 1001, 2499, 2500), (2, 3, 0, 2)),
+    # enough rows for tiles of 256 by pairs of blocks
+    (20045, 72, 3, 32, 24, 3, (5, 100, 300, 384, 9001, 20000), (0, 2, 1, 0, 2)),
+    (20045, 264, 2, 16, 128, 2, (0, 10000, 20045), (1, 0)),
+    (19456, 328, 1, 128, 64, 1, (0, 19456), (0,)),
 ]
 
 
@@ -97,19 +101,21 @@ def test_without_adapters_it_is_the_base_projection():
     assert bool((got["da"] == 0).all()) and bool((got["db"] == 0).all())
 
 
-def test_requests_do_not_reach_one_another():
+@pytest.mark.parametrize("M", [6, 150, 20000])
+def test_requests_do_not_reach_one_another(M):
     """A request's rows are what they are by themselves whatever the other
     requests, their adapters included, hold."""
-    M, C, NH, HD = 150, 128, 2, 64
+    C, NH, HD = 128, 2, 64
     t, g = make(M, C, NH, HD, 16, 2, 2)
-    off, ad = ints(0, 50, 100, 150), ints(0, 1, 0)
+    cuts = (0, 2, 4, 6) if M == 6 else (0, 50, 100, M)
+    off, ad = ints(*cuts), ints(0, 1, 0)
     clean = run(t, g, off, ad, NH, HD)
     want = ref.lora(**t, offsets=off, adapter=ad, HD=HD, dqkv=g)
-    t["x"][50:100] = float("nan")
+    t["x"][cuts[1]:cuts[2]] = float("nan")
     t["lora_a"][1] = float("nan")
     t["lora_b"][1] = float("inf")
     got = run(t, g, off, ad, NH, HD)
-    for rows in (slice(0, 50), slice(100, 150)):
+    for rows in (slice(0, cuts[1]), slice(cuts[2], M)):
         for name in ("qkv", "dx"):
             value, bound = want[name]
             ref.check(name, got[name][rows], (value[rows], bound[rows]))
