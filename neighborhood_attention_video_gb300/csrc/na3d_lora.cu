@@ -34,15 +34,34 @@ __device__ __forceinline__ uint16_t b16(float f) { return __bfloat16_as_ushort(_
 
 // ------------------------------------------------------------------ requests
 
+struct Requests {
+    const int32_t *offsets, *adapter;
+    int n_req, n_ad;
+};
+
+__device__ __forceinline__ Requests requests_of(const LoraParams& p) { return {p.offsets, p.adapter, p.n_req, p.n_ad}; }
+
 // The first request that ends behind row m (n_req where none does).
-__device__ __forceinline__ int first_request(const LoraParams& p, int m) {
-    int lo = 0, hi = p.n_req;
+__device__ __forceinline__ int first_request(const Requests& q, int m) {
+    int lo = 0, hi = q.n_req;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (p.offsets[mid + 1] > m) hi = mid;
+        if (q.offsets[mid + 1] > m) hi = mid;
         else lo = mid + 1;
     }
     return lo;
+}
+
+// The same by a whole warp, which reads 32 offsets at a time: one trip to
+// memory for few requests.
+__device__ __forceinline__ int first_request_warp(const Requests& q, int m) {
+    if (q.n_req > 256) return first_request(q, m);
+    const int lane = threadIdx.x & 31;
+    for (int r = 0; r < q.n_req; r += 32) {
+        const uint32_t behind = __ballot_sync(0xffffffffu, r + lane < q.n_req && q.offsets[r + lane + 1] > m);
+        if (behind) return r + __ffs(behind) - 1;
+    }
+    return q.n_req;
 }
 
 // The requests with an adapter that meet rows [m0, m0 + SPAN), in order. Every
@@ -50,21 +69,25 @@ __device__ __forceinline__ int first_request(const LoraParams& p, int m) {
 template <int SPAN>
 struct WalkOf {
     int r, a, lo, hi;   // request, its adapter, its rows
-    __device__ __forceinline__ void start(const LoraParams& p, int m0) {
-        r = first_request(p, m0) - 1;
-        next(p, m0);
+    __device__ __forceinline__ void start(const Requests& q, int m0) {
+        r = first_request(q, m0) - 1;
+        next(q, m0);
     }
-    __device__ __forceinline__ void next(const LoraParams& p, int m0) {
-        for (++r; r < p.n_req; ++r) {
-            lo = p.offsets[r];
+    __device__ __forceinline__ void start_warp(const Requests& q, int m0) {
+        r = first_request_warp(q, m0) - 1;
+        next(q, m0);
+    }
+    __device__ __forceinline__ void next(const Requests& q, int m0) {
+        for (++r; r < q.n_req; ++r) {
+            lo = q.offsets[r];
+            hi = q.offsets[r + 1];
+            a = q.adapter[r];
             if (lo >= m0 + SPAN) break;
-            hi = p.offsets[r + 1];
-            a = p.adapter[r];
-            if (hi > lo && hi > m0 && a >= 0 && a < p.n_ad) return;
+            if (hi > lo && hi > m0 && a >= 0 && a < q.n_ad) return;
         }
-        r = p.n_req;
+        r = q.n_req;
     }
-    __device__ __forceinline__ bool more(const LoraParams& p) const { return r < p.n_req; }
+    __device__ __forceinline__ bool more(const Requests& q) const { return r < q.n_req; }
 };
 using Walk = WalkOf<128>;
 
@@ -128,8 +151,9 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, uint16_t* out) {
     const uint16_t* const src = BWD ? p.dqkv : p.x;
     const int g = lane >> 2, c2 = lane & 3;
 
+    const Requests rq = requests_of(p);
     Walk w;
-    for (w.start(p, m0); w.more(p); w.next(p, m0)) {
+    for (w.start_warp(rq, m0); w.more(rq); w.next(rq, m0)) {
         uint16_t* const to = out + ((int64_t(m0 >> 7) + w.r) * 128 + (m_first & 127)) * RP;
         const int lo = max(w.lo, m_first), hi = min(min(w.hi, p.M), m_first + RT);   // rows of this block
         if (lo >= hi) {
@@ -257,6 +281,11 @@ __global__ void __launch_bounds__(128) lora_down_both(const LoraParams p, uint16
 constexpr int kBM = 128, kBN = 256, kBK = 64;
 constexpr int kThreads = 320;   // eight epilogue warps, a loading and an issuing one
 
+// As many requests are kept in shared memory: each role of a block walks them
+// for each tile, and trips to memory for the offsets would hold up its loads
+// (103 -> 95 us at 65536 x 512 x 1536).
+constexpr int kFewRequests = 1024;
+
 // Shared memory of a block, alone (CG 1) or one of a pair (CG 2): each block of
 // a pair holds its own 128 rows of A and half of the columns of B.
 template <int CG>
@@ -269,7 +298,8 @@ struct Shape {
                          B_DRAIN = B_AEMPTY + 2, NBAR = B_DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int OFF_BIAS = (OFF_MISC + 16 + 15) & ~15;   // a tile's bias, fp32, for each epilogue warp its columns
-    static constexpr int SMEM = OFF_BIAS + 8 * 128 * 4 + 1024;
+    static constexpr int OFF_REQ = OFF_BIAS + 8 * 128 * 4;        // the requests, where they are few
+    static constexpr int SMEM = OFF_REQ + (2 * kFewRequests + 1) * 4 + 1024;
 };
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 500000000ull;
@@ -403,8 +433,9 @@ __device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& 
         }
         s += sq;
     }
+    const Requests rq = requests_of(p);
     Walk w;
-    for (w.start(p, m & ~127); w.more(p); w.next(p, m & ~127)) {
+    for (w.start(rq, m & ~127); w.more(rq); w.next(rq, m & ~127)) {
         if (m < w.lo || m >= w.hi) continue;
         const uint16_t* t = q.t + ((int64_t(m >> 7) + w.r) * 128 + (m & 127)) * rp;
         for (int r = 0; r < p.R; ++r)
@@ -453,6 +484,14 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         misc[1] = 0u;
         fence_mbar_init();
     }
+    Requests rq = requests_of(p);
+    if (p.n_req <= kFewRequests) {
+        int32_t* const kept = reinterpret_cast<int32_t*>(base_ptr + S::OFF_REQ);
+        for (int r = threadIdx.x; r <= p.n_req; r += kThreads) kept[r] = p.offsets[r];
+        for (int r = threadIdx.x; r < p.n_req; r += kThreads) kept[kFewRequests + 1 + r] = p.adapter[r];
+        rq.offsets = kept;
+        rq.adapter = kept + kFewRequests + 1;
+    }
     if (warp == 8 && lane == 0) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
@@ -496,9 +535,9 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 }
             }
             WalkOf<kBM * CG> w;
-            w.start(p, span0);
-            if (w.more(p)) wait_for_primary();   // t
-            for (; ok && w.more(p); w.next(p, span0))
+            w.start(rq, span0);
+            if (w.more(rq)) wait_for_primary();   // t
+            for (; ok && w.more(rq); w.next(rq, span0))
                 for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
                     const uint32_t st = it % kStages, to = base + st * STAGE;
                     if (!sy.wait(sy.bar(B_EMPTY + st), ((it / kStages) & 1u) ^ 1u)) { ok = false; break; }
@@ -568,7 +607,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 commit<CG>(sy.bar(B_EMPTY + st));
             }
             WalkOf<kBM * CG> w;
-            for (w.start(p, m0); ok && w.more(p); w.next(p, m0))
+            for (w.start(rq, m0); ok && w.more(rq); w.next(rq, m0))
                 for (int r0 = 0; r0 < rp; r0 += rb, ++it) {
                     const uint32_t st = it % kStages;
                     if (!sy.wait(sy.bar(B_FULL + st), (it / kStages) & 1u)) { ok = false; break; }
@@ -607,8 +646,8 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
             // does the tile hold rows of more than one request?
             const int span0 = m0 - rank * kBM;
             WalkOf<kBM * CG> w;
-            w.start(p, span0);
-            const bool shared = w.more(p) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M));
+            w.start(rq, span0);
+            const bool shared = w.more(rq) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M));
             float held[BWD ? 128 : 1];   // BWD: the scaled sums of the q block
             if (BWD) {
                 if (!sy.wait(sy.bar(B_AFULL), lt & 1u)) break;
@@ -700,9 +739,10 @@ constexpr int kSmallRows = 32;   // up to here the product streams W past the ro
 __global__ void __launch_bounds__(256) lora_down_few(const LoraParams p, uint16_t* t) {
     dependents_may_start();
     const int m = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Requests rq = requests_of(p);
     Walk w;
-    for (w.start(p, 0); w.more(p) && w.hi <= m; w.next(p, 0)) {}
-    if (!w.more(p) || w.lo > m) return;   // nothing reads this row's
+    for (w.start_warp(rq, m); w.more(rq) && w.hi <= m; w.next(rq, m)) {}
+    if (!w.more(rq) || w.lo > m) return;   // nothing reads this row's
     const uint4* x = reinterpret_cast<const uint4*>(p.x + int64_t(m) * p.C);
     const uint4* a = reinterpret_cast<const uint4*>(p.a + (int64_t(w.a) * p.R + r) * p.C);
     float s = 0.f;
@@ -730,10 +770,18 @@ template <int MT>
 __global__ void __launch_bounds__(256) lora_fwd_few(const LoraParams p, const uint16_t* t) {
     constexpr int U = MT <= 2 ? 4 : 2;   // blocks of 32 channels in flight
     __shared__ float part[8][16][8 * MT + 1];
+    __shared__ int row_adapter[8 * MT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c2 = lane & 3;
     const int n0 = blockIdx.x * 16;   // N is a multiple of 16
     const uint16_t* const w0 = p.w + int64_t(n0 + g) * p.C;
     const uint16_t* const w1 = w0 + int64_t(8) * p.C;
+    if (int(threadIdx.x) < p.M) {   // one row's adapter, -1 for none
+        const Requests rq = requests_of(p);
+        const int m = threadIdx.x;
+        Walk w;
+        w.start(rq, m);
+        row_adapter[m] = w.more(rq) && w.lo <= m ? w.a : -1;
+    }
     const uint4 zero = make_uint4(0, 0, 0, 0);
     float acc[MT][4] = {};
     const int blocks = (p.C + 31) / 32;
@@ -771,10 +819,9 @@ __global__ void __launch_bounds__(256) lora_fwd_few(const LoraParams p, const ui
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += part[i][n][m];
         if (p.bias) s += f32(p.bias[col]);
-        Walk w;
-        for (w.start(p, 0); w.more(p) && w.hi <= m; w.next(p, 0)) {}
-        if (w.more(p) && w.lo <= m) {
-            const uint4* b = reinterpret_cast<const uint4*>(p.b + (int64_t(w.a) * p.N + col) * p.R);
+        const int a = row_adapter[m];
+        if (a >= 0) {
+            const uint4* b = reinterpret_cast<const uint4*>(p.b + (int64_t(a) * p.N + col) * p.R);
             const uint4* tm = reinterpret_cast<const uint4*>(t + m * p.R);
             for (int i = 0; i < p.R / 8; ++i) {
                 const uint4 u = b[i], v = tm[i];
