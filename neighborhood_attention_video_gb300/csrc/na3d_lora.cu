@@ -629,25 +629,27 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t t_row = tmem + (uint32_t(quad * 32) << 16) + half * 128;
         float* bias_s = reinterpret_cast<float*>(base_ptr + S::OFF_BIAS) + warp * 128;   // this warp's copy
+        // the bias of a tile's columns (0 past N or without bias), read a tile ahead
+        float bias_r[4];
+        auto read_bias = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = (t % q.n_tiles_n) * kBN + half * 128 + 32 * i + lane;
+                bias_r[i] = (p.bias && t < q.n_tiles && c < p.N) ? f32(p.bias[c]) : 0.f;
+            }
+        };
+        if (!BWD) read_bias(unit);
         uint32_t lt = 0;
         for (int t = unit; t < q.n_tiles; t += units, ++lt) {
             const int m0 = ((t / q.n_tiles_n) * CG + rank) * kBM, n0 = (t % q.n_tiles_n) * kBN + half * 128;
             const int row = m0 + quad * 32 + lane;
             uint16_t* orow = q.out + int64_t(row) * q.cols;
             if (!BWD) {
-                // the columns' bias (0 past N or without bias), one coalesced pass
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = n0 + 32 * i + lane;
-                    bias_s[32 * i + lane] = (p.bias && c < p.N) ? f32(p.bias[c]) : 0.f;
-                }
+                for (int i = 0; i < 4; ++i) bias_s[32 * i + lane] = bias_r[i];
                 __syncwarp();
+                read_bias(t + units);
             }
-            // does the tile hold rows of more than one request?
-            const int span0 = m0 - rank * kBM;
-            WalkOf<kBM * CG> w;
-            w.start(rq, span0);
-            const bool shared = w.more(rq) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M));
             float held[BWD ? 128 : 1];   // BWD: the scaled sums of the q block
             if (BWD) {
                 if (!sy.wait(sy.bar(B_AFULL), lt & 1u)) break;
@@ -662,62 +664,73 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
             const uint32_t buf = BWD ? 1u : lt & 1u;
             if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
             tc_fence_after();
+            constexpr int W = BWD ? 32 : 64;   // columns at a time
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int c0 = n0 + 32 * c;
-                if (c0 >= q.cols) break;   // ragged last tile (uniform over the warp)
-                float acc[32];
-                tmem_ld32(t_row + buf * kBN + 32 * c, acc);
+            for (int c = 0; c < 128 / W; ++c) {
+                const int c0 = n0 + W * c;
+                float acc[W];
+                if (BWD) tmem_ld32(t_row + buf * kBN + W * c, acc);
+                else tmem_ld64(t_row + buf * kBN + W * c, acc);
                 tmem_wait_ld();
+                if (c == 128 / W - 1) {   // the accumulator is read
+                    tc_fence_before();
+                    if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + buf)));
+                    else mbar_arrive(sy.bar(B_AEMPTY + buf));
+                }
+                if (c0 >= q.cols || row >= p.M) continue;
                 if (BWD) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
+                    for (int j = 0; j < W; ++j) acc[j] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
                 }
-                if (shared) {
-                    float probe = 0.f;
+                float top = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) probe = fmaf(acc[j], 0.f, probe);
-                    if (probe != 0.f && row < p.M)
+                for (int j = 0; j < W; j += 2)
+                    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(acc[j])), "f"(fabsf(acc[j + 1])));
+                if (!(top < INFINITY)) {
+                    // where the tile holds rows of more than one request, the value may be another's
+                    const int span0 = m0 - rank * kBM;
+                    WalkOf<kBM * CG> w;
+                    w.start(rq, span0);
+                    if (w.more(rq) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M)))
 #pragma unroll 1
-                        for (int j = 0; j < 32 && c0 + j < q.cols; ++j) {
+                        for (int j = 0; j < W && c0 + j < q.cols; ++j) {
                             const float x = lone_value<BWD>(p, q, row, c0 + j);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
+                            for (int k = 0; k < W; ++k)
                                 if (k == j) acc[k] = x;
                         }
                 }
-                uint32_t pk[16];
+                uint32_t pk[W / 2];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float v0 = acc[2 * j], v1 = acc[2 * j + 1];
+                for (int j = 0; j < W / 2; j += 2) {
+                    float v[4] = {acc[2 * j], acc[2 * j + 1], acc[2 * j + 2], acc[2 * j + 3]};
                     if (!BWD) {
-                        const float2 b = *reinterpret_cast<const float2*>(bias_s + 32 * c + 2 * j);
-                        // the q block (columns below NH * HD) carries the HD^-0.5 scale
-                        v0 = (v0 + b.x) * (c0 + 2 * j < p.Nq ? p.q_scale : 1.f);
-                        v1 = (v1 + b.y) * (c0 + 2 * j + 1 < p.Nq ? p.q_scale : 1.f);
+                        const float4 b = *reinterpret_cast<const float4*>(bias_s + W * c + 2 * j);
+                        // the q block (columns below NH * HD, a multiple of 16) carries the HD^-0.5 scale
+                        const float by = c0 + (2 * j & ~15) < p.Nq ? p.q_scale : 1.f;
+                        v[0] = (v[0] + b.x) * by;
+                        v[1] = (v[1] + b.y) * by;
+                        v[2] = (v[2] + b.z) * by;
+                        v[3] = (v[3] + b.w) * by;
                     }
-                    pk[j] = pack_bf16x2(v0, v1);
+                    pk[j] = pack_bf16x2(v[0], v[1]);
+                    pk[j + 1] = pack_bf16x2(v[2], v[3]);
                 }
-                if (row < p.M) {
-                    const int nval = min(32, q.cols - c0);   // a multiple of 8
+                const int nval = min(W, q.cols - c0);   // a multiple of 8
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (q.out_v8 && 16 * i + 16 <= nval) {
-                            st_global_v8(orow + c0 + 16 * i, pk + 8 * i);
-                        } else {
+                for (int i = 0; i < W / 16; ++i) {
+                    if (q.out_v8 && 16 * i + 16 <= nval) {
+                        st_global_v8(orow + c0 + 16 * i, pk + 8 * i);
+                    } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (16 * i + 8 * h < nval)
-                                    *reinterpret_cast<uint4*>(orow + c0 + 16 * i + 8 * h) =
-                                        make_uint4(pk[8 * i + 4 * h], pk[8 * i + 4 * h + 1], pk[8 * i + 4 * h + 2], pk[8 * i + 4 * h + 3]);
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            if (16 * i + 8 * h < nval)
+                                *reinterpret_cast<uint4*>(orow + c0 + 16 * i + 8 * h) =
+                                    make_uint4(pk[8 * i + 4 * h], pk[8 * i + 4 * h + 1], pk[8 * i + 4 * h + 2], pk[8 * i + 4 * h + 3]);
                     }
                 }
             }
             __syncwarp();   // the bias copy is rewritten for the next tile
-            tc_fence_before();
-            if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + buf)));
-            else mbar_arrive(sy.bar(B_AEMPTY + buf));
         }
     }
 
