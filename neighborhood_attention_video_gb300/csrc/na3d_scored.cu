@@ -712,34 +712,43 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         const int in_chunk = g.nhc > 1 ? mine.x - cur.bh.x : 0;
         if ((biased && head != lut_head) || place_h != lut_h || place_w != lut_w || in_chunk != lut_chunk) {
             __syncwarp();
+            // a lane takes one row's place and, with others of the same, the columns in turn
+            const int places = use_lut ? n_hw : 16, r = lane & (places - 1), at_once = 32 / places;
+            const int lh = wh0 + ((r >> g.sw_log2) & (g.sh - 1)), lw = o.w0 + (r & (g.sw - 1));
+            const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
+            const int h_n = lh < p.H && lw < p.W ? range_hi(DKV, lh, p.KH, p.H) - h_lo : 0;
+            const int w_n = range_hi(DKV, lw, p.KW, p.W) - w_lo;
             int at_step = 0;
             for (int ih = 0; ih < g.nhc; ++ih)
                 for (int iw = 0; iw < g.nwc; ++iw) {
                     int hf, w;
-                    const int n = part_of(ih, iw, hf, w);
-                    for (int i0 = 0; i0 < n; i0 += 16, ++at_step) {
-                        const float2 at = hw[i0 + (lane & 15)];
-                        // this lane's column; one past the box is in no window
-                        const int h = i0 + (lane & 15) < n ? hf + int(at.x) : 1 << 30, x = w + int(at.y);
-                        // two rows' places at a time, one in each half of the warp (mask words: all
-                        // sixteen rows)
+                    const int n = part_of(ih, iw, hf, w), steps = n > 0 ? (n + 15) >> 4 : 0;
+                    if (use_lut) {
+                        float* const to = lut + r * g.lut_pitch + at_step * 16;
 #pragma unroll 4
-                        for (int r = hi; r < (use_lut ? n_hw : 16); r += 2) {
-                            const int lh = wh0 + ((r >> g.sw_log2) & (g.sh - 1)), lw = o.w0 + (r & (g.sw - 1));
-                            const int h_lo = range_lo(DKV, lh, p.KH, p.H), w_lo = range_lo(DKV, lw, p.KW, p.W);
-                            const bool in = lh < p.H && lw < p.W && h >= h_lo && x >= w_lo &&
-                                            h < range_hi(DKV, lh, p.KH, p.H) && x < range_hi(DKV, lw, p.KW, p.W);
-                            if (use_lut) {
-                                lut[r * g.lut_pitch + at_step * 16 + (lane & 15)] =
-                                    in ? fmaf(sl[1], float(abs(h - lh)), sl[2] * float(abs(x - lw))) : -INFINITY;
-                            } else {
-                                const uint32_t bits = __ballot_sync(0xffffffffu, in);
-                                if ((lane & 15) == 0)
-                                    reinterpret_cast<uint16_t*>(mask)[at_step * 16 + 2 * (r & 7) + (r >> 3)] =
-                                        uint16_t(hi ? bits >> 16 : bits & 0xffffu);
+                        for (int i = lane / places; i < steps * 16; i += at_once) {
+                            const float2 at = hw[i];
+                            const int y = hf + int(at.x), x = w + int(at.y);
+                            const bool in = i < n && uint32_t(y - h_lo) < uint32_t(h_n) && uint32_t(x - w_lo) < uint32_t(w_n);
+                            to[i] = in ? fmaf(sl[1], float(abs(y - lh)), sl[2] * float(abs(x - lw))) : -INFINITY;
+                        }
+                    } else {
+                        for (int k = 0; k < steps; ++k) {   // eight columns a lane, then both halves' together
+                            uint32_t bits = 0;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int i = 16 * k + 8 * hi + j;
+                                const float2 at = hw[i];
+                                const int y = hf + int(at.x), x = w + int(at.y);
+                                const bool in = i < n && uint32_t(y - h_lo) < uint32_t(h_n) && uint32_t(x - w_lo) < uint32_t(w_n);
+                                bits |= uint32_t(in) << (8 * hi + j);
                             }
+                            bits |= __shfl_xor_sync(0xffffffffu, bits, 16);
+                            if (hi == 0)
+                                reinterpret_cast<uint16_t*>(mask)[(at_step + k) * 16 + 2 * (r & 7) + (r >> 3)] = uint16_t(bits);
                         }
                     }
+                    at_step += steps;
                 }
             __syncwarp();
             lut_head = head;
@@ -975,6 +984,88 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             if (capped) run(integral_constant<bool, true>{});
                             else run(integral_constant<bool, false>{});
                         }
+                        n_steps = 0;
+                    }
+                    // ... and those of the backward passes, without a branch in a step
+                    if (MODE != kFwd && use_lut && !mixed && (!capped || to_log2 <= 96.f)) {
+                        uint32_t ak[KB];
+#pragma unroll
+                        for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
+                        auto plain = [&](auto cap_const) {
+                            constexpr bool CAP = decltype(cap_const)::value;
+                            float sc[8] = {}, dp[8] = {};
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) {
+                                uint32_t f[4], e[4], a[4];
+                                ldsm4(ak[kk], f);
+                                if (NFR < NF) ldsm4(f_at + f_bytes + swizzled<HD>(frag_row, 2 * kk + hi, f_region), a);
+                                ldsm4(ak[kk] + x_bytes, e);
+                                mma16816(sc, fa[0][kk], f[0], f[2]);
+                                mma16816(sc + 4, fa[0][kk], f[1], f[3]);
+                                mma16816(dp, NFR < NF ? a : fa[NFR - 1][kk], e[0], e[2]);
+                                mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], e[1], e[3]);
+                            }
+                            uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
+                            uint32_t pr[4], ds[4];   // probabilities and da, pairs: 2 * tile + row
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                uint64_t minus_ref = 0, minus_delta = 0;
+                                if (DKV) {
+                                    const float2 c0 = stat[8 * j + 2 * c2], c1 = stat[8 * j + 2 * c2 + 1];
+                                    minus_ref = f2_pack(-c0.x, -c1.x);
+                                    minus_delta = f2_pack(-c0.y, -c1.y);
+                                }
+                                const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 8 * j);
+                                const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 8 * j);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const int v = 4 * j + 2 * i;
+                                    uint64_t s = f2_add(i ? y : x, from[i]), slope = 0;
+                                    if (DKV) s = f2_add(s, minus_ref);
+                                    if (CAP) {
+                                        // with r = 1 / (1 + e^(2 a / c)): tanh = 1 - 2 r, its derivative 4 r (1 - r)
+                                        float e0, e1;
+                                        f2_unpack(f2_mul(f2_pack(sc[v], sc[v + 1]), f2_dup(exp_scale)), e0, e1);
+                                        f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);
+                                        const uint64_t r = f2_pack(rcp_approx(e0), rcp_approx(e1));
+                                        s = f2_fma(r, f2_dup(-2.f * to_log2), f2_add(s, f2_dup(to_log2)));
+                                        slope = f2_mul(r, f2_fma(r, f2_dup(-4.f), f2_dup(4.f)));
+                                    } else {
+                                        s = f2_fma(f2_pack(sc[v], sc[v + 1]), f2_dup(kLog2e), s);
+                                    }
+                                    float p0, p1, d0, d1;
+                                    f2_unpack(s, p0, p1);
+                                    p0 = ex2_approx(p0);
+                                    p1 = ex2_approx(p1);
+                                    uint64_t d = f2_add(f2_pack(dp[v], dp[v + 1]), DKV ? minus_delta : f2_dup(-delta[i]));
+                                    d = f2_mul(d, f2_pack(p0, p1));
+                                    if (CAP) d = f2_mul(d, slope);
+                                    f2_unpack(d, d0, d1);
+                                    pr[2 * j + i] = pack_bf16x2(p0, p1);
+                                    ds[2 * j + i] = pack_bf16x2(d0, d1);
+                                }
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) {
+                                uint32_t f[4];
+                                if (DKV) {
+                                    ldsm4t(ak[kk] + x_bytes, f);
+                                    mma16816(acc1[DKV ? 2 * kk : 0], pr, f[0], f[1]);
+                                    mma16816(acc1[DKV ? 2 * kk + 1 : 0], pr, f[2], f[3]);
+                                }
+                                ldsm4t(ak[kk], f);
+                                mma16816(acc0[2 * kk], ds, f[0], f[1]);
+                                mma16816(acc0[2 * kk + 1], ds, f[2], f[3]);
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < KB; ++kk) ak[kk] += 16 * HDB * 2;
+                            lut_at += 16;
+                            stat += 16;
+                        };
+                        if (capped)
+                            for (int k = 0; k < n_steps; ++k) plain(std::integral_constant<bool, true>{});
+                        else
+                            for (int k = 0; k < n_steps; ++k) plain(std::integral_constant<bool, false>{});
                         n_steps = 0;
                     }
                     for (int k = 0; k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8, stat += 16, key_doc += 16) {
@@ -1337,15 +1428,16 @@ bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms
                     }
                     // cycles: a step issues about 140 instructions (more without the table) on
                     // four schedulers that find one ready in two cycles of three; a frame's
-                    // load takes its latency and 45 bytes a cycle, and hides behind the
-                    // computation where two frames fit
+                    // load takes its latency and 60 bytes a cycle, and hides behind the
+                    // computation, all of it where two frames fit
                     const double instr = (mode == kFwd ? 140.0 : 190.0) * (hd + 64) / 128 * (g.lut ? 1.0 : 1.4);
                     const double work = double(all) / et * nw * blocks * instr / 2.6;
                     const double lat = double(all) / et * instr * 2.5;
                     const double comp = work > lat ? work : lat;
-                    const double load = 1500.0 + double(g.nwc) * nhc * g.cr * g.cc * hd * 4 * blocks / 45.0;
+                    const double load = 1000.0 + double(g.nwc) * nhc * g.cr * g.cc * hd * 4 * blocks / 60.0;
                     const bool deep = g.stages >= 2 * g.nwc * nhc;
-                    const double frame_t = deep ? (comp > load ? comp : load) : comp + load;
+                    const double more = comp > load ? comp : load, less = comp + load - more;
+                    const double frame_t = more + (deep ? 0.0 : 0.3 * less);
                     const double unit = et * (frame_t + 0.1 * (comp + load)) + 3000.0;
                     const double slots = double(sms) * blocks;
                     const double waves = g.units <= slots ? 1.0 : double(g.units) / slots;
