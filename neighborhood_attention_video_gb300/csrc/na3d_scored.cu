@@ -232,7 +232,7 @@ enum { kFwd, kDq, kDkv };
 // 60 more a thread).
 __host__ __device__ constexpr int blocks_per_sm(int hd, int mode) { return hd <= 32 && mode == kFwd ? 2 : 1; }
 __host__ __device__ constexpr int max_warps(int hd, int mode) {
-    return blocks_per_sm(hd, mode) == 2 || hd > 64 || (hd > 32 && mode != kDq) ? 8 : 12;
+    return blocks_per_sm(hd, mode) == 2 || hd > 32 ? 8 : 12;
 }
 // Buffers of the fixed tensors: two where a step reads them again (their
 // fragments and the accumulators together exceed the registers).
@@ -860,11 +860,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     auto columns = [&](uint32_t at, int kk) { return (at + (kk >> 2) * x_region) ^ ((kk & 3) << 5); };
                     // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
                     // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
-                    // The plain chunks of the forward pass, with the table and without documents to
-                    // compare, take NS steps at a time, so that the steps' chains of matrix products
+                    // The plain chunks of the forward pass, those with the table, take NS steps at a time, so that the steps' chains of matrix products
                     // and powers overlap.
                     constexpr int NS = 1;
-                    if (MODE == kFwd && use_lut && !mixed && (!capped || bounded)) {
+                    if (MODE == kFwd && use_lut && (!capped || bounded)) {
                         uint32_t ak[KB];   // a column block's address; the next step's is 16 rows on
 #pragma unroll
                         for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
@@ -889,9 +888,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                     mma16816(next[m] + 4, fa[0][kk], f[1], f[3]);
                                 }
                         };
-                        auto plain = [&](auto n_const, auto cap_const, auto ahead_const) {
+                        auto plain = [&](auto n_const, auto cap_const, auto mix_const, auto ahead_const) {
                             constexpr int N = decltype(n_const)::value;
-                            constexpr bool CAP = decltype(cap_const)::value;
+                            constexpr bool CAP = decltype(cap_const)::value, MIX = decltype(mix_const)::value;
                             float sc[N][8];
 #pragma unroll
                             for (int m = 0; m < N; ++m)
@@ -923,6 +922,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                             s = f2_fma(f2_pack(s4[0], s4[1]), f2_dup(kLog2e), bias);
                                         }
                                         f2_unpack(s, sv[m][4 * j + 2 * i], sv[m][4 * j + 2 * i + 1]);
+                                        if (MIX) {
+                                            const int* d = key_doc + 16 * m + 8 * j + 2 * c2;
+                                            if (d[0] != row_doc[i]) sv[m][4 * j + 2 * i] = -INFINITY;
+                                            if (d[1] != row_doc[i]) sv[m][4 * j + 2 * i + 1] = -INFINITY;
+                                        }
                                     }
                                 }
                             if (!CAP) {
@@ -964,35 +968,40 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk) ak[kk] += N * 16 * HDB * 2;
                             lut_at += 16 * N;
+                            if (MIX) key_doc += 16 * N;
                         };
                         using std::integral_constant;
                         const integral_constant<int, NS> full{};
                         const integral_constant<int, 1> one{};
-                        auto run = [&](auto cap_const) {
+                        auto run = [&](auto cap_const, auto mix_const) {
                             int k = 0;
                             if (n_steps >= NS) {
                                 scores(full, 0);
-                                for (; k + 2 * NS <= n_steps; k += NS) plain(full, cap_const, full);
-                                plain(full, cap_const, one);
+                                for (; k + 2 * NS <= n_steps; k += NS) plain(full, cap_const, mix_const, full);
+                                plain(full, cap_const, mix_const, one);
                                 k += NS;
                             } else {
                                 scores(one, 0);
                             }
-                            for (; k < n_steps; ++k) plain(one, cap_const, one);
+                            for (; k < n_steps; ++k) plain(one, cap_const, mix_const, one);
                         };
                         if (n_steps > 0) {
-                            if (capped) run(integral_constant<bool, true>{});
-                            else run(integral_constant<bool, false>{});
+                            const integral_constant<bool, true> yes{};
+                            const integral_constant<bool, false> no{};
+                            if (capped && mixed) run(yes, yes);
+                            else if (capped) run(yes, no);
+                            else if (mixed) run(no, yes);
+                            else run(no, no);
                         }
                         n_steps = 0;
                     }
                     // ... and those of the backward passes, without a branch in a step
-                    if (MODE != kFwd && use_lut && !mixed && (!capped || to_log2 <= 96.f)) {
+                    if (MODE != kFwd && use_lut && (!capped || to_log2 <= 96.f)) {
                         uint32_t ak[KB];
 #pragma unroll
                         for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
-                        auto plain = [&](auto cap_const) {
-                            constexpr bool CAP = decltype(cap_const)::value;
+                        auto plain = [&](auto cap_const, auto mix_const) {
+                            constexpr bool CAP = decltype(cap_const)::value, MIX = decltype(mix_const)::value;
                             float sc[8] = {}, dp[8] = {};
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk) {
@@ -1035,6 +1044,11 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                     }
                                     float p0, p1, d0, d1;
                                     f2_unpack(s, p0, p1);
+                                    if (MIX) {
+                                        const int* d = key_doc + 8 * j + 2 * c2;
+                                        if (d[0] != row_doc[i]) p0 = -INFINITY;
+                                        if (d[1] != row_doc[i]) p1 = -INFINITY;
+                                    }
                                     p0 = ex2_approx(p0);
                                     p1 = ex2_approx(p1);
                                     uint64_t d = f2_add(f2_pack(dp[v], dp[v + 1]), DKV ? minus_delta : f2_dup(-delta[i]));
@@ -1061,11 +1075,17 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             for (int kk = 0; kk < KB; ++kk) ak[kk] += 16 * HDB * 2;
                             lut_at += 16;
                             stat += 16;
+                            if (MIX) key_doc += 16;
                         };
-                        if (capped)
-                            for (int k = 0; k < n_steps; ++k) plain(std::integral_constant<bool, true>{});
-                        else
-                            for (int k = 0; k < n_steps; ++k) plain(std::integral_constant<bool, false>{});
+                        auto run = [&](auto cap_const, auto mix_const) {
+                            for (int k = 0; k < n_steps; ++k) plain(cap_const, mix_const);
+                        };
+                        const std::integral_constant<bool, true> yes{};
+                        const std::integral_constant<bool, false> no{};
+                        if (capped && mixed) run(yes, yes);
+                        else if (capped) run(yes, no);
+                        else if (mixed) run(no, yes);
+                        else run(no, no);
                         n_steps = 0;
                     }
                     for (int k = 0; k < n_steps; ++k, a0 += 16 * HDB * 2, lut_at += 16, mask_at += 8, stat += 16, key_doc += 16) {
