@@ -291,11 +291,11 @@ def _empty(stream, like, shape, dtype):
     call uses, so that the allocator may reuse its memory only behind the call."""
     torch = _torch_module()
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _workspace(work, need, like, stream):
@@ -311,20 +311,35 @@ def _workspace(work, need, like, stream):
     return work
 
 
-def _scored_options(q, softcap, slopes, doc, prefix):
+def _scored_options(shape, softcap, slopes, doc, prefix):
     """The score arguments of the na3d_scored_ calls, checked: (softcap, the
     three pointers or None)."""
     torch = _torch_module()
-    B, T, H, W, NH, _ = q.shape
-    given = []
+    ps = pd = pp = None
     if slopes is not None:
-        given.append(("slopes", slopes, torch.float32, (NH, 3)))
+        _check_on_device((("slopes", slopes, torch.float32, (shape[4], 3)),))
+        ps = slopes.data_ptr()
     if doc is not None:
-        given.append(("doc", doc, torch.int32, (B, T, H, W)))
+        _check_on_device((("doc", doc, torch.int32, shape[:4]),))
+        pd = doc.data_ptr()
     if prefix is not None:
-        given.append(("prefix", prefix, torch.int32, (B,)))
-    _check_on_device(given)
-    return (float(softcap),) + tuple(None if t is None else t.data_ptr() for t in (slopes, doc, prefix))
+        _check_on_device((("prefix", prefix, torch.int32, shape[:1]),))
+        pp = prefix.data_ptr()
+    return softcap, ps, pd, pp
+
+
+def _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc, prefix, stream) -> None:
+    """The call behind na3d_scored_fwd: out and lse are as it needs them."""
+    lib = _lib if _lib is not None else load_library()
+    if len(shape) != 6 or k.shape != shape or v.shape != shape:
+        raise ValueError("q, k, v and out must have the same 6-D (B,T,H,W,NH,HD) shape")
+    KT, KH, KW = kernel_size
+    rc = lib.na3d_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                             None if lse is None else lse.data_ptr(), *shape, int(KT), int(KH), int(KW),
+                             _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
+                             *_scored_options(shape, softcap, slopes, doc, prefix), _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_scored_fwd")
 
 
 def na3d_scored_fwd(q, k, v, out, kernel_size, lse=None, softcap=0.0, slopes=None, doc=None, prefix=None,
@@ -336,23 +351,15 @@ def na3d_scored_fwd(q, k, v, out, kernel_size, lse=None, softcap=0.0, slopes=Non
     along T with a free prefix (``prefix``: int32 (B,) frames). ``lse``, where
     given, receives the fp32 (B, T, H, W, NH) log-sum-exp of the scores. q, k,
     v may be views with a token stride; ``out`` is contiguous. HD up to 128."""
-    lib = _lib if _lib is not None else load_library()
     _check_bf16_on_device((("q", q), ("k", k), ("v", v), ("out", out)))
     shape = q.shape
-    if len(shape) != 6 or k.shape != shape or v.shape != shape or out.shape != shape:
+    if out.shape != shape:
         raise ValueError("q, k, v and out must have the same 6-D (B,T,H,W,NH,HD) shape")
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     if lse is not None:
         _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
-    options = _scored_options(q, softcap, slopes, doc, prefix)
-    KT, KH, KW = (int(x) for x in kernel_size)
-    rc = lib.na3d_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                             None if lse is None else lse.data_ptr(), *shape, KT, KH, KW,
-                             _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
-                             *options, _stream_handle(stream))
-    if rc != NA3D_OK:
-        raise NA3DError(rc, "na3d_scored_fwd")
+    _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc, prefix, stream)
 
 
 def na3d_scored_attention(q, k, v, kernel_size, softcap=0.0, slopes=None, doc=None, prefix=None,
@@ -360,10 +367,11 @@ def na3d_scored_attention(q, k, v, kernel_size, softcap=0.0, slopes=None, doc=No
     """``na3d_scored_fwd`` into a new tensor: returns out, or (out, lse) where
     ``return_lse`` is true (what ``na3d_scored_bwd`` needs)."""
     torch = _torch_module()
-    _check_bf16_on_device((("q", q),))
-    out = _empty(stream, q, q.shape, torch.bfloat16)
-    lse = _empty(stream, q, q.shape[:-1], torch.float32) if return_lse else None
-    na3d_scored_fwd(q, k, v, out, kernel_size, lse, softcap, slopes, doc, prefix, stream)
+    _check_bf16_on_device((("q", q), ("k", k), ("v", v)))
+    shape = q.shape
+    out = _empty(stream, q, shape, torch.bfloat16)
+    lse = _empty(stream, q, shape[:-1], torch.float32) if return_lse else None
+    _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc, prefix, stream)
     return (out, lse) if return_lse else out
 
 
@@ -393,7 +401,7 @@ def na3d_scored_bwd(q, k, v, out, lse, dout, dq, dk, dv, kernel_size, softcap=0.
     if not (out.is_contiguous() and dout.is_contiguous()):
         raise ValueError("out and dout must be contiguous")
     _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
-    options = _scored_options(q, softcap, slopes, doc, prefix)
+    options = _scored_options(shape, softcap, slopes, doc, prefix)
     strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))]
     KT, KH, KW = (int(x) for x in kernel_size)
     work = _workspace(work, lib.na3d_scored_bwd_workspace(*shape[:5]), q, stream)
