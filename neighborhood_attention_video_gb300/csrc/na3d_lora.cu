@@ -160,44 +160,58 @@ __device__ __forceinline__ void down_rows(const LoraParams& p, uint16_t* out) {
             for (int i = threadIdx.x; i < RT * RP / 8; i += 128) reinterpret_cast<uint4*>(to)[i] = make_uint4(0, 0, 0, 0);
             continue;
         }
-        auto load = [&](int kb) {
+        // this thread's 16-byte pieces of a stage, the same rows of x (of A, or columns of B) in
+        // each: pointers that move on by a block, so that a load is an addition and a copy
+        constexpr int XJ = RT * 8 / 128, BJ = RP / 16;
+        const int xc = (threadIdx.x & 7) * 8;   // column in a 64-column block
+        const uint16_t *xp[XJ], *bp[BJ];
+        uint32_t x_in = 0, b_in = 0;
+#pragma unroll
+        for (int j = 0; j < XJ; ++j) {
+            const int m = m_first + (threadIdx.x >> 3) + 16 * j;
+            const bool in = m >= lo && m < hi;
+            x_in |= uint32_t(in) << j;
+            xp[j] = src + (in ? int64_t(m) * K + xc : 0);
+        }
+        constexpr int PR = RP / 8;   // pieces of a row of B
+#pragma unroll
+        for (int j = 0; j < BJ; ++j) {
+            const int i = threadIdx.x + 128 * j, r = BWD ? i / PR : i >> 3, c = BWD ? i % PR : i & 7;
+            const bool in = BWD ? c * 8 < p.R : r < p.R;
+            b_in |= uint32_t(in) << j;
+            bp[j] = BWD ? p.b + (in ? (int64_t(w.a) * K + r) * p.R + c * 8 : 0) : p.a + (in ? (int64_t(w.a) * p.R + r) * K + c * 8 : 0);
+        }
+        auto load = [&](int kb) {   // blocks in order, each once
             const uint32_t st = base + (kb % kDownStages) * STAGE;
-            const int k0 = kb * 64;
-            for (int i = threadIdx.x; i < RT * 8; i += 128) {
-                const int r = i >> 3, c = i & 7, m = m_first + r, k = k0 + c * 8;
-                const bool in = m >= lo && m < hi && k < K;
-                cp16(st + at<128>(r, c), src + (in ? int64_t(m) * K + k : 0), in);
+            const int left = K - kb * 64;
+#pragma unroll
+            for (int j = 0; j < XJ; ++j) {
+                const bool in = (x_in >> j & 1u) && xc < left;
+                cp16(st + at<128>((threadIdx.x >> 3) + 16 * j, threadIdx.x & 7), in ? xp[j] : src, in);
+                xp[j] += 64;
             }
-            if (!BWD) {
-                for (int i = threadIdx.x; i < RP * 8; i += 128) {
-                    const int r = i >> 3, c = i & 7, k = k0 + c * 8;
-                    const bool in = r < p.R && k < K;
-                    cp16(st + X_TILE + at<128>(r, c), p.a + (in ? (int64_t(w.a) * p.R + r) * K + k : 0), in);
-                }
-            } else {
-                for (int i = threadIdx.x; i < 64 * (RP / 8); i += 128) {
-                    const int n = i / (RP / 8), c = i % (RP / 8);
-                    const bool in = k0 + n < K && c * 8 < p.R;
-                    cp16(st + X_TILE + at<RP * 2>(n, c), p.b + (in ? (int64_t(w.a) * K + k0 + n) * p.R + c * 8 : 0), in);
-                }
+#pragma unroll
+            for (int j = 0; j < BJ; ++j) {
+                const int i = threadIdx.x + 128 * j, r = BWD ? i / PR : i >> 3, c = BWD ? i % PR : i & 7;
+                const bool in = (b_in >> j & 1u) && (BWD ? r : c * 8) < left;
+                cp16(st + X_TILE + (BWD ? at<RP * 2>(r, c) : at<128>(r, c)), in ? bp[j] : src, in);
+                bp[j] += BWD ? int64_t(64) * p.R : 64;
             }
         };
         float acc[NT][4] = {};
         auto step = [&](int kb, int kk, int row16) {   // 16 of the contraction
             const uint32_t st = base + (kb % kDownStages) * STAGE, bt = st + X_TILE;
-            uint32_t a[4], f[4];
+            uint32_t a[4], f[NT / 2][4];   // all loads before the products that wait for them
             ldsm4(st + at<128>(row16 + (lane & 15), 2 * kk + (lane >> 4)), a);
 #pragma unroll
             for (int j = 0; j < NT / 2; ++j) {
-                if (!BWD) {
-                    ldsm4(bt + at<128>(16 * j + (lane & 15), 2 * kk + (lane >> 4)), f);
-                    mma16816(acc[2 * j], a, f[0], f[2]);
-                    mma16816(acc[2 * j + 1], a, f[1], f[3]);
-                } else {
-                    ldsm4t(bt + at<RP * 2>(16 * kk + (lane & 15), 2 * j + (lane >> 4)), f);
-                    mma16816(acc[2 * j], a, f[0], f[1]);
-                    mma16816(acc[2 * j + 1], a, f[2], f[3]);
-                }
+                if (!BWD) ldsm4(bt + at<128>(16 * j + (lane & 15), 2 * kk + (lane >> 4)), f[j]);
+                else ldsm4t(bt + at<RP * 2>(16 * kk + (lane & 15), 2 * j + (lane >> 4)), f[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+                mma16816(acc[2 * j], a, f[j][0], f[j][BWD ? 1 : 2]);
+                mma16816(acc[2 * j + 1], a, f[j][BWD ? 2 : 1], f[j][3]);
             }
         };
         __syncthreads();   // the stages of the request before are read
