@@ -858,144 +858,96 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     const float2* stat = col_stat;
                     uint32_t a0 = base + g.off_x + 2 * s * x_bytes + part_at;
                     auto columns = [&](uint32_t at, int kk) { return (at + (kk >> 2) * x_region) ^ ((kk & 3) << 5); };
-                    // scores: columns 0..7 in sc[0..3], 8..15 in sc[4..7]; value i is of row
-                    // (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
-                    // The plain chunks of the forward pass, those with the table, take NS steps at a time, so that the steps' chains of matrix products
-                    // and powers overlap.
-                    constexpr int NS = 1;
+                    // In a step columns 0..7 have their scores in sc[0..3], 8..15 in sc[4..7]; value i is
+                    // of row (i >> 1) & 1 and column 8 * (i >> 2) + 2 * c2 + (i & 1).
+                    // Most chunks take plain steps, without a branch in one: those with the table, but for
+                    // caps or slopes that want a running maximum and the polynomial. Taking the next
+                    // step's scores ahead, or two steps at a time, measured 4 to 9 % slower here: what
+                    // it saves in waiting costs more in registers.
                     if (MODE == kFwd && use_lut && (!capped || bounded)) {
                         uint32_t ak[KB];   // a column block's address; the next step's is 16 rows on
 #pragma unroll
                         for (int kk = 0; kk < KB; ++kk) ak[kk] = columns(a0, kk);
-                        // the scores of N steps, m steps on from ak; N steps ahead of the softmax, whose
-                        // instructions fill the issue slots between these matrix products (the last
-                        // ones read rows past the chunk, for nothing)
-                        float next[NS][8];
-                        auto scores = [&](auto n_const, int m0) {
-                            constexpr int N = decltype(n_const)::value;
-#pragma unroll
-                            for (int m = 0; m < N; ++m)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) next[m][i] = 0.f;
-                            // 2 N accumulators in turn: a product finds its sum ready
-#pragma unroll
-                            for (int kk = 0; kk < KB; ++kk)
-#pragma unroll
-                                for (int m = 0; m < N; ++m) {
-                                    uint32_t f[4];
-                                    ldsm4(ak[kk] + (m0 + m) * 16 * HDB * 2, f);
-                                    mma16816(next[m], fa[0][kk], f[0], f[2]);
-                                    mma16816(next[m] + 4, fa[0][kk], f[1], f[3]);
-                                }
-                        };
-                        auto plain = [&](auto n_const, auto cap_const, auto mix_const, auto ahead_const) {
-                            constexpr int N = decltype(n_const)::value;
+                        auto plain = [&](auto cap_const, auto mix_const) {
                             constexpr bool CAP = decltype(cap_const)::value, MIX = decltype(mix_const)::value;
-                            float sc[N][8];
+                            float sc[8] = {}, sv[8];
+                            uint32_t f[4];
 #pragma unroll
-                            for (int m = 0; m < N; ++m)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) sc[m][i] = next[m][i];
-                            scores(ahead_const, N);
-                            float sv[N][8];
+                            for (int kk = 0; kk < KB; ++kk) {
+                                ldsm4(ak[kk], f);
+                                mma16816(sc, fa[0][kk], f[0], f[2]);
+                                mma16816(sc + 4, fa[0][kk], f[1], f[3]);
+                            }
                             const uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
 #pragma unroll
-                            for (int m = 0; m < N; ++m)
+                            for (int j = 0; j < 2; ++j) {
+                                const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 8 * j);
+                                const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 8 * j);
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const uint64_t x = *reinterpret_cast<const uint64_t*>(lut_at + 16 * m + 8 * j);
-                                    const uint64_t y = same_hw ? x : *reinterpret_cast<const uint64_t*>(lut_at + 8 * g.lut_pitch + 16 * m + 8 * j);
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        float* const s4 = &sc[m][4 * j + 2 * i];
-                                        const uint64_t bias = f2_add(i ? y : x, from[i]);   // minus the reference
-                                        uint64_t s;
-                                        if (CAP) {
-                                            // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)); within a few 2^-24 of c, and
-                                            // c <= 64 here
-                                            const uint64_t z = f2_mul(f2_pack(s4[0], s4[1]), f2_dup(exp_scale));
-                                            float e0, e1;
-                                            f2_unpack(z, e0, e1);
-                                            f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);
-                                            s = f2_fma(f2_pack(rcp_approx(e0), rcp_approx(e1)), f2_dup(-2.f * to_log2), f2_add(bias, f2_dup(to_log2)));
-                                        } else {
-                                            s = f2_fma(f2_pack(s4[0], s4[1]), f2_dup(kLog2e), bias);
-                                        }
-                                        f2_unpack(s, sv[m][4 * j + 2 * i], sv[m][4 * j + 2 * i + 1]);
-                                        if (MIX) {
-                                            const int* d = key_doc + 16 * m + 8 * j + 2 * c2;
-                                            if (d[0] != row_doc[i]) sv[m][4 * j + 2 * i] = -INFINITY;
-                                            if (d[1] != row_doc[i]) sv[m][4 * j + 2 * i + 1] = -INFINITY;
-                                        }
+                                for (int i = 0; i < 2; ++i) {
+                                    const int v = 4 * j + 2 * i;
+                                    const uint64_t a = f2_pack(sc[v], sc[v + 1]), bias = f2_add(i ? y : x, from[i]);   // minus the reference
+                                    uint64_t s;
+                                    if (CAP) {
+                                        // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)); within a few 2^-24 of c, and
+                                        // c <= 64 here
+                                        float e0, e1;
+                                        f2_unpack(f2_mul(a, f2_dup(exp_scale)), e0, e1);
+                                        f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);
+                                        s = f2_fma(f2_pack(rcp_approx(e0), rcp_approx(e1)), f2_dup(-2.f * to_log2), f2_add(bias, f2_dup(to_log2)));
+                                    } else {
+                                        s = f2_fma(a, f2_dup(kLog2e), bias);
+                                    }
+                                    f2_unpack(s, sv[v], sv[v + 1]);
+                                    if (MIX) {
+                                        const int* d = key_doc + 8 * j + 2 * c2;
+                                        if (d[0] != row_doc[i]) sv[v] = -INFINITY;
+                                        if (d[1] != row_doc[i]) sv[v + 1] = -INFINITY;
                                     }
                                 }
+                            }
                             if (!CAP) {
                                 float top[2];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    top[i] = -INFINITY;
-#pragma unroll
-                                    for (int m = 0; m < N; ++m)
-                                        top[i] = max3f(max3f(top[i], sv[m][2 * i], sv[m][2 * i + 1]), sv[m][4 + 2 * i], sv[m][5 + 2 * i]);
-                                }
+                                for (int i = 0; i < 2; ++i)
+                                    top[i] = fmaxf(max3f(sv[2 * i], sv[2 * i + 1], sv[4 + 2 * i]), sv[5 + 2 * i]);
                                 if (__any_sync(0xffffffffu, top[0] > grow[0] || top[1] > grow[1])) {
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) {
                                         const float x = move_reference(top[i], grow[i], ref[i], l[i], acc0, i);
 #pragma unroll
-                                        for (int m = 0; m < N; ++m)
-#pragma unroll
-                                            for (int j = 0; j < 4; ++j) sv[m][4 * (j >> 1) + 2 * i + (j & 1)] -= x;
+                                        for (int j = 0; j < 4; ++j) sv[4 * (j >> 1) + 2 * i + (j & 1)] -= x;
                                     }
                                 }
                             }
 #pragma unroll
-                            for (int m = 0; m < N; ++m) {
+                            for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+                            l[0] += (sv[0] + sv[1]) + (sv[4] + sv[5]);
+                            l[1] += (sv[2] + sv[3]) + (sv[6] + sv[7]);
+                            const uint32_t a[4] = {pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]),
+                                                   pack_bf16x2(sv[4], sv[5]), pack_bf16x2(sv[6], sv[7])};
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) sv[m][i] = ex2_approx(sv[m][i]);
-                                l[0] += (sv[m][0] + sv[m][1]) + (sv[m][4] + sv[m][5]);
-                                l[1] += (sv[m][2] + sv[m][3]) + (sv[m][6] + sv[m][7]);
-                                const uint32_t a[4] = {pack_bf16x2(sv[m][0], sv[m][1]), pack_bf16x2(sv[m][2], sv[m][3]),
-                                                       pack_bf16x2(sv[m][4], sv[m][5]), pack_bf16x2(sv[m][6], sv[m][7])};
-#pragma unroll
-                                for (int kk = 0; kk < KB; ++kk) {
-                                    uint32_t f[4];
-                                    ldsm4t(ak[kk] + x_bytes + m * 16 * HDB * 2, f);
-                                    mma16816(acc0[2 * kk], a, f[0], f[1]);
-                                    mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
-                                }
+                            for (int kk = 0; kk < KB; ++kk) {
+                                ldsm4t(ak[kk] + x_bytes, f);
+                                mma16816(acc0[2 * kk], a, f[0], f[1]);
+                                mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
+                                ak[kk] += 16 * HDB * 2;
                             }
-#pragma unroll
-                            for (int kk = 0; kk < KB; ++kk) ak[kk] += N * 16 * HDB * 2;
-                            lut_at += 16 * N;
-                            if (MIX) key_doc += 16 * N;
+                            lut_at += 16;
+                            if (MIX) key_doc += 16;
                         };
-                        using std::integral_constant;
-                        const integral_constant<int, NS> full{};
-                        const integral_constant<int, 1> one{};
                         auto run = [&](auto cap_const, auto mix_const) {
-                            int k = 0;
-                            if (n_steps >= NS) {
-                                scores(full, 0);
-                                for (; k + 2 * NS <= n_steps; k += NS) plain(full, cap_const, mix_const, full);
-                                plain(full, cap_const, mix_const, one);
-                                k += NS;
-                            } else {
-                                scores(one, 0);
-                            }
-                            for (; k < n_steps; ++k) plain(one, cap_const, mix_const, one);
+                            for (int k = 0; k < n_steps; ++k) plain(cap_const, mix_const);
                         };
-                        if (n_steps > 0) {
-                            const integral_constant<bool, true> yes{};
-                            const integral_constant<bool, false> no{};
-                            if (capped && mixed) run(yes, yes);
-                            else if (capped) run(yes, no);
-                            else if (mixed) run(no, yes);
-                            else run(no, no);
-                        }
+                        const std::integral_constant<bool, true> yes{};
+                        const std::integral_constant<bool, false> no{};
+                        if (capped && mixed) run(yes, yes);
+                        else if (capped) run(yes, no);
+                        else if (mixed) run(no, yes);
+                        else run(no, no);
                         n_steps = 0;
                     }
-                    // ... and those of the backward passes, without a branch in a step
+                    // ... those of the backward passes
                     if (MODE != kFwd && use_lut && (!capped || to_log2 <= 96.f)) {
                         uint32_t ak[KB];
 #pragma unroll
