@@ -175,7 +175,7 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
     // a row that sees nothing has no part in any gradient, whatever dout holds
     const float delta = lse == -INFINITY ? 0.f : g.dot(y);
     acc.zero();
-    float slope[3], ds;
+    float slope[3], ds, inner = 0.f;
     load_slopes(p, o.head, slope);
     const int qdoc = p.doc ? p.doc[o.token] : 0, prefix = p.prefix ? p.prefix[o.b] : 0;
     const int t0 = win_start(o.t, p.KT, p.T), h0 = win_start(o.h, p.KH, p.H), w0 = win_start(o.w, p.KW, p.W);
@@ -188,8 +188,11 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
                     x.load(p.k + tok * p.k_ts + int64_t(o.head) * HD, lane);
                     const float s = shape_score(p, q.dot(x), slope, o.t - t, o.h - h, o.w - w, &ds);
                     y.load(p.v + tok * p.v_ts + int64_t(o.head) * HD, lane);
-                    acc.axpy(expf(s - lse) * (g.dot(y) - delta) * ds, x);
+                    const float e = expf(s - lse), dp = g.dot(y);
+                    inner = fmaf(e, dp, inner);
+                    acc.axpy(e * (dp - delta) * ds, x);
                 }
+    if (lane == 0) p.stat[stat_at(p, o.b, o.token, o.head)].y = inner;
     acc.store(p.dq + o.token * p.dq_ts + int64_t(o.head) * HD, lane);
 }
 
@@ -505,12 +508,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     const uint32_t x_bytes = g.x_bytes, x_region = REG > 1 ? x_bytes / REG : 0;
     const bool docs = p.doc != nullptr;
 
-    // the kernel before (the forward pass has none that lets it start early) brings the
-    // statistics; the one behind needs nothing of this one
-    if (MODE == kDq) {
-        wait_for_primary();
-        dependents_may_start();
-    }
+    if (MODE == kDq) dependents_may_start();
 
     // control words: abort flag, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
@@ -534,6 +532,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     float2* const hw = reinterpret_cast<float2*>(base_ptr + g.off_hw);
     for (int i = threadIdx.x; i < g.cr * g.cc + 16; i += blockDim.x) hw[i] = make_float2(float(i / g.cc), float(i % g.cc));
     fence_proxy_async_smem();
+    // the kernel before brings the statistics (the forward pass has none that lets it start early)
+    if (MODE != kFwd) wait_for_primary();
     __syncthreads();
 
     const int u0 = int(int64_t(g.units) * blockIdx.x / gridDim.x);
@@ -784,6 +784,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // FWD: the sum of e^(s - ref), and the growth that moves the reference:
         // any for a row that has met no key, so that ref starts at a score
         float l[2] = {0.f, 0.f}, grow[2] = {-INFINITY, -INFINITY};
+        float inner[2] = {0.f, 0.f};   // DQ: the sum of p dp
 
         // this warp's part of a chunk: its columns from (hf, w), their steps, and the addresses of
         // the first ones in a stage (and its tables, where a frame has one chunk, once a unit)
@@ -1003,6 +1004,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                     }
                                     p0 = ex2_approx(p0);
                                     p1 = ex2_approx(p1);
+                                    if (MODE == kDq) inner[i] = fmaf(p0, dp[v], fmaf(p1, dp[v + 1], inner[i]));
                                     uint64_t d = f2_add(f2_pack(dp[v], dp[v + 1]), DKV ? minus_delta : f2_dup(-delta[i]));
                                     d = f2_mul(d, f2_pack(p0, p1));
                                     if (CAP) d = f2_mul(d, slope);
@@ -1153,7 +1155,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                             l[1] += (sv[2] + sv[3]) + (sv[6] + sv[7]);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) sv[i] = ex2_approx(sv[i]);
+                            for (int i = 0; i < 8; ++i) {
+                                sv[i] = ex2_approx(sv[i]);
+                                if (MODE == kDq) inner[(i >> 1) & 1] = fmaf(sv[i], dp[i], inner[(i >> 1) & 1]);
+                            }
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint64_t d = f2_add(f2_pack(dp[2 * j], dp[2 * j + 1]),
@@ -1219,6 +1224,12 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 if (row_in[i] && c2 == 0 && p.lse)
                     p.lse[token * p.NH + head] = l[i] == 0.f ? -INFINITY : (ref[i] + log2f(l[i])) * kLn2;
             }
+            if (MODE == kDq) {
+                // what delta is without the rounding of out and of its probabilities: for DKV
+                inner[i] += __shfl_xor_sync(0xffffffffu, inner[i], 1);
+                inner[i] += __shfl_xor_sync(0xffffffffu, inner[i], 2);
+                if (row_in[i] && c2 == 0) p.stat[stat_at(p, o.b, token, head)].y = inner[i];
+            }
             uint16_t* const at0 = out0 + token * ts0 + int64_t(head) * HD + 2 * c2;
             uint16_t* const at1 = p.dv + token * p.dv_ts + int64_t(head) * HD + 2 * c2;
 #pragma unroll
@@ -1253,7 +1264,6 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         next_unit<DKV>(p, g, cur);
     }
 
-    if (DKV) wait_for_primary();   // ends behind the kernel beside it
     // every issued load lands before the block may exit: where all went well
     // each has been waited for
     __syncthreads();
@@ -1264,7 +1274,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 }
 
 // (lse in log2 units, delta) of every row for the backward passes:
-// delta_i = dout_i . out_i; a row that sees nothing gets (0, 0). A row takes HD / 8 lanes, 16 bytes each.
+// delta_i = dout_i . out_i; a row that sees nothing gets (0, 0). The pass for
+// dQ takes delta from here and leaves the sum of p dp, which is the same
+// without the rounding of out, in its place for the one for dK and dV. A row takes HD / 8 lanes, 16 bytes each.
 template <int HD>
 __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t rows) {
     constexpr int L = HD / 8;
