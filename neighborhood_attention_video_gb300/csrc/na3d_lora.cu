@@ -52,16 +52,18 @@ __device__ __forceinline__ int first_request(const Requests& q, int m) {
     return lo;
 }
 
-// The same by a whole warp, which reads 32 offsets at a time: one trip to
-// memory for few requests.
+// The same by a whole warp: few requests' offsets in one trip to memory, and
+// the same search over them.
 __device__ __forceinline__ int first_request_warp(const Requests& q, int m) {
-    if (q.n_req > 256) return first_request(q, m);
-    const int lane = threadIdx.x & 31;
-    for (int r = 0; r < q.n_req; r += 32) {
-        const uint32_t behind = __ballot_sync(0xffffffffu, r + lane < q.n_req && q.offsets[r + lane + 1] > m);
-        if (behind) return r + __ffs(behind) - 1;
+    if (q.n_req > 32) return first_request(q, m);
+    const int lane = threadIdx.x & 31, end = lane < q.n_req ? q.offsets[lane + 1] : 0;
+    int lo = 0, hi = q.n_req;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__shfl_sync(0xffffffffu, end, mid) > m) hi = mid;
+        else lo = mid + 1;
     }
-    return q.n_req;
+    return lo;
 }
 
 // The requests with an adapter that meet rows [m0, m0 + SPAN), in order. Every

@@ -32,9 +32,12 @@ def run(t, dqkv, offsets, adapter, NH, HD, want_dx=True, **kw):
     adapters = (d["lora_a"], d["lora_b"], d["scaling"], off, ad)
     nan = lambda x: torch.full_like(x, float("nan"))  # noqa: E731
     qkv = nan(dqkv.cuda())
+    grad = dqkv.cuda()
+    torch.cuda.synchronize()
     na.na3d_lora_qkv_proj(d["x"], d["w"], d["bias"], *adapters, qkv, NH, HD, **kw)
     dx, da, db = nan(d["x"]) if want_dx else None, nan(d["lora_a"]), nan(d["lora_b"])
-    na.na3d_lora_qkv_proj_bwd(dqkv.cuda(), d["x"], d["w"], *adapters, dx, da, db, NH, HD, **kw)
+    torch.cuda.synchronize()
+    na.na3d_lora_qkv_proj_bwd(grad, d["x"], d["w"], *adapters, dx, da, db, NH, HD, **kw)
     torch.cuda.synchronize()
     assert na.na3d_device_status() == 0
     return dict(qkv=qkv, da=da, db=db, **({"dx": dx} if want_dx else {}))
@@ -46,6 +49,7 @@ CASES = [
     (1, 8, 1, 16, 8, 2, (0, 1), (-1,)),
     (5, 264, 3, 32, 16, 5, (0, 1, 2, 3, 4, 5), (4, 0, 4, -1, 2)),      # single tokens, an adapter twice
     (8, 2048, 4, 128, 16, 8, tuple(range(9)), tuple(range(8))),
+    (32, 1024, 2, 64, 8, 3, (0, 31, 32), (2, 0)),
     (33, 512, 8, 64, 64, 3, (0, 7, 7, 20, 33), (1, 2, 1, 0)),          # an empty request
     (64, 136, 5, 16, 40, 2, (3, 10, 60), (1, 0)),                      # rows outside every request
     (100, 64, 2, 32, 8, 2, (0, 100), (7,)),                            # an id past the adapters: none
@@ -121,6 +125,59 @@ def test_requests_do_not_reach_one_another(M):
             ref.check(name, got[name][rows], (value[rows], bound[rows]))
     for name in ("da", "db"):
         assert torch.equal(got[name][0], clean[name][0]), name
+
+
+@pytest.mark.parametrize("M,n_req", [(3000, 1500), (20, 2000), (19500, 40)])
+def test_many_requests(M, n_req):
+    """More requests than a block keeps at hand, most of them empty or of one row."""
+    gen = torch.Generator().manual_seed(M)
+    C, NH, HD, R, n_ad = 64, 2, 64, 16, 7
+    off = torch.randint(0, M + 1, (n_req + 1,), generator=gen).sort().values.to(torch.int32)
+    ad = torch.randint(-1, n_ad, (n_req,), generator=gen).to(torch.int32)
+    t, g = make(M, C, NH, HD, R, n_ad, 9)
+    want = ref.lora(**t, offsets=off, adapter=ad, HD=HD, dqkv=g)
+    got = run(t, g, off, ad, NH, HD)
+    for name in want:
+        ref.check(name, got[name], want[name])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    C, NH, HD = 128, 2, 64
+    off, ad = ints(0, 100, 900), ints(1, 0)
+    data = [make(900, C, NH, HD, 16, 2, s) for s in (1, 2)]
+    want = [ref.lora(**t, offsets=off, adapter=ad, HD=HD, dqkv=g) for t, g in data]
+    streams = [torch.cuda.Stream() for _ in data]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    results = [None, None]
+    for _ in range(5):
+        for i, (t, g) in enumerate(data):
+            with torch.cuda.stream(streams[i]):
+                d = {n: v.cuda() for n, v in t.items()}
+                adapters = (d["lora_a"], d["lora_b"], d["scaling"], off.cuda(), ad.cuda())
+                qkv = torch.empty((900, 3 * NH * HD), dtype=BF16, device="cuda")
+                na.na3d_lora_qkv_proj(d["x"], d["w"], d["bias"], *adapters, qkv, NH, HD)
+                dx, da, db = (torch.empty_like(d[n]) for n in ("x", "lora_a", "lora_b"))
+                na.na3d_lora_qkv_proj_bwd(g.cuda(), d["x"], d["w"], *adapters, dx, da, db, NH, HD)
+                results[i] = dict(qkv=qkv, dx=dx, da=da, db=db)
+    torch.cuda.synchronize()
+    for w, r in zip(want, results):
+        for name in w:
+            ref.check(name, r[name], w[name])
+
+
+def test_stream_argument():
+    """stream= of another stream than the current one; the binding's own workspace."""
+    C, NH, HD = 64, 1, 64
+    t, g = make(200, C, NH, HD, 16, 2, 3)
+    off, ad = ints(0, 90, 200), ints(1, 0)
+    want = ref.lora(**t, offsets=off, adapter=ad, HD=HD, dqkv=g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = run(t, g, off, ad, NH, HD, stream=side)
+    for name in want:
+        ref.check(name, got[name], want[name])
 
 
 def test_offsets_out_of_order_touch_nothing_else():

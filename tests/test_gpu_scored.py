@@ -67,6 +67,13 @@ CASES = [
     ((1, 12, 13, 13, 1, 64), (11, 11, 11), dict(softcap=50.0)),
     ((3, 2, 5, 6, 5, 32), (1, 5, 3), dict(docs=2, pad=5)),
     ((1, 2, 3, 200, 1, 64), (1, 3, 151), dict(slopes=True)),
+    # windows too wide for a table of biases, with and without what the plain steps leave out
+    ((1, 2, 40, 40, 1, 128), (1, 31, 33), dict(softcap=10.0, slopes=True, docs=2, pad=3)),
+    ((1, 1, 80, 64, 1, 64), (1, 61, 55), dict()),
+    # rows of columns in several chunks
+    ((1, 1, 2, 700, 1, 32), (1, 1, 501), dict(slopes=True, docs=1, pad=100)),
+    # more frames than a warp's rows, causal
+    ((2, 33, 4, 5, 2, 32), (9, 3, 3), dict(softcap=40.0, docs=3, prefix=4)),
 ]
 
 
@@ -90,6 +97,78 @@ def test_large_and_small_scores(scale, softcap):
     got = run(q, k, v, g, kernel, o)
     for name in want:
         ref.check(name, got[name], want[name])
+
+
+@pytest.mark.parametrize("softcap,HD", [(0.0, 64), (12.0, 64), (100.0, 32), (64.0, 128), (70.0, 16)])
+def test_slopes_of_either_sign(softcap, HD):
+    """A bias that grows with the distance, as large as e^60, beside one that
+    falls as fast; caps on both sides of those that need no running maximum."""
+    shape, kernel = (1, 5, 10, 13, 3, HD), (3, 7, 9)
+    q, k, v, g = make(shape, 23, 4.0)
+    o = make_options(shape, 23, softcap, True, 2, 2, 1)
+    o["slopes"] = torch.tensor([[6.0, -7.0, -5.0], [-3.0, 8.0, 5.0], [0.0, -0.5, 0.25]])
+    want = ref.scored(q, k, v, kernel, dout=g, **o)
+    got = run(q, k, v, g, kernel, o)
+    for name in want:
+        ref.check(name, got[name], want[name])
+
+
+def test_extreme_documents_and_prefixes():
+    """Any negative document is padding, documents reach to 2^31 - 1; prefixes
+    below 0 and past the last frame."""
+    shape, kernel = (2, 5, 6, 9, 1, 32), (3, 3, 5)
+    q, k, v, g = make(shape, 29)
+    o = make_options(shape, 29)
+    o["doc"] = torch.full(shape[:4], 2 ** 31 - 1, dtype=torch.int32)
+    o["doc"][0, :, 3:] = 0
+    o["doc"][1, 2] = -2 ** 31
+    o["doc"][1, :, :, :2] = -1
+    for prefix in ((-5, 99), (0, -2 ** 31), (2 ** 31 - 1, 2)):
+        o["prefix"] = torch.tensor(prefix, dtype=torch.int64).to(torch.int32)
+        want = ref.scored(q, k, v, kernel, dout=g, **o)
+        got = run(q, k, v, g, kernel, o)
+        for name in want:
+            ref.check(name, got[name], want[name])
+
+
+def test_two_streams_at_once():
+    """Forward and backward on two streams, each with a workspace of its own."""
+    shape, kernel = (1, 6, 16, 18, 2, 64), (3, 5, 5)
+    data = [(make(shape, s), make_options(shape, s, 20.0, True, 2, 1)) for s in (1, 2)]
+    want = [ref.scored(*x[:3], kernel, dout=x[3], **o) for x, o in data]
+    streams = [torch.cuda.Stream() for _ in data]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    results = [None, None]
+    for _ in range(5):
+        for i, (x, o) in enumerate(data):
+            with torch.cuda.stream(streams[i]):
+                d, co = [y.cuda() for y in x], cuda(o)
+                out, lse = na.na3d_scored_attention(*d[:3], kernel, return_lse=True, **co)
+                grads = [torch.empty_like(d[0]) for _ in range(3)]
+                na.na3d_scored_bwd(*d[:3], out, lse, d[3], *grads, kernel, **co)
+                results[i] = (out, lse, *grads)
+    torch.cuda.synchronize()
+    for w, r in zip(want, results):
+        for name, x in zip(("out", "lse", "dq", "dk", "dv"), r):
+            ref.check(name, x, w[name])
+
+
+def test_stream_argument():
+    """stream= of another stream than the current one, the backward pass's own
+    workspace with it."""
+    shape, kernel = (1, 4, 9, 10, 2, 32), (3, 3, 3)
+    x = make(shape, 31)
+    d = [y.cuda() for y in x]
+    grads = [torch.empty_like(d[0]) for _ in range(3)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, lse = na.na3d_scored_attention(*d[:3], kernel, return_lse=True, stream=side)
+    na.na3d_scored_bwd(*d[:3], out, lse, d[3], *grads, kernel, stream=side)
+    side.synchronize()
+    want = ref.scored(*x[:3], kernel, dout=x[3])
+    for name, y in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        ref.check(name, y, want[name])
 
 
 def test_random_problems():
