@@ -103,10 +103,14 @@ def roofline_terms(shape, kernel, seconds, peaks, tc_tflops=None):
     }
 
 
+# what na3d_fwd's launches are made of: its kernels, its planner and their headers
+KERNEL_SOURCES = ("na3d_api.cu", "na3d_host.cuh", "na3d_kernel.cu", "na3d_kernel.cuh", "sm103_ptx.cuh")
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "neighborhood_attention_video_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in KERNEL_SOURCES:
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]
