@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 __all__ = [
     "NA3DError", "NA3DUnavailable", "na3d_attention", "na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region",
@@ -286,6 +287,21 @@ def _check_on_device(tensors):
             raise ValueError(f"{name} must be contiguous")
 
 
+def _check_bf16_of_shape(shape, names, tensors):
+    """The tensors are bf16, of one 6-D shape, on the current CUDA device."""
+    torch = _torch_module()
+    dev, bf16 = torch.cuda.current_device() if _cuda_ok else -2, torch.bfloat16
+    for name, t in zip(names, tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not bf16 or t.get_device() != dev:
+            raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the (B,T,H,W,NH,HD) shape of q")
+    if len(shape) != 6:
+        raise ValueError("q must have a 6-D (B,T,H,W,NH,HD) shape")
+
+
 def _empty(stream, like, shape, dtype):
     """A new tensor on the device of `like`, allocated on the stream that the
     call uses, so that the allocator may reuse its memory only behind the call."""
@@ -298,11 +314,27 @@ def _empty(stream, like, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+_kept = threading.local()   # a thread's workspaces, by device and stream; 16 at most
+
+
 def _workspace(work, need, like, stream):
-    """`work` where it is given and large enough, else a new workspace."""
+    """`work` where it is given and large enough. Else a workspace that this
+    thread keeps for the current stream: its calls run there one after another
+    (a new one for each call took 8 us of a 28 us call). A call on a stream of
+    the caller's, or one that is being captured and may be replayed beside later
+    calls, gets one of its own."""
     torch = _torch_module()
     if work is None:
-        return _empty(stream, like, (need,), torch.uint8)
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            return _empty(stream, like, (need,), torch.uint8)
+        kept = _kept.__dict__
+        key = (like.get_device(), _stream_handle(None))
+        work = kept.get(key)
+        if work is None or work.numel() < need:
+            if len(kept) >= 16:
+                kept.clear()
+            work = kept[key] = _empty(None, like, (need,), torch.uint8)
+        return work
     dev = torch.cuda.current_device() if _cuda_ok else -2
     if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
         raise TypeError("work must be a contiguous tensor on the current CUDA device")
@@ -328,11 +360,15 @@ def _scored_options(shape, softcap, slopes, doc, prefix):
     return softcap, ps, pd, pp
 
 
+def _shape_of(q):
+    if not isinstance(q, _torch_module().Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    return q.shape
+
+
 def _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc, prefix, stream) -> None:
     """The call behind na3d_scored_fwd: out and lse are as it needs them."""
     lib = _lib if _lib is not None else load_library()
-    if len(shape) != 6 or k.shape != shape or v.shape != shape:
-        raise ValueError("q, k, v and out must have the same 6-D (B,T,H,W,NH,HD) shape")
     KT, KH, KW = kernel_size
     rc = lib.na3d_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                              None if lse is None else lse.data_ptr(), *shape, int(KT), int(KH), int(KW),
@@ -351,10 +387,8 @@ def na3d_scored_fwd(q, k, v, out, kernel_size, lse=None, softcap=0.0, slopes=Non
     along T with a free prefix (``prefix``: int32 (B,) frames). ``lse``, where
     given, receives the fp32 (B, T, H, W, NH) log-sum-exp of the scores. q, k,
     v may be views with a token stride; ``out`` is contiguous. HD up to 128."""
-    _check_bf16_on_device((("q", q), ("k", k), ("v", v), ("out", out)))
-    shape = q.shape
-    if out.shape != shape:
-        raise ValueError("q, k, v and out must have the same 6-D (B,T,H,W,NH,HD) shape")
+    shape = _shape_of(q)
+    _check_bf16_of_shape(shape, ("q", "k", "v", "out"), (q, k, v, out))
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     if lse is not None:
@@ -367,8 +401,8 @@ def na3d_scored_attention(q, k, v, kernel_size, softcap=0.0, slopes=None, doc=No
     """``na3d_scored_fwd`` into a new tensor: returns out, or (out, lse) where
     ``return_lse`` is true (what ``na3d_scored_bwd`` needs)."""
     torch = _torch_module()
-    _check_bf16_on_device((("q", q), ("k", k), ("v", v)))
-    shape = q.shape
+    shape = _shape_of(q)
+    _check_bf16_of_shape(shape, ("q", "k", "v"), (q, k, v))
     out = _empty(stream, q, shape, torch.bfloat16)
     lse = _empty(stream, q, shape[:-1], torch.float32) if return_lse else None
     _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc, prefix, stream)
@@ -390,24 +424,22 @@ def na3d_scored_bwd(q, k, v, out, lse, dout, dq, dk, dv, kernel_size, softcap=0.
     the other arguments are the forward pass's. dq, dk and dv may be views with
     a token stride, e.g. ``qkv_views`` of a fused gradient. ``work``: a tensor of
     ``na3d_scored_bwd_workspace`` bytes, kept by the caller (one call at a time);
-    None allocates one."""
+    None takes one that the binding keeps (for this thread and the current
+    stream; a call with a ``stream`` or under capture allocates its own)."""
     lib = _lib if _lib is not None else load_library()
-    names = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
-    tensors = (q, k, v, out, dout, dq, dk, dv)
-    _check_bf16_on_device(zip(names, tensors))
-    shape = q.shape
-    if len(shape) != 6 or any(t.shape != shape for t in tensors):
-        raise ValueError("q, k, v, out, dout, dq, dk and dv must have the same 6-D (B,T,H,W,NH,HD) shape")
+    shape = _shape_of(q)
+    _check_bf16_of_shape(shape, ("q", "k", "v", "out", "dout", "dq", "dk", "dv"), (q, k, v, out, dout, dq, dk, dv))
     if not (out.is_contiguous() and dout.is_contiguous()):
         raise ValueError("out and dout must be contiguous")
     _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
     options = _scored_options(shape, softcap, slopes, doc, prefix)
-    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))]
-    KT, KH, KW = (int(x) for x in kernel_size)
+    strides = (_token_stride("q", q), _token_stride("k", k), _token_stride("v", v), _token_stride("dq", dq),
+               _token_stride("dk", dk), _token_stride("dv", dv))
+    KT, KH, KW = kernel_size
     work = _workspace(work, lib.na3d_scored_bwd_workspace(*shape[:5]), q, stream)
     rc = lib.na3d_scored_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(),
-                             *shape, KT, KH, KW, *strides, *options, _stream_handle(stream))
+                             *shape, int(KT), int(KH), int(KW), *strides, *options, _stream_handle(stream))
     if rc != NA3D_OK:
         raise NA3DError(rc, "na3d_scored_bwd")
 
@@ -449,7 +481,8 @@ def na3d_lora_qkv_proj(x, w, bias, lora_a, lora_b, scaling, offsets, adapter, qk
     (n_adapters,); offsets int32 (n_requests + 1,) and adapter int32
     (n_requests,) on the device. R is a multiple of 8 up to 128. ``work``: a
     tensor of ``na3d_lora_workspace`` bytes, kept by the caller (one call at a
-    time); None allocates one."""
+    time); None takes one that the binding keeps (for this thread and the current
+    stream; a call with a ``stream`` or under capture allocates its own)."""
     lib = _lib if _lib is not None else load_library()
     sizes = _check_lora(x, w, lora_a, lora_b, scaling, offsets, adapter, num_heads, head_dim)
     _check_bf16_on_device((("qkv", qkv),))

@@ -282,3 +282,57 @@ def test_packed_batch_trains_through_both():
         ref.check(name, x, att[name])
     for name, x in (("dx", dx), ("da", da), ("db", db)):
         ref.check(name, x, proj[name])
+
+
+def test_workspaces_of_calls_that_run_at_once():
+    """Calls without a ``work`` tensor, of growing and shrinking sizes: from two
+    threads on one stream and on streams of their own, and beside replays of a
+    graph that captured the same call. Each gives the bits it gives by itself."""
+    import threading
+    sizes = [(40, 1), (3000, 2), (9, 3), (6000, 4)]
+    data = []
+    for M, seed in sizes:
+        t, g = make(M, 256, 2, 64, 16, 2, seed)
+        d = {n: v.cuda() for n, v in t.items()}
+        off, ad = ints(0, M // 2, M).cuda(), ints(1, 0).cuda()
+        data.append((d, g.cuda(), (d["lora_a"], d["lora_b"], d["scaling"], off, ad)))
+
+    def call(i):
+        d, g, adapters = data[i]
+        qkv, dx, da, db = (torch.empty_like(x) for x in (g, d["x"], d["lora_a"], d["lora_b"]))
+        na.na3d_lora_qkv_proj(d["x"], d["w"], d["bias"], *adapters, qkv, 2, 64)
+        na.na3d_lora_qkv_proj_bwd(g, d["x"], d["w"], *adapters, dx, da, db, 2, 64)
+        return qkv, dx, da, db
+
+    want = [[x.clone() for x in call(i)] for i in range(4)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = call(3)
+    graph.replay()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(own_stream):
+        stream = torch.cuda.Stream() if own_stream else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            got = [(i, call(i)) for _ in range(6) for i in (1, 0, 3, 2)]
+        stream.synchronize()
+        wrong.extend(i for i, r in got for x, y in zip(r, want[i]) if not torch.equal(x, y))
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in (False, True, True)]
+    for th in threads:
+        th.start()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            graph.replay()
+    got = [(i, call(i)) for i in (3, 1, 2, 0)]
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not wrong
+    for i, r in got + [(3, captured)]:
+        for x, y in zip(r, want[i]):
+            assert torch.equal(x, y), i
+    assert na.na3d_device_status() == 0
