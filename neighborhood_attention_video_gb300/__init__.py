@@ -271,20 +271,25 @@ def qkv_views(qkv):
     return qkv.select(-3, 0), qkv.select(-3, 1), qkv.select(-3, 2)
 
 
+def _check_one(torch, dev, name, t, dtype, shape):
+    """t is a contiguous tensor of that dtype and shape on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on the current CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def _check_on_device(tensors):
     """Each (name, tensor, dtype, shape) is a contiguous tensor of that dtype
     and shape on the current CUDA device."""
     torch = _torch_module()
     dev = torch.cuda.current_device() if _cuda_ok else -2
     for name, t, dtype, shape in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not dtype or t.get_device() != dev:
-            raise TypeError(f"{name} must be a {dtype} tensor on the current CUDA device")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        _check_one(torch, dev, name, t, dtype, shape)
 
 
 def _check_bf16_of_shape(shape, names, tensors):
@@ -347,17 +352,25 @@ def _scored_options(shape, softcap, slopes, doc, prefix):
     """The score arguments of the na3d_scored_ calls, checked: (softcap, the
     three pointers or None)."""
     torch = _torch_module()
+    dev = torch.cuda.current_device() if _cuda_ok else -2
     ps = pd = pp = None
     if slopes is not None:
-        _check_on_device((("slopes", slopes, torch.float32, (shape[4], 3)),))
+        _check_one(torch, dev, "slopes", slopes, torch.float32, (shape[4], 3))
         ps = slopes.data_ptr()
     if doc is not None:
-        _check_on_device((("doc", doc, torch.int32, shape[:4]),))
+        _check_one(torch, dev, "doc", doc, torch.int32, shape[:4])
         pd = doc.data_ptr()
     if prefix is not None:
-        _check_on_device((("prefix", prefix, torch.int32, shape[:1]),))
+        _check_one(torch, dev, "prefix", prefix, torch.int32, shape[:1])
         pp = prefix.data_ptr()
     return softcap, ps, pd, pp
+
+
+def _token_strides(names, tensors):
+    """``_token_stride`` of tensors of one shape, which often share strides."""
+    first = tensors[0].stride()
+    ts = _token_stride(names[0], tensors[0])
+    return [ts if t.stride() == first else _token_stride(n, t) for n, t in zip(names, tensors)]
 
 
 def _shape_of(q):
@@ -372,7 +385,7 @@ def _call_scored_fwd(q, k, v, out, lse, shape, kernel_size, softcap, slopes, doc
     KT, KH, KW = kernel_size
     rc = lib.na3d_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                              None if lse is None else lse.data_ptr(), *shape, int(KT), int(KH), int(KW),
-                             _token_stride("q", q), _token_stride("k", k), _token_stride("v", v),
+                             *_token_strides(("q", "k", "v"), (q, k, v)),
                              *_scored_options(shape, softcap, slopes, doc, prefix), _stream_handle(stream))
     if rc != NA3D_OK:
         raise NA3DError(rc, "na3d_scored_fwd")
@@ -433,8 +446,7 @@ def na3d_scored_bwd(q, k, v, out, lse, dout, dq, dk, dv, kernel_size, softcap=0.
         raise ValueError("out and dout must be contiguous")
     _check_on_device((("lse", lse, _torch.float32, shape[:5]),))
     options = _scored_options(shape, softcap, slopes, doc, prefix)
-    strides = (_token_stride("q", q), _token_stride("k", k), _token_stride("v", v), _token_stride("dq", dq),
-               _token_stride("dk", dk), _token_stride("dv", dv))
+    strides = _token_strides(("q", "k", "v", "dq", "dk", "dv"), (q, k, v, dq, dk, dv))
     KT, KH, KW = kernel_size
     work = _workspace(work, lib.na3d_scored_bwd_workspace(*shape[:5]), q, stream)
     rc = lib.na3d_scored_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
