@@ -19,8 +19,9 @@
  * accumulation), and the output is rounded to bf16 (nearest even).
  *
  * The library allocates no memory and is safe to call from several host
- * threads at once. Its only state is a mutex-guarded cache of tiling plans
- * (keyed by grid and window sizes) and, per device, one word that records a
+ * threads at once. Its only state is two caches of tiling plans (keyed by grid
+ * and window sizes; one guarded by a mutex, the na3d_scored_ calls' one kept by
+ * each thread) and, per device and kernel family, one word that records a
  * pipeline-wait timeout plus the small table of words through which
  * na3d_device_status takes it (see there).
  */
@@ -189,7 +190,8 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv,
  * out_i = sum_j p_ij v_j with p the softmax of the s that are not masked, and
  * lse_i = log sum_j e^s. A row that sees nothing has out 0 and lse -infinity.
  * What masked keys and padding hold (infinities and NaN included) reaches no
- * row that does not see them. Sums, statistics and probabilities are fp32; the
+ * row that does not see them; values that are not finite cost time, though,
+ * since the rows about them are computed one by one. Sums, statistics and probabilities are fp32; the
  * probabilities are rounded to bf16 for their product with v, out is rounded
  * once.
  *
@@ -219,8 +221,8 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
  *   dq_i = sum_j da k_j,   dk_j = sum_i da q_i,   dv_j = sum_i p dout_i.
  * dq is the gradient of the scaled q that was passed. slopes, doc and prefix
  * are constants. The sums have a fixed order: equal inputs give equal bits.
- * p and da are rounded to bf16 for their products (fp32 sums), the gradients
- * once at the end.
+ * p and da are rounded to bf16 for their products (fp32 sums; for dq da is
+ * kept in two such parts), the gradients once at the end.
  *
  * out, lse: what na3d_scored_fwd wrote for the same arguments; dout: bf16,
  *   contiguous (B,T,H,W,NH,HD).

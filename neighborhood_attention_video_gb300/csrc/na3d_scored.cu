@@ -248,6 +248,13 @@ constexpr uint64_t kDrainLimitNs = 500000000ull;
 constexpr int kMaxStages = 6, kMaxRing = kMaxStages + 2;   // ring places: stages and fixed buffers
 constexpr int kControl = 8 + 8 * kMaxRing;                     // bytes of the control words
 
+// What the rounding of x and y to the pair p leaves of them, rounded itself. dQ
+// takes da in two such parts: of the three gradients it alone has the rounding
+// of out in it, through delta, and one rounding more would count.
+__device__ __forceinline__ uint32_t left_over(float x, float y, uint32_t p) {
+    return pack_bf16x2(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xffff0000u));
+}
+
 // The positions that row i of an axis of length N meets: keys of its window
 // (FWD, DQ), or the queries whose windows hold it (DKV). Both ends grow with i.
 __host__ __device__ __forceinline__ int range_lo(bool dkv, int i, int K, int N) {
@@ -486,6 +493,17 @@ __device__ __forceinline__ void next_unit(const ScoredParams& p, const TileGeom&
 // to be done with a stage starts the load of the chunk that is next to use it,
 // so no warp waits for an empty stage and none is kept for loading (a
 // thirteenth would cost the other twelve a fifth of their registers).
+//
+// What bounds it: latency. At (1,16,64,64,8,64) with a (3,7,7) window, cap and
+// bias (forward, @CLIP@ us) the schedulers issue in 45 % of the cycles with two
+// warps each, mma.sync takes 26 % of its pipe, memory 15 % of its rate; without
+// its loads the kernel takes 230 of 257 us, without its products 220, without
+// cap, bias and exponential 227, and without any step the units' and frames'
+// own work takes 95. More warps need registers that a step does not have to
+// spare: 12 warps of 168 registers 274 us, 16 of 128 spill, 446. Steps that
+// take the next one's scores early, or two or three steps at once, are 4 to 9 %
+// slower. Whole-row (3,7,33) windows with packed, padded clips at
+// (1,8,64,33,8,64): @ROWS@ us; HD 128, causal, at (1,8,48,64,16,128): @HD128@.
 template <int HD, int MODE>
 __global__ void __launch_bounds__(max_warps(HD, MODE) * 32, blocks_per_sm(HD, MODE))
 scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ CUtensorMap tm_f1,
@@ -968,7 +986,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                 mma16816(dp + 4, NFR < NF ? a : fa[NFR - 1][kk], e[1], e[3]);
                             }
                             uint64_t from[2] = {f2_dup(far_t[0] - ref[0]), f2_dup(far_t[1] - ref[1])};
-                            uint32_t pr[4], ds[4];   // probabilities and da, pairs: 2 * tile + row
+                            uint32_t pr[4], ds[4];   // probabilities (DQ: what da's rounding leaves) and da, pairs: 2 * tile + row
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 uint64_t minus_ref = 0, minus_delta = 0;
@@ -1009,8 +1027,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                     d = f2_mul(d, f2_pack(p0, p1));
                                     if (CAP) d = f2_mul(d, slope);
                                     f2_unpack(d, d0, d1);
-                                    pr[2 * j + i] = pack_bf16x2(p0, p1);
                                     ds[2 * j + i] = pack_bf16x2(d0, d1);
+                                    pr[2 * j + i] = MODE == kDq ? left_over(d0, d1, ds[2 * j + i]) : pack_bf16x2(p0, p1);
                                 }
                             }
 #pragma unroll
@@ -1024,6 +1042,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                 ldsm4t(ak[kk], f);
                                 mma16816(acc0[2 * kk], ds, f[0], f[1]);
                                 mma16816(acc0[2 * kk + 1], ds, f[2], f[3]);
+                                if (MODE == kDq) {
+                                    mma16816(acc0[2 * kk], pr, f[0], f[1]);
+                                    mma16816(acc0[2 * kk + 1], pr, f[2], f[3]);
+                                }
                             }
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk) ak[kk] += 16 * HDB * 2;
@@ -1183,11 +1205,19 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                         if (MODE != kFwd) {
                             const uint32_t a[4] = {pack_bf16x2(dp[0], dp[1]), pack_bf16x2(dp[2], dp[3]),
                                                    pack_bf16x2(dp[4], dp[5]), pack_bf16x2(dp[6], dp[7])};
+                            uint32_t rest[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (MODE == kDq) rest[j] = left_over(dp[2 * j], dp[2 * j + 1], a[j]);
 #pragma unroll
                             for (int kk = 0; kk < KB; ++kk) {
                                 ldsm4t(columns(a0, kk), f);
                                 mma16816(acc0[2 * kk], a, f[0], f[1]);
                                 mma16816(acc0[2 * kk + 1], a, f[2], f[3]);
+                                if (MODE == kDq) {
+                                    mma16816(acc0[2 * kk], rest, f[0], f[1]);
+                                    mma16816(acc0[2 * kk + 1], rest, f[2], f[3]);
+                                }
                             }
                         }
                     }
