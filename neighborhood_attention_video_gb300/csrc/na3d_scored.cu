@@ -495,15 +495,18 @@ __device__ __forceinline__ void next_unit(const ScoredParams& p, const TileGeom&
 // thirteenth would cost the other twelve a fifth of their registers).
 //
 // What bounds it: latency. At (1,16,64,64,8,64) with a (3,7,7) window, cap and
-// bias (forward, @CLIP@ us) the schedulers issue in 45 % of the cycles with two
-// warps each, mma.sync takes 26 % of its pipe, memory 15 % of its rate; without
+// bias (forward, 260 us) the schedulers issue in 36 % of the cycles with two
+// warps each, mma.sync takes 26 % of its pipe, memory 24 % of its rate; without
 // its loads the kernel takes 230 of 257 us, without its products 220, without
 // cap, bias and exponential 227, and without any step the units' and frames'
 // own work takes 95. More warps need registers that a step does not have to
 // spare: 12 warps of 168 registers 274 us, 16 of 128 spill, 446. Steps that
 // take the next one's scores early, or two or three steps at once, are 4 to 9 %
 // slower. Whole-row (3,7,33) windows with packed, padded clips at
-// (1,8,64,33,8,64): @ROWS@ us; HD 128, causal, at (1,8,48,64,16,128): @HD128@.
+// (1,8,64,33,8,64): 225 us; HD 128, causal, at (1,8,48,64,16,128): 387 us. A
+// training step at (1,16,32,48,8,64), (3,7,7): 111 us forward, 145 dQ, 248 dK
+// and dV (four products a step, and 11 columns of a row where the others have
+// 10: near a border more windows hold a key).
 template <int HD, int MODE>
 __global__ void __launch_bounds__(max_warps(HD, MODE) * 32, blocks_per_sm(HD, MODE))
 scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ CUtensorMap tm_f1,
@@ -1306,7 +1309,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 // (lse in log2 units, delta) of every row for the backward passes:
 // delta_i = dout_i . out_i; a row that sees nothing gets (0, 0). The pass for
 // dQ takes delta from here and leaves the sum of p dp, which is the same
-// without the rounding of out, in its place for the one for dK and dV. A row takes HD / 8 lanes, 16 bytes each.
+// without the rounding of out, in its place for the one for dK and dV. A row
+// takes HD / 8 lanes, 16 bytes each. Bound by its reads.
 template <int HD>
 __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t rows) {
     constexpr int L = HD / 8;
