@@ -390,17 +390,6 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
             : "memory");
     }
 }
-template <int CG>
-__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
-    if (CG == 1) {
-        tma_load_3d(dst, map, bar, c0, c1, c2);
-    } else {
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
-            "r"(bar) : "memory");
-    }
-}
 template <int CG, uint32_t ACC>
 __device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
     if (CG == 1) {
@@ -483,13 +472,14 @@ __device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& 
 // epilogue; 32 columns at a time take 103. Storing through shared memory, by
 // TMA (103 -> 111 us then) or in whole lines (102), does not help. At
 // 49152 x 2048 x 6144, rank 64, the tensor cores bound it (90 % of their cycles):
-// 702 us, 1.82 PFLOP/s. The backward product of 65536 x 1536 x 512 takes 97 us,
-// 72 to 82 without loads and epilogue.
+// 702 us, 1.82 PFLOP/s. The backward product of 65536 x 1536 x 512 takes 94 us
+// (72 to 82 without loads and epilogue, in pairs).
 template <bool BWD, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
           const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_l,
           const __grid_constant__ LoraParams p, const __grid_constant__ GemmParams q) {
+    static_assert(!BWD || CG == 1, "the backward product runs by blocks");
     using S = Shape<CG>;
     constexpr int kStages = S::kStages, A_TILE = S::A_TILE, STAGE = S::STAGE, BN = S::BN;
     constexpr int B_FULL = S::B_FULL, B_EMPTY = S::B_EMPTY, B_AFULL = S::B_AFULL, B_AEMPTY = S::B_AEMPTY, B_DRAIN = S::B_DRAIN;
@@ -574,7 +564,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                         load_2d<CG>(to + A_TILE, &tm_l, full, r0, w.a * p.N + n0);
                     } else {
                         for (int c = 0; c < BN / 64; ++c)
-                            load_3d<CG>(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
+                            tma_load_3d(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
                     }
                 }
         }
@@ -682,8 +672,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 for (int c = 0; c < 4; ++c) tmem_ld32(t_row + 32 * c, held + (BWD ? 32 * c : 0));
                 tmem_wait_ld();
                 tc_fence_before();
-                if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY)));
-                else mbar_arrive(sy.bar(B_AEMPTY));
+                mbar_arrive(sy.bar(B_AEMPTY));
             }
             const uint32_t buf = BWD ? 1u : lt & 1u;
             if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
@@ -769,7 +758,9 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------ few rows
 
-constexpr int kSmallRows = 32;   // up to here the product streams W past the rows
+// Up to here the product streams W past the rows: 32 rows of 2048 channels to
+// 6144 take 10.8 us so, 19.9 in the large product (512 to 1536: 5.1 and 10.4).
+constexpr int kSmallRows = 32;
 
 // t of up to kSmallRows rows, [row][R]: a warp for each value. Latency: 7 us by
 // itself, hidden behind the product's read of W.
@@ -1168,8 +1159,10 @@ cudaError_t down_t(const LoraParams& p, uint16_t* t, uint16_t* u, cudaStream_t s
 }
 
 cudaError_t down(const LoraParams& p, uint16_t* t, uint16_t* u, int sms, cudaStream_t stream) {
-    // 64 rows a block leave SMs idle below 64 * sms rows
-    const bool small = p.M < 64 * sms;
+    // Whole calls of 128 rows of 2048 channels take 18 us with 16 rows a block and 29 with 64, 1024
+    // rows 28.8 and 29.5; from 1536 rows on 64 are as good or better (512 channels: 11.6 and 9.4;
+    // 4096 rows: 17.2 and 14.8), since 16 read the adapter four times as often.
+    const bool small = p.M < 8 * sms;
     switch (padded_rank(p.R)) {
         case 16: return small ? down_t<16, 16>(p, t, u, stream) : down_t<16, 64>(p, t, u, stream);
         case 32: return small ? down_t<32, 16>(p, t, u, stream) : down_t<32, 64>(p, t, u, stream);
@@ -1213,9 +1206,13 @@ cudaError_t gemm_t(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t
 
 template <bool BWD>
 cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
-    // pairs where there is a tile of 256 rows for each
-    const int64_t tiles = (p.M / (2 * kBM)) * ceil_div(BWD ? p.C : p.N, kBN);
-    return tiles >= sms / 2 ? gemm_t<BWD, 2>(p, t, sms, stream) : gemm_t<BWD, 1>(p, t, sms, stream);
+    // Forward, pairs where each has six tiles of 256 rows: whole calls of 4096, 16384, 24576 and
+    // 65536 rows of 512 channels to 1536 take 17.8, 33.5, 44.1 and 107 us by pairs and 16.4, 32.7,
+    // 47.4 and 114 by blocks, 49152 of 2048 to 6144 753 and 794. Backward, by blocks: 65536 rows of
+    // 512 channels 195 us (by pairs 199), 49152 of 2048 1280 (1266).
+    if constexpr (!BWD)
+        if ((p.M / (2 * kBM)) * ceil_div(p.N, kBN) >= 3 * sms) return gemm_t<false, 2>(p, t, sms, stream);
+    return gemm_t<BWD, 1>(p, t, sms, stream);
 }
 
 template <int RP>

@@ -185,7 +185,7 @@ int check_lora_sizes(int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R, in
     if (!mul_ok(3 * NH, HD, N) || *N >= lim || M >= lim - 256 || C >= lim ||
         n_req >= lim / 128 - (M + 127) / 128 || n_ad >= lim / *N || n_ad >= lim / 128 ||
         !mul_ok(M, *N, &b) || !mul_ok(b, 2, &b) || !mul_ok(M, C, &b) || !mul_ok(b, 2, &b) ||
-        !mul_ok(n_ad * R, *N, &b) || !mul_ok(b, 2, &b) || !mul_ok(n_ad * R, C, &b) || !mul_ok(b, 2, &b))
+        !mul_ok(n_ad * 128, *N + C, &b) || !mul_ok(b, 8, &b))   // adapters, and the workspace's sums of them
         return NA3D_ERR_OVERFLOW;
     *work_bytes = na3d::lora_workspace(M, C, *N, R, n_req, n_ad, backward);
     return NA3D_OK;

@@ -63,6 +63,10 @@ CASES = [
     (20045, 72, 3, 32, 24, 3, (5, 100, 300, 384, 9001, 20000), (0, 2, 1, 0, 2)),
     (20045, 264, 2, 16, 128, 2, (0, 10000, 20045), (1, 0)),
     (19456, 328, 1, 128, 64, 1, (0, 19456), (0,)),
+    # and more of them: six tiles for each pair
+    (58477, 72, 3, 32, 24, 3, (5, 100, 300, 384, 9001, 58400), (0, 2, 1, 0, 2)),
+    (30001, 264, 5, 64, 128, 2, (0, 10000, 30001), (1, 0)),
+    (25600, 136, 3, 128, 64, 1, (0, 25600), (0,)),
 ]
 
 
@@ -105,7 +109,7 @@ def test_without_adapters_it_is_the_base_projection():
     assert bool((got["da"] == 0).all()) and bool((got["db"] == 0).all())
 
 
-@pytest.mark.parametrize("M", [6, 150, 20000])
+@pytest.mark.parametrize("M", [6, 150, 20000, 58600])
 def test_requests_do_not_reach_one_another(M):
     """A request's rows are what they are by themselves whatever the other
     requests, their adapters included, hold."""
@@ -127,7 +131,7 @@ def test_requests_do_not_reach_one_another(M):
         assert torch.equal(got[name][0], clean[name][0]), name
 
 
-@pytest.mark.parametrize("M,n_req", [(3000, 1500), (20, 2000), (19500, 40)])
+@pytest.mark.parametrize("M,n_req", [(3000, 1500), (20, 2000), (19500, 40), (58600, 1100)])
 def test_many_requests(M, n_req):
     """More requests than a block keeps at hand, most of them empty or of one row."""
     gen = torch.Generator().manual_seed(M)

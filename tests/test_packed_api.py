@@ -142,6 +142,14 @@ def test_workspace_sizes(lib):
         na.na3d_lora_workspace(100, 64, 2, 32, 12, 3, 2)
 
 
+def test_lora_workspace_past_int64_is_refused(lib):
+    """The adapters' sums of these sizes hold 2^60 values, each size by itself in range."""
+    sizes = (100, (1 << 31) - 8, 1, 16, 128, 3, 1 << 23)
+    assert lora(lib, True, sizes=sizes) == ERR_OVERFLOW
+    with pytest.raises(ValueError):
+        na.na3d_lora_workspace(*sizes, backward=True)
+
+
 def test_binding_wants_device_tensors():
     x = torch.zeros(1, 4, 8, 16, 2, 32, dtype=torch.bfloat16)
     lse = torch.zeros(1, 4, 8, 16, 2)
