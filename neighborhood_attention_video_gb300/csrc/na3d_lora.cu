@@ -677,23 +677,36 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
             const uint32_t buf = BWD ? 1u : lt & 1u;
             if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
             tc_fence_after();
+            if (BWD) {   // all sums first: the next tile's are waiting for the accumulator
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float acc[32];
+                    tmem_ld32(t_row + kBN + 32 * c, acc);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) held[BWD ? 32 * c + j : 0] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
+                }
+                tc_fence_before();
+                mbar_arrive(sy.bar(B_AEMPTY + 1));
+            }
             constexpr int W = 32;   // columns at a time (64: longer bursts of stores, 109 us for 103 at 65536 x 512 x 1536)
 #pragma unroll
             for (int c = 0; c < 128 / W; ++c) {
                 const int c0 = n0 + W * c;
                 float acc[W];
-                tmem_ld32(t_row + buf * kBN + W * c, acc);
-                tmem_wait_ld();
-                if (c == 128 / W - 1) {   // the accumulator is read
-                    tc_fence_before();
-                    if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + buf)));
-                    else mbar_arrive(sy.bar(B_AEMPTY + buf));
-                }
-                if (c0 >= q.cols || row >= p.M) continue;
                 if (BWD) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) acc[j] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
+                    for (int j = 0; j < W; ++j) acc[j] = held[BWD ? W * c + j : 0];
+                } else {
+                    tmem_ld32(t_row + buf * kBN + W * c, acc);
+                    tmem_wait_ld();
+                    if (c == 128 / W - 1) {   // the accumulator is read
+                        tc_fence_before();
+                        if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + buf)));
+                        else mbar_arrive(sy.bar(B_AEMPTY + buf));
+                    }
                 }
+                if (c0 >= q.cols || row >= p.M) continue;
                 float top = 0.f;
 #pragma unroll
                 for (int j = 0; j < W; j += 2)
@@ -1082,10 +1095,13 @@ __global__ void __launch_bounds__(256) lora_grad_sum(const LoraParams p, const P
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Runs of chunks that lora_grad's blocks share a column block's rows by: about
-// three blocks an SM.
-int grad_splits(int64_t M, int64_t C, int64_t N) {
-    const int64_t s = ceil_div(3 * 152, ceil_div(C, 128) + ceil_div(N, 128)), most = ceil_div(M, kChunk);
+// Runs of chunks that lora_grad's blocks share a column block's rows by. Blocks
+// that are all resident at once: 65536 rows of 512 channels take, whole calls,
+// at ranks 16, 32, 64 and 128 with 2 blocks an SM 216, 222, 242 and 332 us, with
+// 3 194, 200, 259 and 363, with 4 186, 210, 246 and 337.
+int grad_splits(int64_t M, int64_t C, int64_t N, int64_t R) {
+    const int rp = padded_rank(int(R)), per_sm = rp == 16 ? 4 : rp == 32 ? 3 : 2;
+    const int64_t s = per_sm * 152 / (ceil_div(C, 128) + ceil_div(N, 128)), most = ceil_div(M, kChunk);
     return int(s < 1 ? 1 : s > most ? most : s);
 }
 
@@ -1100,7 +1116,7 @@ Work lay_out(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req, int64_t 
     w.u = w.t + align256(pairs);
     w.plan = w.u + (backward ? align256(pairs) : 0);
     w.part = w.plan + (backward ? align256((3 * n_req + 2 * n_ad + 4) * 4) : 0);
-    w.bytes = w.part + (backward ? (grad_splits(M, C, N) + n_ad) * rp * (C + N) * 4 : 0);
+    w.bytes = w.part + (backward ? (grad_splits(M, C, N, R) + n_ad) * rp * (C + N) * 4 : 0);
     return w;
 }
 
@@ -1220,7 +1236,7 @@ cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const ui
     constexpr int smem = kGradStages * (kChunk * 256 + kChunk * RP * 2);
     cudaError_t e = cudaFuncSetAttribute(lora_grad<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int splits = grad_splits(p.M, p.C, p.N);
+    const int splits = grad_splits(p.M, p.C, p.N, p.R);
     const dim3 grid(unsigned(ceil_div(p.C, 128) + ceil_div(p.N, 128)), unsigned(splits));
     e = launch_dependent(lora_grad<RP>, grid, 256, smem, stream, 1, p, q, t, u, part, splits, p.dx != nullptr);
     if (e != cudaSuccess) return e;
