@@ -390,6 +390,17 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, ui
             : "memory");
     }
 }
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+    if (CG == 1) {
+        tma_load_3d(dst, map, bar, c0, c1, c2);
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2),
+            "r"(bar) : "memory");
+    }
+}
 template <int CG, uint32_t ACC>
 __device__ __forceinline__ void umma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
     if (CG == 1) {
@@ -472,14 +483,13 @@ __device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& 
 // epilogue; 32 columns at a time take 103. Storing through shared memory, by
 // TMA (103 -> 111 us then) or in whole lines (102), does not help. At
 // 49152 x 2048 x 6144, rank 64, the tensor cores bound it (90 % of their cycles):
-// 702 us, 1.82 PFLOP/s. The backward product of 65536 x 1536 x 512 takes 94 us
-// (72 to 82 without loads and epilogue, in pairs).
+// 702 us, 1.82 PFLOP/s. The backward product of 65536 x 1536 x 512 takes 93 us;
+// 97 while it stored before it freed the second accumulator.
 template <bool BWD, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
           const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_l,
           const __grid_constant__ LoraParams p, const __grid_constant__ GemmParams q) {
-    static_assert(!BWD || CG == 1, "the backward product runs by blocks");
     using S = Shape<CG>;
     constexpr int kStages = S::kStages, A_TILE = S::A_TILE, STAGE = S::STAGE, BN = S::BN;
     constexpr int B_FULL = S::B_FULL, B_EMPTY = S::B_EMPTY, B_AFULL = S::B_AFULL, B_AEMPTY = S::B_AEMPTY, B_DRAIN = S::B_DRAIN;
@@ -564,7 +574,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                         load_2d<CG>(to + A_TILE, &tm_l, full, r0, w.a * p.N + n0);
                     } else {
                         for (int c = 0; c < BN / 64; ++c)
-                            tma_load_3d(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
+                            load_3d<CG>(to + A_TILE + c * (rb * 128), &tm_l, full, n0 + c * 64, r0, w.a);
                     }
                 }
         }
@@ -672,7 +682,8 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                 for (int c = 0; c < 4; ++c) tmem_ld32(t_row + 32 * c, held + (BWD ? 32 * c : 0));
                 tmem_wait_ld();
                 tc_fence_before();
-                mbar_arrive(sy.bar(B_AEMPTY));
+                if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY)));
+                else mbar_arrive(sy.bar(B_AEMPTY));
             }
             const uint32_t buf = BWD ? 1u : lt & 1u;
             if (!sy.wait(sy.bar(B_AFULL + buf), (BWD ? lt : lt >> 1) & 1u)) break;
@@ -687,7 +698,8 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                     for (int j = 0; j < 32; ++j) held[BWD ? 32 * c + j : 0] = fmaf(held[BWD ? 32 * c + j : 0], p.q_scale, acc[j]);
                 }
                 tc_fence_before();
-                mbar_arrive(sy.bar(B_AEMPTY + 1));
+                if (CG == 2) arrive_cluster(leaders(sy.bar(B_AEMPTY + 1)));
+                else mbar_arrive(sy.bar(B_AEMPTY + 1));
             }
             constexpr int W = 32;   // columns at a time (64: longer bursts of stores, 109 us for 103 at 65536 x 512 x 1536)
 #pragma unroll
@@ -959,7 +971,7 @@ constexpr int kGradStages = 3;
 // are in the order of the adapters, and writes a sum for each adapter that it
 // meets. Part s + a: along the runs one of the two grows, so the parts are as
 // few as splits and adapters together. Bound by the read of x and dqkv: 65536 x
-// (512 + 1536) at rank 16 in 58 us, 4.7 TB/s.
+// (512 + 1536) at rank 16 in 49 us, 5.5 TB/s.
 template <int RP>
 __global__ void __launch_bounds__(256) lora_grad(const LoraParams p, const Plan q, const uint16_t* tt, const uint16_t* uu,
                                                  float* part, int splits, bool beside) {
@@ -1222,13 +1234,12 @@ cudaError_t gemm_t(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t
 
 template <bool BWD>
 cudaError_t gemm(const LoraParams& p, const uint16_t* t, int sms, cudaStream_t stream) {
-    // Forward, pairs where each has six tiles of 256 rows: whole calls of 4096, 16384, 24576 and
+    // Pairs where each has six tiles of 256 rows. Whole forward calls of 4096, 16384, 24576 and
     // 65536 rows of 512 channels to 1536 take 17.8, 33.5, 44.1 and 107 us by pairs and 16.4, 32.7,
-    // 47.4 and 114 by blocks, 49152 of 2048 to 6144 753 and 794. Backward, by blocks: 65536 rows of
-    // 512 channels 195 us (by pairs 199), 49152 of 2048 1280 (1266).
-    if constexpr (!BWD)
-        if ((p.M / (2 * kBM)) * ceil_div(p.N, kBN) >= 3 * sms) return gemm_t<false, 2>(p, t, sms, stream);
-    return gemm_t<BWD, 1>(p, t, sms, stream);
+    // 47.4 and 114 by blocks, 49152 of 2048 to 6144 753 and 794; backward 16384 and 65536 rows of 512
+    // channels 63.4 and 187 by pairs, 61.5 and 190 by blocks, 49152 of 2048 1263 and 1294.
+    return (p.M / (2 * kBM)) * ceil_div(BWD ? p.C : p.N, kBN) >= 3 * sms ? gemm_t<BWD, 2>(p, t, sms, stream)
+                                                                        : gemm_t<BWD, 1>(p, t, sms, stream);
 }
 
 template <int RP>

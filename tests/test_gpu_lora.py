@@ -64,8 +64,8 @@ CASES = [
     (20045, 264, 2, 16, 128, 2, (0, 10000, 20045), (1, 0)),
     (19456, 328, 1, 128, 64, 1, (0, 19456), (0,)),
     # and more of them: six tiles for each pair
-    (58477, 72, 3, 32, 24, 3, (5, 100, 300, 384, 9001, 58400), (0, 2, 1, 0, 2)),
-    (30001, 264, 5, 64, 128, 2, (0, 10000, 30001), (1, 0)),
+    (58477, 264, 3, 32, 24, 3, (5, 100, 300, 384, 9001, 58400), (0, 2, 1, 0, 2)),
+    (30001, 776, 5, 64, 128, 2, (0, 10000, 30001), (1, 0)),
     (25600, 136, 3, 128, 64, 1, (0, 25600), (0,)),
 ]
 
@@ -113,7 +113,7 @@ def test_without_adapters_it_is_the_base_projection():
 def test_requests_do_not_reach_one_another(M):
     """A request's rows are what they are by themselves whatever the other
     requests, their adapters included, hold."""
-    C, NH, HD = 128, 2, 64
+    C, NH, HD = 264 if M > 50000 else 128, 2, 64   # pairs of blocks in both directions
     t, g = make(M, C, NH, HD, 16, 2, 2)
     cuts = (0, 2, 4, 6) if M == 6 else (0, 50, 100, M)
     off, ad = ints(*cuts), ints(0, 1, 0)
@@ -135,7 +135,7 @@ def test_requests_do_not_reach_one_another(M):
 def test_many_requests(M, n_req):
     """More requests than a block keeps at hand, most of them empty or of one row."""
     gen = torch.Generator().manual_seed(M)
-    C, NH, HD, R, n_ad = 64, 2, 64, 16, 7
+    C, NH, HD, R, n_ad = 264 if M > 50000 else 64, 2, 64, 16, 7
     off = torch.randint(0, M + 1, (n_req + 1,), generator=gen).sort().values.to(torch.int32)
     ad = torch.randint(-1, n_ad, (n_req,), generator=gen).to(torch.int32)
     t, g = make(M, C, NH, HD, R, n_ad, 9)
