@@ -203,6 +203,10 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv,
  *   (B) or NULL. All DEVICE pointers, 4-byte aligned, read when the kernels
  *   run (a replayed graph sees their current contents).
  * HD: 16, 32, 64 or 128; other powers of two return NA3D_ERR_UNSUPPORTED.
+ * Windows: the masks of a frame's part of a window lie in shared memory. Up to
+ *   KH * KW = 2^14 keys they always fit; larger windows that do not (from about
+ *   28000 keys on, by shape and pass) return NA3D_ERR_UNSUPPORTED, and so do
+ *   grids of more than 2^31 - 1 tiles of up to 16 rows and KT above 2^23.
  * out and lse must not overlap an input or one another. All other arguments,
  * the errors, the asynchrony and the capture into graphs are those of
  * na3d_fwd_strided.

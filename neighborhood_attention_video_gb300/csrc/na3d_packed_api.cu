@@ -83,8 +83,6 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
         for (const Span& b : read)
             if (a.ptr && b.ptr && overlaps(a.ptr, a.bytes, b.ptr, b.bytes)) return NA3D_ERR_ALIAS;
     if (lse && overlaps(out, n * row * 2, lse, n * NH * 4)) return NA3D_ERR_ALIAS;
-    int sms;
-    if (const int rc = na3d::current_device(&sms)) return rc;
 
     na3d::ScoredParams p{};
     p.B = int32_t(B); p.T = int32_t(T); p.H = int32_t(H); p.W = int32_t(W); p.NH = int32_t(NH);
@@ -99,6 +97,9 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
     p.slopes = slopes;
     p.doc = doc;
     p.prefix = prefix;
+    if (!na3d::scored_planned(int(HD), p, false)) return NA3D_ERR_UNSUPPORTED;
+    int sms;
+    if (const int rc = na3d::current_device(&sms)) return rc;
     return na3d::launch_scored_fwd(int(HD), p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? NA3D_OK
                                                                                                        : NA3D_ERR_CUDA;
 }
@@ -143,8 +144,6 @@ int na3d_scored_bwd(const void* q, const void* k, const void* v, const void* out
             if (written_overlap(grads[i], bytes[3 + i], ts[3 + i], grads[j], bytes[3 + j], ts[3 + j], row))
                 return NA3D_ERR_ALIAS;
     }
-    int sms;
-    if (const int rc = na3d::current_device(&sms)) return rc;
 
     na3d::ScoredParams p{};
     p.B = int32_t(B); p.T = int32_t(T); p.H = int32_t(H); p.W = int32_t(W); p.NH = int32_t(NH);
@@ -165,6 +164,9 @@ int na3d_scored_bwd(const void* q, const void* k, const void* v, const void* out
     p.slopes = slopes;
     p.doc = doc;
     p.prefix = prefix;
+    if (!na3d::scored_planned(int(HD), p, true)) return NA3D_ERR_UNSUPPORTED;
+    int sms;
+    if (const int rc = na3d::current_device(&sms)) return rc;
     return na3d::launch_scored_bwd(int(HD), p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? NA3D_OK
                                                                                                        : NA3D_ERR_CUDA;
 }

@@ -1286,6 +1286,13 @@ cudaError_t bwd(const ScoredParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+bool scored_planned(int hd, const ScoredParams& p, bool backward) {
+    constexpr int kSms = 152;   // whether there is a plan does not depend on it
+    TileGeom g;
+    if (!backward) return cached_plan(&g, p, hd, kFwd, kSms);
+    return cached_plan(&g, p, hd, kDq, kSms) && cached_plan(&g, p, hd, kDkv, kSms);
+}
+
 cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream) {
     switch (hd) {
         case 16: return launch_tiles<16, kFwd>(p, sms, stream);

@@ -167,42 +167,61 @@ __host__ __device__ __forceinline__ bool has_frame(const Unit& x, int t) { retur
 // multiple of step: inside an axis K + step - 1; a key near a border is held
 // by up to K + K/2 queries' windows, most in the rows around K and N - K.
 inline int widest(bool dkv, int step, int K, int N) {
-    const int inner = K + step - 1 < N ? K + step - 1 : N;
+    const int inner = K <= N - step ? K + step - 1 : N;
     if (!dkv) return inner;
     int best = inner;
     const int at[2] = {(K - 1) / step * step, (N - K) / step * step};
     for (const int i : at) {
-        const int last = i + step - 1 < N ? i + step - 1 : N - 1;
+        const int last = i < N - step ? i + step - 1 : N - 1;
         const int e = range_hi(true, last, K, N) - range_lo(true, i, K, N);
         if (e > best) best = e;
     }
     return best;
 }
 
-inline int align_up(int x, int a) { return (x + a - 1) / a * a; }
+inline int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kSmemMax = 227 * 1024;
 
-// Shared memory of a geometry with `stages` stages and chunks of cr x cc.
-inline void lay_out(TileGeom* g, int hd, int mode, bool docs) {
+// Shared memory of a geometry with `stages` stages and chunks of cr x cc; false where it is more
+// than `room`. The sizes are summed in 64 bits: a large window's masks alone pass 2^31 bytes.
+inline bool lay_out(TileGeom* g, int hd, int mode, bool docs, int64_t frame_steps, int room) {
     const bool dkv = mode == kDkv;
-    const int nf = (mode == kFwd ? 1 : 2) * fixed_buffers(hd, mode);
-    const int hdb = hd > 64 ? 64 : hd, reg = hd > 64 ? hd / 64 : 1;
-    const int f_region = align_up(g->st * g->bh * g->sw * hdb * 2, 1024);
-    g->x_bytes = align_up((g->cr * g->cc + 16) * hdb * 2, 1024) * reg;
-    g->off_x = f_region * reg * nf;
-    g->off_stat = g->off_x + 2 * g->stages * g->x_bytes;
-    g->off_doc = g->off_stat + (dkv ? g->nw * g->chunk_steps * 16 * 8 : 0);
-    g->off_lut = g->off_doc + (docs ? g->nw * g->chunk_steps * 16 * 4 : 0);
-    g->off_hw = align_up(g->off_lut + g->nw * (g->lut ? g->sh * g->sw * g->lut_pitch * 4 : g->frame_steps * 32), 16);
-    g->off_bar = align_up(g->off_hw + (g->cr * g->cc + 16) * 8, 16);
-    g->smem = g->off_bar + kControl + 8 * kMaxRing + 1024;
+    const int64_t nf = (mode == kFwd ? 1 : 2) * fixed_buffers(hd, mode), nw = g->nw, columns = int64_t(g->cr) * g->cc + 16;
+    const int64_t chunk = nw * g->chunk_steps * 16;
+    const int64_t hdb = hd > 64 ? 64 : hd, reg = hd > 64 ? hd / 64 : 1;
+    const int64_t f_region = align_up(int64_t(g->st) * g->bh * g->sw * hdb * 2, 1024);
+    const int64_t x_bytes = align_up(columns * hdb * 2, 1024) * reg;
+    const int64_t off_x = f_region * reg * nf;
+    const int64_t off_stat = off_x + 2 * g->stages * x_bytes;
+    const int64_t off_doc = off_stat + (dkv ? chunk * 8 : 0);
+    const int64_t off_lut = off_doc + (docs ? chunk * 4 : 0);
+    const int64_t pitch = frame_steps * 16 + 8;
+    const int64_t off_hw = align_up(off_lut + nw * (g->lut ? g->sh * g->sw * pitch * 4 : frame_steps * 32), 16);
+    const int64_t off_bar = align_up(off_hw + columns * 8, 16);
+    const int64_t smem = off_bar + kControl + 8 * kMaxRing + 1024;
+    if (smem > room) return false;
+    g->frame_steps = int32_t(frame_steps);
+    g->lut_pitch = int32_t(pitch);
+    g->x_bytes = int32_t(x_bytes);
+    g->off_x = int32_t(off_x);
+    g->off_stat = int32_t(off_stat);
+    g->off_doc = int32_t(off_doc);
+    g->off_lut = int32_t(off_lut);
+    g->off_hw = int32_t(off_hw);
+    g->off_bar = int32_t(off_bar);
+    g->smem = int32_t(smem);
+    return true;
 }
 
-// Chooses rows, brick and chunks for the least modelled time.
+// Chooses rows, brick and chunks for the least modelled time; false where none holds the problem:
+// the masks of a frame's window, 2 bytes a key, want room for one warp's at least.
 inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, int sms) {
     const bool dkv = mode == kDkv, docs = p.doc != nullptr;
-    const int blocks = blocks_per_sm(hd, mode);
+    const int blocks = blocks_per_sm(hd, mode), room = kSmemMax / blocks - 1024;
+    // positions and bricks past an axis' end are still numbers, frames' distances exact in fp32
+    constexpr int most = INT32_MAX - 4096;
+    if (p.T > most || p.H > most || p.W > most || p.KT > (1 << 23) || int64_t(p.KH) * p.KW * 2 > kSmemMax) return false;
     double best_cost = 0;
     bool found = false;
     for (int st = 1; st <= 16; st *= 2)
@@ -220,6 +239,7 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
                 g.nbt = (p.T + st - 1) / st;
                 g.nbh = (p.H + g.bh - 1) / g.bh;
                 g.nbw = (p.W + sw - 1) / sw;
+                // (at most 2^34 rows, a unit for each at worst)
                 const int64_t units = int64_t(p.B) * g.nbt * g.nbh * g.nbw * p.NH;
                 if (units >= (int64_t(1) << 31)) continue;
                 g.units = int32_t(units);
@@ -227,8 +247,8 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
                 const int eh = widest(dkv, g.bh, p.KH, p.H);
                 // chunks: whole rows of the box, as many as leave room for two
                 // stages; narrower ones where a single row does not
-                const int room = kSmemMax / blocks - 1024;
                 g.nwc = (ew + 255) / 256;
+                if (int64_t(eh_w) * ew * 2 > room) continue;
                 for (int parts = (eh + 255) / 256;; ++parts) {
                     if (parts > eh) break;
                     g.cc = (ew + g.nwc - 1) / g.nwc;
@@ -238,31 +258,30 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
                     g.nhc = nhc;
                     // steps of a warp: its box in each chunk that it meets, rounded up to 16
                     const int met = (eh_w + g.cr - 2) / g.cr + 1 < nhc ? (eh_w + g.cr - 2) / g.cr + 1 : nhc;
-                    const int all = et * g.nwc * ((eh_w * g.cc + 15) / 16 + met - 1);
+                    const int64_t frame = int64_t(g.nwc) * ((int64_t(eh_w) * g.cc + 15) / 16 + met - 1);
                     // the table of a frame (its pitch puts the rows of four lanes in different
                     // banks), or mask words where it does not fit
-                    g.frame_steps = all / et;
+                    const int64_t chunks = int64_t(et) * nhc * g.nwc;
                     g.chunk_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
-                    g.stages = et * nhc * g.nwc < 2 ? 1 : 2;
+                    g.stages = chunks < 2 ? 1 : 2;
                     g.lut = 1;
-                    g.lut_pitch = g.frame_steps * 16 + 8;
-                    lay_out(&g, hd, mode, docs);
-                    if (g.smem > room) {
+                    if (!lay_out(&g, hd, mode, docs, frame, room)) {
                         g.lut = 0;
-                        lay_out(&g, hd, mode, docs);
+                        if (!lay_out(&g, hd, mode, docs, frame, room)) {
+                            if (g.cr > 1) {   // on to the next smaller cr
+                                parts = (eh + g.cr - 2) / (g.cr - 1) - 1;
+                                continue;
+                            }
+                            if (found || g.cc == 1) break;
+                            g.nwc *= 2;
+                            parts = (eh + 255) / 256 - 1;
+                            continue;
+                        }
                     }
-                    if (g.smem > room) {
-                        if (g.cr > 1) continue;
-                        if (found || g.cc == 1) break;   // a column a chunk always fits
-                        g.nwc *= 2;
-                        parts = (eh + 255) / 256 - 1;
-                        continue;
-                    }
-                    while (g.stages < kMaxStages && g.stages < et * nhc * g.nwc) {
+                    while (g.stages < kMaxStages && g.stages < chunks) {
                         TileGeom more = g;
                         ++more.stages;
-                        lay_out(&more, hd, mode, docs);
-                        if (more.smem > room) break;
+                        if (!lay_out(&more, hd, mode, docs, frame, room)) break;
                         g = more;
                     }
                     // cycles: a step issues about 140 instructions (more without the table) on
@@ -270,8 +289,8 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
                     // load takes its latency and 60 bytes a cycle, and hides behind the
                     // computation, all of it where two frames fit
                     const double instr = (mode == kFwd ? 140.0 : 190.0) * (hd + 64) / 128 * (g.lut ? 1.0 : 1.4);
-                    const double work = double(all) / et * nw * blocks * instr / 2.6;
-                    const double lat = double(all) / et * instr * 2.5;
+                    const double work = double(frame) * nw * blocks * instr / 2.6;
+                    const double lat = double(frame) * instr * 2.5;
                     const double comp = work > lat ? work : lat;
                     const double load = 1000.0 + double(g.nwc) * nhc * g.cr * g.cc * hd * 4 * blocks / 60.0;
                     const bool deep = g.stages >= 2 * g.nwc * nhc;

@@ -90,6 +90,17 @@ def test_scored_bwd_takes_a_fused_gradient(lib):
     assert fwd(lib) == ERR_CUDA and fwd(lib, lse=0) == ERR_CUDA and fwd(lib, softcap=30.0) == ERR_CUDA
 
 
+def test_windows_without_a_plan_are_refused(lib):
+    """... as unsupported, before anything is enqueued, not as a CUDA error."""
+    wide, kernel = (1, 1, 600, 600, 1, 64), (1, 511, 511)
+    far = {n: (i + 1) << 36 for i, n in enumerate(("q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv", "work"))}
+    assert fwd(lib, wide, kernel, **{n: far[n] for n in ("q", "k", "v", "out", "lse")}) == ERR_UNSUPPORTED
+    call = lib.na3d_scored_bwd
+    assert call(*[P(x) for x in far.values()], *wide, *kernel, *(64,) * 6, 0.0, None, None, None, None) == ERR_UNSUPPORTED
+    many = (1 << 30, 1, 1, 1, 4, 16)
+    assert fwd(lib, many, (1, 1, 1), **{n: (i + 1) << 40 for i, n in enumerate(("q", "k", "v", "out", "lse"))}) == ERR_UNSUPPORTED
+
+
 def lora(lib, backward, sizes=(100, 64, 2, 32, 16, 3, 2), **ptrs):
     names = ("x", "w", "bias", "a", "b", "scaling", "offsets", "adapter", "qkv", "work")
     if backward:

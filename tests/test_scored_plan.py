@@ -62,3 +62,30 @@ def test_random_walks_stay_inside(walk):
             problems.append((shape, kernel, rng.randrange(2), rng.randrange(3)))
     for problem, line in walk(problems):
         assert line.startswith("ok "), (problem, line)
+
+
+def test_large_windows_are_planned_or_refused(walk):
+    """Windows of a frame up to the whole grid of 2^31 positions: a plan whose shared
+    memory fits, or none. Up to 2^14 keys there always is one."""
+    rng = random.Random(2)
+    problems = [((1, 1, n, m, 1, hd), (1, a, b), d, mode)
+                for n, m, a, b in ((600, 600, 511, 511), (300, 300, 299, 299), (400, 400, 255, 255),
+                                   (40001, 40001, 30001, 30001), (4, 2000000, 1, 1999999), (65537, 65537, 65535, 65535),
+                                   (1, 2 ** 31 - 1, 1, 2 ** 31 - 1), (2 ** 31 - 1, 1, 2 ** 31 - 1, 1))
+                for hd in (16, 128) for d in (0, 1) for mode in (0, 1, 2)]
+    problems += [((1, 2 ** 31 - 1, 1, 1, 1, 16), (2 ** 31 - 1, 1, 1), 0, mode) for mode in (0, 1, 2)]
+    problems += [((2 ** 30, 1, 1, 1, 4, 16), (1, 1, 1), 0, mode) for mode in (0, 1, 2)]
+    small = len(problems)
+    while len(problems) < 300:
+        area = 2 ** rng.uniform(10, 17.5)
+        kh = min(int(2 ** rng.uniform(0, 17.5)), int(area)) | 1
+        kw = max(1, int(area / kh)) | 1
+        grid = (kh + rng.choice((0, 1, 7, kh)), kw + rng.choice((0, 1, 7, kw)))
+        if grid[0] * grid[1] <= 60000:
+            problems.append(((1, 1, *grid, 1, rng.choice((16, 32, 64, 128))), (1, kh, kw), rng.randrange(2), rng.randrange(3)))
+    lines = walk(problems)
+    for i, ((shape, kernel, docs, mode), line) in enumerate(lines):
+        assert line == "unplanned" or line.startswith("ok "), ((shape, kernel, docs, mode), line)
+        if i >= small and kernel[1] * kernel[2] <= 2 ** 14:
+            assert line.startswith("ok "), ((shape, kernel, docs, mode), line)
+    assert {x.split()[0] for _, x in lines} == {"ok", "unplanned"}
