@@ -122,10 +122,17 @@ __device__ __forceinline__ void load_slopes(const ScoredParams& p, int head, flo
     for (int a = 0; a < 3; ++a) s[a] = p.slopes ? p.slopes[head * 3 + a] : 0.f;
 }
 
+// A warp on a row by itself keeps the others of its block from their next
+// stages, for longer than their waits allow where the window is large: it
+// counts in `beat` once a line of the window, and they wait on.
+__device__ __forceinline__ void still_going(uint32_t* beat, int lane) {
+    if (lane == 0) atomicAdd_block(beat, 1u);
+}
+
 // Forward row: a running maximum m, the sum l of e^(s - m) and the weighted
 // sum of v, rescaled when m grows.
 template <int HD>
-__device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane) {
+__device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
     Row<HD> q, acc, x;
     q.load(p.q + o.token * p.q_ts + int64_t(o.head) * HD, lane);
     acc.zero();
@@ -134,7 +141,8 @@ __device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane) {
     const int qdoc = p.doc ? p.doc[o.token] : 0, prefix = p.prefix ? p.prefix[o.b] : 0;
     const int t0 = win_start(o.t, p.KT, p.T), h0 = win_start(o.h, p.KH, p.H), w0 = win_start(o.w, p.KW, p.W);
     for (int t = t0; t < t0 + p.KT; ++t)
-        for (int h = h0; h < h0 + p.KH; ++h)
+        for (int h = h0; h < h0 + p.KH; ++h) {
+            still_going(beat, lane);
             for (int w = w0; w < w0 + p.KW; ++w) {
                 const int64_t tok = token_of(p, o.b, t, h, w);
                 if (!visible(p, qdoc, p.doc ? p.doc[tok] : 0, o.t, t, prefix)) continue;
@@ -149,6 +157,7 @@ __device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane) {
                 l = fmaf(l, r, e);
                 m = mn;
             }
+        }
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int i = 0; i < Row<HD>::E; ++i) acc.x[i] *= inv;
@@ -159,7 +168,7 @@ __device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane) {
 
 // Gradient of one query.
 template <int HD>
-__device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
+__device__ void row_dq(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
     Row<HD> q, g, acc, x, y;
     const int64_t row = o.token * p.NH + o.head;
     q.load(p.q + o.token * p.q_ts + int64_t(o.head) * HD, lane);
@@ -175,7 +184,8 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
     const int t0 = win_start(o.t, p.KT, p.T), h0 = win_start(o.h, p.KH, p.H), w0 = win_start(o.w, p.KW, p.W);
     if (lse != -INFINITY)
         for (int t = t0; t < t0 + p.KT; ++t)
-            for (int h = h0; h < h0 + p.KH; ++h)
+            for (int h = h0; h < h0 + p.KH; ++h) {
+                still_going(beat, lane);
                 for (int w = w0; w < w0 + p.KW; ++w) {
                     const int64_t tok = token_of(p, o.b, t, h, w);
                     if (!visible(p, qdoc, p.doc ? p.doc[tok] : 0, o.t, t, prefix)) continue;
@@ -186,13 +196,14 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane) {
                     inner = fmaf(e, dp, inner);
                     acc.axpy(e * (dp - delta) * ds, x);
                 }
+            }
     if (lane == 0) p.stat[stat_at(p, o.b, o.token, o.head)].y = inner;
     acc.store(p.dq + o.token * p.dq_ts + int64_t(o.head) * HD, lane);
 }
 
 // Gradients of one key and value, over the queries whose windows hold it.
 template <int HD>
-__device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane) {
+__device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
     Row<HD> k, v, dk, dv, x, g;
     k.load(p.k + o.token * p.k_ts + int64_t(o.head) * HD, lane);
     v.load(p.v + o.token * p.v_ts + int64_t(o.head) * HD, lane);
@@ -203,7 +214,8 @@ __device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane) {
     const int kdoc = p.doc ? p.doc[o.token] : 0, prefix = p.prefix ? p.prefix[o.b] : 0;
     const int t1 = inv_last(o.t, p.KT, p.T), h1 = inv_last(o.h, p.KH, p.H), w1 = inv_last(o.w, p.KW, p.W);
     for (int t = inv_first(o.t, p.KT); t <= t1; ++t)
-        for (int h = inv_first(o.h, p.KH); h <= h1; ++h)
+        for (int h = inv_first(o.h, p.KH); h <= h1; ++h) {
+            still_going(beat, lane);
             for (int w = inv_first(o.w, p.KW); w <= w1; ++w) {
                 const int64_t tok = token_of(p, o.b, t, h, w), row = tok * p.NH + o.head;
                 if (!visible(p, p.doc ? p.doc[tok] : 0, kdoc, t, o.t, prefix)) continue;
@@ -216,6 +228,7 @@ __device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane) {
                 dv.axpy(e, g);
                 dk.axpy(e * (g.dot(v) - p.stat[stat_at(p, o.b, tok, o.head)].y) * ds, x);
             }
+        }
     dk.store(p.dk + o.token * p.dk_ts + int64_t(o.head) * HD, lane);
     dv.store(p.dv + o.token * p.dv_ts + int64_t(o.head) * HD, lane);
 }
@@ -237,16 +250,23 @@ __device__ __forceinline__ uint32_t left_over(float x, float y, uint32_t p) {
 struct Sync {
     uint32_t bar0;
     volatile uint32_t* abort_flag;
+    uint32_t* beat;   // counts on while a warp of the block is on a row by itself
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
-    // Wait for a barrier phase; false once this block has given up.
+    // Wait for a barrier phase; false once this block has given up: kWaitLimitNs after the wait
+    // began, or after the last beat that it saw.
     __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
         if (mbar_try_wait(b, parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
+        uint64_t t0 = globaltimer_ns();
+        uint32_t seen = *static_cast<volatile uint32_t*>(beat);
         for (uint32_t it = 1;; ++it) {
             if (mbar_try_wait(b, parity)) return true;
             if ((it & 255u) == 0u) {
                 if (*abort_flag) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                const uint32_t now = *static_cast<volatile uint32_t*>(beat);
+                if (now != seen) {
+                    seen = now;
+                    t0 = globaltimer_ns();
+                } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
                     *abort_flag = 1u;
                     atomicOr(&g_scored_timeout_flag, 1u);
                     return false;
@@ -409,10 +429,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
     if (MODE == kDq) dependents_may_start();
 
-    // control words: abort flag, then done and issued counts of each ring
+    // control words: abort flag, beat, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
     uint32_t* misc = reinterpret_cast<uint32_t*>(base_ptr + g.off_bar);
-    const Sync sy{base + g.off_bar + kControl, misc};
+    const Sync sy{base + g.off_bar + kControl, misc, misc + 1};
     uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S + FB; ++i) {
@@ -420,7 +440,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             done[i] = 0;
             issued[i] = 0;
         }
-        misc[0] = 0u;
+        misc[0] = misc[1] = 0u;
         fence_mbar_init();
     }
     // The stages start as zeros: a step reads up to 15 rows past a chunk's box,
@@ -1155,9 +1175,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 q.head = head;
                 q.token = token_of(p, q.b, q.t, q.h, q.w);
                 __syncwarp();
-                if (MODE == kFwd) row_fwd<HD>(p, q, lane);
-                else if (MODE == kDq) row_dq<HD>(p, q, lane);
-                else row_dkv<HD>(p, q, lane);
+                if (MODE == kFwd) row_fwd<HD>(p, q, lane, sy.beat);
+                else if (MODE == kDq) row_dq<HD>(p, q, lane, sy.beat);
+                else row_dkv<HD>(p, q, lane, sy.beat);
             }
         }
         next_unit<DKV>(p, g, cur);

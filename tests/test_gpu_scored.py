@@ -324,3 +324,34 @@ def test_offsets_past_32_bits():
     for name, x in zip(("dk", "dv"), na.qkv_views(dqkv)[1:]):
         value, bound = want[name]
         ref.check(name, x[:, -1:, rows].cpu()[:, :, 3:], (value[:, :, 3:], bound[:, :, 3:]))
+
+
+def test_rows_by_themselves_outlast_no_wait():
+    """Rows that are not finite are computed one by one, here for longer than the two
+    seconds that a wait of the other warps allows: these get their results all the same.
+    (Every row of dk and dv sees the bad queries where every window is the whole grid, so
+    the bad values enter the backward pass through delta, which only dq takes.)"""
+    T, H, W = 41, 91, 99
+    shape, kernel = (1, T, H, W, 1, 16), (T, H, W)
+    q, k, v, g = (x.cuda() for x in make(shape, 41))
+    good = torch.ones(shape[:4], dtype=torch.bool, device="cuda")
+    good[:, 0, :4, :4] = False                                    # the rows of one warp
+    out, lse = na.na3d_scored_attention(q, k, v, kernel, return_lse=True)
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    na.na3d_scored_bwd(q, k, v, out, lse, g, dq, dk, dv, kernel)
+    assert na.na3d_device_status() == 0
+
+    q2, out2, lse2 = q.clone(), torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    q2[~good] = float("nan")
+    na.na3d_scored_fwd(q2, k, v, out2, kernel, lse2)
+    assert na.na3d_device_status() == 0
+    assert torch.equal(out2[good], out[good]) and torch.equal(lse2[good], lse[good])
+    assert bool(torch.isnan(out2[~good]).all())
+
+    bad_out = out.clone()
+    bad_out[~good] = float("nan")
+    dq2, dk2, dv2 = (torch.full_like(q, 7.0) for _ in range(3))
+    na.na3d_scored_bwd(q, k, v, bad_out, lse, g, dq2, dk2, dv2, kernel)
+    assert na.na3d_device_status() == 0
+    assert torch.equal(dq2[good], dq[good]) and bool(torch.isnan(dq2[~good]).all())
+    assert bool(torch.isfinite(dk2).all()) and bool(torch.isfinite(dv2).all())
