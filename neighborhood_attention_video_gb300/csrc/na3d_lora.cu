@@ -315,7 +315,8 @@ struct Shape {
     static constexpr int OFF_BAR = kStages * STAGE;
     static constexpr int B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AEMPTY = B_AFULL + 2,
                          B_DRAIN = B_AEMPTY + 2, NBAR = B_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory's address, abort flag, beat
+    static constexpr int OFF_BEAT = OFF_MISC + 8;
     static constexpr int OFF_BIAS = (OFF_MISC + 16 + 15) & ~15;   // a tile's bias, fp32, for each epilogue warp its columns
     static constexpr int OFF_REQ = OFF_BIAS + 8 * 128 * 4;        // the requests, where they are few
     static constexpr int SMEM = OFF_REQ + (2 * kFewRequests + 1) * 4 + 1024;
@@ -323,8 +324,21 @@ struct Shape {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 500000000ull;
 
+// About a millisecond a tick.
+__device__ __forceinline__ uint32_t beat_clock() { return uint32_t(globaltimer_ns() >> 20); }
+
+// Has the block given up? It does kWaitLimitNs after this wait began (t0) and after the last beat.
+__device__ __noinline__ bool gave_up(volatile uint32_t* abort_flag, uint64_t t0) {
+    if (abort_flag[0]) return true;
+    if (globaltimer_ns() - t0 <= kWaitLimitNs || beat_clock() - abort_flag[1] <= uint32_t(kWaitLimitNs >> 20)) return false;
+    abort_flag[0] = 1u;
+    atomicOr(&g_lora_timeout_flag, 1u);
+    return true;
+}
+
 struct Sync {
     uint32_t bar0;
+    // behind it the beat: when a thread of the block or its pair was last on a value by itself (beat_clock())
     volatile uint32_t* abort_flag;
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
     // (the other block of a pair arrives on some of the barriers)
@@ -342,14 +356,7 @@ struct Sync {
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1;; ++it) {
             if (try_wait(b, parity)) return true;
-            if ((it & 1023u) == 0u) {
-                if (*abort_flag) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                    *abort_flag = 1u;
-                    atomicOr(&g_lora_timeout_flag, 1u);
-                    return false;
-                }
-            }
+            if ((it & 1023u) == 0u && gave_up(abort_flag, t0)) return false;
         }
     }
 };
@@ -437,21 +444,43 @@ struct GemmParams {
     uint16_t* out;
 };
 
-// One output value from the inputs, for a row whose tile holds another
-// request's values that are not finite.
-template <bool BWD>
-__device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& q, int m, int col) {
-    float s = 0.f, sq = 0.f;
-    const int rp = padded_rank(p.R);
-    if (!BWD) {
-        for (int c = 0; c < p.C; ++c) s = fmaf(f32(p.x[int64_t(m) * p.C + c]), f32(p.w[int64_t(col) * p.C + c]), s);
-    } else {
-        for (int n = 0; n < p.N; ++n) {
-            if (n == p.Nq) { sq = s * p.q_scale; s = 0.f; }
-            s = fmaf(f32(p.dqkv[int64_t(m) * p.N + n]), f32(p.w[int64_t(n) * p.C + col]), s);
-        }
-        s += sq;
+// The time into the beat of the block, or of both of a pair.
+template <int CG>
+__device__ __forceinline__ void give_beat(uint32_t addr) {
+    const uint32_t now = beat_clock();
+#pragma unroll
+    for (uint32_t r = 0; r < CG; ++r) {
+        uint32_t at = addr;
+        if (CG == 2) asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(r));
+        if (CG == 2) asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(now) : "memory");
+        else asm volatile("st.relaxed.cta.shared::cta.u32 [%0], %1;" ::"r"(at), "r"(now) : "memory");
     }
+}
+
+// One output value from the inputs, for a row whose tile holds another
+// request's values that are not finite. The accumulator is held meanwhile,
+// for a long contraction longer than the other roles' waits allow: every
+// kBeat terms a thread leaves the time in shared memory, and they wait on.
+constexpr int kBeat = 4096;
+template <bool BWD, int CG>
+__device__ __noinline__ float lone_value(const LoraParams& p, const GemmParams& q, int m, int col) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t beat = ((smem_u32(smem_raw) + 1023u) & ~1023u) + Shape<CG>::OFF_BEAT;
+    float s = 0.f, sq = 0.f;
+    const int rp = padded_rank(p.R), terms = BWD ? p.N : p.C;
+    for (int k0 = 0, k1; k0 < terms; k0 = k1) {
+        give_beat<CG>(beat);
+        k1 = k0 + min(terms - k0, kBeat);
+        if (!BWD) {
+            for (int c = k0; c < k1; ++c) s = fmaf(f32(p.x[int64_t(m) * p.C + c]), f32(p.w[int64_t(col) * p.C + c]), s);
+        } else {
+            for (int n = k0; n < k1; ++n) {
+                if (n == p.Nq) { sq = s * p.q_scale; s = 0.f; }
+                s = fmaf(f32(p.dqkv[int64_t(m) * p.N + n]), f32(p.w[int64_t(n) * p.C + col]), s);
+            }
+        }
+    }
+    s += sq;
     const Requests rq = requests_of(p);
     Walk w;
     for (w.start(rq, m & ~127); w.more(rq); w.next(rq, m & ~127)) {
@@ -508,6 +537,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::NBAR; ++i) mbar_init(sy.bar(i), (i >= B_AEMPTY && i < B_AEMPTY + 2) ? 256u * CG : 1u);
         misc[1] = 0u;
+        misc[2] = beat_clock() - uint32_t(kWaitLimitNs >> 20) - 1u;   // long ago
         fence_mbar_init();
     }
     Requests rq = requests_of(p);
@@ -733,7 +763,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
                     if (w.more(rq) && (w.lo > span0 || w.hi < min(span0 + kBM * CG, p.M)))
 #pragma unroll 1
                         for (int j = 0; j < W && c0 + j < q.cols; ++j) {
-                            const float x = lone_value<BWD>(p, q, row, c0 + j);
+                            const float x = lone_value<BWD, CG>(p, q, row, c0 + j);
 #pragma unroll
                             for (int k = 0; k < W; ++k)
                                 if (k == j) acc[k] = x;

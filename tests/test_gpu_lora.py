@@ -340,3 +340,34 @@ def test_workspaces_of_calls_that_run_at_once():
         for x, y in zip(r, want[i]):
             assert torch.equal(x, y), i
     assert na.na3d_device_status() == 0
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["forward by blocks", "backward by pairs"])
+def test_values_by_themselves_outlast_no_wait(backward):
+    """In a tile that another request's infinite adapter reaches, values are computed one by
+    one, over a contraction this long for more than the two seconds that a wait of the
+    tile's other roles allows: the tiles that follow get their results all the same."""
+    M, HD, R = 456 * 128, 64, 16                    # three tiles for each block, six for each pair
+    C, NH = (264, 800) if backward else (200000, 1)
+    N = 3 * NH * HD
+    t, g = make(128, C, NH, HD, R, 2, 43, bias=False)
+    if backward:
+        t["w"] = (t["w"].float() * (C / N) ** 0.5).to(BF16)
+    tall = lambda x: torch.cat([x.cuda(), torch.zeros((M - 128, x.shape[1]), dtype=BF16, device="cuda")])  # noqa: E731
+    d = {n: v.cuda() for n, v in t.items() if v is not None}
+    adapters = (d["lora_a"], d["lora_b"], d["scaling"], ints(0, 64, 128, M).cuda(), ints(0, 1, -1).cuda())
+    d["lora_a" if backward else "lora_b"][1] = float("inf")
+    x = tall(t["x"])
+    if backward:
+        got = torch.full_like(x, 7.0)
+        da, db = torch.empty_like(d["lora_a"]), torch.empty_like(d["lora_b"])
+        na.na3d_lora_qkv_proj_bwd(tall(g), x, d["w"], *adapters, got, da, db, NH, HD)
+    else:
+        got = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+        na.na3d_lora_qkv_proj(x, d["w"], None, *adapters, got, NH, HD)
+    assert na.na3d_device_status() == 0
+    assert bool((got[128:] == 0).all())
+    t["x"] = t["x"][:64]
+    want = ref.lora(**t, offsets=ints(0, 64), adapter=ints(0), HD=HD, dqkv=g[:64] if backward else None)
+    ref.check("values", got[:64], want["dx" if backward else "qkv"])
+    assert not bool(torch.isfinite(got[64:128]).any())
