@@ -122,17 +122,20 @@ __device__ __forceinline__ void load_slopes(const ScoredParams& p, int head, flo
     for (int a = 0; a < 3; ++a) s[a] = p.slopes ? p.slopes[head * 3 + a] : 0.f;
 }
 
+// About a millisecond a tick.
+__device__ __forceinline__ uint32_t beat_clock() { return uint32_t(globaltimer_ns() >> 20); }
+
 // A warp on a row by itself keeps the others of its block from their next
-// stages, for longer than their waits allow where the window is large: it
-// counts in `beat` once a line of the window, and they wait on.
-__device__ __forceinline__ void still_going(uint32_t* beat, int lane) {
-    if (lane == 0) atomicAdd_block(beat, 1u);
+// stages, for longer than their waits allow where the window is large: once a
+// line of the window it leaves the time, the block's beat, and they wait on.
+__device__ __forceinline__ void still_going(volatile uint32_t* beat, int lane) {
+    if (lane == 0) *beat = beat_clock();
 }
 
 // Forward row: a running maximum m, the sum l of e^(s - m) and the weighted
 // sum of v, rescaled when m grows.
 template <int HD>
-__device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
+__device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane, volatile uint32_t* beat) {
     Row<HD> q, acc, x;
     q.load(p.q + o.token * p.q_ts + int64_t(o.head) * HD, lane);
     acc.zero();
@@ -168,7 +171,7 @@ __device__ void row_fwd(const ScoredParams& p, const Pos& o, int lane, uint32_t*
 
 // Gradient of one query.
 template <int HD>
-__device__ void row_dq(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
+__device__ void row_dq(const ScoredParams& p, const Pos& o, int lane, volatile uint32_t* beat) {
     Row<HD> q, g, acc, x, y;
     const int64_t row = o.token * p.NH + o.head;
     q.load(p.q + o.token * p.q_ts + int64_t(o.head) * HD, lane);
@@ -203,7 +206,7 @@ __device__ void row_dq(const ScoredParams& p, const Pos& o, int lane, uint32_t* 
 
 // Gradients of one key and value, over the queries whose windows hold it.
 template <int HD>
-__device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane, uint32_t* beat) {
+__device__ void row_dkv(const ScoredParams& p, const Pos& o, int lane, volatile uint32_t* beat) {
     Row<HD> k, v, dk, dv, x, g;
     k.load(p.k + o.token * p.k_ts + int64_t(o.head) * HD, lane);
     v.load(p.v + o.token * p.v_ts + int64_t(o.head) * HD, lane);
@@ -247,31 +250,26 @@ __device__ __forceinline__ uint32_t left_over(float x, float y, uint32_t p) {
     return pack_bf16x2(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xffff0000u));
 }
 
+// Has the block given up? It does kWaitLimitNs after this wait began (t0) and after the last beat.
+__device__ __noinline__ bool gave_up(volatile uint32_t* abort_flag, uint64_t t0) {
+    if (abort_flag[0]) return true;
+    if (globaltimer_ns() - t0 <= kWaitLimitNs || beat_clock() - abort_flag[1] <= uint32_t(kWaitLimitNs >> 20)) return false;
+    abort_flag[0] = 1u;
+    atomicOr(&g_scored_timeout_flag, 1u);
+    return true;
+}
+
 struct Sync {
     uint32_t bar0;
-    volatile uint32_t* abort_flag;
-    uint32_t* beat;   // counts on while a warp of the block is on a row by itself
+    volatile uint32_t* abort_flag;   // behind it the beat
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
-    // Wait for a barrier phase; false once this block has given up: kWaitLimitNs after the wait
-    // began, or after the last beat that it saw.
+    // Wait for a barrier phase; false once this block has given up.
     __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
         if (mbar_try_wait(b, parity)) return true;
-        uint64_t t0 = globaltimer_ns();
-        uint32_t seen = *static_cast<volatile uint32_t*>(beat);
+        const uint64_t t0 = globaltimer_ns();
         for (uint32_t it = 1;; ++it) {
             if (mbar_try_wait(b, parity)) return true;
-            if ((it & 255u) == 0u) {
-                if (*abort_flag) return false;
-                const uint32_t now = *static_cast<volatile uint32_t*>(beat);
-                if (now != seen) {
-                    seen = now;
-                    t0 = globaltimer_ns();
-                } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                    *abort_flag = 1u;
-                    atomicOr(&g_scored_timeout_flag, 1u);
-                    return false;
-                }
-            }
+            if ((it & 255u) == 0u && gave_up(abort_flag, t0)) return false;
         }
     }
 };
@@ -432,7 +430,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
     // control words: abort flag, beat, then done and issued counts of each ring
     // (the stages, then the fixed buffers); barriers: one a ring place
     uint32_t* misc = reinterpret_cast<uint32_t*>(base_ptr + g.off_bar);
-    const Sync sy{base + g.off_bar + kControl, misc, misc + 1};
+    const Sync sy{base + g.off_bar + kControl, misc};
     uint32_t *done = misc + 2, *issued = misc + 2 + kMaxRing;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S + FB; ++i) {
@@ -440,7 +438,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
             done[i] = 0;
             issued[i] = 0;
         }
-        misc[0] = misc[1] = 0u;
+        misc[0] = 0u;
+        misc[1] = beat_clock() - uint32_t(kWaitLimitNs >> 20) - 1u;   // long ago
         fence_mbar_init();
     }
     // The stages start as zeros: a step reads up to 15 rows past a chunk's box,
@@ -736,12 +735,12 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                     if ((DKV || docs) && has_frame(cur, t)) {
                         bool other = docs && (row_doc[0] != d0 || row_doc[1] != d0);
                         bool met = other;
-                        const int n = part_steps * 16;   // with the last step's columns past the part
+                        const int n = DKV ? part_steps * 16 : part.n;   // statistics: with the last step's columns past the part
                         auto keep = [&](int i, int doc, const float2& x) {
                             if (docs) {
                                 col_doc[i] = doc;
                                 other = other || doc != d0;
-                                met = met || (doc == d0 && i < part.n);
+                                met = met || (doc == d0 && (!DKV || i < part.n));
                             }
                             if (DKV) col_stat[i] = x;
                         };
@@ -1175,9 +1174,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                 q.head = head;
                 q.token = token_of(p, q.b, q.t, q.h, q.w);
                 __syncwarp();
-                if (MODE == kFwd) row_fwd<HD>(p, q, lane, sy.beat);
-                else if (MODE == kDq) row_dq<HD>(p, q, lane, sy.beat);
-                else row_dkv<HD>(p, q, lane, sy.beat);
+                if (MODE == kFwd) row_fwd<HD>(p, q, lane, sy.abort_flag + 1);
+                else if (MODE == kDq) row_dq<HD>(p, q, lane, sy.abort_flag + 1);
+                else row_dkv<HD>(p, q, lane, sy.abort_flag + 1);
             }
         }
         next_unit<DKV>(p, g, cur);
