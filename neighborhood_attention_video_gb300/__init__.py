@@ -268,7 +268,9 @@ def na3d_qkv_proj(x, w, bias, qkv, num_heads, head_dim, stream=None) -> None:
 def qkv_views(qkv):
     """q, k, v views (B, T, H, W, NH, HD) of a (B, T, H, W, 3, NH, HD)
     projection output, for ``na3d_fwd_strided``."""
-    return qkv.select(-3, 0), qkv.select(-3, 1), qkv.select(-3, 2)
+    if _torch is not None and isinstance(qkv, _torch.Tensor):   # 3 us less than by index
+        return qkv.select(-3, 0), qkv.select(-3, 1), qkv.select(-3, 2)
+    return qkv[..., 0, :, :], qkv[..., 1, :, :], qkv[..., 2, :, :]
 
 
 def _check_one(torch, dev, name, t, dtype, shape):

@@ -176,3 +176,14 @@ def test_binding_wants_device_tensors():
         na.na3d_lora_qkv_proj(y, y, None, y[None], y[None], lse, ids, ids[:1], y, 1, 16)
     with pytest.raises(ValueError):
         na.na3d_lora_qkv_proj(y, y, None, y, y[None], lse, ids, ids[:1], y, 1, 16)
+
+
+def test_qkv_views_of_any_array():
+    """Views of whatever indexes like a tensor, arrays of the oracle's inputs among them."""
+    x = torch.arange(2 * 3 * 2 * 4).reshape(2, 3, 2, 4)
+    for a in (x, x.numpy()):
+        views = na.qkv_views(a)
+        for i, v in enumerate(views):
+            assert type(v) is type(a) and tuple(v.shape) == (2, 2, 4) and (v == a[:, i]).all()
+            v[0, 0, 0] = -1
+            assert a[0, i, 0, 0] == -1
