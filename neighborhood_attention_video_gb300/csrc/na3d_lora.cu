@@ -1293,11 +1293,14 @@ cudaError_t grad(const LoraParams& p, const Plan& q, const uint16_t* t, const ui
 
 }  // namespace
 
+static std::atomic<bool> g_launched{false};
+
 int64_t lora_workspace(int64_t M, int64_t C, int64_t N, int64_t R, int64_t n_req, int64_t n_ad, bool backward) {
     return lay_out(M, C, N, R, n_req, n_ad, backward).bytes;
 }
 
 cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
+    g_launched = true;
     uint16_t* t = static_cast<uint16_t*>(p.work);
     if (p.M <= kSmallRows) {
         lora_down_few<<<dim3(unsigned(p.M), unsigned(p.R / 8)), 256, 0, stream>>>(p, t);
@@ -1313,6 +1316,7 @@ cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_lora_bwd(const LoraParams& p0, int sms, cudaStream_t stream) {
+    g_launched = true;
     const Work w = lay_out(p0.M, p0.C, p0.N, p0.R, p0.n_req, p0.n_ad, true);
     uint8_t* work = static_cast<uint8_t*>(p0.work);
     uint16_t *t = reinterpret_cast<uint16_t*>(work + w.t), *u = reinterpret_cast<uint16_t*>(work + w.u);
@@ -1334,13 +1338,16 @@ cudaError_t launch_lora_bwd(const LoraParams& p0, int sms, cudaStream_t stream) 
 }
 
 // The flag is taken as for the attention kernel: one atomic exchange per
-// status request, its old value left in a slot of that request's own.
+// status request, its old value left in a slot of that request's own. A process
+// that has launched none of these kernels has nothing to ask for.
 constexpr unsigned int kStatusSlots = 256;
 __device__ unsigned int g_lora_status_slots[kStatusSlots];
 
 __global__ void take_lora_flag(unsigned int slot) { g_lora_status_slots[slot] = atomicExch(&g_lora_timeout_flag, 0u); }
 
 cudaError_t take_lora_error(cudaStream_t stream, unsigned int* flag) {
+    *flag = 0;
+    if (!g_launched) return cudaSuccess;
     static std::atomic<unsigned int> next{0};
     const unsigned int slot = next.fetch_add(1u) % kStatusSlots;
     take_lora_flag<<<1, 1, 0, stream>>>(slot);

@@ -28,7 +28,8 @@ cudaError_t launch_lora_fwd(const LoraParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_lora_bwd(const LoraParams& p, int sms, cudaStream_t stream);
 
 // After the work already on `stream`, take (read and clear in one atomic
-// step) these kernels' timeout flag, then synchronize `stream`.
+// step) these kernels' timeout flag, then synchronize `stream`. Nothing is
+// done where the process has launched none of them.
 cudaError_t take_lora_error(cudaStream_t stream, unsigned int* flag);
 
 }  // namespace na3d

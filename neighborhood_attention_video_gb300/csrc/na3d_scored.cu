@@ -1305,6 +1305,8 @@ cudaError_t bwd(const ScoredParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+static std::atomic<bool> g_launched{false};
+
 bool scored_planned(int hd, const ScoredParams& p, bool backward) {
     constexpr int kSms = 152;   // whether there is a plan does not depend on it
     TileGeom g;
@@ -1313,6 +1315,7 @@ bool scored_planned(int hd, const ScoredParams& p, bool backward) {
 }
 
 cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream) {
+    g_launched = true;
     switch (hd) {
         case 16: return launch_tiles<16, kFwd>(p, sms, stream);
         case 32: return launch_tiles<32, kFwd>(p, sms, stream);
@@ -1323,6 +1326,7 @@ cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream
 }
 
 cudaError_t launch_scored_bwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream) {
+    g_launched = true;
     switch (hd) {
         case 16: return bwd<16>(p, sms, stream);
         case 32: return bwd<32>(p, sms, stream);
@@ -1333,7 +1337,8 @@ cudaError_t launch_scored_bwd(int hd, const ScoredParams& p, int sms, cudaStream
 }
 
 // The flag is taken as for the attention kernel: one atomic exchange per
-// status request, its old value left in a slot of that request's own.
+// status request, its old value left in a slot of that request's own. A process
+// that has launched none of these kernels has nothing to ask for.
 constexpr unsigned int kStatusSlots = 256;
 __device__ unsigned int g_scored_status_slots[kStatusSlots];
 
@@ -1342,6 +1347,8 @@ __global__ void take_scored_flag(unsigned int slot) {
 }
 
 cudaError_t take_scored_error(cudaStream_t stream, unsigned int* flag) {
+    *flag = 0;
+    if (!g_launched) return cudaSuccess;
     static std::atomic<unsigned int> next{0};
     const unsigned int slot = next.fetch_add(1u) % kStatusSlots;
     take_scored_flag<<<1, 1, 0, stream>>>(slot);

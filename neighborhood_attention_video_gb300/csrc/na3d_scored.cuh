@@ -32,7 +32,8 @@ cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream
 cudaError_t launch_scored_bwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream);
 
 // After the work already on `stream`, take (read and clear in one atomic
-// step) these kernels' timeout flag, then synchronize `stream`.
+// step) these kernels' timeout flag, then synchronize `stream`. Nothing is
+// done where the process has launched none of them.
 cudaError_t take_scored_error(cudaStream_t stream, unsigned int* flag);
 
 }  // namespace na3d

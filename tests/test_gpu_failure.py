@@ -84,3 +84,49 @@ def test_a_timeout_is_taken_by_exactly_one_status_call():
         t.join()
     assert sorted(results) == [0, 10], results
     assert na.na3d_device_status() == 0
+
+
+STATUS_SCRIPT = """
+import re
+import torch
+from torch.profiler import ProfilerActivity, profile
+import neighborhood_attention_video_gb300 as na
+x = torch.ones((1, 3, 4, 8, 1, 16), dtype=torch.bfloat16, device="cuda")
+y = torch.ones((96, 16), dtype=torch.bfloat16, device="cuda")
+w = torch.ones((48, 16), dtype=torch.bfloat16, device="cuda")
+qkv = torch.empty((96, 48), dtype=torch.bfloat16, device="cuda")
+ids = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+def base():
+    na.na3d_attention(x, x, x, (3, 3, 3))
+    na.na3d_qkv_proj(y, w, None, qkv, 1, 16)
+def scored():
+    na.na3d_scored_attention(x, x, x, (3, 3, 3))
+def lora():
+    na.na3d_lora_qkv_proj(y, w, None, y[None, :8].contiguous(), torch.ones((1, 48, 8), dtype=torch.bfloat16, device="cuda"),
+                          torch.ones(1, device="cuda"), ids(0, 96), ids(0), qkv, 1, 16)
+with profile(activities=[ProfilerActivity.CUDA]):   # the first one may come too late for its kernels
+    y + 1
+    torch.cuda.synchronize()
+for call in (base, scored, lora):
+    call()
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]) as prof:
+        assert na.na3d_device_status() == 0
+    names = re.findall(r"take_\\w+_flag", " ".join(e.name for e in prof.events()))
+    print("asked:", *sorted(names))
+"""
+
+
+def test_status_asks_only_for_kernels_that_ran():
+    """na3d_device_status takes a kernel, a copy and a wait for each family of kernels
+    that the process has launched, and nothing for the others."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", STATUS_SCRIPT], capture_output=True, text=True, cwd=root, timeout=300)
+    assert res.returncode == 0, res.stderr
+    asked = [line.split()[1:] for line in res.stdout.splitlines() if line.startswith("asked:")]
+    if not any(asked):
+        pytest.skip("the profiler records no kernels here")
+    assert [len(a) for a in asked] == [2, 3, 4], asked
