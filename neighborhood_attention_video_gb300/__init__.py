@@ -183,10 +183,16 @@ def _token_stride(name, t) -> int:
         return st[3]
     if st[5] != 1 or (sh[4] > 1 and st[4] != sh[5]):
         raise ValueError(f"{name}: heads must be packed (strides [..., HD, 1])")
-    for i in (2, 1, 0):
-        if sh[i] > 1 and st[i] != sh[i + 1] * st[i + 1]:
+    step = span = None   # axes of one position say nothing about the step
+    for i in (3, 2, 1, 0):
+        if sh[i] == 1:
+            continue
+        if step is None:
+            step = st[i]
+        elif st[i] != span:
             raise ValueError(f"{name}: grid positions must share one token stride")
-    return int(st[3])
+        span = sh[i] * st[i]
+    return int(sh[4] * sh[5] if step is None else step)
 
 
 def na3d_fwd_strided(q, k, v, out, kernel_size, stream=None) -> None:

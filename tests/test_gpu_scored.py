@@ -355,3 +355,16 @@ def test_rows_by_themselves_outlast_no_wait():
     assert na.na3d_device_status() == 0
     assert torch.equal(dq2[good], dq[good]) and bool(torch.isnan(dq2[~good]).all())
     assert bool(torch.isfinite(dk2).all()) and bool(torch.isfinite(dv2).all())
+
+
+def test_views_of_one_column():
+    """A grid cut to one row and column: its frames lie further apart than the strides of
+    the axes of one position say."""
+    full = torch.stack(make((1, 7, 1, 5, 2, 32), 47)[:3], 4).cuda()
+    q, k, v = na.qkv_views(full[:, :, :, :1])
+    for opts in ({}, {"doc": torch.zeros((1, 7, 1, 1), dtype=torch.int32, device="cuda")}):
+        out = na.na3d_scored_attention(q, k, v, (5, 1, 1), **opts)
+        assert torch.equal(out, na.na3d_scored_attention(q.contiguous(), k.contiguous(), v.contiguous(), (5, 1, 1), **opts))
+    base = torch.empty_like(out)
+    na.na3d_fwd_strided(q, k, v, base, (5, 1, 1))
+    assert torch.equal(base, na.na3d_attention(q.contiguous(), k.contiguous(), v.contiguous(), (5, 1, 1)))

@@ -187,3 +187,31 @@ def test_qkv_views_of_any_array():
             assert type(v) is type(a) and tuple(v.shape) == (2, 2, 4) and (v == a[:, i]).all()
             v[0, 0, 0] = -1
             assert a[0, i, 0, 0] == -1
+
+
+@pytest.mark.parametrize("cut", [(0, 3, 1, 1), (0, 3, 2, 1), (0, 1, 1, 4), (0, 3, 1, 4), (0, 1, 5, 1), (2, 1, 1, 1), (0, 1, 1, 1),
+                                 (2, 3, 5, 7), (0, 3, 5, 7)])
+@pytest.mark.parametrize("H0", [5, 1])
+def test_token_stride_of_cut_grids(cut, H0):
+    """The token stride of a view is that of its axes of more than one position: an axis
+    of one says nothing. Where positions share no stride the view is refused."""
+    B, T, H, W = (n or 1 for n in cut)
+    H = min(H, H0)
+    x = torch.zeros(2, 3, H0, 7, 2, 16)[:B, :T, :H, :W]
+    offsets = [sum(i * s for i, s in zip(at, x.stride())) for at in
+               ((b, t, h, w) for b in range(B) for t in range(T) for h in range(H) for w in range(W))]
+    steps = {b - a for a, b in zip(offsets, offsets[1:])}
+    if len(steps) > 1:
+        with pytest.raises(ValueError):
+            na._token_stride("x", x)
+    else:
+        assert na._token_stride("x", x) == (steps.pop() if steps else 2 * 16)
+
+
+def test_token_stride_of_repeated_positions():
+    """Positions that share memory have no stride that the library takes: 0, or none at all."""
+    x = torch.zeros(1, 1, 1, 1, 2, 16)
+    for shape in ((1, 1, 1, 4, 2, 16), (1, 1, 3, 4, 2, 16), (2, 1, 1, 1, 2, 16)):
+        assert na._token_stride("x", x.expand(shape)) == 0
+    with pytest.raises(ValueError):
+        na._token_stride("x", torch.zeros(1, 1, 3, 1, 2, 16).expand(1, 1, 3, 4, 2, 16))
