@@ -273,7 +273,8 @@ int64_t na3d_scored_bwd_workspace(int64_t B, int64_t T, int64_t H, int64_t W, in
  *   so a replayed graph may be given other requests. Offsets that decrease or
  *   leave 0 .. M touch no memory outside the tensors, but which adapter such
  *   rows get is unspecified.
- * n_requests, n_adapters >= 1.
+ * n_requests, n_adapters >= 1; n_requests up to M + 2^20, else
+ *   NA3D_ERR_UNSUPPORTED (more are empty, and a tile's are walked one by one).
  * work: DEVICE workspace of na3d_lora_workspace(..., 0) bytes, 16-byte aligned,
  *   contents arbitrary; as in na3d_scored_bwd, one call at a time.
  * qkv and work must not overlap an input or one another. Errors, asynchrony

@@ -181,7 +181,9 @@ int check_lora_sizes(int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R, in
     if (M < 1 || NH < 1 || C < 1 || HD < 1 || R < 1 || n_req < 1 || n_ad < 1) return NA3D_ERR_SHAPE;
     if (!is_pow2(HD) || HD < 16) return NA3D_ERR_HEAD_DIM;
     if (C % 8 != 0 || R % 8 != 0) return NA3D_ERR_ALIGN;   // 16-byte rows
-    if (R > 128) return NA3D_ERR_UNSUPPORTED;
+    // A tile's roles walk its requests one by one, 0.3 us for each empty one; these must not add up
+    // to the seconds that a wait allows.
+    if (R > 128 || n_req - M > int64_t(1) << 20) return NA3D_ERR_UNSUPPORTED;
     const int64_t lim = int64_t(1) << 31;
     int64_t b;
     if (!mul_ok(3 * NH, HD, N) || *N >= lim || M >= lim - 256 || C >= lim ||

@@ -121,6 +121,7 @@ def lora(lib, backward, sizes=(100, 64, 2, 32, 16, 3, 2), **ptrs):
     (ERR_ALIGN, dict(sizes=(100, 60, 2, 32, 16, 3, 2))),
     (ERR_ALIGN, dict(sizes=(100, 64, 2, 32, 12, 3, 2))),
     (ERR_UNSUPPORTED, dict(sizes=(100, 64, 2, 32, 136, 3, 2))),
+    (ERR_UNSUPPORTED, dict(sizes=(100, 64, 2, 32, 16, 101 + (1 << 20), 2))),
     (ERR_OVERFLOW, dict(sizes=(1 << 31, 64, 2, 32, 16, 3, 2))),
     (ERR_OVERFLOW, dict(sizes=(100, 64, 1 << 27, 32, 16, 3, 2))),
     (ERR_NULL, dict(x=0)),
