@@ -742,6 +742,7 @@ lora_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUte
 #pragma unroll
                     for (int j = 0; j < W; ++j) acc[j] = held[BWD ? W * c + j : 0];
                 } else {
+                    __syncwarp();   // lanes with values by themselves come later; the load is the whole warp's
                     tmem_ld32(t_row + buf * kBN + W * c, acc);
                     tmem_wait_ld();
                     if (c == 128 / W - 1) {   // the accumulator is read

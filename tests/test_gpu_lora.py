@@ -371,3 +371,23 @@ def test_values_by_themselves_outlast_no_wait(backward):
     want = ref.lora(**t, offsets=ints(0, 64), adapter=ints(0), HD=HD, dqkv=g[:64] if backward else None)
     ref.check("values", got[:64], want["dx" if backward else "qkv"])
     assert not bool(torch.isfinite(got[64:128]).any())
+
+
+@pytest.mark.parametrize("M", [150, 58600])
+def test_a_bad_row_is_alone(M):
+    """One row of a tile with two requests is not finite: its lanes of the epilogue compute
+    theirs by themselves, all other rows are what they are without it."""
+    C, NH, HD = 264 if M > 50000 else 128, 3, 64   # pairs of blocks in both directions
+    t, g = make(M, C, NH, HD, 16, 2, 12)
+    off, ad = ints(0, 70, M), ints(0, 1)
+    clean = run(t, g, off, ad, NH, HD)
+    row = 40
+    t["x"][row, 5] = float("nan")
+    g[row, 7] = float("inf")
+    got = run(t, g, off, ad, NH, HD)
+    others = torch.arange(M) != row
+    for name in ("qkv", "dx"):
+        assert torch.equal(got[name].cpu()[others], clean[name].cpu()[others]), name
+        assert not bool(torch.isfinite(got[name][row]).any()), name
+    for name in ("da", "db"):
+        assert torch.equal(got[name][1], clean[name][1]), name
