@@ -368,3 +368,18 @@ def test_views_of_one_column():
     base = torch.empty_like(out)
     na.na3d_fwd_strided(q, k, v, base, (5, 1, 1))
     assert torch.equal(base, na.na3d_attention(q.contiguous(), k.contiguous(), v.contiguous(), (5, 1, 1)))
+
+
+@pytest.mark.parametrize("case", range(4))
+def test_wide_windows_by_norm(case):
+    """Gradients over thousands of keys, whose elementwise bounds would pass a missing
+    term: the norm of each result's error against the roundings' expected one."""
+    import packed_norms as norms
+    from test_packed_norms import WIDE, make as make_wide, slopes_of
+    shape, kernel, scale, softcap, slopes = WIDE[case]
+    q, k, v, g = make_wide(shape, sum(shape), scale)
+    o = dict(softcap=softcap, slopes=slopes_of(shape, slopes), doc=None, prefix=None)
+    want = norms.scored(q, k, v, g, kernel, **o)
+    got = run(q, k, v, g, kernel, o)
+    for name in want:
+        assert norms.excess(got[name], want[name]) <= 1, (name, norms.excess(got[name], want[name]))
