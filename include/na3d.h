@@ -187,6 +187,12 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv,
  *     padding, which sees nothing and is seen by nothing;
  *   - where t_j > t_i and t_j >= prefix[b]             (prefix not NULL):
  *     causal along T, with the first prefix[b] frames seen by every frame.
+ * The masks cut a window that is taken on the whole grid. So a clip that is
+ * packed with others, or padded, is not the clip by itself within half a
+ * window of the cut: alone its windows would shift inward and hold all their
+ * KT * KH * KW keys, here they hold those on the clip's side. Farther from a
+ * cut the rows are equal. prefix counts from the entry's first frame: of the
+ * clips packed along T into one entry only the first can have one.
  * out_i = sum_j p_ij v_j with p the softmax of the s that are not masked, and
  * lse_i = log sum_j e^s. A row that sees nothing has out 0 and lse -infinity.
  * What masked keys and padding hold (infinities and NaN included) reaches no
@@ -271,8 +277,8 @@ int64_t na3d_scored_bwd_workspace(int64_t B, int64_t T, int64_t H, int64_t W, in
  * offsets: DEVICE, int32 (n_requests + 1), not decreasing, within 0 .. M;
  *   adapter: DEVICE, int32 (n_requests). Both are read when the kernels run,
  *   so a replayed graph may be given other requests. Offsets that decrease or
- *   leave 0 .. M touch no memory outside the tensors, but which adapter such
- *   rows get is unspecified.
+ *   leave 0 .. M touch no memory outside the tensors, but the values are then
+ *   unspecified.
  * n_requests, n_adapters >= 1; n_requests up to M + 2^20, else
  *   NA3D_ERR_UNSUPPORTED (more are empty, and a tile's are walked one by one).
  * work: DEVICE workspace of na3d_lora_workspace(..., 0) bytes, 16-byte aligned,

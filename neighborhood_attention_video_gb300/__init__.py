@@ -407,7 +407,11 @@ def na3d_scored_fwd(q, k, v, out, kernel_size, lse=None, softcap=0.0, slopes=Non
     mask (``doc``: int32 (B, T, H, W), negative for padding) and a causal mask
     along T with a free prefix (``prefix``: int32 (B,) frames). ``lse``, where
     given, receives the fp32 (B, T, H, W, NH) log-sum-exp of the scores. q, k,
-    v may be views with a token stride; ``out`` is contiguous. HD up to 128."""
+    v may be views with a token stride; ``out`` is contiguous. HD up to 128.
+    Windows are taken on the whole grid and cut by the masks, so a packed clip
+    has fewer keys next to a cut than the clip by itself; ``prefix`` counts from
+    the entry's first frame. Autograd does not see the call: outputs have no
+    graph, the gradients come from ``na3d_scored_bwd``."""
     shape = _shape_of(q)
     _check_bf16_of_shape(shape, ("q", "k", "v", "out"), (q, k, v, out))
     if not out.is_contiguous():
@@ -502,7 +506,9 @@ def na3d_lora_qkv_proj(x, w, bias, lora_a, lora_b, scaling, offsets, adapter, qk
     (n_requests,) on the device. R is a multiple of 8 up to 128. ``work``: a
     tensor of ``na3d_lora_workspace`` bytes, kept by the caller (one call at a
     time); None takes one that the binding keeps (for this thread and the current
-    stream; a call with a ``stream`` or under capture allocates its own)."""
+    stream; a call with a ``stream`` or under capture allocates its own).
+    Autograd does not see the call: the gradients come from
+    ``na3d_lora_qkv_proj_bwd``."""
     lib = _lib if _lib is not None else load_library()
     sizes = _check_lora(x, w, lora_a, lora_b, scaling, offsets, adapter, num_heads, head_dim)
     _check_bf16_on_device((("qkv", qkv),))

@@ -950,7 +950,9 @@ __host__ __device__ __forceinline__ Plan plan_at(void* work, int n_req, int n_ad
     return q;
 }
 
-// One block; latency, 6 us for four requests.
+// One block; latency, 5 us for four requests. A thread looks at every request
+// for each of its adapters, twice: 0.36 ms for 4096 requests of 64 adapters,
+// 4.4 ms of 4096, and 67 ms for 16384 of as many, before anything else starts.
 __global__ void __launch_bounds__(256) lora_plan(const LoraParams p, const Plan q) {
     dependents_may_start();
     __shared__ int top[256];
@@ -1141,7 +1143,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // Runs of chunks that lora_grad's blocks share a column block's rows by. Blocks
-// that are all resident at once: 65536 rows of 512 channels take, whole calls,
+// that are all resident at once on 152 SMs (a fixed count, since the workspace
+// and the order of the sums follow it): 65536 rows of 512 channels take, whole calls,
 // at ranks 16, 32, 64 and 128 with 2 blocks an SM 216, 222, 242 and 332 us, with
 // 3 194, 200, 259 and 363, with 4 186, 210, 246 and 337.
 int grad_splits(int64_t M, int64_t C, int64_t N, int64_t R) {

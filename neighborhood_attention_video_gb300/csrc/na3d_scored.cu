@@ -14,11 +14,14 @@
 //
 // The tile kernel (scored_tiles) computes all three passes. One warp holds 16
 // rows, a small box of the grid, and streams the union of their windows in
-// steps of 16 keys through mma.sync. Why warps of 16 rows and not 128-row
-// tiles for tcgen05: what bounds this operator is the work on each score (cap,
-// bias, mask, exponential), and the union of a small box's windows holds half
-// as many scores that no row wants: 320 keys a row against 784 for a (3,7,7)
-// window of 147 keys and a 2 x 8 x 8 tile.
+// steps of 16 keys through mma.sync. Warps of 16 rows were taken for the few
+// scores that no row wants: 320 keys a row against 784 of a 128-row tcgen05
+// tile of 2 x 8 x 8, for a (3,7,7) window of 147. A capped score costs three
+// special-function operations, so that 784 of them would be bound by those
+// near 250 us at (1,16,64,64,8,64), where this takes 260. For scores without a
+// cap the count is no reason: na3d_fwd's 128-row tiles take 65 us for each
+// (8,64,33,8,64) entry with a (3,7,33) window, where this takes 222 with a bias
+// and documents. What bounds this kernel is latency (see scored_tiles).
 //
 // The row functions compute one row of one head by one warp, its lanes
 // splitting the head dim, and skip masked keys, so what those hold never
@@ -399,8 +402,8 @@ __device__ __forceinline__ float move_reference(float top, float& grow, float& r
 // spare: 12 warps of 168 registers 274 us, 16 of 128 spill, 446. Steps that
 // take the next one's scores early, or two or three steps at once, are 4 to 9 %
 // slower. Whole-row (3,7,33) windows with packed, padded clips at
-// (1,8,64,33,8,64): 225 us; HD 128, causal, at (1,8,48,64,16,128): 387 us. A
-// training step at (1,16,32,48,8,64), (3,7,7): 111 us forward, 145 dQ, 248 dK
+// (1,8,64,33,8,64): 222 us; HD 128, causal, at (1,8,48,64,16,128): 375 us. A
+// training step at (1,16,32,48,8,64), (3,7,7): 112 us forward, 144 dQ, 243 dK
 // and dV (four products a step, and 11 columns of a row where the others have
 // 10: near a border more windows hold a key).
 template <int HD, int MODE>

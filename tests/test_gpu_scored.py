@@ -383,3 +383,22 @@ def test_wide_windows_by_norm(case):
     got = run(q, k, v, g, kernel, o)
     for name in want:
         assert norms.excess(got[name], want[name]) <= 1, (name, norms.excess(got[name], want[name]))
+
+
+def test_packed_clips_equal_clips_alone_away_from_cuts():
+    """Rows farther than half a window from another clip are those of the clip by itself;
+    the rows at a cut see the keys on their side only."""
+    shape, kernel, cut = (1, 13, 9, 10, 2, 32), (5, 3, 5), 7
+    q, k, v, g = make(shape, 53)
+    o = make_options(shape, 53, 15.0, True)
+    o["doc"] = (torch.arange(13) >= cut).to(torch.int32)[None, :, None, None].expand(shape[:4]).contiguous()
+    got = run(q, k, v, g, kernel, o)
+    whole = ref.scored(q, k, v, kernel, **o)
+    for frames, away in ((slice(0, cut), slice(0, cut - 2)), (slice(cut, 13), slice(2, 13 - cut))):
+        alone = ref.scored(*(x[:, frames] for x in (q, k, v)), kernel, **dict(o, doc=None))
+        for name in ("out", "lse"):
+            value, bound = alone[name]
+            ref.check(name, got[name][:, frames][:, away], (value[:, away], bound[:, away]))
+    near = slice(cut - 2, cut + 2)
+    for name in ("out", "lse"):
+        ref.check(name, got[name][:, near], tuple(x[:, near] for x in whole[name]))
