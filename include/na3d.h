@@ -197,9 +197,10 @@ int na3d_qkv_proj(const void* x, const void* w, const void* bias, void* qkv,
  * lse_i = log sum_j e^s. A row that sees nothing has out 0 and lse -infinity.
  * What masked keys and padding hold (infinities and NaN included) reaches no
  * row that does not see them; values that are not finite cost time, though,
- * since the rows about them are computed one by one. Sums, statistics and probabilities are fp32; the
- * probabilities are rounded to bf16 for their product with v, out is rounded
- * once.
+ * since the rows about them are computed one by one. Sums, statistics and
+ * probabilities are fp32; the probabilities are rounded to bf16 for their
+ * product with v, out is rounded once. Under a cap a score, and with it lse, is
+ * off by up to 2^-21 of the cap beside 2^-19 of the magnitudes in its sums.
  *
  * q (scaled by HD^-0.5), k, v: bf16 with a token stride, as
  *   na3d_fwd_strided; out: contiguous (B,T,H,W,NH,HD).

@@ -799,8 +799,10 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                     const uint64_t a = f2_pack(sc[v], sc[v + 1]), bias = f2_add(i ? y : x, from[i]);   // minus the reference
                                     uint64_t s;
                                     if (CAP) {
-                                        // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)); within a few 2^-24 of c, and
-                                        // c <= 64 here
+                                        // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)), c up to 66 here. The quotient
+                                        // near 1/2 has half the exponential's 2^-22, the sum's 2^-24 and the
+                                        // reciprocal's 2^-23: with the last rounding under 2^-21 of c, where p takes
+                                        // half a step of bf16, 2^-9 of itself
                                         float e0, e1;
                                         f2_unpack(f2_mul(a, f2_dup(exp_scale)), e0, e1);
                                         f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);

@@ -402,3 +402,17 @@ def test_packed_clips_equal_clips_alone_away_from_cuts():
     near = slice(cut - 2, cut + 2)
     for name in ("out", "lse"):
         ref.check(name, got[name][:, near], tuple(x[:, near] for x in whole[name]))
+
+
+@pytest.mark.parametrize("softcap", [0.5, 8.0, 30.0, 66.0, 67.0, 500.0])
+@pytest.mark.parametrize("scale", [0.01, 0.3])
+def test_lse_of_small_scores_under_a_cap(softcap, scale):
+    """Caps are exact to 2^-21 of the cap: half the exponential's 2^-22, 2^-24 of its sum
+    with 1 and 2^-23 of the reciprocal, of a quotient near 1/2 that is taken twice the
+    cap times, and the rounding of the score."""
+    shape, kernel = (1, 5, 8, 9, 2, 32), (3, 1, 3)
+    q, k, v, g = make(shape, 59, scale)
+    o = dict(softcap=softcap, slopes=None, doc=None, prefix=None)
+    value, bound = ref.scored(q, k, v, kernel, **o)["lse"]
+    got = run(q, k, v, g, kernel, o)["lse"]
+    ref.check("lse", got, (value, bound + 2.0 ** -21 * softcap))
