@@ -614,8 +614,9 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
 
         // Scores under a cap whose bias falls with the distance need no running maximum: a
         // row's largest lies within the cap of 0 (its own position has no bias), so that
-        // the powers stay in the range of fp32 and bf16 with 0 as the reference.
-        const bool bounded = MODE == kFwd && capped && to_log2 <= 96.f && fmaxf(fmaxf(sl[0], sl[1]), sl[2]) <= 0.f;
+        // the powers stay in the range of fp32 and bf16 with 0 as the reference. (Windows of one
+        // to three keys take the general steps: see kManyKeys.)
+        const bool bounded = MODE == kFwd && capped && g.lut == 1 && to_log2 <= 96.f && fmaxf(fmaxf(sl[0], sl[1]), sl[2]) <= 0.f;
         // The table: for each (h, w) of the rows, the bias of a frame's columns, -inf
         // outside the window (or the mask words: word r of a step holds row r in its low
         // and row r + 8 in its high half). It is kept while the head (where it matters) and
@@ -802,7 +803,7 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
                                         // c tanh(a / c) = c - 2 c / (1 + e^(2 a / c)), c up to 66 here. The quotient
                                         // near 1/2 has half the exponential's 2^-22, the sum's 2^-24 and the
                                         // reciprocal's 2^-23: with the last rounding under 2^-21 of c, where p takes
-                                        // half a step of bf16, 2^-9 of itself
+                                        // half a step of bf16, 2^-8 of itself
                                         float e0, e1;
                                         f2_unpack(f2_mul(a, f2_dup(exp_scale)), e0, e1);
                                         f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_dup(1.f)), e0, e1);

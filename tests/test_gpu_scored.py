@@ -416,3 +416,26 @@ def test_lse_of_small_scores_under_a_cap(softcap, scale):
     value, bound = ref.scored(q, k, v, kernel, **o)["lse"]
     got = run(q, k, v, g, kernel, o)["lse"]
     ref.check("lse", got, (value, bound + 2.0 ** -21 * softcap))
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 30.0, 66.0, 300.0])
+@pytest.mark.parametrize("kernel", [(1, 1, 1), (3, 1, 1)])
+def test_a_row_of_one_key_is_its_value(softcap, kernel):
+    """A window of one position, or a clip of one frame in a window along T: out is the
+    value, lse the score, to fp32 rounding (2^-18 of the magnitudes, 32 products and the
+    cap in turn), dv the sum's one term. dq has nothing but what delta's fp32 sum leaves of
+    dp, and dk that and (1 - p) dp: its delta is p dp, with p = e^(s - lse) and s off by
+    2^-21 of the cap in the backward passes."""
+    shape = (1, 5, 7, 10, 2, 32)
+    q, k, v, g = make(shape, 61, 2.0)
+    o = dict(softcap=softcap, slopes=None, prefix=None, doc=torch.arange(5, dtype=torch.int32)[None, :, None, None].expand(shape[:4]).contiguous())
+    got = run(q, k, v, g, kernel, o)
+    a, mag = (q.double() * k.double()).sum(-1), (q.double() * k.double()).abs().sum(-1)
+    lse = softcap * torch.tanh(a / softcap) if softcap else a
+    assert torch.equal(got["out"].cpu(), v)
+    assert torch.equal(got["dv"].cpu(), g)
+    assert bool(((got["lse"].cpu() - lse).abs() <= 2.0 ** -18 * mag).all())
+    left = 2.0 ** -18 * (g.double() * v.double()).abs().sum(-1, keepdim=True)
+    assert bool((got["dq"].cpu().abs() <= left * k.double().abs()).all())
+    left = left * (1 + 2.0 ** -3 * softcap)
+    assert bool((got["dk"].cpu().abs() <= left * q.double().abs()).all())
