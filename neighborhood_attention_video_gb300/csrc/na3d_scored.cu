@@ -615,8 +615,8 @@ scored_tiles(const __grid_constant__ CUtensorMap tm_f0, const __grid_constant__ 
         // Scores under a cap whose bias falls with the distance need no running maximum: a
         // row's largest lies within the cap of 0 (its own position has no bias), so that
         // the powers stay in the range of fp32 and bf16 with 0 as the reference. (Windows of one
-        // to three keys take the general steps: see kManyKeys.)
-        const bool bounded = MODE == kFwd && capped && g.lut == 1 && to_log2 <= 96.f && fmaxf(fmaxf(sl[0], sl[1]), sl[2]) <= 0.f;
+        // to three keys have no table and take the general steps: see kManyKeys.)
+        const bool bounded = MODE == kFwd && capped && to_log2 <= 96.f && fmaxf(fmaxf(sl[0], sl[1]), sl[2]) <= 0.f;
         // The table: for each (h, w) of the rows, the bias of a frame's columns, -inf
         // outside the window (or the mask words: word r of a step holds row r in its low
         // and row r + 8 in its high half). It is kept while the head (where it matters) and
@@ -1237,12 +1237,12 @@ __global__ void __launch_bounds__(256) scored_stat(const ScoredParams p, int64_t
 // some microseconds.
 bool cached_plan(TileGeom* out, const ScoredParams& p, int hd, int mode, int sms) {
     struct Entry {
-        int32_t key[12];
+        int32_t key[13];
         TileGeom g;
     };
     static thread_local Entry cache[16] = {};
     static thread_local unsigned next = 0;
-    const int32_t key[12] = {p.B, p.T, p.H, p.W, p.NH, p.KT, p.KH, p.KW, hd, mode, sms, p.doc != nullptr};
+    const int32_t key[13] = {p.B, p.T, p.H, p.W, p.NH, p.KT, p.KH, p.KW, hd, mode, sms, p.doc != nullptr, p.softcap > 0.f};
     for (const Entry& e : cache)
         if (memcmp(e.key, key, sizeof key) == 0) {
             *out = e.g;

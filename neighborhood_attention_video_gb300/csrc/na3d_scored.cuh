@@ -24,8 +24,8 @@ struct ScoredParams {
     const int32_t* prefix;         // (B) or null
 };
 
-// Is there a plan for the forward pass, or for both backward passes? (Sizes and
-// p.doc's presence count; host only.)
+// Is there a plan for the forward pass, or for both backward passes? (Sizes,
+// the presence of documents and a cap count; host only.)
 bool scored_planned(int hd, const ScoredParams& p, bool backward);
 
 cudaError_t launch_scored_fwd(int hd, const ScoredParams& p, int sms, cudaStream_t stream);

@@ -45,11 +45,12 @@ __host__ __device__ __forceinline__ int range_hi(bool dkv, int i, int K, int N) 
     return dkv ? inv_last(i, K, N) + 1 : win_start(i, K, N) + K;
 }
 
-// From so many keys on a row's sum may be taken without a running maximum. A row of one key then
-// has out off by the rounding of its probability, which would be 1, and lse by 2^-21 of the cap: at
-// unit scores and a cap of 50 lse is 2.7e-6 of its norm off over one key, 1.2e-6 over three and
-// 7e-7 over five. Without it (1,16,64,64,8,64) takes 75, 85 and 133 us with windows of (1,1,1),
-// (1,1,3) and (3,1,1), with it 87, 108 and 167.
+// From so many keys on capped scores take the plain steps, with a table. Forward these have no running
+// maximum: a row of one key has out off by the rounding of its probability, which would be 1. Their
+// cap, the backward passes' too, is exact to 2^-21 of the cap, and so is lse, which is near the scores:
+// at unit scores and a cap of 50 lse is 2.7e-6 of its norm off over one key, 1.2e-6 over three and
+// 7e-7 over five. (1,16,64,64,8,64) with windows of (1,1,1), (1,1,3) and (3,1,1) takes 75, 85 and 133 us
+// so and 87, 108 and 168 in the general steps, its gradients 216, 241 and 380 and 235, 280 and 437.
 constexpr int kManyKeys = 5;
 
 // Geometry of one launch. A block's brick is st x (nw * sh) x sw rows, warp w
@@ -64,8 +65,7 @@ struct TileGeom {
     int32_t nt, nhc, nwc;      // chunks of a unit: frames, and parts along H and W
     int32_t stages;
     int32_t lut;               // 1: a frame's biases and (h, w) windows come from a table of each warp,
-                               // 2: so, and the window has fewer than kManyKeys keys, 0: its windows
-                               // from mask words
+                               // 0: its windows from mask words
     int32_t lut_pitch;         // floats of a table row (one for each (h, w) of the warp's rows)
     int32_t frame_steps;       // steps of 16 columns that a warp's box takes in a frame, at most,
     int32_t chunk_steps;       // and in a chunk
@@ -230,6 +230,7 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
     // positions and bricks past an axis' end are still numbers, frames' distances exact in fp32
     constexpr int most = INT32_MAX - 4096;
     if (p.T > most || p.H > most || p.W > most || p.KT > (1 << 23) || int64_t(p.KH) * p.KW * 2 > kSmemMax) return false;
+    const bool few = p.softcap > 0.f && int64_t(p.KT) * p.KH * p.KW < kManyKeys;
     double best_cost = 0;
     bool found = false;
     for (int st = 1; st <= 16; st *= 2)
@@ -272,8 +273,8 @@ inline bool plan_tiles(TileGeom* best, const ScoredParams& p, int hd, int mode, 
                     const int64_t chunks = int64_t(et) * nhc * g.nwc;
                     g.chunk_steps = ((eh_w < g.cr ? eh_w : g.cr) * g.cc + 15) / 16;
                     g.stages = chunks < 2 ? 1 : 2;
-                    g.lut = int64_t(p.KT) * p.KH * p.KW < kManyKeys ? 2 : 1;
-                    if (!lay_out(&g, hd, mode, docs, frame, room)) {
+                    g.lut = few ? 0 : 1;
+                    if (few || !lay_out(&g, hd, mode, docs, frame, room)) {
                         g.lut = 0;
                         if (!lay_out(&g, hd, mode, docs, frame, room)) {
                             if (g.cr > 1) {   // on to the next smaller cr

@@ -1,7 +1,8 @@
 // Replays on the host the walk of the score-shaped attention's tile kernel, with
 // the planner and the geometry functions that the kernel itself uses. Reads
 // problems from standard input, one a line:
-//   B T H W NH HD KT KH KW docs mode      (mode 0 forward, 1 dQ, 2 dK and dV)
+//   B T H W NH HD KT KH KW options mode   (options: 1 documents, 2 a cap, 3 both;
+//                                          mode 0 forward, 1 dQ, 2 dK and dV)
 // and checks for every brick, warp and chunk that what is read lies inside the
 // grid and what is staged inside its buffer. Prints one line for each problem:
 // "ok <chunks>", "unplanned", or the first thing that is wrong.
@@ -69,7 +70,8 @@ int main() {
     int32_t one = 0;
     while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d", &p.B, &p.T, &p.H, &p.W, &p.NH, &hd, &p.KT, &p.KH, &p.KW,
                       &docs, &mode) == 11) {
-        p.doc = docs ? &one : nullptr;
+        p.doc = docs & 1 ? &one : nullptr;
+        p.softcap = docs & 2 ? 1.f : 0.f;
         TileGeom g;
         if (!plan_tiles(&g, p, hd, mode, 152)) std::printf("unplanned\n");
         else if (g.smem > kSmemMax / blocks_per_sm(hd, mode) || g.cc > 256 || g.cr > 256 || g.bh > 256 ||
