@@ -233,7 +233,8 @@ int na3d_scored_fwd(const void* q, const void* k, const void* v, void* out, floa
  * dq is the gradient of the scaled q that was passed. slopes, doc and prefix
  * are constants. The sums have a fixed order: equal inputs give equal bits.
  * p and da are rounded to bf16 for their products (fp32 sums; for dq da is
- * kept in two such parts), the gradients once at the end.
+ * kept in two such parts), the gradients once at the end. The delta of dq has
+ * the rounding of out in it, but for windows of up to five keys.
  *
  * out, lse: what na3d_scored_fwd wrote for the same arguments; dout: bf16,
  *   contiguous (B,T,H,W,NH,HD).

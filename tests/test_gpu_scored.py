@@ -439,3 +439,24 @@ def test_a_row_of_one_key_is_its_value(softcap, kernel):
     assert bool((got["dq"].cpu().abs() <= left * k.double().abs()).all())
     left = left * (1 + lse.abs()[..., None] / 4)
     assert bool((got["dk"].cpu().abs() <= left * q.double().abs()).all())
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 30.0])
+@pytest.mark.parametrize("kernel", [(1, 1, 1), (1, 3, 1), (5, 1, 1)])
+def test_dq_of_few_keys_is_off_by_its_rounding(kernel, softcap):
+    """Over few keys dq does not take the rounding of out, which delta would bring: it is off
+    by half a step and by fp32 arithmetic. With sums of 16 products 2^-20 of their magnitudes
+    off, a score is by 2^-19 of its own and 2^-21 of the cap (o), p by 2 o, and da by p |dp|
+    times 6 o and 2^-15 for its second bf16 part, the cap's slope and the sum of p dp."""
+    T, H, W, NH, HD = shape = (7, 9, 12, 2, 16)
+    q, k, v, g = make((1, *shape), 67, 2.0)
+    o = make_options((1, *shape), 67, softcap, False, 2, 1)
+    got = run(q, k, v, g, kernel, o)["dq"].cpu().double()
+    want, _ = ref.scored(q, k, v, kernel, dout=g, **o)["dq"]
+    idx = ref.window_index(T, H, W, kernel)
+    aq, ak, av, ag = (x.double().abs().reshape(-1, NH, HD) for x in (q, k, v, g))
+    off = 2.0 ** -19 * torch.einsum("nhd,nkhd->nkh", aq, ak[idx]).amax(1) + 2.0 ** -21 * softcap
+    dp = torch.einsum("nhd,nkhd->nkh", ag, av[idx]).amax(1)
+    bound = ((6 * off + 2.0 ** -15) * dp)[..., None] * ak[idx].amax(1)
+    bound = ref.HALF * want.abs() + bound.reshape(want.shape)
+    assert bool(((got - want).abs() <= bound).all())
