@@ -460,3 +460,24 @@ def test_dq_of_few_keys_is_off_by_its_rounding(kernel, softcap):
     bound = ((6 * off + 2.0 ** -15) * dp)[..., None] * ak[idx].amax(1)
     bound = ref.HALF * want.abs() + bound.reshape(want.shape)
     assert bool(((got - want).abs() <= bound).all())
+
+
+def test_small_window_backward_in_a_graph():
+    """Both of its passes for dQ, captured and replayed on other inputs."""
+    shape, kernel = (1, 6, 9, 11, 2, 32), (1, 3, 1)
+    dev = [x.cuda() for x in make(shape, 71)]
+    out, lse = torch.empty_like(dev[0]), torch.empty(shape[:5], device="cuda")
+    grads = [torch.empty_like(dev[0]) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        na.na3d_scored_fwd(*dev[:3], out, kernel, lse, softcap=9.0)
+        na.na3d_scored_bwd(*dev[:3], out, lse, dev[3], *grads, kernel, softcap=9.0)
+    for seed in (72, 73):
+        new = make(shape, seed)
+        for d, s in zip(dev, new):
+            d.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = ref.scored(*new[:3], kernel, dout=new[3], softcap=9.0)
+        for name, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+            ref.check(name, x, want[name])
