@@ -48,7 +48,8 @@ enum na3d_status {
     NA3D_ERR_CUDA = 9,           /* a CUDA runtime or driver call failed */
     NA3D_ERR_DEVICE_TIMEOUT = 10, /* a pipeline wait inside the kernel gave up */
     NA3D_ERR_UNSUPPORTED = 11    /* valid but not implemented: HD > 128 or a softcap outside its range in
-                                     the na3d_scored_ calls, R > 128 in the na3d_lora_ calls */
+                                     the na3d_scored_ calls, R > 128 in the na3d_lora_ calls, what na3d_norm_rope and
+                                     na3d_cross_fwd name */
 };
 
 /*
@@ -322,6 +323,149 @@ int na3d_lora_qkv_proj_bwd(const void* dqkv, const void* x, const void* w, const
  * (backward 1); -1 where a size is invalid or not supported. */
 int64_t na3d_lora_workspace(int64_t M, int64_t C, int64_t NH, int64_t HD, int64_t R,
                             int64_t n_requests, int64_t n_adapters, int backward);
+
+/*
+ * na3d_rope_table - the cosines and sines that na3d_norm_rope turns by. For
+ * axis a of T, H, W with R_a values of a head (R_a / 2 pairs), position n and
+ * pair i: the angle (offset_a + scale_a n) theta^(-2 i / R_a), computed in 64
+ * bits, its cosine and sine rounded to fp32. Layout: (T, RT/2, 2), then
+ * (H, RH/2, 2), then (W, RW/2, 2), so T*RT + H*RH + W*RW values; a caller with
+ * other frequencies fills the same layout. A grid's table is made once and
+ * kept; offsets place a tile in a larger video, scales stretch positions.
+ *
+ * table: DEVICE, fp32, 8-byte aligned.
+ * RT, RH, RW: even, >= 0, not all 0 (else NA3D_ERR_SHAPE). theta > 0, offsets
+ *   and scales finite (else NA3D_ERR_UNSUPPORTED). Fewer than 2^29 values.
+ * Asynchronous on `stream`; errors as na3d_fwd.
+ */
+int na3d_rope_table(float* table, int64_t T, int64_t H, int64_t W, int64_t RT, int64_t RH, int64_t RW,
+                    double theta, double t_offset, double h_offset, double w_offset, double t_scale,
+                    double h_scale, double w_scale, void* stream);
+
+/*
+ * na3d_norm_rope - the RMS norm of each head of q and k and the rotation by the
+ * position, what stands between the projection and the attention in many video
+ * models. For a head x of HD values at grid position (t, h, w):
+ *   u = x / sqrt(mean(x^2) + eps)            (norm; else u = x)
+ *   y = weight u                             (weight NULL: ones)
+ *   out = scale R y                          (scale: q_scale for q, 1 for k)
+ * R turns P = (RT + RH + RW) / 2 pairs of the first 2 P values, (a, b) to
+ * (a cos - b sin, b cos + a sin), by the table's angles: the first RT / 2 pairs
+ * by t's, the next RH / 2 by h's, the next RW / 2 by w's. Pair i is (2 i, 2 i + 1)
+ * where `interleaved`, else (i, P + i). Values from 2 P on do not turn. Sums are
+ * fp32, the result is rounded to bf16 once.
+ *
+ * The attention wants q scaled by HD^-0.5: that is q_scale here, since the norm
+ * takes away the scale that na3d_qkv_proj gives. A norm of q so scaled with
+ * eps / HD is the norm of the unscaled q with eps.
+ *
+ * q, q_out: bf16, tokens of NH heads; k, k_out: of NKV heads, or both NULL with
+ *   NKV = 0. Token strides as in na3d_fwd_strided (for instance blocks of a fused
+ *   projection). An output may be its own input (pointer and stride alike), else
+ *   it shares no element with an input or the other output.
+ * q_weight, k_weight: bf16 (HD), 16-byte aligned, or NULL; with `norm` alone.
+ * table: as na3d_rope_table makes it, or NULL with RT = RH = RW = 0.
+ * RT, RH, RW: even, >= 0, their sum at most HD (else NA3D_ERR_SHAPE).
+ * HD: a power of two from 16 to 512. Not interleaved: RT + RH + RW a multiple of
+ *   16. norm: eps > 0 and finite (k_eps where there is k). q_scale finite. Else
+ *   NA3D_ERR_UNSUPPORTED. B*T*H*W below 2^31.
+ * Asynchronous on `stream`, may be captured; errors as na3d_fwd.
+ */
+int na3d_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const void* q_weight,
+                   const void* k_weight, const float* table, int64_t B, int64_t T, int64_t H, int64_t W,
+                   int64_t NH, int64_t NKV, int64_t HD, int64_t RT, int64_t RH, int64_t RW,
+                   int64_t q_token_stride, int64_t k_token_stride, int64_t q_out_token_stride,
+                   int64_t k_out_token_stride, int norm, float q_eps, float k_eps, float q_scale,
+                   int interleaved, void* stream);
+
+/*
+ * na3d_norm_rope_bwd - the gradients of na3d_norm_rope from those of its
+ * outputs. With r = 1 / sqrt(mean(x^2) + eps), u = x r and g = scale R^T dout:
+ *   dweight = sum over all rows of g u,
+ *   dx = r (weight g - u mean(weight g u))   (without norm: dx = g).
+ * A row whose gradient is all zeros (padding, say) gives dx = 0 and adds nothing
+ * to dweight, whatever x holds there. Sums are fp32 in a fixed order.
+ *
+ * q, k: what the forward pass read; dq_out, dk_out: the gradients of its outputs.
+ * dq, dk: bf16, each may be its own dq_out (dk_out) or q (k) with the same stride;
+ *   else they share no element with an input or one another.
+ * dq_weight, dk_weight: fp32 (HD), or NULL where not wanted; with `norm` alone,
+ *   dk_weight where there is k (else NA3D_ERR_UNSUPPORTED).
+ * work: na3d_norm_rope_workspace(HD) bytes, 16-byte aligned, one call at a time;
+ *   NULL where neither gradient of a weight is wanted.
+ * All other arguments and errors are those of na3d_norm_rope.
+ */
+int na3d_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, void* dq,
+                       void* dk, float* dq_weight, float* dk_weight, const void* q_weight,
+                       const void* k_weight, const float* table, void* work, int64_t B, int64_t T,
+                       int64_t H, int64_t W, int64_t NH, int64_t NKV, int64_t HD, int64_t RT, int64_t RH,
+                       int64_t RW, int64_t q_token_stride, int64_t k_token_stride,
+                       int64_t dq_out_token_stride, int64_t dk_out_token_stride, int64_t dq_token_stride,
+                       int64_t dk_token_stride, int norm, float q_eps, float k_eps, float q_scale,
+                       int interleaved, void* stream);
+
+/* Bytes of workspace of na3d_norm_rope_bwd; -1 where HD is not supported. */
+int64_t na3d_norm_rope_workspace(int64_t HD);
+
+/*
+ * na3d_cross_fwd - attention of a grid's tokens to states of another length: a
+ * prompt's, or those of earlier frames. Token i of an entry sees state j where
+ * doc_i = kv_doc_j >= 0; clips that are packed into one grid so read their own
+ * states. With s_ij = q_i . k_j (q scaled by HD^-0.5), head h of q with head
+ * h / (NH / NKV) of k and v:
+ *   out_i = sum_j p_ij v_j, p the softmax of the s that are seen,
+ *   lse_i = log sum_j e^s_ij.
+ * A token that sees nothing has out 0 and lse -infinity. What unseen states and
+ * tokens of negative documents hold (infinities and NaN included) reaches no
+ * other row. Sums and statistics are fp32; the probabilities are rounded to bf16
+ * for their product with v, out is rounded once.
+ *
+ * q: bf16, L = T*H*W tokens to each of B entries, NH heads; k, v: bf16, S states
+ *   to an entry, NKV heads; token strides as in na3d_fwd_strided (the two blocks
+ *   of a fused (B,S,2,NKV,HD) projection, for instance), L (S) tokens from entry
+ *   to entry.
+ * out: bf16, contiguous (B,L,NH,HD). lse: fp32 (B,L,NH), or NULL.
+ * doc: DEVICE, int32 (B,L), or NULL: all 0. kv_doc: DEVICE, int32 (B,S), or NULL:
+ *   all 0. Negative documents see nothing and are seen by nothing (padding). Read
+ *   when the kernels run.
+ * work: DEVICE workspace of na3d_cross_workspace(..., 0) bytes, 16-byte aligned,
+ *   one call at a time; NULL where that is 0.
+ * B, L, S, NH, NKV >= 1, NKV divides NH (else NA3D_ERR_SHAPE); HD: 16, 32, 64 or
+ *   128, NH / NKV <= 64 (else NA3D_ERR_UNSUPPORTED).
+ * out, lse and work must not overlap an input or one another. Errors,
+ * asynchrony and capture as na3d_fwd_strided.
+ */
+int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* work,
+                   int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD,
+                   int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                   const int32_t* doc, const int32_t* kv_doc, void* stream);
+
+/*
+ * na3d_cross_bwd - the gradients of na3d_cross_fwd. With p = e^(s - lse),
+ * dp = dout_i . v_j, delta_i = sum_j p dp and ds = p (dp - delta_i):
+ *   dq_i = sum_j ds k_j,   dk_j = sum_i ds q_i,   dv_j = sum_i p dout_i,
+ * the last two over the tokens and the heads of q that share the head. dq is the
+ * gradient of the scaled q. Sums are fp32 in a fixed order; p and ds are rounded
+ * to bf16 for their products, the gradients once at the end.
+ *
+ * out, lse: what the forward pass wrote; dout: bf16, contiguous (B,L,NH,HD).
+ * dq, dk, dv: bf16 with token strides, written whole (zeros where nothing is
+ *   seen). They share no element with one another (dk and dv may be blocks of one
+ *   fused gradient) and overlap no input.
+ * work: na3d_cross_workspace(..., 1) bytes.
+ * All other arguments and errors are those of na3d_cross_fwd.
+ */
+int na3d_cross_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                   const void* dout, void* dq, void* dk, void* dv, void* work, int64_t B, int64_t L,
+                   int64_t S, int64_t NH, int64_t NKV, int64_t HD, int64_t q_token_stride,
+                   int64_t k_token_stride, int64_t v_token_stride, int64_t dq_token_stride,
+                   int64_t dk_token_stride, int64_t dv_token_stride, const int32_t* doc,
+                   const int32_t* kv_doc, void* stream);
+
+/* Bytes of workspace of na3d_cross_fwd (backward 0) or na3d_cross_bwd (backward
+ * 1); -1 where a size is invalid or not supported. */
+int64_t na3d_cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD,
+                             int backward);
 
 /*
  * na3d_selftest_withhold - a self-test of the kernel's failure detection:

@@ -17,6 +17,8 @@ __all__ = [
     "NA3DError", "NA3DUnavailable", "na3d_attention", "na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region",
     "na3d_qkv_proj", "qkv_views", "na3d_scored_fwd", "na3d_scored_attention", "na3d_scored_bwd",
     "na3d_lora_qkv_proj", "na3d_lora_qkv_proj_bwd", "na3d_lora_workspace",
+    "na3d_rope_table", "na3d_norm_rope", "na3d_norm_rope_bwd", "na3d_norm_rope_workspace",
+    "na3d_cross_fwd", "na3d_cross_attention", "na3d_cross_bwd", "na3d_cross_workspace",
     "na3d_scored_bwd_workspace", "na3d_status_string", "na3d_plan",
     "na3d_device_status", "library_path", "load_library", "EXPORTED_SYMBOLS",
 ]
@@ -26,6 +28,8 @@ LIB_PATH = os.path.join(_PKG, "libna3d.so")
 EXPORTED_SYMBOLS = ("na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region", "na3d_qkv_proj",
                     "na3d_scored_fwd", "na3d_scored_bwd", "na3d_scored_bwd_workspace",
                     "na3d_lora_qkv_proj", "na3d_lora_qkv_proj_bwd", "na3d_lora_workspace",
+                    "na3d_rope_table", "na3d_norm_rope", "na3d_norm_rope_bwd", "na3d_norm_rope_workspace",
+                    "na3d_cross_fwd", "na3d_cross_bwd", "na3d_cross_workspace",
                     "na3d_selftest_withhold", "na3d_status_string", "na3d_plan",
                     "na3d_device_status")
 
@@ -33,6 +37,7 @@ NA3D_OK = 0
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _lib = None
 
 
@@ -90,6 +95,21 @@ def load_library():
     lib.na3d_lora_qkv_proj_bwd.restype = ctypes.c_int
     lib.na3d_lora_workspace.argtypes = [_I64] * 7 + [ctypes.c_int]
     lib.na3d_lora_workspace.restype = _I64
+    lib.na3d_rope_table.argtypes = [_P] + [_I64] * 6 + [_F64] * 7 + [_P]
+    lib.na3d_rope_table.restype = ctypes.c_int
+    rope_how = [ctypes.c_int, _F32, _F32, _F32, ctypes.c_int, _P]
+    lib.na3d_norm_rope.argtypes = [_P] * 7 + [_I64] * 14 + rope_how
+    lib.na3d_norm_rope.restype = ctypes.c_int
+    lib.na3d_norm_rope_bwd.argtypes = [_P] * 12 + [_I64] * 16 + rope_how
+    lib.na3d_norm_rope_bwd.restype = ctypes.c_int
+    lib.na3d_norm_rope_workspace.argtypes = [_I64]
+    lib.na3d_norm_rope_workspace.restype = _I64
+    lib.na3d_cross_fwd.argtypes = [_P] * 6 + [_I64] * 9 + [_P] * 3
+    lib.na3d_cross_fwd.restype = ctypes.c_int
+    lib.na3d_cross_bwd.argtypes = [_P] * 10 + [_I64] * 12 + [_P] * 3
+    lib.na3d_cross_bwd.restype = ctypes.c_int
+    lib.na3d_cross_workspace.argtypes = [_I64] * 6 + [ctypes.c_int]
+    lib.na3d_cross_workspace.restype = _I64
     lib.na3d_selftest_withhold.argtypes = [_P, _P, _P, _P] + [_I64] * 10 + [_P]
     lib.na3d_selftest_withhold.restype = ctypes.c_int
     lib.na3d_status_string.argtypes = [ctypes.c_int]
@@ -315,16 +335,21 @@ def _check_bf16_of_shape(shape, names, tensors):
         raise ValueError("q must have a 6-D (B,T,H,W,NH,HD) shape")
 
 
-def _empty(stream, like, shape, dtype):
-    """A new tensor on the device of `like`, allocated on the stream that the
-    call uses, so that the allocator may reuse its memory only behind the call."""
+def _empty_on(stream, device, shape, dtype):
+    """A new tensor on `device`, allocated on the stream that the call uses, so
+    that the allocator may reuse its memory only behind the call."""
     torch = _torch_module()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(stream, like, shape, dtype):
+    """``_empty_on`` the device of `like`."""
+    return _empty_on(stream, like.device, shape, dtype)
 
 
 _kept = threading.local()   # a thread's workspaces, by device and stream; 16 at most
@@ -551,6 +576,254 @@ def na3d_lora_qkv_proj_bwd(dqkv, x, w, lora_a, lora_b, scaling, offsets, adapter
                                     work.data_ptr(), *sizes, _stream_handle(stream))
     if rc != NA3D_OK:
         raise NA3DError(rc, "na3d_lora_qkv_proj_bwd")
+
+
+def na3d_rope_table(grid, rope_dims, theta=10000.0, offset=(0.0, 0.0, 0.0), scale=(1.0, 1.0, 1.0), device=None,
+                    stream=None):
+    """The fp32 table of cosines and sines for ``na3d_norm_rope`` on a grid
+    (T, H, W), ``rope_dims`` = (RT, RH, RW) values of a head turning with each
+    axis: (T*RT + H*RH + W*RW) / 2 rows of (cos, sin) of the angles
+    (offset + scale * position) * theta**(-2 i / R), axis after axis, position
+    after position. Made once for a grid and kept; a table of other frequencies
+    is filled in the same layout. On the current CUDA device."""
+    lib = _lib if _lib is not None else load_library()
+    torch = _torch_module()
+    T, H, W = (int(x) for x in grid)
+    RT, RH, RW = (int(x) for x in rope_dims)
+    if min(T, H, W) < 1 or min(RT, RH, RW) < 0 or (RT | RH | RW) & 1 or not RT + RH + RW:
+        raise NA3DError(2, "na3d_rope_table")
+    table = _empty_on(stream, device if device is not None else torch.device("cuda", torch.cuda.current_device()),
+                      ((T * RT + H * RH + W * RW) // 2, 2), torch.float32)
+    if table.get_device() != torch.cuda.current_device():
+        raise TypeError("device must be the current CUDA device")
+    rc = lib.na3d_rope_table(table.data_ptr(), T, H, W, RT, RH, RW, theta, *offset, *scale, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_rope_table")
+    return table
+
+
+def _head_rows(torch, dev, name, t, grid, heads, HD):
+    """t's token stride, t a bf16 view (*grid, heads, HD) on device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+    if t.dim() != 6 or t.shape[:4] != grid or t.shape[5] != HD or (heads is not None and t.shape[4] != heads):
+        raise ValueError(f"{name} must have a 6-D (B,T,H,W,heads,HD) shape that goes with q's")
+    return _token_stride(name, t)
+
+
+def _rope_call(q, k, q_rows, k_rows, q_weight, k_weight, table, rope_dims):
+    """What both directions of the norm and rotation check: (sizes, strides, weight and
+    table pointers). q_rows, k_rows: the (name, tensor) of q's and k's shape besides q and k."""
+    torch = _torch_module()
+    dev = torch.cuda.current_device() if _cuda_ok else -2
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 6:
+        raise ValueError("q must have a 6-D (B,T,H,W,NH,HD) shape")
+    shape = q.shape
+    grid, NH, HD = shape[:4], shape[4], shape[5]
+    q_ts = [_head_rows(torch, dev, n, t, grid, NH, HD) for n, t in (("q", q), *q_rows)]
+    if k is None:
+        if any(t is not None for _, t in k_rows) or k_weight is not None:
+            raise ValueError("k's tensors need k")
+        NKV, k_ts = 0, [0] * len(q_ts)
+    else:
+        k_ts = [_head_rows(torch, dev, "k", k, grid, None, HD)]
+        NKV = k.shape[4]
+        k_ts += [_head_rows(torch, dev, n, t, grid, NKV, HD) for n, t in k_rows]
+    RT, RH, RW = rope_dims
+    pointers = []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check_one(torch, dev, name, w, torch.bfloat16, (HD,))
+        pointers.append(None if w is None else w.data_ptr())
+    if table is not None:
+        rows = (grid[1] * RT + grid[2] * RH + grid[3] * RW) // 2
+        _check_one(torch, dev, "table", table, torch.float32, (rows, 2))
+    pointers.append(None if table is None else table.data_ptr())
+    sizes = (*grid, NH, NKV, HD, int(RT), int(RH), int(RW))
+    return sizes, [x for pair in zip(q_ts, k_ts) for x in pair], pointers
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def na3d_norm_rope(q, k, q_out, k_out, q_weight=None, k_weight=None, table=None, rope_dims=(0, 0, 0), norm=True,
+                   q_eps=1e-6, k_eps=1e-6, q_scale=1.0, interleaved=True, stream=None) -> None:
+    """q_out, k_out = the heads of q and k, RMS-normed (``norm``; ``q_weight``,
+    ``k_weight``: bf16 (HD,) or None for ones) and turned by their position on the
+    grid (see ``na3d_norm_rope`` in include/na3d.h). q and q_out: (B, T, H, W, NH,
+    HD), k and k_out: (B, T, H, W, NKV, HD) or both None; all may be views with a
+    token stride, an output may be its own input. ``table``: what
+    ``na3d_rope_table`` made for (T, H, W) and ``rope_dims`` = (RT, RH, RW), the
+    values of a head that turn with each axis, or None with (0, 0, 0). Pairs are
+    neighbours (``interleaved``) or the halves of the values that turn. ``q_scale``
+    multiplies q_out: HD**-0.5 makes it what the attention wants. For a q that
+    ``na3d_qkv_proj`` scaled by HD**-0.5, q_eps = eps / HD gives the norm of the
+    unscaled q. Autograd does not see the call: the gradients come from
+    ``na3d_norm_rope_bwd``."""
+    lib = _lib if _lib is not None else load_library()
+    sizes, strides, at = _rope_call(q, k, (("q_out", q_out),), (("k_out", k_out),), q_weight, k_weight, table, rope_dims)
+    rc = lib.na3d_norm_rope(q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), *at, *sizes, *strides,
+                            1 if norm else 0, q_eps, k_eps, q_scale, 1 if interleaved else 0, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_norm_rope")
+
+
+def na3d_norm_rope_workspace(head_dim) -> int:
+    """Bytes of workspace that ``na3d_norm_rope_bwd`` uses for the weights' gradients."""
+    need = int(load_library().na3d_norm_rope_workspace(int(head_dim)))
+    if need < 0:
+        raise ValueError("head_dim must be a power of two from 16 to 512")
+    return need
+
+
+def na3d_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=None, q_weight=None, k_weight=None,
+                       table=None, rope_dims=(0, 0, 0), norm=True, q_eps=1e-6, k_eps=1e-6, q_scale=1.0,
+                       interleaved=True, work=None, stream=None) -> None:
+    """dq, dk = the gradients of ``na3d_norm_rope`` with respect to q and k, for
+    those of its outputs (``dq_out``, ``dk_out``); ``dq_weight``, ``dk_weight``: fp32
+    (HD,) for the weights' gradients, or None. dq may be dq_out or q, dk dk_out or
+    k; all may be views with a token stride. q and k are the forward pass's inputs,
+    the other arguments the forward pass's. ``work``: a tensor of
+    ``na3d_norm_rope_workspace`` bytes, kept by the caller (one call at a time);
+    None takes one that the binding keeps (for this thread and the current stream;
+    a call with a ``stream`` or under capture allocates its own)."""
+    lib = _lib if _lib is not None else load_library()
+    sizes, strides, at = _rope_call(q, k, (("dq_out", dq_out), ("dq", dq)), (("dk_out", dk_out), ("dk", dk)), q_weight,
+                                    k_weight, table, rope_dims)
+    _check_on_device([(n, w, _torch.float32, (sizes[6],)) for n, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight))
+                      if w is not None])
+    if dq_weight is not None or dk_weight is not None:
+        work = _workspace(work, max(0, lib.na3d_norm_rope_workspace(sizes[6])), q, stream)
+    rc = lib.na3d_norm_rope_bwd(q.data_ptr(), _at(k), dq_out.data_ptr(), _at(dk_out), dq.data_ptr(), _at(dk),
+                                _at(dq_weight), _at(dk_weight), *at, _at(work), *sizes, *strides, 1 if norm else 0, q_eps,
+                                k_eps, q_scale, 1 if interleaved else 0, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_norm_rope_bwd")
+
+
+def _state_stride(name, t) -> int:
+    """Elements between consecutive states of a (B,S,NKV,HD) view whose heads are packed."""
+    st, sh = t.stride(), t.shape
+    if st[3] != 1 or (sh[2] > 1 and st[2] != sh[3]):
+        raise ValueError(f"{name}: heads must be packed (strides [..., HD, 1])")
+    if sh[1] > 1:
+        if sh[0] > 1 and st[0] != sh[1] * st[1]:
+            raise ValueError(f"{name}: states must share one token stride")
+        return st[1]
+    return st[0] if sh[0] > 1 else sh[2] * sh[3]
+
+
+def _cross_call(q, rows, states, doc, kv_doc):
+    """What both directions of the attention to other states check: (sizes, token
+    strides of the tensors, pointers of doc and kv_doc). rows: (name, tensor) like q;
+    states: (name, tensor) of k's shape, k first."""
+    torch = _torch_module()
+    dev = torch.cuda.current_device() if _cuda_ok else -2
+    bf16 = torch.bfloat16
+    for name, t, dims in (*((n, t, 6) for n, t in (("q", q), *rows)), *((n, t, 4) for n, t in states)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not bf16 or t.get_device() != dev:
+            raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+        if t.dim() != dims:
+            raise ValueError(f"{name} must be {dims}-D: q (B,T,H,W,NH,HD), k and v (B,S,NKV,HD)")
+    shape, k_shape = q.shape, states[0][1].shape
+    for name, t in rows:
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape of q")
+    for name, t in states:
+        if t.shape != k_shape:
+            raise ValueError(f"{name} must have the shape of k")
+    if k_shape[0] != shape[0] or k_shape[3] != shape[5]:
+        raise ValueError("q and k must agree on B and HD")
+    pointers = []
+    for name, t, want in (("doc", doc, shape[:4]), ("kv_doc", kv_doc, k_shape[:2])):
+        if t is not None:
+            _check_one(torch, dev, name, t, torch.int32, want)
+        pointers.append(None if t is None else t.data_ptr())
+    B, T, H, W, NH, HD = shape
+    return (B, T * H * W, k_shape[1], NH, k_shape[2], HD), pointers
+
+
+def na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward=False) -> int:
+    """Bytes of workspace of ``na3d_cross_fwd``, or of ``na3d_cross_bwd``, for L = T*H*W tokens an entry."""
+    need = int(load_library().na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, 1 if backward else 0))
+    if need < 0:
+        raise ValueError("sizes that na3d_cross_fwd does not take")
+    return need
+
+
+def _call_cross_fwd(q, k, v, out, lse, sizes, pointers, work, stream) -> None:
+    """The call behind na3d_cross_fwd: all but work is checked."""
+    lib = _lib if _lib is not None else load_library()
+    need = lib.na3d_cross_workspace(*sizes, 0)
+    if need > 0:
+        work = _workspace(work, need, q, stream)
+    rc = lib.na3d_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(work), *sizes,
+                            _token_stride("q", q), _state_stride("k", k), _state_stride("v", v), *pointers,
+                            _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_cross_fwd")
+
+
+def na3d_cross_fwd(q, k, v, out, lse=None, doc=None, kv_doc=None, work=None, stream=None) -> None:
+    """Attention of a grid's tokens q (B, T, H, W, NH, HD) to states k, v (B, S,
+    NKV, HD) of another length, e.g. a prompt's (see ``na3d_cross_fwd`` in
+    include/na3d.h). q is scaled by HD**-0.5; NKV divides NH, heads of q share those
+    of k and v in runs of NH / NKV; q, k and v may be views with a token stride, e.g.
+    ``kv[:, :, 0]`` of a fused (B, S, 2, NKV, HD) projection. ``doc``: int32 (B, T, H,
+    W), ``kv_doc``: int32 (B, S); a token sees the states of its document, None is
+    document 0 for all, negative ones are padding. ``out`` is contiguous; ``lse``,
+    where given, receives the fp32 (B, T, H, W, NH) log-sum-exp. HD up to 128.
+    ``work``: a tensor of ``na3d_cross_workspace`` bytes, kept by the caller (one
+    call at a time); None takes one that the binding keeps where one is needed (for
+    this thread and the current stream; a call with a ``stream`` or under capture
+    allocates its own). Autograd does not see the call: the gradients come from
+    ``na3d_cross_bwd``."""
+    sizes, pointers = _cross_call(q, (("out", out),), (("k", k), ("v", v)), doc, kv_doc)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    if lse is not None:
+        _check_on_device((("lse", lse, _torch.float32, q.shape[:5]),))
+    _call_cross_fwd(q, k, v, out, lse, sizes, pointers, work, stream)
+
+
+def na3d_cross_attention(q, k, v, doc=None, kv_doc=None, return_lse=False, stream=None):
+    """``na3d_cross_fwd`` into a new tensor: returns out, or (out, lse) where
+    ``return_lse`` is true (what ``na3d_cross_bwd`` needs)."""
+    torch = _torch_module()
+    sizes, pointers = _cross_call(q, (), (("k", k), ("v", v)), doc, kv_doc)
+    out = _empty(stream, q, q.shape, torch.bfloat16)
+    lse = _empty(stream, q, q.shape[:-1], torch.float32) if return_lse else None
+    _call_cross_fwd(q, k, v, out, lse, sizes, pointers, None, stream)
+    return (out, lse) if return_lse else out
+
+
+def na3d_cross_bwd(q, k, v, out, lse, dout, dq, dk, dv, doc=None, kv_doc=None, work=None, stream=None) -> None:
+    """dq, dk, dv = the gradients of ``na3d_cross_fwd`` for the gradient ``dout`` of
+    its output. ``out`` and ``lse`` are what the forward pass wrote; the other
+    arguments are the forward pass's. dq, dk and dv may be views with a token stride,
+    e.g. the blocks of a fused gradient. ``work``: a tensor of
+    ``na3d_cross_workspace`` bytes with ``backward=True``, as there."""
+    lib = _lib if _lib is not None else load_library()
+    sizes, pointers = _cross_call(q, (("out", out), ("dout", dout), ("dq", dq)),
+                                  (("k", k), ("v", v), ("dk", dk), ("dv", dv)), doc, kv_doc)
+    if not (out.is_contiguous() and dout.is_contiguous()):
+        raise ValueError("out and dout must be contiguous")
+    _check_on_device((("lse", lse, _torch.float32, q.shape[:5]),))
+    work = _workspace(work, max(0, lib.na3d_cross_workspace(*sizes, 1)), q, stream)
+    rc = lib.na3d_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+                            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(), *sizes,
+                            *(_token_stride(n, t) if t.dim() == 6 else _state_stride(n, t)
+                              for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))),
+                            *pointers, _stream_handle(stream))
+    if rc != NA3D_OK:
+        raise NA3DError(rc, "na3d_cross_bwd")
 
 
 def na3d_plan(T, H, W, NH, HD, KT, KH, KW) -> dict:

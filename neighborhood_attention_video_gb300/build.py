@@ -18,9 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libna3d.so")
 SOURCES = ["na3d_kernel.cu", "na3d_proj.cu", "na3d_scored.cu", "na3d_lora.cu", "na3d_api.cu",
-           "na3d_packed_api.cu"]
+           "na3d_packed_api.cu", "na3d_rope.cu", "na3d_cross.cu", "na3d_block_api.cu"]
 DEPS = SOURCES + ["na3d_kernel.cuh", "na3d_proj.cuh", "na3d_scored.cuh", "na3d_lora.cuh",
-                  "na3d_scored_plan.cuh", "na3d_host.cuh", "sm103_ptx.cuh"]
+                  "na3d_rope.cuh", "na3d_cross.cuh", "na3d_scored_plan.cuh", "na3d_host.cuh", "sm103_ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -12,38 +12,13 @@
 
 namespace {
 
+using na3d::aligned;
 using na3d::is_pow2;
 using na3d::mul_ok;
 using na3d::overlaps;
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-// `row` values every `stride` elements: bytes spanned, or an error. The strides
-// of a TMA descriptor stay below 2^40 bytes: `grid` tokens of a batch entry.
-int strided_span(int64_t tokens, int64_t grid, int64_t stride, int64_t row, int64_t* bytes) {
-    if (stride < row) return NA3D_ERR_SHAPE;
-    if (stride % 8 != 0) return NA3D_ERR_ALIGN;
-    int64_t span;
-    if (stride >= (int64_t(1) << 39) / grid || !mul_ok(tokens - 1, stride, &span) || !mul_ok(span + row, 2, bytes))
-        return NA3D_ERR_OVERFLOW;
-    return NA3D_OK;
-}
-
-// Do two written tensors of `tokens` rows of `row` values share an element?
-// Views of one fused tensor (equal strides, disjoint columns) do not.
-bool written_overlap(const void* a, int64_t a_bytes, int64_t a_ts, const void* b, int64_t b_bytes, int64_t b_ts,
-                     int64_t row) {
-    if (!overlaps(a, a_bytes, b, b_bytes)) return false;
-    if (a_ts != b_ts) return true;
-    const intptr_t d = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2;
-    const int64_t off = ((d % a_ts) + a_ts) % a_ts;   // column of b's rows in a's
-    return off < row || off > a_ts - row;
-}
-
-struct Span {
-    const void* ptr;
-    int64_t bytes;
-};
+using na3d::Span;
+using na3d::strided_span;
+using na3d::written_overlap;
 
 // Checks that the calls of both directions share; *n = B*T*H*W tokens.
 int check_scored(int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t HD, int64_t KT, int64_t KH,

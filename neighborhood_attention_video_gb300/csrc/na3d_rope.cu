@@ -1,0 +1,302 @@
+// RMS norm of each head of queries and keys and the rotation by their position
+// along T, H and W, in one pass, and its backward pass.
+//
+// A head x of HD values at grid position (t, h, w):
+//   u = x r, r = (mean x^2 + eps)^(-1/2)       (r = 1 without the norm)
+//   z = scale R(t,h,w) (w u)
+// R turns pair i of the first 2 P values by the angle of its axis' position; the
+// values behind them stay. Backward, with g = scale R^T dz:
+//   dw = sum over the rows of g u,   dx = r (w g - u mean(w g u)).
+//
+// Bound by memory: each value is read once and written once, so everything is
+// laid out for whole lines in flight. HD/16 lanes hold a head, two 16-byte
+// pieces each (pairs are within a piece, or the same place of both), a warp
+// 512/HD heads at once; the cosines of a token are read once and serve all its
+// heads of q and k.
+#include <algorithm>
+
+#include "na3d_rope.cuh"
+#include "sm103_ptx.cuh"
+
+namespace na3d {
+
+namespace {
+
+using std::max;
+using std::min;
+
+constexpr int kWarps = 8;
+// The blocks of a backward launch: their sums of the weights' gradients are
+// joined in this order, whatever the device.
+constexpr int kGradBlocks = 152 * 2;
+
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+struct Piece {   // 16 values of a head: two 16-byte pieces
+    uint4 a, b;
+};
+
+__device__ __forceinline__ void unpack(const Piece& p, float (&f)[16]) {
+    const uint32_t v[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[2 * i] = lo16(v[i]);
+        f[2 * i + 1] = hi16(v[i]);
+    }
+}
+
+__device__ __forceinline__ Piece pack(const float (&f)[16]) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
+}
+
+// Data that is used once: past L1, and the first to leave L2.
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+// The 16 values turned by the eight pairs' angles (DIR 1) or back (-1).
+template <bool INTER, int DIR>
+__device__ __forceinline__ void turn(float (&f)[16], const float2 (&cs)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float &x = f[INTER ? 2 * i : i], &y = f[INTER ? 2 * i + 1 : 8 + i];
+        const float a = x, b = y, c = cs[i].x, s = DIR * cs[i].y;
+        x = a * c - b * s;
+        y = b * c + a * s;
+    }
+}
+
+template <int LPH>
+__device__ __forceinline__ float sum_of_head(float v) {
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace
+
+// A block takes tokens of q or of k (the first `q_blocks` along x those of q),
+// a warp one at a time; along y the heads are shared out where there are few
+// tokens. U: heads of a lane in flight.
+template <int HD, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __grid_constant__ RopeParams p, int q_blocks) {
+    constexpr int LPH = HD / 16, HPW = 32 / LPH, U = BWD ? 1 : 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int l = lane % LPH, sub = lane / LPH;
+    const bool is_k = int(blockIdx.x) >= q_blocks;
+    const RopeSide& d = p.side[is_k];
+    const int block = is_k ? blockIdx.x - q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - q_blocks : q_blocks;
+    // this lane's pieces: as halves of the rotated width lie apart, what does not turn behind them
+    const int P = p.PT + p.PH + p.PW;
+    const bool apart = INTER || 8 * l < P;
+    const int ca = apart ? 8 * l : 2 * P + 16 * (l - P / 8), cb = ca + (INTER ? HD / 2 : apart ? P : 8);
+    // the first of the pairs of either piece (the same four and four, INTER; else eight in a row)
+    const int pa = INTER ? ca / 2 : apart ? ca : P, pb = INTER ? cb / 2 : pa + 4;
+
+    float wt[16];
+    {
+        const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        const Piece wp = {d.w ? *reinterpret_cast<const uint4*>(d.w + ca) : one, d.w ? *reinterpret_cast<const uint4*>(d.w + cb) : one};
+        unpack(wp, wt);
+    }
+    float dw[BWD ? 16 : 1] = {};
+
+    for (int64_t token = int64_t(block) * kWarps + warp; token < p.tokens; token += int64_t(blocks) * kWarps) {
+        const uint32_t place = uint32_t(token);   // below 2^31
+        const uint32_t th = place / uint32_t(p.W), w = place - th * p.W, t = th / uint32_t(p.H) % p.T, h = th % uint32_t(p.H);
+        const float2* const of_t = p.table + t * uint32_t(p.PT);
+        const float2* const of_h = p.table + uint32_t(p.T * p.PT) + h * p.PH - p.PT;
+        const float2* const of_w = p.table + uint32_t(p.T * p.PT) + uint32_t(p.H * p.PH) + w * p.PW - p.PT - p.PH;
+        float2 cs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = i < 4 ? pa + i : pb + i - 4;
+            const float2* const of = j < p.PT ? of_t : j < p.PT + p.PH ? of_h : of_w;
+            cs[i] = j < P ? __ldg(of + j) : make_float2(1.f, 0.f);
+        }
+        const uint16_t* const x_row = d.x + token * d.x_ts;
+        const uint16_t* const g_row = BWD ? d.g + token * d.g_ts : nullptr;
+        uint16_t* const y_row = d.y + token * d.y_ts;
+        for (int h0 = int(blockIdx.y) * HPW * U; h0 < d.heads; h0 += int(gridDim.y) * HPW * U) {
+            Piece x[U], g[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int head = h0 + u * HPW + sub;
+                x[u] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                g[u] = x[u];
+                if (head < d.heads) {
+                    x[u] = {load16(x_row + head * HD + ca), load16(x_row + head * HD + cb)};
+                    if (BWD) g[u] = {load16(g_row + head * HD + ca), load16(g_row + head * HD + cb)};
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int head = h0 + u * HPW + sub;
+                float f[16];
+                unpack(x[u], f);
+                float r = 1.f;
+                if (p.norm) {
+                    float sq = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
+                    r = rsqrtf(sum_of_head<LPH>(sq) * (1.f / HD) + d.eps);
+                }
+                if (!BWD) {
+                    const float by = r * d.scale;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = f[i] * by * wt[i];
+                    turn<INTER, 1>(f, cs);
+                } else {
+                    float e[16];
+                    unpack(g[u], e);
+                    turn<INTER, -1>(e, cs);
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        e[i] *= d.scale;
+                        any |= e[i] != 0.f;
+                    }
+                    // a row without a gradient (padding's) adds nothing, whatever x holds there
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, any) >> (sub * LPH);
+                    const bool live = (lanes & (0xffffffffu >> (32 - LPH))) != 0u;
+                    if (p.norm) {
+                        float dot = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            f[i] = live ? f[i] * r : 0.f;
+                            dw[BWD ? i : 0] = fmaf(e[i], f[i], dw[BWD ? i : 0]);
+                            e[i] *= wt[i];
+                            dot = fmaf(e[i], f[i], dot);
+                        }
+                        dot = sum_of_head<LPH>(dot) * (1.f / HD);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = live ? r * fmaf(-f[i], dot, e[i]) : 0.f;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = e[i];
+                    }
+                }
+                if (head < d.heads) {
+                    const Piece o = pack(f);
+                    *reinterpret_cast<uint4*>(y_row + head * HD + ca) = o.a;
+                    *reinterpret_cast<uint4*>(y_row + head * HD + cb) = o.b;
+                }
+            }
+        }
+    }
+    if (BWD && p.work) {
+        // the block's sums: over the heads of a warp, then over the warps
+        __shared__ float sums[kWarps][HD];
+#pragma unroll
+        for (int i = 0; i < (BWD ? 16 : 1); ++i) {
+            float v = dw[i];
+#pragma unroll
+            for (int o = LPH; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (sub == 0) sums[warp][i < 8 ? ca + i : cb + i - 8] = v;
+        }
+        __syncthreads();
+        float* const out = p.work + (int64_t(blockIdx.x) * gridDim.y + blockIdx.y) * HD;
+        for (int i = threadIdx.x; i < HD; i += kWarps * 32) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) v += sums[k][i];
+            out[i] = v;
+        }
+    }
+}
+
+// The sums of the blocks of q (the first q_blocks) and of k, 32 columns to a
+// block, 32 threads to a column.
+__global__ void __launch_bounds__(1024) norm_rope_sum(const float* work, int q_blocks, int blocks, int HD, float* dq, float* dk) {
+    __shared__ float part[32][33];
+    const int x = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int per = gridDim.x / 2;   // blocks of each
+    const bool is_k = int(blockIdx.x) >= per;
+    const int c = (int(blockIdx.x) - (is_k ? per : 0)) * 32 + x, end = is_k ? blocks : q_blocks;
+    float v = 0.f;
+    if (c < HD)
+        for (int b = (is_k ? q_blocks : 0) + r; b < end; b += 32) v += work[int64_t(b) * HD + c];
+    part[r][x] = v;
+    __syncthreads();
+    if (r == 0 && c < HD) {
+        v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v += part[k][x];
+        float* const to = is_k ? dk : dq;
+        if (to) to[c] = v;
+    }
+}
+
+// cos and sin of (offset + scale position) theta^(-i / pairs), angles in 64
+// bits: in 32 a far position's angle would be off by more than its table's step.
+__global__ void __launch_bounds__(256) rope_table(const RopeTable p) {
+    int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    float2* to = p.table + i;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        const int64_t n = int64_t(p.n[a]) * p.pairs[a];
+        if (i < n) {
+            const double at = p.offset[a] + p.scale[a] * double(i / p.pairs[a]);
+            double s, c;
+            sincos(at * pow(p.theta, -double(i % p.pairs[a]) / double(p.pairs[a])), &s, &c);
+            *to = make_float2(float(c), float(s));
+            return;
+        }
+        i -= n;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+cudaError_t launch_rope_table(const RopeTable& p, cudaStream_t stream) {
+    int64_t n = 0;
+    for (int a = 0; a < 3; ++a) n += int64_t(p.n[a]) * p.pairs[a];
+    rope_table<<<unsigned((n + 255) / 256), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+int64_t rope_workspace(int64_t HD) { return int64_t(kGradBlocks) * HD * 4; }
+
+namespace {
+
+template <int HD, bool INTER, bool BWD>
+cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
+    constexpr int batch = 32 / (HD / 16) * (BWD ? 1 : 2);
+    const int NQ = p.side[0].heads, NK = p.side[1].heads;
+    const int most = BWD ? kGradBlocks : sms * 3;
+    const int64_t want = (p.tokens + kWarps - 1) / kWarps;   // blocks for each of q and k
+    // the blocks shared out by the heads of q and k
+    const int64_t most_q = NK ? min(max(int64_t(most) * NQ / (NQ + NK), int64_t(1)), int64_t(most - 1)) : most;
+    const int q_blocks = int(min(want, most_q)), k_blocks = NK ? int(min(want, most - most_q)) : 0;
+    dim3 grid(unsigned(q_blocks + k_blocks));
+    // few tokens: a token's heads over several blocks
+    grid.y = unsigned(max(1, min((max(NQ, NK) + batch - 1) / batch, most / int(grid.x))));
+    norm_rope<HD, INTER, BWD><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !BWD || !p.work) return e;
+    norm_rope_sum<<<(HD + 31) / 32 * 2, 1024, 0, stream>>>(p.work, int(q_blocks * grid.y), int(grid.x * grid.y), HD,
+                                                           p.side[0].dw, p.side[1].dw);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int hd, const RopeParams& p, bool backward, int sms, cudaStream_t stream) {
+#define X(n) \
+    if (hd == n) {                                                                                        \
+        if (p.interleaved) return backward ? launch<n, true, true>(p, sms, stream) : launch<n, true, false>(p, sms, stream); \
+        return backward ? launch<n, false, true>(p, sms, stream) : launch<n, false, false>(p, sms, stream); \
+    }
+    X(16) X(32) X(64) X(128) X(256) X(512)
+#undef X
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace na3d
