@@ -1,20 +1,728 @@
 // Attention of a grid's tokens to states of another length, and its backward
-// pass. Token i and state j of an entry, head h of q and h / (NH / NKV) of k, v:
+// pass. Token i and state j of an entry, head h of q and h / G of k and v
+// (G = NH / NKV):
 //   s_ij = q_i . k_j where doc_i = kv_doc_j >= 0, else masked,
 //   out_i = sum_j p_ij v_j, p the softmax, lse_i = log sum_j e^s_ij;
 // backward, dp = dout_i . v_j, delta_i = sum_j p dp, ds = p (dp - delta_i):
 //   dq_i = sum_j ds k_j, dk_j = sum_i ds q_i, dv_j = sum_i p dout_i.
 //
-// A warp takes a row (of q, or of k and v) and walks the others 32 at a time,
-// one to a lane.
+// All kernels work on tiles of 128 rows (tokens with the G heads that share a
+// head of k, or states) against a stream of column tiles. Documents are taken
+// one at a time: a pass over a row tile streams the column tiles that hold
+// document d, masks whole columns of other documents and is written to the
+// rows of d alone. So a mask is one bit a column, the same for every row, and
+// what other documents' rows and columns hold stays out of it: their columns are
+// zeroed in shared memory where they would meet a product as 0 times a value.
+#include <atomic>
 #include <cuda_bf16.h>
+#include <climits>
 
 #include "na3d_cross.cuh"
+#include "na3d_host.cuh"
 #include "sm103_ptx.cuh"
 
 namespace na3d {
 
+__device__ unsigned int g_cross_timeout_flag = 0;
+
 namespace {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 500000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct Sync {
+    uint32_t bar0;
+    volatile uint32_t* abort_flag;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
+    // Wait for a barrier phase; false once this block has given up.
+    __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
+        if (mbar_try_wait(b, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(b, parity)) return true;
+            if ((it & 1023u) == 0u) {
+                if (*abort_flag) return false;
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    *abort_flag = 1u;
+                    atomicOr(&g_cross_timeout_flag, 1u);
+                    return false;
+                }
+            }
+        }
+    }
+    // The same with an outcome that the whole warp shares.
+    __device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity) const { return __all_sync(kAll, wait(b, parity)); }
+};
+
+__device__ __forceinline__ void drained(uint32_t bar, uint32_t parity) {
+    if (!mbar_wait_bounded(bar, parity, kDrainLimitNs)) atomicOr(&g_cross_timeout_flag, 1u);
+}
+
+// The values of a tensor-memory load stay behind the wait for it.
+__device__ __forceinline__ void behind_wait(float* v) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                     "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// A kernel lets the next one of its stream start, and waits for the one before
+// it to be through (nothing to wait for where it was launched plainly).
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// head * HD + column, heads, tokens, entries: a box of tokens with `heads` heads.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int head, int token, int entry) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(token),
+        "r"(entry), "r"(bar)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ steps
+
+// What the producer tells the other roles of a step: a column tile of one pass.
+struct Step {
+    uint32_t flags;
+    int32_t doc;
+    uint32_t mask[4];   // columns of the document
+    uint32_t pad[2];
+};
+enum : uint32_t {
+    kFirst = 1,       // of its pass
+    kLast = 2,
+    kUnitFirst = 4,   // of its row tiles
+    kUnitLast = 8,
+    kTwo = 16,        // both row tiles are in the grid
+    kMasked = 32,     // some columns are masked ...
+    kForeign = 64,    // ... for their document
+    kNone = 128,      // the rows see no column at all
+    kEnd = 256        // no more rows
+};
+constexpr int kSteps = 8;   // steps that the producer may be ahead in telling
+
+// The documents of one side: of token or state i of entry b, 0 for all where
+// there are none.
+struct Docs {
+    const int32_t* at;
+    int n;
+    __device__ __forceinline__ int of(int64_t b, int i) const { return at ? __ldg(at + b * n + i) : 0; }
+};
+
+// A warp's view of the column tiles of an entry, 32 at a time, one to a lane:
+// the smallest document >= 0 and the largest, and whether there is but one.
+struct Tiles {
+    Docs docs;
+    int per;             // tokens to a tile
+    int64_t b = -1;
+    int first = -1;
+    int lo, hi;
+    bool pure;
+    __device__ __forceinline__ void look(int64_t entry, int tile) {
+        if (entry == b && (tile & ~31) == first) return;
+        b = entry;
+        first = tile & ~31;
+        const int i0 = (first + int(threadIdx.x & 31)) * per, end = min(i0 + per, docs.n);
+        lo = INT_MAX;
+        hi = INT_MIN;
+        int least = INT_MAX;
+        if (docs.at) {
+#pragma unroll 16
+            for (int i = i0; i < end; ++i) {
+                const int d = docs.of(b, i);
+                least = min(least, d);
+                lo = d >= 0 ? min(lo, d) : lo;
+                hi = max(hi, d);
+            }
+        } else if (i0 < end) {
+            lo = hi = least = 0;
+        }
+        pure = least == hi;
+    }
+    // The first tile from `tile` on, before `end`, that may hold document d; `end` where none does.
+    __device__ __forceinline__ int find(int64_t entry, int tile, int end, int d, bool* whole) {
+        while (tile < end) {
+            look(entry, tile);
+            const uint32_t can = __ballot_sync(kAll, lo <= d && d <= hi) & (kAll << (tile & 31));
+            if (can) {
+                const int at = __ffs(can) - 1;
+                *whole = __shfl_sync(kAll, int(pure), at) != 0;
+                return min(first + at, end);
+            }
+            tile = first + 32;
+        }
+        return end;
+    }
+};
+
+// The smallest document > d of this warp's lanes' values (v[i] < 0: none); INT_MAX where there is none.
+template <int N>
+__device__ __forceinline__ int next_doc(const int (&v)[N], int d) {
+    int least = INT_MAX;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (v[i] > d) {
+            least = min(least, v[i]);
+            any = true;
+        }
+    if (!__any_sync(kAll, any)) return -1;
+    return __reduce_min_sync(kAll, least);
+}
+
+// Geometry that the roles share, for head size HD.
+template <int HD>
+struct Geom {
+    static constexpr int HDB = HD < 64 ? HD : 64;      // columns of a shared-memory row
+    static constexpr int NREG = HD / HDB;
+    static constexpr int ROWB = HDB * 2;
+    static constexpr uint32_t SWZ = HDB == 64 ? kSwizzle128B : HDB == 32 ? kSwizzle64B : kSwizzle32B;
+    static constexpr int SBO = 8 * ROWB;
+    static constexpr int kPer = HDB / 16;              // 16-column steps of a row
+};
+
+// D (+)= A B^T over HD columns, both operands row by row in shared memory.
+template <int HD, int REG_A, int REG_B>
+__device__ __forceinline__ void scores(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+    using G = Geom<HD>;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint32_t ao = ((kk / G::kPer) * REG_A + (kk % G::kPer) * 32) >> 4;
+        const uint32_t bo = ((kk / G::kPer) * REG_B + (kk % G::kPer) * 32) >> 4;
+        if (kk == 0) umma_ss_halves<0>(d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
+        else umma_ss_halves<1>(d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
+    }
+}
+
+// D (+)= P Y: P (bf16, 128 x N) in tensor memory, Y's N rows in shared memory, its columns outermost.
+template <int HD, int N>
+__device__ __forceinline__ void product(uint32_t d, uint32_t p, uint32_t y_lo, uint32_t y_hi, uint32_t idesc, bool fresh) {
+    if (fresh) umma_ts_halves<0>(d, p, y_lo, y_hi, idesc);
+    else umma_ts_halves<1>(d, p, y_lo, y_hi, idesc);
+#pragma unroll
+    for (int kk = 1; kk < N / 16; ++kk) umma_ts_halves<1>(d, p + kk * 8, y_lo + ((kk * 16 * Geom<HD>::ROWB) >> 4), y_hi, idesc);
+}
+
+// Zeros over row r of a tile of rows of HD values (regions of REG bytes).
+template <int HD, int REG>
+__device__ __forceinline__ void zero_row(uint32_t tile, int r) {
+    using G = Geom<HD>;
+#pragma unroll
+    for (int c = 0; c < HD / 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (c / (G::HDB / 8)) * REG + r * G::ROWB + (c % (G::HDB / 8)) * 16),
+                     "r"(0) : "memory");
+}
+
+// ------------------------------------------------------------------ forward
+
+struct FwdParams {
+    int32_t L, S, NH, NKV, G, rpt;        // rpt: tokens of a row tile
+    int32_t pairs, units, tiles, splits, per_split;   // pairs of row tiles of an entry; column tiles
+    int32_t out_v8;
+    const int32_t *doc, *kv_doc;
+    uint16_t* out;
+    float* lse;
+    float* part;       // splits > 1: fp32 out of each split, (split, row, HD)
+    float* part_lse;   // ... and its log2-sum-exp2 (split, row)
+    int64_t rows;      // B * L * NH
+    int32_t B;
+};
+
+struct Unit {
+    int pair, kh, split;
+    int64_t b;
+    __device__ __forceinline__ Unit(const FwdParams& p, int u) {
+        pair = u % p.pairs;
+        u /= p.pairs;
+        kh = u % p.NKV;
+        u /= p.NKV;
+        b = u % p.B;
+        split = u / p.B;
+    }
+};
+
+template <int HD>
+struct FwdShape : Geom<HD> {
+    using G = Geom<HD>;
+    static constexpr int REG = 128 * G::ROWB, TILE = G::NREG * REG;
+    static constexpr int SLOTS = HD == 128 ? 5 : 8;    // of k and v in turn
+    static constexpr int OFF_KV = 2 * TILE, OFF_STEP = OFF_KV + SLOTS * TILE, OFF_BAR = OFF_STEP + kSteps * 32;
+    static constexpr int B_FULL = 0, B_EMPTY = SLOTS, B_QFULL = 2 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
+                         B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 2, B_TOLD = B_OFULL + 2, B_HEARD = B_TOLD + kSteps,
+                         B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    // one block on an SM, which tensor memory is shared out for
+    static constexpr int NEED = OFF_MISC + 16 + 1024, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+    static constexpr uint32_t TM_S = 0, TM_O = 256, OW = HD < 32 ? 32 : HD;   // scores of either row tile; their sums
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+constexpr int kFwdThreads = 384;
+// registers: the softmax takes what the third warpgroup leaves of 384 x 168
+constexpr uint32_t kRegsHigh = 216, kRegsLow = 72;
+static_assert(2 * kRegsHigh + kRegsLow <= 3 * 168, "register split");
+
+template <int HD>
+__device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, const CUtensorMap* tq,
+                                             const CUtensorMap* tk, const CUtensorMap* tv) {
+    using F = FwdShape<HD>;
+    const int lane = threadIdx.x & 31;
+    Tiles tiles{{p.kv_doc, p.S}, 128};
+    const Docs rows{p.doc, p.L};
+    uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
+
+    // One operand tile into the next slot.
+    auto load = [&](const CUtensorMap* map, const Unit& U, int tile) -> bool {
+        const uint32_t st = slot_n % F::SLOTS;
+        if (!sy.wait_warp(sy.bar(F::B_EMPTY + st), ((slot_n / F::SLOTS) & 1u) ^ 1u)) return false;
+        ++slot_n;
+        if (lane == 0) {
+            const uint32_t full = sy.bar(F::B_FULL + st);
+            mbar_arrive_expect_tx(full, F::TILE);
+            for (int r = 0; r < F::NREG; ++r)
+                load_box(base + F::OFF_KV + st * F::TILE + r * F::REG, map, full, r * F::HDB, U.kh, tile * 128, int(U.b));
+        }
+        return true;
+    };
+    auto tell = [&](const Step& s) -> bool {
+        const uint32_t e = told % kSteps;
+        if (!sy.wait_warp(sy.bar(F::B_HEARD + e), ((told / kSteps) & 1u) ^ 1u)) return false;
+        ++told;
+        if (lane == 0) {
+            steps[e] = s;
+            mbar_arrive(sy.bar(F::B_TOLD + e));
+        }
+        return true;
+    };
+    // A step is told once the one behind it is known, which says where passes and units end.
+    struct Found { int tile, doc; bool whole; };
+    auto run = [&]() {
+        for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+            const Unit U(p, u);
+            const int t0 = U.pair * 2 * p.rpt, n_tok = min(2 * p.rpt, p.L - t0);
+            const bool two = n_tok > p.rpt;
+            int doc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(U.b, t0 + lane + 32 * i) : -1;
+            const int k0 = U.split * p.per_split, k1 = min(k0 + p.per_split, p.tiles);
+            int d = next_doc(doc, -1);
+            auto next = [&](Found* f) {   // from f->tile on, of document d or those behind it
+                for (; d >= 0; d = next_doc(doc, d), f->tile = k0) {
+                    f->tile = tiles.find(U.b, f->tile, k1, d, &f->whole);
+                    while (f->tile < k1) {
+                        f->doc = d;
+                        if (f->whole) return true;
+                        // in range is not in it: look whether any of its columns is of the document
+                        bool any = false;
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = f->tile * 128 + 32 * i + lane;
+                            any |= j < p.S && tiles.docs.of(U.b, j) == d;
+                        }
+                        if (__any_sync(kAll, any)) return true;
+                        f->tile = tiles.find(U.b, f->tile + 1, k1, d, &f->whole);
+                    }
+                }
+                return false;
+            };
+            const uint32_t base_flags = two ? uint32_t(kTwo) : 0u;
+            Found f{k0, -1, false};
+            bool have = next(&f);
+            if (!have) {
+                if (!tell({base_flags | kNone | kUnitLast, -1})) return false;
+                continue;
+            }
+            int was = -1;
+            for (bool first = true; have; first = false) {
+                Found g = f;
+                ++g.tile;
+                const bool more = next(&g);
+                Step s{base_flags, f.doc};
+                if (f.doc != was) s.flags |= kFirst;
+                if (!more || g.doc != f.doc) s.flags |= kLast;
+                if (first) s.flags |= kUnitFirst;
+                if (!more) s.flags |= kUnitLast;
+                was = f.doc;
+                bool gaps = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = f.tile * 128 + 32 * i + lane;
+                    const bool in = j < p.S, mine = in && (f.whole || tiles.docs.of(U.b, j) == f.doc);
+                    s.mask[i] = __ballot_sync(kAll, mine);
+                    if (s.mask[i] != kAll) s.flags |= kMasked;
+                    gaps |= in && !mine;
+                }
+                if (__any_sync(kAll, gaps)) s.flags |= kForeign;
+                if (!tell(s) || !load(tk, U, f.tile)) return false;
+                if (first) {
+                    for (int a = 0; a < (two ? 2 : 1); ++a) {
+                        if (!sy.wait_warp(sy.bar(F::B_QEMPTY + a), (q_n[a] & 1u) ^ 1u)) return false;
+                        ++q_n[a];
+                        if (lane == 0) {
+                            const uint32_t full = sy.bar(F::B_QFULL + a);
+                            mbar_arrive_expect_tx(full, p.rpt * p.G * HD * 2);
+                            for (int r = 0; r < F::NREG; ++r)
+                                load_box(base + a * F::TILE + r * F::REG, tq, full, r * F::HDB, U.kh * p.G, t0 + a * p.rpt, int(U.b));
+                        }
+                    }
+                }
+                if (!load(tv, U, f.tile)) return false;
+                have = more;
+                f = g;
+            }
+        }
+        return tell({kEnd, -1});
+    };
+    run();
+    // every issued load lands before the block may exit
+    if (lane == 0) {
+        for (uint32_t s = 0; s < F::SLOTS; ++s) {
+            const uint32_t n = slot_n / F::SLOTS + (s < slot_n % F::SLOTS ? 1u : 0u);
+            if (n) drained(sy.bar(F::B_FULL + s), (n - 1u) & 1u);
+        }
+        for (int a = 0; a < 2; ++a)
+            if (q_n[a]) drained(sy.bar(F::B_QFULL + a), (q_n[a] - 1u) & 1u);
+    }
+}
+
+// Tensor-core work in the order of its operands: the product of a step and row
+// tile is followed at once by the scores of the next step, which take the place
+// of its probabilities, so while one row tile is in its softmax the other's
+// products run.
+template <int HD>
+__device__ __forceinline__ void fwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const volatile Step* steps) {
+    using F = FwdShape<HD>;
+    constexpr uint32_t id_s = make_idesc_bf16(128, 128, 0, 0), id_o = make_idesc_bf16(128, HD, 0, 1);
+    const uint64_t qd = make_smem_desc(base, 16, F::SBO, F::SWZ), kd = make_smem_desc(base + F::OFF_KV, 16, F::SBO, F::SWZ);
+    const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
+    const uint32_t q_lo = uint32_t(qd), q_hi = uint32_t(qd >> 32), k_lo = uint32_t(kd), k_hi = uint32_t(kd >> 32);
+    const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
+    uint32_t heard = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0}, slot_n = 0;   // slot_n: k's of the step to come
+
+    auto hear = [&](uint32_t* flags) -> bool {   // of the next step that has columns, or the end
+        do {
+            const uint32_t e = heard % kSteps;
+            if (!sy.wait(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return false;
+            ++heard;
+            *flags = steps[e].flags;
+            mbar_arrive(sy.bar(F::B_HEARD + e));
+        } while (*flags & kNone);
+        return true;
+    };
+    auto issue_scores = [&](uint32_t flags, int a) -> bool {
+        if (flags & kUnitFirst) {
+            if (!sy.wait(sy.bar(F::B_QFULL + a), q_n[a] & 1u)) return false;
+            ++q_n[a];
+        }
+        const uint32_t st = slot_n % F::SLOTS;
+        if (!sy.wait(sy.bar(F::B_FULL + st), (slot_n / F::SLOTS) & 1u)) return false;
+        tc_fence_after();
+        scores<HD, F::REG, F::REG>(tmem + F::TM_S + 128 * a, q_lo + ((a * F::TILE) >> 4), q_hi, k_lo + ((st * F::TILE) >> 4), k_hi, id_s);
+        umma_commit(sy.bar(F::B_SFULL + a));
+        if (flags & kUnitLast) umma_commit(sy.bar(F::B_QEMPTY + a));
+        if (a == 1 || !(flags & kTwo)) umma_commit(sy.bar(F::B_EMPTY + st));
+        return true;
+    };
+    auto run = [&]() {
+        uint32_t now;
+        if (!hear(&now) || (now & kEnd)) return;
+        for (int a = 0; a < ((now & kTwo) ? 2 : 1); ++a)
+            if (!issue_scores(now, a)) return;
+        for (;;) {
+            const uint32_t v_slot = (slot_n + 1) % F::SLOTS, v_par = ((slot_n + 1) / F::SLOTS) & 1u;
+            slot_n += 2;
+            uint32_t then = kEnd;
+            bool asked = false;
+            for (int a = 0; a < 2; ++a) {
+                if (a == 0 || (now & kTwo)) {
+                    if (!sy.wait(sy.bar(F::B_PFULL + a), p_n[a] & 1u)) return;
+                    ++p_n[a];
+                    if (!sy.wait(sy.bar(F::B_FULL + v_slot), v_par)) return;
+                    tc_fence_after();
+                    product<HD, 128>(tmem + F::TM_O + F::OW * a, tmem + F::TM_S + 128 * a, v_lo + ((v_slot * F::TILE) >> 4), v_hi, id_o,
+                                     (now & kFirst) != 0);
+                    if (now & kLast) umma_commit(sy.bar(F::B_OFULL + a));
+                    if (a == 1 || !(now & kTwo)) umma_commit(sy.bar(F::B_EMPTY + v_slot));
+                }
+                if (!asked && !hear(&then)) return;
+                asked = true;
+                if (!(then & kEnd) && (a == 0 || (then & kTwo)) && !issue_scores(then, a)) return;
+            }
+            if (then & kEnd) return;
+            now = then;
+        }
+    };
+    run();
+    umma_commit(sy.bar(F::B_DRAIN));
+    drained(sy.bar(F::B_DRAIN), 0);
+}
+
+// One row of scores to a thread, which keeps the reference maximum and the sum.
+template <int HD>
+__device__ __forceinline__ void fwd_softmax(const FwdParams& p, const Sync& sy, uint32_t base, uint32_t tmem, const volatile Step* steps) {
+    using F = FwdShape<HD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t t_s = t_lane + F::TM_S + 128 * a, t_o = t_lane + F::TM_O + F::OW * a;
+    uint32_t heard = 0, s_n = 0, o_n = 0, slot_n = 0;
+    const int tok = r / p.G, g = r - tok * p.G;
+
+    int u = blockIdx.x, doc = -1;
+    int64_t row = -1;           // of out; < 0: none
+    bool written = false;
+    auto enter = [&]() {
+        row = -1;
+        written = false;
+        if (u >= p.units) return;
+        const Unit U(p, u);
+        const int t = (U.pair * 2 + a) * p.rpt + tok;
+        if (tok < p.rpt && t < p.L) {
+            row = (U.b * p.L + t) * p.NH + U.kh * p.G + g + (p.splits > 1 ? U.split * p.rows : 0);
+            doc = p.doc ? __ldg(p.doc + U.b * p.L + t) : 0;
+        }
+    };
+    enter();
+    float ref = 0.f, l = 0.f;
+    for (;;) {
+        const uint32_t e = heard % kSteps;
+        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return;
+        ++heard;
+        const uint32_t flags = steps[e].flags;
+        const int d = steps[e].doc;
+        uint32_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = steps[e].mask[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
+        if (flags & kEnd) return;
+        if (!(flags & kNone)) slot_n += 2;
+        if (!(flags & kNone) && (a == 0 || (flags & kTwo))) {
+            if (!sy.wait_warp(sy.bar(F::B_SFULL + a), s_n & 1u)) return;
+            ++s_n;
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) behind_wait(s + 32 * q);
+            if (flags & kMasked) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j) s[j] = (m[j >> 5] >> (j & 31)) & 1u ? s[j] : -INFINITY;
+            }
+            float t0 = s[0], t1 = s[1];
+#pragma unroll
+            for (int j = 2; j < 126; j += 4) {
+                t0 = max3f(t0, s[j], s[j + 1]);
+                t1 = max3f(t1, s[j + 2], s[j + 3]);
+            }
+            const float top = max3f(t0, t1, fmaxf(s[126], s[127])) * kLog2e;
+            // the reference is exact at first and rises only by leaps of 2^8: O is seldom scaled
+            if (flags & kFirst) {
+                ref = top == -INFINITY ? 0.f : top;
+                l = 0.f;
+            } else {
+                const bool leap = top > ref + 8.f;
+                if (__any_sync(kAll, leap)) {
+                    const float by = leap ? ex2_approx(ref - top) : 1.f;
+                    ref = leap ? top : ref;
+                    l *= by;
+#pragma unroll 1
+                    for (int q = 0; q < (HD + 31) / 32; ++q) {
+                        float o[32];
+                        tmem_ld32(t_o + 32 * q, o);
+                        tmem_wait_ld();
+                        behind_wait(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] *= by;
+                        tmem_st32(t_o + 32 * q, o);
+                    }
+                }
+            }
+            const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), neg2 = f2_pack(-ref, -ref);
+            uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float e0, e1;
+                    f2_unpack(f2_fma(f2_pack(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]), l2e2, neg2), e0, e1);
+                    e0 = ex2_approx(e0);
+                    e1 = ex2_approx(e1);
+                    pk[j] = pack_bf16x2(e0, e1);
+                    if (j & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
+                    else acc0 = f2_add(acc0, f2_pack(e0, e1));
+                }
+                tmem_st16(t_s + 16 * q, pk);
+            }
+            float x0, x1;
+            f2_unpack(f2_add(acc0, acc1), x0, x1);
+            l += x0 + x1;
+            if (a == 0 && (flags & kForeign)) {
+                // this thread's column, where it is of another document: 0 times its value must be 0
+                const uint32_t vs = slot_n - 1;
+                if (!sy.wait_warp(sy.bar(F::B_FULL + vs % F::SLOTS), (vs / F::SLOTS) & 1u)) {
+                    tmem_wait_st();
+                    return;
+                }
+                if (!((warp & 2 ? (warp & 1 ? m[3] : m[2]) : (warp & 1 ? m[1] : m[0])) >> lane & 1u))
+                    zero_row<HD, F::REG>(base + F::OFF_KV + (vs % F::SLOTS) * F::TILE, r);
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(sy.bar(F::B_PFULL + a));
+            if (flags & kLast) {
+                if (!sy.wait_warp(sy.bar(F::B_OFULL + a), o_n & 1u)) return;
+                ++o_n;
+                tc_fence_after();
+                const bool mine = row >= 0 && doc == d;
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll 1
+                for (int q = 0; q < (HD + 31) / 32; ++q) {
+                    float o[32];
+                    tmem_ld32(t_o + 32 * q, o);
+                    tmem_wait_ld();
+                    behind_wait(o);
+                    if (!mine) continue;
+                    constexpr int W = HD < 32 ? HD : 32;
+                    if (p.splits > 1) {
+                        float4* const to = reinterpret_cast<float4*>(p.part + row * HD + 32 * q);
+#pragma unroll
+                        for (int j = 0; j < W / 4; ++j)
+                            to[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+                    } else {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) pk[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        uint16_t* const to = p.out + row * HD + 32 * q;
+                        if (p.out_v8) {
+#pragma unroll
+                            for (int j = 0; j < W / 16; ++j) st_global_v8(to + 16 * j, pk + 8 * j);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < W / 8; ++j)
+                                reinterpret_cast<uint4*>(to)[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                if (mine) {
+                    const float lse2 = l > 0.f || l != l ? ref + log2f(l) : -INFINITY;
+                    if (p.splits > 1) p.part_lse[row] = lse2;
+                    else if (p.lse) p.lse[row] = lse2 * kLn2;
+                    written = true;
+                }
+            }
+        }
+        if (flags & kUnitLast) {
+            if (row >= 0 && !written) {   // a row that sees nothing
+                if (p.splits > 1) {
+                    p.part_lse[row] = -INFINITY;
+                } else {
+                    uint4* const to = reinterpret_cast<uint4*>(p.out + row * HD);
+#pragma unroll
+                    for (int j = 0; j < HD / 8; ++j) to[j] = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[row] = -INFINITY;
+                }
+            }
+            u += gridDim.x;
+            enter();
+        }
+    }
+}
+
+// Two row tiles to a block, one block to an SM, persistent:
+//   warps 0..3, 4..7  the softmax of either row tile;
+//   warp 8            finds the column tiles that the rows see, TMA;
+//   warp 9            issues the products, owns the tensor memory.
+template <int HD>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                const __grid_constant__ FwdParams p) {
+    using F = FwdShape<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* const base_ptr = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* const misc = reinterpret_cast<volatile uint32_t*>(base_ptr + F::OFF_MISC);
+    Step* const steps = reinterpret_cast<Step*>(base_ptr + F::OFF_STEP);
+    const Sync sy{base + F::OFF_BAR, misc + 1};
+    // rows of q's tiles that no load writes (G does not divide 128) hold zeros
+    if (p.rpt * p.G != 128)
+        for (int i = threadIdx.x; i < 2 * F::TILE / 16; i += kFwdThreads) reinterpret_cast<uint4*>(base_ptr)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::NBAR; ++i)
+            mbar_init(sy.bar(i), i >= F::B_PFULL && i < F::B_PFULL + 2 ? 128u : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 9u : 1u);
+        misc[1] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
+    if (warp == 9) {
+        tmem_alloc(base + F::OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    dependents_may_start();
+    if (warp < 8) {
+        regs_increase<kRegsHigh>();
+        fwd_softmax<HD>(p, sy, base, tmem, steps);
+    } else {
+        regs_decrease<kRegsLow>();
+        if (warp == 8) fwd_producer<HD>(p, sy, base, steps, &tq, &tk, &tv);
+        if (warp == 9 && lane == 0) fwd_issuer<HD>(sy, base, tmem, steps);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The splits of a row joined: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).
+template <int HD>
+__global__ void __launch_bounds__(256) cross_join(const FwdParams p) {
+    constexpr int PER = HD / 4;   // threads of a row
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / PER;
+    const int c = int(i % PER) * 4;
+    wait_for_primary();
+    if (row >= p.rows) return;
+    float top = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * p.rows + row]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, o[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float x = p.part_lse[s * p.rows + row];
+        if (x == -INFINITY) continue;   // nothing written
+        const float w = exp2f(x - ref);
+        const float4 v = *reinterpret_cast<const float4*>(p.part + (s * p.rows + row) * HD + c);
+        sum += w;
+        o[0] = fmaf(w, v.x, o[0]);
+        o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]);
+        o[3] = fmaf(w, v.w, o[3]);
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint2*>(p.out + row * HD + c) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// ------------------------------------------------------------------ backward, simple
 
 constexpr int kWarps = 4;
 
@@ -145,37 +853,149 @@ __global__ void __launch_bounds__(kWarps * 32) cross_states(const CrossParams p)
 }
 
 template <int HD>
-cudaError_t launch(const CrossParams& p, bool backward, cudaStream_t stream) {
+cudaError_t simple_bwd(const CrossParams& p, cudaStream_t stream) {
     const int64_t rows = int64_t(p.B) * p.L * p.NH, states = int64_t(p.B) * p.S * p.NKV;
     const unsigned grid = unsigned((rows + kWarps - 1) / kWarps);
-    if (!backward) {
-        cross_rows<HD, false><<<grid, kWarps * 32, 0, stream>>>(p);
-    } else {
-        cross_rows<HD, true><<<grid, kWarps * 32, 0, stream>>>(p);
-        cross_states<HD><<<unsigned((states + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
-    }
+    cross_rows<HD, true><<<grid, kWarps * 32, 0, stream>>>(p);
+    cross_states<HD><<<unsigned((states + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ host side
+
+// A tensor of heads (B, n, heads, HD), ts elements from token to token: boxes of
+// `tokens` tokens with `box_heads` heads, HDB columns.
+bool encode_heads(CUtensorMap* m, const void* ptr, int HD, int64_t B, int64_t n, int64_t heads, int64_t ts, int box_heads, int tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int hdb = HD < 64 ? HD : 64;
+    const cuuint64_t dims[4] = {cuuint64_t(HD), cuuint64_t(heads), cuuint64_t(n), cuuint64_t(B)};
+    const cuuint64_t strides[3] = {cuuint64_t(HD) * 2, cuuint64_t(ts) * 2, cuuint64_t(ts) * 2 * n};
+    const cuuint32_t box[4] = {cuuint32_t(hdb), cuuint32_t(box_heads), cuuint32_t(tokens), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle swz = hdb == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                   : hdb == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                               : CU_TENSOR_MAP_SWIZZLE_32B;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSms = 152;   // what the work is shared out for: equal on every device
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct FwdPlan {
+    int64_t rpt, pairs, tiles, splits, per_split;
+    FwdPlan(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV) {
+        rpt = 128 / (NH / NKV);
+        pairs = ceil_div(L, 2 * rpt);
+        tiles = ceil_div(S, 128);
+        // few rows: the states shared out too, four column tiles to a split at least
+        const int64_t units = B * NKV * pairs;
+        splits = units * 2 > kSms ? 1 : kSms / units;
+        if (splits > tiles / 4) splits = tiles / 4;
+        if (splits < 1) splits = 1;
+        per_split = ceil_div(tiles, splits);
+        splits = ceil_div(tiles, per_split);
+    }
+};
+
+template <typename... Args>
+cudaError_t launch_after(void (*kernel)(Args...), int64_t grid, int threads, int smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(unsigned(grid));
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+template <int HD>
+cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
+    const FwdPlan pl(c.B, c.L, c.S, c.NH, c.NKV);
+    const int64_t units = int64_t(c.B) * c.NKV * pl.pairs * pl.splits;
+    if (units >= (int64_t(1) << 31) - sms) return cudaErrorInvalidValue;
+    FwdParams p{};
+    p.B = c.B; p.L = c.L; p.S = c.S; p.NH = c.NH; p.NKV = c.NKV;
+    p.G = c.NH / c.NKV;
+    p.rpt = int(pl.rpt);
+    p.pairs = int(pl.pairs);
+    p.units = int(units);
+    p.tiles = int(pl.tiles);
+    p.splits = int(pl.splits);
+    p.per_split = int(pl.per_split);
+    p.rows = int64_t(c.B) * c.L * c.NH;
+    p.out_v8 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
+    p.doc = c.doc;
+    p.kv_doc = c.kv_doc;
+    p.out = c.out;
+    p.lse = c.lse;
+    p.part = static_cast<float*>(c.work);
+    p.part_lse = p.part + pl.splits * p.rows * HD;
+    CUtensorMap tq, tk, tv;
+    if (!encode_heads(&tq, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, p.rpt) || !encode_heads(&tk, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, 128) ||
+        !encode_heads(&tv, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, 128))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(cross_fwd_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<HD>::SMEM);
+    if (e != cudaSuccess) return e;
+    cross_fwd_tiles<HD><<<unsigned(units < sms ? units : sms), kFwdThreads, FwdShape<HD>::SMEM, stream>>>(tq, tk, tv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_after(cross_join<HD>, ceil_div(p.rows * (HD / 4), 256), 256, 0, stream, p);
 }
 
 }  // namespace
 
-int64_t cross_workspace(int64_t B, int64_t L, int64_t, int64_t NH, int64_t, int64_t, bool backward) {
-    return backward ? B * L * NH * 4 : 0;
+static std::atomic<bool> g_launched{false};
+
+int64_t cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, bool backward) {
+    const int64_t rows = B * L * NH;
+    if (backward) return rows * 4;
+    const FwdPlan pl(B, L, S, NH, NKV);
+    return pl.splits > 1 ? pl.splits * rows * (HD + 1) * 4 : 0;
 }
 
-cudaError_t launch_cross_fwd(int hd, const CrossParams& p, int, cudaStream_t stream) {
-    return hd == 16 ? launch<16>(p, false, stream) : hd == 32 ? launch<32>(p, false, stream)
-         : hd == 64 ? launch<64>(p, false, stream) : launch<128>(p, false, stream);
+cudaError_t launch_cross_fwd(int hd, const CrossParams& p, int sms, cudaStream_t stream) {
+    g_launched = true;
+    switch (hd) {
+        case 16: return fwd<16>(p, sms, stream);
+        case 32: return fwd<32>(p, sms, stream);
+        case 64: return fwd<64>(p, sms, stream);
+        case 128: return fwd<128>(p, sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 cudaError_t launch_cross_bwd(int hd, const CrossParams& p, int, cudaStream_t stream) {
-    return hd == 16 ? launch<16>(p, true, stream) : hd == 32 ? launch<32>(p, true, stream)
-         : hd == 64 ? launch<64>(p, true, stream) : launch<128>(p, true, stream);
+    return hd == 16 ? simple_bwd<16>(p, stream) : hd == 32 ? simple_bwd<32>(p, stream)
+         : hd == 64 ? simple_bwd<64>(p, stream) : simple_bwd<128>(p, stream);
 }
 
-cudaError_t take_cross_error(cudaStream_t, unsigned int* flag) {
+// The flag is taken as for the attention kernel: one atomic exchange per
+// status request, its old value left in a slot of that request's own. A process
+// that has launched none of these kernels has nothing to ask for.
+constexpr unsigned int kStatusSlots = 256;
+__device__ unsigned int g_cross_status_slots[kStatusSlots];
+
+__global__ void take_cross_flag(unsigned int slot) { g_cross_status_slots[slot] = atomicExch(&g_cross_timeout_flag, 0u); }
+
+cudaError_t take_cross_error(cudaStream_t stream, unsigned int* flag) {
     *flag = 0;
-    return cudaSuccess;
+    if (!g_launched) return cudaSuccess;
+    static std::atomic<unsigned int> next{0};
+    const unsigned int slot = next.fetch_add(1u) % kStatusSlots;
+    take_cross_flag<<<1, 1, 0, stream>>>(slot);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyFromSymbolAsync(flag, g_cross_status_slots, sizeof(unsigned int), slot * sizeof(unsigned int),
+                                  cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(stream);
 }
 
 }  // namespace na3d
