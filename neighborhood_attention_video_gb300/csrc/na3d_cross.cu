@@ -31,6 +31,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 500000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kSumLimit = 4294967296.0f;   // 2^32: of a row's probabilities in one tile
 
 struct Sync {
     uint32_t bar0;
@@ -73,6 +74,43 @@ __device__ __forceinline__ void behind_wait(float* v) {
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The products are issued by a warp that walks its loop as one, with the one
+// lane that issues as a predicate of the instruction: so descriptors stay in
+// uniform registers. Issued inside a branch of one lane, a product took 83
+// cycles to issue, more than the 64 that it computes.
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes;
+}
+// D (+)= A B^T, A and B in shared memory (ss) or A in tensor memory (ts).
+template <uint32_t ACC>
+__device__ __forceinline__ void mma_ss(uint32_t yes, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .b64 da, db;\n\t.reg .pred p, q;\n\t"
+        "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi),
+        "r"(idesc), "n"(ACC), "r"(yes)
+        : "memory");
+}
+template <uint32_t ACC>
+__device__ __forceinline__ void mma_ts(uint32_t yes, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .b64 db;\n\t.reg .pred p, q;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc),
+        "n"(ACC), "r"(yes)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t yes, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(yes)
+        : "memory");
+}
+
 // head * HD + column, heads, tokens, entries: a box of tokens with `heads` heads.
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int col, int head, int token, int entry) {
     asm volatile(
@@ -85,11 +123,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, u
 // ------------------------------------------------------------------ steps
 
 // What the producer tells the other roles of a step: a column tile of one pass.
-struct Step {
+struct alignas(16) Step {
     uint32_t flags;
     int32_t doc;
+    int32_t t0;         // the unit's first token ...
+    int32_t pad;
     uint32_t mask[4];   // columns of the document
-    uint32_t pad[2];
+    int64_t row;        // ... its row of out
+    int64_t token;      // ... and of doc
 };
 enum : uint32_t {
     kFirst = 1,       // of its pass
@@ -130,7 +171,7 @@ struct Tiles {
         hi = INT_MIN;
         int least = INT_MAX;
         if (docs.at) {
-#pragma unroll 16
+#pragma unroll 4
             for (int i = i0; i < end; ++i) {
                 const int d = docs.of(b, i);
                 least = min(least, d);
@@ -186,24 +227,24 @@ struct Geom {
 
 // D (+)= A B^T over HD columns, both operands row by row in shared memory.
 template <int HD, int REG_A, int REG_B>
-__device__ __forceinline__ void scores(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
+__device__ __forceinline__ void scores(uint32_t yes, uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
     using G = Geom<HD>;
 #pragma unroll
     for (int kk = 0; kk < HD / 16; ++kk) {
         const uint32_t ao = ((kk / G::kPer) * REG_A + (kk % G::kPer) * 32) >> 4;
         const uint32_t bo = ((kk / G::kPer) * REG_B + (kk % G::kPer) * 32) >> 4;
-        if (kk == 0) umma_ss_halves<0>(d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
-        else umma_ss_halves<1>(d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
+        if (kk == 0) mma_ss<0>(yes, d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
+        else mma_ss<1>(yes, d, a_lo + ao, a_hi, b_lo + bo, b_hi, idesc);
     }
 }
 
 // D (+)= P Y: P (bf16, 128 x N) in tensor memory, Y's N rows in shared memory, its columns outermost.
 template <int HD, int N>
-__device__ __forceinline__ void product(uint32_t d, uint32_t p, uint32_t y_lo, uint32_t y_hi, uint32_t idesc, bool fresh) {
-    if (fresh) umma_ts_halves<0>(d, p, y_lo, y_hi, idesc);
-    else umma_ts_halves<1>(d, p, y_lo, y_hi, idesc);
+__device__ __forceinline__ void product(uint32_t yes, uint32_t d, uint32_t p, uint32_t y_lo, uint32_t y_hi, uint32_t idesc, bool fresh) {
+    if (fresh) mma_ts<0>(yes, d, p, y_lo, y_hi, idesc);
+    else mma_ts<1>(yes, d, p, y_lo, y_hi, idesc);
 #pragma unroll
-    for (int kk = 1; kk < N / 16; ++kk) umma_ts_halves<1>(d, p + kk * 8, y_lo + ((kk * 16 * Geom<HD>::ROWB) >> 4), y_hi, idesc);
+    for (int kk = 1; kk < N / 16; ++kk) mma_ts<1>(yes, d, p + kk * 8, y_lo + ((kk * 16 * Geom<HD>::ROWB) >> 4), y_hi, idesc);
 }
 
 // Zeros over row r of a tile of rows of HD values (regions of REG bytes).
@@ -249,21 +290,22 @@ struct FwdShape : Geom<HD> {
     using G = Geom<HD>;
     static constexpr int REG = 128 * G::ROWB, TILE = G::NREG * REG;
     static constexpr int SLOTS = HD == 128 ? 5 : 8;    // of k and v in turn
-    static constexpr int OFF_KV = 2 * TILE, OFF_STEP = OFF_KV + SLOTS * TILE, OFF_BAR = OFF_STEP + kSteps * 32;
+    static constexpr int OFF_KV = 2 * TILE, OFF_STEP = OFF_KV + SLOTS * TILE, OFF_BAR = OFF_STEP + kSteps * 48;
     static constexpr int B_FULL = 0, B_EMPTY = SLOTS, B_QFULL = 2 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
-                         B_PFULL = B_SFULL + 2, B_OFULL = B_PFULL + 2, B_TOLD = B_OFULL + 2, B_HEARD = B_TOLD + kSteps,
-                         B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 1;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+                         B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_HALF = B_STAT + 2, B_TOLD = B_HALF + 2, B_HEARD = B_TOLD + kSteps,
+                         B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 2;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag
+    static constexpr int OFF_STAT = (OFF_MISC + 8 + 15) & ~15;   // sum and reference of each row
     // one block on an SM, which tensor memory is shared out for
-    static constexpr int NEED = OFF_MISC + 16 + 1024, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+    static constexpr int NEED = OFF_STAT + 2 * 128 * 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t TM_S = 0, TM_O = 256, OW = HD < 32 ? 32 : HD;   // scores of either row tile; their sums
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-constexpr int kFwdThreads = 384;
-// registers: the softmax takes what the third warpgroup leaves of 384 x 168
-constexpr uint32_t kRegsHigh = 216, kRegsLow = 72;
-static_assert(2 * kRegsHigh + kRegsLow <= 3 * 168, "register split");
+constexpr int kFwdThreads = 512;
+// registers: what the softmax, the way out and the rest take of 512 x 128
+constexpr uint32_t kRegsSoftmax = 168, kRegsOut = 104, kRegsLow = 72;
+static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
 
 template <int HD>
 __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, const CUtensorMap* tq,
@@ -328,10 +370,11 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 return false;
             };
             const uint32_t base_flags = two ? uint32_t(kTwo) : 0u;
+            const int64_t token0 = U.b * p.L + t0, row0 = token0 * p.NH + U.kh * p.G + (p.splits > 1 ? U.split * p.rows : 0);
             Found f{k0, -1, false};
             bool have = next(&f);
             if (!have) {
-                if (!tell({base_flags | kNone | kUnitLast, -1})) return false;
+                if (!tell({base_flags | kNone | kUnitLast, -1, t0, 0, {}, row0, token0})) return false;
                 continue;
             }
             int was = -1;
@@ -339,7 +382,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 Found g = f;
                 ++g.tile;
                 const bool more = next(&g);
-                Step s{base_flags, f.doc};
+                Step s{base_flags, f.doc, t0, 0, {}, row0, token0};
                 if (f.doc != was) s.flags |= kFirst;
                 if (!more || g.doc != f.doc) s.flags |= kLast;
                 if (first) s.flags |= kUnitFirst;
@@ -387,267 +430,366 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     }
 }
 
-// Tensor-core work in the order of its operands: the product of a step and row
-// tile is followed at once by the scores of the next step, which take the place
-// of its probabilities, so while one row tile is in its softmax the other's
-// products run.
+// The products of row tile a, by a warp of its own. The scores of a step are two
+// tiles of 64 columns in buffers of their own: a half's product is followed at once
+// by the scores of the next step's same half, which take the place of its
+// probabilities, so the softmax has the other half to work on meanwhile. (One tile of
+// 128 columns had the softmax wait 1500 of 3400 cycles a step for its scores. One warp
+// for both row tiles spends 100 cycles on each barrier that it waits for or commits
+// to, in which the tensor core runs dry.)
 template <int HD>
-__device__ __forceinline__ void fwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const volatile Step* steps) {
+__device__ __forceinline__ void fwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps, int a) {
     using F = FwdShape<HD>;
-    constexpr uint32_t id_s = make_idesc_bf16(128, 128, 0, 0), id_o = make_idesc_bf16(128, HD, 0, 1);
-    const uint64_t qd = make_smem_desc(base, 16, F::SBO, F::SWZ), kd = make_smem_desc(base + F::OFF_KV, 16, F::SBO, F::SWZ);
+    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0), id_o = make_idesc_bf16(128, HD, 0, 1);
+    constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;   // to the second 64 rows of a tile
+    const uint64_t qd = make_smem_desc(base + a * F::TILE, 16, F::SBO, F::SWZ), kd = make_smem_desc(base + F::OFF_KV, 16, F::SBO, F::SWZ);
     const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
     const uint32_t q_lo = uint32_t(qd), q_hi = uint32_t(qd >> 32), k_lo = uint32_t(kd), k_hi = uint32_t(kd >> 32);
     const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
-    uint32_t heard = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0}, slot_n = 0;   // slot_n: k's of the step to come
+    const uint32_t t_s = tmem + F::TM_S + 128 * a, t_o = tmem + F::TM_O + F::OW * a;
+    const uint32_t yes = elect();
+    uint32_t heard = 0, q_n = 0, p_n = 0, o_n = 0;
+    uint32_t st = 0, round = 0;   // the slot to come and how often the ring has gone round
 
-    auto hear = [&](uint32_t* flags) -> bool {   // of the next step that has columns, or the end
-        do {
-            const uint32_t e = heard % kSteps;
-            if (!sy.wait(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return false;
-            ++heard;
-            *flags = steps[e].flags;
-            mbar_arrive(sy.bar(F::B_HEARD + e));
-        } while (*flags & kNone);
-        return true;
-    };
-    auto issue_scores = [&](uint32_t flags, int a) -> bool {
-        if (flags & kUnitFirst) {
-            if (!sy.wait(sy.bar(F::B_QFULL + a), q_n[a] & 1u)) return false;
-            ++q_n[a];
+    auto advance = [&]() {
+        if (++st == F::SLOTS) {
+            st = 0;
+            ++round;
         }
-        const uint32_t st = slot_n % F::SLOTS;
-        if (!sy.wait(sy.bar(F::B_FULL + st), (slot_n / F::SLOTS) & 1u)) return false;
-        tc_fence_after();
-        scores<HD, F::REG, F::REG>(tmem + F::TM_S + 128 * a, q_lo + ((a * F::TILE) >> 4), q_hi, k_lo + ((st * F::TILE) >> 4), k_hi, id_s);
-        umma_commit(sy.bar(F::B_SFULL + a));
-        if (flags & kUnitLast) umma_commit(sy.bar(F::B_QEMPTY + a));
-        if (a == 1 || !(flags & kTwo)) umma_commit(sy.bar(F::B_EMPTY + st));
-        return true;
+    };
+    // The next step that this row tile has, or the end; slots that it has no use for are given back.
+    auto hear = [&](uint32_t* flags) -> bool {
+        for (;;) {
+            const uint32_t e = heard % kSteps;
+            if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return false;
+            ++heard;
+            *flags = __reduce_or_sync(kAll, steps[e].flags);
+            if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
+            if (*flags & kEnd) return true;
+            if (*flags & kNone) continue;
+            if (a == 0 || (*flags & kTwo)) return true;
+            for (int i = 0; i < 2; ++i, advance()) {
+                if (!sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return false;
+                if (yes) mbar_arrive(sy.bar(F::B_EMPTY + st));
+            }
+        }
     };
     auto run = [&]() {
-        uint32_t now;
-        if (!hear(&now) || (now & kEnd)) return;
-        for (int a = 0; a < ((now & kTwo) ? 2 : 1); ++a)
-            if (!issue_scores(now, a)) return;
-        for (;;) {
-            const uint32_t v_slot = (slot_n + 1) % F::SLOTS, v_par = ((slot_n + 1) / F::SLOTS) & 1u;
-            slot_n += 2;
-            uint32_t then = kEnd;
-            bool asked = false;
-            for (int a = 0; a < 2; ++a) {
-                if (a == 0 || (now & kTwo)) {
-                    if (!sy.wait(sy.bar(F::B_PFULL + a), p_n[a] & 1u)) return;
-                    ++p_n[a];
-                    if (!sy.wait(sy.bar(F::B_FULL + v_slot), v_par)) return;
-                    tc_fence_after();
-                    product<HD, 128>(tmem + F::TM_O + F::OW * a, tmem + F::TM_S + 128 * a, v_lo + ((v_slot * F::TILE) >> 4), v_hi, id_o,
-                                     (now & kFirst) != 0);
-                    if (now & kLast) umma_commit(sy.bar(F::B_OFULL + a));
-                    if (a == 1 || !(now & kTwo)) umma_commit(sy.bar(F::B_EMPTY + v_slot));
-                }
-                if (!asked && !hear(&then)) return;
-                asked = true;
-                if (!(then & kEnd) && (a == 0 || (then & kTwo)) && !issue_scores(then, a)) return;
+        uint32_t now = 0, then, v_st = 0, v_round = 0;   // v's slot of the step under way
+        if (!hear(&then)) return;
+        for (bool first = true;; first = false) {
+            // scores of the step `then`, behind the product of the step `now`; those of other rows behind
+            // all of it, since it does not wait for them
+            const bool end = (then & kEnd) != 0, apart = (then & kUnitFirst) != 0;
+            if (!end && !apart && !sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return;
+            if (!first) {
+                if (!sy.wait_warp(sy.bar(F::B_FULL + v_st), v_round & 1u)) return;
+                if ((now & kFirst) && !sy.wait_warp(sy.bar(F::B_OREAD + a), (o_n++ & 1u) ^ 1u)) return;
             }
-            if (then & kEnd) return;
+#pragma unroll 1
+            for (int i = 0; i < (apart ? 4 : 2); ++i) {
+                const int h = i & 1;
+                if (!first && i < 2) {
+                    if (!sy.wait_warp(sy.bar(F::B_PFULL + 2 * a + h), p_n & 1u)) return;
+                    tc_fence_after();
+                    product<HD, 64>(yes, t_o, t_s + 64 * h, v_lo + ((v_st * F::TILE) >> 4) + half_rows * h, v_hi, id_o,
+                                    h == 0 && (now & kFirst) != 0);
+                    if (h == 0) {
+                        commit(yes, sy.bar(F::B_HALF + a));
+                    } else {
+                        if (now & kLast) commit(yes, sy.bar(F::B_OFULL + a));
+                        commit(yes, sy.bar(F::B_EMPTY + v_st));
+                        ++p_n;
+                    }
+                }
+                if (apart && i == 2) {
+                    if (!sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
+                    if (!sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return;
+                    tc_fence_after();
+                }
+                if (!end && (!apart || i >= 2)) {
+                    scores<HD, F::REG, F::REG>(yes, t_s + 64 * h, q_lo, q_hi, k_lo + ((st * F::TILE) >> 4) + half_rows * h, k_hi, id_s);
+                    commit(yes, sy.bar(F::B_SFULL + 2 * a + h));
+                }
+            }
+            if (end) return;
+            if (then & kUnitLast) commit(yes, sy.bar(F::B_QEMPTY + a));
+            commit(yes, sy.bar(F::B_EMPTY + st));
+            advance();
+            v_st = st;
+            v_round = round;
+            advance();
             now = then;
+            if (!hear(&then)) return;
         }
     };
     run();
-    umma_commit(sy.bar(F::B_DRAIN));
-    drained(sy.bar(F::B_DRAIN), 0);
+    commit(yes, sy.bar(F::B_DRAIN + a));
+    if (yes) drained(sy.bar(F::B_DRAIN + a), 0);
 }
 
-// One row of scores to a thread, which keeps the reference maximum and the sum.
+// One row of scores to a thread, which keeps the reference of its powers and their
+// sum, and leaves them for the way out.
 template <int HD>
-__device__ __forceinline__ void fwd_softmax(const FwdParams& p, const Sync& sy, uint32_t base, uint32_t tmem, const volatile Step* steps) {
+__device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
     using F = FwdShape<HD>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + F::TM_S + 128 * a, t_o = t_lane + F::TM_O + F::OW * a;
-    uint32_t heard = 0, s_n = 0, o_n = 0, slot_n = 0;
-    const int tok = r / p.G, g = r - tok * p.G;
-
-    int u = blockIdx.x, doc = -1;
-    int64_t row = -1;           // of out; < 0: none
-    bool written = false;
-    auto enter = [&]() {
-        row = -1;
-        written = false;
-        if (u >= p.units) return;
-        const Unit U(p, u);
-        const int t = (U.pair * 2 + a) * p.rpt + tok;
-        if (tok < p.rpt && t < p.L) {
-            row = (U.b * p.L + t) * p.NH + U.kh * p.G + g + (p.splits > 1 ? U.split * p.rows : 0);
-            doc = p.doc ? __ldg(p.doc + U.b * p.L + t) : 0;
-        }
-    };
-    enter();
+    float2* const stat = reinterpret_cast<float2*>(base_ptr + F::OFF_STAT) + a * 128 + r;
+    uint32_t heard = 0, s_n = 0, passes = 0, slot_n = 0;
     float ref = 0.f, l = 0.f;
     for (;;) {
         const uint32_t e = heard % kSteps;
         if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return;
         ++heard;
         const uint32_t flags = steps[e].flags;
-        const int d = steps[e].doc;
-        uint32_t m[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = steps[e].mask[i];
+        const uint4 columns = *reinterpret_cast<const uint4*>(steps[e].mask);
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
         if (flags & kEnd) return;
         if (!(flags & kNone)) slot_n += 2;
         if (!(flags & kNone) && (a == 0 || (flags & kTwo))) {
-            if (!sy.wait_warp(sy.bar(F::B_SFULL + a), s_n & 1u)) return;
+            if (flags & kFirst) l = 0.f;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (!sy.wait_warp(sy.bar(F::B_SFULL + 2 * a + h), s_n & 1u)) return;
+                tc_fence_after();
+                const uint32_t t_h = t_s + 64 * h;
+                float s[64];
+                tmem_ld32(t_h, s);
+                tmem_ld32(t_h + 32, s + 32);
+                tmem_wait_ld();
+                behind_wait(s);
+                behind_wait(s + 32);
+                if (flags & kMasked) {
+                    const uint32_t m0 = h ? columns.z : columns.x, m1 = h ? columns.w : columns.y;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) s[j] = ((j < 32 ? m0 : m1) >> (j & 31)) & 1u ? s[j] : -INFINITY;
+                }
+                // By the reference of the tiles before, which the probabilities, their sums and O hold at
+                // any scale: only where a row's sum leaves 2^32, or is 0 so far, does its maximum become it.
+                // (One copy of this code for all of that: more of it did not stay in the instruction cache.)
+                float sum = 0.f;
+                bool anew = l == 0.f;
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    if (__any_sync(kAll, anew)) {
+                        float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
+#pragma unroll
+                        for (int j = 4; j < 64; j += 4) {
+                            t0 = max3f(t0, s[j], s[j + 1]);
+                            t1 = max3f(t1, s[j + 2], s[j + 3]);
+                        }
+                        const float top = fmaxf(t0, t1) * kLog2e, old = ref;
+                        if (l == 0.f) ref = top == -INFINITY ? 0.f : top;
+                        else if (anew) ref = fmaxf(ref, top);
+                        const float by = l == 0.f ? 1.f : ex2_approx(old - ref);
+                        if (__any_sync(kAll, by != 1.f)) {
+                            // O of the halves before this one: the first half's product of this step, or that of
+                            // the step before's second half, which this step's second scores stand behind
+                            if (!sy.wait_warp(sy.bar(h ? F::B_HALF + a : F::B_SFULL + 2 * a + 1), s_n & 1u)) {
+                                tmem_wait_st();
+                                return;
+                            }
+                            tc_fence_after();
+                            l *= by;
+#pragma unroll 1
+                            for (int q = 0; q < (HD + 31) / 32; ++q) {
+                                float o[32];
+                                tmem_ld32(t_o + 32 * q, o);
+                                tmem_wait_ld();
+                                behind_wait(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] *= by;
+                                tmem_st32(t_o + 32 * q, o);
+                            }
+                        }
+                    }
+                    const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), neg2 = f2_pack(-ref, -ref);
+                    uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float e0, e1;
+                            f2_unpack(f2_fma(f2_pack(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]), l2e2, neg2), e0, e1);
+                            e0 = ex2_approx(e0);
+                            e1 = ex2_approx(e1);
+                            pk[j] = pack_bf16x2(e0, e1);
+                            if (j & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
+                            else acc0 = f2_add(acc0, f2_pack(e0, e1));
+                        }
+                        tmem_st16(t_h + 16 * q, pk);
+                    }
+                    float x0, x1;
+                    f2_unpack(f2_add(acc0, acc1), x0, x1);
+                    sum = x0 + x1;
+                    anew = !(sum <= kSumLimit);
+                    if (again || !__any_sync(kAll, anew)) break;
+                }
+                l += sum;
+                if (h == 0 && (flags & kForeign)) {
+                    // this thread's column, where it is of another document: 0 times its value must be 0.
+                    // Either row tile's warps do so before their product; both write the same zeros.
+                    const uint32_t vs = slot_n - 1;
+                    if (!sy.wait_warp(sy.bar(F::B_FULL + vs % F::SLOTS), (vs / F::SLOTS) & 1u)) {
+                        tmem_wait_st();
+                        return;
+                    }
+                    if (!((warp & 2 ? (warp & 1 ? columns.w : columns.z) : (warp & 1 ? columns.y : columns.x)) >> lane & 1u))
+                        zero_row<HD, F::REG>(base + F::OFF_KV + (vs % F::SLOTS) * F::TILE, r);
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sy.bar(F::B_PFULL + 2 * a + h));
+            }
             ++s_n;
-            tc_fence_after();
-            float s[128];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, s + 32 * q);
-            tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) behind_wait(s + 32 * q);
-            if (flags & kMasked) {
-#pragma unroll
-                for (int j = 0; j < 128; ++j) s[j] = (m[j >> 5] >> (j & 31)) & 1u ? s[j] : -INFINITY;
+            if (flags & kLast) {
+                // the pass before has left (else its values and a barrier's phase would be overtaken)
+                if (!sy.wait_warp(sy.bar(F::B_OREAD + a), (passes++ & 1u) ^ 1u)) return;
+                *stat = make_float2(l, ref);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sy.bar(F::B_STAT + a));
             }
-            float t0 = s[0], t1 = s[1];
+        }
+    }
+}
+
+// The sums of a pass on their way out, by warps of their own: the softmax goes on
+// with the next rows meanwhile. (With its own threads' stores in its way a unit of
+// four steps took 11.3 us, 7.8 of them its steps.)
+template <int HD>
+__device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
+    using F = FwdShape<HD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + F::TM_O;
+    const float2* const stat = reinterpret_cast<const float2*>(base_ptr + F::OFF_STAT) + r;
+    const int tok = r / p.G, g = r - tok * p.G;
+    uint32_t heard = 0, passes[2] = {0, 0};
+    int64_t row[2] = {-1, -1};   // of out; < 0: none
+    int doc[2] = {-1, -1};
+    bool written[2] = {false, false};
+    for (;;) {
+        const uint32_t e = heard % kSteps;
+        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return;
+        ++heard;
+        const uint32_t flags = steps[e].flags;
+        const int d = steps[e].doc;
+        if (flags & (kUnitFirst | kNone)) {
+            const int t0 = steps[e].t0;
+            const int64_t row0 = steps[e].row, token0 = steps[e].token;
 #pragma unroll
-            for (int j = 2; j < 126; j += 4) {
-                t0 = max3f(t0, s[j], s[j + 1]);
-                t1 = max3f(t1, s[j + 2], s[j + 3]);
+            for (int a = 0; a < 2; ++a) {
+                const int i = a * p.rpt + tok;
+                row[a] = tok < p.rpt && t0 + i < p.L ? row0 + int64_t(i) * p.NH + g : -1;
+                doc[a] = row[a] >= 0 && p.doc ? __ldg(p.doc + token0 + i) : 0;
+                written[a] = false;
             }
-            const float top = max3f(t0, t1, fmaxf(s[126], s[127])) * kLog2e;
-            // the reference is exact at first and rises only by leaps of 2^8: O is seldom scaled
-            if (flags & kFirst) {
-                ref = top == -INFINITY ? 0.f : top;
-                l = 0.f;
-            } else {
-                const bool leap = top > ref + 8.f;
-                if (__any_sync(kAll, leap)) {
-                    const float by = leap ? ex2_approx(ref - top) : 1.f;
-                    ref = leap ? top : ref;
-                    l *= by;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
+        if (flags & kEnd) return;
+        if (flags & kLast) {
+#pragma unroll 1
+            for (int a = 0; a < ((flags & kTwo) ? 2 : 1); ++a) {
+                const int64_t to_row = a ? row[1] : row[0];
+                const bool mine = to_row >= 0 && (a ? doc[1] : doc[0]) == d;
+                const uint32_t n = a ? passes[1]++ : passes[0]++;
+                if (!sy.wait_warp(sy.bar(F::B_STAT + a), n & 1u)) return;
+                const float2 st = stat[a * 128];
+                const bool real = st.x > 0.f || st.x != st.x;
+                const float inv = real ? 1.f / st.x : 0.f;
+                if (!sy.wait_warp(sy.bar(F::B_OFULL + a), n & 1u)) return;
+                tc_fence_after();
+                if (p.splits > 1) {   // in 32 bits
 #pragma unroll 1
                     for (int q = 0; q < (HD + 31) / 32; ++q) {
                         float o[32];
-                        tmem_ld32(t_o + 32 * q, o);
+                        tmem_ld32(t_lane + F::OW * a + 32 * q, o);
+                        tmem_wait_ld();
+                        behind_wait(o);
+                        if (!mine) continue;
+                        float4* const to = reinterpret_cast<float4*>(p.part + to_row * HD + 32 * q);
+#pragma unroll
+                        for (int j = 0; j < (HD < 32 ? HD : 32) / 4; ++j)
+                            to[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sy.bar(F::B_OREAD + a));
+                } else {
+                    uint32_t kept[HD < 32 ? 16 : HD / 2];
+#pragma unroll
+                    for (int q = 0; q < (HD + 31) / 32; ++q) {
+                        float o[32];
+                        tmem_ld32(t_lane + F::OW * a + 32 * q, o);
                         tmem_wait_ld();
                         behind_wait(o);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] *= by;
-                        tmem_st32(t_o + 32 * q, o);
+                        for (int j = 0; j < 16; ++j) kept[16 * q + j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
                     }
-                }
-            }
-            const uint64_t l2e2 = f2_pack(kLog2e, kLog2e), neg2 = f2_pack(-ref, -ref);
-            uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float e0, e1;
-                    f2_unpack(f2_fma(f2_pack(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]), l2e2, neg2), e0, e1);
-                    e0 = ex2_approx(e0);
-                    e1 = ex2_approx(e1);
-                    pk[j] = pack_bf16x2(e0, e1);
-                    if (j & 1) acc1 = f2_add(acc1, f2_pack(e0, e1));
-                    else acc0 = f2_add(acc0, f2_pack(e0, e1));
-                }
-                tmem_st16(t_s + 16 * q, pk);
-            }
-            float x0, x1;
-            f2_unpack(f2_add(acc0, acc1), x0, x1);
-            l += x0 + x1;
-            if (a == 0 && (flags & kForeign)) {
-                // this thread's column, where it is of another document: 0 times its value must be 0
-                const uint32_t vs = slot_n - 1;
-                if (!sy.wait_warp(sy.bar(F::B_FULL + vs % F::SLOTS), (vs / F::SLOTS) & 1u)) {
-                    tmem_wait_st();
-                    return;
-                }
-                if (!((warp & 2 ? (warp & 1 ? m[3] : m[2]) : (warp & 1 ? m[1] : m[0])) >> lane & 1u))
-                    zero_row<HD, F::REG>(base + F::OFF_KV + (vs % F::SLOTS) * F::TILE, r);
-                fence_proxy_async_smem();
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(sy.bar(F::B_PFULL + a));
-            if (flags & kLast) {
-                if (!sy.wait_warp(sy.bar(F::B_OFULL + a), o_n & 1u)) return;
-                ++o_n;
-                tc_fence_after();
-                const bool mine = row >= 0 && doc == d;
-                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll 1
-                for (int q = 0; q < (HD + 31) / 32; ++q) {
-                    float o[32];
-                    tmem_ld32(t_o + 32 * q, o);
-                    tmem_wait_ld();
-                    behind_wait(o);
-                    if (!mine) continue;
-                    constexpr int W = HD < 32 ? HD : 32;
-                    if (p.splits > 1) {
-                        float4* const to = reinterpret_cast<float4*>(p.part + row * HD + 32 * q);
-#pragma unroll
-                        for (int j = 0; j < W / 4; ++j)
-                            to[j] = make_float4(o[4 * j] * inv, o[4 * j + 1] * inv, o[4 * j + 2] * inv, o[4 * j + 3] * inv);
-                    } else {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < W / 2; ++j) pk[j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-                        uint16_t* const to = p.out + row * HD + 32 * q;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sy.bar(F::B_OREAD + a));   // the next pass's products may come
+                    if (mine) {
+                        uint16_t* const to = p.out + to_row * HD;
                         if (p.out_v8) {
 #pragma unroll
-                            for (int j = 0; j < W / 16; ++j) st_global_v8(to + 16 * j, pk + 8 * j);
+                            for (int j = 0; j < HD / 16; ++j) st_global_v8(to + 16 * j, kept + 8 * j);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < W / 8; ++j)
-                                reinterpret_cast<uint4*>(to)[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                            for (int j = 0; j < HD / 8; ++j)
+                                reinterpret_cast<uint4*>(to)[j] = make_uint4(kept[4 * j], kept[4 * j + 1], kept[4 * j + 2], kept[4 * j + 3]);
                         }
                     }
                 }
-                tc_fence_before();
                 if (mine) {
-                    const float lse2 = l > 0.f || l != l ? ref + log2f(l) : -INFINITY;
-                    if (p.splits > 1) p.part_lse[row] = lse2;
-                    else if (p.lse) p.lse[row] = lse2 * kLn2;
-                    written = true;
+                    const float lse2 = real ? st.y + log2f(st.x) : -INFINITY;
+                    if (p.splits > 1) p.part_lse[to_row] = lse2;
+                    else if (p.lse) p.lse[to_row] = lse2 * kLn2;
+                    if (a) written[1] = true;
+                    else written[0] = true;
                 }
             }
         }
         if (flags & kUnitLast) {
-            if (row >= 0 && !written) {   // a row that sees nothing
-                if (p.splits > 1) {
-                    p.part_lse[row] = -INFINITY;
-                } else {
-                    uint4* const to = reinterpret_cast<uint4*>(p.out + row * HD);
 #pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                if (row[a] < 0 || written[a]) continue;   // else a row that sees nothing
+                if (p.splits > 1) {
+                    p.part_lse[row[a]] = -INFINITY;
+                } else {
+                    uint4* const to = reinterpret_cast<uint4*>(p.out + row[a] * HD);
+#pragma unroll 1
                     for (int j = 0; j < HD / 8; ++j) to[j] = make_uint4(0, 0, 0, 0);
-                    if (p.lse) p.lse[row] = -INFINITY;
+                    if (p.lse) p.lse[row[a]] = -INFINITY;
                 }
             }
-            u += gridDim.x;
-            enter();
         }
     }
 }
 
 // Two row tiles to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  the softmax of either row tile;
-//   warp 8            finds the column tiles that the rows see, TMA;
-//   warp 9            issues the products, owns the tensor memory.
+//   warps 8..11       results on their way out;
+//   warp 12           finds the column tiles that the rows see, TMA;
+//   warps 13, 14      issue the products of either row tile; 13 owns the tensor memory.
 template <int HD>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const __grid_constant__ FwdParams p) {
     using F = FwdShape<HD>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t* const base_ptr = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t base_ptr[];   // no room to align it here
+    const uint32_t base = smem_u32(base_ptr);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_cross_timeout_flag, 1u);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile uint32_t* const misc = reinterpret_cast<volatile uint32_t*>(base_ptr + F::OFF_MISC);
     Step* const steps = reinterpret_cast<Step*>(base_ptr + F::OFF_STEP);
@@ -657,17 +799,21 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         for (int i = threadIdx.x; i < 2 * F::TILE / 16; i += kFwdThreads) reinterpret_cast<uint4*>(base_ptr)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < F::NBAR; ++i)
-            mbar_init(sy.bar(i), i >= F::B_PFULL && i < F::B_PFULL + 2 ? 128u : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 9u : 1u);
+        for (int i = 0; i < F::NBAR; ++i) {
+            const bool by_warps = (i >= F::B_PFULL && i < F::B_PFULL + 4) || (i >= F::B_OREAD && i < F::B_OREAD + 2) ||
+                                  (i >= F::B_STAT && i < F::B_STAT + 2);
+            mbar_init(sy.bar(i), i >= F::B_EMPTY && i < F::B_EMPTY + F::SLOTS ? 2u : by_warps ? 4u
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 14u : 1u);
+        }
         misc[1] = 0u;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 12 && lane == 0) {
         tma_prefetch_desc(&tq);
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
-    if (warp == 9) {
+    if (warp == 13) {
         tmem_alloc(base + F::OFF_MISC, 512);
         tmem_relinquish();
     }
@@ -677,16 +823,19 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const uint32_t tmem = misc[0];
     dependents_may_start();
     if (warp < 8) {
-        regs_increase<kRegsHigh>();
-        fwd_softmax<HD>(p, sy, base, tmem, steps);
+        regs_increase<kRegsSoftmax>();
+        fwd_softmax<HD>(sy, base, base_ptr, tmem, steps);
+    } else if (warp < 12) {
+        regs_decrease<kRegsOut>();
+        fwd_out<HD>(p, sy, base_ptr, tmem, steps);
     } else {
         regs_decrease<kRegsLow>();
-        if (warp == 8) fwd_producer<HD>(p, sy, base, steps, &tq, &tk, &tv);
-        if (warp == 9 && lane == 0) fwd_issuer<HD>(sy, base, tmem, steps);
+        if (warp == 12) fwd_producer<HD>(p, sy, base, steps, &tq, &tk, &tv);
+        if (warp == 13 || warp == 14) fwd_issuer<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps, warp - 13);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

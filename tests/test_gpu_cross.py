@@ -75,6 +75,9 @@ CASES = [
     ((4, 1, 5, 5, 2, 64), 640, 2, 0, ""),
     ((1, 9, 10, 13, 1, 128), 383, 1, 0, ""),
     ((1, 1, 1, 600, 2, 16), 600, 2, 1, "runs"),
+    # many units of one column tile each to a block
+    ((1, 8, 24, 32, 16, 128), 77, 16, 0, ""),
+    ((2, 4, 24, 32, 16, 64), 20, 16, 2, "runs"),
 ]
 
 
