@@ -14,7 +14,6 @@
 // what other documents' rows and columns hold stays out of it: their columns are
 // zeroed in shared memory where they would meet a product as 0 times a value.
 #include <atomic>
-#include <cuda_bf16.h>
 #include <climits>
 
 #include "na3d_cross.cuh"
@@ -871,143 +870,548 @@ __global__ void __launch_bounds__(256) cross_join(const FwdParams p) {
     if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// ------------------------------------------------------------------ backward, simple
+// ------------------------------------------------------------------ backward
 
-constexpr int kWarps = 4;
+// Two passes of one kernel, each with fixed rows and streamed columns, so that
+// every sum has a place and an order of its own:
+//   DQ:  rows q, dout; columns k, v:   dq += ds k;
+//   DKV: rows k, v; columns q, dout:   dv += p^T dout, dk += ds^T q,
+// with s = rows0 columns0^T and dp = rows1 columns1^T, 128 x 64 a step, in two
+// buffers of tensor memory that two warpgroups take in turns; p and ds take the
+// place of s and dp and are multiplied from there.
+struct BwdParams {
+    int32_t nr, nc, rpt, cpt;            // tokens of an entry and of a tile, rows' and columns'
+    int32_t Gr, Gc, heads, NH, NKV, G;   // heads of a row's and a column's token in a tile; heads of a row's token
+    int32_t tiles_r, tiles_c, splits, per_split, units, B;
+    const int32_t *doc_r, *doc_c;
+    const uint16_t *out, *dout;          // for the statistics
+    const float* lse;
+    float2* stat;                        // (row of q): -lse log2e, -delta
+    uint16_t* grad[2];                   // DQ: dq; DKV: dv, dk
+    int64_t ts[2];
+    float* part;                         // splits > 1: (split, gradient, row, HD) in 32 bits
+    int64_t rows;                        // B * nr * heads
+};
 
-__device__ __forceinline__ float f32(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }
-__device__ __forceinline__ uint16_t b16(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+constexpr int kBwdSteps = 4;
 
 template <int HD>
-__device__ __forceinline__ float dot(const float* a, const uint16_t* b) {
-    float s = 0.f;
+struct BwdShape : Geom<HD> {
+    using G = Geom<HD>;
+    static constexpr int XREG = 128 * G::ROWB, XTILE = G::NREG * XREG, YREG = 64 * G::ROWB, YTILE = G::NREG * YREG;
+    static constexpr int STAGES = 5;
+    static constexpr int OFF_Y = 2 * XTILE, OFF_STAT = OFF_Y + STAGES * 2 * YTILE, OFF_STEP = OFF_STAT + STAGES * 512;
+    static constexpr int OFF_BAR = OFF_STEP + kBwdSteps * 48;
+    static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_XFULL = 2 * STAGES, B_XEMPTY = B_XFULL + 1, B_SFULL = B_XEMPTY + 1,
+                         B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 1, B_TOLD = B_AREAD + 1,
+                         B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+    static constexpr int NEED = OFF_MISC + 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+    static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;   // sums of either gradient; s and dp of either buffer
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+constexpr int kBwdThreads = 384;
+constexpr uint32_t kBwdHigh = 208, kBwdLow = 88;
+static_assert(2 * kBwdHigh + kBwdLow <= 3 * 168, "register split");
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// -lse log2e and -delta of every row of q, HD / 8 lanes to a row. Bound by the
+// read of out and dout. A row that sees nothing gets -infinity: its powers are 0.
+template <int HD>
+__global__ void __launch_bounds__(256) cross_stat(const BwdParams p, int64_t rows) {
+    constexpr int PER = HD / 8;
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / PER;
+    dependents_may_start();
+    const bool in = row < rows;
+    float sum = 0.f;
+    if (in) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p.out + i * 8), y = *reinterpret_cast<const uint4*>(p.dout + i * 8);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int c = 0; c < HD; c += 8) {
-        const uint4 v = *reinterpret_cast<const uint4*>(b + c);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int k = 0; k < 4; ++k) {
+            sum = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(v[k] << 16), sum);
+            sum = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(v[k] & 0xffff0000u), sum);
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s = fmaf(a[c + 2 * i], __uint_as_float(u[i] << 16), s);
-            s = fmaf(a[c + 2 * i + 1], __uint_as_float(u[i] & 0xffff0000u), s);
+    for (int o = PER / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (in && i % PER == 0) {
+        const float lse = p.lse[row];
+        p.stat[row] = make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -sum);
+    }
+}
+
+template <int HD, bool DKV>
+__device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, Step* steps,
+                                             const CUtensorMap* tx0, const CUtensorMap* tx1, const CUtensorMap* ty0, const CUtensorMap* ty1) {
+    using F = BwdShape<HD>;
+    const int lane = threadIdx.x & 31;
+    Tiles tiles{{p.doc_c, p.nc}, p.cpt};
+    const Docs rows{p.doc_r, p.nr};
+    uint32_t told = 0, it = 0, x_n = 0;
+    // this lane's columns of a tile: token and head
+    const int ctok[2] = {lane / p.Gc, (lane + 32) / p.Gc}, chead[2] = {lane % p.Gc, (lane + 32) % p.Gc};
+
+    auto tell = [&](const Step& s) -> bool {
+        const uint32_t e = told % kBwdSteps;
+        if (!sy.wait_warp(sy.bar(F::B_HEARD + e), ((told / kBwdSteps) & 1u) ^ 1u)) return false;
+        ++told;
+        if (lane == 0) {
+            steps[e] = s;
+            mbar_arrive(sy.bar(F::B_TOLD + e));
         }
-    }
-    return s;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    return v;
-}
-
-template <int HD, bool BWD>
-__global__ void __launch_bounds__(kWarps * 32) cross_rows(const CrossParams p) {
-    __shared__ float row_s[kWarps][2][HD];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t rows = int64_t(p.B) * p.L * p.NH, row = int64_t(blockIdx.x) * kWarps + warp;
-    if (row >= rows) return;
-    const int h = int(row % p.NH), kh = h / (p.NH / p.NKV);
-    const int64_t token = row / p.NH, b = token / p.L;
-    const int doc = p.doc ? p.doc[token] : 0;
-    for (int c = lane; c < HD; c += 32) {
-        row_s[warp][0][c] = f32(p.q[token * p.q_ts + int64_t(h) * HD + c]);
-        if (BWD) row_s[warp][1][c] = f32(p.dout[row * HD + c]);
-    }
-    __syncwarp();
-    constexpr int E = (HD + 31) / 32;
-    float acc[E] = {}, top = -INFINITY, sum = 0.f, delta = 0.f;
-    const float lse = BWD ? p.lse[row] : 0.f;
-    for (int pass = 0; pass < (BWD ? 2 : 1); ++pass)
-        for (int64_t j0 = 0; j0 < p.S; j0 += 32) {
-            const int64_t j = b * p.S + j0 + lane;
-            const bool seen = j0 + lane < p.S && doc >= 0 && (p.kv_doc ? p.kv_doc[j] : 0) == doc;
-            float s = seen ? dot<HD>(row_s[warp][0], p.k + j * p.k_ts + int64_t(kh) * HD) : -INFINITY, e;
-            if (!BWD) {
-                const float was = top;
-                top = fmaxf(top, warp_max(s));
-                if (top == -INFINITY) continue;
-                const float by = expf(was - top);
-                e = seen ? expf(s - top) : 0.f;
-                sum = sum * by + warp_sum(e);
-                for (int i = 0; i < E; ++i) acc[i] *= by;
-            } else {
-                e = seen ? expf(s - lse) : 0.f;
-                const float dp = seen ? dot<HD>(row_s[warp][1], p.v + j * p.v_ts + int64_t(kh) * HD) : 0.f;
-                if (pass == 0) {
-                    delta += warp_sum(e * dp);
-                    continue;
+        return true;
+    };
+    struct Found { int tile, doc; bool whole; };
+    auto run = [&]() {
+        for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+            int rest = u;
+            const int tile_r = rest % p.tiles_r;
+            rest /= p.tiles_r;
+            const int kh = rest % p.NKV;
+            rest /= p.NKV;
+            const int64_t b = rest % p.B;
+            const int split = rest / p.B;
+            const int t0 = tile_r * p.rpt, n_tok = min(p.rpt, p.nr - t0);
+            const int64_t token0 = b * p.nr + t0, row0 = token0 * p.heads + kh * p.Gr + split * 2 * p.rows;
+            int doc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(b, t0 + lane + 32 * i) : -1;
+            const int k0 = split * p.per_split, k1 = min(k0 + p.per_split, p.tiles_c);
+            int d = next_doc(doc, -1);
+            // of document d from the tile on, or of those behind it; the columns of this lane that are
+            auto mine = [&](int tile, int dd, int i) {
+                const int t = tile * p.cpt + ctok[i];
+                return ctok[i] < p.cpt && t < p.nc && tiles.docs.of(b, t) == dd;
+            };
+            auto next = [&](Found* f) {
+                for (; d >= 0; d = next_doc(doc, d), f->tile = k0) {
+                    f->tile = tiles.find(b, f->tile, k1, d, &f->whole);
+                    while (f->tile < k1) {
+                        f->doc = d;
+                        if (f->whole || __any_sync(kAll, mine(f->tile, d, 0) || mine(f->tile, d, 1))) return true;
+                        f->tile = tiles.find(b, f->tile + 1, k1, d, &f->whole);
+                    }
                 }
-                e *= dp - delta;
+                return false;
+            };
+            Found f{k0, -1, false};
+            bool have = next(&f);
+            if (!have) {
+                if (!tell({kNone | kUnitLast, -1, t0, kh, {}, row0, token0})) return false;
+                continue;
             }
-            const uint32_t live = __ballot_sync(~0u, seen);
-            for (int n = 0; n < 32; ++n) {
-                if (!(live >> n & 1u)) continue;
-                const float w = __shfl_sync(~0u, e, n);
-                const uint16_t* const from = (BWD ? p.k + (b * p.S + j0 + n) * p.k_ts : p.v + (b * p.S + j0 + n) * p.v_ts) + int64_t(kh) * HD;
-                for (int i = 0; i < E; ++i)
-                    if (lane + 32 * i < HD) acc[i] = fmaf(w, f32(from[lane + 32 * i]), acc[i]);
-            }
-        }
-    const float by = BWD ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
-    uint16_t* const to = BWD ? p.dq + token * p.dq_ts + int64_t(h) * HD : p.out + row * HD;
-    for (int i = 0; i < E; ++i)
-        if (lane + 32 * i < HD) to[lane + 32 * i] = b16(acc[i] * by);
-    if (!BWD && p.lse && lane == 0) p.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
-    if (BWD && lane == 0) static_cast<float*>(p.work)[row] = delta;
-}
-
-template <int HD>
-__global__ void __launch_bounds__(kWarps * 32) cross_states(const CrossParams p) {
-    __shared__ float row_s[kWarps][2][HD];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t rows = int64_t(p.B) * p.S * p.NKV, row = int64_t(blockIdx.x) * kWarps + warp;
-    if (row >= rows) return;
-    const int kh = int(row % p.NKV), G = p.NH / p.NKV;
-    const int64_t token = row / p.NKV, b = token / p.S;
-    const int doc = p.kv_doc ? p.kv_doc[token] : 0;
-    for (int c = lane; c < HD; c += 32) {
-        row_s[warp][0][c] = f32(p.k[token * p.k_ts + int64_t(kh) * HD + c]);
-        row_s[warp][1][c] = f32(p.v[token * p.v_ts + int64_t(kh) * HD + c]);
-    }
-    __syncwarp();
-    constexpr int E = (HD + 31) / 32;
-    float dk[E] = {}, dv[E] = {};
-    const int64_t n_rows = int64_t(p.L) * G;
-    for (int64_t i0 = 0; i0 < n_rows; i0 += 32) {
-        const int64_t i = i0 + lane, t = b * p.L + i / G, r = t * p.NH + kh * G + i % G;
-        const bool seen = i < n_rows && doc >= 0 && (p.doc ? p.doc[t] : 0) == doc;
-        const float s = seen ? dot<HD>(row_s[warp][0], p.q + t * p.q_ts + (r % p.NH) * HD) : 0.f;
-        const float e = seen ? expf(s - p.lse[r]) : 0.f;
-        const float ds = seen ? e * (dot<HD>(row_s[warp][1], p.dout + r * HD) - static_cast<const float*>(p.work)[r]) : 0.f;
-        const uint32_t live = __ballot_sync(~0u, seen);
-        for (int n = 0; n < 32; ++n) {
-            if (!(live >> n & 1u)) continue;
-            const float w = __shfl_sync(~0u, e, n), w2 = __shfl_sync(~0u, ds, n);
-            const int64_t tn = b * p.L + (i0 + n) / G, hn = kh * G + (i0 + n) % G;
-            for (int k = 0; k < E; ++k)
-                if (lane + 32 * k < HD) {
-                    dv[k] = fmaf(w, f32(p.dout[(tn * p.NH + hn) * HD + lane + 32 * k]), dv[k]);
-                    dk[k] = fmaf(w2, f32(p.q[tn * p.q_ts + hn * HD + lane + 32 * k]), dk[k]);
+            int was = -1;
+            for (bool first = true; have; first = false) {
+                Found g = f;
+                ++g.tile;
+                const bool more = next(&g);
+                Step s{0, f.doc, t0, kh, {}, row0, token0};
+                if (f.doc != was) s.flags |= kFirst;
+                if (!more || g.doc != f.doc) s.flags |= kLast;
+                if (first) s.flags |= kUnitFirst;
+                if (!more) s.flags |= kUnitLast;
+                was = f.doc;
+                bool gaps = false;
+                float2 st[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = f.tile * p.cpt + ctok[i];
+                    const bool in = ctok[i] < p.cpt && t < p.nc, of = in && (f.whole || tiles.docs.of(b, t) == f.doc);
+                    s.mask[i] = __ballot_sync(kAll, of);
+                    if (s.mask[i] != kAll) s.flags |= kMasked;
+                    gaps |= in && !of;
+                    st[i] = DKV && of ? __ldg(p.stat + (b * p.nc + t) * p.NH + kh * p.G + chead[i]) : make_float2(0.f, 0.f);
                 }
+                if (__any_sync(kAll, gaps)) s.flags |= kForeign;
+                if (!tell(s)) return false;
+                const uint32_t sl = it % F::STAGES;
+                if (!sy.wait_warp(sy.bar(F::B_EMPTY + sl), ((it / F::STAGES) & 1u) ^ 1u)) return false;
+                ++it;
+                if (DKV) {
+                    float* const to = reinterpret_cast<float*>(base_ptr + F::OFF_STAT + sl * 512);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        to[lane + 32 * i] = st[i].x;
+                        to[64 + lane + 32 * i] = st[i].y;
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    const uint32_t full = sy.bar(F::B_FULL + sl), to = base + F::OFF_Y + sl * 2 * F::YTILE;
+                    mbar_arrive_expect_tx(full, 2 * p.cpt * p.Gc * HD * 2);
+                    for (int r = 0; r < F::NREG; ++r) {
+                        load_box(to + r * F::YREG, ty0, full, r * F::HDB, kh * p.Gc, f.tile * p.cpt, int(b));
+                        load_box(to + F::YTILE + r * F::YREG, ty1, full, r * F::HDB, kh * p.Gc, f.tile * p.cpt, int(b));
+                    }
+                }
+                if (first) {
+                    if (!sy.wait_warp(sy.bar(F::B_XEMPTY), (x_n & 1u) ^ 1u)) return false;
+                    ++x_n;
+                    if (lane == 0) {
+                        const uint32_t full = sy.bar(F::B_XFULL);
+                        mbar_arrive_expect_tx(full, 2 * p.rpt * p.Gr * HD * 2);
+                        for (int r = 0; r < F::NREG; ++r) {
+                            load_box(base + r * F::XREG, tx0, full, r * F::HDB, kh * p.Gr, t0, int(b));
+                            load_box(base + F::XTILE + r * F::XREG, tx1, full, r * F::HDB, kh * p.Gr, t0, int(b));
+                        }
+                    }
+                }
+                have = more;
+                f = g;
+            }
         }
+        return tell({kEnd, -1});
+    };
+    run();
+    // every issued load lands before the block may exit
+    if (lane == 0) {
+        for (uint32_t s = 0; s < F::STAGES; ++s) {
+            const uint32_t n = it / F::STAGES + (s < it % F::STAGES ? 1u : 0u);
+            if (n) drained(sy.bar(F::B_FULL + s), (n - 1u) & 1u);
+        }
+        if (x_n) drained(sy.bar(F::B_XFULL), (x_n - 1u) & 1u);
     }
-    for (int i = 0; i < E; ++i)
-        if (lane + 32 * i < HD) {
-            p.dk[token * p.dk_ts + int64_t(kh) * HD + lane + 32 * i] = b16(dk[i]);
-            p.dv[token * p.dv_ts + int64_t(kh) * HD + lane + 32 * i] = b16(dv[i]);
-        }
 }
 
+// The products of step i are followed by the scores of step i + 2, which take the
+// place of its probabilities; scores of other rows wait until the products of the
+// rows before are on their way, since those rows' tiles come late.
+template <int HD, bool DKV>
+__device__ __forceinline__ void bwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+    using F = BwdShape<HD>;
+    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0), id_a = make_idesc_bf16(128, HD, 0, 1);
+    const uint64_t xd = make_smem_desc(base, 16, F::SBO, F::SWZ), yd = make_smem_desc(base + F::OFF_Y, 16, F::SBO, F::SWZ);
+    const uint64_t zd = make_smem_desc(base + F::OFF_Y, F::YREG, F::SBO, F::SWZ);   // Y's columns outermost
+    const uint32_t x_lo = uint32_t(xd), x_hi = uint32_t(xd >> 32), y_lo = uint32_t(yd), y_hi = uint32_t(yd >> 32);
+    const uint32_t z_lo = uint32_t(zd), z_hi = uint32_t(zd >> 32);
+    const uint32_t yes = elect();
+    uint32_t heard = 0, x_n = 0, a_n = 0;
+    auto hear = [&](uint32_t* flags) -> bool {
+        do {
+            const uint32_t e = heard % kBwdSteps;
+            if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return false;
+            ++heard;
+            *flags = __reduce_or_sync(kAll, steps[e].flags);
+            if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
+        } while (*flags & kNone);
+        return true;
+    };
+    auto run = [&]() {
+        uint32_t f0, f1 = 0, f2 = 0;   // of steps i, i + 1, i + 2, where they are known
+        bool know1 = false, know2 = false;
+        uint32_t issued = 0, i = 0;
+        auto issue = [&](uint32_t flags) -> bool {   // scores of step `issued`
+            if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) return false;
+            const uint32_t sl = issued % F::STAGES;
+            if (!sy.wait_warp(sy.bar(F::B_FULL + sl), (issued / F::STAGES) & 1u)) return false;
+            tc_fence_after();
+            const uint32_t t_s = tmem + F::TM_S + 128 * (issued & 1u);
+            const uint32_t y = y_lo + ((sl * 2 * F::YTILE) >> 4);
+            scores<HD, F::XREG, F::YREG>(yes, t_s, x_lo, x_hi, y, y_hi, id_s);
+            scores<HD, F::XREG, F::YREG>(yes, t_s + 64, x_lo + (F::XTILE >> 4), x_hi, y + (F::YTILE >> 4), y_hi, id_s);
+            commit(yes, sy.bar(F::B_SFULL + (issued & 1u)));
+            if (flags & kUnitLast) commit(yes, sy.bar(F::B_XEMPTY));
+            ++issued;
+            return true;
+        };
+        if (!hear(&f0) || (f0 & kEnd)) return;
+#pragma unroll 1
+        for (;; ++i) {
+            // One copy of the scores: of step i, i + 1 and, behind i's products, i + 2. A step is asked for
+            // when the scores before it are on their way: its rows may be waiting for that.
+#pragma unroll 1
+            for (int j = 0; j < 3; ++j) {
+                const uint32_t f = j == 0 ? f0 : j == 1 ? f1 : f2;
+                if (j == 2) {
+                    if ((f0 & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) return;
+                    if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) return;
+                    tc_fence_after();
+                    const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), sl = i % F::STAGES;
+                    const uint32_t z = z_lo + ((sl * 2 * F::YTILE) >> 4);
+                    const bool fresh = (f0 & kFirst) != 0;
+                    if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
+                    product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
+                    commit(yes, sy.bar(F::B_EMPTY + sl));
+                    if (f0 & kLast) commit(yes, sy.bar(F::B_AFULL));
+                }
+                const bool known = j == 0 || (j == 1 ? know1 : know2);
+                if (known && issued == i + j && !(f & kEnd) && (j == 0 || !(f & kUnitFirst)) && !issue(f)) return;
+                if (j == 0 && !know1) {
+                    if (!hear(&f1)) return;
+                    know1 = true;
+                }
+                if (j == 1 && !know2 && issued == i + 2) {
+                    if (!hear(&f2)) return;
+                    know2 = true;
+                }
+            }
+            if (f1 & kEnd) return;
+            f0 = f1;
+            f1 = f2;
+            know1 = know2;
+            know2 = false;
+        }
+    };
+    run();
+    commit(yes, sy.bar(F::B_DRAIN));
+    if (yes) drained(sy.bar(F::B_DRAIN), 0);
+}
+
+// Probabilities and their gradients of every second step, a row to a thread, and a
+// half of the results: a gradient (DKV) or half of its columns.
+template <int HD, bool DKV>
+__device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
+    using F = BwdShape<HD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16), t_s = t_lane + F::TM_S + 128 * a;
+    const int tok = r / p.Gr, g = r - tok * p.Gr;
+    // this warpgroup's columns of the results
+    constexpr int OC = DKV ? (HD < 32 ? 32 : HD) : HD >= 64 ? HD / 2 : 32;
+    const bool outs = DKV || HD >= 64 || a == 0;
+    const int c0 = !DKV && HD >= 64 ? a * OC : 0;
+    const uint32_t t_a = t_lane + (DKV ? F::AW * a : c0);
+    uint32_t heard = 0, n = 0, passes = 0;   // n: steps with columns
+    bool in = false, written = false;
+    int doc = -1, kh = 0;
+    int64_t row = 0, token = 0;   // of the workspace's rows and of the gradient's tokens
+    float2 st = make_float2(0.f, 0.f);
+    for (;;) {
+        const uint32_t e = heard % kBwdSteps;
+        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return;
+        ++heard;
+        const uint32_t flags = steps[e].flags;
+        const int d = steps[e].doc;
+        const uint2 columns = *reinterpret_cast<const uint2*>(steps[e].mask);
+        if (flags & (kUnitFirst | kNone)) {
+            in = tok < p.rpt && steps[e].t0 + tok < p.nr;
+            kh = steps[e].pad;
+            token = steps[e].token + tok;
+            row = steps[e].row + int64_t(tok) * p.heads + g;
+            doc = in && p.doc_r ? __ldg(p.doc_r + token) : 0;
+            written = false;
+            if (!DKV && in) st = p.stat[token * p.NH + kh * p.G + g];   // written by an earlier kernel, or by this row's thread
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
+        if (flags & kEnd) return;
+        if (!(flags & kNone) && (n & 1u) == uint32_t(a)) {
+            if (!sy.wait_warp(sy.bar(F::B_SFULL + a), (n >> 1) & 1u)) return;
+            tc_fence_after();
+            const uint32_t sl = n % F::STAGES;
+            const float4* const cs = reinterpret_cast<const float4*>(base_ptr + F::OFF_STAT + sl * 512);
+            const uint64_t l2e2 = f2_pack(kLog2e, kLog2e);
+            // A row that sees one tile alone: delta from its products, without the rounding that out has.
+            const bool exact = !DKV && p.splits == 1 && (flags & (kFirst | kLast)) == (kFirst | kLast);
+            float delta = 0.f;
+#pragma unroll 1
+            for (int k = exact ? 0 : 1; k < 2; ++k) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    float s[32], dp[32];
+                    tmem_ld32(t_s + 32 * q, s);
+                    tmem_ld32(t_s + 64 + 32 * q, dp);
+                    tmem_wait_ld();
+                    behind_wait(s);
+                    behind_wait(dp);
+                    const uint32_t m = q ? columns.y : columns.x;
+                    if (flags & kMasked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            s[j] = (m >> j) & 1u ? s[j] : -INFINITY;
+                            dp[j] = (m >> j) & 1u ? dp[j] : 0.f;
+                        }
+                    }
+                    uint32_t pk[DKV ? 16 : 1], dk[16];
+                    uint64_t nl = f2_pack(st.x, st.x), nd = f2_pack(st.y, st.y);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        float4 l4, d4;
+                        if (DKV) {
+                            l4 = cs[(32 * q + j) / 4];
+                            d4 = cs[16 + (32 * q + j) / 4];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (DKV) {
+                                nl = i ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
+                                nd = i ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
+                            }
+                            const int c = j + 2 * i;
+                            float p0, p1, d0, d1;
+                            f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), l2e2, nl), p0, p1);
+                            p0 = ex2_approx(p0);
+                            p1 = ex2_approx(p1);
+                            if (DKV) pk[DKV ? c / 2 : 0] = pack_bf16x2(p0, p1);
+                            if (!DKV && exact && k == 0) delta = fmaf(p0, dp[c], fmaf(p1, dp[c + 1], delta));
+                            f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(dp[c], dp[c + 1]), nd)), d0, d1);
+                            dk[c / 2] = pack_bf16x2(d0, d1);
+                        }
+                    }
+                    if (k == 0) continue;
+                    if (DKV) tmem_st16(t_s + 16 * q, pk);
+                    tmem_st16(t_s + 64 + 16 * q, dk);
+                }
+                if (k == 0) {
+                    const bool mine = in && doc == d;
+                    if (mine) {
+                        st.y = -delta;
+                        p.stat[token * p.NH + kh * p.G + g] = st;
+                    }
+                }
+            }
+            if (flags & kForeign) {
+                // columns of other documents, whose probabilities are 0: 0 times their values must be 0
+                const int c = r & 63;
+                if (!((c < 32 ? columns.x : columns.y) >> (c & 31) & 1u))
+                    zero_row<HD, F::YREG>(base + F::OFF_Y + sl * 2 * F::YTILE + (r < 64 ? 0 : F::YTILE), c);
+                fence_proxy_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sy.bar(F::B_PFULL + a));
+        }
+        if (!(flags & kNone)) ++n;
+        const bool last = (flags & kLast) != 0;
+        if (last) {
+            if (!sy.wait_warp(sy.bar(F::B_AFULL), passes++ & 1u)) return;
+            tc_fence_after();
+        }
+        const bool mine = in && doc == d, none = (flags & kUnitLast) && in && !written && !(last && mine);
+        if (last || (flags & kUnitLast)) {
+            uint16_t* const to = p.grad[DKV ? a : 0] + token * p.ts[DKV ? a : 0] + int64_t(kh * p.Gr + g) * HD + c0;
+            float* const part = p.part + (row + (DKV ? a * p.rows : 0)) * HD + c0;
+            constexpr int W = HD < 32 ? HD : 32;
+            if (outs) {
+#pragma unroll 1
+                for (int q = 0; q < OC / 32; ++q) {
+                    __syncwarp();
+                    float o[32];
+                    if (last) {
+                        tmem_ld32(t_a + 32 * q, o);
+                        tmem_wait_ld();
+                        behind_wait(o);
+                    }
+                    if (!(last && mine)) {
+                        if (!none) continue;   // another document's row, or one that is written: else one that sees nothing
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                    }
+                    if (p.splits > 1) {
+#pragma unroll
+                        for (int j = 0; j < W / 4; ++j)
+                            reinterpret_cast<float4*>(part + 32 * q)[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    } else {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < W / 2; ++j) pk[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+#pragma unroll
+                        for (int j = 0; j < W / 8; ++j)
+                            reinterpret_cast<uint4*>(to + 32 * q)[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                    }
+                }
+            }
+            if (last && mine) written = true;
+        }
+        if (last) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sy.bar(F::B_AREAD));
+        }
+    }
+}
+
+// One row tile to a block, one block to an SM, persistent:
+//   warps 0..3, 4..7  every second step's probabilities each, and the results;
+//   warp 8            finds the column tiles that the rows see, TMA;
+//   warp 9            issues the products, owns the tensor memory.
+template <int HD, bool DKV>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ CUtensorMap tx1, const __grid_constant__ CUtensorMap ty0,
+                const __grid_constant__ CUtensorMap ty1, const __grid_constant__ BwdParams p) {
+    using F = BwdShape<HD>;
+    extern __shared__ __align__(1024) uint8_t base_ptr[];   // no room to align it here
+    const uint32_t base = smem_u32(base_ptr);
+    if (base & 1023u) {
+        if (threadIdx.x == 0) atomicOr(&g_cross_timeout_flag, 1u);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* const misc = reinterpret_cast<volatile uint32_t*>(base_ptr + F::OFF_MISC);
+    Step* const steps = reinterpret_cast<Step*>(base_ptr + F::OFF_STEP);
+    const Sync sy{base + F::OFF_BAR, misc + 1};
+    // rows that no load writes (G does not divide a tile's) hold zeros
+    if (p.rpt * p.Gr != 128 || p.cpt * p.Gc != 64)
+        for (int i = threadIdx.x; i < F::OFF_STAT / 16; i += kBwdThreads) reinterpret_cast<uint4*>(base_ptr)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::NBAR; ++i)
+            mbar_init(sy.bar(i), i >= F::B_PFULL && i < F::B_PFULL + 2 ? 4u : i == F::B_AREAD ? 8u
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 9u : 1u);
+        misc[1] = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_desc(&tx0);
+        tma_prefetch_desc(&tx1);
+        tma_prefetch_desc(&ty0);
+        tma_prefetch_desc(&ty1);
+    }
+    if (warp == 9) {
+        tmem_alloc(base + F::OFF_MISC, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc[0];
+    dependents_may_start();
+    wait_for_primary();   // the statistics
+    if (warp < 8) {
+        regs_increase<kBwdHigh>();
+        bwd_softmax<HD, DKV>(p, sy, base, base_ptr, tmem, steps);
+    } else {
+        regs_decrease<kBwdLow>();
+        if (warp == 8) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, &tx0, &tx1, &ty0, &ty1);
+        if (warp == 9) bwd_issuer<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The splits of a gradient summed in order. grads: 1 (dq) or 2 (dv, dk).
 template <int HD>
-cudaError_t simple_bwd(const CrossParams& p, cudaStream_t stream) {
-    const int64_t rows = int64_t(p.B) * p.L * p.NH, states = int64_t(p.B) * p.S * p.NKV;
-    const unsigned grid = unsigned((rows + kWarps - 1) / kWarps);
-    cross_rows<HD, true><<<grid, kWarps * 32, 0, stream>>>(p);
-    cross_states<HD><<<unsigned((states + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(256) cross_sum(const BwdParams p, int grads) {
+    constexpr int PER = HD / 4;
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / PER;
+    const int c = int(i % PER) * 4, n = blockIdx.y;
+    dependents_may_start();
+    wait_for_primary();
+    if (row >= p.rows) return;
+    float o[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part + ((int64_t(s) * 2 + n) * p.rows + row) * HD + c);
+        o[0] += v.x;
+        o[1] += v.y;
+        o[2] += v.z;
+        o[3] += v.w;
+    }
+    const int64_t token = row / p.heads;
+    uint16_t* const to = p.grad[n] + token * p.ts[n] + (row - token * p.heads) * HD + c;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
 }
 
 // ------------------------------------------------------------------ host side
@@ -1032,6 +1436,9 @@ bool encode_heads(CUtensorMap* m, const void* ptr, int HD, int64_t B, int64_t n,
 constexpr int kSms = 152;   // what the work is shared out for: equal on every device
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The statistics of the backward pass, and the splits' sums behind them.
+int64_t stat_bytes(int64_t B, int64_t L, int64_t NH) { return (B * L * NH * 8 + 127) / 128 * 128; }
 
 struct FwdPlan {
     int64_t rpt, pairs, tiles, splits, per_split;
@@ -1098,13 +1505,113 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     return launch_after(cross_join<HD>, ceil_div(p.rows * (HD / 4), 256), 256, 0, stream, p);
 }
 
+// How a backward pass is shared out: `units` row tiles over `tiles` column tiles each, in so
+// many splits that the blocks' rounds hold the least of column tiles.
+struct BwdPlan {
+    int64_t rpt, cpt, tiles_r, tiles_c, splits, per_split, rows;
+    BwdPlan(bool dkv, int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV) {
+        const int64_t G = NH / NKV;
+        rpt = dkv ? 128 : 128 / G;
+        cpt = dkv ? 64 / G : 64;
+        tiles_r = ceil_div(dkv ? S : L, rpt);
+        tiles_c = ceil_div(dkv ? L : S, cpt);
+        rows = dkv ? B * S * NKV : B * L * NH;
+        const int64_t units = B * NKV * tiles_r;
+        splits = 1;
+        // a unit's beginning and end cost some four column tiles, a split's sums their memory
+        int64_t best = ceil_div(units, kSms) * (tiles_c + 4);
+        for (int64_t s = 2; s <= 64 && units < 4 * kSms && tiles_c / s >= 4; ++s) {
+            const int64_t cost = ceil_div(units * s, kSms) * (ceil_div(tiles_c, s) + 6);
+            if (cost < best - best / 16) {
+                best = cost;
+                splits = s;
+            }
+        }
+        per_split = ceil_div(tiles_c, splits);
+        splits = ceil_div(tiles_c, per_split);
+    }
+    int64_t part_bytes(int64_t HD) const { return splits > 1 ? splits * 2 * rows * HD * 4 : 0; }
+};
+
+template <int HD, bool DKV>
+cudaError_t bwd_pass(const CrossParams& c, int sms, cudaStream_t stream) {
+    const BwdPlan pl(DKV, c.B, c.L, c.S, c.NH, c.NKV);
+    const int64_t units = int64_t(c.B) * c.NKV * pl.tiles_r * pl.splits;
+    if (units >= (int64_t(1) << 31) - sms) return cudaErrorInvalidValue;
+    BwdParams p{};
+    p.B = c.B; p.NH = c.NH; p.NKV = c.NKV; p.G = c.NH / c.NKV;
+    p.nr = DKV ? c.S : c.L;
+    p.nc = DKV ? c.L : c.S;
+    p.rpt = int(pl.rpt);
+    p.cpt = int(pl.cpt);
+    p.Gr = DKV ? 1 : p.G;
+    p.Gc = DKV ? p.G : 1;
+    p.heads = DKV ? c.NKV : c.NH;
+    p.tiles_r = int(pl.tiles_r);
+    p.tiles_c = int(pl.tiles_c);
+    p.splits = int(pl.splits);
+    p.per_split = int(pl.per_split);
+    p.units = int(units);
+    p.doc_r = DKV ? c.kv_doc : c.doc;
+    p.doc_c = DKV ? c.doc : c.kv_doc;
+    p.out = c.out;
+    p.dout = c.dout;
+    p.lse = c.lse;
+    p.stat = static_cast<float2*>(c.work);
+    p.rows = pl.rows;
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(c.work) + stat_bytes(c.B, c.L, c.NH));
+    p.grad[0] = DKV ? c.dv : c.dq;
+    p.grad[1] = c.dk;
+    p.ts[0] = DKV ? c.dv_ts : c.dq_ts;
+    p.ts[1] = c.dk_ts;
+    if (!DKV) {   // the first of the two passes: the statistics before it
+        const int64_t rows = int64_t(c.B) * c.L * c.NH, blocks = ceil_div(rows * (HD / 8), 256);
+        if (blocks >= int64_t(1) << 31) return cudaErrorInvalidValue;
+        cross_stat<HD><<<unsigned(blocks), 256, 0, stream>>>(p, rows);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t row = int64_t(c.NH) * HD;
+    CUtensorMap q, d, k, v;
+    const int qt = DKV ? p.cpt : p.rpt, kt = DKV ? 128 : 64;
+    if (!encode_heads(&q, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, qt) || !encode_heads(&d, c.dout, HD, c.B, c.L, c.NH, row, p.G, qt) ||
+        !encode_heads(&k, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, kt) || !encode_heads(&v, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, kt))
+        return cudaErrorInvalidValue;
+    constexpr int smem = BwdShape<HD>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(cross_bwd_tiles<HD, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = units < sms ? units : sms;
+    e = DKV ? launch_after(cross_bwd_tiles<HD, DKV>, grid, kBwdThreads, smem, stream, k, v, q, d, p)
+            : launch_after(cross_bwd_tiles<HD, DKV>, grid, kBwdThreads, smem, stream, q, d, k, v, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(unsigned(ceil_div(pl.rows * (HD / 4), 256)), DKV ? 2 : 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cross_sum<HD>, p, DKV ? 2 : 1);
+}
+
+template <int HD>
+cudaError_t bwd(const CrossParams& c, int sms, cudaStream_t stream) {
+    const cudaError_t e = bwd_pass<HD, false>(c, sms, stream);
+    return e != cudaSuccess ? e : bwd_pass<HD, true>(c, sms, stream);
+}
+
 }  // namespace
 
 static std::atomic<bool> g_launched{false};
 
 int64_t cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, bool backward) {
     const int64_t rows = B * L * NH;
-    if (backward) return rows * 4;
+    if (backward) {
+        const int64_t a = BwdPlan(false, B, L, S, NH, NKV).part_bytes(HD), b = BwdPlan(true, B, L, S, NH, NKV).part_bytes(HD);
+        return stat_bytes(B, L, NH) + (a > b ? a : b);
+    }
     const FwdPlan pl(B, L, S, NH, NKV);
     return pl.splits > 1 ? pl.splits * rows * (HD + 1) * 4 : 0;
 }
@@ -1120,9 +1627,15 @@ cudaError_t launch_cross_fwd(int hd, const CrossParams& p, int sms, cudaStream_t
     }
 }
 
-cudaError_t launch_cross_bwd(int hd, const CrossParams& p, int, cudaStream_t stream) {
-    return hd == 16 ? simple_bwd<16>(p, stream) : hd == 32 ? simple_bwd<32>(p, stream)
-         : hd == 64 ? simple_bwd<64>(p, stream) : simple_bwd<128>(p, stream);
+cudaError_t launch_cross_bwd(int hd, const CrossParams& p, int sms, cudaStream_t stream) {
+    g_launched = true;
+    switch (hd) {
+        case 16: return bwd<16>(p, sms, stream);
+        case 32: return bwd<32>(p, sms, stream);
+        case 64: return bwd<64>(p, sms, stream);
+        case 128: return bwd<128>(p, sms, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 // The flag is taken as for the attention kernel: one atomic exchange per
