@@ -313,6 +313,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     const int lane = threadIdx.x & 31;
     Tiles tiles{{p.kv_doc, p.S}, 128};
     const Docs rows{p.doc, p.L};
+    const bool plain = !p.doc && !p.kv_doc;   // every column is of every row's document
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
 
     // One operand tile into the next slot.
@@ -345,12 +346,18 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
             const Unit U(p, u);
             const int t0 = U.pair * 2 * p.rpt, n_tok = min(2 * p.rpt, p.L - t0);
             const bool two = n_tok > p.rpt;
-            int doc[8];
+            int doc[8] = {};
+            if (!plain)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(U.b, t0 + lane + 32 * i) : -1;
+                for (int i = 0; i < 8; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(U.b, t0 + lane + 32 * i) : -1;
             const int k0 = U.split * p.per_split, k1 = min(k0 + p.per_split, p.tiles);
-            int d = next_doc(doc, -1);
+            int d = plain ? 0 : next_doc(doc, -1);
             auto next = [&](Found* f) {   // from f->tile on, of document d or those behind it
+                if (plain) {
+                    f->doc = 0;
+                    f->whole = true;
+                    return f->tile < k1;
+                }
                 for (; d >= 0; d = next_doc(doc, d), f->tile = k0) {
                     f->tile = tiles.find(U.b, f->tile, k1, d, &f->whole);
                     while (f->tile < k1) {
@@ -387,16 +394,21 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 if (first) s.flags |= kUnitFirst;
                 if (!more) s.flags |= kUnitLast;
                 was = f.doc;
-                bool gaps = false;
+                if (plain && f.tile * 128 + 128 <= p.S) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = f.tile * 128 + 32 * i + lane;
-                    const bool in = j < p.S, mine = in && (f.whole || tiles.docs.of(U.b, j) == f.doc);
-                    s.mask[i] = __ballot_sync(kAll, mine);
-                    if (s.mask[i] != kAll) s.flags |= kMasked;
-                    gaps |= in && !mine;
+                    for (int i = 0; i < 4; ++i) s.mask[i] = kAll;
+                } else {
+                    bool gaps = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = f.tile * 128 + 32 * i + lane;
+                        const bool in = j < p.S, mine = in && (f.whole || tiles.docs.of(U.b, j) == f.doc);
+                        s.mask[i] = __ballot_sync(kAll, mine);
+                        if (s.mask[i] != kAll) s.flags |= kMasked;
+                        gaps |= in && !mine;
+                    }
+                    if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 }
-                if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 if (!tell(s) || !load(tk, U, f.tile)) return false;
                 if (first) {
                     for (int a = 0; a < (two ? 2 : 1); ++a) {
@@ -954,6 +966,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
     const int lane = threadIdx.x & 31;
     Tiles tiles{{p.doc_c, p.nc}, p.cpt};
     const Docs rows{p.doc_r, p.nr};
+    const bool plain = !p.doc_r && !p.doc_c;   // every column is of every row's document
     uint32_t told = 0, it = 0, x_n = 0;
     // this lane's columns of a tile: token and head
     const int ctok[2] = {lane / p.Gc, (lane + 32) / p.Gc}, chead[2] = {lane % p.Gc, (lane + 32) % p.Gc};
@@ -980,17 +993,23 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
             const int split = rest / p.B;
             const int t0 = tile_r * p.rpt, n_tok = min(p.rpt, p.nr - t0);
             const int64_t token0 = b * p.nr + t0, row0 = token0 * p.heads + kh * p.Gr + split * 2 * p.rows;
-            int doc[4];
+            int doc[4] = {};
+            if (!plain)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(b, t0 + lane + 32 * i) : -1;
+                for (int i = 0; i < 4; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(b, t0 + lane + 32 * i) : -1;
             const int k0 = split * p.per_split, k1 = min(k0 + p.per_split, p.tiles_c);
-            int d = next_doc(doc, -1);
+            int d = plain ? 0 : next_doc(doc, -1);
             // of document d from the tile on, or of those behind it; the columns of this lane that are
             auto mine = [&](int tile, int dd, int i) {
                 const int t = tile * p.cpt + ctok[i];
                 return ctok[i] < p.cpt && t < p.nc && tiles.docs.of(b, t) == dd;
             };
             auto next = [&](Found* f) {
+                if (plain) {
+                    f->doc = 0;
+                    f->whole = true;
+                    return f->tile < k1;
+                }
                 for (; d >= 0; d = next_doc(doc, d), f->tile = k0) {
                     f->tile = tiles.find(b, f->tile, k1, d, &f->whole);
                     while (f->tile < k1) {
@@ -1007,29 +1026,45 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                 if (!tell({kNone | kUnitLast, -1, t0, kh, {}, row0, token0})) return false;
                 continue;
             }
+            // DKV: a step's statistics are read a step ahead
+            float2 st[2], ahead[2];
+            auto read = [&](const Found& x) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = x.tile * p.cpt + ctok[i];
+                    const bool of = ctok[i] < p.cpt && t < p.nc && (x.whole || tiles.docs.of(b, t) == x.doc);
+                    ahead[i] = of ? p.stat[(b * p.nc + t) * p.NH + kh * p.G + chead[i]] : make_float2(0.f, 0.f);
+                }
+            };
+            if (DKV) read(f);
             int was = -1;
             for (bool first = true; have; first = false) {
                 Found g = f;
                 ++g.tile;
                 const bool more = next(&g);
+                st[0] = ahead[0];
+                st[1] = ahead[1];
+                if (DKV && more) read(g);
                 Step s{0, f.doc, t0, kh, {}, row0, token0};
                 if (f.doc != was) s.flags |= kFirst;
                 if (!more || g.doc != f.doc) s.flags |= kLast;
                 if (first) s.flags |= kUnitFirst;
                 if (!more) s.flags |= kUnitLast;
                 was = f.doc;
-                bool gaps = false;
-                float2 st[2];
+                if (plain && p.cpt * p.Gc == 64 && (f.tile + 1) * p.cpt <= p.nc) {
+                    s.mask[0] = s.mask[1] = kAll;
+                } else {
+                    bool gaps = false;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int t = f.tile * p.cpt + ctok[i];
-                    const bool in = ctok[i] < p.cpt && t < p.nc, of = in && (f.whole || tiles.docs.of(b, t) == f.doc);
-                    s.mask[i] = __ballot_sync(kAll, of);
-                    if (s.mask[i] != kAll) s.flags |= kMasked;
-                    gaps |= in && !of;
-                    st[i] = DKV && of ? __ldg(p.stat + (b * p.nc + t) * p.NH + kh * p.G + chead[i]) : make_float2(0.f, 0.f);
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = f.tile * p.cpt + ctok[i];
+                        const bool in = ctok[i] < p.cpt && t < p.nc, of = in && (f.whole || tiles.docs.of(b, t) == f.doc);
+                        s.mask[i] = __ballot_sync(kAll, of);
+                        if (s.mask[i] != kAll) s.flags |= kMasked;
+                        gaps |= in && !of;
+                    }
+                    if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 }
-                if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 if (!tell(s)) return false;
                 const uint32_t sl = it % F::STAGES;
                 if (!sy.wait_warp(sy.bar(F::B_EMPTY + sl), ((it / F::STAGES) & 1u) ^ 1u)) return false;
@@ -1104,8 +1139,6 @@ __device__ __forceinline__ void bwd_issuer(const Sync& sy, uint32_t base, uint32
         return true;
     };
     auto run = [&]() {
-        uint32_t f0, f1 = 0, f2 = 0;   // of steps i, i + 1, i + 2, where they are known
-        bool know1 = false, know2 = false;
         uint32_t issued = 0, i = 0;
         auto issue = [&](uint32_t flags) -> bool {   // scores of step `issued`
             if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) return false;
@@ -1121,42 +1154,34 @@ __device__ __forceinline__ void bwd_issuer(const Sync& sy, uint32_t base, uint32
             ++issued;
             return true;
         };
-        if (!hear(&f0) || (f0 & kEnd)) return;
-#pragma unroll 1
-        for (;; ++i) {
-            // One copy of the scores: of step i, i + 1 and, behind i's products, i + 2. A step is asked for
-            // when the scores before it are on their way: its rows may be waiting for that.
-#pragma unroll 1
-            for (int j = 0; j < 3; ++j) {
-                const uint32_t f = j == 0 ? f0 : j == 1 ? f1 : f2;
-                if (j == 2) {
-                    if ((f0 & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) return;
-                    if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) return;
-                    tc_fence_after();
-                    const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), sl = i % F::STAGES;
-                    const uint32_t z = z_lo + ((sl * 2 * F::YTILE) >> 4);
-                    const bool fresh = (f0 & kFirst) != 0;
-                    if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
-                    product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
-                    commit(yes, sy.bar(F::B_EMPTY + sl));
-                    if (f0 & kLast) commit(yes, sy.bar(F::B_AFULL));
-                }
-                const bool known = j == 0 || (j == 1 ? know1 : know2);
-                if (known && issued == i + j && !(f & kEnd) && (j == 0 || !(f & kUnitFirst)) && !issue(f)) return;
-                if (j == 0 && !know1) {
-                    if (!hear(&f1)) return;
-                    know1 = true;
-                }
-                if (j == 1 && !know2 && issued == i + 2) {
-                    if (!hear(&f2)) return;
-                    know2 = true;
-                }
+        uint32_t f = 0, f0 = 0, f1 = 0;   // of step `issued` where it is known, and of steps i and i + 1
+        bool known = false;
+        for (;;) {
+            // scores of the steps i and i + 1; of other rows (whose tiles come late) only when they are next
+            while (issued < i + 2) {
+                if (!known && !hear(&f)) return;
+                known = true;
+                if ((f & kEnd) || (issued > i && (f & kUnitFirst))) break;
+                if (issued == i) f0 = f;
+                else f1 = f;
+                if (!issue(f)) return;
+                known = false;
             }
-            if (f1 & kEnd) return;
+            if (issued == i) return;
+            if (!known && !hear(&f)) return;   // ahead of need
+            known = true;
+            if ((f0 & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) return;
+            if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) return;
+            tc_fence_after();
+            const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), sl = i % F::STAGES;
+            const uint32_t z = z_lo + ((sl * 2 * F::YTILE) >> 4);
+            const bool fresh = (f0 & kFirst) != 0;
+            if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
+            product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
+            commit(yes, sy.bar(F::B_EMPTY + sl));
+            if (f0 & kLast) commit(yes, sy.bar(F::B_AFULL));
             f0 = f1;
-            f1 = f2;
-            know1 = know2;
-            know2 = false;
+            ++i;
         }
     };
     run();
