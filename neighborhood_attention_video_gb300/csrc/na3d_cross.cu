@@ -916,7 +916,7 @@ struct BwdShape : Geom<HD> {
     static constexpr int OFF_BAR = OFF_STEP + kBwdSteps * 48;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_XFULL = 2 * STAGES, B_XEMPTY = B_XFULL + 1, B_SFULL = B_XEMPTY + 1,
                          B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 1, B_TOLD = B_AREAD + 1,
-                         B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 1;
+                         B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int NEED = OFF_MISC + 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;   // sums of either gradient; s and dp of either buffer
@@ -1115,78 +1115,70 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
     }
 }
 
-// The products of step i are followed by the scores of step i + 2, which take the
-// place of its probabilities; scores of other rows wait until the products of the
-// rows before are on their way, since those rows' tiles come late.
-template <int HD, bool DKV>
-__device__ __forceinline__ void bwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+// Two warps issue: one the scores of a step, once the products of the last but one
+// are through with their place, one those products. (One warp for both took 2800
+// cycles a step of HD 128, its waits and commits between 24 products of 50.)
+template <int HD>
+__device__ __forceinline__ bool bwd_hear(const Sync& sy, const Step* steps, uint32_t yes, uint32_t& heard, uint32_t* flags) {
     using F = BwdShape<HD>;
-    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0), id_a = make_idesc_bf16(128, HD, 0, 1);
+    do {
+        const uint32_t e = heard % kBwdSteps;
+        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return false;
+        ++heard;
+        *flags = __reduce_or_sync(kAll, steps[e].flags);
+        if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
+    } while (*flags & kNone);
+    return !(*flags & kEnd);
+}
+
+template <int HD>
+__device__ __forceinline__ void bwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+    using F = BwdShape<HD>;
+    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0);
     const uint64_t xd = make_smem_desc(base, 16, F::SBO, F::SWZ), yd = make_smem_desc(base + F::OFF_Y, 16, F::SBO, F::SWZ);
-    const uint64_t zd = make_smem_desc(base + F::OFF_Y, F::YREG, F::SBO, F::SWZ);   // Y's columns outermost
     const uint32_t x_lo = uint32_t(xd), x_hi = uint32_t(xd >> 32), y_lo = uint32_t(yd), y_hi = uint32_t(yd >> 32);
-    const uint32_t z_lo = uint32_t(zd), z_hi = uint32_t(zd >> 32);
     const uint32_t yes = elect();
-    uint32_t heard = 0, x_n = 0, a_n = 0;
-    auto hear = [&](uint32_t* flags) -> bool {
-        do {
-            const uint32_t e = heard % kBwdSteps;
-            if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return false;
-            ++heard;
-            *flags = __reduce_or_sync(kAll, steps[e].flags);
-            if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
-        } while (*flags & kNone);
-        return true;
-    };
-    auto run = [&]() {
-        uint32_t issued = 0, i = 0;
-        auto issue = [&](uint32_t flags) -> bool {   // scores of step `issued`
-            if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) return false;
-            const uint32_t sl = issued % F::STAGES;
-            if (!sy.wait_warp(sy.bar(F::B_FULL + sl), (issued / F::STAGES) & 1u)) return false;
-            tc_fence_after();
-            const uint32_t t_s = tmem + F::TM_S + 128 * (issued & 1u);
-            const uint32_t y = y_lo + ((sl * 2 * F::YTILE) >> 4);
-            scores<HD, F::XREG, F::YREG>(yes, t_s, x_lo, x_hi, y, y_hi, id_s);
-            scores<HD, F::XREG, F::YREG>(yes, t_s + 64, x_lo + (F::XTILE >> 4), x_hi, y + (F::YTILE >> 4), y_hi, id_s);
-            commit(yes, sy.bar(F::B_SFULL + (issued & 1u)));
-            if (flags & kUnitLast) commit(yes, sy.bar(F::B_XEMPTY));
-            ++issued;
-            return true;
-        };
-        uint32_t f = 0, f0 = 0, f1 = 0;   // of step `issued` where it is known, and of steps i and i + 1
-        bool known = false;
-        for (;;) {
-            // scores of the steps i and i + 1; of other rows (whose tiles come late) only when they are next
-            while (issued < i + 2) {
-                if (!known && !hear(&f)) return;
-                known = true;
-                if ((f & kEnd) || (issued > i && (f & kUnitFirst))) break;
-                if (issued == i) f0 = f;
-                else f1 = f;
-                if (!issue(f)) return;
-                known = false;
-            }
-            if (issued == i) return;
-            if (!known && !hear(&f)) return;   // ahead of need
-            known = true;
-            if ((f0 & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) return;
-            if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) return;
-            tc_fence_after();
-            const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), sl = i % F::STAGES;
-            const uint32_t z = z_lo + ((sl * 2 * F::YTILE) >> 4);
-            const bool fresh = (f0 & kFirst) != 0;
-            if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
-            product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
-            commit(yes, sy.bar(F::B_EMPTY + sl));
-            if (f0 & kLast) commit(yes, sy.bar(F::B_AFULL));
-            f0 = f1;
-            ++i;
-        }
-    };
-    run();
+    uint32_t heard = 0, x_n = 0, flags;
+    uint32_t sl = 0, par = 0, was = F::STAGES - 2, was_par = 1;   // this step's stage and that of the last but one
+    for (uint32_t i = 0; bwd_hear<HD>(sy, steps, yes, heard, &flags); ++i) {
+        if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) break;
+        if (!sy.wait_warp(sy.bar(F::B_FULL + sl), par)) break;
+        if (i >= 2 && !sy.wait_warp(sy.bar(F::B_EMPTY + was), was_par)) break;
+        tc_fence_after();
+        const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), y = y_lo + ((sl * 2 * F::YTILE) >> 4);
+        scores<HD, F::XREG, F::YREG>(yes, t_s, x_lo, x_hi, y, y_hi, id_s);
+        scores<HD, F::XREG, F::YREG>(yes, t_s + 64, x_lo + (F::XTILE >> 4), x_hi, y + (F::YTILE >> 4), y_hi, id_s);
+        commit(yes, sy.bar(F::B_SFULL + (i & 1u)));
+        if (flags & kUnitLast) commit(yes, sy.bar(F::B_XEMPTY));
+        if (++sl == F::STAGES) { sl = 0; par ^= 1u; }
+        if (++was == F::STAGES) { was = 0; was_par ^= 1u; }
+    }
     commit(yes, sy.bar(F::B_DRAIN));
     if (yes) drained(sy.bar(F::B_DRAIN), 0);
+}
+
+template <int HD, bool DKV>
+__device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+    using F = BwdShape<HD>;
+    constexpr uint32_t id_a = make_idesc_bf16(128, HD, 0, 1);
+    const uint64_t zd = make_smem_desc(base + F::OFF_Y, F::YREG, F::SBO, F::SWZ);   // Y's columns outermost
+    const uint32_t z_lo = uint32_t(zd), z_hi = uint32_t(zd >> 32);
+    const uint32_t yes = elect();
+    uint32_t heard = 0, a_n = 0, flags, sl = 0;
+    for (uint32_t i = 0; bwd_hear<HD>(sy, steps, yes, heard, &flags); ++i) {
+        if ((flags & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) break;
+        if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) break;
+        tc_fence_after();
+        const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), z = z_lo + ((sl * 2 * F::YTILE) >> 4);
+        const bool fresh = (flags & kFirst) != 0;
+        if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
+        product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
+        commit(yes, sy.bar(F::B_EMPTY + sl));
+        if (flags & kLast) commit(yes, sy.bar(F::B_AFULL));
+        if (++sl == F::STAGES) sl = 0;
+    }
+    commit(yes, sy.bar(F::B_DRAIN + 1));
+    if (yes) drained(sy.bar(F::B_DRAIN + 1), 0);
 }
 
 // Probabilities and their gradients of every second step, a row to a thread, and a
@@ -1357,7 +1349,7 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
 // One row tile to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  every second step's probabilities each, and the results;
 //   warp 8            finds the column tiles that the rows see, TMA;
-//   warp 9            issues the products, owns the tensor memory.
+//   warps 9, 10       issue the scores and the products; 9 owns the tensor memory.
 template <int HD, bool DKV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ CUtensorMap tx1, const __grid_constant__ CUtensorMap ty0,
@@ -1380,7 +1372,7 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::NBAR; ++i)
             mbar_init(sy.bar(i), i >= F::B_PFULL && i < F::B_PFULL + 2 ? 4u : i == F::B_AREAD ? 8u
-                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 9u : 1u);
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 10u : 1u);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -1406,7 +1398,8 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     } else {
         regs_decrease<kBwdLow>();
         if (warp == 8) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, &tx0, &tx1, &ty0, &ty1);
-        if (warp == 9) bwd_issuer<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 9) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 10) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
     }
     tc_fence_before();
     __syncthreads();
