@@ -291,8 +291,8 @@ struct FwdShape : Geom<HD> {
     static constexpr int SLOTS = HD == 128 ? 5 : 8;    // of k and v in turn
     static constexpr int OFF_KV = 2 * TILE, OFF_STEP = OFF_KV + SLOTS * TILE, OFF_BAR = OFF_STEP + kSteps * 48;
     static constexpr int B_FULL = 0, B_EMPTY = SLOTS, B_QFULL = 2 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
-                         B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_HALF = B_STAT + 2, B_TOLD = B_HALF + 2, B_HEARD = B_TOLD + kSteps,
-                         B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 2;
+                         B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_DONE = B_STAT + 2, B_TOLD = B_DONE + 4, B_HEARD = B_TOLD + kSteps,
+                         B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 3;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag
     static constexpr int OFF_STAT = (OFF_MISC + 8 + 15) & ~15;   // sum and reference of each row
     // one block on an SM, which tensor memory is shared out for
@@ -303,7 +303,7 @@ struct FwdShape : Geom<HD> {
 
 constexpr int kFwdThreads = 512;
 // registers: what the softmax, the way out and the rest take of 512 x 128
-constexpr uint32_t kRegsSoftmax = 168, kRegsOut = 104, kRegsLow = 72;
+constexpr uint32_t kRegsSoftmax = 160, kRegsOut = 112, kRegsLow = 80;
 static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
 
 template <int HD>
@@ -441,102 +441,112 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     }
 }
 
-// The products of row tile a, by a warp of its own. The scores of a step are two
-// tiles of 64 columns in buffers of their own: a half's product is followed at once
-// by the scores of the next step's same half, which take the place of its
-// probabilities, so the softmax has the other half to work on meanwhile. (One tile of
-// 128 columns had the softmax wait 1500 of 3400 cycles a step for its scores. One warp
-// for both row tiles spends 100 cycles on each barrier that it waits for or commits
-// to, in which the tensor core runs dry.)
+// Three warps issue, the scores of either row tile and the products of both. The
+// scores of a step are two tiles of 64 columns in buffers of their own, which the
+// probabilities take over: a half's next scores follow when its product is through,
+// while the softmax works on the other half. (Each barrier that is waited for or
+// committed to costs an issuing warp some 100 cycles in which it issues nothing: one
+// warp for scores and products took 3600 cycles a step of HD 128, whose products are
+// 2048.)
+__device__ __forceinline__ bool fwd_hear(const Sync& sy, uint32_t told0, uint32_t heard0, const Step* steps, uint32_t yes, uint32_t& heard,
+                                         uint32_t* flags) {
+    do {
+        const uint32_t e = heard % kSteps;
+        if (!sy.wait_warp(told0 + 8 * e, (heard / kSteps) & 1u)) return false;
+        ++heard;
+        *flags = __reduce_or_sync(kAll, steps[e].flags);
+        if (yes) mbar_arrive(heard0 + 8 * e);
+    } while (*flags & kNone);
+    return !(*flags & kEnd);
+}
+
+// The slots of k (V 0) or v (V 1) of one step after another.
+template <int SLOTS>
+struct Slot {
+    uint32_t st, par = 0;
+    __device__ __forceinline__ explicit Slot(uint32_t first) : st(first) {}
+    __device__ __forceinline__ void next() {
+        st += 2;
+        if (st >= SLOTS) {
+            st -= SLOTS;
+            par ^= 1u;
+        }
+    }
+};
+
 template <int HD>
-__device__ __forceinline__ void fwd_issuer(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps, int a) {
+__device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps, int a) {
     using F = FwdShape<HD>;
-    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0), id_o = make_idesc_bf16(128, HD, 0, 1);
+    constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0);
     constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;   // to the second 64 rows of a tile
     const uint64_t qd = make_smem_desc(base + a * F::TILE, 16, F::SBO, F::SWZ), kd = make_smem_desc(base + F::OFF_KV, 16, F::SBO, F::SWZ);
-    const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
     const uint32_t q_lo = uint32_t(qd), q_hi = uint32_t(qd >> 32), k_lo = uint32_t(kd), k_hi = uint32_t(kd >> 32);
-    const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
-    const uint32_t t_s = tmem + F::TM_S + 128 * a, t_o = tmem + F::TM_O + F::OW * a;
+    const uint32_t t_s = tmem + F::TM_S + 128 * a;
     const uint32_t yes = elect();
-    uint32_t heard = 0, q_n = 0, p_n = 0, o_n = 0;
-    uint32_t st = 0, round = 0;   // the slot to come and how often the ring has gone round
-
-    auto advance = [&]() {
-        if (++st == F::SLOTS) {
-            st = 0;
-            ++round;
-        }
-    };
-    // The next step that this row tile has, or the end; slots that it has no use for are given back.
-    auto hear = [&](uint32_t* flags) -> bool {
-        for (;;) {
-            const uint32_t e = heard % kSteps;
-            if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return false;
-            ++heard;
-            *flags = __reduce_or_sync(kAll, steps[e].flags);
-            if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
-            if (*flags & kEnd) return true;
-            if (*flags & kNone) continue;
-            if (a == 0 || (*flags & kTwo)) return true;
-            for (int i = 0; i < 2; ++i, advance()) {
-                if (!sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return false;
-                if (yes) mbar_arrive(sy.bar(F::B_EMPTY + st));
-            }
-        }
-    };
+    uint32_t heard = 0, q_n = 0, n = 0, flags;
+    Slot<F::SLOTS> k(0);
     auto run = [&]() {
-        uint32_t now = 0, then, v_st = 0, v_round = 0;   // v's slot of the step under way
-        if (!hear(&then)) return;
-        for (bool first = true;; first = false) {
-            // scores of the step `then`, behind the product of the step `now`; those of other rows behind
-            // all of it, since it does not wait for them
-            const bool end = (then & kEnd) != 0, apart = (then & kUnitFirst) != 0;
-            if (!end && !apart && !sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return;
-            if (!first) {
-                if (!sy.wait_warp(sy.bar(F::B_FULL + v_st), v_round & 1u)) return;
-                if ((now & kFirst) && !sy.wait_warp(sy.bar(F::B_OREAD + a), (o_n++ & 1u) ^ 1u)) return;
+        for (; fwd_hear(sy, sy.bar(F::B_TOLD), sy.bar(F::B_HEARD), steps, yes, heard, &flags); k.next()) {
+            const bool mine = a == 0 || (flags & kTwo);
+            if (mine && (flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
+            if (!sy.wait_warp(sy.bar(F::B_FULL + k.st), k.par)) return;
+            if (!mine) {
+                if (yes) mbar_arrive(sy.bar(F::B_EMPTY + k.st));
+                continue;
             }
-#pragma unroll 1
-            for (int i = 0; i < (apart ? 4 : 2); ++i) {
-                const int h = i & 1;
-                if (!first && i < 2) {
-                    if (!sy.wait_warp(sy.bar(F::B_PFULL + 2 * a + h), p_n & 1u)) return;
-                    tc_fence_after();
-                    product<HD, 64>(yes, t_o, t_s + 64 * h, v_lo + ((v_st * F::TILE) >> 4) + half_rows * h, v_hi, id_o,
-                                    h == 0 && (now & kFirst) != 0);
-                    if (h == 0) {
-                        commit(yes, sy.bar(F::B_HALF + a));
-                    } else {
-                        if (now & kLast) commit(yes, sy.bar(F::B_OFULL + a));
-                        commit(yes, sy.bar(F::B_EMPTY + v_st));
-                        ++p_n;
-                    }
-                }
-                if (apart && i == 2) {
-                    if (!sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
-                    if (!sy.wait_warp(sy.bar(F::B_FULL + st), round & 1u)) return;
-                    tc_fence_after();
-                }
-                if (!end && (!apart || i >= 2)) {
-                    scores<HD, F::REG, F::REG>(yes, t_s + 64 * h, q_lo, q_hi, k_lo + ((st * F::TILE) >> 4) + half_rows * h, k_hi, id_s);
-                    commit(yes, sy.bar(F::B_SFULL + 2 * a + h));
-                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!sy.wait_warp(sy.bar(F::B_DONE + 2 * a + h), (n & 1u) ^ 1u)) return;
+                tc_fence_after();
+                scores<HD, F::REG, F::REG>(yes, t_s + 64 * h, q_lo, q_hi, k_lo + ((k.st * F::TILE) >> 4) + half_rows * h, k_hi, id_s);
+                commit(yes, sy.bar(F::B_SFULL + 2 * a + h));
             }
-            if (end) return;
-            if (then & kUnitLast) commit(yes, sy.bar(F::B_QEMPTY + a));
-            commit(yes, sy.bar(F::B_EMPTY + st));
-            advance();
-            v_st = st;
-            v_round = round;
-            advance();
-            now = then;
-            if (!hear(&then)) return;
+            ++n;
+            if (flags & kUnitLast) commit(yes, sy.bar(F::B_QEMPTY + a));
+            commit(yes, sy.bar(F::B_EMPTY + k.st));
         }
     };
     run();
     commit(yes, sy.bar(F::B_DRAIN + a));
     if (yes) drained(sy.bar(F::B_DRAIN + a), 0);
+}
+
+template <int HD>
+__device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+    using F = FwdShape<HD>;
+    constexpr uint32_t id_o = make_idesc_bf16(128, HD, 0, 1);
+    constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;
+    const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
+    const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
+    const uint32_t yes = elect();
+    uint32_t heard = 0, n[2] = {0, 0}, o_n[2] = {0, 0}, flags;
+    Slot<F::SLOTS> v(1);
+    auto run = [&]() {
+        for (; fwd_hear(sy, sy.bar(F::B_TOLD), sy.bar(F::B_HEARD), steps, yes, heard, &flags); v.next()) {
+            const int act = (flags & kTwo) ? 2 : 1;
+            if (!sy.wait_warp(sy.bar(F::B_FULL + v.st), v.par)) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int h = i >> 1, a = i & 1;
+                if (a >= act) continue;
+                if (h == 0 && (flags & kFirst) && !sy.wait_warp(sy.bar(F::B_OREAD + a), (o_n[a]++ & 1u) ^ 1u)) return;
+                if (!sy.wait_warp(sy.bar(F::B_PFULL + 2 * a + h), n[a] & 1u)) return;
+                tc_fence_after();
+                product<HD, 64>(yes, tmem + F::TM_O + F::OW * a, tmem + F::TM_S + 128 * a + 64 * h,
+                                v_lo + ((v.st * F::TILE) >> 4) + half_rows * h, v_hi, id_o, h == 0 && (flags & kFirst) != 0);
+                commit(yes, sy.bar(F::B_DONE + 2 * a + h));
+                if (h == 1) {
+                    ++n[a];
+                    if (flags & kLast) commit(yes, sy.bar(F::B_OFULL + a));
+                }
+            }
+            if (yes) mbar_arrive(sy.bar(F::B_EMPTY + v.st));   // k's slots are given back by two
+            commit(yes, sy.bar(F::B_EMPTY + v.st));
+        }
+    };
+    run();
+    commit(yes, sy.bar(F::B_DRAIN + 2));
+    if (yes) drained(sy.bar(F::B_DRAIN + 2), 0);
 }
 
 // One row of scores to a thread, which keeps the reference of its powers and their
@@ -598,9 +608,8 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
                         else if (anew) ref = fmaxf(ref, top);
                         const float by = l == 0.f ? 1.f : ex2_approx(old - ref);
                         if (__any_sync(kAll, by != 1.f)) {
-                            // O of the halves before this one: the first half's product of this step, or that of
-                            // the step before's second half, which this step's second scores stand behind
-                            if (!sy.wait_warp(sy.bar(h ? F::B_HALF + a : F::B_SFULL + 2 * a + 1), s_n & 1u)) {
+                            // O of the halves before this one
+                            if (!sy.wait_warp(sy.bar(F::B_DONE + 2 * a + (h ^ 1)), (s_n + h + 1) & 1u)) {
                                 tmem_wait_st();
                                 return;
                             }
@@ -789,7 +798,8 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 //   warps 0..3, 4..7  the softmax of either row tile;
 //   warps 8..11       results on their way out;
 //   warp 12           finds the column tiles that the rows see, TMA;
-//   warps 13, 14      issue the products of either row tile; 13 owns the tensor memory.
+//   warps 13, 14      issue the scores of either row tile; 13 owns the tensor memory;
+//   warp 15           issues the products.
 template <int HD>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -814,7 +824,7 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const bool by_warps = (i >= F::B_PFULL && i < F::B_PFULL + 4) || (i >= F::B_OREAD && i < F::B_OREAD + 2) ||
                                   (i >= F::B_STAT && i < F::B_STAT + 2);
             mbar_init(sy.bar(i), i >= F::B_EMPTY && i < F::B_EMPTY + F::SLOTS ? 2u : by_warps ? 4u
-                                 : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 14u : 1u);
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 15u : 1u);
         }
         misc[1] = 0u;
         fence_mbar_init();
@@ -842,7 +852,8 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     } else {
         regs_decrease<kRegsLow>();
         if (warp == 12) fwd_producer<HD>(p, sy, base, steps, &tq, &tk, &tv);
-        if (warp == 13 || warp == 14) fwd_issuer<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps, warp - 13);
+        if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps, warp - 13);
+        if (warp == 15) fwd_products<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
     }
     tc_fence_before();
     __syncthreads();
