@@ -926,17 +926,18 @@ struct BwdShape : Geom<HD> {
     static constexpr int OFF_Y = 2 * XTILE, OFF_STAT = OFF_Y + STAGES * 2 * YTILE, OFF_STEP = OFF_STAT + STAGES * 512;
     static constexpr int OFF_BAR = OFF_STEP + kBwdSteps * 48;
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_XFULL = 2 * STAGES, B_XEMPTY = B_XFULL + 1, B_SFULL = B_XEMPTY + 1,
-                         B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 1, B_TOLD = B_AREAD + 1,
+                         B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 2, B_TOLD = B_AREAD + 2,
                          B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 2;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int NEED = OFF_MISC + 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
-    static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;   // sums of either gradient; s and dp of either buffer
+    // sums: dv and dk, or dq of one pass and of the next; s and dp of either buffer
+    static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-constexpr int kBwdThreads = 384;
-constexpr uint32_t kBwdHigh = 208, kBwdLow = 88;
-static_assert(2 * kBwdHigh + kBwdLow <= 3 * 168, "register split");
+constexpr int kBwdThreads = 512;
+constexpr uint32_t kBwdSoftmax = 160, kBwdOut = 112, kBwdLow = 80;   // of 512 x 128
+static_assert(2 * kBwdSoftmax + kBwdOut + kBwdLow <= 4 * 128, "register split");
 
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     uint64_t d;
@@ -1175,25 +1176,28 @@ __device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint
     const uint64_t zd = make_smem_desc(base + F::OFF_Y, F::YREG, F::SBO, F::SWZ);   // Y's columns outermost
     const uint32_t z_lo = uint32_t(zd), z_hi = uint32_t(zd >> 32);
     const uint32_t yes = elect();
-    uint32_t heard = 0, a_n = 0, flags, sl = 0;
+    uint32_t heard = 0, passes = 0, flags, sl = 0;
     for (uint32_t i = 0; bwd_hear<HD>(sy, steps, yes, heard, &flags); ++i) {
-        if ((flags & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD), (a_n++ & 1u) ^ 1u)) break;
+        const uint32_t buf = DKV ? 0u : passes & 1u;
+        if ((flags & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD + buf), ((DKV ? passes : passes >> 1) & 1u) ^ 1u)) break;
         if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) break;
         tc_fence_after();
         const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), z = z_lo + ((sl * 2 * F::YTILE) >> 4);
         const bool fresh = (flags & kFirst) != 0;
         if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
-        product<HD, 64>(yes, tmem + (DKV ? F::AW : 0), t_s + 64, z, z_hi, id_a, fresh);
+        product<HD, 64>(yes, tmem + F::AW * (DKV ? 1u : buf), t_s + 64, z, z_hi, id_a, fresh);
         commit(yes, sy.bar(F::B_EMPTY + sl));
-        if (flags & kLast) commit(yes, sy.bar(F::B_AFULL));
+        if (flags & kLast) {
+            commit(yes, sy.bar(F::B_AFULL + buf));
+            ++passes;
+        }
         if (++sl == F::STAGES) sl = 0;
     }
     commit(yes, sy.bar(F::B_DRAIN + 1));
     if (yes) drained(sy.bar(F::B_DRAIN + 1), 0);
 }
 
-// Probabilities and their gradients of every second step, a row to a thread, and a
-// half of the results: a gradient (DKV) or half of its columns.
+// Probabilities and their gradients of every second step, a row to a thread.
 template <int HD, bool DKV>
 __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
     using F = BwdShape<HD>;
@@ -1201,15 +1205,10 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16), t_s = t_lane + F::TM_S + 128 * a;
     const int tok = r / p.Gr, g = r - tok * p.Gr;
-    // this warpgroup's columns of the results
-    constexpr int OC = DKV ? (HD < 32 ? 32 : HD) : HD >= 64 ? HD / 2 : 32;
-    const bool outs = DKV || HD >= 64 || a == 0;
-    const int c0 = !DKV && HD >= 64 ? a * OC : 0;
-    const uint32_t t_a = t_lane + (DKV ? F::AW * a : c0);
-    uint32_t heard = 0, n = 0, passes = 0;   // n: steps with columns
-    bool in = false, written = false;
-    int doc = -1, kh = 0;
-    int64_t row = 0, token = 0;   // of the workspace's rows and of the gradient's tokens
+    uint32_t heard = 0, n = 0;   // n: steps with columns
+    bool in = false;
+    int doc = -1;
+    float2* stat = nullptr;   // DQ: of this row
     float2 st = make_float2(0.f, 0.f);
     for (;;) {
         const uint32_t e = heard % kBwdSteps;
@@ -1218,14 +1217,12 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
         const uint32_t flags = steps[e].flags;
         const int d = steps[e].doc;
         const uint2 columns = *reinterpret_cast<const uint2*>(steps[e].mask);
-        if (flags & (kUnitFirst | kNone)) {
+        if (!DKV && (flags & kUnitFirst)) {
             in = tok < p.rpt && steps[e].t0 + tok < p.nr;
-            kh = steps[e].pad;
-            token = steps[e].token + tok;
-            row = steps[e].row + int64_t(tok) * p.heads + g;
+            const int64_t token = steps[e].token + tok;
             doc = in && p.doc_r ? __ldg(p.doc_r + token) : 0;
-            written = false;
-            if (!DKV && in) st = p.stat[token * p.NH + kh * p.G + g];   // written by an earlier kernel, or by this row's thread
+            stat = p.stat + token * p.NH + steps[e].pad * p.G + g;
+            if (in) st = *stat;   // written by an earlier kernel
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
@@ -1288,10 +1285,9 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                     tmem_st16(t_s + 64 + 16 * q, dk);
                 }
                 if (k == 0) {
-                    const bool mine = in && doc == d;
-                    if (mine) {
+                    if (in && doc == d) {
                         st.y = -delta;
-                        p.stat[token * p.NH + kh * p.G + g] = st;
+                        *stat = st;
                     }
                 }
             }
@@ -1308,59 +1304,87 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
             if (lane == 0) mbar_arrive(sy.bar(F::B_PFULL + a));
         }
         if (!(flags & kNone)) ++n;
-        const bool last = (flags & kLast) != 0;
-        if (last) {
-            if (!sy.wait_warp(sy.bar(F::B_AFULL), passes++ & 1u)) return;
-            tc_fence_after();
+    }
+}
+
+// The gradients of a pass on their way out.
+template <int HD, bool DKV>
+__device__ __forceinline__ void bwd_out(const BwdParams& p, const Sync& sy, uint32_t tmem, const Step* steps) {
+    using F = BwdShape<HD>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const int tok = r / p.Gr, g = r - tok * p.Gr;
+    constexpr int GRADS = DKV ? 2 : 1, W = HD < 32 ? HD : 32;
+    uint32_t heard = 0, passes = 0;
+    bool in = false, written = false;
+    int doc = -1, kh = 0;
+    int64_t row = 0, token = 0;   // of the workspace's rows and of the gradient's tokens
+    for (;;) {
+        const uint32_t e = heard % kBwdSteps;
+        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return;
+        ++heard;
+        const uint32_t flags = steps[e].flags;
+        const int d = steps[e].doc;
+        if (flags & (kUnitFirst | kNone)) {
+            in = tok < p.rpt && steps[e].t0 + tok < p.nr;
+            kh = steps[e].pad;
+            token = steps[e].token + tok;
+            row = steps[e].row + int64_t(tok) * p.heads + g;
+            doc = in && p.doc_r ? __ldg(p.doc_r + token) : 0;
+            written = false;
         }
-        const bool mine = in && doc == d, none = (flags & kUnitLast) && in && !written && !(last && mine);
-        if (last || (flags & kUnitLast)) {
-            uint16_t* const to = p.grad[DKV ? a : 0] + token * p.ts[DKV ? a : 0] + int64_t(kh * p.Gr + g) * HD + c0;
-            float* const part = p.part + (row + (DKV ? a * p.rows : 0)) * HD + c0;
-            constexpr int W = HD < 32 ? HD : 32;
-            if (outs) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
+        if (flags & kEnd) return;
+        const bool last = (flags & kLast) != 0, end = (flags & kUnitLast) != 0;
+        if (!last && !end) continue;
+        const uint32_t buf = DKV ? 0u : passes & 1u;
+        if (last && !sy.wait_warp(sy.bar(F::B_AFULL + buf), (DKV ? passes : passes >> 1) & 1u)) return;
+        if (last) tc_fence_after();
+        // a row of another document, or one that is written, is left; one that sees nothing gets zeros
+        const bool mine = last && in && doc == d, none = end && in && !written && !mine;
 #pragma unroll 1
-                for (int q = 0; q < OC / 32; ++q) {
-                    __syncwarp();
-                    float o[32];
-                    if (last) {
-                        tmem_ld32(t_a + 32 * q, o);
-                        tmem_wait_ld();
-                        behind_wait(o);
-                    }
-                    if (!(last && mine)) {
-                        if (!none) continue;   // another document's row, or one that is written: else one that sees nothing
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
-                    }
-                    if (p.splits > 1) {
-#pragma unroll
-                        for (int j = 0; j < W / 4; ++j)
-                            reinterpret_cast<float4*>(part + 32 * q)[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    } else {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < W / 2; ++j) pk[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-#pragma unroll
-                        for (int j = 0; j < W / 8; ++j)
-                            reinterpret_cast<uint4*>(to + 32 * q)[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-                    }
-                }
+        for (int i = 0; i < GRADS * ((HD + 31) / 32); ++i) {
+            const int n = DKV ? i / ((HD + 31) / 32) : 0, q = DKV ? i % ((HD + 31) / 32) : i;
+            __syncwarp();
+            float o[32];
+            if (last) {
+                tmem_ld32(t_lane + F::AW * (DKV ? n : buf) + 32 * q, o);
+                tmem_wait_ld();
+                behind_wait(o);
             }
-            if (last && mine) written = true;
+            if (!mine) {
+                if (!none) continue;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = 0.f;
+            }
+            if (p.splits > 1) {
+                float4* const to = reinterpret_cast<float4*>(p.part + (row + n * p.rows) * HD + 32 * q);
+#pragma unroll
+                for (int j = 0; j < W / 4; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else {
+                uint4* const to = reinterpret_cast<uint4*>(p.grad[n] + token * p.ts[n] + int64_t(kh * p.Gr + g) * HD + 32 * q);
+#pragma unroll
+                for (int j = 0; j < W / 8; ++j)
+                    to[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                       pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+            }
         }
+        if (mine) written = true;
         if (last) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sy.bar(F::B_AREAD));
+            if (lane == 0) mbar_arrive(sy.bar(F::B_AREAD + buf));
+            ++passes;
         }
     }
 }
 
 // One row tile to a block, one block to an SM, persistent:
-//   warps 0..3, 4..7  every second step's probabilities each, and the results;
-//   warp 8            finds the column tiles that the rows see, TMA;
-//   warps 9, 10       issue the scores and the products; 9 owns the tensor memory.
+//   warps 0..3, 4..7  every second step's probabilities each;
+//   warps 8..11       results on their way out;
+//   warp 12           finds the column tiles that the rows see, TMA;
+//   warps 13, 14      issue the scores and the products; 13 owns the tensor memory.
 template <int HD, bool DKV>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ CUtensorMap tx1, const __grid_constant__ CUtensorMap ty0,
@@ -1382,18 +1406,18 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     fence_proxy_async_smem();
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::NBAR; ++i)
-            mbar_init(sy.bar(i), i >= F::B_PFULL && i < F::B_PFULL + 2 ? 4u : i == F::B_AREAD ? 8u
-                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 10u : 1u);
+            mbar_init(sy.bar(i), (i >= F::B_PFULL && i < F::B_PFULL + 2) || (i >= F::B_AREAD && i < F::B_AREAD + 2) ? 4u
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 14u : 1u);
         misc[1] = 0u;
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 12 && lane == 0) {
         tma_prefetch_desc(&tx0);
         tma_prefetch_desc(&tx1);
         tma_prefetch_desc(&ty0);
         tma_prefetch_desc(&ty1);
     }
-    if (warp == 9) {
+    if (warp == 13) {
         tmem_alloc(base + F::OFF_MISC, 512);
         tmem_relinquish();
     }
@@ -1404,17 +1428,20 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     dependents_may_start();
     wait_for_primary();   // the statistics
     if (warp < 8) {
-        regs_increase<kBwdHigh>();
+        regs_increase<kBwdSoftmax>();
         bwd_softmax<HD, DKV>(p, sy, base, base_ptr, tmem, steps);
+    } else if (warp < 12) {
+        regs_decrease<kBwdOut>();
+        bwd_out<HD, DKV>(p, sy, tmem, steps);
     } else {
         regs_decrease<kBwdLow>();
-        if (warp == 8) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, &tx0, &tx1, &ty0, &ty1);
-        if (warp == 9) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
-        if (warp == 10) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 12) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, &tx0, &tx1, &ty0, &ty1);
+        if (warp == 13) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 14) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 13) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
