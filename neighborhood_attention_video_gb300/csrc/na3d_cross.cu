@@ -293,8 +293,8 @@ struct FwdShape : Geom<HD> {
     static constexpr int B_FULL = 0, B_EMPTY = SLOTS, B_QFULL = 2 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
                          B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_DONE = B_STAT + 2, B_TOLD = B_DONE + 4, B_HEARD = B_TOLD + kSteps,
                          B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 3;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag
-    static constexpr int OFF_STAT = (OFF_MISC + 8 + 15) & ~15;   // sum and reference of each row
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the slots' flags
+    static constexpr int OFF_STAT = (OFF_MISC + 8 + 4 * SLOTS + 15) & ~15;   // sum and reference of each row
     // one block on an SM, which tensor memory is shared out for
     static constexpr int NEED = OFF_STAT + 2 * 128 * 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t TM_S = 0, TM_O = 256, OW = HD < 32 ? 32 : HD;   // scores of either row tile; their sums
@@ -307,7 +307,7 @@ constexpr uint32_t kRegsSoftmax = 160, kRegsOut = 112, kRegsLow = 80;
 static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
 
 template <int HD>
-__device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, const CUtensorMap* tq,
+__device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, volatile uint32_t* said, const CUtensorMap* tq,
                                              const CUtensorMap* tk, const CUtensorMap* tv) {
     using F = FwdShape<HD>;
     const int lane = threadIdx.x & 31;
@@ -316,13 +316,18 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     const bool plain = !p.doc && !p.kv_doc;   // every column is of every row's document
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
 
-    // One operand tile into the next slot.
-    auto load = [&](const CUtensorMap* map, const Unit& U, int tile) -> bool {
+    // One operand tile into the next slot, with its step's flags.
+    auto load = [&](const CUtensorMap* map, const Unit& U, int tile, uint32_t flags) -> bool {
         const uint32_t st = slot_n % F::SLOTS;
         if (!sy.wait_warp(sy.bar(F::B_EMPTY + st), ((slot_n / F::SLOTS) & 1u) ^ 1u)) return false;
         ++slot_n;
         if (lane == 0) {
             const uint32_t full = sy.bar(F::B_FULL + st);
+            said[st] = flags;
+            if (flags & kEnd) {
+                mbar_arrive(full);
+                return true;
+            }
             mbar_arrive_expect_tx(full, F::TILE);
             for (int r = 0; r < F::NREG; ++r)
                 load_box(base + F::OFF_KV + st * F::TILE + r * F::REG, map, full, r * F::HDB, U.kh, tile * 128, int(U.b));
@@ -409,7 +414,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                     }
                     if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 }
-                if (!tell(s) || !load(tk, U, f.tile)) return false;
+                if (!tell(s) || !load(tk, U, f.tile, s.flags)) return false;
                 if (first) {
                     for (int a = 0; a < (two ? 2 : 1); ++a) {
                         if (!sy.wait_warp(sy.bar(F::B_QEMPTY + a), (q_n[a] & 1u) ^ 1u)) return false;
@@ -422,12 +427,13 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                         }
                     }
                 }
-                if (!load(tv, U, f.tile)) return false;
+                if (!load(tv, U, f.tile, s.flags)) return false;
                 have = more;
                 f = g;
             }
         }
-        return tell({kEnd, -1});
+        const Unit none(p, 0);
+        return tell({kEnd, -1}) && load(tk, none, 0, kEnd) && load(tv, none, 0, kEnd);
     };
     run();
     // every issued load lands before the block may exit
@@ -448,18 +454,6 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
 // committed to costs an issuing warp some 100 cycles in which it issues nothing: one
 // warp for scores and products took 3600 cycles a step of HD 128, whose products are
 // 2048.)
-__device__ __forceinline__ bool fwd_hear(const Sync& sy, uint32_t told0, uint32_t heard0, const Step* steps, uint32_t yes, uint32_t& heard,
-                                         uint32_t* flags) {
-    do {
-        const uint32_t e = heard % kSteps;
-        if (!sy.wait_warp(told0 + 8 * e, (heard / kSteps) & 1u)) return false;
-        ++heard;
-        *flags = __reduce_or_sync(kAll, steps[e].flags);
-        if (yes) mbar_arrive(heard0 + 8 * e);
-    } while (*flags & kNone);
-    return !(*flags & kEnd);
-}
-
 // The slots of k (V 0) or v (V 1) of one step after another.
 template <int SLOTS>
 struct Slot {
@@ -475,7 +469,7 @@ struct Slot {
 };
 
 template <int HD>
-__device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps, int a) {
+__device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said, int a) {
     using F = FwdShape<HD>;
     constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0);
     constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;   // to the second 64 rows of a tile
@@ -483,13 +477,15 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
     const uint32_t q_lo = uint32_t(qd), q_hi = uint32_t(qd >> 32), k_lo = uint32_t(kd), k_hi = uint32_t(kd >> 32);
     const uint32_t t_s = tmem + F::TM_S + 128 * a;
     const uint32_t yes = elect();
-    uint32_t heard = 0, q_n = 0, n = 0, flags;
+    uint32_t q_n = 0, n = 0;
     Slot<F::SLOTS> k(0);
     auto run = [&]() {
-        for (; fwd_hear(sy, sy.bar(F::B_TOLD), sy.bar(F::B_HEARD), steps, yes, heard, &flags); k.next()) {
+        for (;; k.next()) {
+            if (!sy.wait_warp(sy.bar(F::B_FULL + k.st), k.par)) return;
+            const uint32_t flags = __reduce_or_sync(kAll, said[k.st]);
+            if (flags & kEnd) return;
             const bool mine = a == 0 || (flags & kTwo);
             if (mine && (flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
-            if (!sy.wait_warp(sy.bar(F::B_FULL + k.st), k.par)) return;
             if (!mine) {
                 if (yes) mbar_arrive(sy.bar(F::B_EMPTY + k.st));
                 continue;
@@ -512,19 +508,21 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
 }
 
 template <int HD>
-__device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+__device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said) {
     using F = FwdShape<HD>;
     constexpr uint32_t id_o = make_idesc_bf16(128, HD, 0, 1);
     constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;
     const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
     const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
     const uint32_t yes = elect();
-    uint32_t heard = 0, n[2] = {0, 0}, o_n[2] = {0, 0}, flags;
+    uint32_t n[2] = {0, 0}, o_n[2] = {0, 0};
     Slot<F::SLOTS> v(1);
     auto run = [&]() {
-        for (; fwd_hear(sy, sy.bar(F::B_TOLD), sy.bar(F::B_HEARD), steps, yes, heard, &flags); v.next()) {
-            const int act = (flags & kTwo) ? 2 : 1;
+        for (;; v.next()) {
             if (!sy.wait_warp(sy.bar(F::B_FULL + v.st), v.par)) return;
+            const uint32_t flags = __reduce_or_sync(kAll, said[v.st]);
+            if (flags & kEnd) return;
+            const int act = (flags & kTwo) ? 2 : 1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int h = i >> 1, a = i & 1;
@@ -824,7 +822,7 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
             const bool by_warps = (i >= F::B_PFULL && i < F::B_PFULL + 4) || (i >= F::B_OREAD && i < F::B_OREAD + 2) ||
                                   (i >= F::B_STAT && i < F::B_STAT + 2);
             mbar_init(sy.bar(i), i >= F::B_EMPTY && i < F::B_EMPTY + F::SLOTS ? 2u : by_warps ? 4u
-                                 : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 15u : 1u);
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 12u : 1u);
         }
         misc[1] = 0u;
         fence_mbar_init();
@@ -851,9 +849,9 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         fwd_out<HD>(p, sy, base_ptr, tmem, steps);
     } else {
         regs_decrease<kRegsLow>();
-        if (warp == 12) fwd_producer<HD>(p, sy, base, steps, &tq, &tk, &tv);
-        if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps, warp - 13);
-        if (warp == 15) fwd_products<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 12) fwd_producer<HD>(p, sy, base, steps, misc + 2, &tq, &tk, &tv);
+        if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2, warp - 13);
+        if (warp == 15) fwd_products<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -928,8 +926,8 @@ struct BwdShape : Geom<HD> {
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_XFULL = 2 * STAGES, B_XEMPTY = B_XFULL + 1, B_SFULL = B_XEMPTY + 1,
                          B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 2, B_TOLD = B_AREAD + 2,
                          B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 2;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int NEED = OFF_MISC + 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the stages' flags
+    static constexpr int NEED = OFF_MISC + 8 + 4 * STAGES, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     // sums: dv and dk, or dq of one pass and of the next; s and dp of either buffer
     static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;
     static_assert(SMEM <= 232448, "shared memory");
@@ -972,7 +970,7 @@ __global__ void __launch_bounds__(256) cross_stat(const BwdParams p, int64_t row
 }
 
 template <int HD, bool DKV>
-__device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, Step* steps,
+__device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, Step* steps, volatile uint32_t* said,
                                              const CUtensorMap* tx0, const CUtensorMap* tx1, const CUtensorMap* ty0, const CUtensorMap* ty1) {
     using F = BwdShape<HD>;
     const int lane = threadIdx.x & 31;
@@ -1092,6 +1090,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                 }
                 if (lane == 0) {
                     const uint32_t full = sy.bar(F::B_FULL + sl), to = base + F::OFF_Y + sl * 2 * F::YTILE;
+                    said[sl] = s.flags;
                     mbar_arrive_expect_tx(full, 2 * p.cpt * p.Gc * HD * 2);
                     for (int r = 0; r < F::NREG; ++r) {
                         load_box(to + r * F::YREG, ty0, full, r * F::HDB, kh * p.Gc, f.tile * p.cpt, int(b));
@@ -1114,7 +1113,15 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                 f = g;
             }
         }
-        return tell({kEnd, -1});
+        if (!tell({kEnd, -1})) return false;
+        const uint32_t sl = it % F::STAGES;
+        if (!sy.wait_warp(sy.bar(F::B_EMPTY + sl), ((it / F::STAGES) & 1u) ^ 1u)) return false;
+        ++it;
+        if (lane == 0) {
+            said[sl] = kEnd;
+            mbar_arrive(sy.bar(F::B_FULL + sl));
+        }
+        return true;
     };
     run();
     // every issued load lands before the block may exit
@@ -1131,30 +1138,19 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
 // are through with their place, one those products. (One warp for both took 2800
 // cycles a step of HD 128, its waits and commits between 24 products of 50.)
 template <int HD>
-__device__ __forceinline__ bool bwd_hear(const Sync& sy, const Step* steps, uint32_t yes, uint32_t& heard, uint32_t* flags) {
-    using F = BwdShape<HD>;
-    do {
-        const uint32_t e = heard % kBwdSteps;
-        if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kBwdSteps) & 1u)) return false;
-        ++heard;
-        *flags = __reduce_or_sync(kAll, steps[e].flags);
-        if (yes) mbar_arrive(sy.bar(F::B_HEARD + e));
-    } while (*flags & kNone);
-    return !(*flags & kEnd);
-}
-
-template <int HD>
-__device__ __forceinline__ void bwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+__device__ __forceinline__ void bwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said) {
     using F = BwdShape<HD>;
     constexpr uint32_t id_s = make_idesc_bf16(128, 64, 0, 0);
     const uint64_t xd = make_smem_desc(base, 16, F::SBO, F::SWZ), yd = make_smem_desc(base + F::OFF_Y, 16, F::SBO, F::SWZ);
     const uint32_t x_lo = uint32_t(xd), x_hi = uint32_t(xd >> 32), y_lo = uint32_t(yd), y_hi = uint32_t(yd >> 32);
     const uint32_t yes = elect();
-    uint32_t heard = 0, x_n = 0, flags;
+    uint32_t x_n = 0;
     uint32_t sl = 0, par = 0, was = F::STAGES - 2, was_par = 1;   // this step's stage and that of the last but one
-    for (uint32_t i = 0; bwd_hear<HD>(sy, steps, yes, heard, &flags); ++i) {
-        if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) break;
+    for (uint32_t i = 0;; ++i) {
         if (!sy.wait_warp(sy.bar(F::B_FULL + sl), par)) break;
+        const uint32_t flags = __reduce_or_sync(kAll, said[sl]);
+        if (flags & kEnd) break;
+        if ((flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_XFULL), x_n++ & 1u)) break;
         if (i >= 2 && !sy.wait_warp(sy.bar(F::B_EMPTY + was), was_par)) break;
         tc_fence_after();
         const uint32_t t_s = tmem + F::TM_S + 128 * (i & 1u), y = y_lo + ((sl * 2 * F::YTILE) >> 4);
@@ -1170,14 +1166,17 @@ __device__ __forceinline__ void bwd_scores(const Sync& sy, uint32_t base, uint32
 }
 
 template <int HD, bool DKV>
-__device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const Step* steps) {
+__device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said) {
     using F = BwdShape<HD>;
     constexpr uint32_t id_a = make_idesc_bf16(128, HD, 0, 1);
     const uint64_t zd = make_smem_desc(base + F::OFF_Y, F::YREG, F::SBO, F::SWZ);   // Y's columns outermost
     const uint32_t z_lo = uint32_t(zd), z_hi = uint32_t(zd >> 32);
     const uint32_t yes = elect();
-    uint32_t heard = 0, passes = 0, flags, sl = 0;
-    for (uint32_t i = 0; bwd_hear<HD>(sy, steps, yes, heard, &flags); ++i) {
+    uint32_t passes = 0, sl = 0, par = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (!sy.wait_warp(sy.bar(F::B_FULL + sl), par)) break;
+        const uint32_t flags = __reduce_or_sync(kAll, said[sl]);
+        if (flags & kEnd) break;
         const uint32_t buf = DKV ? 0u : passes & 1u;
         if ((flags & kFirst) && !sy.wait_warp(sy.bar(F::B_AREAD + buf), ((DKV ? passes : passes >> 1) & 1u) ^ 1u)) break;
         if (!sy.wait_warp(sy.bar(F::B_PFULL + (i & 1u)), (i >> 1) & 1u)) break;
@@ -1191,7 +1190,7 @@ __device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint
             commit(yes, sy.bar(F::B_AFULL + buf));
             ++passes;
         }
-        if (++sl == F::STAGES) sl = 0;
+        if (++sl == F::STAGES) { sl = 0; par ^= 1u; }
     }
     commit(yes, sy.bar(F::B_DRAIN + 1));
     if (yes) drained(sy.bar(F::B_DRAIN + 1), 0);
@@ -1407,7 +1406,7 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::NBAR; ++i)
             mbar_init(sy.bar(i), (i >= F::B_PFULL && i < F::B_PFULL + 2) || (i >= F::B_AREAD && i < F::B_AREAD + 2) ? 4u
-                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 14u : 1u);
+                                 : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 12u : 1u);
         misc[1] = 0u;
         fence_mbar_init();
     }
@@ -1435,9 +1434,9 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
         bwd_out<HD, DKV>(p, sy, tmem, steps);
     } else {
         regs_decrease<kBwdLow>();
-        if (warp == 12) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, &tx0, &tx1, &ty0, &ty1);
-        if (warp == 13) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), steps);
-        if (warp == 14) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), steps);
+        if (warp == 12) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, misc + 2, &tx0, &tx1, &ty0, &ty1);
+        if (warp == 13) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
+        if (warp == 14) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
     }
     tc_fence_before();
     __syncthreads();
