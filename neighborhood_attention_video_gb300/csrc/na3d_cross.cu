@@ -727,6 +727,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
                 if (p.splits > 1) {   // in 32 bits
 #pragma unroll 1
                     for (int q = 0; q < (HD + 31) / 32; ++q) {
+                        __syncwarp();
                         float o[32];
                         tmem_ld32(t_lane + F::OW * a + 32 * q, o);
                         tmem_wait_ld();
@@ -741,27 +742,34 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sy.bar(F::B_OREAD + a));
                 } else {
-                    uint32_t kept[HD < 32 ? 16 : HD / 2];
+                    // 32 columns, or 64, to a round: the registers of a whole row are too many
+                    constexpr int Q = (HD + 31) / 32, N = Q < 2 ? Q : 2, COLS = HD < 64 ? HD : 64;
+#pragma unroll 1
+                    for (int c = 0; c < Q / N; ++c) {
+                        __syncwarp();
+                        uint32_t kept[16 * N];
 #pragma unroll
-                    for (int q = 0; q < (HD + 31) / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(t_lane + F::OW * a + 32 * q, o);
-                        tmem_wait_ld();
-                        behind_wait(o);
+                        for (int q = 0; q < N; ++q) {
+                            float o[32];
+                            tmem_ld32(t_lane + F::OW * a + 32 * (N * c + q), o);
+                            tmem_wait_ld();
+                            behind_wait(o);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) kept[16 * q + j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sy.bar(F::B_OREAD + a));   // the next pass's products may come
-                    if (mine) {
-                        uint16_t* const to = p.out + to_row * HD;
+                            for (int j = 0; j < 16; ++j) kept[16 * q + j] = pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                        }
+                        if (c == Q / N - 1) {   // the next pass's products may come
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(sy.bar(F::B_OREAD + a));
+                        }
+                        if (!mine) continue;
+                        uint16_t* const to = p.out + to_row * HD + 32 * N * c;
                         if (p.out_v8) {
 #pragma unroll
-                            for (int j = 0; j < HD / 16; ++j) st_global_v8(to + 16 * j, kept + 8 * j);
+                            for (int j = 0; j < COLS / 16; ++j) st_global_v8(to + 16 * j, kept + 8 * j);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < HD / 8; ++j)
+                            for (int j = 0; j < COLS / 8; ++j)
                                 reinterpret_cast<uint4*>(to)[j] = make_uint4(kept[4 * j], kept[4 * j + 1], kept[4 * j + 2], kept[4 * j + 3]);
                         }
                     }
