@@ -30,27 +30,45 @@ constexpr int kWarps = 8;
 // joined in this order, whatever the device.
 constexpr int kGradBlocks = 152 * 2;
 
-__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-
 struct Piece {   // 16 values of a head: two 16-byte pieces
     uint4 a, b;
 };
 
-__device__ __forceinline__ void unpack(const Piece& p, float (&f)[16]) {
+// ... as eight pairs of fp32 values, the arithmetic of which goes two at a time.
+__device__ __forceinline__ void unpack(const Piece& p, uint64_t (&f)[8]) {
     const uint32_t v[8] = {p.a.x, p.a.y, p.a.z, p.a.w, p.b.x, p.b.y, p.b.z, p.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        f[2 * i] = lo16(v[i]);
-        f[2 * i + 1] = hi16(v[i]);
-    }
+    for (int i = 0; i < 8; ++i) f[i] = f2_pack(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ Piece pack(const float (&f)[16]) {
+__device__ __forceinline__ Piece pack(const uint64_t (&f)[8]) {
     uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) {
+        float x, y;
+        f2_unpack(f[i], x, y);
+        v[i] = pack_bf16x2(x, y);
+    }
     return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The sum of the products of 16 values.
+__device__ __forceinline__ float dot(const uint64_t (&a)[8], const uint64_t (&b)[8]) {
+    uint64_t s = f2_mul(a[0], b[0]), t = f2_mul(a[1], b[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) {
+        s = f2_fma(a[i], b[i], s);
+        t = f2_fma(a[i + 1], b[i + 1], t);
+    }
+    float x, y;
+    f2_unpack(f2_add(s, t), x, y);
+    return x + y;
 }
 
 // Data that is used once: past L1, and the first to leave L2.
@@ -63,15 +81,27 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) {
 
 // The 16 values turned by the eight pairs' angles (DIR 1) or back (-1).
 template <bool INTER, int DIR>
-__device__ __forceinline__ void turn(float (&f)[16], const float2 (&cs)[8]) {
+__device__ __forceinline__ void turn(uint64_t (&f)[8], const float2 (&cs)[8]) {
+    if (INTER) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float &x = f[INTER ? 2 * i : i], &y = f[INTER ? 2 * i + 1 : 8 + i];
-        const float a = x, b = y, c = cs[i].x, s = DIR * cs[i].y;
-        x = a * c - b * s;
-        y = b * c + a * s;
+        for (int i = 0; i < 8; ++i) {
+            float a, b;
+            const float c = cs[i].x, s = DIR * cs[i].y;
+            f2_unpack(f[i], a, b);
+            f[i] = f2_pack(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t c = f2_pack(cs[2 * i].x, cs[2 * i + 1].x), s = f2_pack(DIR * cs[2 * i].y, DIR * cs[2 * i + 1].y);
+            const uint64_t n = f2_pack(-DIR * cs[2 * i].y, -DIR * cs[2 * i + 1].y), a = f[i], b = f[4 + i];
+            f[i] = f2_fma(a, c, f2_mul(b, n));
+            f[4 + i] = f2_fma(b, c, f2_mul(a, s));
+        }
     }
 }
+
+__device__ __forceinline__ uint32_t divided(uint32_t n, uint64_t by, int s) { return uint32_t((uint64_t(n) * by) >> s); }
 
 template <int LPH>
 __device__ __forceinline__ float sum_of_head(float v) {
@@ -85,9 +115,9 @@ __device__ __forceinline__ float sum_of_head(float v) {
 // A block takes tokens of q or of k (the first `q_blocks` along x those of q),
 // a warp one at a time; along y the heads are shared out where there are few
 // tokens. U: heads of a lane in flight.
-template <int HD, bool INTER, bool BWD>
+template <int HD, bool INTER, bool BWD, int U>
 __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __grid_constant__ RopeParams p, int q_blocks) {
-    constexpr int LPH = HD / 16, HPW = 32 / LPH, U = BWD ? 1 : 2;
+    constexpr int LPH = HD / 16, HPW = 32 / LPH;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPH, sub = lane / LPH;
     const bool is_k = int(blockIdx.x) >= q_blocks;
@@ -100,17 +130,22 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
     // the first of the pairs of either piece (the same four and four, INTER; else eight in a row)
     const int pa = INTER ? ca / 2 : apart ? ca : P, pb = INTER ? cb / 2 : pa + 4;
 
-    float wt[16];
+    uint64_t wt[8];   // weight and scale
     {
         const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
         const Piece wp = {d.w ? *reinterpret_cast<const uint4*>(d.w + ca) : one, d.w ? *reinterpret_cast<const uint4*>(d.w + cb) : one};
         unpack(wp, wt);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wt[i] = f2_mul(wt[i], f2_pack(d.scale, d.scale));
     }
-    float dw[BWD ? 16 : 1] = {};
+    uint64_t dw[BWD ? 8 : 1];   // without the scale
+#pragma unroll
+    for (int i = 0; i < (BWD ? 8 : 1); ++i) dw[i] = f2_pack(0.f, 0.f);
 
     for (int64_t token = int64_t(block) * kWarps + warp; token < p.tokens; token += int64_t(blocks) * kWarps) {
         const uint32_t place = uint32_t(token);   // below 2^31
-        const uint32_t th = place / uint32_t(p.W), w = place - th * p.W, t = th / uint32_t(p.H) % p.T, h = th % uint32_t(p.H);
+        const uint32_t th = divided(place, p.by_w, p.s_w), w = place - th * p.W;
+        const uint32_t bt = divided(th, p.by_h, p.s_h), h = th - bt * p.H, t = bt - divided(bt, p.by_t, p.s_t) * p.T;
         const float2* const of_t = p.table + t * uint32_t(p.PT);
         const float2* const of_h = p.table + uint32_t(p.T * p.PT) + h * p.PH - p.PT;
         const float2* const of_w = p.table + uint32_t(p.T * p.PT) + uint32_t(p.H * p.PH) + w * p.PW - p.PT - p.PH;
@@ -139,48 +174,41 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int head = h0 + u * HPW + sub;
-                float f[16];
+                uint64_t f[8];
+                bool live = true;
+                if (BWD) {
+                    // a row without a gradient (padding's) adds nothing, whatever x holds there
+                    const uint32_t bits = (g[u].a.x | g[u].a.y | g[u].a.z | g[u].a.w | g[u].b.x | g[u].b.y | g[u].b.z | g[u].b.w) & 0x7FFF7FFFu;
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, bits != 0u) >> (sub * LPH);
+                    live = (lanes & (0xffffffffu >> (32 - LPH))) != 0u;
+                    if (!live) x[u] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                }
                 unpack(x[u], f);
                 float r = 1.f;
-                if (p.norm) {
-                    float sq = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sq = fmaf(f[i], f[i], sq);
-                    r = rsqrtf(sum_of_head<LPH>(sq) * (1.f / HD) + d.eps);
-                }
+                if (p.norm) r = rsqrtf(sum_of_head<LPH>(dot(f, f)) * (1.f / HD) + d.eps);
+                const uint64_t r2 = f2_pack(r, r);
                 if (!BWD) {
-                    const float by = r * d.scale;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = f[i] * by * wt[i];
+                    for (int i = 0; i < 8; ++i) f[i] = f2_mul(f2_mul(f[i], r2), wt[i]);
                     turn<INTER, 1>(f, cs);
                 } else {
-                    float e[16];
+                    uint64_t e[8];
                     unpack(g[u], e);
                     turn<INTER, -1>(e, cs);
-                    bool any = false;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        e[i] *= d.scale;
-                        any |= e[i] != 0.f;
-                    }
-                    // a row without a gradient (padding's) adds nothing, whatever x holds there
-                    const uint32_t lanes = __ballot_sync(0xffffffffu, any) >> (sub * LPH);
-                    const bool live = (lanes & (0xffffffffu >> (32 - LPH))) != 0u;
                     if (p.norm) {
-                        float dot = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            f[i] = live ? f[i] * r : 0.f;
-                            dw[BWD ? i : 0] = fmaf(e[i], f[i], dw[BWD ? i : 0]);
-                            e[i] *= wt[i];
-                            dot = fmaf(e[i], f[i], dot);
+                        for (int i = 0; i < 8; ++i) {
+                            f[i] = f2_mul(f[i], r2);
+                            dw[BWD ? i : 0] = f2_fma(e[i], f[i], dw[BWD ? i : 0]);
+                            e[i] = f2_mul(e[i], wt[i]);
                         }
-                        dot = sum_of_head<LPH>(dot) * (1.f / HD);
+                        const float m = -sum_of_head<LPH>(dot(e, f)) * (1.f / HD);
+                        const uint64_t m2 = f2_pack(m, m);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = live ? r * fmaf(-f[i], dot, e[i]) : 0.f;
+                        for (int i = 0; i < 8; ++i) f[i] = f2_mul(r2, f2_fma(f[i], m2, e[i]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = e[i];
+                        for (int i = 0; i < 8; ++i) f[i] = f2_mul(e[i], wt[i]);
                     }
                 }
                 if (head < d.heads) {
@@ -195,11 +223,15 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
         // the block's sums: over the heads of a warp, then over the warps
         __shared__ float sums[kWarps][HD];
 #pragma unroll
-        for (int i = 0; i < (BWD ? 16 : 1); ++i) {
-            float v = dw[i];
+        for (int i = 0; i < (BWD ? 8 : 1); ++i) {
+            float v[2];
+            f2_unpack(dw[i], v[0], v[1]);
 #pragma unroll
-            for (int o = LPH; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (sub == 0) sums[warp][i < 8 ? ca + i : cb + i - 8] = v;
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int o = LPH; o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+                if (sub == 0) sums[warp][(i < 4 ? ca : cb - 8) + 2 * i + k] = v[k] * d.scale;
+            }
         }
         __syncthreads();
         float* const out = p.work + (int64_t(blockIdx.x) * gridDim.y + blockIdx.y) * HD;
@@ -266,9 +298,9 @@ int64_t rope_workspace(int64_t HD) { return int64_t(kGradBlocks) * HD * 4; }
 
 namespace {
 
-template <int HD, bool INTER, bool BWD>
+template <int HD, bool INTER, bool BWD, int U>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
-    constexpr int batch = 32 / (HD / 16) * (BWD ? 1 : 2);
+    constexpr int batch = 32 / (HD / 16) * U;
     const int NQ = p.side[0].heads, NK = p.side[1].heads;
     const int most = BWD ? kGradBlocks : sms * 3;
     const int64_t want = (p.tokens + kWarps - 1) / kWarps;   // blocks for each of q and k
@@ -278,7 +310,7 @@ cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     dim3 grid(unsigned(q_blocks + k_blocks));
     // few tokens: a token's heads over several blocks
     grid.y = unsigned(max(1, min((max(NQ, NK) + batch - 1) / batch, most / int(grid.x))));
-    norm_rope<HD, INTER, BWD><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
+    norm_rope<HD, INTER, BWD, U><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || !p.work) return e;
     norm_rope_sum<<<(HD + 31) / 32 * 2, 1024, 0, stream>>>(p.work, int(q_blocks * grid.y), int(grid.x * grid.y), HD,
@@ -286,9 +318,28 @@ cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// n / d as (n by) >> s, exact for n < 2^31: by exceeds 2^s / d by less than 1, and n times that
+// excess stays below 2^s / d, s being 31 more than the bits of d.
+void division(int32_t d, uint64_t* by, int32_t* s) {
+    *s = 31;
+    while ((int64_t(1) << (*s - 31)) < d) ++*s;
+    *by = (uint64_t(1) << *s) / uint32_t(d) + 1;
+}
+
+template <int HD, bool INTER, bool BWD>
+cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
+    // heads enough for two at a time
+    return max(p.side[0].heads, p.side[1].heads) > 32 / (HD / 16) ? launch<HD, INTER, BWD, 2>(p, sms, stream)
+                                                                  : launch<HD, INTER, BWD, 1>(p, sms, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_rope(int hd, const RopeParams& p, bool backward, int sms, cudaStream_t stream) {
+cudaError_t launch_rope(int hd, const RopeParams& args, bool backward, int sms, cudaStream_t stream) {
+    RopeParams p = args;
+    division(p.W, &p.by_w, &p.s_w);
+    division(p.H, &p.by_h, &p.s_h);
+    division(p.T, &p.by_t, &p.s_t);
 #define X(n) \
     if (hd == n) {                                                                                        \
         if (p.interleaved) return backward ? launch<n, true, true>(p, sms, stream) : launch<n, true, false>(p, sms, stream); \

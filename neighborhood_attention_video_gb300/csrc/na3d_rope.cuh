@@ -26,6 +26,8 @@ struct RopeParams {
     int32_t PT, PH, PW;       // pairs that turn with each axis
     int32_t norm, interleaved;
     float* work;              // backward: the blocks' sums of the weights' gradients
+    uint64_t by_w, by_h, by_t;   // n / W = (n by_w) >> s_w for n < 2^31, and so on (set by the launch)
+    int32_t s_w, s_h, s_t;
 };
 
 // Bytes of workspace of the backward pass with gradients of the weights.
