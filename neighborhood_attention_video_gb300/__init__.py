@@ -602,49 +602,61 @@ def na3d_rope_table(grid, rope_dims, theta=10000.0, offset=(0.0, 0.0, 0.0), scal
     return table
 
 
-def _head_rows(torch, dev, name, t, grid, heads, HD):
-    """t's token stride, t a bf16 view (*grid, heads, HD) on device `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
-        raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
-    if t.dim() != 6 or t.shape[:4] != grid or t.shape[5] != HD or (heads is not None and t.shape[4] != heads):
-        raise ValueError(f"{name} must have a 6-D (B,T,H,W,heads,HD) shape that goes with q's")
-    return _token_stride(name, t)
-
-
 def _rope_call(q, k, q_rows, k_rows, q_weight, k_weight, table, rope_dims):
     """What both directions of the norm and rotation check: (sizes, strides, weight and
     table pointers). q_rows, k_rows: the (name, tensor) of q's and k's shape besides q and k."""
     torch = _torch_module()
     dev = torch.cuda.current_device() if _cuda_ok else -2
-    if not isinstance(q, torch.Tensor):
+    Tensor, bf16 = torch.Tensor, torch.bfloat16
+    if not isinstance(q, Tensor):
         raise TypeError("q must be a torch.Tensor")
-    if q.dim() != 6:
-        raise ValueError("q must have a 6-D (B,T,H,W,NH,HD) shape")
     shape = q.shape
-    grid, NH, HD = shape[:4], shape[4], shape[5]
-    q_ts = [_head_rows(torch, dev, n, t, grid, NH, HD) for n, t in (("q", q), *q_rows)]
+    if len(shape) != 6:
+        raise ValueError("q must have a 6-D (B,T,H,W,NH,HD) shape")
+    B, T, H, W, NH, HD = shape
     if k is None:
-        if any(t is not None for _, t in k_rows) or k_weight is not None:
+        if k_weight is not None or any(t is not None for _, t in k_rows):
             raise ValueError("k's tensors need k")
-        NKV, k_ts = 0, [0] * len(q_ts)
+        k_shape, NKV = None, 0
+        sides = ((shape, (("q", q), *q_rows)),)
     else:
-        k_ts = [_head_rows(torch, dev, "k", k, grid, None, HD)]
-        NKV = k.shape[4]
-        k_ts += [_head_rows(torch, dev, n, t, grid, NKV, HD) for n, t in k_rows]
+        if not isinstance(k, Tensor):
+            raise TypeError("k must be a torch.Tensor")
+        k_shape = k.shape
+        if len(k_shape) != 6 or k_shape[:4] != shape[:4] or k_shape[5] != HD:
+            raise ValueError("k must have a 6-D (B,T,H,W,NKV,HD) shape that goes with q's")
+        NKV = k_shape[4]
+        sides = ((shape, (("q", q), *q_rows)), (k_shape, (("k", k), *k_rows)))
+    strides = []
+    for want, tensors in sides:
+        was = row = None
+        for name, t in tensors:
+            if not isinstance(t, Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype is not bf16 or t.get_device() != dev:
+                raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+            if t.shape != want:
+                raise ValueError(f"{name} must have the shape {tuple(want)}, not {tuple(t.shape)}")
+            st = t.stride()
+            if st != was:
+                was, row = st, _token_stride(name, t)
+            strides.append(row)
+    if k is None:
+        strides += [0] * len(strides)
+    n = len(strides) // 2
     RT, RH, RW = rope_dims
-    pointers = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check_one(torch, dev, name, w, torch.bfloat16, (HD,))
-        pointers.append(None if w is None else w.data_ptr())
+    pointers = [None, None, None]
+    if q_weight is not None:
+        _check_one(torch, dev, "q_weight", q_weight, bf16, (HD,))
+        pointers[0] = q_weight.data_ptr()
+    if k_weight is not None:
+        _check_one(torch, dev, "k_weight", k_weight, bf16, (HD,))
+        pointers[1] = k_weight.data_ptr()
     if table is not None:
-        rows = (grid[1] * RT + grid[2] * RH + grid[3] * RW) // 2
-        _check_one(torch, dev, "table", table, torch.float32, (rows, 2))
-    pointers.append(None if table is None else table.data_ptr())
-    sizes = (*grid, NH, NKV, HD, int(RT), int(RH), int(RW))
-    return sizes, [x for pair in zip(q_ts, k_ts) for x in pair], pointers
+        _check_one(torch, dev, "table", table, torch.float32, ((T * RT + H * RH + W * RW) // 2, 2))
+        pointers[2] = table.data_ptr()
+    sizes = (B, T, H, W, NH, NKV, HD, int(RT), int(RH), int(RW))
+    return sizes, [x for i in range(n) for x in (strides[i], strides[n + i])], pointers
 
 
 def _at(t):
