@@ -290,7 +290,10 @@ struct FwdShape : Geom<HD> {
     static constexpr int REG = 128 * G::ROWB, TILE = G::NREG * REG;
     static constexpr int SLOTS = HD == 128 ? 5 : 8;    // of k and v in turn
     static constexpr int OFF_KV = 2 * TILE, OFF_STEP = OFF_KV + SLOTS * TILE, OFF_BAR = OFF_STEP + kSteps * 48;
-    static constexpr int B_FULL = 0, B_EMPTY = SLOTS, B_QFULL = 2 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
+    // Steps until k's (and v's) slots come round. A slot's k and v have barriers of their own: who waits for
+    // the k's alone would take the phase of a v between them, still on its way, for one that is over.
+    static constexpr uint32_t CYCLE = SLOTS % 2 ? SLOTS : SLOTS / 2;
+    static constexpr int B_KFULL = 0, B_VFULL = SLOTS, B_EMPTY = 2 * SLOTS, B_QFULL = 3 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
                          B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_DONE = B_STAT + 2, B_TOLD = B_DONE + 4, B_HEARD = B_TOLD + kSteps,
                          B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 3;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the slots' flags
@@ -317,12 +320,12 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
 
     // One operand tile into the next slot, with its step's flags.
-    auto load = [&](const CUtensorMap* map, const Unit& U, int tile, uint32_t flags) -> bool {
+    auto load = [&](const CUtensorMap* map, int fulls, const Unit& U, int tile, uint32_t flags) -> bool {
         const uint32_t st = slot_n % F::SLOTS;
         if (!sy.wait_warp(sy.bar(F::B_EMPTY + st), ((slot_n / F::SLOTS) & 1u) ^ 1u)) return false;
         ++slot_n;
         if (lane == 0) {
-            const uint32_t full = sy.bar(F::B_FULL + st);
+            const uint32_t full = sy.bar(fulls + st);
             said[st] = flags;
             if (flags & kEnd) {
                 mbar_arrive(full);
@@ -414,7 +417,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                     }
                     if (__any_sync(kAll, gaps)) s.flags |= kForeign;
                 }
-                if (!tell(s) || !load(tk, U, f.tile, s.flags)) return false;
+                if (!tell(s) || !load(tk, F::B_KFULL, U, f.tile, s.flags)) return false;
                 if (first) {
                     for (int a = 0; a < (two ? 2 : 1); ++a) {
                         if (!sy.wait_warp(sy.bar(F::B_QEMPTY + a), (q_n[a] & 1u) ^ 1u)) return false;
@@ -427,21 +430,19 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                         }
                     }
                 }
-                if (!load(tv, U, f.tile, s.flags)) return false;
+                if (!load(tv, F::B_VFULL, U, f.tile, s.flags)) return false;
                 have = more;
                 f = g;
             }
         }
         const Unit none(p, 0);
-        return tell({kEnd, -1}) && load(tk, none, 0, kEnd) && load(tv, none, 0, kEnd);
+        return tell({kEnd, -1}) && load(tk, F::B_KFULL, none, 0, kEnd) && load(tv, F::B_VFULL, none, 0, kEnd);
     };
     run();
     // every issued load lands before the block may exit
     if (lane == 0) {
-        for (uint32_t s = 0; s < F::SLOTS; ++s) {
-            const uint32_t n = slot_n / F::SLOTS + (s < slot_n % F::SLOTS ? 1u : 0u);
-            if (n) drained(sy.bar(F::B_FULL + s), (n - 1u) & 1u);
-        }
+        for (uint32_t n = slot_n < F::SLOTS ? 0u : slot_n - F::SLOTS; n < slot_n; ++n)   // k's are even
+            drained(sy.bar((n & 1u ? F::B_VFULL : F::B_KFULL) + n % F::SLOTS), (n / 2u / F::CYCLE) & 1u);
         for (int a = 0; a < 2; ++a)
             if (q_n[a]) drained(sy.bar(F::B_QFULL + a), (q_n[a] - 1u) & 1u);
     }
@@ -454,17 +455,15 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
 // committed to costs an issuing warp some 100 cycles in which it issues nothing: one
 // warp for scores and products took 3600 cycles a step of HD 128, whose products are
 // 2048.)
-// The slots of k (V 0) or v (V 1) of one step after another.
+// The slots of k (from 0) or v (from 1) of one step after another, and the parity of their barriers.
 template <int SLOTS>
 struct Slot {
+    const uint32_t first;
     uint32_t st, par = 0;
-    __device__ __forceinline__ explicit Slot(uint32_t first) : st(first) {}
+    __device__ __forceinline__ explicit Slot(uint32_t at) : first(at), st(at) {}
     __device__ __forceinline__ void next() {
-        st += 2;
-        if (st >= SLOTS) {
-            st -= SLOTS;
-            par ^= 1u;
-        }
+        st = st + 2 < SLOTS ? st + 2 : st + 2 - SLOTS;
+        par ^= st == first ? 1u : 0u;
     }
 };
 
@@ -481,7 +480,7 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
     Slot<F::SLOTS> k(0);
     auto run = [&]() {
         for (;; k.next()) {
-            if (!sy.wait_warp(sy.bar(F::B_FULL + k.st), k.par)) return;
+            if (!sy.wait_warp(sy.bar(F::B_KFULL + k.st), k.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[k.st]);
             if (flags & kEnd) return;
             const bool mine = a == 0 || (flags & kTwo);
@@ -519,7 +518,7 @@ __device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint
     Slot<F::SLOTS> v(1);
     auto run = [&]() {
         for (;; v.next()) {
-            if (!sy.wait_warp(sy.bar(F::B_FULL + v.st), v.par)) return;
+            if (!sy.wait_warp(sy.bar(F::B_VFULL + v.st), v.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[v.st]);
             if (flags & kEnd) return;
             const int act = (flags & kTwo) ? 2 : 1;
@@ -653,7 +652,7 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
                     // this thread's column, where it is of another document: 0 times its value must be 0.
                     // Either row tile's warps do so before their product; both write the same zeros.
                     const uint32_t vs = slot_n - 1;
-                    if (!sy.wait_warp(sy.bar(F::B_FULL + vs % F::SLOTS), (vs / F::SLOTS) & 1u)) {
+                    if (!sy.wait_warp(sy.bar(F::B_VFULL + vs % F::SLOTS), (vs / 2u / F::CYCLE) & 1u)) {
                         tmem_wait_st();
                         return;
                     }

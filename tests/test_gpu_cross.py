@@ -210,6 +210,20 @@ def test_repeats_have_equal_bits():
             assert all(torch.equal(first[n], again[n]) for n in first)
 
 
+@pytest.mark.parametrize("L,S,NH,NKV", [(1, 40000, 16, 4), (300, 1300, 3, 3)])
+def test_long_runs_of_lone_row_tiles(L, S, NH, NKV):
+    """Blocks whose second row tile is empty, in some units or all, walk many column
+    tiles: over thousands of calls, which the operands reach in any order, the bits stay."""
+    q, kv, _ = make((5, 1, 1, L, NH, 128), S, NKV, 21)
+    q, kv = q.cuda(), kv.cuda()
+    first, lse = na.na3d_cross_attention(q, kv[:, :, 0], kv[:, :, 1], return_lse=True)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(3000):
+        out, other = na.na3d_cross_attention(q, kv[:, :, 0], kv[:, :, 1], return_lse=True)
+        differ += (out.view(torch.int16) != first.view(torch.int16)).sum() + (other != lse).sum()
+    assert int(differ) == 0 and na.na3d_device_status() == 0
+
+
 def test_two_streams_at_once():
     cases = [((1, 3, 10, 17, 4, 64), 250, 2), ((1, 1, 1, 1, 8, 128), 6000, 2)]
     data = [make(*c, seed) for seed, c in enumerate(cases)]
