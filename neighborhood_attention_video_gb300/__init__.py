@@ -139,11 +139,16 @@ def _torch_module():
     return _torch
 
 
+def _device() -> int:
+    """The current CUDA device, -2 where there is none (behind _torch_module())."""
+    return _torch._C._cuda_getDevice() if _cuda_ok else -2
+
+
 def _check_bf16_on_device(tensors):
     """Each (name, tensor) is a bf16 tensor on the current CUDA device: the
     kernels get raw pointers, so a host or other-device tensor must not pass."""
     torch = _torch_module()
-    dev = torch.cuda.current_device() if _cuda_ok else -2
+    dev = _device()
     for name, t in tensors:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -156,7 +161,7 @@ def _stream_handle(stream) -> int:
         torch = _torch_module()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(_device() if _cuda_ok else torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -315,7 +320,7 @@ def _check_on_device(tensors):
     """Each (name, tensor, dtype, shape) is a contiguous tensor of that dtype
     and shape on the current CUDA device."""
     torch = _torch_module()
-    dev = torch.cuda.current_device() if _cuda_ok else -2
+    dev = _device()
     for name, t, dtype, shape in tensors:
         _check_one(torch, dev, name, t, dtype, shape)
 
@@ -323,7 +328,7 @@ def _check_on_device(tensors):
 def _check_bf16_of_shape(shape, names, tensors):
     """The tensors are bf16, of one 6-D shape, on the current CUDA device."""
     torch = _torch_module()
-    dev, bf16 = torch.cuda.current_device() if _cuda_ok else -2, torch.bfloat16
+    dev, bf16 = _device(), torch.bfloat16
     for name, t in zip(names, tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -373,7 +378,7 @@ def _workspace(work, need, like, stream):
                 kept.clear()
             work = kept[key] = _empty(None, like, (need,), torch.uint8)
         return work
-    dev = torch.cuda.current_device() if _cuda_ok else -2
+    dev = _device()
     if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
         raise TypeError("work must be a contiguous tensor on the current CUDA device")
     if work.numel() * work.element_size() < need:
@@ -385,7 +390,7 @@ def _scored_options(shape, softcap, slopes, doc, prefix):
     """The score arguments of the na3d_scored_ calls, checked: (softcap, the
     three pointers or None)."""
     torch = _torch_module()
-    dev = torch.cuda.current_device() if _cuda_ok else -2
+    dev = _device()
     ps = pd = pp = None
     if slopes is not None:
         _check_one(torch, dev, "slopes", slopes, torch.float32, (shape[4], 3))
@@ -606,7 +611,7 @@ def _rope_call(q, k, q_rows, k_rows, q_weight, k_weight, table, rope_dims):
     """What both directions of the norm and rotation check: (sizes, strides, weight and
     table pointers). q_rows, k_rows: the (name, tensor) of q's and k's shape besides q and k."""
     torch = _torch_module()
-    dev = torch.cuda.current_device() if _cuda_ok else -2
+    dev = _device()
     Tensor, bf16 = torch.Tensor, torch.bfloat16
     if not isinstance(q, Tensor):
         raise TypeError("q must be a torch.Tensor")
@@ -732,34 +737,43 @@ def _state_stride(name, t) -> int:
 
 def _cross_call(q, rows, states, doc, kv_doc):
     """What both directions of the attention to other states check: (sizes, token
-    strides of the tensors, pointers of doc and kv_doc). rows: (name, tensor) like q;
-    states: (name, tensor) of k's shape, k first."""
+    strides of q, rows and states in turn, pointers of doc and kv_doc). rows: (name,
+    tensor) like q; states: (name, tensor) of k's shape, k first."""
     torch = _torch_module()
-    dev = torch.cuda.current_device() if _cuda_ok else -2
-    bf16 = torch.bfloat16
-    for name, t, dims in (*((n, t, 6) for n, t in (("q", q), *rows)), *((n, t, 4) for n, t in states)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not bf16 or t.get_device() != dev:
-            raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
-        if t.dim() != dims:
-            raise ValueError(f"{name} must be {dims}-D: q (B,T,H,W,NH,HD), k and v (B,S,NKV,HD)")
-    shape, k_shape = q.shape, states[0][1].shape
-    for name, t in rows:
-        if t.shape != shape:
-            raise ValueError(f"{name} must have the shape of q")
-    for name, t in states:
-        if t.shape != k_shape:
-            raise ValueError(f"{name} must have the shape of k")
-    if k_shape[0] != shape[0] or k_shape[3] != shape[5]:
-        raise ValueError("q and k must agree on B and HD")
-    pointers = []
-    for name, t, want in (("doc", doc, shape[:4]), ("kv_doc", kv_doc, k_shape[:2])):
-        if t is not None:
-            _check_one(torch, dev, name, t, torch.int32, want)
-        pointers.append(None if t is None else t.data_ptr())
+    dev = _device()
+    Tensor, bf16 = torch.Tensor, torch.bfloat16
+    k = states[0][1]
+    if not isinstance(q, Tensor) or not isinstance(k, Tensor):
+        raise TypeError("q and k must be a torch.Tensor")
+    shape, k_shape = q.shape, k.shape
+    strides = []
+    for want, dims, like, step, tensors in ((shape, 6, "q", _token_stride, (("q", q), *rows)),
+                                            (k_shape, 4, "k", _state_stride, states)):
+        if len(want) != dims:
+            raise ValueError(f"{like} must be {dims}-D: q (B,T,H,W,NH,HD), k and v (B,S,NKV,HD)")
+        was = row = None
+        for name, t in tensors:
+            if not isinstance(t, Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype is not bf16 or t.get_device() != dev:
+                raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+            if t.shape != want:
+                raise ValueError(f"{name} must have the shape of {like}")
+            st = t.stride()
+            if st != was:
+                was, row = st, step(name, t)
+            strides.append(row)
     B, T, H, W, NH, HD = shape
-    return (B, T * H * W, k_shape[1], NH, k_shape[2], HD), pointers
+    if k_shape[0] != B or k_shape[3] != HD:
+        raise ValueError("q and k must agree on B and HD")
+    at = [None, None]
+    if doc is not None:
+        _check_one(torch, dev, "doc", doc, torch.int32, (B, T, H, W))
+        at[0] = doc.data_ptr()
+    if kv_doc is not None:
+        _check_one(torch, dev, "kv_doc", kv_doc, torch.int32, (B, k_shape[1]))
+        at[1] = kv_doc.data_ptr()
+    return (B, T * H * W, k_shape[1], NH, k_shape[2], HD), strides, at
 
 
 def na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward=False) -> int:
@@ -770,15 +784,14 @@ def na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward=False)
     return need
 
 
-def _call_cross_fwd(q, k, v, out, lse, sizes, pointers, work, stream) -> None:
+def _call_cross_fwd(q, k, v, out, lse, sizes, strides, pointers, work, stream) -> None:
     """The call behind na3d_cross_fwd: all but work is checked."""
     lib = _lib if _lib is not None else load_library()
     need = lib.na3d_cross_workspace(*sizes, 0)
     if need > 0:
         work = _workspace(work, need, q, stream)
     rc = lib.na3d_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(work), *sizes,
-                            _token_stride("q", q), _state_stride("k", k), _state_stride("v", v), *pointers,
-                            _stream_handle(stream))
+                            *strides, *pointers, _stream_handle(stream))
     if rc != NA3D_OK:
         raise NA3DError(rc, "na3d_cross_fwd")
 
@@ -797,22 +810,22 @@ def na3d_cross_fwd(q, k, v, out, lse=None, doc=None, kv_doc=None, work=None, str
     this thread and the current stream; a call with a ``stream`` or under capture
     allocates its own). Autograd does not see the call: the gradients come from
     ``na3d_cross_bwd``."""
-    sizes, pointers = _cross_call(q, (("out", out),), (("k", k), ("v", v)), doc, kv_doc)
+    sizes, (q_ts, _, *kv_ts), pointers = _cross_call(q, (("out", out),), (("k", k), ("v", v)), doc, kv_doc)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     if lse is not None:
-        _check_on_device((("lse", lse, _torch.float32, q.shape[:5]),))
-    _call_cross_fwd(q, k, v, out, lse, sizes, pointers, work, stream)
+        _check_one(_torch, _device(), "lse", lse, _torch.float32, q.shape[:5])
+    _call_cross_fwd(q, k, v, out, lse, sizes, (q_ts, *kv_ts), pointers, work, stream)
 
 
 def na3d_cross_attention(q, k, v, doc=None, kv_doc=None, return_lse=False, stream=None):
     """``na3d_cross_fwd`` into a new tensor: returns out, or (out, lse) where
     ``return_lse`` is true (what ``na3d_cross_bwd`` needs)."""
     torch = _torch_module()
-    sizes, pointers = _cross_call(q, (), (("k", k), ("v", v)), doc, kv_doc)
+    sizes, strides, pointers = _cross_call(q, (), (("k", k), ("v", v)), doc, kv_doc)
     out = _empty(stream, q, q.shape, torch.bfloat16)
     lse = _empty(stream, q, q.shape[:-1], torch.float32) if return_lse else None
-    _call_cross_fwd(q, k, v, out, lse, sizes, pointers, None, stream)
+    _call_cross_fwd(q, k, v, out, lse, sizes, strides, pointers, None, stream)
     return (out, lse) if return_lse else out
 
 
@@ -823,17 +836,15 @@ def na3d_cross_bwd(q, k, v, out, lse, dout, dq, dk, dv, doc=None, kv_doc=None, w
     e.g. the blocks of a fused gradient. ``work``: a tensor of
     ``na3d_cross_workspace`` bytes with ``backward=True``, as there."""
     lib = _lib if _lib is not None else load_library()
-    sizes, pointers = _cross_call(q, (("out", out), ("dout", dout), ("dq", dq)),
-                                  (("k", k), ("v", v), ("dk", dk), ("dv", dv)), doc, kv_doc)
+    sizes, (q_ts, _, _, dq_ts, k_ts, v_ts, dk_ts, dv_ts), pointers = _cross_call(
+        q, (("out", out), ("dout", dout), ("dq", dq)), (("k", k), ("v", v), ("dk", dk), ("dv", dv)), doc, kv_doc)
     if not (out.is_contiguous() and dout.is_contiguous()):
         raise ValueError("out and dout must be contiguous")
-    _check_on_device((("lse", lse, _torch.float32, q.shape[:5]),))
+    _check_one(_torch, _device(), "lse", lse, _torch.float32, q.shape[:5])
     work = _workspace(work, max(0, lib.na3d_cross_workspace(*sizes, 1)), q, stream)
     rc = lib.na3d_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(), *sizes,
-                            *(_token_stride(n, t) if t.dim() == 6 else _state_stride(n, t)
-                              for n, t in (("q", q), ("k", k), ("v", v), ("dq", dq), ("dk", dk), ("dv", dv))),
-                            *pointers, _stream_handle(stream))
+                            q_ts, k_ts, v_ts, dq_ts, dk_ts, dv_ts, *pointers, _stream_handle(stream))
     if rc != NA3D_OK:
         raise NA3DError(rc, "na3d_cross_bwd")
 
