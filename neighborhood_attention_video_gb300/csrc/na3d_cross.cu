@@ -136,11 +136,17 @@ enum : uint32_t {
     kLast = 2,
     kUnitFirst = 4,   // of its row tiles
     kUnitLast = 8,
-    kTwo = 16,        // both row tiles are in the grid
+    kTile0 = 16,      // which row tiles the step is for
+    kTile1 = 512,
     kMasked = 32,     // some columns are masked ...
     kForeign = 64,    // ... for their document
     kNone = 128,      // the rows see no column at all
-    kEnd = 256        // no more rows
+    kEnd = 256,       // no more rows
+    // of forward passes, where the two row tiles may be one, which takes the steps in turns
+    kTileFirst = 1024,   // the first of the unit for its row tiles
+    kTileLast = 2048,
+    kPassLast = 4096,    // of the pass, for both row tiles (kLast: for the step's)
+    kJoin = 8192         // ... which both have taken steps of
 };
 constexpr int kSteps = 8;   // steps that the producer may be ahead in telling
 
@@ -262,6 +268,7 @@ struct FwdParams {
     int32_t L, S, NH, NKV, G, rpt;        // rpt: tokens of a row tile
     int32_t pairs, units, tiles, splits, per_split;   // pairs of row tiles of an entry; column tiles
     int32_t out_v8;
+    int32_t lone;                         // the grid has one row tile: both are that one
     const int32_t *doc, *kv_doc;
     uint16_t* out;
     float* lse;
@@ -383,25 +390,35 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 }
                 return false;
             };
-            const uint32_t base_flags = two ? uint32_t(kTwo) : 0u;
             const int64_t token0 = U.b * p.L + t0, row0 = token0 * p.NH + U.kh * p.G + (p.splits > 1 ? U.split * p.rows : 0);
-            Found f{k0, -1, false};
-            bool have = next(&f);
-            if (!have) {
-                if (!tell({base_flags | kNone | kUnitLast, -1, t0, 0, {}, row0, token0})) return false;
-                continue;
-            }
-            int was = -1;
-            for (bool first = true; have; first = false) {
+            auto behind = [&](const Found& f) {
                 Found g = f;
                 ++g.tile;
-                const bool more = next(&g);
-                Step s{base_flags, f.doc, t0, 0, {}, row0, token0};
-                if (f.doc != was) s.flags |= kFirst;
-                if (!more || g.doc != f.doc) s.flags |= kLast;
-                if (first) s.flags |= kUnitFirst;
-                if (!more) s.flags |= kUnitLast;
-                was = f.doc;
+                if (f.doc < 0 || !next(&g)) g.doc = -1;
+                return g;
+            };
+            // this step's tile, the next one's and the one's after that; document < 0: none
+            Found f{k0, -1, false};
+            if (!next(&f)) {
+                if (!tell({kNone | kUnitLast, -1, t0, 0, {}, row0, token0})) return false;
+                continue;
+            }
+            Found f1 = behind(f), f2 = behind(f1);
+            int was[2] = {-1, -1};   // documents of the last steps but one, and but none, of either row tile's
+            for (int n = 0; f.doc >= 0; ++n) {
+                const uint32_t tiles_of = !p.lone ? (two ? kTile0 | kTile1 : uint32_t(kTile0)) : n & 1 ? uint32_t(kTile1) : uint32_t(kTile0);
+                const int before = p.lone ? was[0] : was[1], after = p.lone ? f2.doc : f1.doc;   // of the same row tiles
+                const bool first = n < (p.lone ? 2 : 1);
+                Step s{tiles_of, f.doc, t0, 0, {}, row0, token0};
+                if (f.doc != before) s.flags |= kFirst;
+                if (f.doc != after) s.flags |= kLast;
+                if (f.doc != f1.doc) s.flags |= f.doc == was[1] ? kPassLast | kJoin : uint32_t(kPassLast);
+                if (n == 0) s.flags |= kUnitFirst;
+                if (f1.doc < 0) s.flags |= kUnitLast;
+                if (first) s.flags |= kTileFirst;
+                if (after < 0) s.flags |= kTileLast;
+                was[0] = was[1];
+                was[1] = f.doc;
                 if (plain && f.tile * 128 + 128 <= p.S) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s.mask[i] = kAll;
@@ -419,20 +436,22 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 }
                 if (!tell(s) || !load(tk, F::B_KFULL, U, f.tile, s.flags)) return false;
                 if (first) {
-                    for (int a = 0; a < (two ? 2 : 1); ++a) {
+                    for (int a = 0; a < 2; ++a) {
+                        if (!(tiles_of & (a ? kTile1 : kTile0))) continue;
                         if (!sy.wait_warp(sy.bar(F::B_QEMPTY + a), (q_n[a] & 1u) ^ 1u)) return false;
                         ++q_n[a];
                         if (lane == 0) {
                             const uint32_t full = sy.bar(F::B_QFULL + a);
                             mbar_arrive_expect_tx(full, p.rpt * p.G * HD * 2);
                             for (int r = 0; r < F::NREG; ++r)
-                                load_box(base + a * F::TILE + r * F::REG, tq, full, r * F::HDB, U.kh * p.G, t0 + a * p.rpt, int(U.b));
+                                load_box(base + a * F::TILE + r * F::REG, tq, full, r * F::HDB, U.kh * p.G, t0 + (p.lone ? 0 : a * p.rpt), int(U.b));
                         }
                     }
                 }
                 if (!load(tv, F::B_VFULL, U, f.tile, s.flags)) return false;
-                have = more;
-                f = g;
+                f = f1;
+                f1 = f2;
+                f2 = behind(f1);
             }
         }
         const Unit none(p, 0);
@@ -483,8 +502,8 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
             if (!sy.wait_warp(sy.bar(F::B_KFULL + k.st), k.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[k.st]);
             if (flags & kEnd) return;
-            const bool mine = a == 0 || (flags & kTwo);
-            if (mine && (flags & kUnitFirst) && !sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
+            const bool mine = flags & (a ? kTile1 : kTile0);
+            if (mine && (flags & kTileFirst) && !sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
             if (!mine) {
                 if (yes) mbar_arrive(sy.bar(F::B_EMPTY + k.st));
                 continue;
@@ -497,7 +516,7 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
                 commit(yes, sy.bar(F::B_SFULL + 2 * a + h));
             }
             ++n;
-            if (flags & kUnitLast) commit(yes, sy.bar(F::B_QEMPTY + a));
+            if (flags & kTileLast) commit(yes, sy.bar(F::B_QEMPTY + a));
             commit(yes, sy.bar(F::B_EMPTY + k.st));
         }
     };
@@ -521,11 +540,10 @@ __device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint
             if (!sy.wait_warp(sy.bar(F::B_VFULL + v.st), v.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[v.st]);
             if (flags & kEnd) return;
-            const int act = (flags & kTwo) ? 2 : 1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int h = i >> 1, a = i & 1;
-                if (a >= act) continue;
+                if (!(flags & (a ? kTile1 : kTile0))) continue;
                 if (h == 0 && (flags & kFirst) && !sy.wait_warp(sy.bar(F::B_OREAD + a), (o_n[a]++ & 1u) ^ 1u)) return;
                 if (!sy.wait_warp(sy.bar(F::B_PFULL + 2 * a + h), n[a] & 1u)) return;
                 tc_fence_after();
@@ -568,7 +586,7 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
         if (flags & kEnd) return;
         if (!(flags & kNone)) slot_n += 2;
-        if (!(flags & kNone) && (a == 0 || (flags & kTwo))) {
+        if (flags & (a ? kTile1 : kTile0)) {
             if (flags & kFirst) l = 0.f;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -691,6 +709,69 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
     int64_t row[2] = {-1, -1};   // of out; < 0: none
     int doc[2] = {-1, -1};
     bool written[2] = {false, false};
+    // One row tile that both have taken steps of: their sums joined, by references of their own.
+    auto out_joined = [&](uint32_t flags, bool mine, int64_t to_row) -> bool {
+        const bool has[2] = {(flags & (kTile0 | kJoin)) != 0, (flags & (kTile1 | kJoin)) != 0};
+        float2 st[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            if (!has[a]) continue;
+            const uint32_t n = passes[a]++;
+            if (!sy.wait_warp(sy.bar(F::B_STAT + a), n & 1u)) return false;
+            st[a] = stat[a * 128];
+            if (!sy.wait_warp(sy.bar(F::B_OFULL + a), n & 1u)) return false;
+        }
+        tc_fence_after();
+        const bool r0 = st[0].x != 0.f, r1 = st[1].x != 0.f;
+        const float ref = r0 && r1 ? fmaxf(st[0].y, st[1].y) : r0 ? st[0].y : st[1].y;
+        const float w0 = r0 ? exp2f(st[0].y - ref) : 0.f, w1 = r1 ? exp2f(st[1].y - ref) : 0.f;
+        const float l = st[0].x * w0 + st[1].x * w1, inv = r0 || r1 ? 1.f / l : 0.f, by0 = w0 * inv, by1 = w1 * inv;
+#pragma unroll 1
+        for (int q = 0; q < (HD + 31) / 32; ++q) {
+            __syncwarp();
+            float o[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+            if (has[0]) {
+                tmem_ld32(t_lane + 32 * q, o);
+                tmem_wait_ld();
+                behind_wait(o);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= by0;
+            if (has[1]) {
+                float x[32];
+                tmem_ld32(t_lane + F::OW + 32 * q, x);
+                tmem_wait_ld();
+                behind_wait(x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = fmaf(x[j], by1, o[j]);
+            }
+            if (!mine) continue;
+            constexpr int W = HD < 32 ? HD : 32;
+            if (p.splits > 1) {
+                float4* const to = reinterpret_cast<float4*>(p.part + to_row * HD + 32 * q);
+#pragma unroll
+                for (int j = 0; j < W / 4; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            } else {
+                uint4* const to = reinterpret_cast<uint4*>(p.out + to_row * HD + 32 * q);
+#pragma unroll
+                for (int j = 0; j < W / 8; ++j)
+                    to[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                       pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            for (int a = 0; a < 2; ++a)
+                if (has[a]) mbar_arrive(sy.bar(F::B_OREAD + a));
+        if (!mine) return false;
+        const float lse2 = r0 || r1 ? ref + log2f(l) : -INFINITY;
+        if (p.splits > 1) p.part_lse[to_row] = lse2;
+        else if (p.lse) p.lse[to_row] = lse2 * kLn2;
+        return true;
+    };
     for (;;) {
         const uint32_t e = heard % kSteps;
         if (!sy.wait_warp(sy.bar(F::B_TOLD + e), (heard / kSteps) & 1u)) return;
@@ -703,7 +784,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const int i = a * p.rpt + tok;
-                row[a] = tok < p.rpt && t0 + i < p.L ? row0 + int64_t(i) * p.NH + g : -1;
+                row[a] = tok < p.rpt && t0 + i < p.L && !(a && p.lone) ? row0 + int64_t(i) * p.NH + g : -1;
                 doc[a] = row[a] >= 0 && p.doc ? __ldg(p.doc + token0 + i) : 0;
                 written[a] = false;
             }
@@ -711,9 +792,11 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
         if (flags & kEnd) return;
-        if (flags & kLast) {
+        if (p.lone) {
+            if (flags & kPassLast) written[0] |= out_joined(flags, row[0] >= 0 && doc[0] == d, row[0]);
+        } else if (flags & kLast) {
 #pragma unroll 1
-            for (int a = 0; a < ((flags & kTwo) ? 2 : 1); ++a) {
+            for (int a = 0; a < ((flags & kTile1) ? 2 : 1); ++a) {
                 const int64_t to_row = a ? row[1] : row[0];
                 const bool mine = to_row >= 0 && (a ? doc[1] : doc[0]) == d;
                 const uint32_t n = a ? passes[1]++ : passes[0]++;
@@ -868,34 +951,52 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     }
 }
 
-// The splits of a row joined: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top).
+// The splits of a row joined: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top),
+// by `parts` groups of HD / 4 threads that take every so many-th split.
 template <int HD>
-__global__ void __launch_bounds__(256) cross_join(const FwdParams p) {
-    constexpr int PER = HD / 4;   // threads of a row
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / PER;
-    const int c = int(i % PER) * 4;
+__global__ void __launch_bounds__(256) cross_join(const FwdParams p, int parts) {
+    constexpr int PER = HD / 4;
+    __shared__ float4 sums[256];
+    __shared__ float weights[256];
+    const int rows = 256 / (PER * parts);   // of a block
+    const int group = threadIdx.x / PER, part = group % parts, c = threadIdx.x % PER * 4;
+    const int64_t row = int64_t(blockIdx.x) * rows + group / parts;
     wait_for_primary();
-    if (row >= p.rows) return;
-    float top = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * p.rows + row]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, o[4] = {};
+    const bool in = row < p.rows;
+    float top = -INFINITY, sum = 0.f, o[4] = {};
+    if (in) {
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        const float x = p.part_lse[s * p.rows + row];
-        if (x == -INFINITY) continue;   // nothing written
-        const float w = exp2f(x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(p.part + (s * p.rows + row) * HD + c);
-        sum += w;
-        o[0] = fmaf(w, v.x, o[0]);
-        o[1] = fmaf(w, v.y, o[1]);
-        o[2] = fmaf(w, v.z, o[2]);
-        o[3] = fmaf(w, v.w, o[3]);
+        for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * p.rows + row]);
+        if (top == -INFINITY) top = 0.f;
+#pragma unroll 4
+        for (int s = part; s < p.splits; s += parts) {
+            const float x = p.part_lse[s * p.rows + row];
+            if (x == -INFINITY) continue;   // nothing written
+            const float w = exp2f(x - top);
+            const float4 v = *reinterpret_cast<const float4*>(p.part + (s * p.rows + row) * HD + c);
+            sum += w;
+            o[0] = fmaf(w, v.x, o[0]);
+            o[1] = fmaf(w, v.y, o[1]);
+            o[2] = fmaf(w, v.z, o[2]);
+            o[3] = fmaf(w, v.w, o[3]);
+        }
+    }
+    sums[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
+    weights[threadIdx.x] = sum;
+    __syncthreads();
+    if (!in || part) return;
+    for (int i = 1; i < parts; ++i) {
+        const float4 v = sums[threadIdx.x + i * PER];
+        sum += weights[threadIdx.x + i * PER];
+        o[0] += v.x;
+        o[1] += v.y;
+        o[2] += v.z;
+        o[3] += v.w;
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
     *reinterpret_cast<uint2*>(p.out + row * HD + c) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (ref + log2f(sum)) * kLn2 : -INFINITY;
+    if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ backward
@@ -1547,6 +1648,7 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     p.tiles = int(pl.tiles);
     p.splits = int(pl.splits);
     p.per_split = int(pl.per_split);
+    p.lone = c.L <= pl.rpt && pl.per_split > 1;
     p.rows = int64_t(c.B) * c.L * c.NH;
     p.out_v8 = reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
     p.doc = c.doc;
@@ -1564,7 +1666,9 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     cross_fwd_tiles<HD><<<unsigned(units < sms ? units : sms), kFwdThreads, FwdShape<HD>::SMEM, stream>>>(tq, tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
-    return launch_after(cross_join<HD>, ceil_div(p.rows * (HD / 4), 256), 256, 0, stream, p);
+    int parts = 1;   // four splits to a group of threads, as far as a block's go
+    while (parts < 256 / (HD / 4) && parts * 4 < p.splits) parts *= 2;
+    return launch_after(cross_join<HD>, ceil_div(p.rows * (HD / 4) * parts, 256), 256, 0, stream, p, parts);
 }
 
 // How a backward pass is shared out: `units` row tiles over `tiles` column tiles each, in so

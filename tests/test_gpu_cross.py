@@ -75,6 +75,12 @@ CASES = [
     ((4, 1, 5, 5, 2, 64), 640, 2, 0, ""),
     ((1, 9, 10, 13, 1, 128), 383, 1, 0, ""),
     ((1, 1, 1, 600, 2, 16), 600, 2, 1, "runs"),
+    # one row tile, whose column tiles go by turns: passes of one, of an odd number, of none
+    ((2, 1, 1, 5, 8, 128), 1400, 2, 4, "runs"),
+    ((1, 1, 2, 20, 3, 64), 900, 1, 3, "scattered"),
+    ((1, 1, 1, 7, 4, 32), 385, 4, 0, ""),
+    ((2, 1, 1, 3, 2, 16), 20000, 1, 5, "runs"),
+    ((1, 1, 1, 1, 12, 64), 300000, 3, 0, ""),
     # many units of one column tile each to a block
     ((1, 8, 24, 32, 16, 128), 77, 16, 0, ""),
     ((2, 4, 24, 32, 16, 64), 20, 16, 2, "runs"),
