@@ -312,3 +312,44 @@ def test_gradients_are_differences():
         # every term of the sum is off by a few roundings: 4 half steps of its magnitude, in quadrature
         scale = float((grad.cpu().double() * step).norm())
         assert abs(want - have) <= 4 * 2.0 ** -8 * scale * 4, (name, want, have)
+
+
+def test_states_past_32_bits():
+    """A memory of more than 2^31 values: its last states alone are seen."""
+    S, n, NH, HD = 140000, 300, 64, 128
+    gen = torch.Generator("cuda").manual_seed(31)
+    kv = torch.empty((1, S, 2, NH, HD), dtype=BF16, device="cuda").normal_(generator=gen)
+    q, _, g = make((1, 1, 1, 2, NH, HD), 1, 1, 31)
+    kv_doc = torch.full((1, S), -1, dtype=torch.int32)
+    kv_doc[:, -n:] = 0
+    assert kv.numel() > 2 ** 31
+    end = kv[:, -n:].cpu()
+    want = ref.cross(q, end[:, :, 0], end[:, :, 1], dout=g)
+    k, v, q, g, kv_doc = kv[:, :, 0], kv[:, :, 1], q.cuda(), g.cuda(), kv_doc.cuda()
+    out, lse = na.na3d_cross_attention(q, k, v, kv_doc=kv_doc, return_lse=True)
+    dq, dkv = torch.empty_like(q), torch.full_like(kv, float("nan"))
+    na.na3d_cross_bwd(q, k, v, out, lse, g, dq, dkv[:, :, 0], dkv[:, :, 1], kv_doc=kv_doc)
+    got = dict(out=out, lse=lse, dq=dq, dk=dkv[:, -n:, 0], dv=dkv[:, -n:, 1])
+    for name in want:
+        check(name, got[name], want[name])
+    assert not dkv[:, :-n].any()
+
+
+def test_tokens_past_32_bits():
+    """More than 2^31 values of q: the last tokens are those of the tokens by themselves."""
+    L, n, S, NH, HD = 1100000, 300, 40, 16, 128
+    gen = torch.Generator("cuda").manual_seed(32)
+    q = torch.empty((1, 1, 1, L, NH, HD), dtype=BF16, device="cuda").normal_(std=HD ** -0.5, generator=gen)
+    _, kv, g = make((1, 1, 1, n, NH, HD), S, NH, 32)
+    assert q.numel() > 2 ** 31
+    want = ref.cross(q[:, :, :, -n:].cpu(), kv[:, :, 0], kv[:, :, 1], dout=g)
+    kv = kv.cuda()
+    k, v = kv[:, :, 0], kv[:, :, 1]
+    out, lse = na.na3d_cross_attention(q, k, v, return_lse=True)
+    dout, dq, dkv = torch.zeros_like(q), torch.empty_like(q), torch.empty_like(kv)
+    dout[:, :, :, -n:] = g.cuda()
+    na.na3d_cross_bwd(q, k, v, out, lse, dout, dq, dkv[:, :, 0], dkv[:, :, 1])
+    got = dict(out=out[:, :, :, -n:], lse=lse[:, :, :, -n:], dq=dq[:, :, :, -n:], dk=dkv[:, :, 0], dv=dkv[:, :, 1])
+    for name in want:
+        check(name, got[name], want[name])
+    assert not dq[:, :, :, :-n].any()

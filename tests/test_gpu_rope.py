@@ -179,3 +179,21 @@ def test_graph_streams_and_repeats():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(b[-1], want[1]))
+
+
+def test_past_32_bits():
+    """More than 2^31 values: the last frame's rows are those of the frame by itself."""
+    B, T, H, W, NH, HD, dims = 1, 34, 128, 128, 32, 128, (44, 42, 42)
+    shape, last = (B, T, H, W, NH, HD), (B, 1, H, W, NH, HD)
+    q = torch.empty(shape, dtype=BF16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(5))
+    out = torch.empty_like(q)
+    table = na.na3d_rope_table((T, H, W), dims)
+    na.na3d_norm_rope(q, None, out, None, table=table, rope_dims=dims)
+    want = torch.empty(last, dtype=BF16, device="cuda")
+    alone = dict(table=na.na3d_rope_table((1, H, W), dims, offset=(T - 1, 0, 0)), rope_dims=dims)
+    na.na3d_norm_rope(q[:, -1:], None, want, None, **alone)
+    assert torch.equal(out[:, -1:], want)
+    dq = torch.empty_like(q)
+    na.na3d_norm_rope_bwd(q, None, out, None, dq, None, table=table, rope_dims=dims)
+    na.na3d_norm_rope_bwd(q[:, -1:], None, out[:, -1:], None, want, None, **alone)
+    assert torch.equal(dq[:, -1:], want)
