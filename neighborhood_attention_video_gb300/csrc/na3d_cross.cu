@@ -952,12 +952,14 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
 }
 
 // The splits of a row joined: out = sum_s 2^(lse_s - top) out_s / sum_s 2^(lse_s - top),
-// by `parts` groups of HD / 4 threads that take every so many-th split.
+// by `parts` groups of HD / 4 threads, each of every so many-th split and by a
+// reference of its own. Bound by the latency of its loads: all of a group's are in
+// flight at once.
 template <int HD>
 __global__ void __launch_bounds__(256) cross_join(const FwdParams p, int parts) {
     constexpr int PER = HD / 4;
     __shared__ float4 sums[256];
-    __shared__ float weights[256];
+    __shared__ float2 weights[256];
     const int rows = 256 / (PER * parts);   // of a block
     const int group = threadIdx.x / PER, part = group % parts, c = threadIdx.x % PER * 4;
     const int64_t row = int64_t(blockIdx.x) * rows + group / parts;
@@ -965,38 +967,60 @@ __global__ void __launch_bounds__(256) cross_join(const FwdParams p, int parts) 
     const bool in = row < p.rows;
     float top = -INFINITY, sum = 0.f, o[4] = {};
     if (in) {
-#pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_lse[s * p.rows + row]);
-        if (top == -INFINITY) top = 0.f;
-#pragma unroll 4
-        for (int s = part; s < p.splits; s += parts) {
-            const float x = p.part_lse[s * p.rows + row];
-            if (x == -INFINITY) continue;   // nothing written
-            const float w = exp2f(x - top);
-            const float4 v = *reinterpret_cast<const float4*>(p.part + (s * p.rows + row) * HD + c);
-            sum += w;
-            o[0] = fmaf(w, v.x, o[0]);
-            o[1] = fmaf(w, v.y, o[1]);
-            o[2] = fmaf(w, v.z, o[2]);
-            o[3] = fmaf(w, v.w, o[3]);
+        for (int s0 = part; s0 < p.splits; s0 += 8 * parts) {
+            float x[8];
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int s = s0 + i * parts;
+                x[i] = s < p.splits ? p.part_lse[s * p.rows + row] : -INFINITY;
+                if (s < p.splits) v[i] = *reinterpret_cast<const float4*>(p.part + (s * p.rows + row) * HD + c);
+            }
+            float most = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, x[i]);
+            const float by = top == -INFINITY ? 0.f : exp2f(top - most);
+            sum *= by;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] *= by;
+            top = most;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (x[i] == -INFINITY) continue;   // nothing written there
+                const float w = exp2f(x[i] - top);
+                sum += w;
+                o[0] = fmaf(w, v[i].x, o[0]);
+                o[1] = fmaf(w, v[i].y, o[1]);
+                o[2] = fmaf(w, v[i].z, o[2]);
+                o[3] = fmaf(w, v[i].w, o[3]);
+            }
         }
     }
     sums[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
-    weights[threadIdx.x] = sum;
+    weights[threadIdx.x] = make_float2(top, sum);
     __syncthreads();
     if (!in || part) return;
+    float ref = top;
+    for (int i = 1; i < parts; ++i) ref = fmaxf(ref, weights[threadIdx.x + i * PER].x);
+    if (ref == -INFINITY) ref = 0.f;
+    const float by = exp2f(top - ref);
+    sum *= by;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] *= by;
     for (int i = 1; i < parts; ++i) {
         const float4 v = sums[threadIdx.x + i * PER];
-        sum += weights[threadIdx.x + i * PER];
-        o[0] += v.x;
-        o[1] += v.y;
-        o[2] += v.z;
-        o[3] += v.w;
+        const float2 x = weights[threadIdx.x + i * PER];
+        const float w = exp2f(x.x - ref);
+        sum = fmaf(w, x.y, sum);
+        o[0] = fmaf(w, v.x, o[0]);
+        o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]);
+        o[3] = fmaf(w, v.w, o[3]);
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
     *reinterpret_cast<uint2*>(p.out + row * HD + c) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (p.lse && c == 0) p.lse[row] = sum > 0.f || sum != sum ? (ref + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ backward
