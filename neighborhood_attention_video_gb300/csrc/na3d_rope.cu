@@ -114,14 +114,22 @@ __device__ __forceinline__ float sum_of_head(float v) {
 
 // A block takes tokens of q or of k (the first `q_blocks` along x those of q),
 // a warp one at a time; along y the heads are shared out where there are few
-// tokens. U: heads of a lane in flight.
-template <int HD, bool INTER, bool BWD, int U>
-__global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __grid_constant__ RopeParams p, int q_blocks) {
-    constexpr int LPH = HD / 16, HPW = 32 / LPH;
+// tokens. U: heads of a lane in flight. BOTH (U 2): a warp takes the heads of q and
+// those of k of its token, which a batch holds each.
+//
+// 49152 tokens, 16 heads of 128 each: 129 us, 6.2 TB/s (6.7 is a copy); backward
+// 202 us, 6.0 TB/s. 65536 tokens, 8 heads of 64 each: 53 us, 5.0 TB/s; backward 95
+// us, 4.2 TB/s: what a token takes before its few values (its place, its cosines)
+// is a good part of the instructions. Heads of 8 and 1: 44 us and 89 us.
+template <int HD, bool INTER, bool BWD, int U, bool BOTH>
+__global__ void __launch_bounds__(kWarps * 32, BWD || BOTH ? 2 : 3) norm_rope(const __grid_constant__ RopeParams p, int q_blocks) {
+    static_assert(!BOTH || (U == 2 && !BWD), "q and k at once");
+    constexpr int LPH = HD / 16, HPW = 32 / LPH, SIDES = BOTH ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPH, sub = lane / LPH;
     const bool is_k = int(blockIdx.x) >= q_blocks;
-    const RopeSide& d = p.side[is_k];
+    auto side = [&](int u) -> const RopeSide& { return p.side[BOTH ? u : is_k]; };
+    const RopeSide& d = side(0);
     const int block = is_k ? blockIdx.x - q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - q_blocks : q_blocks;
     // this lane's pieces: as halves of the rotated width lie apart, what does not turn behind them
     const int P = p.PT + p.PH + p.PW;
@@ -130,13 +138,15 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
     // the first of the pairs of either piece (the same four and four, INTER; else eight in a row)
     const int pa = INTER ? ca / 2 : apart ? ca : P, pb = INTER ? cb / 2 : pa + 4;
 
-    uint64_t wt[8];   // weight and scale
-    {
+    uint64_t wt[SIDES][8];   // weight and scale
+#pragma unroll
+    for (int s = 0; s < SIDES; ++s) {
+        const RopeSide& d = side(s);
         const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
         const Piece wp = {d.w ? *reinterpret_cast<const uint4*>(d.w + ca) : one, d.w ? *reinterpret_cast<const uint4*>(d.w + cb) : one};
-        unpack(wp, wt);
+        unpack(wp, wt[s]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wt[i] = f2_mul(wt[i], f2_pack(d.scale, d.scale));
+        for (int i = 0; i < 8; ++i) wt[s][i] = f2_mul(wt[s][i], f2_pack(d.scale, d.scale));
     }
     uint64_t dw[BWD ? 8 : 1];   // without the scale
 #pragma unroll
@@ -156,24 +166,28 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
             const float2* const of = j < p.PT ? of_t : j < p.PT + p.PH ? of_h : of_w;
             cs[i] = j < P ? __ldg(of + j) : make_float2(1.f, 0.f);
         }
-        const uint16_t* const x_row = d.x + token * d.x_ts;
-        const uint16_t* const g_row = BWD ? d.g + token * d.g_ts : nullptr;
-        uint16_t* const y_row = d.y + token * d.y_ts;
-        for (int h0 = int(blockIdx.y) * HPW * U; h0 < d.heads; h0 += int(gridDim.y) * HPW * U) {
+        const uint16_t *x_row[SIDES], *const g_row = BWD ? d.g + token * d.g_ts : nullptr;
+        uint16_t* y_row[SIDES];
+#pragma unroll
+        for (int s = 0; s < SIDES; ++s) {
+            x_row[s] = side(s).x + token * side(s).x_ts;
+            y_row[s] = side(s).y + token * side(s).y_ts;
+        }
+        for (int h0 = BOTH ? 0 : int(blockIdx.y) * HPW * U; BOTH ? h0 == 0 : h0 < d.heads; h0 += BOTH ? 1 : int(gridDim.y) * HPW * U) {
             Piece x[U], g[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int head = h0 + u * HPW + sub;
+                const int s = BOTH ? u : 0, head = h0 + (BOTH ? 0 : u * HPW) + sub;
                 x[u] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                 g[u] = x[u];
-                if (head < d.heads) {
-                    x[u] = {load16(x_row + head * HD + ca), load16(x_row + head * HD + cb)};
+                if (head < side(u).heads) {
+                    x[u] = {load16(x_row[s] + head * HD + ca), load16(x_row[s] + head * HD + cb)};
                     if (BWD) g[u] = {load16(g_row + head * HD + ca), load16(g_row + head * HD + cb)};
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int head = h0 + u * HPW + sub;
+                const int s = BOTH ? u : 0, head = h0 + (BOTH ? 0 : u * HPW) + sub;
                 uint64_t f[8];
                 bool live = true;
                 if (BWD) {
@@ -185,11 +199,11 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
                 }
                 unpack(x[u], f);
                 float r = 1.f;
-                if (p.norm) r = rsqrtf(sum_of_head<LPH>(dot(f, f)) * (1.f / HD) + d.eps);
+                if (p.norm) r = rsqrtf(sum_of_head<LPH>(dot(f, f)) * (1.f / HD) + side(u).eps);
                 const uint64_t r2 = f2_pack(r, r);
                 if (!BWD) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = f2_mul(f2_mul(f[i], r2), wt[i]);
+                    for (int i = 0; i < 8; ++i) f[i] = f2_mul(f2_mul(f[i], r2), wt[s][i]);
                     turn<INTER, 1>(f, cs);
                 } else {
                     uint64_t e[8];
@@ -200,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
                         for (int i = 0; i < 8; ++i) {
                             f[i] = f2_mul(f[i], r2);
                             dw[BWD ? i : 0] = f2_fma(e[i], f[i], dw[BWD ? i : 0]);
-                            e[i] = f2_mul(e[i], wt[i]);
+                            e[i] = f2_mul(e[i], wt[0][i]);
                         }
                         const float m = -sum_of_head<LPH>(dot(e, f)) * (1.f / HD);
                         const uint64_t m2 = f2_pack(m, m);
@@ -208,13 +222,13 @@ __global__ void __launch_bounds__(kWarps * 32, BWD ? 2 : 3) norm_rope(const __gr
                         for (int i = 0; i < 8; ++i) f[i] = f2_mul(r2, f2_fma(f[i], m2, e[i]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = f2_mul(e[i], wt[i]);
+                        for (int i = 0; i < 8; ++i) f[i] = f2_mul(e[i], wt[0][i]);
                     }
                 }
-                if (head < d.heads) {
+                if (head < side(u).heads) {
                     const Piece o = pack(f);
-                    *reinterpret_cast<uint4*>(y_row + head * HD + ca) = o.a;
-                    *reinterpret_cast<uint4*>(y_row + head * HD + cb) = o.b;
+                    *reinterpret_cast<uint4*>(y_row[s] + head * HD + ca) = o.a;
+                    *reinterpret_cast<uint4*>(y_row[s] + head * HD + cb) = o.b;
                 }
             }
         }
@@ -298,19 +312,26 @@ int64_t rope_workspace(int64_t HD) { return int64_t(kGradBlocks) * HD * 4; }
 
 namespace {
 
-template <int HD, bool INTER, bool BWD, int U>
+template <int HD, bool INTER, bool BWD, int U, bool BOTH>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     constexpr int batch = 32 / (HD / 16) * U;
     const int NQ = p.side[0].heads, NK = p.side[1].heads;
-    const int most = BWD ? kGradBlocks : sms * 3;
     const int64_t want = (p.tokens + kWarps - 1) / kWarps;   // blocks for each of q and k
-    // the blocks shared out by the heads of q and k
-    const int64_t most_q = NK ? min(max(int64_t(most) * NQ / (NQ + NK), int64_t(1)), int64_t(most - 1)) : most;
+    if (BOTH) {
+        const unsigned blocks = unsigned(min(want, int64_t(sms) * 2));
+        norm_rope<HD, INTER, BWD, U, BOTH><<<blocks, kWarps * 32, 0, stream>>>(p, int(blocks));
+        return cudaGetLastError();
+    }
+    const int most = BWD ? kGradBlocks : sms * 3;
+    // the blocks shared out by the batches of heads of q and k, a token's beginning as another batch
+    // of each (16 heads of 128 and 1: 89 us; by heads alone 288)
+    const int cost_q = 1 + (NQ + batch - 1) / batch, cost_k = 1 + (NK + batch - 1) / batch;
+    const int64_t most_q = NK ? min(max(int64_t(most) * cost_q / (cost_q + cost_k), int64_t(1)), int64_t(most - 1)) : most;
     const int q_blocks = int(min(want, most_q)), k_blocks = NK ? int(min(want, most - most_q)) : 0;
     dim3 grid(unsigned(q_blocks + k_blocks));
     // few tokens: a token's heads over several blocks
     grid.y = unsigned(max(1, min((max(NQ, NK) + batch - 1) / batch, most / int(grid.x))));
-    norm_rope<HD, INTER, BWD, U><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
+    norm_rope<HD, INTER, BWD, U, BOTH><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || !p.work) return e;
     norm_rope_sum<<<(HD + 31) / 32 * 2, 1024, 0, stream>>>(p.work, int(q_blocks * grid.y), int(grid.x * grid.y), HD,
@@ -328,9 +349,13 @@ void division(int32_t d, uint64_t* by, int32_t* s) {
 
 template <int HD, bool INTER, bool BWD>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
-    // heads enough for two at a time
-    return max(p.side[0].heads, p.side[1].heads) > 32 / (HD / 16) ? launch<HD, INTER, BWD, 2>(p, sms, stream)
-                                                                  : launch<HD, INTER, BWD, 1>(p, sms, stream);
+    // Heads enough for two batches at a time; else q's and k's at once, which reads a token's
+    // cosines once (8 heads of 64 each: 53 us, 64 by blocks of their own; of 8 and 1: 44, 161).
+    // Backward the second side's sums and weights do not fit the registers.
+    if (max(p.side[0].heads, p.side[1].heads) > 32 / (HD / 16)) return launch<HD, INTER, BWD, 2, false>(p, sms, stream);
+    if constexpr (!BWD)
+        if (p.side[1].heads) return launch<HD, INTER, BWD, 2, true>(p, sms, stream);
+    return launch<HD, INTER, BWD, 1, false>(p, sms, stream);
 }
 
 }  // namespace
