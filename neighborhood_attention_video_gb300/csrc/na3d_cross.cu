@@ -467,13 +467,6 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     }
 }
 
-// Three warps issue, the scores of either row tile and the products of both. The
-// scores of a step are two tiles of 64 columns in buffers of their own, which the
-// probabilities take over: a half's next scores follow when its product is through,
-// while the softmax works on the other half. (Each barrier that is waited for or
-// committed to costs an issuing warp some 100 cycles in which it issues nothing: one
-// warp for scores and products took 3600 cycles a step of HD 128, whose products are
-// 2048.)
 // The slots of k (from 0) or v (from 1) of one step after another, and the parity of their barriers.
 template <int SLOTS>
 struct Slot {
@@ -486,6 +479,13 @@ struct Slot {
     }
 };
 
+// Three warps issue, the scores of either row tile and the products of both. The
+// scores of a step are two tiles of 64 columns in buffers of their own, which the
+// probabilities take over: a half's next scores follow when its product is through,
+// while the softmax works on the other half. (Each barrier that is waited for or
+// committed to costs an issuing warp some 100 cycles in which it issues nothing: one
+// warp for scores and products took 3600 cycles a step of HD 128, whose products are
+// 2048.)
 template <int HD>
 __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said, int a) {
     using F = FwdShape<HD>;
@@ -882,6 +882,21 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
     }
 }
 
+// out and lse of the softmax over a stream of column tiles: s = q k^T into tensor
+// memory, p = 2^(s log2e - ref) back into its place in bf16, O += p v. A row keeps
+// its reference while its sums stay in range, so O is scaled anew only where they
+// do not. Where the grid has one row tile, the block's two are the same rows and
+// take the column tiles in turns: one chain of scores, softmax and products leaves
+// the block waiting (one token, 16 heads of 128 over 65536 states of 4 heads: 40 us
+// by one, 33 by two). Few rows share their states out over blocks as well.
+//
+// Bound by the chain of its warps: each half of a step passes from the scores to
+// the softmax to the products and back, and every hand-over costs some 170 to 230
+// cycles. 49152 tokens, 16 heads of 128 over 512 states: 185 us, 1.11 PFLOP/s, tensor
+// cores 61 % busy; 24576 over 6144: 896 us, 1.38 PFLOP/s, 74 % (1.93 is a large
+// product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
+// states of 4 heads 6.6 TB/s; below it by the chain (64: 3.9 TB/s).
+//
 // Two row tiles to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  the softmax of either row tile;
 //   warps 8..11       results on their way out;
@@ -1076,7 +1091,7 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 
 // -lse log2e and -delta of every row of q, HD / 8 lanes to a row. Bound by the
-// read of out and dout. A row that sees nothing gets -infinity: its powers are 0.
+// read of out and dout (24576 tokens, 16 heads of 128: 37 us, 5.6 TB/s). A row that sees nothing gets -infinity: its powers are 0.
 template <int HD>
 __global__ void __launch_bounds__(256) cross_stat(const BwdParams p, int64_t rows) {
     constexpr int PER = HD / 8;
@@ -1511,6 +1526,12 @@ __device__ __forceinline__ void bwd_out(const BwdParams& p, const Sync& sy, uint
     }
 }
 
+// Seven products in the two passes, where one pass would make five: s and dp are
+// made anew, so that each sum stays in one block's tensor memory, no gradient needs
+// an atomic, and equal inputs give equal bits. Bound as the forward pass is: 24576
+// tokens, 16 heads of 128 over 512 states, dq 157 us (0.98 PFLOP/s, tensor cores
+// 62 % busy), dk and dv 168 us (1.23, 66 %).
+//
 // One row tile to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  every second step's probabilities each;
 //   warps 8..11       results on their way out;
@@ -1578,7 +1599,8 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
     }
 }
 
-// The splits of a gradient summed in order. grads: 1 (dq) or 2 (dv, dk).
+// The splits of a gradient summed in order, bound by their read (7 splits of dk and
+// dv of 512 states, 16 heads of 128: 59 MB in 14 us). grads: 1 (dq) or 2 (dv, dk).
 template <int HD>
 __global__ void __launch_bounds__(256) cross_sum(const BwdParams p, int grads) {
     constexpr int PER = HD / 4;
