@@ -10,6 +10,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -690,9 +691,14 @@ def na3d_norm_rope(q, k, q_out, k_out, q_weight=None, k_weight=None, table=None,
         raise NA3DError(rc, "na3d_norm_rope")
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_need(head_dim) -> int:
+    return load_library().na3d_norm_rope_workspace(head_dim)
+
+
 def na3d_norm_rope_workspace(head_dim) -> int:
     """Bytes of workspace that ``na3d_norm_rope_bwd`` uses for the weights' gradients."""
-    need = int(load_library().na3d_norm_rope_workspace(int(head_dim)))
+    need = _rope_need(int(head_dim))
     if need < 0:
         raise ValueError("head_dim must be a power of two from 16 to 512")
     return need
@@ -712,10 +718,11 @@ def na3d_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=N
     lib = _lib if _lib is not None else load_library()
     sizes, strides, at = _rope_call(q, k, (("dq_out", dq_out), ("dq", dq)), (("dk_out", dk_out), ("dk", dk)), q_weight,
                                     k_weight, table, rope_dims)
-    _check_on_device([(n, w, _torch.float32, (sizes[6],)) for n, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight))
-                      if w is not None])
     if dq_weight is not None or dk_weight is not None:
-        work = _workspace(work, max(0, lib.na3d_norm_rope_workspace(sizes[6])), q, stream)
+        for name, w in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+            if w is not None:
+                _check_one(_torch, _device(), name, w, _torch.float32, (sizes[6],))
+        work = _workspace(work, max(0, _rope_need(sizes[6])), q, stream)
     rc = lib.na3d_norm_rope_bwd(q.data_ptr(), _at(k), dq_out.data_ptr(), _at(dk_out), dq.data_ptr(), _at(dk),
                                 _at(dq_weight), _at(dk_weight), *at, _at(work), *sizes, *strides, 1 if norm else 0, q_eps,
                                 k_eps, q_scale, 1 if interleaved else 0, _stream_handle(stream))
@@ -746,24 +753,23 @@ def _cross_call(q, rows, states, doc, kv_doc):
     if not isinstance(q, Tensor) or not isinstance(k, Tensor):
         raise TypeError("q and k must be a torch.Tensor")
     shape, k_shape = q.shape, k.shape
-    strides = []
-    for want, dims, like, step, tensors in ((shape, 6, "q", _token_stride, (("q", q), *rows)),
-                                            (k_shape, 4, "k", _state_stride, states)):
-        if len(want) != dims:
-            raise ValueError(f"{like} must be {dims}-D: q (B,T,H,W,NH,HD), k and v (B,S,NKV,HD)")
-        was = row = None
-        for name, t in tensors:
-            if not isinstance(t, Tensor):
-                raise TypeError(f"{name} must be a torch.Tensor")
-            if t.dtype is not bf16 or t.get_device() != dev:
-                raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
-            if t.shape != want:
-                raise ValueError(f"{name} must have the shape of {like}")
-            st = t.stride()
-            if st != was:
-                was, row = st, step(name, t)
-            strides.append(row)
+    if len(shape) != 6 or len(k_shape) != 4:
+        raise ValueError("q must be 6-D (B,T,H,W,NH,HD), k and v 4-D (B,S,NKV,HD)")
     B, T, H, W, NH, HD = shape
+    strides, row, want, was = [], _token_stride, shape, None
+    for name, t in (("q", q), *rows, *states):
+        if t is k:
+            row, want, was = _state_stride, k_shape, None
+        if not isinstance(t, Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not bf16 or t.get_device() != dev:
+            raise TypeError(f"{name} must be a bfloat16 tensor on the current CUDA device")
+        if t.shape != want:
+            raise ValueError(f"{name} must have the shape of {'q' if want is shape else 'k'}")
+        st = t.stride()
+        if st != was:
+            was, step = st, row(name, t)
+        strides.append(step)
     if k_shape[0] != B or k_shape[3] != HD:
         raise ValueError("q and k must agree on B and HD")
     at = [None, None]
@@ -774,6 +780,12 @@ def _cross_call(q, rows, states, doc, kv_doc):
         _check_one(torch, dev, "kv_doc", kv_doc, torch.int32, (B, k_shape[1]))
         at[1] = kv_doc.data_ptr()
     return (B, T * H * W, k_shape[1], NH, k_shape[2], HD), strides, at
+
+
+@functools.lru_cache(maxsize=256)
+def _cross_need(B, L, S, num_heads, kv_heads, head_dim, backward) -> int:
+    """What the library answers of these sizes (asking takes a microsecond of a call's twenty)."""
+    return load_library().na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward)
 
 
 def na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward=False) -> int:
@@ -787,7 +799,7 @@ def na3d_cross_workspace(B, L, S, num_heads, kv_heads, head_dim, backward=False)
 def _call_cross_fwd(q, k, v, out, lse, sizes, strides, pointers, work, stream) -> None:
     """The call behind na3d_cross_fwd: all but work is checked."""
     lib = _lib if _lib is not None else load_library()
-    need = lib.na3d_cross_workspace(*sizes, 0)
+    need = _cross_need(*sizes, 0)
     if need > 0:
         work = _workspace(work, need, q, stream)
     rc = lib.na3d_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), _at(work), *sizes,
@@ -823,8 +835,9 @@ def na3d_cross_attention(q, k, v, doc=None, kv_doc=None, return_lse=False, strea
     ``return_lse`` is true (what ``na3d_cross_bwd`` needs)."""
     torch = _torch_module()
     sizes, strides, pointers = _cross_call(q, (), (("k", k), ("v", v)), doc, kv_doc)
-    out = _empty(stream, q, q.shape, torch.bfloat16)
-    lse = _empty(stream, q, q.shape[:-1], torch.float32) if return_lse else None
+    shape, device = q.shape, q.device
+    out = _empty_on(stream, device, shape, torch.bfloat16)
+    lse = _empty_on(stream, device, shape[:5], torch.float32) if return_lse else None
     _call_cross_fwd(q, k, v, out, lse, sizes, strides, pointers, None, stream)
     return (out, lse) if return_lse else out
 
@@ -841,7 +854,7 @@ def na3d_cross_bwd(q, k, v, out, lse, dout, dq, dk, dv, doc=None, kv_doc=None, w
     if not (out.is_contiguous() and dout.is_contiguous()):
         raise ValueError("out and dout must be contiguous")
     _check_one(_torch, _device(), "lse", lse, _torch.float32, q.shape[:5])
-    work = _workspace(work, max(0, lib.na3d_cross_workspace(*sizes, 1)), q, stream)
+    work = _workspace(work, max(0, _cross_need(*sizes, 1)), q, stream)
     rc = lib.na3d_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), work.data_ptr(), *sizes,
                             q_ts, k_ts, v_ts, dq_ts, dk_ts, dv_ts, *pointers, _stream_handle(stream))
