@@ -313,13 +313,14 @@ struct FwdShape : Geom<HD> {
 
 constexpr int kFwdThreads = 512;
 // registers: what the softmax, the way out and the rest take of 512 x 128
-constexpr uint32_t kRegsSoftmax = 160, kRegsOut = 112, kRegsLow = 80;
+constexpr uint32_t kRegsSoftmax = 160, kRegsOut = 104, kRegsLow = 88;
 static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
 
-template <int HD>
+template <int HD, bool FEW>
 __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, volatile uint32_t* said, const CUtensorMap* tq,
                                              const CUtensorMap* tk, const CUtensorMap* tv) {
     using F = FwdShape<HD>;
+    const bool lone = FEW && p.lone;
     const int lane = threadIdx.x & 31;
     Tiles tiles{{p.kv_doc, p.S}, 128};
     const Docs rows{p.doc, p.L};
@@ -406,9 +407,9 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
             Found f1 = behind(f), f2 = behind(f1);
             int was[2] = {-1, -1};   // documents of the last steps but one, and but none, of either row tile's
             for (int n = 0; f.doc >= 0; ++n) {
-                const uint32_t tiles_of = !p.lone ? (two ? kTile0 | kTile1 : uint32_t(kTile0)) : n & 1 ? uint32_t(kTile1) : uint32_t(kTile0);
-                const int before = p.lone ? was[0] : was[1], after = p.lone ? f2.doc : f1.doc;   // of the same row tiles
-                const bool first = n < (p.lone ? 2 : 1);
+                const uint32_t tiles_of = !lone ? (two ? kTile0 | kTile1 : uint32_t(kTile0)) : n & 1 ? uint32_t(kTile1) : uint32_t(kTile0);
+                const int before = lone ? was[0] : was[1], after = lone ? f2.doc : f1.doc;   // of the same row tiles
+                const bool first = n < (lone ? 2 : 1);
                 Step s{tiles_of, f.doc, t0, 0, {}, row0, token0};
                 if (f.doc != before) s.flags |= kFirst;
                 if (f.doc != after) s.flags |= kLast;
@@ -444,7 +445,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                             const uint32_t full = sy.bar(F::B_QFULL + a);
                             mbar_arrive_expect_tx(full, p.rpt * p.G * HD * 2);
                             for (int r = 0; r < F::NREG; ++r)
-                                load_box(base + a * F::TILE + r * F::REG, tq, full, r * F::HDB, U.kh * p.G, t0 + (p.lone ? 0 : a * p.rpt), int(U.b));
+                                load_box(base + a * F::TILE + r * F::REG, tq, full, r * F::HDB, U.kh * p.G, t0 + (lone ? 0 : a * p.rpt), int(U.b));
                         }
                     }
                 }
@@ -698,9 +699,10 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
 // The sums of a pass on their way out, by warps of their own: the softmax goes on
 // with the next rows meanwhile. (With its own threads' stores in its way a unit of
 // four steps took 11.3 us, 7.8 of them its steps.)
-template <int HD>
+template <int HD, bool FEW>
 __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
     using F = FwdShape<HD>;
+    const bool lone = FEW && p.lone, split = FEW && p.splits > 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + F::TM_O;
     const float2* const stat = reinterpret_cast<const float2*>(base_ptr + F::OFF_STAT) + r;
@@ -749,7 +751,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
             }
             if (!mine) continue;
             constexpr int W = HD < 32 ? HD : 32;
-            if (p.splits > 1) {
+            if (split) {
                 float4* const to = reinterpret_cast<float4*>(p.part + to_row * HD + 32 * q);
 #pragma unroll
                 for (int j = 0; j < W / 4; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
@@ -768,7 +770,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
                 if (has[a]) mbar_arrive(sy.bar(F::B_OREAD + a));
         if (!mine) return false;
         const float lse2 = r0 || r1 ? ref + log2f(l) : -INFINITY;
-        if (p.splits > 1) p.part_lse[to_row] = lse2;
+        if (split) p.part_lse[to_row] = lse2;
         else if (p.lse) p.lse[to_row] = lse2 * kLn2;
         return true;
     };
@@ -784,7 +786,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const int i = a * p.rpt + tok;
-                row[a] = tok < p.rpt && t0 + i < p.L && !(a && p.lone) ? row0 + int64_t(i) * p.NH + g : -1;
+                row[a] = tok < p.rpt && t0 + i < p.L && !(a && lone) ? row0 + int64_t(i) * p.NH + g : -1;
                 doc[a] = row[a] >= 0 && p.doc ? __ldg(p.doc + token0 + i) : 0;
                 written[a] = false;
             }
@@ -792,7 +794,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
         if (flags & kEnd) return;
-        if (p.lone) {
+        if (lone) {
             if (flags & kPassLast) written[0] |= out_joined(flags, row[0] >= 0 && doc[0] == d, row[0]);
         } else if (flags & kLast) {
 #pragma unroll 1
@@ -806,7 +808,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
                 const float inv = real ? 1.f / st.x : 0.f;
                 if (!sy.wait_warp(sy.bar(F::B_OFULL + a), n & 1u)) return;
                 tc_fence_after();
-                if (p.splits > 1) {   // in 32 bits
+                if (split) {   // in 32 bits
 #pragma unroll 1
                     for (int q = 0; q < (HD + 31) / 32; ++q) {
                         __syncwarp();
@@ -858,7 +860,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
                 }
                 if (mine) {
                     const float lse2 = real ? st.y + log2f(st.x) : -INFINITY;
-                    if (p.splits > 1) p.part_lse[to_row] = lse2;
+                    if (split) p.part_lse[to_row] = lse2;
                     else if (p.lse) p.lse[to_row] = lse2 * kLn2;
                     if (a) written[1] = true;
                     else written[0] = true;
@@ -869,7 +871,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 if (row[a] < 0 || written[a]) continue;   // else a row that sees nothing
-                if (p.splits > 1) {
+                if (split) {
                     p.part_lse[row[a]] = -INFINITY;
                 } else {
                     uint4* const to = reinterpret_cast<uint4*>(p.out + row[a] * HD);
@@ -892,18 +894,22 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 //
 // Bound by the chain of its warps: each half of a step passes from the scores to
 // the softmax to the products and back, and every hand-over costs some 170 to 230
-// cycles. 49152 tokens, 16 heads of 128 over 512 states: 185 us, 1.11 PFLOP/s, tensor
-// cores 61 % busy; 24576 over 6144: 896 us, 1.38 PFLOP/s, 74 % (1.93 is a large
-// product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
+// cycles. 49152 tokens, 16 heads of 128 over 512 states: 178 us, 1.16 PFLOP/s, tensor
+// cores 61 % busy; 24576 over 6144: 870 to 905 us, 1.4 PFLOP/s, 74 % (1.93 is a
+// large product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
 // states of 4 heads 6.6 TB/s; below it by the chain (64: 3.9 TB/s).
 //
 // Two row tiles to a block, one block to an SM, persistent:
+// FEW: row tiles so few that the states are split, or one alone. What that takes is
+// left out of the kernel for the rest, whose warps of five kinds share little room
+// for instructions (49152 tokens over 512 states 185 -> 178 us, frames 949 -> 905).
+//
 //   warps 0..3, 4..7  the softmax of either row tile;
 //   warps 8..11       results on their way out;
 //   warp 12           finds the column tiles that the rows see, TMA;
 //   warps 13, 14      issue the scores of either row tile; 13 owns the tensor memory;
 //   warp 15           issues the products.
-template <int HD>
+template <int HD, bool FEW>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const __grid_constant__ FwdParams p) {
@@ -951,10 +957,10 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         fwd_softmax<HD>(sy, base, base_ptr, tmem, steps);
     } else if (warp < 12) {
         regs_decrease<kRegsOut>();
-        fwd_out<HD>(p, sy, base_ptr, tmem, steps);
+        fwd_out<HD, FEW>(p, sy, base_ptr, tmem, steps);
     } else {
         regs_decrease<kRegsLow>();
-        if (warp == 12) fwd_producer<HD>(p, sy, base, steps, misc + 2, &tq, &tk, &tv);
+        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, steps, misc + 2, &tq, &tk, &tv);
         if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2, warp - 13);
         if (warp == 15) fwd_products<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
     }
@@ -1081,7 +1087,7 @@ struct BwdShape : Geom<HD> {
 };
 
 constexpr int kBwdThreads = 512;
-constexpr uint32_t kBwdSoftmax = 160, kBwdOut = 112, kBwdLow = 80;   // of 512 x 128
+constexpr uint32_t kBwdSoftmax = 160, kBwdOut = 104, kBwdLow = 88;   // of 512 x 128
 static_assert(2 * kBwdSoftmax + kBwdOut + kBwdLow <= 4 * 128, "register split");
 
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
@@ -1091,28 +1097,39 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 
 // -lse log2e and -delta of every row of q, HD / 8 lanes to a row. Bound by the
-// read of out and dout (24576 tokens, 16 heads of 128: 37 us, 5.6 TB/s). A row that sees nothing gets -infinity: its powers are 0.
+// read of out and dout (24576 tokens, 16 heads of 128: some 34 us, 6 TB/s). A row that sees nothing gets -infinity: its powers are 0.
+constexpr int kStatLoads = 4;   // of either tensor to a thread, in flight at once
+
 template <int HD>
 __global__ void __launch_bounds__(256) cross_stat(const BwdParams p, int64_t rows) {
     constexpr int PER = HD / 8;
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, row = i / PER;
+    const int64_t first = int64_t(blockIdx.x) * (256 * kStatLoads) + threadIdx.x;
     dependents_may_start();
-    const bool in = row < rows;
-    float sum = 0.f;
-    if (in) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p.out + i * 8), y = *reinterpret_cast<const uint4*>(p.dout + i * 8);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    uint4 x[kStatLoads], y[kStatLoads];
+    float lse[kStatLoads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            sum = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(v[k] << 16), sum);
-            sum = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(v[k] & 0xffff0000u), sum);
-        }
+    for (int k = 0; k < kStatLoads; ++k) {
+        const int64_t i = first + 256 * k, row = i / PER;
+        x[k] = y[k] = make_uint4(0, 0, 0, 0);
+        lse[k] = 0.f;
+        if (row >= rows) continue;
+        x[k] = __ldcs(reinterpret_cast<const uint4*>(p.out + i * 8));
+        y[k] = *reinterpret_cast<const uint4*>(p.dout + i * 8);
+        if (i % PER == 0) lse[k] = p.lse[row];
     }
 #pragma unroll
-    for (int o = PER / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (in && i % PER == 0) {
-        const float lse = p.lse[row];
-        p.stat[row] = make_float2(lse == -INFINITY ? -INFINITY : -lse * kLog2e, -sum);
+    for (int k = 0; k < kStatLoads; ++k) {
+        const int64_t i = first + 256 * k, row = i / PER;
+        const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum = fmaf(__uint_as_float(u[j] << 16), __uint_as_float(v[j] << 16), sum);
+            sum = fmaf(__uint_as_float(u[j] & 0xffff0000u), __uint_as_float(v[j] & 0xffff0000u), sum);
+        }
+#pragma unroll
+        for (int o = PER / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        if (row < rows && i % PER == 0) p.stat[row] = make_float2(lse[k] == -INFINITY ? -INFINITY : -lse[k] * kLog2e, -sum);
     }
 }
 
@@ -1707,9 +1724,10 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     if (!encode_heads(&tq, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, p.rpt) || !encode_heads(&tk, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, 128) ||
         !encode_heads(&tv, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, 128))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(cross_fwd_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<HD>::SMEM);
+    const auto kernel = p.lone || p.splits > 1 ? cross_fwd_tiles<HD, true> : cross_fwd_tiles<HD, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<HD>::SMEM);
     if (e != cudaSuccess) return e;
-    cross_fwd_tiles<HD><<<unsigned(units < sms ? units : sms), kFwdThreads, FwdShape<HD>::SMEM, stream>>>(tq, tk, tv, p);
+    kernel<<<unsigned(units < sms ? units : sms), kFwdThreads, FwdShape<HD>::SMEM, stream>>>(tq, tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
     int parts = 1;   // four splits to a group of threads, as far as a block's go
@@ -1777,7 +1795,7 @@ cudaError_t bwd_pass(const CrossParams& c, int sms, cudaStream_t stream) {
     p.ts[0] = DKV ? c.dv_ts : c.dq_ts;
     p.ts[1] = c.dk_ts;
     if (!DKV) {   // the first of the two passes: the statistics before it
-        const int64_t rows = int64_t(c.B) * c.L * c.NH, blocks = ceil_div(rows * (HD / 8), 256);
+        const int64_t rows = int64_t(c.B) * c.L * c.NH, blocks = ceil_div(rows * (HD / 8), 256 * kStatLoads);
         if (blocks >= int64_t(1) << 31) return cudaErrorInvalidValue;
         cross_stat<HD><<<unsigned(blocks), 256, 0, stream>>>(p, rows);
         const cudaError_t e = cudaGetLastError();
