@@ -464,7 +464,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
         for (uint32_t n = slot_n < F::SLOTS ? 0u : slot_n - F::SLOTS; n < slot_n; ++n)   // k's are even
             drained(sy.bar((n & 1u ? F::B_VFULL : F::B_KFULL) + n % F::SLOTS), (n / 2u / F::CYCLE) & 1u);
         for (int a = 0; a < 2; ++a)
-            if (q_n[a]) drained(sy.bar(F::B_QFULL + a), (q_n[a] - 1u) & 1u);
+            for (uint32_t n = q_n[a] < 1u ? 0u : q_n[a] - 1u; n < q_n[a]; ++n) drained(sy.bar(F::B_QFULL + a), n & 1u);
     }
 }
 
@@ -504,7 +504,9 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
             const uint32_t flags = __reduce_or_sync(kAll, said[k.st]);
             if (flags & kEnd) return;
             const bool mine = flags & (a ? kTile1 : kTile0);
-            if (mine && (flags & kTileFirst) && !sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
+            if (mine && (flags & kTileFirst)) {
+                if (!sy.wait_warp(sy.bar(F::B_QFULL + a), q_n++ & 1u)) return;
+            }
             if (!mine) {
                 if (yes) mbar_arrive(sy.bar(F::B_EMPTY + k.st));
                 continue;
@@ -894,15 +896,16 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 //
 // Bound by the chain of its warps: each half of a step passes from the scores to
 // the softmax to the products and back, and every hand-over costs some 170 to 230
-// cycles. 49152 tokens, 16 heads of 128 over 512 states: 178 us, 1.16 PFLOP/s, tensor
-// cores 61 % busy; 24576 over 6144: 870 to 905 us, 1.4 PFLOP/s, 74 % (1.93 is a
-// large product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
+// cycles. 49152 tokens, 16 heads of 128 over 512 states: 176 us, 1.17 PFLOP/s, tensor
+// cores 61 % busy; 24576 over 6144: 820 us, 1.51 PFLOP/s, 74 % (1.93 is a large
+// product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
 // states of 4 heads 6.6 TB/s; below it by the chain (64: 3.9 TB/s).
 //
 // Two row tiles to a block, one block to an SM, persistent:
 // FEW: row tiles so few that the states are split, or one alone. What that takes is
 // left out of the kernel for the rest, whose warps of five kinds share little room
-// for instructions (49152 tokens over 512 states 185 -> 178 us, frames 949 -> 905).
+// for instructions (49152 tokens over 512 states 185 -> 176 us, 77 states 101 -> 94).
+// The same source laid out otherwise by the compiler is up to 5 % faster or slower.
 //
 //   warps 0..3, 4..7  the softmax of either row tile;
 //   warps 8..11       results on their way out;
