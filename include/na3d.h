@@ -446,7 +446,8 @@ int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float
  *   dq_i = sum_j ds k_j,   dk_j = sum_i ds q_i,   dv_j = sum_i p dout_i,
  * the last two over the tokens and the heads of q that share the head. dq is the
  * gradient of the scaled q. Sums are fp32 in a fixed order; p and ds are rounded
- * to bf16 for their products, the gradients once at the end. delta is taken as
+ * to bf16 for their products (ds for dq to two bf16 parts), the gradients once at
+ * the end. delta is taken as
  * out_i . dout_i, so it has the rounding of out in it; only for a token whose
  * states lie in one run of 64 is it the sum itself, since there out may be a
  * state's value and ds nothing but what the rounding leaves.

@@ -1352,6 +1352,7 @@ __device__ __forceinline__ void bwd_products(const Sync& sy, uint32_t base, uint
         const bool fresh = (flags & kFirst) != 0;
         if (DKV) product<HD, 64>(yes, tmem, t_s, z + (F::YTILE >> 4), z_hi, id_a, fresh);
         product<HD, 64>(yes, tmem + F::AW * (DKV ? 1u : buf), t_s + 64, z, z_hi, id_a, fresh);
+        if (!DKV) product<HD, 64>(yes, tmem + F::AW * buf, t_s, z, z_hi, id_a, false);
         commit(yes, sy.bar(F::B_EMPTY + sl));
         if (flags & kLast) {
             commit(yes, sy.bar(F::B_AFULL + buf));
@@ -1420,7 +1421,7 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                             dp[j] = (m >> j) & 1u ? dp[j] : 0.f;
                         }
                     }
-                    uint32_t pk[DKV ? 16 : 1], dk[16];
+                    uint32_t pk[16], dk[16];   // p or, DQ, what the rounding of ds leaves; ds
                     uint64_t nl = f2_pack(st.x, st.x), nd = f2_pack(st.y, st.y);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -1440,14 +1441,16 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                             f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), l2e2, nl), p0, p1);
                             p0 = ex2_approx(p0);
                             p1 = ex2_approx(p1);
-                            if (DKV) pk[DKV ? c / 2 : 0] = pack_bf16x2(p0, p1);
+                            if (DKV) pk[c / 2] = pack_bf16x2(p0, p1);
                             if (!DKV && exact && k == 0) delta = fmaf(p0, dp[c], fmaf(p1, dp[c + 1], delta));
                             f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(dp[c], dp[c + 1]), nd)), d0, d1);
-                            dk[c / 2] = pack_bf16x2(d0, d1);
+                            const uint32_t high = dk[c / 2] = pack_bf16x2(d0, d1);
+                            // dq's ds in two parts: delta brings the rounding of out into it as well
+                            if (!DKV) pk[c / 2] = pack_bf16x2(d0 - __uint_as_float(high << 16), d1 - __uint_as_float(high & 0xffff0000u));
                         }
                     }
                     if (k == 0) continue;
-                    if (DKV) tmem_st16(t_s + 16 * q, pk);
+                    tmem_st16(t_s + 16 * q, pk);
                     tmem_st16(t_s + 64 + 16 * q, dk);
                 }
                 if (k == 0) {
@@ -1546,11 +1549,14 @@ __device__ __forceinline__ void bwd_out(const BwdParams& p, const Sync& sy, uint
     }
 }
 
-// Seven products in the two passes, where one pass would make five: s and dp are
+// Eight products in the two passes, where one pass would make five: s and dp are
 // made anew, so that each sum stays in one block's tensor memory, no gradient needs
-// an atomic, and equal inputs give equal bits. Bound as the forward pass is: 24576
-// tokens, 16 heads of 128 over 512 states, dq 157 us (0.98 PFLOP/s, tensor cores
-// 62 % busy), dk and dv 168 us (1.23, 66 %).
+// an atomic, and equal inputs give equal bits; and dq takes ds in two bf16 parts,
+// the second what the rounding of the first leaves. (Its error over that of a result
+// rounded once falls from 1.5 to 1.1 at head size 16, from 1.44 to 1.15 at 128, for
+// 15 us of the next figure.) Bound as the forward pass is: 24576 tokens, 16 heads of
+// 128 over 512 states, dq 172 us, dk and dv 168 us (1.23 PFLOP/s, tensor cores 66 %
+// busy).
 //
 // One row tile to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  every second step's probabilities each;
