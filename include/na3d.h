@@ -448,8 +448,9 @@ int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float
  * gradient of the scaled q. Sums are fp32 in a fixed order; p and ds are rounded
  * to bf16 for their products (ds for dq to two bf16 parts), the gradients once at
  * the end. delta is taken as out_i . dout_i, so it has the rounding of out in it;
- * only for a token whose states lie in one run of 64 is it the sum itself, since
- * there out may be a state's value and ds nothing but what the rounding leaves.
+ * only for a token whose states lie in one run of 64 (from a multiple of 64 on) is
+ * it the sum itself, since there out may be a state's value and ds nothing but what
+ * the rounding leaves: a token that sees one state has a dq of 0 and adds 0 to dk.
  *
  * out, lse: what the forward pass wrote; dout: bf16, contiguous (B,L,NH,HD).
  * dq, dk, dv: bf16 with token strides, written whole (zeros where nothing is

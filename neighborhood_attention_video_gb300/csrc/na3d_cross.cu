@@ -60,6 +60,15 @@ __device__ __forceinline__ void drained(uint32_t bar, uint32_t parity) {
     if (!mbar_wait_bounded(bar, parity, kDrainLimitNs)) atomicOr(&g_cross_timeout_flag, 1u);
 }
 
+// One column of this thread's lane (32x32b shape).
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    float v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr) : "memory");
+    tmem_wait_ld();
+    asm volatile("" : "+f"(v));
+    return v;
+}
+
 // The values of a tensor-memory load stay behind the wait for it.
 __device__ __forceinline__ void behind_wait(float* v) {
 #pragma unroll
@@ -1063,7 +1072,8 @@ struct BwdParams {
     const int32_t *doc_r, *doc_c;
     const uint16_t *out, *dout;          // for the statistics
     const float* lse;
-    float2* stat;                        // (row of q): -lse log2e, -delta
+    float2* stat;                        // (row of q): -lse log2e, -delta: out . dout
+    float2* stat_kv;                     // ... as DQ leaves it for DKV: where it has the sum itself, that
     uint16_t* grad[2];                   // DQ: dq; DKV: dv, dk
     int64_t ts[2];
     float* part;                         // splits > 1: (split, gradient, row, HD) in 32 bits
@@ -1132,7 +1142,11 @@ __global__ void __launch_bounds__(256) cross_stat(const BwdParams p, int64_t row
         }
 #pragma unroll
         for (int o = PER / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        if (row < rows && i % PER == 0) p.stat[row] = make_float2(lse[k] == -INFINITY ? -INFINITY : -lse[k] * kLog2e, -sum);
+        if (row < rows && i % PER == 0) {
+            const float2 st = make_float2(lse[k] == -INFINITY ? -INFINITY : -lse[k] * kLog2e, -sum);
+            p.stat[row] = st;
+            p.stat_kv[row] = st;
+        }
     }
 }
 
@@ -1210,7 +1224,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                 for (int i = 0; i < 2; ++i) {
                     const int t = x.tile * p.cpt + ctok[i];
                     const bool of = ctok[i] < p.cpt && t < p.nc && (x.whole || tiles.docs.of(b, t) == x.doc);
-                    ahead[i] = of ? p.stat[(b * p.nc + t) * p.NH + kh * p.G + chead[i]] : make_float2(0.f, 0.f);
+                    ahead[i] = of ? p.stat_kv[(b * p.nc + t) * p.NH + kh * p.G + chead[i]] : make_float2(0.f, 0.f);
                 }
             };
             if (DKV) read(f);
@@ -1375,7 +1389,7 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
     uint32_t heard = 0, n = 0;   // n: steps with columns
     bool in = false;
     int doc = -1;
-    float2* stat = nullptr;   // DQ: of this row
+    int64_t row = 0;   // DQ: of the statistics
     float2 st = make_float2(0.f, 0.f);
     for (;;) {
         const uint32_t e = heard % kBwdSteps;
@@ -1388,8 +1402,8 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
             in = tok < p.rpt && steps[e].t0 + tok < p.nr;
             const int64_t token = steps[e].token + tok;
             doc = in && p.doc_r ? __ldg(p.doc_r + token) : 0;
-            stat = p.stat + token * p.NH + steps[e].pad * p.G + g;
-            if (in) st = *stat;   // written by an earlier kernel
+            row = token * p.NH + steps[e].pad * p.G + g;
+            if (in) st = p.stat[row];   // written by an earlier kernel
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
@@ -1400,9 +1414,12 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
             const uint32_t sl = n % F::STAGES;
             const float4* const cs = reinterpret_cast<const float4*>(base_ptr + F::OFF_STAT + sl * 512);
             const uint64_t l2e2 = f2_pack(kLog2e, kLog2e);
-            // A row that sees one tile alone: delta from its products, without the rounding that out has.
-            const bool exact = !DKV && p.splits == 1 && (flags & (kFirst | kLast)) == (kFirst | kLast);
-            float delta = 0.f;
+            // A row that sees one tile alone: delta from its products, without the rounding that out has,
+            // as a mean of dp by its distances from the first seen column's, so that it is that dp, and ds 0,
+            // where there is one state, or all have the same dp, whatever the rounding of p.
+            const bool exact = !DKV && (flags & (kFirst | kLast)) == (kFirst | kLast);
+            float at = 0.f, total = 0.f, lean = 0.f;
+            if (exact) at = tmem_ld1(t_s + 64 + (columns.x ? __ffs(columns.x) - 1 : (__ffs(columns.y) + 31) & 63));
 #pragma unroll 1
             for (int k = exact ? 0 : 1; k < 2; ++k) {
 #pragma unroll 1
@@ -1442,7 +1459,10 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                             p0 = ex2_approx(p0);
                             p1 = ex2_approx(p1);
                             if (DKV) pk[c / 2] = pack_bf16x2(p0, p1);
-                            if (!DKV && exact && k == 0) delta = fmaf(p0, dp[c], fmaf(p1, dp[c + 1], delta));
+                            if (!DKV && exact && k == 0) {
+                                total += p0 + p1;
+                                lean = fmaf(p0, dp[c] - at, fmaf(p1, dp[c + 1] - at, lean));
+                            }
                             f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(dp[c], dp[c + 1]), nd)), d0, d1);
                             const uint32_t high = dk[c / 2] = pack_bf16x2(d0, d1);
                             // dq's ds in two parts: delta brings the rounding of out into it as well
@@ -1453,11 +1473,12 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                     tmem_st16(t_s + 16 * q, pk);
                     tmem_st16(t_s + 64 + 16 * q, dk);
                 }
-                if (k == 0) {
-                    if (in && doc == d) {
-                        st.y = -delta;
-                        *stat = st;
-                    }
+                // Of a split the tile is all that the row sees where its probabilities are 1 in all: less may
+                // be missing than their own error or what out's rounding would do. (Other splits' blocks
+                // keep what p.stat has, whenever they read it: equal inputs, equal bits.)
+                if (k == 0 && in && doc == d && (p.splits == 1 || total >= 1.f - 0x1p-12f - fminf(fabsf(st.x) * 0x1p-20f, 0x1p-4f))) {
+                    st.y = -(at + lean / total);
+                    p.stat_kv[row] = st;
                 }
             }
             if (flags & kForeign) {
@@ -1672,7 +1693,7 @@ constexpr int kSms = 152;   // what the work is shared out for: equal on every d
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The statistics of the backward pass, and the splits' sums behind them.
+// Each of the two copies of the statistics of the backward pass; the splits' sums lie behind them.
 int64_t stat_bytes(int64_t B, int64_t L, int64_t NH) { return (B * L * NH * 8 + 127) / 128 * 128; }
 
 struct FwdPlan {
@@ -1796,9 +1817,11 @@ cudaError_t bwd_pass(const CrossParams& c, int sms, cudaStream_t stream) {
     p.out = c.out;
     p.dout = c.dout;
     p.lse = c.lse;
-    p.stat = static_cast<float2*>(c.work);
+    uint8_t* const work = static_cast<uint8_t*>(c.work);
+    p.stat = reinterpret_cast<float2*>(work);
+    p.stat_kv = reinterpret_cast<float2*>(work + stat_bytes(c.B, c.L, c.NH));
     p.rows = pl.rows;
-    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(c.work) + stat_bytes(c.B, c.L, c.NH));
+    p.part = reinterpret_cast<float*>(work + 2 * stat_bytes(c.B, c.L, c.NH));
     p.grad[0] = DKV ? c.dv : c.dq;
     p.grad[1] = c.dk;
     p.ts[0] = DKV ? c.dv_ts : c.dq_ts;
@@ -1849,7 +1872,7 @@ int64_t cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV
     const int64_t rows = B * L * NH;
     if (backward) {
         const int64_t a = BwdPlan(false, B, L, S, NH, NKV).part_bytes(HD), b = BwdPlan(true, B, L, S, NH, NKV).part_bytes(HD);
-        return stat_bytes(B, L, NH) + (a > b ? a : b);
+        return 2 * stat_bytes(B, L, NH) + (a > b ? a : b);
     }
     const FwdPlan pl(B, L, S, NH, NKV);
     return pl.splits > 1 ? pl.splits * rows * (HD + 1) * 4 : 0;
