@@ -313,7 +313,10 @@ struct FwdShape : Geom<HD> {
                          B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_DONE = B_STAT + 2, B_TOLD = B_DONE + 4, B_HEARD = B_TOLD + kSteps,
                          B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 3;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the slots' flags
-    static constexpr int OFF_STAT = (OFF_MISC + 8 + 4 * SLOTS + 15) & ~15;   // sum and reference of each row
+    // The columns of the last 8 steps that have some: before a step is told, k and v of the one before it
+    // have their slots, and so the v of four (SLOTS 5; 8: of five) steps before it has been used.
+    static constexpr int OFF_MASK = (OFF_MISC + 8 + 4 * SLOTS + 15) & ~15, MASKS = 8;
+    static constexpr int OFF_STAT = OFF_MASK + 16 * MASKS;   // sum and reference of each row
     // one block on an SM, which tensor memory is shared out for
     static constexpr int NEED = OFF_STAT + 2 * 128 * 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     static constexpr uint32_t TM_S = 0, TM_O = 256, OW = HD < 32 ? 32 : HD;   // scores of either row tile; their sums
@@ -322,12 +325,12 @@ struct FwdShape : Geom<HD> {
 
 constexpr int kFwdThreads = 512;
 // registers: what the softmax, the way out and the rest take of 512 x 128
-constexpr uint32_t kRegsSoftmax = 160, kRegsOut = 104, kRegsLow = 88;
+constexpr uint32_t kRegsSoftmax = 144, kRegsOut = 112, kRegsLow = 112;
 static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
 
 template <int HD, bool FEW>
-__device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, Step* steps, volatile uint32_t* said, const CUtensorMap* tq,
-                                             const CUtensorMap* tk, const CUtensorMap* tv) {
+__device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, Step* steps, volatile uint32_t* said,
+                                             const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv) {
     using F = FwdShape<HD>;
     const bool lone = FEW && p.lone;
     const int lane = threadIdx.x & 31;
@@ -354,12 +357,14 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
         }
         return true;
     };
+    uint4* const masks = reinterpret_cast<uint4*>(base_ptr + F::OFF_MASK);
     auto tell = [&](const Step& s) -> bool {
         const uint32_t e = told % kSteps;
         if (!sy.wait_warp(sy.bar(F::B_HEARD + e), ((told / kSteps) & 1u) ^ 1u)) return false;
         ++told;
         if (lane == 0) {
             steps[e] = s;
+            masks[slot_n / 2 % F::MASKS] = *reinterpret_cast<const uint4*>(s.mask);
             mbar_arrive(sy.bar(F::B_TOLD + e));
         }
         return true;
@@ -538,20 +543,32 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
 }
 
 template <int HD>
-__device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint32_t tmem, const volatile uint32_t* said) {
+__device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, const uint8_t* base_ptr, uint32_t tmem, const volatile uint32_t* said) {
     using F = FwdShape<HD>;
     constexpr uint32_t id_o = make_idesc_bf16(128, HD, 0, 1);
     constexpr uint32_t half_rows = (64 * F::ROWB) >> 4;
     const uint64_t vd = make_smem_desc(base + F::OFF_KV, F::REG, F::SBO, F::SWZ);
     const uint32_t v_lo = uint32_t(vd), v_hi = uint32_t(vd >> 32);
     const uint32_t yes = elect();
-    uint32_t n[2] = {0, 0}, o_n[2] = {0, 0};
+    uint32_t n[2] = {0, 0}, o_n[2] = {0, 0}, v_n = 0;
     Slot<F::SLOTS> v(1);
     auto run = [&]() {
-        for (;; v.next()) {
+        for (;; v.next(), ++v_n) {
             if (!sy.wait_warp(sy.bar(F::B_VFULL + v.st), v.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[v.st]);
             if (flags & kEnd) return;
+            if (flags & kForeign) {
+                // Columns of other documents, whose probabilities are 0: 0 times their values must be 0. By
+                // this warp, since it waits for every v; who did so for some alone could take the phase of an
+                // earlier one, still on its way, for its own.
+                const uint32_t* const mask = reinterpret_cast<const uint32_t*>(base_ptr + F::OFF_MASK) + 4 * (v_n % F::MASKS);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i)
+                    if (!(mask[i] >> (threadIdx.x & 31) & 1u))
+                        zero_row<HD, F::REG>(base + F::OFF_KV + v.st * F::TILE, 32 * i + int(threadIdx.x & 31));
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int h = i >> 1, a = i & 1;
@@ -579,14 +596,14 @@ __device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, uint
 // One row of scores to a thread, which keeps the reference of its powers and their
 // sum, and leaves them for the way out.
 template <int HD>
-__device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
+__device__ __forceinline__ void fwd_softmax(const Sync& sy, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
     using F = FwdShape<HD>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + F::TM_S + 128 * a, t_o = t_lane + F::TM_O + F::OW * a;
     float2* const stat = reinterpret_cast<float2*>(base_ptr + F::OFF_STAT) + a * 128 + r;
-    uint32_t heard = 0, s_n = 0, passes = 0, slot_n = 0;
+    uint32_t heard = 0, s_n = 0, passes = 0;
     float ref = 0.f, l = 0.f;
     for (;;) {
         const uint32_t e = heard % kSteps;
@@ -597,7 +614,6 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(F::B_HEARD + e));
         if (flags & kEnd) return;
-        if (!(flags & kNone)) slot_n += 2;
         if (flags & (a ? kTile1 : kTile0)) {
             if (flags & kFirst) l = 0.f;
 #pragma unroll 1
@@ -678,18 +694,6 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint32_t base, uint8
                     if (again || !__any_sync(kAll, anew)) break;
                 }
                 l += sum;
-                if (h == 0 && (flags & kForeign)) {
-                    // this thread's column, where it is of another document: 0 times its value must be 0.
-                    // Either row tile's warps do so before their product; both write the same zeros.
-                    const uint32_t vs = slot_n - 1;
-                    if (!sy.wait_warp(sy.bar(F::B_VFULL + vs % F::SLOTS), (vs / 2u / F::CYCLE) & 1u)) {
-                        tmem_wait_st();
-                        return;
-                    }
-                    if (!((warp & 2 ? (warp & 1 ? columns.w : columns.z) : (warp & 1 ? columns.y : columns.x)) >> lane & 1u))
-                        zero_row<HD, F::REG>(base + F::OFF_KV + (vs % F::SLOTS) * F::TILE, r);
-                    fence_proxy_async_smem();
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -966,15 +970,15 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     dependents_may_start();
     if (warp < 8) {
         regs_increase<kRegsSoftmax>();
-        fwd_softmax<HD>(sy, base, base_ptr, tmem, steps);
+        fwd_softmax<HD>(sy, base_ptr, tmem, steps);
     } else if (warp < 12) {
         regs_decrease<kRegsOut>();
         fwd_out<HD, FEW>(p, sy, base_ptr, tmem, steps);
     } else {
         regs_decrease<kRegsLow>();
-        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, steps, misc + 2, &tq, &tk, &tv);
+        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, base_ptr, steps, misc + 2, &tq, &tk, &tv);
         if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2, warp - 13);
-        if (warp == 15) fwd_products<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
+        if (warp == 15) fwd_products<HD>(sy, base, base_ptr, __reduce_or_sync(kAll, tmem), misc + 2);
     }
     tc_fence_before();
     __syncthreads();

@@ -1,0 +1,49 @@
+"""Documents of the attention to other states over thousands of calls and long
+lists: operands arrive in any order, searches take as long as they take."""
+import pytest
+import torch
+
+import block_reference as ref
+import neighborhood_attention_video_gb300 as na
+from packed_reference import check
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def make(shape, S, NKV, seed):
+    gen = torch.Generator().manual_seed(seed)
+    q = (torch.randn(shape, generator=gen) * shape[5] ** -0.5).to(BF16)
+    return q, torch.randn((shape[0], S, 2, NKV, shape[5]), generator=gen).to(BF16), torch.randn(shape, generator=gen).to(BF16)
+
+
+@pytest.mark.parametrize("HD", [16, 64, 128])
+@pytest.mark.parametrize("B,L,S,NKV", [
+    (5, 300, 1300, 16),    # pairs of row tiles of which every second has one alone: the other's steps come late
+    (3, 700, 90, 16),      # one column tile a document
+    (200, 5, 40, 1),       # one row tile, units of one column tile and of several in turn
+    (40, 7, 700, 5),
+], ids=str)
+def test_columns_of_other_documents_stay_out_over_many_calls(B, L, S, NKV, HD):
+    """Every step has columns of other documents and of padding, which hold NaN: over
+    thousands of calls the results of the others keep their bits."""
+    q, kv, _ = make((B, 1, 1, L, NKV, HD), S, NKV, 1)
+    gen = torch.Generator().manual_seed(2)
+    doc = (torch.arange(L) * 3 // L).expand(B, 1, 1, L).to(torch.int32).contiguous()
+    kv_doc = torch.randint(-1, 4, (B, S), generator=gen).sort(1).values.to(torch.int32)
+    kv_doc[:, ::7] = -1
+    kv_doc[1::2, 3 * S // 8:] = 1
+    kv[(kv_doc < 0) | (kv_doc > 2)] = float("nan")
+    q, kv, doc, kv_doc = (x.cuda() for x in (q, kv, doc, kv_doc))
+    k, v = kv.unbind(2)
+    first, lse = na.na3d_cross_attention(q, k, v, doc=doc, kv_doc=kv_doc, return_lse=True)
+    n = min(B, 2)
+    want = ref.cross(q[:n], k[:n], v[:n], doc[:n], kv_doc[:n])
+    check("out", first[:n], want["out"])
+    check("lse", lse[:n], want["lse"])
+    assert torch.isfinite(first).all()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(1500):
+        out, other = na.na3d_cross_attention(q, k, v, doc=doc, kv_doc=kv_doc, return_lse=True)
+        differ += (out.view(torch.int16) != first.view(torch.int16)).sum() + (other.view(torch.int32) != lse.view(torch.int32)).sum()
+    assert int(differ) == 0 and na.na3d_device_status() == 0
