@@ -32,11 +32,20 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kSumLimit = 4294967296.0f;   // 2^32: of a row's probabilities in one tile
 
+// About a millisecond a tick.
+__device__ __forceinline__ uint32_t beat_clock() { return uint32_t(globaltimer_ns() >> 20); }
+constexpr uint32_t kWaitTicks = uint32_t(kWaitLimitNs >> 20);
+
 struct Sync {
     uint32_t bar0;
+    // behind it the beat: when the producer, which tells nothing meanwhile, was last looking for a document
     volatile uint32_t* abort_flag;
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
-    // Wait for a barrier phase; false once this block has given up.
+    __device__ __forceinline__ void still_going(int lane) const {
+        if (lane == 0) abort_flag[1] = beat_clock();
+    }
+    // Wait for a barrier phase; false once this block has given up, kWaitLimitNs after this wait began and after
+    // the last beat.
     __device__ __forceinline__ bool wait(uint32_t b, uint32_t parity) const {
         if (mbar_try_wait(b, parity)) return true;
         const uint64_t t0 = globaltimer_ns();
@@ -44,7 +53,7 @@ struct Sync {
             if (mbar_try_wait(b, parity)) return true;
             if ((it & 1023u) == 0u) {
                 if (*abort_flag) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                if (globaltimer_ns() - t0 > kWaitLimitNs && beat_clock() - abort_flag[1] > kWaitTicks) {
                     *abort_flag = 1u;
                     atomicOr(&g_cross_timeout_flag, 1u);
                     return false;
@@ -172,6 +181,7 @@ struct Docs {
 struct Tiles {
     Docs docs;
     int per;             // tokens to a tile
+    Sync sync;
     int64_t b = -1;
     int first = -1;
     int lo, hi;
@@ -180,6 +190,7 @@ struct Tiles {
         if (entry == b && (tile & ~31) == first) return;
         b = entry;
         first = tile & ~31;
+        sync.still_going(threadIdx.x & 31);
         const int i0 = (first + int(threadIdx.x & 31)) * per, end = min(i0 + per, docs.n);
         lo = INT_MAX;
         hi = INT_MIN;
@@ -312,10 +323,10 @@ struct FwdShape : Geom<HD> {
     static constexpr int B_KFULL = 0, B_VFULL = SLOTS, B_EMPTY = 2 * SLOTS, B_QFULL = 3 * SLOTS, B_QEMPTY = B_QFULL + 2, B_SFULL = B_QEMPTY + 2,
                          B_PFULL = B_SFULL + 4, B_OFULL = B_PFULL + 4, B_OREAD = B_OFULL + 2, B_STAT = B_OREAD + 2, B_DONE = B_STAT + 2, B_TOLD = B_DONE + 4, B_HEARD = B_TOLD + kSteps,
                          B_DRAIN = B_HEARD + kSteps, NBAR = B_DRAIN + 3;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the slots' flags
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, beat, the slots' flags
     // The columns of the last 8 steps that have some: before a step is told, k and v of the one before it
     // have their slots, and so the v of four (SLOTS 5; 8: of five) steps before it has been used.
-    static constexpr int OFF_MASK = (OFF_MISC + 8 + 4 * SLOTS + 15) & ~15, MASKS = 8;
+    static constexpr int OFF_MASK = (OFF_MISC + 12 + 4 * SLOTS + 15) & ~15, MASKS = 8;
     static constexpr int OFF_STAT = OFF_MASK + 16 * MASKS;   // sum and reference of each row
     // one block on an SM, which tensor memory is shared out for
     static constexpr int NEED = OFF_STAT + 2 * 128 * 8, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
@@ -334,7 +345,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     using F = FwdShape<HD>;
     const bool lone = FEW && p.lone;
     const int lane = threadIdx.x & 31;
-    Tiles tiles{{p.kv_doc, p.S}, 128};
+    Tiles tiles{{p.kv_doc, p.S}, 128, sy};
     const Docs rows{p.doc, p.L};
     const bool plain = !p.doc && !p.kv_doc;   // every column is of every row's document
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
@@ -952,6 +963,7 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
                                  : i >= F::B_HEARD && i < F::B_HEARD + kSteps ? 12u : 1u);
         }
         misc[1] = 0u;
+        misc[2] = beat_clock() - kWaitTicks - 1u;   // long ago
         fence_mbar_init();
     }
     if (warp == 12 && lane == 0) {
@@ -976,9 +988,9 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
         fwd_out<HD, FEW>(p, sy, base_ptr, tmem, steps);
     } else {
         regs_decrease<kRegsLow>();
-        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, base_ptr, steps, misc + 2, &tq, &tk, &tv);
-        if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2, warp - 13);
-        if (warp == 15) fwd_products<HD>(sy, base, base_ptr, __reduce_or_sync(kAll, tmem), misc + 2);
+        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, base_ptr, steps, misc + 3, &tq, &tk, &tv);
+        if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 3, warp - 13);
+        if (warp == 15) fwd_products<HD>(sy, base, base_ptr, __reduce_or_sync(kAll, tmem), misc + 3);
     }
     tc_fence_before();
     __syncthreads();
@@ -1096,8 +1108,8 @@ struct BwdShape : Geom<HD> {
     static constexpr int B_FULL = 0, B_EMPTY = STAGES, B_XFULL = 2 * STAGES, B_XEMPTY = B_XFULL + 1, B_SFULL = B_XEMPTY + 1,
                          B_PFULL = B_SFULL + 2, B_AFULL = B_PFULL + 2, B_AREAD = B_AFULL + 2, B_TOLD = B_AREAD + 2,
                          B_HEARD = B_TOLD + kBwdSteps, B_DRAIN = B_HEARD + kBwdSteps, NBAR = B_DRAIN + 2;
-    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, the stages' flags
-    static constexpr int NEED = OFF_MISC + 8 + 4 * STAGES, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tensor memory, abort flag, beat, the stages' flags
+    static constexpr int NEED = OFF_MISC + 12 + 4 * STAGES, SMEM = NEED > 120 * 1024 ? NEED : 120 * 1024;
     // sums: dv and dk, or dq of one pass and of the next; s and dp of either buffer
     static constexpr uint32_t AW = HD < 32 ? 32 : HD, TM_S = 256;
     static_assert(SMEM <= 232448, "shared memory");
@@ -1159,7 +1171,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                                              const CUtensorMap* tx0, const CUtensorMap* tx1, const CUtensorMap* ty0, const CUtensorMap* ty1) {
     using F = BwdShape<HD>;
     const int lane = threadIdx.x & 31;
-    Tiles tiles{{p.doc_c, p.nc}, p.cpt};
+    Tiles tiles{{p.doc_c, p.nc}, p.cpt, sy};
     const Docs rows{p.doc_r, p.nr};
     const bool plain = !p.doc_r && !p.doc_c;   // every column is of every row's document
     uint32_t told = 0, it = 0, x_n = 0;
@@ -1612,6 +1624,7 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
             mbar_init(sy.bar(i), (i >= F::B_PFULL && i < F::B_PFULL + 2) || (i >= F::B_AREAD && i < F::B_AREAD + 2) ? 4u
                                  : i >= F::B_HEARD && i < F::B_HEARD + kBwdSteps ? 12u : 1u);
         misc[1] = 0u;
+        misc[2] = beat_clock() - kWaitTicks - 1u;   // long ago
         fence_mbar_init();
     }
     if (warp == 12 && lane == 0) {
@@ -1638,9 +1651,9 @@ cross_bwd_tiles(const __grid_constant__ CUtensorMap tx0, const __grid_constant__
         bwd_out<HD, DKV>(p, sy, tmem, steps);
     } else {
         regs_decrease<kBwdLow>();
-        if (warp == 12) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, misc + 2, &tx0, &tx1, &ty0, &ty1);
-        if (warp == 13) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
-        if (warp == 14) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), misc + 2);
+        if (warp == 12) bwd_producer<HD, DKV>(p, sy, base, base_ptr, steps, misc + 3, &tx0, &tx1, &ty0, &ty1);
+        if (warp == 13) bwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 3);
+        if (warp == 14) bwd_products<HD, DKV>(sy, base, __reduce_or_sync(kAll, tmem), misc + 3);
     }
     tc_fence_before();
     __syncthreads();

@@ -47,3 +47,23 @@ def test_columns_of_other_documents_stay_out_over_many_calls(B, L, S, NKV, HD):
         out, other = na.na3d_cross_attention(q, k, v, doc=doc, kv_doc=kv_doc, return_lse=True)
         differ += (out.view(torch.int16) != first.view(torch.int16)).sum() + (other.view(torch.int32) != lse.view(torch.int32)).sum()
     assert int(differ) == 0 and na.na3d_device_status() == 0
+
+
+def test_a_search_may_take_its_time():
+    """256 documents a row tile, most of them without states, in a list of 2^24 states of
+    which no part can be left out by its smallest and largest document: the search tells
+    nothing for longer than a wait's limit of two seconds, and the call is right."""
+    S, L, HD, n = 1 << 24, 77 * 256, 16, 5
+    q, end, _ = make((1, 1, 1, L, 1, HD), n, 1, 3)
+    kv = torch.zeros((1, S, 2, 1, HD), dtype=BF16, device="cuda")
+    kv[:, -n:] = end.cuda()
+    kv_doc = ((torch.arange(S // 128, device="cuda", dtype=torch.int32) & 1) << 30).repeat_interleave(128).view(1, S)
+    kv_doc[:, -n:] = 256
+    doc = (1 + torch.arange(L) % 256).to(torch.int32).view(1, 1, 1, L)
+    k, v = kv.unbind(2)
+    out, lse = na.na3d_cross_attention(q.cuda(), k, v, doc=doc.cuda(), kv_doc=kv_doc, return_lse=True)
+    torch.cuda.synchronize()
+    assert na.na3d_device_status() == 0
+    want = ref.cross(q, end[:, :, 0], end[:, :, 1], (doc != 256).to(torch.int32))
+    check("out", out, want["out"])
+    check("lse", lse, want["lse"])
