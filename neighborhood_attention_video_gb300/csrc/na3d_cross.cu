@@ -1430,72 +1430,79 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
             const uint32_t sl = n % F::STAGES;
             const float4* const cs = reinterpret_cast<const float4*>(base_ptr + F::OFF_STAT + sl * 512);
             const uint64_t l2e2 = f2_pack(kLog2e, kLog2e);
-            // A row that sees one tile alone: delta from its products, without the rounding that out has,
-            // as a mean of dp by its distances from the first seen column's, so that it is that dp, and ds 0,
-            // where there is one state, or all have the same dp, whatever the rounding of p.
-            const bool exact = !DKV && (flags & (kFirst | kLast)) == (kFirst | kLast);
-            float at = 0.f, total = 0.f, lean = 0.f;
-            if (exact) at = tmem_ld1(t_s + 64 + (columns.x ? __ffs(columns.x) - 1 : (__ffs(columns.y) + 31) & 63));
-#pragma unroll 1
-            for (int k = exact ? 0 : 1; k < 2; ++k) {
+            auto load = [&](int q, float (&s)[32], float (&dp)[32]) {
+                tmem_ld32(t_s + 32 * q, s);
+                tmem_ld32(t_s + 64 + 32 * q, dp);
+                tmem_wait_ld();
+                behind_wait(s);
+                behind_wait(dp);
+                if (flags & kMasked) {
+                    const uint32_t m = q ? columns.y : columns.x;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        s[j] = (m >> j) & 1u ? s[j] : -INFINITY;
+                        dp[j] = (m >> j) & 1u ? dp[j] : 0.f;
+                    }
+                }
+            };
+            if (!DKV && (flags & (kFirst | kLast)) == (kFirst | kLast)) {
+                // A row that sees one tile alone: delta from its products, without the rounding that out has,
+                // as a mean of dp by its distances from the first seen column's, so that it is that dp, and ds
+                // 0, where there is one state, or all have the same dp, whatever the rounding of p.
+                const float at = tmem_ld1(t_s + 64 + (columns.x ? __ffs(columns.x) - 1 : (__ffs(columns.y) + 31) & 63));
+                float total = 0.f, lean = 0.f;
 #pragma unroll 1
                 for (int q = 0; q < 2; ++q) {
                     float s[32], dp[32];
-                    tmem_ld32(t_s + 32 * q, s);
-                    tmem_ld32(t_s + 64 + 32 * q, dp);
-                    tmem_wait_ld();
-                    behind_wait(s);
-                    behind_wait(dp);
-                    const uint32_t m = q ? columns.y : columns.x;
-                    if (flags & kMasked) {
+                    load(q, s, dp);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            s[j] = (m >> j) & 1u ? s[j] : -INFINITY;
-                            dp[j] = (m >> j) & 1u ? dp[j] : 0.f;
-                        }
+                    for (int j = 0; j < 32; ++j) {
+                        const float p0 = ex2_approx(fmaf(s[j], kLog2e, st.x));
+                        total += p0;
+                        lean = fmaf(p0, dp[j] - at, lean);
                     }
-                    uint32_t pk[16], dk[16];   // p or, DQ, what the rounding of ds leaves; ds
-                    uint64_t nl = f2_pack(st.x, st.x), nd = f2_pack(st.y, st.y);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        float4 l4, d4;
-                        if (DKV) {
-                            l4 = cs[(32 * q + j) / 4];
-                            d4 = cs[16 + (32 * q + j) / 4];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (DKV) {
-                                nl = i ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
-                                nd = i ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
-                            }
-                            const int c = j + 2 * i;
-                            float p0, p1, d0, d1;
-                            f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), l2e2, nl), p0, p1);
-                            p0 = ex2_approx(p0);
-                            p1 = ex2_approx(p1);
-                            if (DKV) pk[c / 2] = pack_bf16x2(p0, p1);
-                            if (!DKV && exact && k == 0) {
-                                total += p0 + p1;
-                                lean = fmaf(p0, dp[c] - at, fmaf(p1, dp[c + 1] - at, lean));
-                            }
-                            f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(dp[c], dp[c + 1]), nd)), d0, d1);
-                            const uint32_t high = dk[c / 2] = pack_bf16x2(d0, d1);
-                            // dq's ds in two parts: delta brings the rounding of out into it as well
-                            if (!DKV) pk[c / 2] = pack_bf16x2(d0 - __uint_as_float(high << 16), d1 - __uint_as_float(high & 0xffff0000u));
-                        }
-                    }
-                    if (k == 0) continue;
-                    tmem_st16(t_s + 16 * q, pk);
-                    tmem_st16(t_s + 64 + 16 * q, dk);
                 }
                 // Of a split the tile is all that the row sees where its probabilities are 1 in all: less may
                 // be missing than their own error or what out's rounding would do. (Other splits' blocks
                 // keep what p.stat has, whenever they read it: equal inputs, equal bits.)
-                if (k == 0 && in && doc == d && (p.splits == 1 || total >= 1.f - 0x1p-12f - fminf(fabsf(st.x) * 0x1p-20f, 0x1p-4f))) {
+                if (in && doc == d && (p.splits == 1 || total >= 1.f - 0x1p-12f - fminf(fabsf(st.x) * 0x1p-20f, 0x1p-4f))) {
                     st.y = -(at + lean / total);
                     p.stat_kv[row] = st;
                 }
+            }
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                float s[32], dp[32];
+                load(q, s, dp);
+                uint32_t pk[16], dk[16];   // p or, DQ, what the rounding of ds leaves; ds
+                uint64_t nl = f2_pack(st.x, st.x), nd = f2_pack(st.y, st.y);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    float4 l4, d4;
+                    if (DKV) {
+                        l4 = cs[(32 * q + j) / 4];
+                        d4 = cs[16 + (32 * q + j) / 4];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (DKV) {
+                            nl = i ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
+                            nd = i ? f2_pack(d4.z, d4.w) : f2_pack(d4.x, d4.y);
+                        }
+                        const int c = j + 2 * i;
+                        float p0, p1, d0, d1;
+                        f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), l2e2, nl), p0, p1);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
+                        if (DKV) pk[c / 2] = pack_bf16x2(p0, p1);
+                        f2_unpack(f2_mul(f2_pack(p0, p1), f2_add(f2_pack(dp[c], dp[c + 1]), nd)), d0, d1);
+                        const uint32_t high = dk[c / 2] = pack_bf16x2(d0, d1);
+                        // dq's ds in two parts: delta brings the rounding of out into it as well
+                        if (!DKV) pk[c / 2] = pack_bf16x2(d0 - __uint_as_float(high << 16), d1 - __uint_as_float(high & 0xffff0000u));
+                    }
+                }
+                tmem_st16(t_s + 16 * q, pk);
+                tmem_st16(t_s + 64 + 16 * q, dk);
             }
             if (flags & kForeign) {
                 // columns of other documents, whose probabilities are 0: 0 times their values must be 0
