@@ -427,7 +427,9 @@ int64_t na3d_norm_rope_workspace(int64_t HD);
  * out: bf16, contiguous (B,L,NH,HD). lse: fp32 (B,L,NH), or NULL.
  * doc: DEVICE, int32 (B,L), or NULL: all 0. kv_doc: DEVICE, int32 (B,S), or NULL:
  *   all 0. Negative documents see nothing and are seen by nothing (padding). Read
- *   when the kernels run.
+ *   when the kernels run. Each tile of some 128 rows looks for its documents one
+ *   after another: cheap where a document's states lie together, a walk of kv_doc
+ *   for each document where they are scattered.
  * work: DEVICE workspace of na3d_cross_workspace(..., 0) bytes, 16-byte aligned,
  *   one call at a time; NULL where that is 0.
  * B, L, S, NH, NKV >= 1, NKV divides NH (else NA3D_ERR_SHAPE); HD: 16, 32, 64 or

@@ -176,41 +176,118 @@ struct Docs {
     __device__ __forceinline__ int of(int64_t b, int i) const { return at ? __ldg(at + b * n + i) : 0; }
 };
 
-// A warp's view of the column tiles of an entry, 32 at a time, one to a lane:
-// the smallest document >= 0 and the largest, and whether there is but one.
+// A warp's view of the column tiles of an entry, 32 at a time, one to a lane: the
+// smallest document >= 0 and the largest, and whether there is but one. Where a row
+// tile has several documents, each is looked for among the same tiles: the warp
+// then keeps the smallest and the largest document of 32 runs of them as well, and
+// looks at those that may hold the document. So documents whose states lie
+// together cost about their own tiles, documents that are scattered all of them
+// each. (A look at 4096 states takes 3.7 us. 5120 tokens of 256 documents, 4 heads
+// of 64 over 262144 states: sorted 118 -> 5.1 ms, in runs that come in any order
+// 118 -> 61; scattered over 16384 states 41, as without.) N: loads to a tile, 32
+// documents each.
+template <int N>
 struct Tiles {
     Docs docs;
-    int per;             // tokens to a tile
+    int per;             // tokens to a tile, up to 32 N
     Sync sync;
-    int64_t b = -1;
-    int first = -1;
-    int lo, hi;
-    bool pure;
+    int64_t b = -1, run_b = -1;
+    int first = -1, run_first = -1, run_tiles = 32;   // of the runs: the first tile, the tiles of each
+    int lo, hi, run_lo, run_hi;
+    bool pure, runs = false;
     __device__ __forceinline__ void look(int64_t entry, int tile) {
         if (entry == b && (tile & ~31) == first) return;
         b = entry;
         first = tile & ~31;
-        sync.still_going(threadIdx.x & 31);
-        const int i0 = (first + int(threadIdx.x & 31)) * per, end = min(i0 + per, docs.n);
+        const int lane = threadIdx.x & 31;
+        sync.still_going(lane);
         lo = INT_MAX;
         hi = INT_MIN;
-        int least = INT_MAX;
-        if (docs.at) {
-#pragma unroll 4
-            for (int i = i0; i < end; ++i) {
-                const int d = docs.of(b, i);
-                least = min(least, d);
-                lo = d >= 0 ? min(lo, d) : lo;
-                hi = max(hi, d);
+        pure = false;
+        if (!docs.at) {
+            if (int64_t(first + lane) * per < docs.n) {
+                lo = hi = 0;
+                pure = true;
             }
-        } else if (i0 < end) {
-            lo = hi = least = 0;
+            return;
         }
-        pure = least == hi;
+        constexpr int TILES = 8 / N;   // whose loads are in flight at once
+        const int32_t* at = docs.at + entry * docs.n + int64_t(first) * per + lane;
+#pragma unroll 1
+        for (int t0 = 0; t0 < 32; t0 += TILES, at += TILES * per) {
+            const int64_t left = docs.n - int64_t(first + t0) * per;   // documents from here on
+            if (left <= 0) break;
+            int d[TILES][N];
+            uint32_t negative = 0;   // tiles that hold negative ones
+            if (per == 32 * N && left >= TILES * 32 * N) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) d[t][j] = __ldg(at + 32 * (t * N + j));
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) negative |= uint32_t(d[t][j] >> 31) & 1u << t;
+            } else {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        const int i = 32 * j + lane;
+                        const bool in = i < per && t * per + i < left;
+                        d[t][j] = in ? __ldg(at + t * per + 32 * j) : INT_MIN;
+                        if (in && d[t][j] < 0) negative |= 1u << t;
+                    }
+            }
+            negative = __reduce_or_sync(kAll, negative);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                uint32_t least = uint32_t(d[t][0]);   // negative ones are above all others
+                int most = d[t][0];
+#pragma unroll
+                for (int j = 1; j < N; ++j) {
+                    least = min(least, uint32_t(d[t][j]));
+                    most = max(most, d[t][j]);
+                }
+                least = __reduce_min_sync(kAll, least);
+                most = __reduce_max_sync(kAll, most);
+                if (lane == t0 + t) {
+                    lo = int(min(least, uint32_t(INT_MAX)));
+                    hi = most;
+                    pure = !(negative >> t & 1u) && lo == hi;
+                }
+            }
+        }
+    }
+    // Before the tiles from k0 to k1 are looked through, for several documents or one.
+    __device__ __forceinline__ void begin(int64_t entry, int k0, int k1, bool several) {
+        runs = entry == run_b && k0 == run_first;
+        if (runs || !several || k1 - k0 <= 32) return;
+        runs = true;
+        run_b = entry;
+        run_first = k0;
+        run_tiles = (k1 - (k0 & ~31) + 1023) / 1024 * 32;
+        run_lo = INT_MAX;
+        run_hi = INT_MIN;
+        for (int t = k0 & ~31; t < k1; t += 32) {
+            look(entry, t);
+            const int least = __reduce_min_sync(kAll, lo), most = __reduce_max_sync(kAll, hi);
+            if (int(threadIdx.x & 31) == (t - (k0 & ~31)) / run_tiles) {
+                run_lo = min(run_lo, least);
+                run_hi = max(run_hi, most);
+            }
+        }
     }
     // The first tile from `tile` on, before `end`, that may hold document d; `end` where none does.
     __device__ __forceinline__ int find(int64_t entry, int tile, int end, int d, bool* whole) {
         while (tile < end) {
+            if (runs) {
+                const int start = run_first & ~31, run = (tile - start) / run_tiles;
+                const uint32_t can = __ballot_sync(kAll, run_lo <= d && d <= run_hi) & (kAll << run);
+                if (!can) return end;
+                tile = max(tile, start + (__ffs(can) - 1) * run_tiles);
+                if (tile >= end) return end;
+            }
             look(entry, tile);
             const uint32_t can = __ballot_sync(kAll, lo <= d && d <= hi) & (kAll << (tile & 31));
             if (can) {
@@ -345,7 +422,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
     using F = FwdShape<HD>;
     const bool lone = FEW && p.lone;
     const int lane = threadIdx.x & 31;
-    Tiles tiles{{p.kv_doc, p.S}, 128, sy};
+    Tiles<4> tiles{{p.kv_doc, p.S}, 128, sy};
     const Docs rows{p.doc, p.L};
     const bool plain = !p.doc && !p.kv_doc;   // every column is of every row's document
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
@@ -393,6 +470,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
                 for (int i = 0; i < 8; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(U.b, t0 + lane + 32 * i) : -1;
             const int k0 = U.split * p.per_split, k1 = min(k0 + p.per_split, p.tiles);
             int d = plain ? 0 : next_doc(doc, -1);
+            if (!plain) tiles.begin(U.b, k0, k1, next_doc(doc, d) >= 0);
             auto next = [&](Found* f) {   // from f->tile on, of document d or those behind it
                 if (plain) {
                     f->doc = 0;
@@ -1116,7 +1194,7 @@ struct BwdShape : Geom<HD> {
 };
 
 constexpr int kBwdThreads = 512;
-constexpr uint32_t kBwdSoftmax = 160, kBwdOut = 104, kBwdLow = 88;   // of 512 x 128
+constexpr uint32_t kBwdSoftmax = 144, kBwdOut = 112, kBwdLow = 112;   // of 512 x 128
 static_assert(2 * kBwdSoftmax + kBwdOut + kBwdLow <= 4 * 128, "register split");
 
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
@@ -1171,7 +1249,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                                              const CUtensorMap* tx0, const CUtensorMap* tx1, const CUtensorMap* ty0, const CUtensorMap* ty1) {
     using F = BwdShape<HD>;
     const int lane = threadIdx.x & 31;
-    Tiles tiles{{p.doc_c, p.nc}, p.cpt, sy};
+    Tiles<2> tiles{{p.doc_c, p.nc}, p.cpt, sy};
     const Docs rows{p.doc_r, p.nr};
     const bool plain = !p.doc_r && !p.doc_c;   // every column is of every row's document
     uint32_t told = 0, it = 0, x_n = 0;
@@ -1206,6 +1284,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
                 for (int i = 0; i < 4; ++i) doc[i] = lane + 32 * i < n_tok ? rows.of(b, t0 + lane + 32 * i) : -1;
             const int k0 = split * p.per_split, k1 = min(k0 + p.per_split, p.tiles_c);
             int d = plain ? 0 : next_doc(doc, -1);
+            if (!plain) tiles.begin(b, k0, k1, next_doc(doc, d) >= 0);
             // of document d from the tile on, or of those behind it; the columns of this lane that are
             auto mine = [&](int tile, int dd, int i) {
                 const int t = tile * p.cpt + ctok[i];

@@ -67,3 +67,39 @@ def test_a_search_may_take_its_time():
     want = ref.cross(q, end[:, :, 0], end[:, :, 1], (doc != 256).to(torch.int32))
     check("out", out, want["out"])
     check("lse", lse, want["lse"])
+
+
+@pytest.mark.parametrize("order", ["sorted", "shuffled", "mixed"])
+@pytest.mark.parametrize("B,L,S,NKV,docs", [
+    (1, 600, 20000, 2, 300),     # the states split over blocks
+    (1, 600, 9300, 20, 300),     # ... in two
+    (1, 600, 9000, 26, 300),     # not split
+    (2, 5000, 300, 2, 200),      # many tokens to a state's tile
+    (1, 257, 70000, 1, 257),
+], ids=str)
+def test_hundreds_of_documents(B, L, S, NKV, docs, order):
+    """Documents one behind another, scattered, and in runs that come in any order; some
+    without states, some without tokens."""
+    HD = 16
+    q, kv, g = make((B, 1, 1, L, NKV, HD), S, NKV, 4)
+    gen = torch.Generator().manual_seed(5)
+    doc, kv_doc = torch.arange(L) * docs // L, torch.arange(S) * docs // S
+    if order == "mixed":
+        doc, kv_doc = torch.randperm(docs, generator=gen)[doc], torch.randperm(docs, generator=gen)[kv_doc]
+    doc, kv_doc = doc.expand(B, L).clone(), kv_doc.expand(B, S).clone()
+    if order == "shuffled":
+        doc, kv_doc = (torch.stack([x[b, torch.randperm(x.shape[1], generator=gen)] for b in range(B)]) for x in (doc, kv_doc))
+    doc[doc % 17 == 3] = -1
+    kv_doc[kv_doc % 13 == 5] = -2 ** 31
+    doc, kv_doc = doc.to(torch.int32).view(B, 1, 1, L), kv_doc.to(torch.int32)
+    want = ref.cross(q, kv[:, :, 0], kv[:, :, 1], doc, kv_doc, g)
+    q, kv, g, doc, kv_doc = (x.cuda() for x in (q, kv, g, doc, kv_doc))
+    k, v = kv.unbind(2)
+    out, lse = na.na3d_cross_attention(q, k, v, doc=doc, kv_doc=kv_doc, return_lse=True)
+    dq, dkv = torch.full_like(q, float("nan")), torch.full_like(kv, float("nan"))
+    na.na3d_cross_bwd(q, k, v, out, lse, g, dq, *dkv.unbind(2), doc=doc, kv_doc=kv_doc)
+    torch.cuda.synchronize()
+    assert na.na3d_device_status() == 0
+    got = dict(out=out, lse=lse, dq=dq, dk=dkv[:, :, 0], dv=dkv[:, :, 1])
+    for name in want:
+        check(name, got[name], want[name])
