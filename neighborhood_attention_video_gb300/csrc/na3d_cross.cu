@@ -412,19 +412,24 @@ struct FwdShape : Geom<HD> {
 };
 
 constexpr int kFwdThreads = 512;
-// registers: what the softmax, the way out and the rest take of 512 x 128
-constexpr uint32_t kRegsSoftmax = 144, kRegsOut = 112, kRegsLow = 112;
-static_assert(2 * kRegsSoftmax + kRegsOut + kRegsLow <= 4 * 128, "register split");
+enum { kPlain, kDocuments, kFew };   // kernels of calls without documents, with them, of few rows
+// registers: what the softmax, the way out and the rest take of 512 x 128. The producer needs few where it
+// does not search (24576 tokens over 6144 states 781 -> 751 us with more for the softmax).
+template <int KIND>
+struct FwdRegs {
+    static constexpr uint32_t kSoftmax = KIND == kPlain ? 160 : 144, kOut = 112, kLow = KIND == kPlain ? 80 : 112;
+    static_assert(2 * kSoftmax + kOut + kLow <= 4 * 128, "register split");
+};
 
-template <int HD, bool FEW>
+template <int HD, int KIND>
 __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy, uint32_t base, uint8_t* base_ptr, Step* steps, volatile uint32_t* said,
                                              const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv) {
     using F = FwdShape<HD>;
-    const bool lone = FEW && p.lone;
+    const bool lone = KIND == kFew && p.lone;
     const int lane = threadIdx.x & 31;
     Tiles<4> tiles{{p.kv_doc, p.S}, 128, sy};
     const Docs rows{p.doc, p.L};
-    const bool plain = !p.doc && !p.kv_doc;   // every column is of every row's document
+    const bool plain = KIND == kPlain || (!p.doc && !p.kv_doc);   // every column is of every row's document
     uint32_t told = 0, slot_n = 0, q_n[2] = {0, 0};
 
     // One operand tile into the next slot, with its step's flags.
@@ -631,7 +636,7 @@ __device__ __forceinline__ void fwd_scores(const Sync& sy, uint32_t base, uint32
     if (yes) drained(sy.bar(F::B_DRAIN + a), 0);
 }
 
-template <int HD>
+template <int HD, int KIND>
 __device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, const uint8_t* base_ptr, uint32_t tmem, const volatile uint32_t* said) {
     using F = FwdShape<HD>;
     constexpr uint32_t id_o = make_idesc_bf16(128, HD, 0, 1);
@@ -646,7 +651,7 @@ __device__ __forceinline__ void fwd_products(const Sync& sy, uint32_t base, cons
             if (!sy.wait_warp(sy.bar(F::B_VFULL + v.st), v.par)) return;
             const uint32_t flags = __reduce_or_sync(kAll, said[v.st]);
             if (flags & kEnd) return;
-            if (flags & kForeign) {
+            if (KIND != kPlain && (flags & kForeign)) {
                 // Columns of other documents, whose probabilities are 0: 0 times their values must be 0. By
                 // this warp, since it waits for every v; who did so for some alone could take the phase of an
                 // earlier one, still on its way, for its own.
@@ -803,10 +808,10 @@ __device__ __forceinline__ void fwd_softmax(const Sync& sy, uint8_t* base_ptr, u
 // The sums of a pass on their way out, by warps of their own: the softmax goes on
 // with the next rows meanwhile. (With its own threads' stores in its way a unit of
 // four steps took 11.3 us, 7.8 of them its steps.)
-template <int HD, bool FEW>
+template <int HD, int KIND>
 __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint8_t* base_ptr, uint32_t tmem, const Step* steps) {
     using F = FwdShape<HD>;
-    const bool lone = FEW && p.lone, split = FEW && p.splits > 1;
+    const bool lone = KIND == kFew && p.lone, split = KIND == kFew && p.splits > 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + F::TM_O;
     const float2* const stat = reinterpret_cast<const float2*>(base_ptr + F::OFF_STAT) + r;
@@ -891,7 +896,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
             for (int a = 0; a < 2; ++a) {
                 const int i = a * p.rpt + tok;
                 row[a] = tok < p.rpt && t0 + i < p.L && !(a && lone) ? row0 + int64_t(i) * p.NH + g : -1;
-                doc[a] = row[a] >= 0 && p.doc ? __ldg(p.doc + token0 + i) : 0;
+                doc[a] = KIND != kPlain && row[a] >= 0 && p.doc ? __ldg(p.doc + token0 + i) : 0;
                 written[a] = false;
             }
         }
@@ -1014,7 +1019,7 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 //   warp 12           finds the column tiles that the rows see, TMA;
 //   warps 13, 14      issue the scores of either row tile; 13 owns the tensor memory;
 //   warp 15           issues the products.
-template <int HD, bool FEW>
+template <int HD, int KIND>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const __grid_constant__ FwdParams p) {
@@ -1059,16 +1064,16 @@ cross_fwd_tiles(const __grid_constant__ CUtensorMap tq, const __grid_constant__ 
     const uint32_t tmem = misc[0];
     dependents_may_start();
     if (warp < 8) {
-        regs_increase<kRegsSoftmax>();
+        regs_increase<FwdRegs<KIND>::kSoftmax>();
         fwd_softmax<HD>(sy, base_ptr, tmem, steps);
     } else if (warp < 12) {
-        regs_decrease<kRegsOut>();
-        fwd_out<HD, FEW>(p, sy, base_ptr, tmem, steps);
+        regs_decrease<FwdRegs<KIND>::kOut>();
+        fwd_out<HD, KIND>(p, sy, base_ptr, tmem, steps);
     } else {
-        regs_decrease<kRegsLow>();
-        if (warp == 12) fwd_producer<HD, FEW>(p, sy, base, base_ptr, steps, misc + 3, &tq, &tk, &tv);
+        regs_decrease<FwdRegs<KIND>::kLow>();
+        if (warp == 12) fwd_producer<HD, KIND>(p, sy, base, base_ptr, steps, misc + 3, &tq, &tk, &tv);
         if (warp == 13 || warp == 14) fwd_scores<HD>(sy, base, __reduce_or_sync(kAll, tmem), misc + 3, warp - 13);
-        if (warp == 15) fwd_products<HD>(sy, base, base_ptr, __reduce_or_sync(kAll, tmem), misc + 3);
+        if (warp == 15) fwd_products<HD, KIND>(sy, base, base_ptr, __reduce_or_sync(kAll, tmem), misc + 3);
     }
     tc_fence_before();
     __syncthreads();
@@ -1857,7 +1862,7 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     if (!encode_heads(&tq, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, p.rpt) || !encode_heads(&tk, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, 128) ||
         !encode_heads(&tv, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, 128))
         return cudaErrorInvalidValue;
-    const auto kernel = p.lone || p.splits > 1 ? cross_fwd_tiles<HD, true> : cross_fwd_tiles<HD, false>;
+    const auto kernel = p.lone || p.splits > 1 ? cross_fwd_tiles<HD, kFew> : p.doc || p.kv_doc ? cross_fwd_tiles<HD, kDocuments> : cross_fwd_tiles<HD, kPlain>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdShape<HD>::SMEM);
     if (e != cudaSuccess) return e;
     kernel<<<unsigned(units < sms ? units : sms), kFwdThreads, FwdShape<HD>::SMEM, stream>>>(tq, tk, tv, p);
