@@ -572,7 +572,7 @@ __device__ __forceinline__ void fwd_producer(const FwdParams& p, const Sync& sy,
         for (uint32_t n = slot_n < F::SLOTS ? 0u : slot_n - F::SLOTS; n < slot_n; ++n)   // k's are even
             drained(sy.bar((n & 1u ? F::B_VFULL : F::B_KFULL) + n % F::SLOTS), (n / 2u / F::CYCLE) & 1u);
         for (int a = 0; a < 2; ++a)
-            for (uint32_t n = q_n[a] < 1u ? 0u : q_n[a] - 1u; n < q_n[a]; ++n) drained(sy.bar(F::B_QFULL + a), n & 1u);
+            if (q_n[a]) drained(sy.bar(F::B_QFULL + a), (q_n[a] - 1u) & 1u);
     }
 }
 
