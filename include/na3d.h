@@ -352,8 +352,10 @@ int na3d_rope_table(float* table, int64_t T, int64_t H, int64_t W, int64_t RT, i
  * R turns P = (RT + RH + RW) / 2 pairs of the first 2 P values, (a, b) to
  * (a cos - b sin, b cos + a sin), by the table's angles: the first RT / 2 pairs
  * by t's, the next RH / 2 by h's, the next RW / 2 by w's. Pair i is (2 i, 2 i + 1)
- * where `interleaved`, else (i, P + i). Values from 2 P on do not turn. Sums are
- * fp32, the result is rounded to bf16 once.
+ * where `interleaved`, else (i, P + i). Values from 2 P on do not turn: without the
+ * norm they stay what they are and reach no other. Sums are fp32 (a head whose mean
+ * square leaves its range, by values of some 2^63, is normed to 0), the result is
+ * rounded to bf16 once.
  *
  * The attention wants q scaled by HD^-0.5: that is q_scale here, since the norm
  * takes away the scale that na3d_qkv_proj gives. A norm of q so scaled with

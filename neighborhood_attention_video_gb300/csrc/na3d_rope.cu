@@ -79,18 +79,21 @@ __device__ __forceinline__ uint4 load16(const uint16_t* p) {
     return v;
 }
 
-// The 16 values turned by the eight pairs' angles (DIR 1) or back (-1).
-template <bool INTER, int DIR>
-__device__ __forceinline__ void turn(uint64_t (&f)[8], const float2 (&cs)[8]) {
+// The 16 values turned by the eight pairs' angles (DIR 1) or back (-1). PART: the pairs
+// in `still` (a bit each; all or none of them where the pairs are halves) stay what they
+// are; products by 1 and 0 would spread what is not finite among them.
+template <bool INTER, bool PART, int DIR>
+__device__ __forceinline__ void turn(uint64_t (&f)[8], const float2 (&cs)[8], uint32_t still) {
     if (INTER) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float a, b;
             const float c = cs[i].x, s = DIR * cs[i].y;
             f2_unpack(f[i], a, b);
-            f[i] = f2_pack(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
+            const uint64_t turned = f2_pack(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
+            f[i] = PART && (still >> i & 1u) ? f[i] : turned;
         }
-    } else {
+    } else if (!PART || !still) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint64_t c = f2_pack(cs[2 * i].x, cs[2 * i + 1].x), s = f2_pack(DIR * cs[2 * i].y, DIR * cs[2 * i + 1].y);
@@ -121,7 +124,7 @@ __device__ __forceinline__ float sum_of_head(float v) {
 // 202 us, 6.0 TB/s. 65536 tokens, 8 heads of 64 each: 53 us, 5.0 TB/s; backward 95
 // us, 4.2 TB/s: what a token takes before its few values (its place, its cosines)
 // is a good part of the instructions. Heads of 8 and 1: 44 us and 89 us.
-template <int HD, bool INTER, bool BWD, int U, bool BOTH>
+template <int HD, bool INTER, bool PART, bool BWD, int U, bool BOTH>
 __global__ void __launch_bounds__(kWarps * 32, BWD || BOTH ? 2 : 3) norm_rope(const __grid_constant__ RopeParams p, int q_blocks) {
     static_assert(!BOTH || (U == 2 && !BWD), "q and k at once");
     constexpr int LPH = HD / 16, HPW = 32 / LPH, SIDES = BOTH ? 2 : 1;
@@ -137,6 +140,12 @@ __global__ void __launch_bounds__(kWarps * 32, BWD || BOTH ? 2 : 3) norm_rope(co
     const int ca = apart ? 8 * l : 2 * P + 16 * (l - P / 8), cb = ca + (INTER ? HD / 2 : apart ? P : 8);
     // the first of the pairs of either piece (the same four and four, INTER; else eight in a row)
     const int pa = INTER ? ca / 2 : apart ? ca : P, pb = INTER ? cb / 2 : pa + 4;
+
+    uint32_t still = apart ? 0u : 255u;   // PART: pairs of this lane that do not turn
+    if (PART && INTER)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i < 4 ? pa + i : pb + i - 4) >= P) still |= 1u << i;
 
     uint64_t wt[SIDES][8];   // weight and scale
 #pragma unroll
@@ -204,11 +213,11 @@ __global__ void __launch_bounds__(kWarps * 32, BWD || BOTH ? 2 : 3) norm_rope(co
                 if (!BWD) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = f2_mul(f2_mul(f[i], r2), wt[s][i]);
-                    turn<INTER, 1>(f, cs);
+                    turn<INTER, PART, 1>(f, cs, still);
                 } else {
                     uint64_t e[8];
                     unpack(g[u], e);
-                    turn<INTER, -1>(e, cs);
+                    turn<INTER, PART, -1>(e, cs, still);
                     if (p.norm) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -312,14 +321,14 @@ int64_t rope_workspace(int64_t HD) { return int64_t(kGradBlocks) * HD * 4; }
 
 namespace {
 
-template <int HD, bool INTER, bool BWD, int U, bool BOTH>
+template <int HD, bool INTER, bool PART, bool BWD, int U, bool BOTH>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     constexpr int batch = 32 / (HD / 16) * U;
     const int NQ = p.side[0].heads, NK = p.side[1].heads;
     const int64_t want = (p.tokens + kWarps - 1) / kWarps;   // blocks for each of q and k
     if (BOTH) {
         const unsigned blocks = unsigned(min(want, int64_t(sms) * 2));
-        norm_rope<HD, INTER, BWD, U, BOTH><<<blocks, kWarps * 32, 0, stream>>>(p, int(blocks));
+        norm_rope<HD, INTER, PART, BWD, U, BOTH><<<blocks, kWarps * 32, 0, stream>>>(p, int(blocks));
         return cudaGetLastError();
     }
     const int most = BWD ? kGradBlocks : sms * 3;
@@ -331,7 +340,7 @@ cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     dim3 grid(unsigned(q_blocks + k_blocks));
     // few tokens: a token's heads over several blocks
     grid.y = unsigned(max(1, min((max(NQ, NK) + batch - 1) / batch, most / int(grid.x))));
-    norm_rope<HD, INTER, BWD, U, BOTH><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
+    norm_rope<HD, INTER, PART, BWD, U, BOTH><<<grid, kWarps * 32, 0, stream>>>(p, q_blocks);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !BWD || !p.work) return e;
     norm_rope_sum<<<(HD + 31) / 32 * 2, 1024, 0, stream>>>(p.work, int(q_blocks * grid.y), int(grid.x * grid.y), HD,
@@ -347,15 +356,28 @@ void division(int32_t d, uint64_t* by, int32_t* s) {
     *by = (uint64_t(1) << *s) / uint32_t(d) + 1;
 }
 
-template <int HD, bool INTER, bool BWD>
+template <int HD, bool INTER, bool PART, bool BWD>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t stream) {
     // Heads enough for two batches at a time; else q's and k's at once, which reads a token's
     // cosines once (8 heads of 64 each: 53 us, 64 by blocks of their own; of 8 and 1: 44, 161).
     // Backward the second side's sums and weights do not fit the registers.
-    if (max(p.side[0].heads, p.side[1].heads) > 32 / (HD / 16)) return launch<HD, INTER, BWD, 2, false>(p, sms, stream);
+    if (max(p.side[0].heads, p.side[1].heads) > 32 / (HD / 16)) return launch<HD, INTER, PART, BWD, 2, false>(p, sms, stream);
     if constexpr (!BWD)
-        if (p.side[1].heads) return launch<HD, INTER, BWD, 2, true>(p, sms, stream);
-    return launch<HD, INTER, BWD, 1, false>(p, sms, stream);
+        if (p.side[1].heads) return launch<HD, INTER, PART, BWD, 2, true>(p, sms, stream);
+    return launch<HD, INTER, PART, BWD, 1, false>(p, sms, stream);
+}
+
+template <int HD>
+cudaError_t launch(const RopeParams& p, bool backward, int sms, cudaStream_t stream) {
+    // Heads that turn whole do without the choice between turned and kept pairs (backward, 49152
+    // tokens with 16 heads of 128 each: 202 us, 208 with it).
+    const bool part = 2 * (p.PT + p.PH + p.PW) < HD;
+    if (p.interleaved) {
+        if (part) return backward ? launch<HD, true, true, true>(p, sms, stream) : launch<HD, true, true, false>(p, sms, stream);
+        return backward ? launch<HD, true, false, true>(p, sms, stream) : launch<HD, true, false, false>(p, sms, stream);
+    }
+    if (part) return backward ? launch<HD, false, true, true>(p, sms, stream) : launch<HD, false, true, false>(p, sms, stream);
+    return backward ? launch<HD, false, false, true>(p, sms, stream) : launch<HD, false, false, false>(p, sms, stream);
 }
 
 }  // namespace
@@ -365,11 +387,7 @@ cudaError_t launch_rope(int hd, const RopeParams& args, bool backward, int sms, 
     division(p.W, &p.by_w, &p.s_w);
     division(p.H, &p.by_h, &p.s_h);
     division(p.T, &p.by_t, &p.s_t);
-#define X(n) \
-    if (hd == n) {                                                                                        \
-        if (p.interleaved) return backward ? launch<n, true, true>(p, sms, stream) : launch<n, true, false>(p, sms, stream); \
-        return backward ? launch<n, false, true>(p, sms, stream) : launch<n, false, false>(p, sms, stream); \
-    }
+#define X(n) if (hd == n) return launch<n>(p, backward, sms, stream);
     X(16) X(32) X(64) X(128) X(256) X(512)
 #undef X
     return cudaErrorInvalidValue;
