@@ -129,20 +129,24 @@ def na3d_status_string(status: int) -> str:
 
 _torch = None
 _cuda_ok = None   # torch.cuda.is_available(), fixed for the process
+_get_device = None
 
 
 def _torch_module():
-    global _torch, _cuda_ok
+    global _torch, _cuda_ok, _get_device
     if _torch is None:
         import torch
-        _torch = torch
-        _cuda_ok = torch.cuda.is_available()
+        ok = torch.cuda.is_available()
+        if ok:
+            torch.cuda.init()   # which torch.cuda.current_device() does, and the call that is quicker does not
+            _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _torch, _cuda_ok = torch, ok
     return _torch
 
 
 def _device() -> int:
     """The current CUDA device, -2 where there is none (behind _torch_module())."""
-    return _torch._C._cuda_getDevice() if _cuda_ok else -2
+    return _get_device() if _cuda_ok else -2
 
 
 def _check_bf16_on_device(tensors):
