@@ -1282,7 +1282,7 @@ __device__ __forceinline__ void bwd_producer(const BwdParams& p, const Sync& sy,
             const int64_t b = rest % p.B;
             const int split = rest / p.B;
             const int t0 = tile_r * p.rpt, n_tok = min(p.rpt, p.nr - t0);
-            const int64_t token0 = b * p.nr + t0, row0 = token0 * p.heads + kh * p.Gr + split * 2 * p.rows;
+            const int64_t token0 = b * p.nr + t0, row0 = token0 * p.heads + kh * p.Gr + split * (DKV ? 2 : 1) * p.rows;
             int doc[4] = {};
             if (!plain)
 #pragma unroll
@@ -1767,7 +1767,7 @@ __global__ void __launch_bounds__(256) cross_sum(const BwdParams p, int grads) {
     float o[4] = {};
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part + ((int64_t(s) * 2 + n) * p.rows + row) * HD + c);
+        const float4 v = *reinterpret_cast<const float4*>(p.part + ((int64_t(s) * grads + n) * p.rows + row) * HD + c);
         o[0] += v.x;
         o[1] += v.y;
         o[2] += v.z;
@@ -1876,7 +1876,7 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
 // How a backward pass is shared out: `units` row tiles over `tiles` column tiles each, in so
 // many splits that the blocks' rounds hold the least of column tiles.
 struct BwdPlan {
-    int64_t rpt, cpt, tiles_r, tiles_c, splits, per_split, rows;
+    int64_t rpt, cpt, tiles_r, tiles_c, splits, per_split, rows, grads;
     BwdPlan(bool dkv, int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV) {
         const int64_t G = NH / NKV;
         rpt = dkv ? 128 : 128 / G;
@@ -1884,6 +1884,7 @@ struct BwdPlan {
         tiles_r = ceil_div(dkv ? S : L, rpt);
         tiles_c = ceil_div(dkv ? L : S, cpt);
         rows = dkv ? B * S * NKV : B * L * NH;
+        grads = dkv ? 2 : 1;
         const int64_t units = B * NKV * tiles_r;
         splits = 1;
         // a unit's beginning and end cost some four column tiles, a split's sums their memory
@@ -1898,7 +1899,7 @@ struct BwdPlan {
         per_split = ceil_div(tiles_c, splits);
         splits = ceil_div(tiles_c, per_split);
     }
-    int64_t part_bytes(int64_t HD) const { return splits > 1 ? splits * 2 * rows * HD * 4 : 0; }
+    int64_t part_bytes(int64_t HD) const { return splits > 1 ? splits * grads * rows * HD * 4 : 0; }
 };
 
 template <int HD, bool DKV>
@@ -1958,12 +1959,12 @@ cudaError_t bwd_pass(const CrossParams& c, int sms, cudaStream_t stream) {
     cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(unsigned(ceil_div(pl.rows * (HD / 4), 256)), DKV ? 2 : 1);
+    cfg.gridDim = dim3(unsigned(ceil_div(pl.rows * (HD / 4), 256)), unsigned(pl.grads));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cross_sum<HD>, p, DKV ? 2 : 1);
+    return cudaLaunchKernelEx(&cfg, cross_sum<HD>, p, int(pl.grads));
 }
 
 template <int HD>
