@@ -89,3 +89,24 @@ def test_short_documents_take_delta_from_the_sum(B, L, NH, HD, n, pad):
     want = ref.cross(q, k, v, dout=g)["dq"][0]
     once = (want.to(BF16).to(F64) - want).norm()
     assert (got["dq"].cpu().to(F64) - want).norm() <= 1.2 * once
+
+
+@pytest.mark.parametrize("B,L,S,NH,NKV,HD,docs", [(3, 120, 130, 4, 2, 64, 2), (2, 700, 300, 3, 3, 32, 3), (3, 1300, 520, 16, 16, 16, 2),
+                                                  (2, 5, 2000, 8, 1, 128, 1)], ids=str)
+def test_an_entry_is_the_entry_by_itself(B, L, S, NH, NKV, HD, docs):
+    """All five results of an entry of a batch and of the entry alone, which may be shared
+    out over blocks otherwise: each within its bound of the same value, so within two of
+    one another; of a row that sees nothing, the same."""
+    q, kv, g = make((B, 1, 1, L, NH, HD), S, NKV, 16)
+    gen = torch.Generator().manual_seed(17)
+    doc = torch.randint(-1, docs, (B, 1, 1, L), generator=gen).to(torch.int32)
+    kv_doc = torch.randint(-1, docs + 1, (B, S), generator=gen).sort(1).values.to(torch.int32)
+    both = run(q, kv, g, doc, kv_doc)
+    want = ref.cross(q, kv[:, :, 0], kv[:, :, 1], doc, kv_doc, g)
+    for b in range(B):
+        one = run(*(x[b:b + 1].contiguous() for x in (q, kv, g, doc, kv_doc)))
+        for name, (value, bound) in want.items():
+            x, y, off = one[name][0].cpu().to(F64), both[name][b].cpu().to(F64), bound[b]
+            unseen = torch.isinf(value[b])
+            assert torch.equal(torch.isinf(x), unseen) and torch.equal(torch.isinf(y), unseen), name
+            assert ((x - y).abs() <= 2 * off)[~unseen].all(), name
