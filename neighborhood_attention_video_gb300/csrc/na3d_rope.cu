@@ -52,12 +52,6 @@ __device__ __forceinline__ Piece pack(const uint64_t (&f)[8]) {
     return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // The sum of the products of 16 values.
 __device__ __forceinline__ float dot(const uint64_t (&a)[8], const uint64_t (&b)[8]) {
     uint64_t s = f2_mul(a[0], b[0]), t = f2_mul(a[1], b[1]);
@@ -71,7 +65,7 @@ __device__ __forceinline__ float dot(const uint64_t (&a)[8], const uint64_t (&b)
     return x + y;
 }
 
-// Data that is used once: past L1, and the first to leave L2.
+// Data that is used once: past L1.
 __device__ __forceinline__ uint4 load16(const uint16_t* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

@@ -307,11 +307,6 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c, uint32_t region) {
     return (c >> 3) * region + uint32_t(r) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t f2_dup(float x) { return f2_pack(x, x); }
 
 // tanh z = z + z^3 P(z^2) for |z| <= 1/2.
