@@ -490,6 +490,18 @@ int na3d_selftest_withhold(const void* q, const void* k, const void* v, void* ou
                            int64_t B, int64_t T, int64_t H, int64_t W, int64_t NH, int64_t HD,
                            int64_t KT, int64_t KH, int64_t KW, int64_t chunk, void* stream);
 
+/*
+ * na3d_cross_selftest_withhold - the same for na3d_cross_fwd (dout NULL; dq, dk and
+ * dv are not looked at) and na3d_cross_bwd, on contiguous tensors: of each tile of
+ * rows one token less is loaded than the wait for it counts. Every block gives up
+ * after about 2 s (backward in each of the two passes). NH * HD and the other sizes,
+ * workspaces and errors as there; the results are left partly unwritten.
+ */
+int na3d_cross_selftest_withhold(const void* q, const void* k, const void* v, void* out, float* lse,
+                                 const void* dout, void* dq, void* dk, void* dv, void* work, int64_t B,
+                                 int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD,
+                                 const int32_t* doc, const int32_t* kv_doc, void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* na3d_status_string(int status);
 

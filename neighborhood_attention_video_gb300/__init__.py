@@ -31,7 +31,7 @@ EXPORTED_SYMBOLS = ("na3d_fwd", "na3d_fwd_strided", "na3d_fwd_region", "na3d_qkv
                     "na3d_lora_qkv_proj", "na3d_lora_qkv_proj_bwd", "na3d_lora_workspace",
                     "na3d_rope_table", "na3d_norm_rope", "na3d_norm_rope_bwd", "na3d_norm_rope_workspace",
                     "na3d_cross_fwd", "na3d_cross_bwd", "na3d_cross_workspace",
-                    "na3d_selftest_withhold", "na3d_status_string", "na3d_plan",
+                    "na3d_selftest_withhold", "na3d_cross_selftest_withhold", "na3d_status_string", "na3d_plan",
                     "na3d_device_status")
 
 NA3D_OK = 0
@@ -113,6 +113,8 @@ def load_library():
     lib.na3d_cross_workspace.restype = _I64
     lib.na3d_selftest_withhold.argtypes = [_P, _P, _P, _P] + [_I64] * 10 + [_P]
     lib.na3d_selftest_withhold.restype = ctypes.c_int
+    lib.na3d_cross_selftest_withhold.argtypes = [_P] * 10 + [_I64] * 6 + [_P] * 3
+    lib.na3d_cross_selftest_withhold.restype = ctypes.c_int
     lib.na3d_status_string.argtypes = [ctypes.c_int]
     lib.na3d_status_string.restype = ctypes.c_char_p
     lib.na3d_plan.argtypes = [_I64] * 8 + [ctypes.POINTER(PlanInfo)]

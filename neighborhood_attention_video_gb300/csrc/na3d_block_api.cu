@@ -251,18 +251,9 @@ na3d::CrossParams cross_params(const Rows* in, int64_t B, int64_t L, int64_t S, 
     return p;
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t na3d_cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, int backward) {
-    return check_cross(B, L, S, NH, NKV, HD) == NA3D_OK ? na3d::cross_workspace(B, L, S, NH, NKV, HD, backward != 0) : -1;
-}
-
-int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* work, int64_t B,
-                   int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, int64_t q_token_stride,
-                   int64_t k_token_stride, int64_t v_token_stride, const int32_t* doc, const int32_t* kv_doc,
-                   void* stream) {
+int cross_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* work, int64_t B, int64_t L,
+              int64_t S, int64_t NH, int64_t NKV, int64_t HD, int64_t q_token_stride, int64_t k_token_stride,
+              int64_t v_token_stride, const int32_t* doc, const int32_t* kv_doc, void* stream, bool withhold) {
     if (const int rc = check_cross(B, L, S, NH, NKV, HD)) return rc;
     const int64_t need = na3d::cross_workspace(B, L, S, NH, NKV, HD, false);
     if (!q || !k || !v || !out || (need && !work)) return NA3D_ERR_NULL;
@@ -289,14 +280,15 @@ int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float
     na3d::CrossParams p = cross_params(in, B, L, S, NH, NKV, doc, kv_doc, work);
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
+    p.withhold = withhold;
     return na3d::launch_cross_fwd(int(HD), p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? NA3D_OK : NA3D_ERR_CUDA;
 }
 
-int na3d_cross_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
-                   void* dq, void* dk, void* dv, void* work, int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV,
-                   int64_t HD, int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
-                   int64_t dq_token_stride, int64_t dk_token_stride, int64_t dv_token_stride, const int32_t* doc,
-                   const int32_t* kv_doc, void* stream) {
+int cross_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout, void* dq,
+              void* dk, void* dv, void* work, int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD,
+              int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride, int64_t dq_token_stride,
+              int64_t dk_token_stride, int64_t dv_token_stride, const int32_t* doc, const int32_t* kv_doc, void* stream,
+              bool withhold) {
     if (const int rc = check_cross(B, L, S, NH, NKV, HD)) return rc;
     const void* const all[10] = {q, k, v, out, lse, dout, dq, dk, dv, work};
     for (const void* p : all)
@@ -334,7 +326,42 @@ int na3d_cross_bwd(const void* q, const void* k, const void* v, const void* out,
     p.dq = static_cast<uint16_t*>(dq);
     p.dk = static_cast<uint16_t*>(dk);
     p.dv = static_cast<uint16_t*>(dv);
+    p.withhold = withhold;
     return na3d::launch_cross_bwd(int(HD), p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? NA3D_OK : NA3D_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t na3d_cross_workspace(int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, int backward) {
+    return check_cross(B, L, S, NH, NKV, HD) == NA3D_OK ? na3d::cross_workspace(B, L, S, NH, NKV, HD, backward != 0) : -1;
+}
+
+int na3d_cross_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* work, int64_t B,
+                   int64_t L, int64_t S, int64_t NH, int64_t NKV, int64_t HD, int64_t q_token_stride,
+                   int64_t k_token_stride, int64_t v_token_stride, const int32_t* doc, const int32_t* kv_doc,
+                   void* stream) {
+    return cross_fwd(q, k, v, out, lse, work, B, L, S, NH, NKV, HD, q_token_stride, k_token_stride, v_token_stride, doc, kv_doc,
+                     stream, false);
+}
+
+int na3d_cross_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
+                   void* dq, void* dk, void* dv, void* work, int64_t B, int64_t L, int64_t S, int64_t NH, int64_t NKV,
+                   int64_t HD, int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                   int64_t dq_token_stride, int64_t dk_token_stride, int64_t dv_token_stride, const int32_t* doc,
+                   const int32_t* kv_doc, void* stream) {
+    return cross_bwd(q, k, v, out, lse, dout, dq, dk, dv, work, B, L, S, NH, NKV, HD, q_token_stride, k_token_stride,
+                     v_token_stride, dq_token_stride, dk_token_stride, dv_token_stride, doc, kv_doc, stream, false);
+}
+
+int na3d_cross_selftest_withhold(const void* q, const void* k, const void* v, void* out, float* lse, const void* dout,
+                                 void* dq, void* dk, void* dv, void* work, int64_t B, int64_t L, int64_t S, int64_t NH,
+                                 int64_t NKV, int64_t HD, const int32_t* doc, const int32_t* kv_doc, void* stream) {
+    if (!dout)
+        return cross_fwd(q, k, v, out, lse, work, B, L, S, NH, NKV, HD, NH * HD, NKV * HD, NKV * HD, doc, kv_doc, stream, true);
+    return cross_bwd(q, k, v, out, lse, dout, dq, dk, dv, work, B, L, S, NH, NKV, HD, NH * HD, NKV * HD, NKV * HD, NH * HD,
+                     NKV * HD, NKV * HD, doc, kv_doc, stream, true);
 }
 
 }  // extern "C"

@@ -1854,7 +1854,7 @@ cudaError_t fwd(const CrossParams& c, int sms, cudaStream_t stream) {
     p.part = static_cast<float*>(c.work);
     p.part_lse = p.part + pl.splits * p.rows * HD;
     CUtensorMap tq, tk, tv;
-    if (!encode_heads(&tq, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, p.rpt) || !encode_heads(&tk, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, 128) ||
+    if (!encode_heads(&tq, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, p.rpt - c.withhold) || !encode_heads(&tk, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, 128) ||
         !encode_heads(&tv, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, 128))
         return cudaErrorInvalidValue;
     const auto kernel = p.lone || p.splits > 1 ? cross_fwd_tiles<HD, kFew> : p.doc || p.kv_doc ? cross_fwd_tiles<HD, kDocuments> : cross_fwd_tiles<HD, kPlain>;
@@ -1939,7 +1939,7 @@ cudaError_t bwd_pass(const CrossParams& c, int sms, cudaStream_t stream) {
     }
     const int64_t row = int64_t(c.NH) * HD;
     CUtensorMap q, d, k, v;
-    const int qt = DKV ? p.cpt : p.rpt, kt = DKV ? 128 : 64;
+    const int qt = DKV ? p.cpt : p.rpt - c.withhold, kt = DKV ? p.rpt - c.withhold : p.cpt;
     if (!encode_heads(&q, c.q, HD, c.B, c.L, c.NH, c.q_ts, p.G, qt) || !encode_heads(&d, c.dout, HD, c.B, c.L, c.NH, row, p.G, qt) ||
         !encode_heads(&k, c.k, HD, c.B, c.S, c.NKV, c.k_ts, 1, kt) || !encode_heads(&v, c.v, HD, c.B, c.S, c.NKV, c.v_ts, 1, kt))
         return cudaErrorInvalidValue;

@@ -17,6 +17,7 @@ struct CrossParams {
     uint16_t *dq, *dk, *dv;
     const int32_t *doc, *kv_doc;     // (B, L), (B, S) or null: all 0
     void* work;
+    bool withhold;                   // self-test: of each row tile's last token nothing is loaded, which its wait misses
 };
 
 // Bytes of workspace a forward or backward call uses.

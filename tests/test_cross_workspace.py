@@ -12,3 +12,14 @@ def test_sums_of_dq_take_one_gradients_room():
         need = na.na3d_cross_workspace(1, L, S, NH, NH, HD, True)
         assert need <= S // 256 * rows * HD * 4 + 2 * (rows * 8 + 128), (L, S, NH, HD, need)
         assert need > 2 * rows * 8
+
+
+def test_the_self_test_refuses_what_the_calls_refuse():
+    import ctypes
+    na_build.build()
+    lib, P = na.load_library(), ctypes.c_void_p
+    at = [P((1 << 30) + (i << 26)) for i in range(10)]     # never touched
+    for sizes, code in (((0, 100, 40, 4, 2, 32), 2), ((2, 100, 40, 4, 3, 32), 2), ((2, 100, 40, 4, 2, 256), 11)):
+        assert lib.na3d_cross_selftest_withhold(*at, *sizes, None, None, None) == code
+    for i in (0, 1, 2, 3, 4, 6, 7, 8, 9):                  # (without dout it is the forward call)
+        assert lib.na3d_cross_selftest_withhold(*at[:i], None, *at[i + 1:], 2, 100, 40, 4, 2, 32, None, None, None) == 1
