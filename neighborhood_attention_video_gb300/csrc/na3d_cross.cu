@@ -1545,7 +1545,7 @@ __device__ __forceinline__ void bwd_softmax(const BwdParams& p, const Sync& sy, 
                 // be missing than their own error or what out's rounding would do. (Other splits' blocks
                 // keep what p.stat has, whenever they read it: equal inputs, equal bits.)
                 if (in && doc == d && (p.splits == 1 || total >= 1.f - 0x1p-12f - fminf(fabsf(st.x) * 0x1p-20f, 0x1p-4f))) {
-                    st.y = -(at + lean / total);
+                    st.y = -(at + (total == 0.f ? 0.f : lean / total));   // 0: scores of -infinity alone, ds 0 as well
                     p.stat_kv[row] = st;
                 }
             }

@@ -110,3 +110,18 @@ def test_an_entry_is_the_entry_by_itself(B, L, S, NH, NKV, HD, docs):
             unseen = torch.isinf(value[b])
             assert torch.equal(torch.isinf(x), unseen) and torch.equal(torch.isinf(y), unseen), name
             assert ((x - y).abs() <= 2 * off)[~unseen].all(), name
+
+
+@pytest.mark.parametrize("S", [1, 40, 600])
+def test_scores_past_the_range_of_fp32_have_no_gradient(S):
+    """Rows whose scores are all -infinity (products past fp32): lse is that, out and the
+    gradients are 0, beside rows that are as ever."""
+    q, kv, g = make((1, 1, 1, 30, 2, 64), S, 2, 5)
+    kv[:, :, 0].abs_().neg_()
+    q[:, :, :, ::3] = 2.0 ** 126
+    got = run(q, kv, g)
+    far = torch.zeros(30, dtype=torch.bool)
+    far[::3] = True
+    assert torch.isneginf(got["lse"][0, 0, 0, far]).all() and torch.isfinite(got["lse"][0, 0, 0, ~far]).all()
+    assert not got["out"][0, 0, 0, far].any() and not got["dq"][0, 0, 0, far].any()
+    assert all(torch.isfinite(got[n]).all() for n in ("out", "dq", "dk", "dv"))
