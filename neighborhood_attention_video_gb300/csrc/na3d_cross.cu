@@ -414,10 +414,13 @@ struct FwdShape : Geom<HD> {
 constexpr int kFwdThreads = 512;
 enum { kPlain, kDocuments, kFew };   // kernels of calls without documents, with them, of few rows
 // registers: what the softmax, the way out and the rest take of 512 x 128. The producer needs few where it
-// does not search (24576 tokens over 6144 states 781 -> 751 us with more for the softmax).
+// does not search (24576 tokens over 6144 states 782 -> 748 us with more for the softmax), a hundred where it
+// does: 8 tokens over 131072 states, head size 64, 42.7 us by kDocuments' split, 41 by kFew's; 49152 tokens
+// over 128 states of each of 4 documents, 16 heads of 128, 119 us by kFew's split, 108 by kDocuments'.
 template <int KIND>
 struct FwdRegs {
-    static constexpr uint32_t kSoftmax = KIND == kPlain ? 160 : 144, kOut = 112, kLow = KIND == kPlain ? 80 : 112;
+    static constexpr uint32_t kSoftmax = KIND == kPlain ? 160 : KIND == kDocuments ? 144 : 152;
+    static constexpr uint32_t kOut = KIND == kFew ? 104 : 112, kLow = KIND == kPlain ? 80 : KIND == kDocuments ? 112 : 104;
     static_assert(2 * kSoftmax + kOut + kLow <= 4 * 128, "register split");
 };
 
@@ -1001,18 +1004,20 @@ __device__ __forceinline__ void fwd_out(const FwdParams& p, const Sync& sy, uint
 // the block waiting (one token, 16 heads of 128 over 65536 states of 4 heads: 40 us
 // by one, 33 by two). Few rows share their states out over blocks as well.
 //
-// Bound by the chain of its warps: each half of a step passes from the scores to
-// the softmax to the products and back, and every hand-over costs some 170 to 230
-// cycles. 49152 tokens, 16 heads of 128 over 512 states: 176 us, 1.17 PFLOP/s, tensor
-// cores 61 % busy; 24576 over 6144: 820 us, 1.51 PFLOP/s, 74 % (1.93 is a large
-// product alone). Few rows at head size 128 are bound by memory: 8 tokens over 131072
-// states of 4 heads 6.6 TB/s; below it by the chain (64: 3.9 TB/s).
+// Bound by the chain of its warps where the states are few: each half of a step
+// passes from the scores to the softmax to the products and back, and every hand-over
+// costs some 170 to 230 cycles. 49152 tokens, 16 heads of 128 over 512 states: 168 us,
+// 1.23 PFLOP/s, tensor cores 68 % busy; 24576 over 6144: 748 us, 1.65 PFLOP/s, 87 %
+// (1.93 is a large product alone). Few rows at head size 128 are near the memory's
+// bound: 8 tokens over 131072 states of 4 heads 5.7 TB/s; below it the chain's (64:
+// 3.3 TB/s).
 //
-// Two row tiles to a block, one block to an SM, persistent:
-// FEW: row tiles so few that the states are split, or one alone. What that takes is
-// left out of the kernel for the rest, whose warps of five kinds share little room
-// for instructions (49152 tokens over 512 states 185 -> 176 us, 77 states 101 -> 94).
-// The same source laid out otherwise by the compiler is up to 5 % faster or slower.
+// Two row tiles to a block, one block to an SM, persistent. Its warps of five kinds
+// share little room for instructions, so what a call does not need is left out:
+// KIND kFew has row tiles so few that the states are split, or one alone; kDocuments
+// the search for documents' tiles, which kPlain does without (24576 tokens over 6144
+// states 862 -> 782 us, 49152 over 512 183 -> 170 by that alone). The same source laid
+// out otherwise by the compiler is up to 5 % faster or slower.
 //
 //   warps 0..3, 4..7  the softmax of either row tile;
 //   warps 8..11       results on their way out;
@@ -1677,9 +1682,9 @@ __device__ __forceinline__ void bwd_out(const BwdParams& p, const Sync& sy, uint
 // an atomic, and equal inputs give equal bits; and dq takes ds in two bf16 parts,
 // the second what the rounding of the first leaves. (Its error over that of a result
 // rounded once falls from 1.5 to 1.1 at head size 16, from 1.44 to 1.15 at 128, for
-// 15 us of the next figure.) Bound as the forward pass is: 24576 tokens, 16 heads of
-// 128 over 512 states, dq 172 us, dk and dv 168 us (1.23 PFLOP/s, tensor cores 66 %
-// busy).
+// 15 us of the next figure.) Bound as the forward pass over few states is: 24576
+// tokens, 16 heads of 128 over 512 states, dq 176 us, dk and dv 179 us (1.15 PFLOP/s,
+// tensor cores 66 % busy).
 //
 // One row tile to a block, one block to an SM, persistent:
 //   warps 0..3, 4..7  every second step's probabilities each;
