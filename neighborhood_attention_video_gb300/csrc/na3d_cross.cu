@@ -53,7 +53,8 @@ struct Sync {
             if (mbar_try_wait(b, parity)) return true;
             if ((it & 1023u) == 0u) {
                 if (*abort_flag) return false;
-                if (globaltimer_ns() - t0 > kWaitLimitNs && beat_clock() - abort_flag[1] > kWaitTicks) {
+                // (a beat may be given between the two reads)
+                if (globaltimer_ns() - t0 > kWaitLimitNs && int32_t(beat_clock() - abort_flag[1]) > int32_t(kWaitTicks)) {
                     *abort_flag = 1u;
                     atomicOr(&g_cross_timeout_flag, 1u);
                     return false;
