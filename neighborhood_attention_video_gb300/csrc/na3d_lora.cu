@@ -328,9 +328,10 @@ constexpr uint64_t kDrainLimitNs = 500000000ull;
 __device__ __forceinline__ uint32_t beat_clock() { return uint32_t(globaltimer_ns() >> 20); }
 
 // Has the block given up? It does kWaitLimitNs after this wait began (t0) and after the last beat.
+// (One given between the reads of clock and beat is ahead: the difference is signed.)
 __device__ __noinline__ bool gave_up(volatile uint32_t* abort_flag, uint64_t t0) {
     if (abort_flag[0]) return true;
-    if (globaltimer_ns() - t0 <= kWaitLimitNs || beat_clock() - abort_flag[1] <= uint32_t(kWaitLimitNs >> 20)) return false;
+    if (globaltimer_ns() - t0 <= kWaitLimitNs || int32_t(beat_clock() - abort_flag[1]) <= int32_t(kWaitLimitNs >> 20)) return false;
     abort_flag[0] = 1u;
     atomicOr(&g_lora_timeout_flag, 1u);
     return true;
