@@ -184,9 +184,9 @@ struct Docs {
 // looks at those that may hold the document. So documents whose states lie
 // together cost about their own tiles, documents that are scattered all of them
 // each. (A look at 4096 states takes 3.7 us. 5120 tokens of 256 documents, 4 heads
-// of 64 over 262144 states: sorted 118 -> 5.1 ms, in runs that come in any order
-// 118 -> 61; scattered over 16384 states 41, as without.) N: loads to a tile, 32
-// documents each.
+// of 64 over 262144 states: sorted 118 -> 5.0 ms, in runs that come in any order
+// 118 -> 60; scattered over 16384 states 39 -> 41.) N: loads to a tile, 32 documents
+// each.
 template <int N>
 struct Tiles {
     Docs docs;
